@@ -58,6 +58,52 @@ int gdn_scan(const void *q, const void *k, const void *v, const float *alpha, co
              const float *state_in, float *state_out, void *o, int T, int n_k_heads,
              int n_v_heads, int d_k, int d_v, void *cuda_stream);
 
+/*
+ * Linear attention with one decay per value head: the recurrence without the
+ * delta, S a head's state [d_v][d_k],
+ *
+ *     S   <- decay[h] * S + v_t[h] k_t^T     (k_t, q_t of key head h / (H_v / H_k))
+ *     o_t[h] = S q_t
+ *
+ * over n_seq independent sequences in one call: prompts and single tokens.
+ *   q, k      bf16 [n_tokens][n_k_heads][d_k], tokens q_stride / k_stride
+ *             elements apart (the slices of a fused projection are taken as
+ *             they are)
+ *   v         bf16 [n_tokens][n_v_heads][d_v], tokens v_stride elements apart
+ *   decay     float32 [n_v_heads], in [0, 1] (0: the state holds one token)
+ *   state_in  float32 [n_seq][n_v_heads][d_v][d_k], or NULL for zero states
+ *   state_out float32, same layout, or NULL; may be state_in.  A sequence
+ *             without tokens gets its state_in.
+ *   o         bf16 [n_tokens][n_v_heads][d_v], contiguous, round-to-nearest
+ *   offsets   int32 [n_seq + 1] in device memory: sequence i is the tokens
+ *             offsets[i] .. offsets[i + 1] - 1 (from 0, never decreasing, to
+ *             n_tokens; lengths may be 0).  Values outside that are clamped to
+ *             it, and tokens of no sequence keep what o held.  NULL: n_seq
+ *             sequences of n_tokens / n_seq tokens.
+ *   workspace device memory of at least the bytes gdn_decay_workspace gives
+ *             for the same sizes, 16-byte aligned, used by the call's kernels
+ *             alone; NULL where that is 0.
+ * A long sequence may be taken in pieces, passing the state along; pieces
+ * agree with one call up to float rounding.  The caller applies the model's
+ * preprocessing (norms, query scale) before the call.
+ * Supported: d_k 64 or 128, d_v a multiple of 16 up to 1024, n_v_heads a
+ * multiple of n_k_heads and at most 4096, n_tokens < 2^31.
+ * Pointers 16-byte aligned (decay and offsets 4-byte), strides multiples of 8.
+ * n_seq == 0 is a no-op.  Asynchronous on cuda_stream; all checks are made on
+ * the host before anything is launched.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_ALIGNMENT, MOE_ERR_UNSUPPORTED,
+ * MOE_ERR_CUDA.
+ */
+int gdn_decay_scan(const void *q, const void *k, const void *v, const float *decay,
+                   const float *state_in, float *state_out, void *o, const int *offsets,
+                   long long n_tokens, int n_seq, int n_k_heads, int n_v_heads, int d_k, int d_v,
+                   long long q_stride, long long k_stride, long long v_stride, void *workspace,
+                   size_t workspace_bytes, void *cuda_stream);
+
+/* Bytes of workspace that gdn_decay_scan wants for these sizes (host only). */
+int gdn_decay_workspace(long long n_tokens, int n_seq, int n_v_heads, int d_k, int d_v,
+                        size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -377,6 +377,66 @@ int moe_decode_noalloc(const moe_config *cfg, const void *x, void *out, void *cu
  */
 int moe_noalloc_status(void *cuda_stream, int *detail);
 
+/*
+ * The operators that stand between two layers and around the mixer of a
+ * hybrid model (its linear attention is in gdn.h): residual addition with the
+ * root-mean-square norm, quantisation to 8 bits, and the 8-bit matrix product.
+ * They need no handle and allocate nothing.  The 8-bit type is e4m3 (1 sign,
+ * 4 exponent and 3 mantissa bits, largest value 448), with one float32 scale
+ * per row: the row's values are scale * code.
+ *
+ * moe_add_rmsnorm: per row i < rows of d elements, in float32,
+ *     s = x + residual                       (x alone where residual is NULL)
+ *     out = s * weight / sqrt(mean(s^2) + eps)
+ * and sum = s, each rounded once to dtype.  The norm uses the unrounded s.
+ *   x, residual  dtype, rows x_stride / residual_stride elements apart
+ *                (residual NULL: none, its stride is ignored)
+ *   weight       dtype [d]
+ *   sum          dtype [rows][d] or NULL; may be residual (or x) itself when
+ *                that one's stride is d: each element is read before it is
+ *                written, by the same thread
+ *   out          dtype [rows][d]; may be x when x_stride is d
+ * moe_add_rmsnorm_fp8: the same norm y, quantised:
+ *     scales[i] = max|y| / 448,   codes = e4m3(y / scales[i])
+ *   codes [rows][d], scales float32 [rows].  A row of zeros (or one so small
+ *   that its scale is zero) has scale 0 and zero codes; a row that holds a NaN
+ *   or an infinity has a NaN scale and NaN codes.
+ * moe_quantize_fp8: the same codes and scales of w's rows without a norm
+ *   (weights [N][K] for moe_matmul_fp8, rows `stride` elements apart).
+ * Supported: 1 <= d <= 16384 (any d; rows and pointers on 16-byte boundaries
+ * are read with wide loads), dtype MOE_BF16 or MOE_F32, strides >= d.
+ * Pointers are device memory, aligned to their elements.  Asynchronous on
+ * cuda_stream.  rows == 0 is a no-op returning MOE_OK.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, CUDA.
+ */
+int moe_add_rmsnorm(const void *x, const void *residual, const void *weight, moe_dtype dtype,
+                    long long rows, int d, long long x_stride, long long residual_stride,
+                    float eps, void *sum, void *out, void *cuda_stream);
+int moe_add_rmsnorm_fp8(const void *x, const void *residual, const void *weight, moe_dtype dtype,
+                        long long rows, int d, long long x_stride, long long residual_stride,
+                        float eps, void *sum, uint8_t *codes, float *scales, void *cuda_stream);
+int moe_quantize_fp8(const void *w, moe_dtype dtype, long long rows, int cols, long long stride,
+                     uint8_t *codes, float *scales, void *cuda_stream);
+
+/*
+ * Matrix product of e4m3 codes with a scale per token and a scale per output
+ * channel, out bf16 [T][N]:
+ *     out[t][n] = x_scales[t] * w_scales[n] * sum_k x[t][k] * w[n][k]
+ * summed in float32 and rounded once.
+ *   x  codes [T][K], rows x_stride bytes apart;  x_scales float32 [T]
+ *   w  codes [N][K], rows w_stride bytes apart;  w_scales float32 [N]
+ *   out  rows out_stride elements apart, overlapping none of the inputs
+ * Supported: K a multiple of 16, up to 131072; T up to 4194304; N up to
+ * 1048576, any number of either.  x and w start on 16-byte boundaries and
+ * their strides are multiples of 16; the others are aligned to their elements.
+ * Asynchronous on cuda_stream; the result does not depend on what else runs.
+ * T == 0 is a no-op returning MOE_OK.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, CUDA.
+ */
+int moe_matmul_fp8(const uint8_t *x, const float *x_scales, int T, long long x_stride,
+                   const uint8_t *w, const float *w_scales, int N, int K, long long w_stride,
+                   void *out, long long out_stride, void *cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif

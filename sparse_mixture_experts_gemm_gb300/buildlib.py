@@ -31,8 +31,8 @@ def nvcc() -> str:
 
 def _deps() -> list[str]:
     return (glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + glob.glob(os.path.join(CSRC, "*.h")) + [os.path.join(ROOT, "include", "moe.h"),
-                                                     os.path.abspath(__file__)])
+            + glob.glob(os.path.join(CSRC, "*.h"))
+            + glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
