@@ -1,66 +1,540 @@
 // matmul_fp8.cu -- matrix product of e4m3 codes with a scale per token and a
 // scale per output channel (moe_matmul_fp8 in include/moe.h):
 //     out[t][n] = x_scale[t] * w_scale[n] * sum_k x[t][k] * w[n][k]
-// The scales do not depend on k, so the sum runs over the codes alone, in
-// fp32, and each output is scaled and rounded to bf16 once.
+// The scales do not depend on k, so the sum runs over the codes alone on the
+// tensor cores (e4m3 products, fp32 accumulators in TMEM), and each output is
+// scaled in fp32 and rounded to bf16 once.  Codes arrive by TMA in blocks of
+// 128 bytes of K in the 128-byte swizzle; what lies past T, N or K reads as
+// zero, so any number of tokens and channels takes the same code.
+//
+// Two kernels:
+//   * few tokens: the channels take the MMA's 128 rows and the tokens its
+//     columns (16 to 256 of them), so that a handful of tokens wastes no
+//     weight bandwidth; a cluster of up to 8 CTAs splits K and adds its
+//     partial sums through distributed shared memory in a fixed order;
+//   * many tokens: persistent CTA pairs compute 256 tokens x 256 channels on
+//     the two-CTA MMA, each CTA holding its 128 tokens' accumulator twice
+//     (512 TMEM columns), so that one tile is drained while the next is
+//     multiplied.
+// Every wait is bounded; one that runs out raises the CTA's abort flag and
+// records a timeout in the status word of the calls without a handle.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
+
+#include <mutex>
 
 #include "../../include/moe.h"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kTile = 64;  // tokens and channels of a block's tile
-constexpr int kTileK = 16;
+constexpr int kBK = 128;         // bytes of K per column block (one swizzle row)
+constexpr int kRowsM = 128;      // MMA rows of one CTA
+constexpr int kBlkBytes = kRowsM * kBK;
+constexpr int kMmThreads = 192;  // TMA producer, MMA issuer, four epilogue warps
+constexpr int kCtrl = 2048;      // barriers, TMEM address, abort flag, scales
+constexpr int kMaxSmem = 227 * 1024;
 
 struct MatmulArgs {
-  const uint8_t *x, *w;
   const float *xs, *ws;
   __nv_bfloat16 *out;
-  int T, N, K;
-  long long x_stride, w_stride, out_stride;
+  long long out_stride;
+  int T, N, nkb;   // nkb: K blocks of 128
+  int *status;
+  // few tokens
+  int bt, split, stages, tt;  // tokens per tile, CTAs along K, ring stages, token tiles
+  // many tokens
+  int mt, nt;  // 256-token and 256-channel tiles
+  bool wide;   // out's rows start on 32-byte boundaries
 };
 
-__device__ __forceinline__ float e4m3(uint8_t c) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+__device__ __forceinline__ void fail(const MatmulArgs &p, volatile int *abort_flag, int site) {
+  *abort_flag = 1;
+  report_error(p.status, MOE_ERR_DEVICE_TIMEOUT, KID_MATMUL_FP8 * 100 + site);
+}
+
+__device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
+  return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) &
+                                     ~static_cast<uintptr_t>(1023));
 }
 
 }  // namespace
 
-// 256 threads, 4 x 4 outputs each, codes widened to fp32 in shared memory.
-__global__ void __launch_bounds__(256) matmul_fp8_kernel(const MatmulArgs a) {
-  __shared__ float sx[kTileK][kTile + 1], sw[kTileK][kTile + 1];
-  const int n0 = blockIdx.x * kTile, t0 = blockIdx.y * kTile;
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < a.K; k0 += kTileK) {
-    for (int i = threadIdx.x; i < kTile * kTileK; i += 256) {
-      const int r = i / kTileK, c = i % kTileK;
-      sx[c][r] = t0 + r < a.T ? e4m3(a.x[(t0 + r) * a.x_stride + k0 + c]) : 0.0f;
-      sw[c][r] = n0 + r < a.N ? e4m3(a.w[(n0 + r) * a.w_stride + k0 + c]) : 0.0f;
+// Few tokens.  Cluster of p.split CTAs per (128 channels, p.bt tokens); CTA r
+// multiplies the K blocks [r nkb / split, (r + 1) nkb / split).  TMEM lane =
+// channel, column = token.
+__global__ void __launch_bounds__(kMmThreads, 1)
+    matmul_fp8_few_kernel(const __grid_constant__ CUtensorMap tmX,
+                          const __grid_constant__ CUtensorMap tmW, const MatmulArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = align1024(smem_raw);
+  const int stage_bytes = kBlkBytes + p.bt * kBK;
+  float *exch = reinterpret_cast<float *>(smem + p.stages * stage_bytes);  // [split][bt / split][128]
+  uint8_t *ctrl = reinterpret_cast<uint8_t *>(exch) + (p.split > 1 ? p.bt * kRowsM * 4 : 0);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(ctrl);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctrl + 512);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(ctrl + 516);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * p.stages, tfull = empty0 + 8 * p.stages;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long limit = MOE_WAIT_LIMIT_CYCLES;
+  const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int tile = static_cast<int>(blockIdx.x) / p.split;
+  const int n0 = tile / p.tt * kRowsM, t0 = tile % p.tt * p.bt;
+  const int kb0 = static_cast<int>(static_cast<long long>(p.nkb) * rank / p.split);
+  const int kb1 = static_cast<int>(static_cast<long long>(p.nkb) * (rank + 1) / p.split);
+  uint32_t cols = 32;
+  while (static_cast<int>(cols) < p.bt) cols *= 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
     }
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < kTileK; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sx[c][ty + 16 * i], sw[c][tx + 16 * j], acc[i][j]);
-    __syncthreads();
+    mbar_init(tfull, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmX);
+    prefetch_tmap(&tmW);
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int t = t0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (t < a.T && n < a.N)
-        a.out[t * a.out_stride + n] = __float2bfloat16_rn(acc[i][j] * a.xs[t] * a.ws[n]);
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+
+  bool ok = true;
+  if (warp == 0 && lane == 0) {
+    const uint64_t pol = policy_evict_last();
+    int stage = 0;
+    uint32_t phase = 0;
+    int kb = kb0;
+    for (; kb < kb1; ++kb) {
+      if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, limit, abort_flag)) {
+        fail(p, abort_flag, SITE_PRODUCER_EMPTY);
+        break;
+      }
+      const uint32_t fb = full0 + 8 * stage, dst = smem_u32(smem) + stage * stage_bytes;
+      mbar_arrive_expect_tx(fb, stage_bytes);
+      tma_load_2d(dst, &tmW, fb, kb * kBK, n0, pol);
+      tma_load_2d(dst + kBlkBytes, &tmX, fb, kb * kBK, t0, pol);
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
     }
+    if (*abort_flag) {  // copies in flight land before the shared memory goes away
+      const int issued = kb - kb0;
+      for (int i = max(0, issued - p.stages); i < issued; ++i)
+        if (!mbar_wait(full0 + 8 * (i % p.stages), (i / p.stages) & 1, limit, nullptr))
+          fail(p, abort_flag, SITE_DRAIN);
+    }
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_make(kRowsM, p.bt, 0);
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait(full0 + 8 * stage, phase, limit, abort_flag)) {
+        fail(p, abort_flag, SITE_MMA_FULL);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t a0 = smem_u32(smem) + stage * stage_bytes, b0 = a0 + kBlkBytes;
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_e4m3(tmem, sdesc_sw128(a0 + 32 * kk), sdesc_sw128(b0 + 32 * kk), idesc,
+                 (kb != kb0 || kk != 0) ? 1u : 0u);
+      tc_commit(empty0 + 8 * stage);
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    tc_commit(tfull);  // (also after an abort: the MMAs issued so far)
+  }
+  __syncwarp();
+  // every warp waits for the accumulator: after this the CTA's copies and
+  // MMAs are done
+  ok = mbar_wait(tfull, 0, limit, nullptr);
+  if (!__all_sync(0xffffffffu, ok)) {
+    if (lane == 0) fail(p, abort_flag, SITE_EPI_TMEM_FULL);
+    ok = false;
+  }
+  tc_fence_after();
+
+  const int wq = warp & 3;               // TMEM lane quarter of an epilogue warp
+  const int c = wq * 32 + lane;          // its lane's channel in the tile
+  const uint32_t tb = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+  const int n = n0 + c;
+  const bool epi = warp >= 2;
+  const float wsn = (epi && n < p.N) ? p.ws[n] : 0.0f;
+  if (p.split == 1) {
+    if (epi) {
+      for (int j = 0; j < p.bt; j += 16) {
+        float v[16];
+        tmem_ld16_sync(tb + j, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int t = t0 + j + i;
+          if (t < p.T && n < p.N)
+            p.out[t * p.out_stride + n] = __float2bfloat16_rn(v[i] * wsn * p.xs[t]);
+        }
+      }
+    }
+  } else {
+    // tokens [s per, (s + 1) per) of every CTA's partial sums go to CTA s
+    const int per = p.bt / p.split;
+    cluster_sync_all();  // every CTA of the cluster runs
+    if (epi) {
+      const uint32_t mine = smem_u32(exch + (static_cast<long long>(rank) * per) * kRowsM + c);
+      for (int j = 0; j < p.bt; j += 16) {
+        float v[16];
+        tmem_ld16_sync(tb + j, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int dst = (j + i) / per, at = (j + i) - dst * per;
+          const uint32_t a = cluster_map(mine + at * kRowsM * 4, dst);
+          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v[i]) : "memory");
+        }
+      }
+    }
+    cluster_sync_all();
+    if (epi) {
+      for (int i = 0; i < per; ++i) {
+        const int t = t0 + rank * per + i;
+        if (t >= p.T) break;
+        float v = 0.0f;
+        for (int s = 0; s < p.split; ++s) v += exch[(s * per + i) * kRowsM + c];
+        if (n < p.N) p.out[t * p.out_stride + n] = __float2bfloat16_rn(v * wsn * p.xs[t]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, cols);
 }
+
+namespace {
+
+// many tokens: a stage holds two column blocks of the CTA's 128 tokens and of
+// its 128 of the tile's 256 channels
+constexpr int kCB = 2;
+constexpr int kHalf = kCB * kBlkBytes;
+constexpr int kStages = 3;
+constexpr int kPairCols = 512;
+constexpr int kStageOut = 4 * 32 * 17 * 4;  // per epilogue warp: 32 rows of 32 bf16, padded
+constexpr int kPairSmem = kStages * 2 * kHalf + 1024 + kCtrl + kStageOut;
+constexpr int kBand = 16;  // 256-token tiles per band
+static_assert(kPairSmem <= kMaxSmem, "shared memory");
+
+// Tile i of the fixed order: bands of kBand token tiles, in a band one channel
+// tile after another with the token tiles innermost, so that the CTA pairs
+// at work share few weight tiles and a band of tokens that stays in L2.
+__device__ __forceinline__ void pair_tile(const MatmulArgs &p, int i, int &m, int &n) {
+  const int per = kBand * p.nt, b = i / per, m0 = b * kBand, h = min(kBand, p.mt - m0);
+  const int r = i - b * per;
+  n = r / h;
+  m = m0 + r - n * h;
+}
+
+__device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+}  // namespace
+
+// Many tokens: CTA pairs (clusters of two) on the two-CTA MMA.  CTA r of a pair
+// stages its own 128 tokens and 128 of the tile's 256 channels; CTA 0 issues
+// the MMAs, which read both CTAs' halves and leave 128 tokens x 256 channels
+// in each CTA's TMEM.  Barriers: full[s] in CTA 0 counts the bytes of both
+// CTAs; empty[s] and tfull[a] in both, by the MMA's multicast commit;
+// tempty[a] in CTA 0, by the eight epilogue warps of the pair.
+__global__ void __launch_bounds__(kMmThreads, 1)
+    matmul_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmX,
+                           const __grid_constant__ CUtensorMap tmW, const MatmulArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = align1024(smem_raw);
+  uint8_t *sA = smem, *sB = smem + kStages * kHalf;
+  uint8_t *ctrl = smem + kStages * 2 * kHalf;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(ctrl);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctrl + 512);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(ctrl + 516);
+  float *s_ws = reinterpret_cast<float *>(ctrl + 1024);              // [4 warps][32]
+  uint32_t *s_out = reinterpret_cast<uint32_t *>(ctrl + kCtrl);      // [4 warps][32][17]
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages;
+  const uint32_t tfull0 = empty0 + 8 * kStages, tempty0 = tfull0 + 16, drain_bar = tempty0 + 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long limit = MOE_WAIT_LIMIT_CYCLES;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int cl = static_cast<int>(blockIdx.x >> 1), ncl = static_cast<int>(gridDim.x >> 1);
+  constexpr uint16_t kBoth = 3;
+  const int tiles = p.mt * p.nt, nks = (p.nkb + kCB - 1) / kCB;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull0 + 8 * a, 1);
+      mbar_init(tempty0 + 8 * a, 8);
+    }
+    mbar_init(drain_bar, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tmX);
+    prefetch_tmap(&tmW);
+  }
+  if (warp == 1) {
+    tmem_alloc2(smem_u32(tmem_slot), kPairCols);
+    tmem_relinquish2();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers exist
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_last();
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t pend_mask = 0, pend_phase = 0;
+      bool ok = true;
+      for (int ti = cl; ok && ti < tiles; ti += ncl) {
+        int m, n;
+        pair_tile(p, ti, m, n);
+        const int xrow = (2 * m + rank) * kRowsM, wrow = (2 * n + rank) * kRowsM;
+        for (int ks = 0; ks < nks; ++ks) {
+          if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, limit, abort_flag)) {
+            fail(p, abort_flag, SITE_PRODUCER_EMPTY);
+            ok = false;
+            break;
+          }
+          const int cb = min(kCB, p.nkb - ks * kCB);
+          const uint32_t fb = full0 + 8 * stage, fb0 = cluster_map(fb, 0);
+          if (rank == 0) mbar_arrive_expect_tx(fb, 4 * cb * kBlkBytes);
+          for (int h = 0; h < cb; ++h) {
+            const int kx = (ks * kCB + h) * kBK;
+            tma_load_2d_pair(smem_u32(sA + stage * kHalf + h * kBlkBytes), &tmX, fb0, kx, xrow, pol);
+            tma_load_2d_pair(smem_u32(sB + stage * kHalf + h * kBlkBytes), &tmW, fb0, kx, wrow, pol);
+          }
+          pend_mask |= 1u << stage;
+          pend_phase = (pend_phase & ~(1u << stage)) | (phase << stage);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // the commits of the last stages arrive here too: none may land after
+      // the CTA has ended
+      for (int j = 0; ok && j < kStages; ++j) {
+        if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, limit, abort_flag)) {
+          fail(p, abort_flag, SITE_DRAIN);
+          ok = false;
+        }
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok && rank == 0)  // copies of both CTAs that complete here
+        for (int s = 0; s < kStages; ++s)
+          if ((pend_mask >> s) & 1)
+            if (!mbar_wait(full0 + 8 * s, (pend_phase >> s) & 1, limit, nullptr))
+              fail(p, abort_flag, SITE_DRAIN);
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t idesc = idesc_make(2 * kRowsM, 256, 0);
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int ti = cl; ok && ti < tiles; ti += ncl) {
+        if (!mbar_wait(tempty0 + 8 * acc, acc_phase ^ 1, limit, abort_flag)) {
+          fail(p, abort_flag, SITE_MMA_TMEM_EMPTY);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
+        for (int ks = 0; ks < nks; ++ks) {
+          if (!mbar_wait(full0 + 8 * stage, phase, limit, abort_flag)) {
+            fail(p, abort_flag, SITE_MMA_FULL);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(sA + stage * kHalf), b0 = smem_u32(sB + stage * kHalf);
+          const int cb = min(kCB, p.nkb - ks * kCB);
+          for (int h = 0; h < cb; ++h)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint32_t off = h * kBlkBytes + 32 * kk;
+              mma2_e4m3(d, sdesc_sw128(a0 + off), sdesc_sw128(b0 + off), idesc,
+                        (ks | h | kk) != 0 ? 1u : 0u);
+            }
+          tc_commit2_mc(empty0 + 8 * stage, kBoth);
+          if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        tc_commit2_mc(tfull0 + 8 * acc, kBoth);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+      }
+      if (!ok) {  // the MMAs issued so far end before TMEM or shared memory go away
+        tc_commit2(drain_bar);
+        if (!mbar_wait(drain_bar, 0, limit, nullptr)) fail(p, abort_flag, SITE_DRAIN);
+      }
+    }
+  } else {
+    const int wq = warp & 3;
+    float *ws = s_ws + wq * 32;
+    uint32_t *so = s_out + wq * 32 * 17;
+    const uint32_t tempty_r = cluster_map(tempty0, 0);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int ti = cl; ti < tiles; ti += ncl) {
+      int m, n;
+      pair_tile(p, ti, m, n);
+      const bool ok = mbar_wait(tfull0 + 8 * acc, acc_phase, limit, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) {
+        if (lane == 0) fail(p, abort_flag, SITE_EPI_TMEM_FULL);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t tb =
+          tmem + static_cast<uint32_t>(acc * 256) + (static_cast<uint32_t>(wq * 32) << 16);
+      const int t0 = (2 * m + rank) * kRowsM + wq * 32, t = t0 + lane;
+      const float xs = t < p.T ? p.xs[t] : 0.0f;
+      const int rows = min(32, p.T - t0);
+#pragma unroll 1
+      for (int c = 0; c < 256; c += 32) {
+        const int nc = n * 256 + c;
+        if (nc >= p.N) break;
+        float v[32];
+        tmem_ld32_sync(tb + c, v);
+        __syncwarp();
+        ws[lane] = nc + lane < p.N ? p.ws[nc + lane] : 0.0f;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const float4 w4 = *reinterpret_cast<const float4 *>(ws + i);
+          v[i] *= w4.x * xs;
+          v[i + 1] *= w4.y * xs;
+          v[i + 2] *= w4.z * xs;
+          v[i + 3] *= w4.w * xs;
+        }
+        if (p.wide && nc + 32 <= p.N) {
+          // 32 bytes per thread and store: whole sectors
+          if (t < p.T) {
+            __nv_bfloat16 *o = p.out + t * p.out_stride + nc;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              uint32_t b[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                b[j] = bf16x2_bits(v[16 * q + 2 * j], v[16 * q + 2 * j + 1]);
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o + 16 * q),
+                           "r"(b[0]), "r"(b[1]), "r"(b[2]), "r"(b[3]), "r"(b[4]), "r"(b[5]),
+                           "r"(b[6]), "r"(b[7])
+                           : "memory");
+            }
+          }
+        } else {
+          // rows off the 32-byte grid, or the last columns: through shared
+          // memory, so that the lanes of a store lie side by side in one row
+#pragma unroll
+          for (int j = 0; j < 16; ++j) so[lane * 17 + j] = bf16x2_bits(v[2 * j], v[2 * j + 1]);
+          __syncwarp();
+          const uint16_t *sh = reinterpret_cast<const uint16_t *>(so);
+          if (nc + lane < p.N)
+            for (int r = 0; r < rows; ++r)
+              reinterpret_cast<uint16_t *>(p.out)[(t0 + r) * p.out_stride + nc + lane] =
+                  sh[r * 34 + lane];
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(tempty_r + 8 * acc);
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no MMA of the pair is in flight, no arrival is pending
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc2(tmem, kPairCols);
+  if (*abort_flag)  // after an abort the partner's copies get time to land
+    for (int i = 0; i < 200; ++i) __nanosleep(1000);
+}
+
+namespace {
+
+template <typename K>
+cudaError_t launch_clusters(K kern, int grid, int cluster, int smem, cudaStream_t st,
+                            const CUtensorMap &x, const CUtensorMap &w, const MatmulArgs &p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kMmThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, x, w, p);
+}
+
+// Per device: what the launches need to know, looked up once.
+struct MatmulDevice {
+  int sms = 0;
+  int *status = nullptr;
+  int rc = MOE_ERR_CUDA;
+};
+
+const MatmulDevice &matmul_device() {
+  static MatmulDevice devs[64];
+  static std::once_flag once[64];
+  static const MatmulDevice none;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return none;
+  std::call_once(once[dev], [dev] {
+    MatmulDevice &d = devs[dev];
+    d.status = noalloc_status_word();
+    if (d.status &&
+        cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
+        cudaFuncSetAttribute(matmul_fp8_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMaxSmem) == cudaSuccess &&
+        cudaFuncSetAttribute(matmul_fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kPairSmem) == cudaSuccess)
+      d.rc = MOE_OK;
+  });
+  return devs[dev];
+}
+
+}  // namespace
 
 }  // namespace moe
 
@@ -73,7 +547,9 @@ extern "C" int moe_matmul_fp8(const uint8_t *x, const float *x_scales, int T, lo
   if (T < 0 || N <= 0 || K <= 0 || x_stride < K || w_stride < K || out_stride < N)
     return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!x || !x_scales || !w || !w_scales || !out)) return MOE_ERR_INVALID_ARG;
-  if (K % 16 != 0 || T > (1 << 22) || N > (1 << 20) || K > (1 << 17)) return MOE_ERR_UNSUPPORTED;
+  if (K % 16 != 0 || T > (1 << 22) || N > (1 << 20) || K > (1 << 17) ||
+      x_stride >= (1LL << 40) || w_stride >= (1LL << 40))
+    return MOE_ERR_UNSUPPORTED;
   auto misaligned = [](const void *p, uintptr_t n) {
     return (reinterpret_cast<uintptr_t>(p) % n) != 0;
   };
@@ -81,9 +557,45 @@ extern "C" int moe_matmul_fp8(const uint8_t *x, const float *x_scales, int T, lo
       misaligned(x_scales, 4) || misaligned(w_scales, 4) || misaligned(out, 2))
     return MOE_ERR_ALIGNMENT;
   if (T == 0) return MOE_OK;
-  const MatmulArgs a = {x, w, x_scales, w_scales, static_cast<__nv_bfloat16 *>(out), T, N, K,
-                        x_stride, w_stride, out_stride};
-  matmul_fp8_kernel<<<dim3((N + kTile - 1) / kTile, (T + kTile - 1) / kTile), 256, 0,
-                      static_cast<cudaStream_t>(cuda_stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  const MatmulDevice &dev = matmul_device();
+  if (dev.rc != MOE_OK) return dev.rc;
+  const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+  MatmulArgs p = {};
+  p.xs = x_scales;
+  p.ws = w_scales;
+  p.out = static_cast<__nv_bfloat16 *>(out);
+  p.out_stride = out_stride;
+  p.T = T;
+  p.N = N;
+  p.nkb = (K + kBK - 1) / kBK;
+  p.status = dev.status;
+  p.wide = !misaligned(out, 32) && out_stride % 16 == 0;
+  CUtensorMap mx, mw;
+  if (!encode_map_2d(&mw, w, 1, N, K, kBK, kRowsM, true, w_stride)) return MOE_ERR_CUDA;
+  p.mt = (T + 255) / 256;
+  p.nt = (N + 255) / 256;
+  cudaError_t e;
+  const int pairs = dev.sms / 2;
+  if (p.mt * p.nt > pairs / 2) {
+    if (!encode_map_2d(&mx, x, 1, T, K, kBK, kRowsM, true, x_stride)) return MOE_ERR_CUDA;
+    e = launch_clusters(matmul_fp8_pair_kernel, 2 * (p.mt * p.nt < pairs ? p.mt * p.nt : pairs), 2,
+                        kPairSmem, st, mx, mw, p);
+  } else {
+    // tokens in equal tiles of at most 128, and K split over as many CTAs as
+    // keep the grid within the SMs
+    p.tt = (T + 127) / 128;
+    p.bt = ((T + p.tt - 1) / p.tt + 15) / 16 * 16;
+    const int tiles = (N + kRowsM - 1) / kRowsM * p.tt;
+    p.split = 1;
+    while (p.split < 8 && 2 * p.split * tiles <= dev.sms && 2 * p.split <= p.nkb) p.split *= 2;
+    const int stage = kBlkBytes + p.bt * kBK, exch = p.split > 1 ? p.bt * kRowsM * 4 : 0;
+    const int mine = (p.nkb + p.split - 1) / p.split;
+    p.stages = (kMaxSmem - 1024 - kCtrl - exch) / stage;
+    if (p.stages > mine) p.stages = mine;
+    if (p.stages > 16) p.stages = 16;
+    if (!encode_map_2d(&mx, x, 1, T, K, kBK, p.bt, true, x_stride)) return MOE_ERR_CUDA;
+    e = launch_clusters(matmul_fp8_few_kernel, tiles * p.split, p.split,
+                        p.stages * stage + exch + kCtrl + 1024, st, mx, mw, p);
+  }
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

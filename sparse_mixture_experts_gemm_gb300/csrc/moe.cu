@@ -56,7 +56,7 @@ EncodeTiledFn get_encode() {
 // box_rows elements; 128-byte swizzle or none; out-of-range elements read as
 // zero.  Host-only (encodes the descriptor, allocates nothing).
 bool moe::encode_map_2d(CUtensorMap *m, const void *base, size_t esz, uint64_t rows, uint64_t cols,
-                        uint32_t box_cols, uint32_t box_rows, bool swizzle128) {
+                        uint32_t box_cols, uint32_t box_rows, bool swizzle128, uint64_t pitch) {
   EncodeTiledFn enc = get_encode();
   if (!enc) return false;
   // 2-byte elements travel as bf16 (also the raw bits of 4-bit scales and
@@ -65,7 +65,7 @@ bool moe::encode_map_2d(CUtensorMap *m, const void *base, size_t esz, uint64_t r
                                  : esz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * esz};
+  cuuint64_t strides[1] = {pitch ? pitch : cols * esz};
   cuuint32_t box[2] = {box_cols, box_rows};
   cuuint32_t estr[2] = {1, 1};
   return enc(m, dt, 2, const_cast<void *>(base), dims, strides, box, estr,

@@ -12,6 +12,7 @@ enum KernelId {
   KID_GEMM_DOWN = 4,
   KID_COMBINE = 5,
   KID_DECODE = 6,
+  KID_MATMUL_FP8 = 7,
   KID_DEBUG = 9,
 };
 
