@@ -100,8 +100,9 @@ int gdn_decay_scan(const void *q, const void *k, const void *v, const float *dec
                    long long q_stride, long long k_stride, long long v_stride, void *workspace,
                    size_t workspace_bytes, void *cuda_stream);
 
-/* Bytes of workspace that gdn_decay_scan wants for these sizes (host only). */
-int gdn_decay_workspace(long long n_tokens, int n_seq, int n_v_heads, int d_k, int d_v,
+/* Bytes of workspace that gdn_decay_scan wants for these sizes; ragged: 1 for
+ * a call with offsets, 0 for one without (host only). */
+int gdn_decay_workspace(long long n_tokens, int n_seq, int ragged, int n_v_heads, int d_k, int d_v,
                         size_t *bytes);
 
 #ifdef __cplusplus

@@ -123,7 +123,7 @@ def lib() -> ctypes.CDLL:
     L.moe_matmul_fp8.argtypes = [vp, vp, ip, ll, vp, vp, ip, ip, ll, vp, ll, vp]
     L.gdn_decay_scan.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ll, ip, ip, ip, ip, ip, ll, ll,
                                  ll, vp, ctypes.c_size_t, vp]
-    L.gdn_decay_workspace.argtypes = [ll, ip, ip, ip, ip, ctypes.POINTER(ctypes.c_size_t)]
+    L.gdn_decay_workspace.argtypes = [ll, ip, ip, ip, ip, ip, ctypes.POINTER(ctypes.c_size_t)]
     for name in EXPORTED:
         if name != "moe_strerror":
             getattr(L, name).restype = ip
@@ -643,7 +643,7 @@ def gdn_decay_scan(q, k, v, decay, state=None, offsets=None, out=None, state_out
         _given("state", state, s_shape, f32)
     L = lib()
     need = ctypes.c_size_t(0)
-    _check(L.gdn_decay_workspace(N, n, Hv, dk, dv, ctypes.byref(need)), "gdn_decay_workspace")
+    _check(L.gdn_decay_workspace(N, n, offsets is not None, Hv, dk, dv, ctypes.byref(need)), "gdn_decay_workspace")
     with _on(stream):
         out = torch.empty(sv, dtype=torch.bfloat16, device=v.device) if out is None \
             else _given("out", out, sv, torch.bfloat16)

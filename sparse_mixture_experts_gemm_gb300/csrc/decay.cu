@@ -11,37 +11,16 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "../../include/gdn.h"
+#include "decay_common.cuh"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace moe {
 
 namespace {
-
-struct DecayArgs {
-  const __nv_bfloat16 *q, *k, *v;
-  const float *decay, *s_in;
-  float *s_out;
-  __nv_bfloat16 *o;
-  const int *offsets;  // null: n_seq sequences of n_tokens / n_seq tokens
-  long long n_tokens, q_stride, k_stride, v_stride;
-  int n_seq, Hk, Hv, dv;
-};
-
-// first token and number of tokens of sequence i; offsets outside
-// [0, n_tokens] or running backwards are clamped
-__device__ __forceinline__ void seq_range(const DecayArgs &a, int i, long long &first,
-                                          long long &len) {
-  if (a.offsets) {
-    const long long lo = min(max(static_cast<long long>(a.offsets[i]), 0LL), a.n_tokens);
-    const long long hi = min(max(static_cast<long long>(a.offsets[i + 1]), lo), a.n_tokens);
-    first = lo;
-    len = hi - lo;
-  } else {
-    len = a.n_tokens / a.n_seq;
-    first = len * i;
-  }
-}
 
 __device__ __forceinline__ float4 ld_bf16x4(const __nv_bfloat16 *p) {
   const uint2 u = *reinterpret_cast<const uint2 *>(p);
@@ -68,6 +47,7 @@ __global__ void __launch_bounds__(kRecWarps * 32) decay_recurrent_kernel(const D
   if (j0 - lane / kLpr >= a.dv) return;
   long long first, len;
   seq_range(a, seq, first, len);
+  if (len > a.recur) return;  // the chunked kernels take it
   const long long sbase = (static_cast<long long>(seq) * a.Hv + h) * a.dv * kDk + 4 * c;
   float4 S[kR];
 #pragma unroll
@@ -128,11 +108,88 @@ cudaError_t launch_recurrent(const DecayArgs &a, cudaStream_t st) {
 
 using namespace moe;
 
-extern "C" int gdn_decay_workspace(long long n_tokens, int n_seq, int n_v_heads, int d_k, int d_v,
-                                   size_t *bytes) {
+namespace {
+
+// Longest sequence that takes the recurrent form.
+constexpr long long kRecur = 8;
+constexpr long long kGpuSms = 152;
+
+// How a call is cut: the sequences that are not recurrent, their segments.
+struct Plan {
+  bool recurrent, chunked, segmented;
+  long long seg_len, items, slots;
+};
+
+long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+// Chunks per segment, by the time of the kernels in units of one chunk of the
+// main kernel: a CTA takes its segment's chunks and about two more to start
+// and end; with more than one segment per sequence the segment kernel (0.45
+// per chunk) and the chain come first.
+Plan make_plan(bool ragged, long long n_tokens, long long n_seq, long long heads) {
+  Plan p = {};
+  const long long len = ragged ? n_tokens : n_seq ? n_tokens / n_seq : 0;
+  const long long seqs = ragged ? 1 : n_seq;  // of length len at most
+  p.chunked = len > kRecur;
+  p.recurrent = ragged || !p.chunked;
+  if (!p.chunked) return p;
+  const long long chunks = ceil_div(len, kChunkTok);
+  const long long extra = ragged ? (n_seq - 1) / 2 : 0;  // part-filled segments
+  double best = 0;
+  for (long long n = 1; n <= 256 && n <= chunks; ++n) {
+    const long long lc = ceil_div(chunks, n);
+    if (n > 1 && lc < 4) break;
+    const long long ns = ceil_div(chunks, lc);
+    double t = static_cast<double>(ceil_div((ns * seqs + extra) * heads, kGpuSms)) * (lc + 2);
+    if (ns > 1)
+      t += static_cast<double>(ceil_div((ns - 1) * seqs * heads, kGpuSms)) * (0.45 * lc + 2) + 3 +
+           0.002 * ns * seqs * heads;
+    if (n == 1 || t < best) {
+      best = t;
+      p.seg_len = lc * kChunkTok;
+    }
+  }
+  const long long per = ceil_div(len, p.seg_len);
+  p.segmented = per > 1;
+  if (ragged) {
+    p.slots = p.segmented ? n_tokens / p.seg_len : 0;
+    const long long longest = n_tokens / (kRecur + 1);
+    p.items = n_tokens / p.seg_len + (n_seq < longest ? n_seq : longest);
+  } else {
+    p.items = n_seq * per;
+    p.slots = n_seq * (per - 1);
+  }
+  return p;
+}
+
+struct DecayDevice {
+  int *status = nullptr;
+  int rc = MOE_ERR_CUDA;
+};
+
+// Per device, looked up once.
+const DecayDevice &decay_device() {
+  static DecayDevice devs[64];
+  static std::once_flag once[64];
+  static const DecayDevice none;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return none;
+  std::call_once(once[dev], [dev] {
+    devs[dev].status = noalloc_status_word();
+    if (devs[dev].status && decay_chunk_setup()) devs[dev].rc = MOE_OK;
+  });
+  return devs[dev];
+}
+
+}  // namespace
+
+extern "C" int gdn_decay_workspace(long long n_tokens, int n_seq, int ragged, int n_v_heads, int d_k,
+                                   int d_v, size_t *bytes) {
   if (!bytes || n_tokens < 0 || n_seq < 0 || n_v_heads <= 0 || d_k <= 0 || d_v <= 0)
     return MOE_ERR_INVALID_ARG;
-  *bytes = 0;
+  const Plan p = make_plan(ragged != 0, n_tokens, n_seq,
+                           static_cast<long long>(n_v_heads) * ceil_div(d_v, 128));
+  *bytes = static_cast<size_t>(p.slots) * n_v_heads * d_v * d_k * sizeof(float);
   return MOE_OK;
 }
 
@@ -163,12 +220,17 @@ extern "C" int gdn_decay_scan(const void *q, const void *k, const void *v, const
       misaligned(state_out, 16) || misaligned(decay, 4) || misaligned(offsets, 4) ||
       misaligned(workspace, 16))
     return MOE_ERR_ALIGNMENT;
-  size_t need = 0;
-  const int rc = gdn_decay_workspace(n_tokens, n_seq, n_v_heads, d_k, d_v, &need);
-  if (rc != MOE_OK) return rc;
+  DecayArgs a = {};
+  a.tiles = (d_v + 127) / 128;
+  const Plan plan =
+      make_plan(offsets != nullptr, n_tokens, n_seq, static_cast<long long>(n_v_heads) * a.tiles);
+  const size_t need = static_cast<size_t>(plan.slots) * n_v_heads * d_v * d_k * sizeof(float);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_INVALID_ARG;
+  if (plan.items * n_v_heads * ceil_div(static_cast<long long>(d_v) * d_k, 1024) > 0x7fffffffLL)
+    return MOE_ERR_UNSUPPORTED;
+  const DecayDevice &dev = decay_device();
+  if (dev.rc != MOE_OK) return dev.rc;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  DecayArgs a;
   a.q = static_cast<const __nv_bfloat16 *>(q);
   a.k = static_cast<const __nv_bfloat16 *>(k);
   a.v = static_cast<const __nv_bfloat16 *>(v);
@@ -185,6 +247,23 @@ extern "C" int gdn_decay_scan(const void *q, const void *k, const void *v, const
   a.Hk = n_k_heads;
   a.Hv = n_v_heads;
   a.dv = d_v;
-  const cudaError_t e = d_k == 128 ? launch_recurrent<128, 8>(a, st) : launch_recurrent<64, 8>(a, st);
+  a.recur = kRecur;
+  a.seg_len = plan.seg_len;
+  a.slots = plan.slots;
+  a.items = plan.items;
+  a.ws = static_cast<float *>(workspace);
+  a.status = dev.status;
+  cudaError_t e = cudaSuccess;
+  if (plan.recurrent)
+    e = d_k == 128 ? launch_recurrent<128, 8>(a, st) : launch_recurrent<64, 8>(a, st);
+  if (e == cudaSuccess && plan.chunked) {
+    const uint64_t kw = static_cast<uint64_t>(n_k_heads) * d_k, vw = static_cast<uint64_t>(n_v_heads) * d_v;
+    CUtensorMap mq, mk, mv;
+    if (!encode_map_2d(&mq, q, 2, n_tokens, kw, 64, kChunkTok, true, 2 * q_stride) ||
+        !encode_map_2d(&mk, k, 2, n_tokens, kw, 64, kChunkTok, true, 2 * k_stride) ||
+        !encode_map_2d(&mv, v, 2, n_tokens, vw, 64, kChunkTok, true, 2 * v_stride))
+      return MOE_ERR_CUDA;
+    e = launch_decay_chunked(a, d_k, mq, mk, mv, plan.segmented, st);
+  }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -1,0 +1,775 @@
+// decay_chunk.cu -- the chunked form of linear attention with a decay per head
+// (gdn_decay_scan in include/gdn.h), on the tcgen05 tensor cores.
+//
+// With the tokens of a sequence in chunks of C = 64 and S the state before a
+// chunk, lambda the head's decay, i and j tokens of the chunk:
+//     o_i = lambda^(i+1) S q_i + sum_{j <= i} lambda^(i-j) (q_i . k_j) v_j
+//     S  <- lambda^C S + U,   U = sum_j lambda^(C-1-j) v_j k_j^T
+// as matrix products, d_v along the MMA's 128 rows (TMEM lanes):
+//     scores  [i][j]     = Q K^T                          (bf16, exact operands)
+//     O^T     [d_v][i]   = S Q~^T,  Q~_i = lambda^(i+1) q_i   (tf32)
+//                        + V^T P^T,  P_ij = lambda^(i-j) scores (bf16 hi + lo)
+//     U       [d_v][d_k] = V~^T K,  V~_j = lambda^(C-1-j) v_j   (bf16, three parts)
+// Every decay is a power <= 1 of lambda: nothing is divided by a decay.
+//
+// Precision.  V~ is written as three bf16 parts (24 bits; the products with
+// bf16 k are exact), each chunk's U starts from zero in TMEM, and the state
+// lives in registers, where lambda^C S + U is one fp32 fused multiply-add per
+// element: tensor-core accumulation truncates, and adding chunk after chunk
+// into one accumulator drifted to several 1e-6 of the state.  The outputs are
+// rounded to bf16 (rms 1.7e-3) in the end; S and Q~ enter them as tf32 (2^-11)
+// and P as two bf16 parts (2^-17), so nothing before the last rounding shows.
+//
+// Work split.  One CTA scans one segment of one (sequence, value head, 128
+// columns of d_v).  A sequence is one segment when the batch has enough heads
+// to fill the GPU; otherwise it is cut: a first launch of the same kernel
+// without the outputs computes what each segment leaves, a small kernel
+// chains these into the state before each segment, and the main launch runs
+// all segments at once.
+//
+// Roles (512 threads): warp 0 TMA producer; warp 1 issues every MMA; warps 2-3
+// P (scores in TMEM lanes 64..127); warps 4-7 V~ (a thread per column of V)
+// and Q~; warps 8-15 the state (a thread per row and half of d_k) and O^T to
+// global memory.  The issuer's order per chunk is S Q~^T, V^T P^T, the next
+// chunk's scores, the next chunk's U, so that only the products wait for one
+// another and the other roles work under them.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "../../include/moe.h"
+#include "decay_common.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kC = kChunkTok;
+constexpr int kBlk = kC * 128;  // a 64-token tile of 128 bytes (64 bf16) per token: 8 KB
+constexpr int kThreadsC = 512;
+constexpr int kStg = 3;    // TMA stages
+constexpr int kTerms = 3;  // bf16 parts of V~
+constexpr uint32_t kTmemAll = 512;
+
+// TMEM columns
+template <int kDk, bool kOut>
+struct Cols {
+  static constexpr int kUBufs = kOut ? 1 : 2;
+  static constexpr uint32_t U = 0;                   // kUBufs x kDk
+  static constexpr uint32_t V = kUBufs * kDk;        // V~: two halves of 32 tokens, kTerms x 16 each
+  static constexpr uint32_t S = V + 2 * kTerms * 16; // state of the chunk (outputs only)
+  static constexpr uint32_t O = S + kDk;             // O^T: 64
+  static constexpr uint32_t P = O + 64;              // scores: 64 (lanes 64..127)
+  static_assert((kOut ? P + 64 : S) <= kTmemAll, "TMEM columns");
+};
+
+// Shared-memory descriptor of an operand whose M or N index is contiguous
+// (128-byte swizzle): 128-byte rows of 64 bf16, one per K index; 8 rows make a
+// 1024-byte swizzle atom (stride byte offset, along K), `lbo` bytes lie
+// between blocks of 64 along M / N.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(lbo >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(2) << 61;
+  return d;
+}
+constexpr uint32_t kTransA = 1u << 15, kTransB = 1u << 16;  // A / B contiguous along M / N
+
+// A operand in TMEM
+__device__ __forceinline__ void mma_ts_bf16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_tf32(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t ta, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16};" ::"r"(ta),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// bf16 parts of a pair of floats, the first in the low half: returns the
+// nearest bf16 pair and leaves the remainders in a, b
+__device__ __forceinline__ uint32_t take_bf16(float &a, float &b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  const uint32_t u = *reinterpret_cast<const uint32_t *>(&h);
+  a -= __uint_as_float(u << 16);
+  b -= __uint_as_float(u & 0xffff0000u);
+  return u;
+}
+
+__device__ __forceinline__ float to_tf32(float x) {
+  uint32_t u;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(u) : "f"(x));
+  return __uint_as_float(u);
+}
+
+// The segment that work item `item` stands for.
+struct Segment {
+  int seq = -1;          // -1: no such item
+  long long first, len;  // its tokens
+  long long index;       // its place in the sequence
+  bool last;
+  long long slot;        // of the state before it (index > 0); slot + 1: before the next one
+};
+
+// Items in order of the sequences that take this path.  All threads of the
+// block call it; `scratch`: 32 + 4 shared words.
+__device__ __forceinline__ Segment find_segment(const DecayArgs &a, long long item, int *scratch) {
+  Segment g;
+  long long len = 0, first = 0, before = 0;
+  int seq = -1, rank = 0;
+  if (!a.offsets) {
+    len = a.n_tokens / a.n_seq;
+    const long long n = max((len + a.seg_len - 1) / a.seg_len, 1LL);
+    if (item < n * a.n_seq) {
+      seq = static_cast<int>(item / n);
+      rank = seq;
+      before = n * seq;
+      first = len * seq;
+    }
+  } else {
+    // running number of segments, a block's worth of sequences at a time
+    int *warp_sum = scratch, *found = scratch + 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    if (threadIdx.x == 0) found[0] = -1;
+    __syncthreads();
+    long long base = 0;
+    int ranks = 0;  // sequences before this block's worth that take this path
+    for (int i0 = 0; i0 < a.n_seq; i0 += blockDim.x) {
+      const int i = i0 + threadIdx.x;
+      int n = 0;
+      long long l = 0, f = 0;
+      if (i < a.n_seq) {
+        seq_range(a, i, f, l);
+        n = l <= a.recur ? 0 : static_cast<int>((l + a.seg_len - 1) / a.seg_len);
+      }
+      int inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      const uint32_t mine = __ballot_sync(0xffffffffu, n > 0);
+      if (lane == 31) warp_sum[warp] = inc;
+      __syncthreads();
+      int pre = 0, total = 0;
+      for (int w = 0; w < nw; ++w) {
+        if (w < warp) pre += warp_sum[w];
+        total += warp_sum[w];
+      }
+      const long long lo = base + pre + inc - n;
+      if (n > 0 && item >= lo && item < lo + n) {
+        found[0] = i;
+        found[1] = static_cast<int>(item - lo);
+      }
+      __syncthreads();
+      // ranks of the sequences (one slot fewer than segments each)
+      if (lane == 0) warp_sum[warp] = __popc(mine);
+      __syncthreads();
+      if (n > 0 && found[0] == i) {
+        int r = ranks + __popc(mine & ((1u << lane) - 1u));
+        for (int w = 0; w < warp; ++w) r += warp_sum[w];
+        found[2] = r;
+      }
+      for (int w = 0; w < nw; ++w) ranks += warp_sum[w];
+      base += total;
+      __syncthreads();
+      if (found[0] >= 0) break;
+    }
+    seq = found[0];
+    if (seq >= 0) {
+      rank = found[2];
+      before = item - found[1];
+      seq_range(a, seq, first, len);
+    }
+    __syncthreads();
+  }
+  if (seq < 0) return g;
+  g.seq = seq;
+  g.index = item - before;
+  const long long at = g.index * a.seg_len;
+  g.first = first + at;
+  g.last = at + a.seg_len >= len;
+  g.len = g.last ? len - at : a.seg_len;
+  g.slot = before - rank + g.index - 1;  // each earlier sequence has one slot fewer than segments
+  return g;
+}
+
+// V~ of tokens j0 .. j0 + 31 of a chunk for one d_v column, as kTerms bf16
+// parts of two tokens per TMEM column: token j's value times `w`[j], or, in a
+// sequence's last chunk of n < 64 tokens, times tab[n - 1 - j] (0 from n on).
+// `v` points at the staged V (128-byte swizzle).
+__device__ __forceinline__ void make_vt(const uint8_t *v, int col, const float *w, const float *tab,
+                                        int n, int j0, uint32_t ta) {
+  const int chunk = (col & 63) >> 3;
+  const uint8_t *base = v + (col >> 6) * kBlk + (col & 7) * 2 + j0 * 128;
+  uint32_t t0[16], t1[16], t2[16];
+#pragma unroll
+  for (int j = 0; j < 32; j += 4) {
+    float wj[4];
+    if (n == kC) {
+      const float4 u = *reinterpret_cast<const float4 *>(w + j0 + j);
+      wj[0] = u.x;
+      wj[1] = u.y;
+      wj[2] = u.z;
+      wj[3] = u.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) wj[e] = j0 + j + e < n ? tab[n - 1 - j0 - j - e] : 0.0f;
+    }
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint16_t raw =
+          *reinterpret_cast<const uint16_t *>(base + (j + e) * 128 + ((chunk ^ ((j + e) & 7)) << 4));
+      x[e] = __uint_as_float(static_cast<uint32_t>(raw) << 16) * wj[e];
+    }
+    if (n != kC) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j0 + j + e >= n) x[e] = 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      t0[(j + e) / 2] = take_bf16(x[e], x[e + 1]);
+      t1[(j + e) / 2] = take_bf16(x[e], x[e + 1]);
+      t2[(j + e) / 2] = take_bf16(x[e], x[e + 1]);
+    }
+  }
+  tmem_st16(ta, t0);
+  tmem_st16(ta + 16, t1);
+  tmem_st16(ta + 32, t2);
+}
+
+// zero rows [n, 64) of a staged tile of `blocks` 8 KB blocks (the tokens
+// after a sequence's end belong to others, and 0 x NaN is NaN)
+__device__ __forceinline__ void zero_rows(uint8_t *tile, int blocks, int n, int tid, int nthreads) {
+  const int rows = kC - n;
+  for (int i = tid; i < blocks * rows * 8; i += nthreads) {
+    const int b = i / (rows * 8), r = i - b * rows * 8;
+    *reinterpret_cast<uint4 *>(tile + b * kBlk + n * 128 + r * 16) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// half of the update product: U[d_v][d_k] += V~^T K over 32 tokens
+template <int kDk>
+__device__ __forceinline__ void mma_update(uint32_t u, uint32_t vt, uint32_t k, bool accumulate) {
+  constexpr uint32_t idesc = idesc_make(128, kDk, 1) | kTransB;
+#pragma unroll
+  for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+      mma_ts_bf16(u, vt + 16 * t + 8 * kk, sdesc_mn(k + kk * 2048, kBlk), idesc,
+                  (accumulate || t + kk > 0) ? 1u : 0u);
+}
+
+__device__ __forceinline__ void fail(const DecayArgs &a, volatile int *abort_flag, int site) {
+  *abort_flag = 1;
+  report_error(a.status, MOE_ERR_DEVICE_TIMEOUT, KID_DECAY * 100 + site);
+}
+
+// one warp's wait: false in every lane when it ran out or the CTA aborted
+__device__ __forceinline__ bool warp_wait(const DecayArgs &a, uint32_t bar, uint32_t parity,
+                                          volatile int *abort_flag, int site) {
+  const bool ok = mbar_wait(bar, parity, MOE_WAIT_LIMIT_CYCLES, abort_flag);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  if ((threadIdx.x & 31) == 0) fail(a, abort_flag, site);
+  return false;
+}
+__device__ __forceinline__ bool lane_wait(const DecayArgs &a, uint32_t bar, uint32_t parity,
+                                          volatile int *abort_flag, int site) {
+  if (mbar_wait(bar, parity, MOE_WAIT_LIMIT_CYCLES, abort_flag)) return true;
+  fail(a, abort_flag, site);
+  return false;
+}
+// this warp's writes (TMEM and shared memory) before its arrival
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
+  return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) &
+                                     ~static_cast<uintptr_t>(1023));
+}
+
+// Shared memory: P hi and lo, then the stages of (Q, K, V), Q~ (fp32), control.
+// (The scores' A operand starts 64 rows before Q, so something lies there.)
+template <int kDk, bool kOut>
+struct Smem {
+  static constexpr int kP = 0;
+  static constexpr int kStages = kOut ? 2 * kBlk : 0;
+  static constexpr int kQ = kOut ? kDk / 64 * kBlk : 0, kK = kDk / 64 * kBlk, kV = 2 * kBlk;
+  static constexpr int kStage = kQ + kK + kV;
+  static constexpr int kQf = kStages + kStg * kStage;  // kDk / 32 blocks of 64 x 128 bytes
+  static constexpr int kCtl = kQf + (kOut ? kDk / 32 * kBlk : 0);
+  static constexpr int kTotal = kCtl + 1536 + 1024;
+};
+
+struct Ctl {
+  uint64_t bars[32];
+  uint32_t tmem;
+  int abort_flag;
+  int scratch[36];
+  alignas(16) float tab[72];  // lambda^0 .. lambda^64
+  alignas(16) float w[kC];    // lambda^63 .. lambda^0
+};
+static_assert(sizeof(Ctl) <= 1536, "control block");
+
+}  // namespace
+
+// ws: what each segment leaves -> the state before the next segment, in place,
+// along each sequence.  One thread per 4 elements of a (sequence, head) state.
+__global__ void __launch_bounds__(256) decay_chain_kernel(const DecayArgs a, int dk) {
+  __shared__ int scratch[36];
+  const long long per = static_cast<long long>(a.dv) * dk / 4;  // vectors of a state
+  const int blocks = static_cast<int>((per + 255) / 256);
+  const int hb = static_cast<int>(blockIdx.x % (a.Hv * blocks));
+  const int h = hb / blocks;
+  const long long e = static_cast<long long>(hb % blocks) * 256 + threadIdx.x;
+  pdl_wait();
+  // the item list is walked sequence by sequence: block y starts at the y-th
+  // sequence of more than one segment by looking for its first segment
+  long long item = blockIdx.x / (a.Hv * blocks);
+  const Segment g = find_segment(a, item, scratch);
+  if (g.seq < 0 || g.index != 0 || g.last) return;
+  long long first, len;
+  seq_range(a, g.seq, first, len);
+  const long long n = (len + a.seg_len - 1) / a.seg_len - 1;  // slots of the sequence
+  if (e >= per || g.slot + 1 + n > a.slots) return;
+  const float f = decay_pow(a.decay[h], static_cast<float>(a.seg_len));
+  const long long step = static_cast<long long>(a.Hv) * per;
+  float4 *w = reinterpret_cast<float4 *>(a.ws) + ((g.slot + 1) * a.Hv + h) * per + e;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.s_in) s = reinterpret_cast<const float4 *>(a.s_in)[(static_cast<long long>(g.seq) * a.Hv + h) * per + e];
+  for (long long i0 = 0; i0 < n; i0 += 4) {
+    float4 u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i0 + i < n) u[i] = w[(i0 + i) * step];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i0 + i < n) {
+        s.x = fmaf(f, s.x, u[i].x);
+        s.y = fmaf(f, s.y, u[i].y);
+        s.z = fmaf(f, s.z, u[i].z);
+        s.w = fmaf(f, s.w, u[i].w);
+        w[(i0 + i) * step] = s;
+      }
+  }
+}
+
+// kOut: the segment's outputs, from the state before it (of its sequence, or
+// slot g.slot), and the final state if it is the sequence's last.  Otherwise:
+// what the segment leaves from a zero state, into slot g.slot + 1, unless it
+// is the last.
+template <int kDk, bool kOut>
+__global__ void __launch_bounds__(kThreadsC, 1)
+    decay_chunk_kernel(const __grid_constant__ CUtensorMap tmQ,
+                       const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const DecayArgs a) {
+  using L = Smem<kDk, kOut>;
+  using M = Cols<kDk, kOut>;
+  constexpr int kHalfDk = kDk / 2;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = align1024(smem_raw);
+  Ctl &ctl = *reinterpret_cast<Ctl *>(smem + L::kCtl);
+  volatile int *abort_flag = &ctl.abort_flag;
+  const uint32_t full0 = smem_u32(ctl.bars), empty0 = full0 + 8 * kStg;
+  const uint32_t bar = empty0 + 8 * kStg;
+  const uint32_t sc_full = bar, p_full = bar + 8, qf_full = bar + 16, s_ready = bar + 24;
+  const uint32_t i_done = bar + 32, o_full = bar + 40, o_empty = bar + 48, drain = bar + 56;
+  const uint32_t vt_full0 = bar + 64, vt_empty0 = bar + 80, u_full0 = bar + 96, u_empty0 = bar + 112;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3;
+  const int ht = static_cast<int>(blockIdx.x % (a.Hv * a.tiles));
+  const int h = ht / a.tiles, d0 = ht % a.tiles * 128;
+  pdl_wait();
+  const Segment g = find_segment(a, blockIdx.x / (a.Hv * a.tiles), ctl.scratch);
+  if (g.seq < 0 || (!kOut && (g.last || g.slot + 1 >= a.slots))) return;
+  const int nc = static_cast<int>((g.len + kC - 1) / kC);
+  const float lam = a.decay[h];
+  if (threadIdx.x <= kC) {
+    const float p = decay_pow(lam, static_cast<float>(threadIdx.x));
+    ctl.tab[threadIdx.x] = p;
+    if (threadIdx.x < kC) ctl.w[kC - 1 - threadIdx.x] = p;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStg; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    mbar_init(sc_full, 1);
+    mbar_init(p_full, 2);
+    mbar_init(qf_full, 4);
+    mbar_init(s_ready, 8);
+    mbar_init(i_done, 1);
+    mbar_init(o_full, 1);
+    mbar_init(o_empty, 8);
+    mbar_init(drain, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(vt_full0 + 8 * b, 4);
+      mbar_init(vt_empty0 + 8 * b, 1);
+      mbar_init(u_full0 + 8 * b, 1);
+      mbar_init(u_empty0 + 8 * b, 8);
+    }
+    ctl.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&ctl.tmem), kTmemAll);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem;
+  const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+  const int tail = static_cast<int>(g.len - static_cast<long long>(nc - 1) * kC);  // tokens of the last chunk
+  const uint32_t stages = smem_u32(smem) + L::kStages;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_last();
+      const int hk = h / (a.Hv / a.Hk);
+      int c = 0;
+      for (; c < nc; ++c) {
+        const int s = c % kStg;
+        if (!lane_wait(a, empty0 + 8 * s, ((c / kStg) & 1) ^ 1, abort_flag, SITE_PRODUCER_EMPTY)) break;
+        const uint32_t dst = stages + s * L::kStage, fb = full0 + 8 * s;
+        const int y = static_cast<int>(g.first) + c * kC;
+        mbar_arrive_expect_tx(fb, L::kStage);
+        for (int b = 0; b < kDk / 64; ++b) {
+          tma_load_2d(dst + L::kQ + b * kBlk, &tmK, fb, hk * kDk + 64 * b, y, pol);
+          if (kOut) tma_load_2d(dst + b * kBlk, &tmQ, fb, hk * kDk + 64 * b, y, pol);
+        }
+        for (int b = 0; b < 2; ++b)
+          tma_load_2d(dst + L::kQ + L::kK + b * kBlk, &tmV, fb, h * a.dv + d0 + 64 * b, y, pol);
+      }
+      if (*abort_flag)
+        for (int i = max(0, c - kStg); i < c; ++i)
+          mbar_wait(full0 + 8 * (i % kStg), (i / kStg) & 1, MOE_WAIT_LIMIT_CYCLES, nullptr);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t id_sc = idesc_make(128, kC, 1);
+      constexpr uint32_t id_o1 = idesc_make(128, kC, 2);
+      constexpr uint32_t id_o2 = idesc_make(128, kC, 1) | kTransA;
+      const uint32_t qf = smem_u32(smem) + L::kQf, pb = smem_u32(smem) + L::kP;
+      // Scores of a staged chunk, queries in rows 64..127 of the A operand:
+      // rows 0..63 are the 8 KB before each block of Q, and their results
+      // (lanes 0..63) are not read.
+      auto scores = [&](int c) {
+        if (!lane_wait(a, full0 + 8 * (c % kStg), (c / kStg) & 1, abort_flag, SITE_MMA_FULL)) return false;
+        tc_fence_after();
+        const uint32_t q = stages + (c % kStg) * L::kStage, k = q + L::kQ;
+#pragma unroll
+        for (int kk = 0; kk < kDk / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kBlk + 32 * (kk & 3);
+          MmaKind<__nv_bfloat16>::mma(tmem + M::P, sdesc_sw128(q + off - kBlk), sdesc_sw128(k + off),
+                                      id_sc, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(sc_full);
+        return true;
+      };
+      auto update = [&](int c) {
+        const int ub = c % M::kUBufs, use = c / M::kUBufs;
+        const uint32_t k = stages + (c % kStg) * L::kStage + L::kQ, u = tmem + M::U + ub * kDk;
+        if (!kOut && !lane_wait(a, full0 + 8 * (c % kStg), (c / kStg) & 1, abort_flag, SITE_MMA_FULL)) return false;
+        if (!lane_wait(a, u_empty0 + 8 * ub, (use & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY)) return false;
+        for (int b = 0; b < 2; ++b) {
+          if (!lane_wait(a, vt_full0 + 8 * b, c & 1, abort_flag, SITE_STAGE)) return false;
+          tc_fence_after();
+          mma_update<kDk>(u, tmem + M::V + b * kTerms * 16, k + b * 4096, b > 0);
+          tc_commit(vt_empty0 + 8 * b);
+        }
+        tc_commit(u_full0 + 8 * ub);
+        return true;
+      };
+      if (kOut) {
+        bool ok = nc == 0 || (scores(0) && update(0));
+        for (int c = 0; ok && c < nc; ++c) {
+          const uint32_t ph = c & 1;
+          const uint32_t st = stages + (c % kStg) * L::kStage;
+          if (!lane_wait(a, s_ready, ph, abort_flag, SITE_STAGE) ||
+              !lane_wait(a, qf_full, ph, abort_flag, SITE_STAGE) ||
+              (c > 0 && !lane_wait(a, o_empty, ph ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY)))
+            break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kDk / 8; ++kk)
+            mma_ts_tf32(tmem + M::O, tmem + M::S + 8 * kk,
+                        sdesc_sw128(qf + (kk >> 2) * kBlk + 32 * (kk & 3)), id_o1, kk > 0 ? 1u : 0u);
+          tc_commit(i_done);
+          if (!lane_wait(a, p_full, ph, abort_flag, SITE_STAGE)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int kk = 0; kk < kC / 16; ++kk)
+              MmaKind<__nv_bfloat16>::mma(tmem + M::O, sdesc_mn(st + L::kQ + L::kK + kk * 2048, kBlk),
+                                          sdesc_sw128(pb + t * kBlk + 32 * kk), id_o2, 1u);
+          tc_commit(o_full);
+          tc_commit(empty0 + 8 * (c % kStg));
+          ok = c + 1 == nc || (scores(c + 1) && update(c + 1));
+        }
+      } else {
+        for (int c = 0; c < nc; ++c) {
+          if (!update(c)) break;
+          tc_commit(empty0 + 8 * (c % kStg));
+        }
+      }
+      tc_commit(drain);
+    }
+  } else if (kOut && warp < 4) {
+    // ------------------------------------------------------------ P
+    const int i = (wq - 2) * 32 + lane;
+    float w[kC];  // lambda^(i - j)
+#pragma unroll
+    for (int j = 0; j < kC; ++j) w[j] = j <= i ? ctl.tab[i - j] : 0.0f;
+    uint8_t *row = smem + L::kP + i * 128;
+    for (int c = 0; c < nc; ++c) {
+      if (!warp_wait(a, sc_full, c & 1, abort_flag, SITE_EPI_TMEM_FULL)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int j0 = 0; j0 < kC; j0 += 16) {
+        float v[16];
+        tmem_ld16_sync(tmem + M::P + lanes + j0, v);
+#pragma unroll
+        for (int x = 0; x < 16; x += 8) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const int j = j0 + x + e;  // (a score past the diagonal may be anything)
+            float p = j <= i ? v[x + e] * w[j] : 0.0f;
+            float q = j + 1 <= i ? v[x + e + 1] * w[j + 1] : 0.0f;
+            hi[e / 2] = take_bf16(p, q);
+            lo[e / 2] = take_bf16(p, q);
+          }
+          const int at = (((j0 + x) >> 3) ^ (i & 7)) << 4;
+          *reinterpret_cast<uint4 *>(row + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4 *>(row + kBlk + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      warp_arrive(p_full);
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------------------ V~, Q~
+    const int r = (threadIdx.x - 128) >> 1, hf = threadIdx.x & 1;  // Q~: half of a row
+    const float f = ctl.tab[r + 1];
+    for (int c = 0; c < nc; ++c) {
+      const int s = c % kStg, n = c == nc - 1 ? tail : kC;
+      if (!warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL)) break;
+      uint8_t *st = smem + L::kStages + s * L::kStage;
+      if (n < kC) {
+        zero_rows(st + L::kQ, kDk / 64 + 2, n, threadIdx.x - 128, 128);
+        fence_proxy_async_smem();
+      }
+      bool ok = true;
+      for (int b = 0; ok && b < 2; ++b) {
+        ok = warp_wait(a, vt_empty0 + 8 * b, (c & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY);
+        if (!ok) break;
+        tc_fence_after();
+        make_vt(st + L::kQ + L::kK, wq * 32 + lane, ctl.w, ctl.tab, n, 32 * b,
+                tmem + M::V + b * kTerms * 16 + lanes);
+        tmem_wait_st();
+        warp_arrive(vt_full0 + 8 * b);
+      }
+      if (!ok) break;
+      if (kOut) {
+        if (c > 0 && !warp_wait(a, i_done, (c & 1) ^ 1, abort_flag, SITE_DRAIN)) break;
+        const uint8_t *src = st + r * 128;
+        uint8_t *dst = smem + L::kQf + r * 128;
+#pragma unroll 4
+        for (int y = 0; y < kDk / 16; ++y) {  // 8 elements: 16 bytes of bf16, 32 of fp32
+          const int x = 2 * y + hf;
+          const uint4 u = *reinterpret_cast<const uint4 *>(src + (x >> 3) * kBlk + (((x & 7) ^ (r & 7)) << 4));
+          const uint32_t q[4] = {u.x, u.y, u.z, u.w};
+          float t[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            t[2 * e] = to_tf32(__uint_as_float(q[e] << 16) * f);
+            t[2 * e + 1] = to_tf32(__uint_as_float(q[e] & 0xffff0000u) * f);
+          }
+          uint8_t *blk = dst + (x >> 2) * kBlk;
+          const int p0 = (2 * (x & 3)) ^ (r & 7);
+          *reinterpret_cast<float4 *>(blk + (p0 << 4)) = make_float4(t[0], t[1], t[2], t[3]);
+          *reinterpret_cast<float4 *>(blk + ((p0 ^ 1) << 4)) = make_float4(t[4], t[5], t[6], t[7]);
+        }
+        fence_proxy_async_smem();
+        warp_arrive(qf_full);
+      }
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------ state, O
+    const int half = (warp - 8) >> 2;
+    const int d = d0 + wq * 32 + lane;
+    const bool valid = d < a.dv;
+    const long long srow = ((static_cast<long long>(g.seq) * a.Hv + h) * a.dv + d) * kDk + half * kHalfDk;
+    float S[kHalfDk];
+    const float *src = nullptr;
+    if (kOut && valid) {
+      if (g.index == 0)
+        src = a.s_in ? a.s_in + srow : nullptr;
+      else if (g.slot < a.slots)
+        src = a.ws + ((g.slot * a.Hv + h) * a.dv + d) * kDk + half * kHalfDk;
+    }
+#pragma unroll
+    for (int i = 0; i < kHalfDk; i += 4) {
+      const float4 u = src ? *reinterpret_cast<const float4 *>(src + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+      S[i] = u.x;
+      S[i + 1] = u.y;
+      S[i + 2] = u.z;
+      S[i + 3] = u.w;
+    }
+    const uint32_t ts = tmem + M::S + half * kHalfDk + lanes;
+    auto put_state = [&] {
+#pragma unroll
+      for (int x = 0; x < kHalfDk; x += 16) {
+        uint32_t r[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(S[x + i]);
+        tmem_st16(ts + x, r);
+      }
+      tmem_wait_st();
+      warp_arrive(s_ready);
+    };
+    if (kOut) put_state();
+    bool ok = true;
+    for (int c = 0; c < nc; ++c) {
+      const int n = c == nc - 1 ? tail : kC;
+      const int ub = c % M::kUBufs, use = c / M::kUBufs;
+      const float f = ctl.tab[n];
+      ok = warp_wait(a, u_full0 + 8 * ub, use & 1, abort_flag, SITE_EPI_TMEM_FULL);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int x = 0; x < kHalfDk; x += 16) {
+        float u[16];
+        tmem_ld16_sync(tmem + M::U + ub * kDk + half * kHalfDk + x + lanes, u);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) S[x + i] = fmaf(f, S[x + i], u[i]);
+      }
+      warp_arrive(u_empty0 + 8 * ub);
+      if (kOut) {
+        if (c + 1 < nc) {
+          ok = warp_wait(a, i_done, c & 1, abort_flag, SITE_DRAIN);
+          if (!ok) break;
+          tc_fence_after();
+          put_state();
+        }
+        ok = warp_wait(a, o_full, c & 1, abort_flag, SITE_EPI_TMEM_FULL);
+        if (!ok) break;
+        tc_fence_after();
+        float v[32];  // tokens 32 half .. of this d_v row
+        tmem_ld32_sync(tmem + M::O + 32 * half + lanes, v);
+        warp_arrive(o_empty);
+        if (valid) {
+          const long long ostride = static_cast<long long>(a.Hv) * a.dv;
+          __nv_bfloat16 *o = a.o + (g.first + static_cast<long long>(c) * kC + 32 * half) * ostride +
+                             static_cast<long long>(h) * a.dv + d;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (32 * half + i < n) o[i * ostride] = __float2bfloat16_rn(v[i]);
+        }
+      }
+    }
+    float *dst = nullptr;
+    if (ok && valid) {
+      if (!kOut)
+        dst = a.ws + (((g.slot + 1) * a.Hv + h) * a.dv + d) * kDk + half * kHalfDk;
+      else if (g.last && a.s_out)
+        dst = a.s_out + srow;
+    }
+    if (dst) {
+#pragma unroll
+      for (int i = 0; i < kHalfDk; i += 4)
+        *reinterpret_cast<float4 *>(dst + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+    }
+  }
+  __syncwarp();
+  const bool fin = mbar_wait(drain, 0, MOE_WAIT_LIMIT_CYCLES, nullptr);
+  if (!__all_sync(0xffffffffu, fin) && lane == 0) fail(a, abort_flag, SITE_DRAIN);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kTmemAll);
+}
+
+namespace {
+
+template <typename K, typename... Args>
+cudaError_t launch_pdl(K kern, long long grid, int threads, int smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int kDk>
+cudaError_t launch_chunked(const DecayArgs &a, const CUtensorMap &mq, const CUtensorMap &mk,
+                           const CUtensorMap &mv, bool segmented, cudaStream_t st) {
+  const long long per = static_cast<long long>(a.Hv) * a.tiles;
+  if (segmented) {
+    cudaError_t e = launch_pdl(decay_chunk_kernel<kDk, false>, a.items * per, kThreadsC,
+                               Smem<kDk, false>::kTotal, st, mq, mk, mv, a);
+    if (e != cudaSuccess) return e;
+    const long long blocks = (static_cast<long long>(a.dv) * kDk / 4 + 255) / 256;
+    e = launch_pdl(decay_chain_kernel, a.items * a.Hv * blocks, 256, 0, st, a, kDk);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(decay_chunk_kernel<kDk, true>, a.items * per, kThreadsC, Smem<kDk, true>::kTotal,
+                    st, mq, mk, mv, a);
+}
+
+}  // namespace
+
+bool decay_chunk_setup() {
+  auto set = [](auto kern, int bytes) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+  };
+  return set(decay_chunk_kernel<128, true>, Smem<128, true>::kTotal) &&
+         set(decay_chunk_kernel<64, true>, Smem<64, true>::kTotal) &&
+         set(decay_chunk_kernel<128, false>, Smem<128, false>::kTotal) &&
+         set(decay_chunk_kernel<64, false>, Smem<64, false>::kTotal);
+}
+
+cudaError_t launch_decay_chunked(const DecayArgs &a, int dk, const CUtensorMap &mq,
+                                 const CUtensorMap &mk, const CUtensorMap &mv, bool segmented,
+                                 cudaStream_t st) {
+  return dk == 128 ? launch_chunked<128>(a, mq, mk, mv, segmented, st)
+                   : launch_chunked<64>(a, mq, mk, mv, segmented, st);
+}
+
+}  // namespace moe

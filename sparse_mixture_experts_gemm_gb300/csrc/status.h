@@ -13,6 +13,7 @@ enum KernelId {
   KID_COMBINE = 5,
   KID_DECODE = 6,
   KID_MATMUL_FP8 = 7,
+  KID_DECAY = 8,
   KID_DEBUG = 9,
 };
 

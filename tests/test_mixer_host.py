@@ -200,9 +200,10 @@ def test_decay_scan_refusals(lib, kw, code):
 def test_decay_workspace_is_asked_for(lib):
     """A call that needs a workspace is refused without one."""
     need = ctypes.c_size_t(0)
-    assert lib.gdn_decay_workspace(16, 2, 4, 128, 64, None) == moe.MOE_ERR_INVALID_ARG
-    assert lib.gdn_decay_workspace(-1, 2, 4, 128, 64, ctypes.byref(need)) == moe.MOE_ERR_INVALID_ARG
-    assert lib.gdn_decay_workspace(65536, 1, 4, 128, 128, ctypes.byref(need)) == moe.MOE_OK
+    assert lib.gdn_decay_workspace(16, 2, 0, 4, 128, 64, None) == moe.MOE_ERR_INVALID_ARG
+    assert lib.gdn_decay_workspace(-1, 2, 0, 4, 128, 64, ctypes.byref(need)) == moe.MOE_ERR_INVALID_ARG
+    assert lib.gdn_decay_workspace(65536, 1, 0, 4, 128, 128, ctypes.byref(need)) == moe.MOE_OK
+    assert need.value % (4 * 4 * 128 * 128) == 0  # whole states
     if need.value:
         for ws, n in ((None, need.value), (P, need.value - 1)):
             assert lib.gdn_decay_scan(P, P, P, P, None, P, P, None, 65536, 1, 4, 4, 128, 128, 512, 512,
