@@ -108,20 +108,84 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// bf16 parts of a pair of floats, the first in the low half: returns the
-// nearest bf16 pair and leaves the remainders in a, b
-__device__ __forceinline__ uint32_t take_bf16(float &a, float &b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  const uint32_t u = *reinterpret_cast<const uint32_t *>(&h);
-  a -= __uint_as_float(u << 16);
-  b -= __uint_as_float(u & 0xffff0000u);
-  return u;
+// Pairs of floats in one 64-bit register: one instruction for two operations.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
 }
 
-__device__ __forceinline__ float to_tf32(float x) {
-  uint32_t u;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(u) : "f"(x));
-  return __uint_as_float(u);
+// The leading bf16 parts of a pair (its upper halves, the first in the low
+// half of the result); `v` keeps what they leave.  Cutting instead of rounding
+// leaves the remainder exact and one bit longer: three parts hold all 24 bits.
+__device__ __forceinline__ uint32_t high_parts(f32x2 v) {
+  float a, b;
+  unpack2(v, a, b);
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ uint32_t take_bf16(f32x2 &v) {
+  float a, b;
+  unpack2(v, a, b);
+  const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+  v = sub2(v, pack2(__uint_as_float(x & 0xffff0000u), __uint_as_float(y & 0xffff0000u)));
+  return __byte_perm(x, y, 0x7632);
+}
+
+// one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+// shared-memory accesses by 32-bit address
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+// four 8 x 8 matrices of 16-bit values, transposed: lane l gets entries
+// (column l / 4; rows 2 (l % 4), + 1) of each; lanes 8 m .. 8 m + 7 give the
+// addresses of matrix m's rows
+__device__ __forceinline__ void ldsm4_trans(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+// 16 lanes x 16 columns: lane l of the warp holds rows l / 4 (even registers)
+// and l / 4 + 8 (odd) of column l % 4 of each group of four
+__device__ __forceinline__ void tmem_st_16x16(uint32_t ta, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(ta),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // The segment that work item `item` stands for.
@@ -216,71 +280,76 @@ __device__ __forceinline__ Segment find_segment(const DecayArgs &a, long long it
   return g;
 }
 
-// V~ of tokens j0 .. j0 + 31 of a chunk for one d_v column, as kTerms bf16
-// parts of two tokens per TMEM column: token j's value times `w`[j], or, in a
-// sequence's last chunk of n < 64 tokens, times tab[n - 1 - j] (0 from n on).
-// `v` points at the staged V (128-byte swizzle).
-__device__ __forceinline__ void make_vt(const uint8_t *v, int col, const float *w, const float *tab,
-                                        int n, int j0, uint32_t ta) {
-  const int chunk = (col & 63) >> 3;
-  const uint8_t *base = v + (col >> 6) * kBlk + (col & 7) * 2 + j0 * 128;
-  uint32_t t0[16], t1[16], t2[16];
+// V~ of tokens j0 .. j0 + 31 of a chunk for a warp's 32 columns of V: the
+// staged V (address `v`, 128-byte swizzle) times a weight per token, as kTerms
+// bf16 parts of two tokens per TMEM column, [d_v lane][token pair].  Transposed
+// matrix loads give lane l tokens 8 i + 2 (l % 4), + 1 of columns l / 4, + 8 of
+// each 16, the layout of a 16-lane TMEM store; w[j0 / 8 + i] are those tokens'
+// weights.
+__device__ __forceinline__ void make_vt(uint32_t v, int wq, const f32x2 (&w)[8], int j0,
+                                        uint32_t ta) {
+  const int lane = threadIdx.x & 31, m = lane >> 3;
+  const uint32_t row = v + (wq >> 1) * kBlk + (j0 + 8 * (m >> 1) + (lane & 7)) * 128;
+#pragma unroll 1
+  for (int hl = 0; hl < 2; ++hl) {
+    const uint32_t at = row + ((((wq & 1) * 4 + 2 * hl + (m & 1)) ^ (lane & 7)) << 4);
+    uint32_t p[kTerms][8];
 #pragma unroll
-  for (int j = 0; j < 32; j += 4) {
-    float wj[4];
-    if (n == kC) {
-      const float4 u = *reinterpret_cast<const float4 *>(w + j0 + j);
-      wj[0] = u.x;
-      wj[1] = u.y;
-      wj[2] = u.z;
-      wj[3] = u.w;
-    } else {
+    for (int g = 0; g < 2; ++g) {  // 16 tokens
+      uint32_t r[4];
+      ldsm4_trans(at + g * 2048, r);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) wj[e] = j0 + j + e < n ? tab[n - 1 - j0 - j - e] : 0.0f;
-    }
-    float x[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint16_t raw =
-          *reinterpret_cast<const uint16_t *>(base + (j + e) * 128 + ((chunk ^ ((j + e) & 7)) << 4));
-      x[e] = __uint_as_float(static_cast<uint32_t>(raw) << 16) * wj[e];
-    }
-    if (n != kC) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (j0 + j + e >= n) x[e] = 0.0f;
+      for (int e = 0; e < 4; ++e) {
+        const int i = 2 * g + (e >> 1);
+        f32x2 x = pack2(__uint_as_float(r[e] << 16), __uint_as_float(r[e] & 0xffff0000u));
+        x = mul2(x, w[j0 / 8 + i]);
+        p[0][4 * g + e] = take_bf16(x);
+        p[1][4 * g + e] = take_bf16(x);
+        p[2][4 * g + e] = high_parts(x);
+      }
     }
 #pragma unroll
-    for (int e = 0; e < 4; e += 2) {
-      t0[(j + e) / 2] = take_bf16(x[e], x[e + 1]);
-      t1[(j + e) / 2] = take_bf16(x[e], x[e + 1]);
-      t2[(j + e) / 2] = take_bf16(x[e], x[e + 1]);
-    }
+    for (int t = 0; t < kTerms; ++t)
+      tmem_st_16x16(ta + 16 * t + (static_cast<uint32_t>(16 * hl) << 16), p[t]);
   }
-  tmem_st16(ta, t0);
-  tmem_st16(ta + 16, t1);
-  tmem_st16(ta + 32, t2);
 }
 
-// zero rows [n, 64) of a staged tile of `blocks` 8 KB blocks (the tokens
-// after a sequence's end belong to others, and 0 x NaN is NaN)
-__device__ __forceinline__ void zero_rows(uint8_t *tile, int blocks, int n, int tid, int nthreads) {
-  const int rows = kC - n;
-  for (int i = tid; i < blocks * rows * 8; i += nthreads) {
-    const int b = i / (rows * 8), r = i - b * rows * 8;
-    *reinterpret_cast<uint4 *>(tile + b * kBlk + n * 128 + r * 16) = make_uint4(0, 0, 0, 0);
+// the weights of make_vt for a chunk of n tokens: tab[n - 1 - t] of token t
+__device__ __forceinline__ void vt_weights(const float *tab, int n, f32x2 (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int t = 8 * i + 2 * (threadIdx.x & 3);
+    w[i] = pack2(t < n ? tab[n - 1 - t] : 0.0f, t + 1 < n ? tab[n - 2 - t] : 0.0f);
   }
+}
+
+// Rows [n, 64) of the staged K and of warp wq's columns of V become zero: the
+// tokens after a sequence's end belong to others, and 0 x NaN is NaN.  Each
+// warp reads only its own columns of V.
+template <int kDk>
+__device__ __forceinline__ void zero_rows(uint32_t k, uint32_t v, int wq, int n) {
+  const int lane = threadIdx.x & 31, rows = kC - n;
+  for (int i = lane; i < rows * 4; i += 32) {
+    const int r = n + (i >> 2), p = ((wq & 1) * 4 + (i & 3)) ^ (r & 7);
+    sts128(v + (wq >> 1) * kBlk + r * 128 + (p << 4), 0u, 0u, 0u, 0u);
+  }
+  for (int i = wq * 32 + lane; i < kDk / 64 * rows * 8; i += 128) {
+    const int b = i / (rows * 8), p = i - b * rows * 8;
+    sts128(k + b * kBlk + n * 128 + p * 16, 0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
 }
 
 // half of the update product: U[d_v][d_k] += V~^T K over 32 tokens
 template <int kDk>
-__device__ __forceinline__ void mma_update(uint32_t u, uint32_t vt, uint32_t k, bool accumulate) {
+__device__ __forceinline__ void mma_update(uint32_t u, uint32_t vt, uint64_t k, bool accumulate) {
   constexpr uint32_t idesc = idesc_make(128, kDk, 1) | kTransB;
 #pragma unroll
   for (int t = 0; t < kTerms; ++t)
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk)
-      mma_ts_bf16(u, vt + 16 * t + 8 * kk, sdesc_mn(k + kk * 2048, kBlk), idesc,
+      mma_ts_bf16(u, vt + 16 * t + 8 * kk, k + kk * (2048 >> 4), idesc,
                   (accumulate || t + kk > 0) ? 1u : 0u);
 }
 
@@ -289,18 +358,22 @@ __device__ __forceinline__ void fail(const DecayArgs &a, volatile int *abort_fla
   report_error(a.status, MOE_ERR_DEVICE_TIMEOUT, KID_DECAY * 100 + site);
 }
 
-// one warp's wait: false in every lane when it ran out or the CTA aborted
-__device__ __forceinline__ bool warp_wait(const DecayArgs &a, uint32_t bar, uint32_t parity,
-                                          volatile int *abort_flag, int site) {
-  const bool ok = mbar_wait(bar, parity, MOE_WAIT_LIMIT_CYCLES, abort_flag);
-  if (__all_sync(0xffffffffu, ok)) return true;
-  if ((threadIdx.x & 31) == 0) fail(a, abort_flag, site);
+// A warp's wait for phase `parity`: false in every lane when the CTA aborted
+// or the polls (a few us each at most) ran out.  Short on purpose: it is
+// inlined at each wait, and the roles share one instruction cache.
+constexpr int kPolls = 1 << 22;
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, const volatile int *abort_flag) {
+#pragma unroll 1
+  for (int i = 0; i < kPolls; ++i) {
+    if (mbar_try_wait_sleep(bar, parity, 4000u)) return true;
+    if (abort_flag && *abort_flag) return false;
+  }
   return false;
 }
-__device__ __forceinline__ bool lane_wait(const DecayArgs &a, uint32_t bar, uint32_t parity,
+__device__ __forceinline__ bool warp_wait(const DecayArgs &a, uint32_t bar, uint32_t parity,
                                           volatile int *abort_flag, int site) {
-  if (mbar_wait(bar, parity, MOE_WAIT_LIMIT_CYCLES, abort_flag)) return true;
-  fail(a, abort_flag, site);
+  if (__all_sync(0xffffffffu, poll(bar, parity, abort_flag))) return true;
+  if ((threadIdx.x & 31) == 0) fail(a, abort_flag, site);
   return false;
 }
 // this warp's writes (TMEM and shared memory) before its arrival
@@ -333,8 +406,8 @@ struct Ctl {
   uint32_t tmem;
   int abort_flag;
   int scratch[36];
-  alignas(16) float tab[72];  // lambda^0 .. lambda^64
-  alignas(16) float w[kC];    // lambda^63 .. lambda^0
+  float tab[kC + 1];   // lambda^0 .. lambda^64
+  float rtab[2 * kC];  // lambda^63 .. lambda^0, then zeros
 };
 static_assert(sizeof(Ctl) <= 1536, "control block");
 
@@ -413,7 +486,10 @@ __global__ void __launch_bounds__(kThreadsC, 1)
   if (threadIdx.x <= kC) {
     const float p = decay_pow(lam, static_cast<float>(threadIdx.x));
     ctl.tab[threadIdx.x] = p;
-    if (threadIdx.x < kC) ctl.w[kC - 1 - threadIdx.x] = p;
+    if (threadIdx.x < kC) {
+      ctl.rtab[kC - 1 - threadIdx.x] = p;
+      ctl.rtab[kC + threadIdx.x] = 0.0f;
+    }
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStg; ++s) {
@@ -444,7 +520,6 @@ __global__ void __launch_bounds__(kThreadsC, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = ctl.tmem;
   const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
   const int tail = static_cast<int>(g.len - static_cast<long long>(nc - 1) * kC);  // tokens of the last chunk
   const uint32_t stages = smem_u32(smem) + L::kStages;
@@ -457,7 +532,10 @@ __global__ void __launch_bounds__(kThreadsC, 1)
       int c = 0;
       for (; c < nc; ++c) {
         const int s = c % kStg;
-        if (!lane_wait(a, empty0 + 8 * s, ((c / kStg) & 1) ^ 1, abort_flag, SITE_PRODUCER_EMPTY)) break;
+        if (!poll(empty0 + 8 * s, ((c / kStg) & 1) ^ 1, abort_flag)) {
+          fail(a, abort_flag, SITE_PRODUCER_EMPTY);
+          break;
+        }
         const uint32_t dst = stages + s * L::kStage, fb = full0 + 8 * s;
         const int y = static_cast<int>(g.first) + c * kC;
         mbar_arrive_expect_tx(fb, L::kStage);
@@ -470,108 +548,124 @@ __global__ void __launch_bounds__(kThreadsC, 1)
       }
       if (*abort_flag)
         for (int i = max(0, c - kStg); i < c; ++i)
-          mbar_wait(full0 + 8 * (i % kStg), (i / kStg) & 1, MOE_WAIT_LIMIT_CYCLES, nullptr);
+          poll(full0 + 8 * (i % kStg), (i / kStg) & 1, nullptr);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id_sc = idesc_make(128, kC, 1);
-      constexpr uint32_t id_o1 = idesc_make(128, kC, 2);
-      constexpr uint32_t id_o2 = idesc_make(128, kC, 1) | kTransA;
-      const uint32_t qf = smem_u32(smem) + L::kQf, pb = smem_u32(smem) + L::kP;
-      // Scores of a staged chunk, queries in rows 64..127 of the A operand:
-      // rows 0..63 are the 8 KB before each block of Q, and their results
-      // (lanes 0..63) are not read.
-      auto scores = [&](int c) {
-        if (!lane_wait(a, full0 + 8 * (c % kStg), (c / kStg) & 1, abort_flag, SITE_MMA_FULL)) return false;
-        tc_fence_after();
-        const uint32_t q = stages + (c % kStg) * L::kStage, k = q + L::kQ;
+    // The whole warp runs the loop, so that descriptors stay in uniform
+    // registers; one lane issues.  All 512 TMEM columns are this CTA's, so
+    // their addresses start at 0.
+    constexpr uint32_t id_sc = idesc_make(128, kC, 1);
+    constexpr uint32_t id_o1 = idesc_make(128, kC, 2);
+    constexpr uint32_t id_o2 = idesc_make(128, kC, 1) | kTransA;
+    const bool one = elect_one();
+    const uint64_t dqf = sdesc_sw128(smem_u32(smem) + L::kQf), dp = sdesc_sw128(smem_u32(smem) + L::kP);
+    const uint64_t dkm0 = sdesc_mn(stages + L::kQ, kBlk), dvm0 = sdesc_mn(stages + L::kQ + L::kK, kBlk);
+    const uint64_t dk0 = sdesc_sw128(stages + L::kQ), dq0 = sdesc_sw128(stages - (kOut ? kBlk : 0));
+    // Scores of a staged chunk, queries in rows 64..127 of the A operand:
+    // rows 0..63 are the 8 KB before each block of Q, and their results
+    // (lanes 0..63) are not read.
+    auto scores = [&](int c, uint32_t s) {
+      if (!warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL)) return false;
+      tc_fence_after();
+      const uint32_t at = s * (L::kStage >> 4);
+      if (one) {
 #pragma unroll
         for (int kk = 0; kk < kDk / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kBlk + 32 * (kk & 3);
-          MmaKind<__nv_bfloat16>::mma(tmem + M::P, sdesc_sw128(q + off - kBlk), sdesc_sw128(k + off),
-                                      id_sc, kk > 0 ? 1u : 0u);
+          const uint32_t off = at + (((kk >> 2) * kBlk + 32 * (kk & 3)) >> 4);
+          MmaKind<__nv_bfloat16>::mma(M::P, dq0 + off, dk0 + off, id_sc, kk > 0 ? 1u : 0u);
         }
         tc_commit(sc_full);
-        return true;
-      };
-      auto update = [&](int c) {
-        const int ub = c % M::kUBufs, use = c / M::kUBufs;
-        const uint32_t k = stages + (c % kStg) * L::kStage + L::kQ, u = tmem + M::U + ub * kDk;
-        if (!kOut && !lane_wait(a, full0 + 8 * (c % kStg), (c / kStg) & 1, abort_flag, SITE_MMA_FULL)) return false;
-        if (!lane_wait(a, u_empty0 + 8 * ub, (use & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY)) return false;
-        for (int b = 0; b < 2; ++b) {
-          if (!lane_wait(a, vt_full0 + 8 * b, c & 1, abort_flag, SITE_STAGE)) return false;
-          tc_fence_after();
-          mma_update<kDk>(u, tmem + M::V + b * kTerms * 16, k + b * 4096, b > 0);
+      }
+      return true;
+    };
+    auto update = [&](int c, uint32_t s) {
+      const int ub = c % M::kUBufs, use = c / M::kUBufs;
+      const uint32_t u = M::U + ub * kDk;
+      if (!kOut && !warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL)) return false;
+      if (!warp_wait(a, u_empty0 + 8 * ub, (use & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY)) return false;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if (!warp_wait(a, vt_full0 + 8 * b, c & 1, abort_flag, SITE_STAGE)) return false;
+        tc_fence_after();
+        if (one) {
+          mma_update<kDk>(u, M::V + b * kTerms * 16, dkm0 + s * (L::kStage >> 4) + b * (4096 >> 4), b > 0);
           tc_commit(vt_empty0 + 8 * b);
-        }
-        tc_commit(u_full0 + 8 * ub);
-        return true;
-      };
-      if (kOut) {
-        bool ok = nc == 0 || (scores(0) && update(0));
-        for (int c = 0; ok && c < nc; ++c) {
-          const uint32_t ph = c & 1;
-          const uint32_t st = stages + (c % kStg) * L::kStage;
-          if (!lane_wait(a, s_ready, ph, abort_flag, SITE_STAGE) ||
-              !lane_wait(a, qf_full, ph, abort_flag, SITE_STAGE) ||
-              (c > 0 && !lane_wait(a, o_empty, ph ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY)))
-            break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < kDk / 8; ++kk)
-            mma_ts_tf32(tmem + M::O, tmem + M::S + 8 * kk,
-                        sdesc_sw128(qf + (kk >> 2) * kBlk + 32 * (kk & 3)), id_o1, kk > 0 ? 1u : 0u);
-          tc_commit(i_done);
-          if (!lane_wait(a, p_full, ph, abort_flag, SITE_STAGE)) break;
-          tc_fence_after();
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int kk = 0; kk < kC / 16; ++kk)
-              MmaKind<__nv_bfloat16>::mma(tmem + M::O, sdesc_mn(st + L::kQ + L::kK + kk * 2048, kBlk),
-                                          sdesc_sw128(pb + t * kBlk + 32 * kk), id_o2, 1u);
-          tc_commit(o_full);
-          tc_commit(empty0 + 8 * (c % kStg));
-          ok = c + 1 == nc || (scores(c + 1) && update(c + 1));
-        }
-      } else {
-        for (int c = 0; c < nc; ++c) {
-          if (!update(c)) break;
-          tc_commit(empty0 + 8 * (c % kStg));
+          if (b == 1) tc_commit(u_full0 + 8 * ub);
         }
       }
-      tc_commit(drain);
+      return true;
+    };
+    if (kOut) {
+      uint32_t s = 0;  // stage of chunk c
+      bool ok = true;
+      for (int c = -1; ok && c < nc; ++c) {
+        const uint32_t ph = c & 1, next = (c < 0 || s + 1 == kStg) ? 0 : s + 1;
+        if (c >= 0) {
+          if (!warp_wait(a, s_ready, ph, abort_flag, SITE_STAGE) ||
+              !warp_wait(a, qf_full, ph, abort_flag, SITE_STAGE) ||
+              !warp_wait(a, o_empty, ph ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY))
+            break;
+          tc_fence_after();
+          if (one) {
+#pragma unroll
+            for (int kk = 0; kk < kDk / 8; ++kk)
+              mma_ts_tf32(M::O, M::S + 8 * kk, dqf + (((kk >> 2) * kBlk + 32 * (kk & 3)) >> 4), id_o1,
+                          kk > 0 ? 1u : 0u);
+            tc_commit(i_done);
+          }
+          if (!warp_wait(a, p_full, ph, abort_flag, SITE_STAGE)) break;
+          tc_fence_after();
+          if (one) {
+            const uint64_t dv = dvm0 + s * (L::kStage >> 4);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int kk = 0; kk < kC / 16; ++kk)
+                MmaKind<__nv_bfloat16>::mma(M::O, dv + kk * (2048 >> 4), dp + ((t * kBlk + 32 * kk) >> 4),
+                                            id_o2, 1u);
+            tc_commit(o_full);
+            tc_commit(empty0 + 8 * s);
+          }
+        }
+        if (c + 1 < nc) ok = scores(c + 1, next) && update(c + 1, next);
+        s = next;
+      }
+    } else {
+      uint32_t s = 0;
+      for (int c = 0; c < nc; ++c) {
+        if (!update(c, s)) break;
+        if (one) tc_commit(empty0 + 8 * s);
+        s = s + 1 == kStg ? 0 : s + 1;
+      }
     }
+    if (one) tc_commit(drain);
   } else if (kOut && warp < 4) {
     // ------------------------------------------------------------ P
     const int i = (wq - 2) * 32 + lane;
-    float w[kC];  // lambda^(i - j)
-#pragma unroll
-    for (int j = 0; j < kC; ++j) w[j] = j <= i ? ctl.tab[i - j] : 0.0f;
-    uint8_t *row = smem + L::kP + i * 128;
+    const uint32_t row = smem_u32(smem) + L::kP + i * 128;
     for (int c = 0; c < nc; ++c) {
       if (!warp_wait(a, sc_full, c & 1, abort_flag, SITE_EPI_TMEM_FULL)) break;
       tc_fence_after();
-#pragma unroll
+      const float *w = ctl.rtab + kC - 1 - i;  // w[j] = lambda^(i - j), 0 for j > i
+#pragma unroll 1
       for (int j0 = 0; j0 < kC; j0 += 16) {
         float v[16];
-        tmem_ld16_sync(tmem + M::P + lanes + j0, v);
+        tmem_ld16_sync(M::P + lanes + j0, v);
 #pragma unroll
         for (int x = 0; x < 16; x += 8) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
-            const int j = j0 + x + e;  // (a score past the diagonal may be anything)
-            float p = j <= i ? v[x + e] * w[j] : 0.0f;
-            float q = j + 1 <= i ? v[x + e + 1] * w[j + 1] : 0.0f;
-            hi[e / 2] = take_bf16(p, q);
-            lo[e / 2] = take_bf16(p, q);
+            const int j = x + e;  // (a score past the diagonal may be anything)
+            f32x2 p = mul2(pack2(j0 + j <= i ? v[j] : 0.0f, j0 + j < i ? v[j + 1] : 0.0f),
+                           pack2(w[j0 + j], w[j0 + j + 1]));
+            hi[e / 2] = take_bf16(p);
+            lo[e / 2] = high_parts(p);
           }
-          const int at = (((j0 + x) >> 3) ^ (i & 7)) << 4;
-          *reinterpret_cast<uint4 *>(row + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4 *>(row + kBlk + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          const uint32_t at = row + ((((j0 + x) >> 3) ^ (i & 7)) << 4);
+          sts128(at, hi[0], hi[1], hi[2], hi[3]);
+          sts128(at + kBlk, lo[0], lo[1], lo[2], lo[3]);
         }
       }
       fence_proxy_async_smem();
@@ -579,46 +673,52 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     }
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------ V~, Q~
-    const int r = (threadIdx.x - 128) >> 1, hf = threadIdx.x & 1;  // Q~: half of a row
-    const float f = ctl.tab[r + 1];
+    const int r = threadIdx.x & 63, hf = (threadIdx.x >> 6) & 1;  // Q~: half of a row
+    const f32x2 f = pack2(ctl.tab[r + 1], ctl.tab[r + 1]);
+    f32x2 w[8];
+    vt_weights(ctl.tab, kC, w);
     for (int c = 0; c < nc; ++c) {
       const int s = c % kStg, n = c == nc - 1 ? tail : kC;
       if (!warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL)) break;
-      uint8_t *st = smem + L::kStages + s * L::kStage;
+      const uint32_t st = stages + s * L::kStage;
       if (n < kC) {
-        zero_rows(st + L::kQ, kDk / 64 + 2, n, threadIdx.x - 128, 128);
-        fence_proxy_async_smem();
+        zero_rows<kDk>(st + L::kQ, st + L::kQ + L::kK, wq, n);
+        vt_weights(ctl.tab, n, w);
       }
       bool ok = true;
-      for (int b = 0; ok && b < 2; ++b) {
-        ok = warp_wait(a, vt_empty0 + 8 * b, (c & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        ok = ok && warp_wait(a, vt_empty0 + 8 * b, (c & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY);
         if (!ok) break;
         tc_fence_after();
-        make_vt(st + L::kQ + L::kK, wq * 32 + lane, ctl.w, ctl.tab, n, 32 * b,
-                tmem + M::V + b * kTerms * 16 + lanes);
+        make_vt(st + L::kQ + L::kK, wq, w, 32 * b, M::V + b * kTerms * 16 + lanes);
         tmem_wait_st();
         warp_arrive(vt_full0 + 8 * b);
       }
       if (!ok) break;
       if (kOut) {
         if (c > 0 && !warp_wait(a, i_done, (c & 1) ^ 1, abort_flag, SITE_DRAIN)) break;
-        const uint8_t *src = st + r * 128;
-        uint8_t *dst = smem + L::kQf + r * 128;
-#pragma unroll 4
-        for (int y = 0; y < kDk / 16; ++y) {  // 8 elements: 16 bytes of bf16, 32 of fp32
-          const int x = 2 * y + hf;
-          const uint4 u = *reinterpret_cast<const uint4 *>(src + (x >> 3) * kBlk + (((x & 7) ^ (r & 7)) << 4));
+        // 8 elements at a time: 16 bytes of bf16 become 32 of fp32, rounded to
+        // tf32 (half up in magnitude) by adding half of its last bit
+        const uint32_t src = st + hf * (kDk == 128 ? kBlk : 0) + r * 128;
+        const uint32_t dst = smem_u32(smem) + L::kQf + hf * (kDk / 64) * kBlk + r * 128;
+#pragma unroll 2
+        for (int y = 0; y < kDk / 16; ++y) {
+          const int x = kDk == 128 ? y : 4 * hf + y;  // 16-byte piece of the staged row
+          const uint4 u = lds128(src + ((x ^ (r & 7)) << 4));
           const uint32_t q[4] = {u.x, u.y, u.z, u.w};
-          float t[8];
+          uint32_t t[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            t[2 * e] = to_tf32(__uint_as_float(q[e] << 16) * f);
-            t[2 * e + 1] = to_tf32(__uint_as_float(q[e] & 0xffff0000u) * f);
+            float lo, hi;
+            unpack2(mul2(pack2(__uint_as_float(q[e] << 16), __uint_as_float(q[e] & 0xffff0000u)), f), lo, hi);
+            t[2 * e] = __float_as_uint(lo) + 0x1000u;
+            t[2 * e + 1] = __float_as_uint(hi) + 0x1000u;
           }
-          uint8_t *blk = dst + (x >> 2) * kBlk;
-          const int p0 = (2 * (x & 3)) ^ (r & 7);
-          *reinterpret_cast<float4 *>(blk + (p0 << 4)) = make_float4(t[0], t[1], t[2], t[3]);
-          *reinterpret_cast<float4 *>(blk + ((p0 ^ 1) << 4)) = make_float4(t[4], t[5], t[6], t[7]);
+          const uint32_t blk = dst + (y >> 2) * kBlk;
+          const int p0 = (2 * (y & 3)) ^ (r & 7);
+          sts128(blk + (p0 << 4), t[0], t[1], t[2], t[3]);
+          sts128(blk + ((p0 ^ 1) << 4), t[4], t[5], t[6], t[7]);
         }
         fence_proxy_async_smem();
         warp_arrive(qf_full);
@@ -630,7 +730,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     const int d = d0 + wq * 32 + lane;
     const bool valid = d < a.dv;
     const long long srow = ((static_cast<long long>(g.seq) * a.Hv + h) * a.dv + d) * kDk + half * kHalfDk;
-    float S[kHalfDk];
+    f32x2 S[kHalfDk / 2];
     const float *src = nullptr;
     if (kOut && valid) {
       if (g.index == 0)
@@ -641,18 +741,21 @@ __global__ void __launch_bounds__(kThreadsC, 1)
 #pragma unroll
     for (int i = 0; i < kHalfDk; i += 4) {
       const float4 u = src ? *reinterpret_cast<const float4 *>(src + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-      S[i] = u.x;
-      S[i + 1] = u.y;
-      S[i + 2] = u.z;
-      S[i + 3] = u.w;
+      S[i / 2] = pack2(u.x, u.y);
+      S[i / 2 + 1] = pack2(u.z, u.w);
     }
-    const uint32_t ts = tmem + M::S + half * kHalfDk + lanes;
+    const uint32_t ts = M::S + half * kHalfDk + lanes;
     auto put_state = [&] {
 #pragma unroll
       for (int x = 0; x < kHalfDk; x += 16) {
         uint32_t r[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(S[x + i]);
+        for (int i = 0; i < 16; i += 2) {
+          float lo, hi;
+          unpack2(S[(x + i) / 2], lo, hi);
+          r[i] = __float_as_uint(lo);
+          r[i + 1] = __float_as_uint(hi);
+        }
         tmem_st16(ts + x, r);
       }
       tmem_wait_st();
@@ -663,16 +766,17 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     for (int c = 0; c < nc; ++c) {
       const int n = c == nc - 1 ? tail : kC;
       const int ub = c % M::kUBufs, use = c / M::kUBufs;
-      const float f = ctl.tab[n];
+      const f32x2 f = pack2(ctl.tab[n], ctl.tab[n]);
       ok = warp_wait(a, u_full0 + 8 * ub, use & 1, abort_flag, SITE_EPI_TMEM_FULL);
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
       for (int x = 0; x < kHalfDk; x += 16) {
         float u[16];
-        tmem_ld16_sync(tmem + M::U + ub * kDk + half * kHalfDk + x + lanes, u);
+        tmem_ld16_sync(M::U + ub * kDk + half * kHalfDk + x + lanes, u);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) S[x + i] = fmaf(f, S[x + i], u[i]);
+        for (int i = 0; i < 16; i += 2)
+          S[(x + i) / 2] = fma2(f, S[(x + i) / 2], pack2(u[i], u[i + 1]));
       }
       warp_arrive(u_empty0 + 8 * ub);
       if (kOut) {
@@ -686,15 +790,22 @@ __global__ void __launch_bounds__(kThreadsC, 1)
         if (!ok) break;
         tc_fence_after();
         float v[32];  // tokens 32 half .. of this d_v row
-        tmem_ld32_sync(tmem + M::O + 32 * half + lanes, v);
+        tmem_ld32_sync(M::O + 32 * half + lanes, v);
         warp_arrive(o_empty);
-        if (valid) {
-          const long long ostride = static_cast<long long>(a.Hv) * a.dv;
-          __nv_bfloat16 *o = a.o + (g.first + static_cast<long long>(c) * kC + 32 * half) * ostride +
-                             static_cast<long long>(h) * a.dv + d;
+        // Lanes 2 x and 2 x + 1 hold neighbouring columns: they trade values,
+        // so that each stores both columns of every other token (4 bytes).
+        const long long ostride = static_cast<long long>(a.Hv) * a.dv;
+        const int t0 = 32 * half + (lane & 1);
+        __nv_bfloat16 *o = a.o + (g.first + static_cast<long long>(c) * kC + t0) * ostride +
+                           static_cast<long long>(h) * a.dv + (d & ~1);
+        const uint32_t sel = (lane & 1) ? 0x3276u : 0x5410u;
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (32 * half + i < n) o[i * ostride] = __float2bfloat16_rn(v[i]);
+        for (int i = 0; i < 32; i += 2) {
+          const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[i], v[i + 1]);
+          const uint32_t mine = *reinterpret_cast<const uint32_t *>(&b2);
+          const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+          if (valid && t0 + i < n) *reinterpret_cast<uint32_t *>(o) = __byte_perm(mine, other, sel);
+          o += 2 * ostride;
         }
       }
     }
@@ -707,17 +818,21 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     }
     if (dst) {
 #pragma unroll
-      for (int i = 0; i < kHalfDk; i += 4)
-        *reinterpret_cast<float4 *>(dst + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+      for (int i = 0; i < kHalfDk; i += 4) {
+        float4 u;
+        unpack2(S[i / 2], u.x, u.y);
+        unpack2(S[i / 2 + 1], u.z, u.w);
+        *reinterpret_cast<float4 *>(dst + i) = u;
+      }
     }
   }
   __syncwarp();
-  const bool fin = mbar_wait(drain, 0, MOE_WAIT_LIMIT_CYCLES, nullptr);
+  const bool fin = poll(drain, 0, nullptr);
   if (!__all_sync(0xffffffffu, fin) && lane == 0) fail(a, abort_flag, SITE_DRAIN);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, kTmemAll);
+  if (warp == 1) tmem_dealloc(ctl.tmem, kTmemAll);
 }
 
 namespace {
