@@ -280,33 +280,29 @@ __device__ __forceinline__ Segment find_segment(const DecayArgs &a, long long it
   return g;
 }
 
-// V~ of tokens j0 .. j0 + 31 of a chunk for a warp's 32 columns of V: the
-// staged V (address `v`, 128-byte swizzle) times a weight per token, as kTerms
-// bf16 parts of two tokens per TMEM column, [d_v lane][token pair].  Transposed
-// matrix loads give lane l tokens 8 i + 2 (l % 4), + 1 of columns l / 4, + 8 of
-// each 16, the layout of a 16-lane TMEM store; w[j0 / 8 + i] are those tokens'
-// weights.
-__device__ __forceinline__ void make_vt(uint32_t v, int wq, const f32x2 (&w)[8], int j0,
-                                        uint32_t ta) {
+// V~ of 32 tokens of a chunk for a warp's 32 columns of V: the staged V
+// (address `v` of the first token's row, 128-byte swizzle) times a weight per
+// token, as kTerms bf16 parts of two tokens per TMEM column, [d_v lane][token
+// pair].  Transposed matrix loads give lane l tokens 8 i + 2 (l % 4), + 1 of
+// columns l / 4, + 8 of each 16, the layout of a 16-lane TMEM store; w[i] are
+// those tokens' weights.
+__device__ __forceinline__ void make_vt(uint32_t v, int wq, const f32x2 (&w)[8], uint32_t ta) {
   const int lane = threadIdx.x & 31, m = lane >> 3;
-  const uint32_t row = v + (wq >> 1) * kBlk + (j0 + 8 * (m >> 1) + (lane & 7)) * 128;
-#pragma unroll 1
+  const uint32_t row = v + (wq >> 1) * kBlk + (8 * (m >> 1) + (lane & 7)) * 128;
+  uint32_t r[4][4];  // [16 columns, 16 tokens]
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    ldsm4_trans(row + ((((wq & 1) * 4 + 2 * (x >> 1) + (m & 1)) ^ (lane & 7)) << 4) + (x & 1) * 2048, r[x]);
+#pragma unroll
   for (int hl = 0; hl < 2; ++hl) {
-    const uint32_t at = row + ((((wq & 1) * 4 + 2 * hl + (m & 1)) ^ (lane & 7)) << 4);
     uint32_t p[kTerms][8];
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {  // 16 tokens
-      uint32_t r[4];
-      ldsm4_trans(at + g * 2048, r);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 2 * g + (e >> 1);
-        f32x2 x = pack2(__uint_as_float(r[e] << 16), __uint_as_float(r[e] & 0xffff0000u));
-        x = mul2(x, w[j0 / 8 + i]);
-        p[0][4 * g + e] = take_bf16(x);
-        p[1][4 * g + e] = take_bf16(x);
-        p[2][4 * g + e] = high_parts(x);
-      }
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t u = r[2 * hl + (e >> 2)][e & 3];
+      f32x2 x = mul2(pack2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)), w[e >> 1]);
+      p[0][e] = take_bf16(x);
+      p[1][e] = take_bf16(x);
+      p[2][e] = high_parts(x);
     }
 #pragma unroll
     for (int t = 0; t < kTerms; ++t)
@@ -359,13 +355,14 @@ __device__ __forceinline__ void fail(const DecayArgs &a, volatile int *abort_fla
 }
 
 // A warp's wait for phase `parity`: false in every lane when the CTA aborted
-// or the polls (a few us each at most) ran out.  Short on purpose: it is
-// inlined at each wait, and the roles share one instruction cache.
-constexpr int kPolls = 1 << 22;
+// or the polls (each sleeps in the barrier for a while) ran out.  Short on
+// purpose: it is inlined at each wait, and the roles share one instruction
+// cache.
+constexpr int kPolls = 1 << 24;
 __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, const volatile int *abort_flag) {
 #pragma unroll 1
   for (int i = 0; i < kPolls; ++i) {
-    if (mbar_try_wait_sleep(bar, parity, 4000u)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if (abort_flag && *abort_flag) return false;
   }
   return false;
@@ -398,7 +395,7 @@ struct Smem {
   static constexpr int kStage = kQ + kK + kV;
   static constexpr int kQf = kStages + kStg * kStage;  // kDk / 32 blocks of 64 x 128 bytes
   static constexpr int kCtl = kQf + (kOut ? kDk / 32 * kBlk : 0);
-  static constexpr int kTotal = kCtl + 1536 + 1024;
+  static constexpr int kTotal = kCtl + 3072 + 1024;
 };
 
 struct Ctl {
@@ -406,10 +403,11 @@ struct Ctl {
   uint32_t tmem;
   int abort_flag;
   int scratch[36];
-  float tab[kC + 1];   // lambda^0 .. lambda^64
-  float rtab[2 * kC];  // lambda^63 .. lambda^0, then zeros
+  // lambda^63 .. lambda^0 and zeros in copies that start 0..3 words late
+  alignas(16) float rtab[4][2 * kC + 8];
+  float tab[kC + 1];  // lambda^0 .. lambda^64
 };
-static_assert(sizeof(Ctl) <= 1536, "control block");
+static_assert(sizeof(Ctl) <= 3072, "control block");
 
 }  // namespace
 
@@ -472,8 +470,8 @@ __global__ void __launch_bounds__(kThreadsC, 1)
   volatile int *abort_flag = &ctl.abort_flag;
   const uint32_t full0 = smem_u32(ctl.bars), empty0 = full0 + 8 * kStg;
   const uint32_t bar = empty0 + 8 * kStg;
-  const uint32_t sc_full = bar, p_full = bar + 8, qf_full = bar + 16, s_ready = bar + 24;
-  const uint32_t i_done = bar + 32, o_full = bar + 40, o_empty = bar + 48, drain = bar + 56;
+  const uint32_t sc_full = bar, p_full = bar + 8, in_ready = bar + 16;
+  const uint32_t i_done = bar + 32, o_full = bar + 40, drain = bar + 56;
   const uint32_t vt_full0 = bar + 64, vt_empty0 = bar + 80, u_full0 = bar + 96, u_empty0 = bar + 112;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3;
   const int ht = static_cast<int>(blockIdx.x % (a.Hv * a.tiles));
@@ -486,10 +484,11 @@ __global__ void __launch_bounds__(kThreadsC, 1)
   if (threadIdx.x <= kC) {
     const float p = decay_pow(lam, static_cast<float>(threadIdx.x));
     ctl.tab[threadIdx.x] = p;
-    if (threadIdx.x < kC) {
-      ctl.rtab[kC - 1 - threadIdx.x] = p;
-      ctl.rtab[kC + threadIdx.x] = 0.0f;
-    }
+    if (kOut && threadIdx.x < kC)
+      for (int m = 0; m < 4; ++m) {
+        ctl.rtab[m][m + kC - 1 - threadIdx.x] = p;
+        ctl.rtab[m][m + kC + threadIdx.x] = 0.0f;
+      }
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStg; ++s) {
@@ -498,14 +497,13 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     }
     mbar_init(sc_full, 1);
     mbar_init(p_full, 2);
-    mbar_init(qf_full, 4);
-    mbar_init(s_ready, 8);
+    mbar_init(in_ready, 4 + 8);  // Q~; the state in TMEM and the last O^T read
     mbar_init(i_done, 1);
     mbar_init(o_full, 1);
-    mbar_init(o_empty, 8);
     mbar_init(drain, 1);
     for (int b = 0; b < 2; ++b) {
-      mbar_init(vt_full0 + 8 * b, 4);
+      // (with outputs, also the last U read: U has one buffer then)
+      mbar_init(vt_full0 + 8 * b, kOut && b == 0 ? 4 + 8 : 4);
       mbar_init(vt_empty0 + 8 * b, 1);
       mbar_init(u_full0 + 8 * b, 1);
       mbar_init(u_empty0 + 8 * b, 8);
@@ -583,7 +581,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
       const int ub = c % M::kUBufs, use = c / M::kUBufs;
       const uint32_t u = M::U + ub * kDk;
       if (!kOut && !warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL)) return false;
-      if (!warp_wait(a, u_empty0 + 8 * ub, (use & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY)) return false;
+      if (!kOut && !warp_wait(a, u_empty0 + 8 * ub, (use & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY)) return false;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         if (!warp_wait(a, vt_full0 + 8 * b, c & 1, abort_flag, SITE_STAGE)) return false;
@@ -602,10 +600,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
       for (int c = -1; ok && c < nc; ++c) {
         const uint32_t ph = c & 1, next = (c < 0 || s + 1 == kStg) ? 0 : s + 1;
         if (c >= 0) {
-          if (!warp_wait(a, s_ready, ph, abort_flag, SITE_STAGE) ||
-              !warp_wait(a, qf_full, ph, abort_flag, SITE_STAGE) ||
-              !warp_wait(a, o_empty, ph ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY))
-            break;
+          if (!warp_wait(a, in_ready, ph, abort_flag, SITE_STAGE)) break;
           tc_fence_after();
           if (one) {
 #pragma unroll
@@ -644,22 +639,27 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     // ------------------------------------------------------------ P
     const int i = (wq - 2) * 32 + lane;
     const uint32_t row = smem_u32(smem) + L::kP + i * 128;
+    // the copy of the weights in which this row's start on a 16-byte boundary
+    const float *wrow = ctl.rtab[(i + 1) & 3] + (kC - 1 - i + ((i + 1) & 3));
     for (int c = 0; c < nc; ++c) {
       if (!warp_wait(a, sc_full, c & 1, abort_flag, SITE_EPI_TMEM_FULL)) break;
       tc_fence_after();
-      const float *w = ctl.rtab + kC - 1 - i;  // w[j] = lambda^(i - j), 0 for j > i
 #pragma unroll 1
-      for (int j0 = 0; j0 < kC; j0 += 16) {
-        float v[16];
-        tmem_ld16_sync(M::P + lanes + j0, v);
+      for (int j0 = 0; j0 < kC; j0 += 32) {
+        float4 w[8];  // lambda^(i - j), 0 for j > i
 #pragma unroll
-        for (int x = 0; x < 16; x += 8) {
+        for (int x = 0; x < 8; ++x) w[x] = *reinterpret_cast<const float4 *>(wrow + j0 + 4 * x);
+        float v[32];
+        tmem_ld32_sync(M::P + lanes + j0, v);
+#pragma unroll
+        for (int x = 0; x < 32; x += 8) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
             const int j = x + e;  // (a score past the diagonal may be anything)
+            const float4 w4 = w[j >> 2];
             f32x2 p = mul2(pack2(j0 + j <= i ? v[j] : 0.0f, j0 + j < i ? v[j + 1] : 0.0f),
-                           pack2(w[j0 + j], w[j0 + j + 1]));
+                           (e & 2) ? pack2(w4.z, w4.w) : pack2(w4.x, w4.y));
             hi[e / 2] = take_bf16(p);
             lo[e / 2] = high_parts(p);
           }
@@ -686,14 +686,20 @@ __global__ void __launch_bounds__(kThreadsC, 1)
         vt_weights(ctl.tab, n, w);
       }
       bool ok = true;
-#pragma unroll
+#pragma unroll 1
       for (int b = 0; b < 2; ++b) {
-        ok = ok && warp_wait(a, vt_empty0 + 8 * b, (c & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY);
+        ok = warp_wait(a, vt_empty0 + 8 * b, (c & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY);
         if (!ok) break;
         tc_fence_after();
-        make_vt(st + L::kQ + L::kK, wq, w, 32 * b, M::V + b * kTerms * 16 + lanes);
+        make_vt(st + L::kQ + L::kK + b * 4096, wq, w, M::V + b * kTerms * 16 + lanes);
         tmem_wait_st();
         warp_arrive(vt_full0 + 8 * b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // the other half's weights come first
+          const f32x2 u = w[i];
+          w[i] = w[i + 4];
+          w[i + 4] = u;
+        }
       }
       if (!ok) break;
       if (kOut) {
@@ -702,26 +708,30 @@ __global__ void __launch_bounds__(kThreadsC, 1)
         // tf32 (half up in magnitude) by adding half of its last bit
         const uint32_t src = st + hf * (kDk == 128 ? kBlk : 0) + r * 128;
         const uint32_t dst = smem_u32(smem) + L::kQf + hf * (kDk / 64) * kBlk + r * 128;
-#pragma unroll 2
-        for (int y = 0; y < kDk / 16; ++y) {
-          const int x = kDk == 128 ? y : 4 * hf + y;  // 16-byte piece of the staged row
-          const uint4 u = lds128(src + ((x ^ (r & 7)) << 4));
-          const uint32_t q[4] = {u.x, u.y, u.z, u.w};
-          uint32_t t[8];
+#pragma unroll 1
+        for (int y0 = 0; y0 < kDk / 16; y0 += 4) {
+          uint4 u[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float lo, hi;
-            unpack2(mul2(pack2(__uint_as_float(q[e] << 16), __uint_as_float(q[e] & 0xffff0000u)), f), lo, hi);
-            t[2 * e] = __float_as_uint(lo) + 0x1000u;
-            t[2 * e + 1] = __float_as_uint(hi) + 0x1000u;
+          for (int y = 0; y < 4; ++y)  // 16-byte pieces of the staged row
+            u[y] = lds128(src + (((kDk == 128 ? y0 + y : 4 * hf + y) ^ (r & 7)) << 4));
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t q[4] = {u[y].x, u[y].y, u[y].z, u[y].w};
+            uint32_t t[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float lo, hi;
+              unpack2(mul2(pack2(__uint_as_float(q[e] << 16), __uint_as_float(q[e] & 0xffff0000u)), f), lo, hi);
+              t[2 * e] = __float_as_uint(lo) + 0x1000u;
+              t[2 * e + 1] = __float_as_uint(hi) + 0x1000u;
+            }
+            const uint32_t at = dst + (y0 >> 2) * kBlk + (((2 * y) ^ (r & 7)) << 4);
+            sts128(at, t[0], t[1], t[2], t[3]);
+            sts128(at ^ 16u, t[4], t[5], t[6], t[7]);
           }
-          const uint32_t blk = dst + (y >> 2) * kBlk;
-          const int p0 = (2 * (y & 3)) ^ (r & 7);
-          sts128(blk + (p0 << 4), t[0], t[1], t[2], t[3]);
-          sts128(blk + ((p0 ^ 1) << 4), t[4], t[5], t[6], t[7]);
         }
         fence_proxy_async_smem();
-        warp_arrive(qf_full);
+        warp_arrive(in_ready);
       }
     }
   } else if (warp >= 8) {
@@ -759,9 +769,12 @@ __global__ void __launch_bounds__(kThreadsC, 1)
         tmem_st16(ts + x, r);
       }
       tmem_wait_st();
-      warp_arrive(s_ready);
     };
-    if (kOut) put_state();
+    if (kOut) {
+      put_state();
+      warp_arrive(in_ready);
+      warp_arrive(vt_full0);
+    }
     bool ok = true;
     for (int c = 0; c < nc; ++c) {
       const int n = c == nc - 1 ? tail : kC;
@@ -771,15 +784,16 @@ __global__ void __launch_bounds__(kThreadsC, 1)
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
-      for (int x = 0; x < kHalfDk; x += 16) {
-        float u[16];
-        tmem_ld16_sync(M::U + ub * kDk + half * kHalfDk + x + lanes, u);
+      for (int x = 0; x < kHalfDk; x += 32) {
+        float u[32];
+        tmem_ld32_sync(M::U + ub * kDk + half * kHalfDk + x + lanes, u);
 #pragma unroll
-        for (int i = 0; i < 16; i += 2)
+        for (int i = 0; i < 32; i += 2)
           S[(x + i) / 2] = fma2(f, S[(x + i) / 2], pack2(u[i], u[i + 1]));
       }
-      warp_arrive(u_empty0 + 8 * ub);
+      if (!kOut) warp_arrive(u_empty0 + 8 * ub);
       if (kOut) {
+        if (c + 1 < nc) warp_arrive(vt_full0);
         if (c + 1 < nc) {
           ok = warp_wait(a, i_done, c & 1, abort_flag, SITE_DRAIN);
           if (!ok) break;
@@ -791,7 +805,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
         tc_fence_after();
         float v[32];  // tokens 32 half .. of this d_v row
         tmem_ld32_sync(M::O + 32 * half + lanes, v);
-        warp_arrive(o_empty);
+        if (c + 1 < nc) warp_arrive(in_ready);
         // Lanes 2 x and 2 x + 1 hold neighbouring columns: they trade values,
         // so that each stores both columns of every other token (4 bytes).
         const long long ostride = static_cast<long long>(a.Hv) * a.dv;
