@@ -7,9 +7,10 @@
 //     S  <- lambda^C S + U,   U = sum_j lambda^(C-1-j) v_j k_j^T
 // as matrix products, d_v along the MMA's 128 rows (TMEM lanes):
 //     scores  [i][j]     = Q K^T                          (bf16, exact operands)
-//     O^T     [d_v][i]   = S Q~^T,  Q~_i = lambda^(i+1) q_i   (tf32)
-//                        + V^T P^T,  P_ij = lambda^(i-j) scores (bf16 hi + lo)
-//     U       [d_v][d_k] = V~^T K,  V~_j = lambda^(C-1-j) v_j   (bf16, three parts)
+//     O1^T    [d_v][i]   = S Q^T                          (S rounded to bf16)
+//     O2^T    [d_v][i]   = V^T P^T,  P_ij = lambda^(i-j) scores   (P in bf16)
+//     o_i                = lambda^(i+1) O1_i + O2_i
+//     U       [d_v][d_k] = V~^T K,  V~_j = lambda^(C-1-j) v_j  (bf16, three parts)
 // Every decay is a power <= 1 of lambda: nothing is divided by a decay.
 //
 // Precision.  V~ is written as three bf16 parts (24 bits; the products with
@@ -17,8 +18,11 @@
 // lives in registers, where lambda^C S + U is one fp32 fused multiply-add per
 // element: tensor-core accumulation truncates, and adding chunk after chunk
 // into one accumulator drifted to several 1e-6 of the state.  The outputs are
-// rounded to bf16 (rms 1.7e-3) in the end; S and Q~ enter them as tf32 (2^-11)
-// and P as two bf16 parts (2^-17), so nothing before the last rounding shows.
+// rounded to bf16 (rms 1.7e-3) in the end; S (state's part of an output) and P
+// (the chunk's own part) enter their products as bf16, as large a rounding
+// each on its part, so that an output's rms error is sqrt(2) times that of the
+// last rounding alone.  A second bf16 part for S or P takes that away and was
+// measured at 15 % of the kernel's time each.
 //
 // Work split.  One CTA scans one segment of one (sequence, value head, 128
 // columns of d_v).  A sequence is one segment when the batch has enough heads
@@ -27,12 +31,13 @@
 // chains these into the state before each segment, and the main launch runs
 // all segments at once.
 //
-// Roles (512 threads): warp 0 TMA producer; warp 1 issues every MMA; warps 2-3
-// P (scores in TMEM lanes 64..127); warps 4-7 V~ (a thread per column of V)
-// and Q~; warps 8-15 the state (a thread per row and half of d_k) and O^T to
-// global memory.  The issuer's order per chunk is S Q~^T, V^T P^T, the next
-// chunk's scores, the next chunk's U, so that only the products wait for one
-// another and the other roles work under them.
+// Roles (512 threads): warp 0 TMA producer; warp 1 issues every MMA, per chunk
+// S Q^T, V^T P^T, the next chunk's scores and its U; warps 4-7 P and V~; warps
+// 8-15 the state (a thread per row and half of d_k) and the outputs.  What a
+// role makes is waited for under other products.  Shared memory is the scarce
+// resource (an M = 128, N = 64 product reads 6 KB in its 48 cycles, all of the
+// 128 bytes a cycle): operands that threads make go to TMEM where the MMA can
+// take them from there (V~, S), and the scores use 64 rows.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -48,7 +53,7 @@ namespace {
 constexpr int kC = kChunkTok;
 constexpr int kBlk = kC * 128;  // a 64-token tile of 128 bytes (64 bf16) per token: 8 KB
 constexpr int kThreadsC = 512;
-constexpr int kStg = 3;    // TMA stages
+constexpr int kStg = 4;    // TMA stages
 constexpr int kTerms = 3;  // bf16 parts of V~
 constexpr uint32_t kTmemAll = 512;
 
@@ -58,9 +63,10 @@ struct Cols {
   static constexpr int kUBufs = kOut ? 1 : 2;
   static constexpr uint32_t U = 0;                   // kUBufs x kDk
   static constexpr uint32_t V = kUBufs * kDk;        // V~: two halves of 32 tokens, kTerms x 16 each
-  static constexpr uint32_t S = V + 2 * kTerms * 16; // state of the chunk (outputs only)
-  static constexpr uint32_t O = S + kDk;             // O^T: 64
-  static constexpr uint32_t P = O + 64;              // scores: 64 (lanes 64..127)
+  static constexpr uint32_t S = V + 2 * kTerms * 16; // S, two columns of d_k per TMEM column
+  static constexpr uint32_t O1 = S + kDk / 2;        // 64
+  static constexpr uint32_t O2 = O1 + 64;            // 64
+  static constexpr uint32_t P = O2 + 64;             // scores: 64
   static_assert((kOut ? P + 64 : S) <= kTmemAll, "TMEM columns");
 };
 
@@ -87,22 +93,50 @@ __device__ __forceinline__ void mma_ts_bf16(uint32_t d, uint32_t a, uint64_t b, 
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts_tf32(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 
-__device__ __forceinline__ void tmem_st16(uint32_t ta, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st8(uint32_t ta, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(ta),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// 16 lanes x 64 fp32 columns: lane l of the warp gets, for each 8 columns n,
+// v[4 n], v[4 n + 1] = row l / 4, columns 8 n + 2 (l % 4), + 1, and v[4 n + 2],
+// v[4 n + 3] = row l / 4 + 8
+__device__ __forceinline__ void tmem_ld_16x64_sync(uint32_t ta, float (&v)[32]) {
+  uint32_t r[32];
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16};" ::"r"(ta),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(ta)
       : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// the same for 32 columns of two accumulators
+__device__ __forceinline__ void tmem_ld_16x32x2_sync(uint32_t ta, uint32_t tb, float (&a)[16],
+                                                     float (&b)[16]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(ta), "r"(tb)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    a[i] = __uint_as_float(r[i]);
+    b[i] = __uint_as_float(r[16 + i]);
+  }
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -159,14 +193,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 // shared-memory accesses by 32-bit address
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a)
-               : "memory");
-  return v;
-}
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
                : "memory");
@@ -179,6 +205,27 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t a, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(a)
                : "memory");
+}
+// four 8 x 8 matrices of 16-bit values: lane l gives row l / 4, columns
+// 2 (l % 4), + 1 of each; lanes 8 m .. 8 m + 7 the addresses of matrix m's rows
+__device__ __forceinline__ void stsm4(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(r0),
+               "r"(r1), "r"(r2), "r"(r3)
+               : "memory");
+}
+// the same, each matrix stored transposed
+__device__ __forceinline__ void stsm4_trans(uint32_t a, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(r0),
+               "r"(r1), "r"(r2), "r"(r3)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
 }
 // 16 lanes x 16 columns: lane l of the warp holds rows l / 4 (even registers)
 // and l / 4 + 8 (odd) of column l % 4 of each group of four
@@ -385,17 +432,16 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
                                      ~static_cast<uintptr_t>(1023));
 }
 
-// Shared memory: P hi and lo, then the stages of (Q, K, V), Q~ (fp32), control.
-// (The scores' A operand starts 64 rows before Q, so something lies there.)
+// Shared memory: the stages of (Q, K, V), P, a 32 x 32 output tile for each of
+// the state's warps, control
 template <int kDk, bool kOut>
 struct Smem {
-  static constexpr int kP = 0;
-  static constexpr int kStages = kOut ? 2 * kBlk : 0;
   static constexpr int kQ = kOut ? kDk / 64 * kBlk : 0, kK = kDk / 64 * kBlk, kV = 2 * kBlk;
   static constexpr int kStage = kQ + kK + kV;
-  static constexpr int kQf = kStages + kStg * kStage;  // kDk / 32 blocks of 64 x 128 bytes
-  static constexpr int kCtl = kQf + (kOut ? kDk / 32 * kBlk : 0);
-  static constexpr int kTotal = kCtl + 3072 + 1024;
+  static constexpr int kP = kStg * kStage;
+  static constexpr int kO = kP + (kOut ? kBlk : 0);
+  static constexpr int kCtl = kO + (kOut ? 8 * 2048 : 0);
+  static constexpr int kTotal = kCtl + 1024 + 1024;
 };
 
 struct Ctl {
@@ -403,11 +449,9 @@ struct Ctl {
   uint32_t tmem;
   int abort_flag;
   int scratch[36];
-  // lambda^63 .. lambda^0 and zeros in copies that start 0..3 words late
-  alignas(16) float rtab[4][2 * kC + 8];
   float tab[kC + 1];  // lambda^0 .. lambda^64
 };
-static_assert(sizeof(Ctl) <= 3072, "control block");
+static_assert(sizeof(Ctl) <= 1024, "control block");
 
 }  // namespace
 
@@ -470,8 +514,8 @@ __global__ void __launch_bounds__(kThreadsC, 1)
   volatile int *abort_flag = &ctl.abort_flag;
   const uint32_t full0 = smem_u32(ctl.bars), empty0 = full0 + 8 * kStg;
   const uint32_t bar = empty0 + 8 * kStg;
-  const uint32_t sc_full = bar, p_full = bar + 8, in_ready = bar + 16;
-  const uint32_t i_done = bar + 32, o_full = bar + 40, drain = bar + 56;
+  const uint32_t sc_full = bar, p_full = bar + 8, s_ready = bar + 24;
+  const uint32_t o_full = bar + 32, drain = bar + 40;
   const uint32_t vt_full0 = bar + 64, vt_empty0 = bar + 80, u_full0 = bar + 96, u_empty0 = bar + 112;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3;
   const int ht = static_cast<int>(blockIdx.x % (a.Hv * a.tiles));
@@ -481,24 +525,15 @@ __global__ void __launch_bounds__(kThreadsC, 1)
   if (g.seq < 0 || (!kOut && (g.last || g.slot + 1 >= a.slots))) return;
   const int nc = static_cast<int>((g.len + kC - 1) / kC);
   const float lam = a.decay[h];
-  if (threadIdx.x <= kC) {
-    const float p = decay_pow(lam, static_cast<float>(threadIdx.x));
-    ctl.tab[threadIdx.x] = p;
-    if (kOut && threadIdx.x < kC)
-      for (int m = 0; m < 4; ++m) {
-        ctl.rtab[m][m + kC - 1 - threadIdx.x] = p;
-        ctl.rtab[m][m + kC + threadIdx.x] = 0.0f;
-      }
-  }
+  if (threadIdx.x <= kC) ctl.tab[threadIdx.x] = decay_pow(lam, static_cast<float>(threadIdx.x));
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStg; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
     }
     mbar_init(sc_full, 1);
-    mbar_init(p_full, 2);
-    mbar_init(in_ready, 4 + 8);  // Q~; the state in TMEM and the last O^T read
-    mbar_init(i_done, 1);
+    mbar_init(p_full, 4);
+    mbar_init(s_ready, 8);  // the chunk's S is in TMEM, the last chunk's O1, O2 are read
     mbar_init(o_full, 1);
     mbar_init(drain, 1);
     for (int b = 0; b < 2; ++b) {
@@ -520,7 +555,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
   tc_fence_after();
   const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
   const int tail = static_cast<int>(g.len - static_cast<long long>(nc - 1) * kC);  // tokens of the last chunk
-  const uint32_t stages = smem_u32(smem) + L::kStages;
+  const uint32_t stages = smem_u32(smem);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -553,189 +588,157 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     // The whole warp runs the loop, so that descriptors stay in uniform
     // registers; one lane issues.  All 512 TMEM columns are this CTA's, so
     // their addresses start at 0.
-    constexpr uint32_t id_sc = idesc_make(128, kC, 1);
-    constexpr uint32_t id_o1 = idesc_make(128, kC, 2);
+    constexpr uint32_t id_sc = idesc_make(64, kC, 1);
+    constexpr uint32_t id_o1 = idesc_make(128, kC, 1);
     constexpr uint32_t id_o2 = idesc_make(128, kC, 1) | kTransA;
     const bool one = elect_one();
-    const uint64_t dqf = sdesc_sw128(smem_u32(smem) + L::kQf), dp = sdesc_sw128(smem_u32(smem) + L::kP);
+    const uint64_t dp = sdesc_sw128(smem_u32(smem) + L::kP);
     const uint64_t dkm0 = sdesc_mn(stages + L::kQ, kBlk), dvm0 = sdesc_mn(stages + L::kQ + L::kK, kBlk);
-    const uint64_t dk0 = sdesc_sw128(stages + L::kQ), dq0 = sdesc_sw128(stages - (kOut ? kBlk : 0));
-    // Scores of a staged chunk, queries in rows 64..127 of the A operand:
-    // rows 0..63 are the 8 KB before each block of Q, and their results
-    // (lanes 0..63) are not read.
-    auto scores = [&](int c, uint32_t s) {
-      if (!warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL)) return false;
+    const uint64_t dk0 = sdesc_sw128(stages + L::kQ), dq0 = sdesc_sw128(stages);
+    // half b of U of chunk c, staged at `at` (descriptor units)
+    auto update = [&](int c, uint32_t at, int b) {
+      const int ub = c % M::kUBufs;
+      if (!warp_wait(a, vt_full0 + 8 * b, c & 1, abort_flag, SITE_STAGE)) return false;
       tc_fence_after();
-      const uint32_t at = s * (L::kStage >> 4);
       if (one) {
-#pragma unroll
-        for (int kk = 0; kk < kDk / 16; ++kk) {
-          const uint32_t off = at + (((kk >> 2) * kBlk + 32 * (kk & 3)) >> 4);
-          MmaKind<__nv_bfloat16>::mma(M::P, dq0 + off, dk0 + off, id_sc, kk > 0 ? 1u : 0u);
-        }
-        tc_commit(sc_full);
-      }
-      return true;
-    };
-    auto update = [&](int c, uint32_t s) {
-      const int ub = c % M::kUBufs, use = c / M::kUBufs;
-      const uint32_t u = M::U + ub * kDk;
-      if (!kOut && !warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL)) return false;
-      if (!kOut && !warp_wait(a, u_empty0 + 8 * ub, (use & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY)) return false;
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        if (!warp_wait(a, vt_full0 + 8 * b, c & 1, abort_flag, SITE_STAGE)) return false;
-        tc_fence_after();
-        if (one) {
-          mma_update<kDk>(u, M::V + b * kTerms * 16, dkm0 + s * (L::kStage >> 4) + b * (4096 >> 4), b > 0);
-          tc_commit(vt_empty0 + 8 * b);
-          if (b == 1) tc_commit(u_full0 + 8 * ub);
-        }
+        mma_update<kDk>(M::U + ub * kDk, M::V + b * kTerms * 16, dkm0 + at + b * (4096 >> 4), b > 0);
+        tc_commit(vt_empty0 + 8 * b);
+        if (b == 1) tc_commit(u_full0 + 8 * ub);
       }
       return true;
     };
     if (kOut) {
       uint32_t s = 0;  // stage of chunk c
-      bool ok = true;
-      for (int c = -1; ok && c < nc; ++c) {
+      for (int c = -1; c < nc; ++c) {
         const uint32_t ph = c & 1, next = (c < 0 || s + 1 == kStg) ? 0 : s + 1;
         if (c >= 0) {
-          if (!warp_wait(a, in_ready, ph, abort_flag, SITE_STAGE)) break;
+          const uint32_t at = s * (L::kStage >> 4);
+          if (!warp_wait(a, s_ready, ph, abort_flag, SITE_STAGE)) break;
           tc_fence_after();
           if (one) {
 #pragma unroll
-            for (int kk = 0; kk < kDk / 8; ++kk)
-              mma_ts_tf32(M::O, M::S + 8 * kk, dqf + (((kk >> 2) * kBlk + 32 * (kk & 3)) >> 4), id_o1,
+            for (int kk = 0; kk < kDk / 16; ++kk)
+              mma_ts_bf16(M::O1, M::S + 8 * kk, dq0 + at + (((kk >> 2) * kBlk + 32 * (kk & 3)) >> 4), id_o1,
                           kk > 0 ? 1u : 0u);
-            tc_commit(i_done);
           }
           if (!warp_wait(a, p_full, ph, abort_flag, SITE_STAGE)) break;
           tc_fence_after();
           if (one) {
-            const uint64_t dv = dvm0 + s * (L::kStage >> 4);
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int kk = 0; kk < kC / 16; ++kk)
-                MmaKind<__nv_bfloat16>::mma(M::O, dv + kk * (2048 >> 4), dp + ((t * kBlk + 32 * kk) >> 4),
-                                            id_o2, 1u);
+            for (int kk = 0; kk < kC / 16; ++kk)
+              MmaKind<__nv_bfloat16>::mma(M::O2, dvm0 + at + kk * (2048 >> 4), dp + ((32 * kk) >> 4), id_o2,
+                                          kk > 0 ? 1u : 0u);
             tc_commit(o_full);
             tc_commit(empty0 + 8 * s);
           }
         }
-        if (c + 1 < nc) ok = scores(c + 1, next) && update(c + 1, next);
+        if (c + 1 < nc) {
+          const uint32_t at = next * (L::kStage >> 4);
+          if (!warp_wait(a, full0 + 8 * next, ((c + 1) / kStg) & 1, abort_flag, SITE_MMA_FULL)) break;
+          tc_fence_after();
+          if (one) {
+            // rows 16 g .. 16 g + 15 of a 64-row accumulator are lanes 32 g ..
+#pragma unroll
+            for (int kk = 0; kk < kDk / 16; ++kk) {
+              const uint32_t off = at + (((kk >> 2) * kBlk + 32 * (kk & 3)) >> 4);
+              MmaKind<__nv_bfloat16>::mma(M::P, dq0 + off, dk0 + off, id_sc, kk > 0 ? 1u : 0u);
+            }
+            tc_commit(sc_full);
+          }
+          if (!update(c + 1, at, 0) || !update(c + 1, at, 1)) break;
+        }
         s = next;
       }
     } else {
       uint32_t s = 0;
       for (int c = 0; c < nc; ++c) {
-        if (!update(c, s)) break;
+        const uint32_t at = s * (L::kStage >> 4);
+        if (!warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL) ||
+            !warp_wait(a, u_empty0 + 8 * (c & 1), ((c >> 1) & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY) ||
+            !update(c, at, 0) || !update(c, at, 1))
+          break;
         if (one) tc_commit(empty0 + 8 * s);
         s = s + 1 == kStg ? 0 : s + 1;
       }
     }
     if (one) tc_commit(drain);
-  } else if (kOut && warp < 4) {
-    // ------------------------------------------------------------ P
-    const int i = (wq - 2) * 32 + lane;
-    const uint32_t row = smem_u32(smem) + L::kP + i * 128;
-    // the copy of the weights in which this row's start on a 16-byte boundary
-    const float *wrow = ctl.rtab[(i + 1) & 3] + (kC - 1 - i + ((i + 1) & 3));
-    for (int c = 0; c < nc; ++c) {
-      if (!warp_wait(a, sc_full, c & 1, abort_flag, SITE_EPI_TMEM_FULL)) break;
-      tc_fence_after();
-#pragma unroll 1
-      for (int j0 = 0; j0 < kC; j0 += 32) {
-        float4 w[8];  // lambda^(i - j), 0 for j > i
-#pragma unroll
-        for (int x = 0; x < 8; ++x) w[x] = *reinterpret_cast<const float4 *>(wrow + j0 + 4 * x);
-        float v[32];
-        tmem_ld32_sync(M::P + lanes + j0, v);
-#pragma unroll
-        for (int x = 0; x < 32; x += 8) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const int j = x + e;  // (a score past the diagonal may be anything)
-            const float4 w4 = w[j >> 2];
-            f32x2 p = mul2(pack2(j0 + j <= i ? v[j] : 0.0f, j0 + j < i ? v[j + 1] : 0.0f),
-                           (e & 2) ? pack2(w4.z, w4.w) : pack2(w4.x, w4.y));
-            hi[e / 2] = take_bf16(p);
-            lo[e / 2] = high_parts(p);
-          }
-          const uint32_t at = row + ((((j0 + x) >> 3) ^ (i & 7)) << 4);
-          sts128(at, hi[0], hi[1], hi[2], hi[3]);
-          sts128(at + kBlk, lo[0], lo[1], lo[2], lo[3]);
-        }
-      }
-      fence_proxy_async_smem();
-      warp_arrive(p_full);
-    }
   } else if (warp >= 4 && warp < 8) {
-    // ------------------------------------------------------------ V~, Q~
-    const int r = threadIdx.x & 63, hf = (threadIdx.x >> 6) & 1;  // Q~: half of a row
-    const f32x2 f = pack2(ctl.tab[r + 1], ctl.tab[r + 1]);
+    // ------------------------------------------------------------ V~, P
+    // P: rows 16 wq + lane / 4, + 8; columns 8 n + 2 (lane % 4), + 1.  Past
+    // column 16 wq + 15 these rows have nothing: zeros, written once.
+    const int i = 16 * wq + (lane >> 2), j = 2 * (lane & 3);
+    f32x2 pw[8][2];  // lambda^(row - column), 0 past the diagonal
+    // this lane's row address for P's matrix stores: rows 0..7, 8..15 of two
+    // neighbouring column groups
+    const int m = lane >> 3;
+    const uint32_t dst = smem_u32(smem) + L::kP + (16 * wq + 8 * (m & 1) + (lane & 7)) * 128;
+    if (kOut) {
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int g = i + 8 * e - 8 * n - j;
+          pw[n][e] = pack2(g >= 0 ? ctl.tab[max(g, 0)] : 0.0f, g >= 1 ? ctl.tab[max(g - 1, 0)] : 0.0f);
+        }
+      for (int n = 2 * wq + 2; n < 8; n += 2) stsm4(dst + (((n + (m >> 1)) ^ (lane & 7)) << 4), 0u, 0u, 0u, 0u);
+    }
     f32x2 w[8];
     vt_weights(ctl.tab, kC, w);
-    for (int c = 0; c < nc; ++c) {
-      const int s = c % kStg, n = c == nc - 1 ? tail : kC;
-      if (!warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL)) break;
-      const uint32_t st = stages + s * L::kStage;
-      if (n < kC) {
-        zero_rows<kDk>(st + L::kQ, st + L::kQ + L::kK, wq, n);
-        vt_weights(ctl.tab, n, w);
-      }
-      bool ok = true;
+    // step x: half x % 2 of V~ of chunk x / 2, before it P of the last chunk
 #pragma unroll 1
-      for (int b = 0; b < 2; ++b) {
-        ok = warp_wait(a, vt_empty0 + 8 * b, (c & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY);
-        if (!ok) break;
+    for (int x = 0; x < 2 * nc + (kOut ? 1 : 0); ++x) {
+      const int c = x >> 1, b = x & 1, s = c % kStg;
+      if (kOut && b == 0 && c > 0) {
+        if (!warp_wait(a, sc_full, (c & 1) ^ 1, abort_flag, SITE_EPI_TMEM_FULL)) break;
+        tc_fence_after();
+        float v[32];
+        tmem_ld_16x64_sync(M::P + lanes, v);
+#pragma unroll
+        for (int n = 0; n < 8; n += 2) {
+          if (n > 2 * wq) break;
+          uint32_t p[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int nn = n + (y >> 1), e = y & 1;
+            float lo = v[4 * nn + 2 * e], hi = v[4 * nn + 2 * e + 1];
+            if (n == 2 * wq) {  // (a score past the diagonal may be anything)
+              const int g = i + 8 * e - 8 * nn - j;
+              lo = g >= 0 ? lo : 0.0f;
+              hi = g >= 1 ? hi : 0.0f;
+            }
+            unpack2(mul2(pack2(lo, hi), pw[nn][e]), lo, hi);
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(lo, hi);
+            p[y] = *reinterpret_cast<const uint32_t *>(&b2);
+          }
+          stsm4(dst + (((n + (m >> 1)) ^ (lane & 7)) << 4), p[0], p[1], p[2], p[3]);
+        }
+        fence_proxy_async_smem();
+        warp_arrive(p_full);
+      }
+      if (c < nc) {
+        const uint32_t st = stages + s * L::kStage;
+        if (b == 0) {
+          if (!warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL)) break;
+          if (c == nc - 1 && tail < kC) {
+            zero_rows<kDk>(st + L::kQ, st + L::kQ + L::kK, wq, tail);
+            vt_weights(ctl.tab, tail, w);
+          }
+        }
+        if (!warp_wait(a, vt_empty0 + 8 * b, (c & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY)) break;
         tc_fence_after();
         make_vt(st + L::kQ + L::kK + b * 4096, wq, w, M::V + b * kTerms * 16 + lanes);
         tmem_wait_st();
         warp_arrive(vt_full0 + 8 * b);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // the other half's weights come first
-          const f32x2 u = w[i];
-          w[i] = w[i + 4];
-          w[i + 4] = u;
+        for (int y = 0; y < 4; ++y) {  // the other half's weights come first
+          const f32x2 u = w[y];
+          w[y] = w[y + 4];
+          w[y + 4] = u;
         }
-      }
-      if (!ok) break;
-      if (kOut) {
-        if (c > 0 && !warp_wait(a, i_done, (c & 1) ^ 1, abort_flag, SITE_DRAIN)) break;
-        // 8 elements at a time: 16 bytes of bf16 become 32 of fp32, rounded to
-        // tf32 (half up in magnitude) by adding half of its last bit
-        const uint32_t src = st + hf * (kDk == 128 ? kBlk : 0) + r * 128;
-        const uint32_t dst = smem_u32(smem) + L::kQf + hf * (kDk / 64) * kBlk + r * 128;
-#pragma unroll 1
-        for (int y0 = 0; y0 < kDk / 16; y0 += 4) {
-          uint4 u[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y)  // 16-byte pieces of the staged row
-            u[y] = lds128(src + (((kDk == 128 ? y0 + y : 4 * hf + y) ^ (r & 7)) << 4));
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const uint32_t q[4] = {u[y].x, u[y].y, u[y].z, u[y].w};
-            uint32_t t[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float lo, hi;
-              unpack2(mul2(pack2(__uint_as_float(q[e] << 16), __uint_as_float(q[e] & 0xffff0000u)), f), lo, hi);
-              t[2 * e] = __float_as_uint(lo) + 0x1000u;
-              t[2 * e + 1] = __float_as_uint(hi) + 0x1000u;
-            }
-            const uint32_t at = dst + (y0 >> 2) * kBlk + (((2 * y) ^ (r & 7)) << 4);
-            sts128(at, t[0], t[1], t[2], t[3]);
-            sts128(at ^ 16u, t[4], t[5], t[6], t[7]);
-          }
-        }
-        fence_proxy_async_smem();
-        warp_arrive(in_ready);
       }
     }
   } else if (warp >= 8) {
-    // ------------------------------------------------------------ state, O
+    // ------------------------------------------------------------ state, outputs
     const int half = (warp - 8) >> 2;
     const int d = d0 + wq * 32 + lane;
     const bool valid = d < a.dv;
@@ -754,25 +757,41 @@ __global__ void __launch_bounds__(kThreadsC, 1)
       S[i / 2] = pack2(u.x, u.y);
       S[i / 2 + 1] = pack2(u.z, u.w);
     }
-    const uint32_t ts = M::S + half * kHalfDk + lanes;
+    // outputs: weights lambda^(i + 1) of this lane's tokens, its places in the
+    // warp's tile (rows of 64 bytes, pieces of 16 swizzled over pairs of rows)
+    f32x2 ow[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 32 * half + 8 * i + 2 * (lane & 3);
+      ow[i] = pack2(ctl.tab[t + 1], ctl.tab[t + 2]);
+    }
+    const int mm = lane >> 3;
+    const uint32_t tile = smem_u32(smem) + L::kO + (warp - 8) * 2048;
+    const uint32_t otile = tile + (8 * (mm >> 1) + (lane & 7)) * 64;
+    const uint32_t oread = tile + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+    const bool ovalid = d0 + wq * 32 + 8 * (lane & 3) < a.dv;
+    const long long ostride = static_cast<long long>(a.Hv) * a.dv;
+    __nv_bfloat16 *obase = a.o + (g.first + 32 * half + (lane >> 2)) * ostride +
+                           static_cast<long long>(h) * a.dv + d0 + wq * 32 + 8 * (lane & 3);
+    const uint32_t ts = M::S + half * (kHalfDk / 2) + lanes;
     auto put_state = [&] {
 #pragma unroll
-      for (int x = 0; x < kHalfDk; x += 16) {
-        uint32_t r[16];
+      for (int x = 0; x < kHalfDk / 2; x += 8) {
+        uint32_t r[8];
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
+        for (int i = 0; i < 8; ++i) {
           float lo, hi;
-          unpack2(S[(x + i) / 2], lo, hi);
-          r[i] = __float_as_uint(lo);
-          r[i + 1] = __float_as_uint(hi);
+          unpack2(S[x + i], lo, hi);
+          const __nv_bfloat162 b2 = __floats2bfloat162_rn(lo, hi);
+          r[i] = *reinterpret_cast<const uint32_t *>(&b2);
         }
-        tmem_st16(ts + x, r);
+        tmem_st8(ts + x, r);
       }
       tmem_wait_st();
     };
     if (kOut) {
       put_state();
-      warp_arrive(in_ready);
+      warp_arrive(s_ready);
       warp_arrive(vt_full0);
     }
     bool ok = true;
@@ -794,33 +813,43 @@ __global__ void __launch_bounds__(kThreadsC, 1)
       if (!kOut) warp_arrive(u_empty0 + 8 * ub);
       if (kOut) {
         if (c + 1 < nc) warp_arrive(vt_full0);
-        if (c + 1 < nc) {
-          ok = warp_wait(a, i_done, c & 1, abort_flag, SITE_DRAIN);
-          if (!ok) break;
-          tc_fence_after();
-          put_state();
-        }
         ok = warp_wait(a, o_full, c & 1, abort_flag, SITE_EPI_TMEM_FULL);
         if (!ok) break;
         tc_fence_after();
-        float v[32];  // tokens 32 half .. of this d_v row
-        tmem_ld32_sync(M::O + 32 * half + lanes, v);
-        if (c + 1 < nc) warp_arrive(in_ready);
-        // Lanes 2 x and 2 x + 1 hold neighbouring columns: they trade values,
-        // so that each stores both columns of every other token (4 bytes).
-        const long long ostride = static_cast<long long>(a.Hv) * a.dv;
-        const int t0 = 32 * half + (lane & 1);
-        __nv_bfloat16 *o = a.o + (g.first + static_cast<long long>(c) * kC + t0) * ostride +
-                           static_cast<long long>(h) * a.dv + (d & ~1);
-        const uint32_t sel = (lane & 1) ? 0x3276u : 0x5410u;
+        // tokens 32 half .. of the warp's 32 rows of d_v: combined 16 rows at a
+        // time, two tokens per word, and stored transposed into the warp's tile
+        // of 32 tokens x 64 bytes
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[i], v[i + 1]);
-          const uint32_t mine = *reinterpret_cast<const uint32_t *>(&b2);
-          const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-          if (valid && t0 + i < n) *reinterpret_cast<uint32_t *>(o) = __byte_perm(mine, other, sel);
-          o += 2 * ostride;
+        for (int hl = 0; hl < 2; ++hl) {
+          float u[16], v[16];
+          const uint32_t at = 32 * half + lanes + (static_cast<uint32_t>(16 * hl) << 16);
+          tmem_ld_16x32x2_sync(M::O1 + at, M::O2 + at, u, v);
+          uint32_t p[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float lo, hi;
+            unpack2(fma2(ow[i >> 1], pack2(u[2 * i], u[2 * i + 1]), pack2(v[2 * i], v[2 * i + 1])), lo, hi);
+            const __nv_bfloat162 b2 = __floats2bfloat162_rn(lo, hi);
+            p[i] = *reinterpret_cast<const uint32_t *>(&b2);
+          }
+          const uint32_t to = otile + (((2 * hl + (mm & 1)) ^ ((lane >> 1) & 3)) << 4);
+          stsm4_trans(to, p[0], p[1], p[2], p[3]);
+          stsm4_trans(to + 16 * 64, p[4], p[5], p[6], p[7]);
         }
+        if (c + 1 < nc) {
+          put_state();  // (S Q^T of this chunk is done: O1 was)
+          warp_arrive(s_ready);
+        }
+        __syncwarp();
+        // 16 bytes of a token per lane, 8 tokens per store
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = 8 * i + (lane >> 2);
+          const uint4 r = lds128(oread + 512 * i);
+          if (ovalid && 32 * half + t < n)
+            *reinterpret_cast<uint4 *>(obase + (static_cast<long long>(c) * kC + 8 * i) * ostride) = r;
+        }
+        __syncwarp();
       }
     }
     float *dst = nullptr;
