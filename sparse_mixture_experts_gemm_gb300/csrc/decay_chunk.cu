@@ -10,14 +10,19 @@
 //     O1^T    [d_v][i]   = S Q^T                          (S rounded to bf16)
 //     O2^T    [d_v][i]   = V^T P^T,  P_ij = lambda^(i-j) scores   (P in bf16)
 //     o_i                = lambda^(i+1) O1_i + O2_i
-//     U       [d_v][d_k] = V~^T K,  V~_j = lambda^(C-1-j) v_j  (bf16, three parts)
+//     U       [d_v][d_k] = V~^T K,  V~_j = lambda^(C-1-j) v_j  (bf16, four parts)
 // Every decay is a power <= 1 of lambda: nothing is divided by a decay.
 //
-// Precision.  V~ is written as three bf16 parts (24 bits; the products with
-// bf16 k are exact), each chunk's U starts from zero in TMEM, and the state
-// lives in registers, where lambda^C S + U is one fp32 fused multiply-add per
-// element: tensor-core accumulation truncates, and adding chunk after chunk
-// into one accumulator drifted to several 1e-6 of the state.  The outputs are
+// Precision.  V~ is four bf16 parts.  With the weight w = lambda^(C-1-j) as three
+// bf16 parts w1 + w2 + w3 (24 bits) and v of 8 bits, v w1 and v w2 have 16
+// bits each: a rounded bf16 product and its remainder, which a bf16 fused
+// multiply-add returns exactly; v w3 goes with the second remainder.  That is
+// five packed instructions for two values, where cutting fp32 products into
+// three parts took twelve (and those of the slower kind).  The parts are
+// multiplied smallest first, each chunk's U starts from zero in TMEM, and the
+// state lives in registers, where lambda^C S + U is one fp32 fused
+// multiply-add per element: tensor-core accumulation truncates, and adding
+// chunk after chunk into one accumulator drifted to several 1e-6 of the state.  The outputs are
 // rounded to bf16 (rms 1.7e-3) in the end; S (state's part of an output) and P
 // (the chunk's own part) enter their products as bf16, as large a rounding
 // each on its part, so that an output's rms error is sqrt(2) times that of the
@@ -54,16 +59,16 @@ constexpr int kC = kChunkTok;
 constexpr int kBlk = kC * 128;  // a 64-token tile of 128 bytes (64 bf16) per token: 8 KB
 constexpr int kThreadsC = 512;
 constexpr int kStg = 4;    // TMA stages
-constexpr int kTerms = 3;  // bf16 parts of V~
+constexpr int kTerms = 4;  // bf16 parts of V~
 constexpr uint32_t kTmemAll = 512;
 
 // TMEM columns
 template <int kDk, bool kOut>
 struct Cols {
-  static constexpr int kUBufs = kOut ? 1 : 2;
-  static constexpr uint32_t U = 0;                   // kUBufs x kDk
-  static constexpr uint32_t V = kUBufs * kDk;        // V~: two halves of 32 tokens, kTerms x 16 each
-  static constexpr uint32_t S = V + 2 * kTerms * 16; // S, two columns of d_k per TMEM column
+  static constexpr int kBufs = kOut ? 1 : 2;            // of U and V~
+  static constexpr uint32_t U = 0;                      // kDk each
+  static constexpr uint32_t V = kBufs * kDk;            // kTerms x 32 each, two tokens per column
+  static constexpr uint32_t S = V + kBufs * kTerms * 32;  // S, two columns of d_k per TMEM column
   static constexpr uint32_t O1 = S + kDk / 2;        // 64
   static constexpr uint32_t O2 = O1 + 64;            // 64
   static constexpr uint32_t P = O2 + 64;             // scores: 64
@@ -142,46 +147,10 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Pairs of floats in one 64-bit register: one instruction for two operations.
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 pack2(float a, float b) {
-  f32x2 d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
-  return d;
-}
-__device__ __forceinline__ void unpack2(f32x2 v, float &a, float &b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) {
-  f32x2 d;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-
-// The leading bf16 parts of a pair (its upper halves, the first in the low
-// half of the result); `v` keeps what they leave.  Cutting instead of rounding
-// leaves the remainder exact and one bit longer: three parts hold all 24 bits.
-__device__ __forceinline__ uint32_t high_parts(f32x2 v) {
-  float a, b;
-  unpack2(v, a, b);
-  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-}
-__device__ __forceinline__ uint32_t take_bf16(f32x2 &v) {
-  float a, b;
-  unpack2(v, a, b);
-  const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
-  v = sub2(v, pack2(__uint_as_float(x & 0xffff0000u), __uint_as_float(y & 0xffff0000u)));
-  return __byte_perm(x, y, 0x7632);
+// a pair rounded to bf16, the first in the low half
+__device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // one lane of the (converged) warp
@@ -327,13 +296,19 @@ __device__ __forceinline__ Segment find_segment(const DecayArgs &a, long long it
   return g;
 }
 
+// The weights of two tokens as bf16 parts.
+struct VtWeight {
+  __nv_bfloat162 w1, w2, w3;
+};
+
 // V~ of 32 tokens of a chunk for a warp's 32 columns of V: the staged V
 // (address `v` of the first token's row, 128-byte swizzle) times a weight per
 // token, as kTerms bf16 parts of two tokens per TMEM column, [d_v lane][token
 // pair].  Transposed matrix loads give lane l tokens 8 i + 2 (l % 4), + 1 of
-// columns l / 4, + 8 of each 16, the layout of a 16-lane TMEM store; w[i] are
-// those tokens' weights.
-__device__ __forceinline__ void make_vt(uint32_t v, int wq, const f32x2 (&w)[8], uint32_t ta) {
+// columns l / 4, + 8 of each 16, the layout of a 16-lane TMEM store; w[4 kHalf
+// + i] are those tokens' weights.
+template <int kHalf>
+__device__ __forceinline__ void make_vt(uint32_t v, int wq, const VtWeight (&w)[8], uint32_t ta) {
   const int lane = threadIdx.x & 31, m = lane >> 3;
   const uint32_t row = v + (wq >> 1) * kBlk + (8 * (m >> 1) + (lane & 7)) * 128;
   uint32_t r[4][4];  // [16 columns, 16 tokens]
@@ -345,24 +320,31 @@ __device__ __forceinline__ void make_vt(uint32_t v, int wq, const f32x2 (&w)[8],
     uint32_t p[kTerms][8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint32_t u = r[2 * hl + (e >> 2)][e & 3];
-      f32x2 x = mul2(pack2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)), w[e >> 1]);
-      p[0][e] = take_bf16(x);
-      p[1][e] = take_bf16(x);
-      p[2][e] = high_parts(x);
+      const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&r[2 * hl + (e >> 2)][e & 3]);
+      const VtWeight &u = w[4 * kHalf + (e >> 1)];
+      const __nv_bfloat162 t1 = __hmul2_rn(x, u.w1), t2 = __hmul2_rn(x, u.w2);
+      const __nv_bfloat162 t[kTerms] = {t1, __hfma2(x, u.w1, __hneg2(t1)), t2,
+                                        __hfma2(x, u.w3, __hfma2(x, u.w2, __hneg2(t2)))};
+#pragma unroll
+      for (int y = 0; y < kTerms; ++y) p[y][e] = *reinterpret_cast<const uint32_t *>(&t[y]);
     }
 #pragma unroll
     for (int t = 0; t < kTerms; ++t)
-      tmem_st_16x16(ta + 16 * t + (static_cast<uint32_t>(16 * hl) << 16), p[t]);
+      tmem_st_16x16(ta + 32 * t + (static_cast<uint32_t>(16 * hl) << 16), p[t]);
   }
 }
 
 // the weights of make_vt for a chunk of n tokens: tab[n - 1 - t] of token t
-__device__ __forceinline__ void vt_weights(const float *tab, int n, f32x2 (&w)[8]) {
+__device__ __forceinline__ void vt_weights(const float *tab, int n, VtWeight (&w)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int t = 8 * i + 2 * (threadIdx.x & 3);
-    w[i] = pack2(t < n ? tab[n - 1 - t] : 0.0f, t + 1 < n ? tab[n - 2 - t] : 0.0f);
+    float a = t < n ? tab[n - 1 - t] : 0.0f, b = t + 1 < n ? tab[n - 2 - t] : 0.0f;
+    w[i].w1 = __floats2bfloat162_rn(a, b);
+    a -= __low2float(w[i].w1);
+    b -= __high2float(w[i].w1);
+    w[i].w2 = __floats2bfloat162_rn(a, b);
+    w[i].w3 = __floats2bfloat162_rn(a - __low2float(w[i].w2), b - __high2float(w[i].w2));
   }
 }
 
@@ -384,16 +366,16 @@ __device__ __forceinline__ void zero_rows(uint32_t k, uint32_t v, int wq, int n)
   __syncwarp();
 }
 
-// half of the update product: U[d_v][d_k] += V~^T K over 32 tokens
+// the update product of a chunk, U[d_v][d_k] = V~^T K, its small parts first
 template <int kDk>
-__device__ __forceinline__ void mma_update(uint32_t u, uint32_t vt, uint64_t k, bool accumulate) {
+__device__ __forceinline__ void mma_update(uint32_t u, uint32_t vt, uint64_t k) {
   constexpr uint32_t idesc = idesc_make(128, kDk, 1) | kTransB;
 #pragma unroll
-  for (int t = 0; t < kTerms; ++t)
+  for (int t = kTerms - 1; t >= 0; --t)
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
-      mma_ts_bf16(u, vt + 16 * t + 8 * kk, k + kk * (2048 >> 4), idesc,
-                  (accumulate || t + kk > 0) ? 1u : 0u);
+    for (int kk = 0; kk < kC / 16; ++kk)
+      mma_ts_bf16(u, vt + 32 * t + 8 * kk, k + kk * (2048 >> 4), idesc,
+                  (t < kTerms - 1 || kk > 0) ? 1u : 0u);
 }
 
 __device__ __forceinline__ void fail(const DecayArgs &a, volatile int *abort_flag, int site) {
@@ -405,11 +387,12 @@ __device__ __forceinline__ void fail(const DecayArgs &a, volatile int *abort_fla
 // or the polls (each sleeps in the barrier for a while) ran out.  Short on
 // purpose: it is inlined at each wait, and the roles share one instruction
 // cache.
-constexpr int kPolls = 1 << 24;
+constexpr int kPolls = 1 << 22;
 __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, const volatile int *abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
 #pragma unroll 1
   for (int i = 0; i < kPolls; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_sleep(bar, parity, 2000u)) return true;
     if (abort_flag && *abort_flag) return false;
   }
   return false;
@@ -516,7 +499,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
   const uint32_t bar = empty0 + 8 * kStg;
   const uint32_t sc_full = bar, p_full = bar + 8, s_ready = bar + 24;
   const uint32_t o_full = bar + 32, drain = bar + 40;
-  const uint32_t vt_full0 = bar + 64, vt_empty0 = bar + 80, u_full0 = bar + 96, u_empty0 = bar + 112;
+  const uint32_t vt_full0 = bar + 64, u_full0 = bar + 80, u_empty0 = bar + 96;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3;
   const int ht = static_cast<int>(blockIdx.x % (a.Hv * a.tiles));
   const int h = ht / a.tiles, d0 = ht % a.tiles * 128;
@@ -538,8 +521,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     mbar_init(drain, 1);
     for (int b = 0; b < 2; ++b) {
       // (with outputs, also the last U read: U has one buffer then)
-      mbar_init(vt_full0 + 8 * b, kOut && b == 0 ? 4 + 8 : 4);
-      mbar_init(vt_empty0 + 8 * b, 1);
+      mbar_init(vt_full0 + 8 * b, kOut ? 4 + 8 : 4);
       mbar_init(u_full0 + 8 * b, 1);
       mbar_init(u_empty0 + 8 * b, 8);
     }
@@ -595,15 +577,14 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     const uint64_t dp = sdesc_sw128(smem_u32(smem) + L::kP);
     const uint64_t dkm0 = sdesc_mn(stages + L::kQ, kBlk), dvm0 = sdesc_mn(stages + L::kQ + L::kK, kBlk);
     const uint64_t dk0 = sdesc_sw128(stages + L::kQ), dq0 = sdesc_sw128(stages);
-    // half b of U of chunk c, staged at `at` (descriptor units)
-    auto update = [&](int c, uint32_t at, int b) {
-      const int ub = c % M::kUBufs;
-      if (!warp_wait(a, vt_full0 + 8 * b, c & 1, abort_flag, SITE_STAGE)) return false;
+    // U of chunk c, staged at `at` (descriptor units)
+    auto update = [&](int c, uint32_t at) {
+      const int ub = c % M::kBufs;
+      if (!warp_wait(a, vt_full0 + 8 * ub, (c / M::kBufs) & 1, abort_flag, SITE_STAGE)) return false;
       tc_fence_after();
       if (one) {
-        mma_update<kDk>(M::U + ub * kDk, M::V + b * kTerms * 16, dkm0 + at + b * (4096 >> 4), b > 0);
-        tc_commit(vt_empty0 + 8 * b);
-        if (b == 1) tc_commit(u_full0 + 8 * ub);
+        mma_update<kDk>(M::U + ub * kDk, M::V + ub * kTerms * 32, dkm0 + at);
+        tc_commit(u_full0 + 8 * ub);
       }
       return true;
     };
@@ -645,7 +626,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
             }
             tc_commit(sc_full);
           }
-          if (!update(c + 1, at, 0) || !update(c + 1, at, 1)) break;
+          if (!update(c + 1, at)) break;
         }
         s = next;
       }
@@ -655,7 +636,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
         const uint32_t at = s * (L::kStage >> 4);
         if (!warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL) ||
             !warp_wait(a, u_empty0 + 8 * (c & 1), ((c >> 1) & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY) ||
-            !update(c, at, 0) || !update(c, at, 1))
+            !update(c, at))
           break;
         if (one) tc_commit(empty0 + 8 * s);
         s = s + 1 == kStg ? 0 : s + 1;
@@ -667,7 +648,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     // P: rows 16 wq + lane / 4, + 8; columns 8 n + 2 (lane % 4), + 1.  Past
     // column 16 wq + 15 these rows have nothing: zeros, written once.
     const int i = 16 * wq + (lane >> 2), j = 2 * (lane & 3);
-    f32x2 pw[8][2];  // lambda^(row - column), 0 past the diagonal
+    float pw[8][2][2];  // lambda^(row - column), 0 past the diagonal
     // this lane's row address for P's matrix stores: rows 0..7, 8..15 of two
     // neighbouring column groups
     const int m = lane >> 3;
@@ -678,18 +659,32 @@ __global__ void __launch_bounds__(kThreadsC, 1)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int g = i + 8 * e - 8 * n - j;
-          pw[n][e] = pack2(g >= 0 ? ctl.tab[max(g, 0)] : 0.0f, g >= 1 ? ctl.tab[max(g - 1, 0)] : 0.0f);
+          pw[n][e][0] = g >= 0 ? ctl.tab[max(g, 0)] : 0.0f;
+          pw[n][e][1] = g >= 1 ? ctl.tab[max(g - 1, 0)] : 0.0f;
         }
       for (int n = 2 * wq + 2; n < 8; n += 2) stsm4(dst + (((n + (m >> 1)) ^ (lane & 7)) << 4), 0u, 0u, 0u, 0u);
     }
-    f32x2 w[8];
+    VtWeight w[8];
     vt_weights(ctl.tab, kC, w);
-    // step x: half x % 2 of V~ of chunk x / 2, before it P of the last chunk
-#pragma unroll 1
-    for (int x = 0; x < 2 * nc + (kOut ? 1 : 0); ++x) {
-      const int c = x >> 1, b = x & 1, s = c % kStg;
-      if (kOut && b == 0 && c > 0) {
-        if (!warp_wait(a, sc_full, (c & 1) ^ 1, abort_flag, SITE_EPI_TMEM_FULL)) break;
+    for (int c = 0; c < nc; ++c) {
+      const int s = c % kStg, vb = c % M::kBufs;
+      const uint32_t st = stages + s * L::kStage;
+      // U of the chunk that last used this buffer of V~ is done
+      if (!warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL) ||
+          !warp_wait(a, u_full0 + 8 * vb, ((c / M::kBufs) & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY))
+        break;
+      tc_fence_after();
+      if (c == nc - 1 && tail < kC) {
+        zero_rows<kDk>(st + L::kQ, st + L::kQ + L::kK, wq, tail);
+        vt_weights(ctl.tab, tail, w);
+      }
+      const uint32_t v = st + L::kQ + L::kK, ta = M::V + vb * kTerms * 32 + lanes;
+      make_vt<0>(v, wq, w, ta);
+      make_vt<1>(v + 32 * 128, wq, w, ta + 16);
+      tmem_wait_st();
+      warp_arrive(vt_full0 + 8 * vb);
+      if (kOut) {
+        if (!warp_wait(a, sc_full, c & 1, abort_flag, SITE_EPI_TMEM_FULL)) break;
         tc_fence_after();
         float v[32];
         tmem_ld_16x64_sync(M::P + lanes, v);
@@ -706,35 +701,12 @@ __global__ void __launch_bounds__(kThreadsC, 1)
               lo = g >= 0 ? lo : 0.0f;
               hi = g >= 1 ? hi : 0.0f;
             }
-            unpack2(mul2(pack2(lo, hi), pw[nn][e]), lo, hi);
-            const __nv_bfloat162 b2 = __floats2bfloat162_rn(lo, hi);
-            p[y] = *reinterpret_cast<const uint32_t *>(&b2);
+            p[y] = bf16x2_bits(lo * pw[nn][e][0], hi * pw[nn][e][1]);
           }
           stsm4(dst + (((n + (m >> 1)) ^ (lane & 7)) << 4), p[0], p[1], p[2], p[3]);
         }
         fence_proxy_async_smem();
         warp_arrive(p_full);
-      }
-      if (c < nc) {
-        const uint32_t st = stages + s * L::kStage;
-        if (b == 0) {
-          if (!warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL)) break;
-          if (c == nc - 1 && tail < kC) {
-            zero_rows<kDk>(st + L::kQ, st + L::kQ + L::kK, wq, tail);
-            vt_weights(ctl.tab, tail, w);
-          }
-        }
-        if (!warp_wait(a, vt_empty0 + 8 * b, (c & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY)) break;
-        tc_fence_after();
-        make_vt(st + L::kQ + L::kK + b * 4096, wq, w, M::V + b * kTerms * 16 + lanes);
-        tmem_wait_st();
-        warp_arrive(vt_full0 + 8 * b);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {  // the other half's weights come first
-          const f32x2 u = w[y];
-          w[y] = w[y + 4];
-          w[y + 4] = u;
-        }
       }
     }
   } else if (warp >= 8) {
@@ -743,7 +715,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     const int d = d0 + wq * 32 + lane;
     const bool valid = d < a.dv;
     const long long srow = ((static_cast<long long>(g.seq) * a.Hv + h) * a.dv + d) * kDk + half * kHalfDk;
-    f32x2 S[kHalfDk / 2];
+    float S[kHalfDk];
     const float *src = nullptr;
     if (kOut && valid) {
       if (g.index == 0)
@@ -754,16 +726,19 @@ __global__ void __launch_bounds__(kThreadsC, 1)
 #pragma unroll
     for (int i = 0; i < kHalfDk; i += 4) {
       const float4 u = src ? *reinterpret_cast<const float4 *>(src + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-      S[i / 2] = pack2(u.x, u.y);
-      S[i / 2 + 1] = pack2(u.z, u.w);
+      S[i] = u.x;
+      S[i + 1] = u.y;
+      S[i + 2] = u.z;
+      S[i + 3] = u.w;
     }
     // outputs: weights lambda^(i + 1) of this lane's tokens, its places in the
     // warp's tile (rows of 64 bytes, pieces of 16 swizzled over pairs of rows)
-    f32x2 ow[4];
+    float ow[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = 32 * half + 8 * i + 2 * (lane & 3);
-      ow[i] = pack2(ctl.tab[t + 1], ctl.tab[t + 2]);
+      ow[i][0] = ctl.tab[t + 1];
+      ow[i][1] = ctl.tab[t + 2];
     }
     const int mm = lane >> 3;
     const uint32_t tile = smem_u32(smem) + L::kO + (warp - 8) * 2048;
@@ -779,12 +754,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
       for (int x = 0; x < kHalfDk / 2; x += 8) {
         uint32_t r[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float lo, hi;
-          unpack2(S[x + i], lo, hi);
-          const __nv_bfloat162 b2 = __floats2bfloat162_rn(lo, hi);
-          r[i] = *reinterpret_cast<const uint32_t *>(&b2);
-        }
+        for (int i = 0; i < 8; ++i) r[i] = bf16x2_bits(S[2 * (x + i)], S[2 * (x + i) + 1]);
         tmem_st8(ts + x, r);
       }
       tmem_wait_st();
@@ -797,8 +767,8 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     bool ok = true;
     for (int c = 0; c < nc; ++c) {
       const int n = c == nc - 1 ? tail : kC;
-      const int ub = c % M::kUBufs, use = c / M::kUBufs;
-      const f32x2 f = pack2(ctl.tab[n], ctl.tab[n]);
+      const int ub = c % M::kBufs, use = c / M::kBufs;
+      const float f = ctl.tab[n];
       ok = warp_wait(a, u_full0 + 8 * ub, use & 1, abort_flag, SITE_EPI_TMEM_FULL);
       if (!ok) break;
       tc_fence_after();
@@ -807,8 +777,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
         float u[32];
         tmem_ld32_sync(M::U + ub * kDk + half * kHalfDk + x + lanes, u);
 #pragma unroll
-        for (int i = 0; i < 32; i += 2)
-          S[(x + i) / 2] = fma2(f, S[(x + i) / 2], pack2(u[i], u[i + 1]));
+        for (int i = 0; i < 32; ++i) S[x + i] = fmaf(f, S[x + i], u[i]);
       }
       if (!kOut) warp_arrive(u_empty0 + 8 * ub);
       if (kOut) {
@@ -827,10 +796,8 @@ __global__ void __launch_bounds__(kThreadsC, 1)
           uint32_t p[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            float lo, hi;
-            unpack2(fma2(ow[i >> 1], pack2(u[2 * i], u[2 * i + 1]), pack2(v[2 * i], v[2 * i + 1])), lo, hi);
-            const __nv_bfloat162 b2 = __floats2bfloat162_rn(lo, hi);
-            p[i] = *reinterpret_cast<const uint32_t *>(&b2);
+            p[i] = bf16x2_bits(fmaf(ow[i >> 1][0], u[2 * i], v[2 * i]),
+                               fmaf(ow[i >> 1][1], u[2 * i + 1], v[2 * i + 1]));
           }
           const uint32_t to = otile + (((2 * hl + (mm & 1)) ^ ((lane >> 1) & 3)) << 4);
           stsm4_trans(to, p[0], p[1], p[2], p[3]);
@@ -861,12 +828,8 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     }
     if (dst) {
 #pragma unroll
-      for (int i = 0; i < kHalfDk; i += 4) {
-        float4 u;
-        unpack2(S[i / 2], u.x, u.y);
-        unpack2(S[i / 2 + 1], u.z, u.w);
-        *reinterpret_cast<float4 *>(dst + i) = u;
-      }
+      for (int i = 0; i < kHalfDk; i += 4)
+        *reinterpret_cast<float4 *>(dst + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
     }
   }
   __syncwarp();
