@@ -247,8 +247,9 @@ extern "C" int gdn_decay_scan(const void *q, const void *k, const void *v, const
   a.Hk = n_k_heads;
   a.Hv = n_v_heads;
   a.dv = d_v;
-  a.recur = kRecur;
-  a.seg_len = plan.seg_len;
+  a.recur = static_cast<int>(kRecur);
+  a.seg_len = static_cast<int>(plan.seg_len);
+  a.seq_len = static_cast<int>(n_tokens / n_seq);
   a.slots = plan.slots;
   a.items = plan.items;
   a.ws = static_cast<float *>(workspace);

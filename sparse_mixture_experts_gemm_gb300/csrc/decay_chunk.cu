@@ -220,14 +220,13 @@ __device__ __forceinline__ Segment find_segment(const DecayArgs &a, long long it
   long long len = 0, first = 0, before = 0;
   int seq = -1, rank = 0;
   if (!a.offsets) {
-    len = a.n_tokens / a.n_seq;
-    const long long n = max((len + a.seg_len - 1) / a.seg_len, 1LL);
-    if (item < n * a.n_seq) {
-      seq = static_cast<int>(item / n);
-      rank = seq;
-      before = n * seq;
-      first = len * seq;
-    }
+    len = a.seq_len;  // (fewer than 2^31 tokens, segments and items)
+    const int n = max((static_cast<int>(len) + a.seg_len - 1) / a.seg_len, 1);
+    seq = static_cast<int>(item) / n;
+    if (seq >= a.n_seq) seq = -1;
+    rank = seq;
+    before = n * seq;
+    first = len * seq;
   } else {
     // running number of segments, a block's worth of sequences at a time
     int *warp_sum = scratch, *found = scratch + 32;
@@ -242,7 +241,7 @@ __device__ __forceinline__ Segment find_segment(const DecayArgs &a, long long it
       long long l = 0, f = 0;
       if (i < a.n_seq) {
         seq_range(a, i, f, l);
-        n = l <= a.recur ? 0 : static_cast<int>((l + a.seg_len - 1) / a.seg_len);
+        n = l <= a.recur ? 0 : (static_cast<int>(l) + a.seg_len - 1) / a.seg_len;
       }
       int inc = n;
 #pragma unroll
@@ -288,7 +287,7 @@ __device__ __forceinline__ Segment find_segment(const DecayArgs &a, long long it
   if (seq < 0) return g;
   g.seq = seq;
   g.index = item - before;
-  const long long at = g.index * a.seg_len;
+  const long long at = static_cast<long long>(g.index) * a.seg_len;
   g.first = first + at;
   g.last = at + a.seg_len >= len;
   g.len = g.last ? len - at : a.seg_len;
@@ -306,9 +305,11 @@ struct VtWeight {
 // token, as kTerms bf16 parts of two tokens per TMEM column, [d_v lane][token
 // pair].  Transposed matrix loads give lane l tokens 8 i + 2 (l % 4), + 1 of
 // columns l / 4, + 8 of each 16, the layout of a 16-lane TMEM store; w[4 kHalf
-// + i] are those tokens' weights.
+// + i] are those tokens' weights.  The leading parts are left to the caller,
+// because their TMEM columns are the last to become free.
 template <int kHalf>
-__device__ __forceinline__ void make_vt(uint32_t v, int wq, const VtWeight (&w)[8], uint32_t ta) {
+__device__ __forceinline__ void make_vt(uint32_t v, int wq, const VtWeight (&w)[8], uint32_t ta,
+                                        uint32_t (&lead)[2][8]) {
   const int lane = threadIdx.x & 31, m = lane >> 3;
   const uint32_t row = v + (wq >> 1) * kBlk + (8 * (m >> 1) + (lane & 7)) * 128;
   uint32_t r[4][4];  // [16 columns, 16 tokens]
@@ -317,20 +318,21 @@ __device__ __forceinline__ void make_vt(uint32_t v, int wq, const VtWeight (&w)[
     ldsm4_trans(row + ((((wq & 1) * 4 + 2 * (x >> 1) + (m & 1)) ^ (lane & 7)) << 4) + (x & 1) * 2048, r[x]);
 #pragma unroll
   for (int hl = 0; hl < 2; ++hl) {
-    uint32_t p[kTerms][8];
+    uint32_t p[kTerms - 1][8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162 *>(&r[2 * hl + (e >> 2)][e & 3]);
       const VtWeight &u = w[4 * kHalf + (e >> 1)];
       const __nv_bfloat162 t1 = __hmul2_rn(x, u.w1), t2 = __hmul2_rn(x, u.w2);
-      const __nv_bfloat162 t[kTerms] = {t1, __hfma2(x, u.w1, __hneg2(t1)), t2,
-                                        __hfma2(x, u.w3, __hfma2(x, u.w2, __hneg2(t2)))};
+      const __nv_bfloat162 t[kTerms - 1] = {__hfma2(x, u.w1, __hneg2(t1)), t2,
+                                            __hfma2(x, u.w3, __hfma2(x, u.w2, __hneg2(t2)))};
+      lead[hl][e] = *reinterpret_cast<const uint32_t *>(&t1);
 #pragma unroll
-      for (int y = 0; y < kTerms; ++y) p[y][e] = *reinterpret_cast<const uint32_t *>(&t[y]);
+      for (int y = 0; y < kTerms - 1; ++y) p[y][e] = *reinterpret_cast<const uint32_t *>(&t[y]);
     }
 #pragma unroll
-    for (int t = 0; t < kTerms; ++t)
-      tmem_st_16x16(ta + 32 * t + (static_cast<uint32_t>(16 * hl) << 16), p[t]);
+    for (int t = 1; t < kTerms; ++t)
+      tmem_st_16x16(ta + 32 * t + (static_cast<uint32_t>(16 * hl) << 16), p[t - 1]);
   }
 }
 
@@ -345,6 +347,61 @@ __device__ __forceinline__ void vt_weights(const float *tab, int n, VtWeight (&w
     b -= __high2float(w[i].w1);
     w[i].w2 = __floats2bfloat162_rn(a, b);
     w[i].w3 = __floats2bfloat162_rn(a - __low2float(w[i].w2), b - __high2float(w[i].w2));
+  }
+}
+
+// A warp's 32 rows of kN floats, `pitch` floats apart in global memory, one row
+// per lane: whole lines in global memory, turned in the warp's `tile` of shared
+// memory (16-byte pieces swizzled by row).  Rows from `rows` on are zeros, not
+// touched in global memory.
+template <int kN>
+__device__ __forceinline__ void load_rows(float (&v)[kN], uint32_t tile, const float *src, int pitch,
+                                          int rows) {
+  constexpr int kP = kN / 4;
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int i0 = 0; i0 < kP; i0 += 8) {
+    uint4 u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = ((i0 + i) * 32 + lane) / kP, p = ((i0 + i) * 32 + lane) % kP;
+      u[i] = make_uint4(0, 0, 0, 0);
+      if (src && r < rows)
+        u[i] = *reinterpret_cast<const uint4 *>(src + static_cast<long long>(r) * pitch + 4 * p);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = ((i0 + i) * 32 + lane) / kP, p = ((i0 + i) * 32 + lane) % kP;
+      sts128(tile + (r * kP + (p ^ (r & (kP - 1)))) * 16, u[i].x, u[i].y, u[i].z, u[i].w);
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int p = 0; p < kP; ++p) {
+    const uint4 w = lds128(tile + (lane * kP + (p ^ (lane & (kP - 1)))) * 16);
+    v[4 * p] = __uint_as_float(w.x);
+    v[4 * p + 1] = __uint_as_float(w.y);
+    v[4 * p + 2] = __uint_as_float(w.z);
+    v[4 * p + 3] = __uint_as_float(w.w);
+  }
+  __syncwarp();
+}
+template <int kN>
+__device__ __forceinline__ void store_rows(const float (&v)[kN], uint32_t tile, float *dst, int pitch,
+                                           int rows) {
+  constexpr int kP = kN / 4;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int p = 0; p < kP; ++p)
+    sts128(tile + (lane * kP + (p ^ (lane & (kP - 1)))) * 16, __float_as_uint(v[4 * p]),
+           __float_as_uint(v[4 * p + 1]), __float_as_uint(v[4 * p + 2]), __float_as_uint(v[4 * p + 3]));
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kP; ++i) {
+    const int r = (i * 32 + lane) / kP, p = (i * 32 + lane) % kP;
+    if (r < rows)
+      *reinterpret_cast<uint4 *>(dst + static_cast<long long>(r) * pitch + 4 * p) =
+          lds128(tile + (r * kP + (p ^ (r & (kP - 1)))) * 16);
   }
 }
 
@@ -366,16 +423,15 @@ __device__ __forceinline__ void zero_rows(uint32_t k, uint32_t v, int wq, int n)
   __syncwarp();
 }
 
-// the update product of a chunk, U[d_v][d_k] = V~^T K, its small parts first
+// One part of the update product U[d_v][d_k] = V~^T K over k steps kk0, kk0 + 1
+// (16 tokens each)
 template <int kDk>
-__device__ __forceinline__ void mma_update(uint32_t u, uint32_t vt, uint64_t k) {
+__device__ __forceinline__ void mma_update(uint32_t u, uint32_t vt, uint64_t k, int t, int kk0,
+                                           bool accumulate) {
   constexpr uint32_t idesc = idesc_make(128, kDk, 1) | kTransB;
 #pragma unroll
-  for (int t = kTerms - 1; t >= 0; --t)
-#pragma unroll
-    for (int kk = 0; kk < kC / 16; ++kk)
-      mma_ts_bf16(u, vt + 32 * t + 8 * kk, k + kk * (2048 >> 4), idesc,
-                  (t < kTerms - 1 || kk > 0) ? 1u : 0u);
+  for (int kk = kk0; kk < kk0 + 2; ++kk)
+    mma_ts_bf16(u, vt + 32 * t + 8 * kk, k + kk * (2048 >> 4), idesc, (accumulate || kk > kk0) ? 1u : 0u);
 }
 
 __device__ __forceinline__ void fail(const DecayArgs &a, volatile int *abort_flag, int site) {
@@ -424,7 +480,7 @@ struct Smem {
   static constexpr int kP = kStg * kStage;
   static constexpr int kO = kP + (kOut ? kBlk : 0);
   static constexpr int kCtl = kO + (kOut ? 8 * 2048 : 0);
-  static constexpr int kTotal = kCtl + 1024 + 1024;
+  static constexpr int kTotal = kCtl + 2048 + 1024;
 };
 
 struct Ctl {
@@ -432,9 +488,11 @@ struct Ctl {
   uint32_t tmem;
   int abort_flag;
   int scratch[36];
+  // lambda^63 .. lambda^0, then zeros, in copies that start 0 and 1 words late
+  alignas(16) float rtab[2][2 * kC + 8];
   float tab[kC + 1];  // lambda^0 .. lambda^64
 };
-static_assert(sizeof(Ctl) <= 1024, "control block");
+static_assert(sizeof(Ctl) <= 2048, "control block");
 
 }  // namespace
 
@@ -455,7 +513,7 @@ __global__ void __launch_bounds__(256) decay_chain_kernel(const DecayArgs a, int
   if (g.seq < 0 || g.index != 0 || g.last) return;
   long long first, len;
   seq_range(a, g.seq, first, len);
-  const long long n = (len + a.seg_len - 1) / a.seg_len - 1;  // slots of the sequence
+  const long long n = (static_cast<int>(len) + a.seg_len - 1) / a.seg_len - 1;  // slots of the sequence
   if (e >= per || g.slot + 1 + n > a.slots) return;
   const float f = decay_pow(a.decay[h], static_cast<float>(a.seg_len));
   const long long step = static_cast<long long>(a.Hv) * per;
@@ -499,7 +557,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
   const uint32_t bar = empty0 + 8 * kStg;
   const uint32_t sc_full = bar, p_full = bar + 8, s_ready = bar + 24;
   const uint32_t o_full = bar + 32, drain = bar + 40;
-  const uint32_t vt_full0 = bar + 64, u_full0 = bar + 80, u_empty0 = bar + 96;
+  const uint32_t vt_full0 = bar + 64, u_full0 = bar + 80, u_empty0 = bar + 96, vt_part0 = bar + 112;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3;
   const int ht = static_cast<int>(blockIdx.x % (a.Hv * a.tiles));
   const int h = ht / a.tiles, d0 = ht % a.tiles * 128;
@@ -508,7 +566,15 @@ __global__ void __launch_bounds__(kThreadsC, 1)
   if (g.seq < 0 || (!kOut && (g.last || g.slot + 1 >= a.slots))) return;
   const int nc = static_cast<int>((g.len + kC - 1) / kC);
   const float lam = a.decay[h];
-  if (threadIdx.x <= kC) ctl.tab[threadIdx.x] = decay_pow(lam, static_cast<float>(threadIdx.x));
+  if (threadIdx.x <= kC) {
+    const float p = decay_pow(lam, static_cast<float>(threadIdx.x));
+    ctl.tab[threadIdx.x] = p;
+    if (kOut && threadIdx.x < kC)
+      for (int m = 0; m < 2; ++m) {
+        ctl.rtab[m][m + kC - 1 - threadIdx.x] = p;
+        ctl.rtab[m][m + kC + threadIdx.x] = 0.0f;
+      }
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStg; ++s) {
       mbar_init(full0 + 8 * s, 1);
@@ -522,6 +588,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     for (int b = 0; b < 2; ++b) {
       // (with outputs, also the last U read: U has one buffer then)
       mbar_init(vt_full0 + 8 * b, kOut ? 4 + 8 : 4);
+      mbar_init(vt_part0 + 8 * b, 1);
       mbar_init(u_full0 + 8 * b, 1);
       mbar_init(u_empty0 + 8 * b, 8);
     }
@@ -548,6 +615,10 @@ __global__ void __launch_bounds__(kThreadsC, 1)
       for (; c < nc; ++c) {
         const int s = c % kStg;
         if (!poll(empty0 + 8 * s, ((c / kStg) & 1) ^ 1, abort_flag)) {
+          fail(a, abort_flag, SITE_PRODUCER_EMPTY);
+          break;
+        }
+        if (kOut && c == kStg - 2 && !poll(s_ready, 0, abort_flag)) {  // (the state's rows lie there)
           fail(a, abort_flag, SITE_PRODUCER_EMPTY);
           break;
         }
@@ -583,7 +654,19 @@ __global__ void __launch_bounds__(kThreadsC, 1)
       if (!warp_wait(a, vt_full0 + 8 * ub, (c / M::kBufs) & 1, abort_flag, SITE_STAGE)) return false;
       tc_fence_after();
       if (one) {
-        mma_update<kDk>(M::U + ub * kDk, M::V + ub * kTerms * 32, dkm0 + at);
+        // the small parts of each half of the tokens, then the leading ones:
+        // few sums are truncated at the size of the result, and V~ of the next
+        // chunk can follow part by part
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+          for (int t = kTerms - 1; t > 0; --t)
+            mma_update<kDk>(M::U + ub * kDk, M::V + ub * kTerms * 32, dkm0 + at, t, 2 * b,
+                            b > 0 || t < kTerms - 1);
+          if (kOut) tc_commit(vt_part0 + 8 * b);
+        }
+        mma_update<kDk>(M::U + ub * kDk, M::V + ub * kTerms * 32, dkm0 + at, 0, 0, true);
+        mma_update<kDk>(M::U + ub * kDk, M::V + ub * kTerms * 32, dkm0 + at, 0, 2, true);
         tc_commit(u_full0 + 8 * ub);
       }
       return true;
@@ -648,20 +731,14 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     // P: rows 16 wq + lane / 4, + 8; columns 8 n + 2 (lane % 4), + 1.  Past
     // column 16 wq + 15 these rows have nothing: zeros, written once.
     const int i = 16 * wq + (lane >> 2), j = 2 * (lane & 3);
-    float pw[8][2][2];  // lambda^(row - column), 0 past the diagonal
+    // weights lambda^(row - column): pairs in the copy of the table in which
+    // this lane's pairs start on 8-byte boundaries
+    const float *pw = ctl.rtab[(i + 1) & 1] + (kC - 1 - i + ((i + 1) & 1)) + j;
     // this lane's row address for P's matrix stores: rows 0..7, 8..15 of two
     // neighbouring column groups
     const int m = lane >> 3;
     const uint32_t dst = smem_u32(smem) + L::kP + (16 * wq + 8 * (m & 1) + (lane & 7)) * 128;
     if (kOut) {
-#pragma unroll
-      for (int n = 0; n < 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int g = i + 8 * e - 8 * n - j;
-          pw[n][e][0] = g >= 0 ? ctl.tab[max(g, 0)] : 0.0f;
-          pw[n][e][1] = g >= 1 ? ctl.tab[max(g - 1, 0)] : 0.0f;
-        }
       for (int n = 2 * wq + 2; n < 8; n += 2) stsm4(dst + (((n + (m >> 1)) ^ (lane & 7)) << 4), 0u, 0u, 0u, 0u);
     }
     VtWeight w[8];
@@ -669,9 +746,11 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     for (int c = 0; c < nc; ++c) {
       const int s = c % kStg, vb = c % M::kBufs;
       const uint32_t st = stages + s * L::kStage;
-      // U of the chunk that last used this buffer of V~ is done
+      // the products that last used this buffer of V~ are done: with outputs
+      // (one buffer) part by part, below
+      const uint32_t before = ((c / M::kBufs) & 1) ^ 1;
       if (!warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL) ||
-          !warp_wait(a, u_full0 + 8 * vb, ((c / M::kBufs) & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY))
+          !warp_wait(a, kOut ? vt_part0 : u_full0 + 8 * vb, before, abort_flag, SITE_MMA_TMEM_EMPTY))
         break;
       tc_fence_after();
       if (c == nc - 1 && tail < kC) {
@@ -679,8 +758,22 @@ __global__ void __launch_bounds__(kThreadsC, 1)
         vt_weights(ctl.tab, tail, w);
       }
       const uint32_t v = st + L::kQ + L::kK, ta = M::V + vb * kTerms * 32 + lanes;
-      make_vt<0>(v, wq, w, ta);
-      make_vt<1>(v + 32 * 128, wq, w, ta + 16);
+      uint32_t lead[2][2][8];
+      make_vt<0>(v, wq, w, ta, lead[0]);
+      if (kOut) {
+        if (!warp_wait(a, vt_part0 + 8, before, abort_flag, SITE_MMA_TMEM_EMPTY)) break;
+        tc_fence_after();
+      }
+      make_vt<1>(v + 32 * 128, wq, w, ta + 16, lead[1]);
+      if (kOut) {
+        if (!warp_wait(a, u_full0, before, abort_flag, SITE_MMA_TMEM_EMPTY)) break;
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int hl = 0; hl < 2; ++hl)
+          tmem_st_16x16(ta + 16 * b + (static_cast<uint32_t>(16 * hl) << 16), lead[b][hl]);
       tmem_wait_st();
       warp_arrive(vt_full0 + 8 * vb);
       if (kOut) {
@@ -701,7 +794,8 @@ __global__ void __launch_bounds__(kThreadsC, 1)
               lo = g >= 0 ? lo : 0.0f;
               hi = g >= 1 ? hi : 0.0f;
             }
-            p[y] = bf16x2_bits(lo * pw[nn][e][0], hi * pw[nn][e][1]);
+            const float2 pw2 = *reinterpret_cast<const float2 *>(pw + 8 * nn - 8 * e);
+            p[y] = bf16x2_bits(lo * pw2.x, hi * pw2.y);
           }
           stsm4(dst + (((n + (m >> 1)) ^ (lane & 7)) << 4), p[0], p[1], p[2], p[3]);
         }
@@ -712,24 +806,24 @@ __global__ void __launch_bounds__(kThreadsC, 1)
   } else if (warp >= 8) {
     // ------------------------------------------------------------ state, outputs
     const int half = (warp - 8) >> 2;
-    const int d = d0 + wq * 32 + lane;
-    const bool valid = d < a.dv;
-    const long long srow = ((static_cast<long long>(g.seq) * a.Hv + h) * a.dv + d) * kDk + half * kHalfDk;
+    const long long srow =
+        ((static_cast<long long>(g.seq) * a.Hv + h) * a.dv + d0 + wq * 32) * kDk + half * kHalfDk;
     float S[kHalfDk];
+    // this warp's 32 rows, this half of d_k
     const float *src = nullptr;
-    if (kOut && valid) {
+    if (kOut) {
       if (g.index == 0)
         src = a.s_in ? a.s_in + srow : nullptr;
       else if (g.slot < a.slots)
-        src = a.ws + ((g.slot * a.Hv + h) * a.dv + d) * kDk + half * kHalfDk;
+        src = a.ws + ((g.slot * a.Hv + h) * a.dv + d0 + wq * 32) * kDk + half * kHalfDk;
     }
+    // (the last two stages are not loaded before the state is in TMEM)
+    const uint32_t srows = stages + (kStg - 2) * L::kStage + (warp - 8) * 32 * kHalfDk * 4;
+    if (kOut) {
+      load_rows<kHalfDk>(S, srows, src, kDk, a.dv - d0 - wq * 32);
+    } else {
 #pragma unroll
-    for (int i = 0; i < kHalfDk; i += 4) {
-      const float4 u = src ? *reinterpret_cast<const float4 *>(src + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-      S[i] = u.x;
-      S[i + 1] = u.y;
-      S[i + 2] = u.z;
-      S[i + 3] = u.w;
+      for (int i = 0; i < kHalfDk; ++i) S[i] = 0.0f;
     }
     // outputs: weights lambda^(i + 1) of this lane's tokens, its places in the
     // warp's tile (rows of 64 bytes, pieces of 16 swizzled over pairs of rows)
@@ -820,17 +914,14 @@ __global__ void __launch_bounds__(kThreadsC, 1)
       }
     }
     float *dst = nullptr;
-    if (ok && valid) {
+    if (ok) {
       if (!kOut)
-        dst = a.ws + (((g.slot + 1) * a.Hv + h) * a.dv + d) * kDk + half * kHalfDk;
+        dst = a.ws + (((g.slot + 1) * a.Hv + h) * a.dv + d0 + wq * 32) * kDk + half * kHalfDk;
       else if (g.last && a.s_out)
         dst = a.s_out + srow;
     }
-    if (dst) {
-#pragma unroll
-      for (int i = 0; i < kHalfDk; i += 4)
-        *reinterpret_cast<float4 *>(dst + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
-    }
+    // (every product of the CTA that reads the stages is done)
+    if (dst) store_rows<kHalfDk>(S, srows, dst, kDk, a.dv - d0 - wq * 32);
   }
   __syncwarp();
   const bool fin = poll(drain, 0, nullptr);

@@ -22,7 +22,8 @@ struct DecayArgs {
   // the chunked ones, in segments of seg_len tokens (a multiple of 64); ws
   // holds the state before each segment but a sequence's first, `slots` of
   // them at most, [slot][Hv][dv][dk].
-  long long recur, seg_len, slots, items;
+  int recur, seg_len, seq_len;  // seq_len: of every sequence without offsets
+  long long slots, items;
   float *ws;
   int tiles;  // 128-wide tiles of d_v
   int *status;
@@ -38,7 +39,7 @@ __device__ __forceinline__ void seq_range(const DecayArgs &a, int i, long long &
     first = lo;
     len = hi - lo;
   } else {
-    len = a.n_tokens / a.n_seq;
+    len = a.seq_len;
     first = len * i;
   }
 }
