@@ -575,6 +575,22 @@ __global__ void __launch_bounds__(kThreadsC, 1)
         ctl.rtab[m][m + kC + threadIdx.x] = 0.0f;
       }
   }
+  const uint32_t stages = smem_u32(smem);
+  // (one thread) the copies of chunk c
+  auto load = [&](int c) {
+    const uint64_t pol = policy_evict_last();
+    const int s = c % kStg, hk = h / (a.Hv / a.Hk);
+    const uint32_t dst = stages + s * L::kStage, fb = full0 + 8 * s;
+    const int y = static_cast<int>(g.first) + c * kC;
+    mbar_arrive_expect_tx(fb, L::kStage);
+    for (int b = 0; b < kDk / 64; ++b) {
+      tma_load_2d(dst + L::kQ + b * kBlk, &tmK, fb, hk * kDk + 64 * b, y, pol);
+      if (kOut) tma_load_2d(dst + b * kBlk, &tmQ, fb, hk * kDk + 64 * b, y, pol);
+    }
+    for (int b = 0; b < 2; ++b)
+      tma_load_2d(dst + L::kQ + L::kK + b * kBlk, &tmV, fb, h * a.dv + d0 + 64 * b, y, pol);
+  };
+  constexpr int kFirst = kStg - 2;  // chunks whose copies start before the CTA is set up
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStg; ++s) {
       mbar_init(full0 + 8 * s, 1);
@@ -594,6 +610,26 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     }
     ctl.abort_flag = 0;
     fence_mbar_init();
+    for (int c = 0; c < nc && c < kFirst; ++c) load(c);
+  }
+  // the state's warps fetch its rows meanwhile
+  const int half = (warp - 8) >> 2;
+  const long long srow =
+      ((static_cast<long long>(g.seq) * a.Hv + h) * a.dv + d0 + wq * 32) * kDk + half * kHalfDk;
+  const uint32_t srows = stages + kFirst * L::kStage + (warp - 8) * 32 * kHalfDk * 4;
+  float S[kHalfDk];
+  if (warp >= 8) {
+    if (kOut) {
+      const float *src = nullptr;
+      if (g.index == 0)
+        src = a.s_in ? a.s_in + srow : nullptr;
+      else if (g.slot < a.slots)
+        src = a.ws + ((g.slot * a.Hv + h) * a.dv + d0 + wq * 32) * kDk + half * kHalfDk;
+      load_rows<kHalfDk>(S, srows, src, kDk, a.dv - d0 - wq * 32);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kHalfDk; ++i) S[i] = 0.0f;
+    }
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&ctl.tmem), kTmemAll);
@@ -604,33 +640,20 @@ __global__ void __launch_bounds__(kThreadsC, 1)
   tc_fence_after();
   const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
   const int tail = static_cast<int>(g.len - static_cast<long long>(nc - 1) * kC);  // tokens of the last chunk
-  const uint32_t stages = smem_u32(smem);
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      const uint64_t pol = policy_evict_last();
-      const int hk = h / (a.Hv / a.Hk);
-      int c = 0;
+      int c = min(nc, kFirst);
       for (; c < nc; ++c) {
         const int s = c % kStg;
-        if (!poll(empty0 + 8 * s, ((c / kStg) & 1) ^ 1, abort_flag)) {
+        if (!poll(empty0 + 8 * s, ((c / kStg) & 1) ^ 1, abort_flag) ||
+            // the last two stages hold the initial state's rows at first
+            (kOut && c == kFirst && !poll(s_ready, 0, abort_flag))) {
           fail(a, abort_flag, SITE_PRODUCER_EMPTY);
           break;
         }
-        if (kOut && c == kStg - 2 && !poll(s_ready, 0, abort_flag)) {  // (the state's rows lie there)
-          fail(a, abort_flag, SITE_PRODUCER_EMPTY);
-          break;
-        }
-        const uint32_t dst = stages + s * L::kStage, fb = full0 + 8 * s;
-        const int y = static_cast<int>(g.first) + c * kC;
-        mbar_arrive_expect_tx(fb, L::kStage);
-        for (int b = 0; b < kDk / 64; ++b) {
-          tma_load_2d(dst + L::kQ + b * kBlk, &tmK, fb, hk * kDk + 64 * b, y, pol);
-          if (kOut) tma_load_2d(dst + b * kBlk, &tmQ, fb, hk * kDk + 64 * b, y, pol);
-        }
-        for (int b = 0; b < 2; ++b)
-          tma_load_2d(dst + L::kQ + L::kK + b * kBlk, &tmV, fb, h * a.dv + d0 + 64 * b, y, pol);
+        load(c);
       }
       if (*abort_flag)
         for (int i = max(0, c - kStg); i < c; ++i)
@@ -805,26 +828,6 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------ state, outputs
-    const int half = (warp - 8) >> 2;
-    const long long srow =
-        ((static_cast<long long>(g.seq) * a.Hv + h) * a.dv + d0 + wq * 32) * kDk + half * kHalfDk;
-    float S[kHalfDk];
-    // this warp's 32 rows, this half of d_k
-    const float *src = nullptr;
-    if (kOut) {
-      if (g.index == 0)
-        src = a.s_in ? a.s_in + srow : nullptr;
-      else if (g.slot < a.slots)
-        src = a.ws + ((g.slot * a.Hv + h) * a.dv + d0 + wq * 32) * kDk + half * kHalfDk;
-    }
-    // (the last two stages are not loaded before the state is in TMEM)
-    const uint32_t srows = stages + (kStg - 2) * L::kStage + (warp - 8) * 32 * kHalfDk * 4;
-    if (kOut) {
-      load_rows<kHalfDk>(S, srows, src, kDk, a.dv - d0 - wq * 32);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kHalfDk; ++i) S[i] = 0.0f;
-    }
     // outputs: weights lambda^(i + 1) of this lane's tokens, its places in the
     // warp's tile (rows of 64 bytes, pieces of 16 swizzled over pairs of rows)
     float ow[4][2];
@@ -854,9 +857,9 @@ __global__ void __launch_bounds__(kThreadsC, 1)
       tmem_wait_st();
     };
     if (kOut) {
+      warp_arrive(vt_full0);
       put_state();
       warp_arrive(s_ready);
-      warp_arrive(vt_full0);
     }
     bool ok = true;
     for (int c = 0; c < nc; ++c) {
