@@ -123,9 +123,12 @@ struct Plan {
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
 // Chunks per segment, by the time of the kernels in units of one chunk of the
-// main kernel: a CTA takes its segment's chunks and about two more to start
-// and end; with more than one segment per sequence the segment kernel (0.45
-// per chunk) and the chain come first.
+// main kernel (1.4 us): a CTA takes its segment's chunks and 3.2 more to start
+// and end; with more than one segment per sequence the first launch (0.42 per
+// chunk and 2) and the chain (2.5, and its traffic) come before.  With offsets
+// the lengths are not known here: a segment is as long as for one sequence of
+// all tokens, and at least twice the average sequence, so that few sequences
+// of a batch are cut.
 Plan make_plan(bool ragged, long long n_tokens, long long n_seq, long long heads) {
   Plan p = {};
   const long long len = ragged ? n_tokens : n_seq ? n_tokens / n_seq : 0;
@@ -134,16 +137,16 @@ Plan make_plan(bool ragged, long long n_tokens, long long n_seq, long long heads
   p.recurrent = ragged || !p.chunked;
   if (!p.chunked) return p;
   const long long chunks = ceil_div(len, kChunkTok);
-  const long long extra = ragged ? (n_seq - 1) / 2 : 0;  // part-filled segments
+  const long long least = ragged ? ceil_div(2 * n_tokens, n_seq * kChunkTok) : 4;
   double best = 0;
   for (long long n = 1; n <= 256 && n <= chunks; ++n) {
     const long long lc = ceil_div(chunks, n);
-    if (n > 1 && lc < 4) break;
+    if (n > 1 && lc < least) break;
     const long long ns = ceil_div(chunks, lc);
-    double t = static_cast<double>(ceil_div((ns * seqs + extra) * heads, kGpuSms)) * (lc + 2);
+    double t = static_cast<double>(ceil_div(ns * seqs * heads, kGpuSms)) * (lc + 3.2);
     if (ns > 1)
-      t += static_cast<double>(ceil_div((ns - 1) * seqs * heads, kGpuSms)) * (0.45 * lc + 2) + 3 +
-           0.002 * ns * seqs * heads;
+      t += static_cast<double>(ceil_div((ns - 1) * seqs * heads, kGpuSms)) * (0.42 * lc + 2) + 2.5 +
+           0.01 * (ns - 1) * seqs * heads;
     if (n == 1 || t < best) {
       best = t;
       p.seg_len = lc * kChunkTok;

@@ -34,7 +34,8 @@
 // to fill the GPU; otherwise it is cut: a first launch of the same kernel
 // without the outputs computes what each segment leaves, a small kernel
 // chains these into the state before each segment, and the main launch runs
-// all segments at once.
+// all segments at once.  Each lets the next one start its CTAs early (they wait
+// for its results).
 //
 // Roles (512 threads): warp 0 TMA producer; warp 1 issues every MMA, per chunk
 // S Q^T, V^T P^T, the next chunk's scores and its U; warps 4-7 P and V~; warps
@@ -57,7 +58,9 @@ namespace {
 
 constexpr int kC = kChunkTok;
 constexpr int kBlk = kC * 128;  // a 64-token tile of 128 bytes (64 bf16) per token: 8 KB
-constexpr int kThreadsC = 512;
+// threads: four warps for copies and MMAs, one warpgroup for V~ and P (two for
+// V~ where there are no outputs), two for the state
+constexpr int kThreadsC(bool out) { return out ? 512 : 640; }
 constexpr int kStg = 4;    // TMA stages
 constexpr int kTerms = 4;  // bf16 parts of V~
 constexpr uint32_t kTmemAll = 512;
@@ -497,36 +500,41 @@ static_assert(sizeof(Ctl) <= 2048, "control block");
 }  // namespace
 
 // ws: what each segment leaves -> the state before the next segment, in place,
-// along each sequence.  One thread per 4 elements of a (sequence, head) state.
+// along each sequence.  One thread per 4 elements of a (sequence, head) state;
+// without offsets a block's sequence is known, with them block row y looks at
+// item y and works if that is the first segment of several.
 __global__ void __launch_bounds__(256) decay_chain_kernel(const DecayArgs a, int dk) {
   __shared__ int scratch[36];
-  const long long per = static_cast<long long>(a.dv) * dk / 4;  // vectors of a state
-  const int blocks = static_cast<int>((per + 255) / 256);
-  const int hb = static_cast<int>(blockIdx.x % (a.Hv * blocks));
-  const int h = hb / blocks;
-  const long long e = static_cast<long long>(hb % blocks) * 256 + threadIdx.x;
+  const int per = a.dv * dk / 4;  // vectors of a state
+  const int blocks = (per + 255) / 256;
+  const int hb = static_cast<int>(blockIdx.x) % (a.Hv * blocks), y = static_cast<int>(blockIdx.x) / (a.Hv * blocks);
+  const int h = hb / blocks, e = hb % blocks * 256 + threadIdx.x;
   pdl_wait();
-  // the item list is walked sequence by sequence: block y starts at the y-th
-  // sequence of more than one segment by looking for its first segment
-  long long item = blockIdx.x / (a.Hv * blocks);
-  const Segment g = find_segment(a, item, scratch);
-  if (g.seq < 0 || g.index != 0 || g.last) return;
-  long long first, len;
-  seq_range(a, g.seq, first, len);
-  const long long n = (static_cast<int>(len) + a.seg_len - 1) / a.seg_len - 1;  // slots of the sequence
-  if (e >= per || g.slot + 1 + n > a.slots) return;
+  pdl_launch_dependents();
+  int seq = y, n = (a.seq_len + a.seg_len - 1) / a.seg_len - 1;  // slots of the sequence
+  long long slot = static_cast<long long>(n) * y;                // its first one
+  if (a.offsets) {
+    const Segment g = find_segment(a, y, scratch);
+    if (g.seq < 0 || g.index != 0 || g.last) return;
+    long long first, len;
+    seq_range(a, g.seq, first, len);
+    seq = g.seq;
+    n = (static_cast<int>(len) + a.seg_len - 1) / a.seg_len - 1;
+    slot = g.slot + 1;
+  }
+  if (e >= per || slot + n > a.slots) return;
   const float f = decay_pow(a.decay[h], static_cast<float>(a.seg_len));
   const long long step = static_cast<long long>(a.Hv) * per;
-  float4 *w = reinterpret_cast<float4 *>(a.ws) + ((g.slot + 1) * a.Hv + h) * per + e;
+  float4 *w = reinterpret_cast<float4 *>(a.ws) + (slot * a.Hv + h) * per + e;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (a.s_in) s = reinterpret_cast<const float4 *>(a.s_in)[(static_cast<long long>(g.seq) * a.Hv + h) * per + e];
-  for (long long i0 = 0; i0 < n; i0 += 4) {
-    float4 u[4];
+  if (a.s_in) s = reinterpret_cast<const float4 *>(a.s_in)[(static_cast<long long>(seq) * a.Hv + h) * per + e];
+  for (int i0 = 0; i0 < n; i0 += 8) {
+    float4 u[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i)
       if (i0 + i < n) u[i] = w[(i0 + i) * step];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 8; ++i)
       if (i0 + i < n) {
         s.x = fmaf(f, s.x, u[i].x);
         s.y = fmaf(f, s.y, u[i].y);
@@ -542,13 +550,14 @@ __global__ void __launch_bounds__(256) decay_chain_kernel(const DecayArgs a, int
 // what the segment leaves from a zero state, into slot g.slot + 1, unless it
 // is the last.
 template <int kDk, bool kOut>
-__global__ void __launch_bounds__(kThreadsC, 1)
+__global__ void __launch_bounds__(kThreadsC(kOut), 1)
     decay_chunk_kernel(const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const DecayArgs a) {
   using L = Smem<kDk, kOut>;
   using M = Cols<kDk, kOut>;
   constexpr int kHalfDk = kDk / 2;
+  constexpr int kState = kOut ? 8 : 12;  // the state's first warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = align1024(smem_raw);
   Ctl &ctl = *reinterpret_cast<Ctl *>(smem + L::kCtl);
@@ -562,6 +571,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
   const int ht = static_cast<int>(blockIdx.x % (a.Hv * a.tiles));
   const int h = ht / a.tiles, d0 = ht % a.tiles * 128;
   pdl_wait();
+  pdl_launch_dependents();
   const Segment g = find_segment(a, blockIdx.x / (a.Hv * a.tiles), ctl.scratch);
   if (g.seq < 0 || (!kOut && (g.last || g.slot + 1 >= a.slots))) return;
   const int nc = static_cast<int>((g.len + kC - 1) / kC);
@@ -613,12 +623,12 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     for (int c = 0; c < nc && c < kFirst; ++c) load(c);
   }
   // the state's warps fetch its rows meanwhile
-  const int half = (warp - 8) >> 2;
+  const int half = (warp - kState) >> 2;
   const long long srow =
       ((static_cast<long long>(g.seq) * a.Hv + h) * a.dv + d0 + wq * 32) * kDk + half * kHalfDk;
-  const uint32_t srows = stages + kFirst * L::kStage + (warp - 8) * 32 * kHalfDk * 4;
+  const uint32_t srows = stages + kFirst * L::kStage + (warp - kState) * 32 * kHalfDk * 4;
   float S[kHalfDk];
-  if (warp >= 8) {
+  if (warp >= kState) {
     if (kOut) {
       const float *src = nullptr;
       if (g.index == 0)
@@ -749,7 +759,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
       }
     }
     if (one) tc_commit(drain);
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp >= 4 && warp < kState) {
     // ------------------------------------------------------------ V~, P
     // P: rows 16 wq + lane / 4, + 8; columns 8 n + 2 (lane % 4), + 1.  Past
     // column 16 wq + 15 these rows have nothing: zeros, written once.
@@ -766,7 +776,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
     }
     VtWeight w[8];
     vt_weights(ctl.tab, kC, w);
-    for (int c = 0; c < nc; ++c) {
+    for (int c = (warp - 4) >> 2; c < nc; c += M::kBufs) {  // (one warpgroup per buffer)
       const int s = c % kStg, vb = c % M::kBufs;
       const uint32_t st = stages + s * L::kStage;
       // the products that last used this buffer of V~ are done: with outputs
@@ -826,7 +836,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
         warp_arrive(p_full);
       }
     }
-  } else if (warp >= 8) {
+  } else if (warp >= kState) {
     // ------------------------------------------------------------ state, outputs
     // outputs: weights lambda^(i + 1) of this lane's tokens, its places in the
     // warp's tile (rows of 64 bytes, pieces of 16 swizzled over pairs of rows)
@@ -838,7 +848,7 @@ __global__ void __launch_bounds__(kThreadsC, 1)
       ow[i][1] = ctl.tab[t + 2];
     }
     const int mm = lane >> 3;
-    const uint32_t tile = smem_u32(smem) + L::kO + (warp - 8) * 2048;
+    const uint32_t tile = smem_u32(smem) + L::kO + (warp - kState) * 2048;
     const uint32_t otile = tile + (8 * (mm >> 1) + (lane & 7)) * 64;
     const uint32_t oread = tile + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
     const bool ovalid = d0 + wq * 32 + 8 * (lane & 3) < a.dv;
@@ -870,11 +880,11 @@ __global__ void __launch_bounds__(kThreadsC, 1)
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
-      for (int x = 0; x < kHalfDk; x += 32) {
-        float u[32];
-        tmem_ld32_sync(M::U + ub * kDk + half * kHalfDk + x + lanes, u);
+      for (int x = 0; x < kHalfDk; x += 16) {
+        float u[16];
+        tmem_ld16_sync(M::U + ub * kDk + half * kHalfDk + x + lanes, u);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) S[x + i] = fmaf(f, S[x + i], u[i]);
+        for (int i = 0; i < 16; ++i) S[x + i] = fmaf(f, S[x + i], u[i]);
       }
       if (!kOut) warp_arrive(u_empty0 + 8 * ub);
       if (kOut) {
@@ -957,14 +967,14 @@ cudaError_t launch_chunked(const DecayArgs &a, const CUtensorMap &mq, const CUte
                            const CUtensorMap &mv, bool segmented, cudaStream_t st) {
   const long long per = static_cast<long long>(a.Hv) * a.tiles;
   if (segmented) {
-    cudaError_t e = launch_pdl(decay_chunk_kernel<kDk, false>, a.items * per, kThreadsC,
+    cudaError_t e = launch_pdl(decay_chunk_kernel<kDk, false>, a.items * per, kThreadsC(false),
                                Smem<kDk, false>::kTotal, st, mq, mk, mv, a);
     if (e != cudaSuccess) return e;
     const long long blocks = (static_cast<long long>(a.dv) * kDk / 4 + 255) / 256;
-    e = launch_pdl(decay_chain_kernel, a.items * a.Hv * blocks, 256, 0, st, a, kDk);
+    e = launch_pdl(decay_chain_kernel, (a.offsets ? a.items : a.n_seq) * a.Hv * blocks, 256, 0, st, a, kDk);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(decay_chunk_kernel<kDk, true>, a.items * per, kThreadsC, Smem<kDk, true>::kTotal,
+  return launch_pdl(decay_chunk_kernel<kDk, true>, a.items * per, kThreadsC(true), Smem<kDk, true>::kTotal,
                     st, mq, mk, mv, a);
 }
 
