@@ -611,10 +611,10 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
     mbar_init(s_ready, 8);  // the chunk's S is in TMEM, the last chunk's O1, O2 are read
     mbar_init(o_full, 1);
     mbar_init(drain, 1);
+    for (int b = 0; b < 4; ++b) mbar_init(vt_part0 + 8 * b, 1);
     for (int b = 0; b < 2; ++b) {
       // (with outputs, also the last U read: U has one buffer then)
       mbar_init(vt_full0 + 8 * b, kOut ? 4 + 8 : 4);
-      mbar_init(vt_part0 + 8 * b, 1);
       mbar_init(u_full0 + 8 * b, 1);
       mbar_init(u_empty0 + 8 * b, 8);
     }
@@ -681,28 +681,23 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
     const uint64_t dp = sdesc_sw128(smem_u32(smem) + L::kP);
     const uint64_t dkm0 = sdesc_mn(stages + L::kQ, kBlk), dvm0 = sdesc_mn(stages + L::kQ + L::kK, kBlk);
     const uint64_t dk0 = sdesc_sw128(stages + L::kQ), dq0 = sdesc_sw128(stages);
-    // U of chunk c, staged at `at` (descriptor units)
+    // (one lane) U of chunk c, staged at `at` (descriptor units): the small parts
+    // of each half of the tokens, then the leading ones.  Few sums are truncated
+    // at the size of the result, and V~ of the next chunk can follow part by
+    // part.
     auto update = [&](int c, uint32_t at) {
       const int ub = c % M::kBufs;
-      if (!warp_wait(a, vt_full0 + 8 * ub, (c / M::kBufs) & 1, abort_flag, SITE_STAGE)) return false;
-      tc_fence_after();
-      if (one) {
-        // the small parts of each half of the tokens, then the leading ones:
-        // few sums are truncated at the size of the result, and V~ of the next
-        // chunk can follow part by part
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < 2; ++b) {
 #pragma unroll
-          for (int t = kTerms - 1; t > 0; --t)
-            mma_update<kDk>(M::U + ub * kDk, M::V + ub * kTerms * 32, dkm0 + at, t, 2 * b,
-                            b > 0 || t < kTerms - 1);
-          if (kOut) tc_commit(vt_part0 + 8 * b);
-        }
-        mma_update<kDk>(M::U + ub * kDk, M::V + ub * kTerms * 32, dkm0 + at, 0, 0, true);
-        mma_update<kDk>(M::U + ub * kDk, M::V + ub * kTerms * 32, dkm0 + at, 0, 2, true);
-        tc_commit(u_full0 + 8 * ub);
+        for (int t = kTerms - 1; t > 0; --t)
+          mma_update<kDk>(M::U + ub * kDk, M::V + ub * kTerms * 32, dkm0 + at, t, 2 * b,
+                          b > 0 || t < kTerms - 1);
+        tc_commit(vt_part0 + 8 * (2 * ub + b));
       }
-      return true;
+      mma_update<kDk>(M::U + ub * kDk, M::V + ub * kTerms * 32, dkm0 + at, 0, 0, true);
+      mma_update<kDk>(M::U + ub * kDk, M::V + ub * kTerms * 32, dkm0 + at, 0, 2, true);
+      tc_commit(u_full0 + 8 * ub);
     };
     if (kOut) {
       uint32_t s = 0;  // stage of chunk c
@@ -742,7 +737,9 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
             }
             tc_commit(sc_full);
           }
-          if (!update(c + 1, at)) break;
+          if (!warp_wait(a, vt_full0, (c + 1) & 1, abort_flag, SITE_STAGE)) break;
+          tc_fence_after();
+          if (one) update(c + 1, at);
         }
         s = next;
       }
@@ -750,11 +747,14 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
       uint32_t s = 0;
       for (int c = 0; c < nc; ++c) {
         const uint32_t at = s * (L::kStage >> 4);
-        if (!warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL) ||
-            !warp_wait(a, u_empty0 + 8 * (c & 1), ((c >> 1) & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY) ||
-            !update(c, at))
+        if (!warp_wait(a, u_empty0 + 8 * (c & 1), ((c >> 1) & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY) ||
+            !warp_wait(a, vt_full0 + 8 * (c & 1), (c >> 1) & 1, abort_flag, SITE_STAGE))
           break;
-        if (one) tc_commit(empty0 + 8 * s);
+        tc_fence_after();
+        if (one) {
+          update(c, at);
+          tc_commit(empty0 + 8 * s);
+        }
         s = s + 1 == kStg ? 0 : s + 1;
       }
     }
@@ -779,11 +779,10 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
     for (int c = (warp - 4) >> 2; c < nc; c += M::kBufs) {  // (one warpgroup per buffer)
       const int s = c % kStg, vb = c % M::kBufs;
       const uint32_t st = stages + s * L::kStage;
-      // the products that last used this buffer of V~ are done: with outputs
-      // (one buffer) part by part, below
+      // the products that last used this buffer of V~ end part by part
       const uint32_t before = ((c / M::kBufs) & 1) ^ 1;
       if (!warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL) ||
-          !warp_wait(a, kOut ? vt_part0 : u_full0 + 8 * vb, before, abort_flag, SITE_MMA_TMEM_EMPTY))
+          !warp_wait(a, vt_part0 + 16 * vb, before, abort_flag, SITE_MMA_TMEM_EMPTY))
         break;
       tc_fence_after();
       if (c == nc - 1 && tail < kC) {
@@ -793,15 +792,11 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
       const uint32_t v = st + L::kQ + L::kK, ta = M::V + vb * kTerms * 32 + lanes;
       uint32_t lead[2][2][8];
       make_vt<0>(v, wq, w, ta, lead[0]);
-      if (kOut) {
-        if (!warp_wait(a, vt_part0 + 8, before, abort_flag, SITE_MMA_TMEM_EMPTY)) break;
-        tc_fence_after();
-      }
+      if (!warp_wait(a, vt_part0 + 16 * vb + 8, before, abort_flag, SITE_MMA_TMEM_EMPTY)) break;
+      tc_fence_after();
       make_vt<1>(v + 32 * 128, wq, w, ta + 16, lead[1]);
-      if (kOut) {
-        if (!warp_wait(a, u_full0, before, abort_flag, SITE_MMA_TMEM_EMPTY)) break;
-        tc_fence_after();
-      }
+      if (!warp_wait(a, u_full0 + 8 * vb, before, abort_flag, SITE_MMA_TMEM_EMPTY)) break;
+      tc_fence_after();
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
