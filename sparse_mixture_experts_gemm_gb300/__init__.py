@@ -427,231 +427,15 @@ def gdn_scan(q, k, v, alpha, beta, state=None, out=None, state_out=None, stream=
     return out, state_out
 
 
-
 # ---------------------------------------------------- the mixer's operators
-def _on(stream):
-    """Context in which results and workspaces are allocated for `stream`, so
-    that the caching allocator hands their memory on in that stream's order."""
-    import contextlib
-    import torch
-    if stream is None:
-        return contextlib.nullcontext()
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
-    return torch.cuda.stream(stream)
+_MIXER = ("add_rmsnorm", "add_rmsnorm_fp8", "quantize_fp8", "matmul_fp8", "gdn_decay_scan")
 
 
-def _rows(name, t, dtype=None):
-    """(rows, width, row stride in elements) of a CUDA tensor whose last
-    dimension is contiguous and whose leading ones are evenly spaced rows."""
-    if not t.is_cuda or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name} must be a CUDA {dtype or ''} tensor")
-    if t.dim() == 0:
-        raise ValueError(f"{name} must have at least one dimension")
-    shape, strides = t.shape, t.stride()
-    d = shape[-1]
-    rows = t.numel() // d if d else 0
-    if t.is_contiguous():
-        return rows, d, d
-    if strides[-1] != 1 and d > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    step, stride = None, d
-    for n, s in zip(reversed(shape[:-1]), reversed(strides[:-1])):
-        if n == 1:
-            continue
-        if step is None:
-            step, stride = s, s
-        elif s != step:
-            raise ValueError(f"{name}: rows must be evenly spaced")
-        step *= n
-    return rows, d, max(stride, d) if rows <= 1 else stride
-
-
-def _moe_dtype(name, t):
-    import torch
-    if t.dtype == torch.bfloat16:
-        return MOE_BF16
-    if t.dtype == torch.float32:
-        return MOE_F32
-    raise ValueError(f"{name} must be bfloat16 or float32")
-
-
-def _given(name, t, shape, dtype):
-    """A caller's output tensor: of this shape and type, contiguous, on the GPU."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}")
-    return t
-
-
-def _norm_args(x, weight, residual):
-    dt = _moe_dtype("x", x)
-    rows, d, xs = _rows("x", x)
-    rs = d
-    if weight.dtype != x.dtype or weight.shape != (d,) or not weight.is_contiguous() \
-            or not weight.is_cuda:
-        raise ValueError("weight must be a contiguous CUDA tensor [d] of x's type")
-    if residual is not None:
-        if residual.shape != x.shape:
-            raise ValueError("residual must have x's shape")
-        _, _, rs = _rows("residual", residual, x.dtype)
-    return dt, rows, d, xs, rs
-
-
-def add_rmsnorm(x, weight, residual=None, eps=1e-6, out=None, sum_out=None, stream=None):
-    """moe_add_rmsnorm over the last dimension of x (bf16 or float32): returns
-    (out, sum) with sum = x + residual, None without a residual unless sum_out
-    is given.  Rows may be strided (a slice of a wider tensor)."""
-    import torch
-    dt, rows, d, xs, rs = _norm_args(x, weight, residual)
-    with _on(stream):
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None \
-            else _given("out", out, x.shape, x.dtype)
-        if sum_out is not None:
-            _given("sum_out", sum_out, x.shape, x.dtype)
-        elif residual is not None:
-            sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _check(lib().moe_add_rmsnorm(x.data_ptr(), _ptr(residual), weight.data_ptr(), dt, rows, d, xs,
-                                 rs, eps, _ptr(sum_out), out.data_ptr(), _stream(stream)),
-           "moe_add_rmsnorm")
-    return out, sum_out
-
-
-def add_rmsnorm_fp8(x, weight, residual=None, eps=1e-6, codes=None, scales=None, sum_out=None,
-                    stream=None):
-    """moe_add_rmsnorm_fp8 over the last dimension of x: returns (codes
-    float8_e4m3fn of x's shape, scales float32 of its leading shape, sum as in
-    add_rmsnorm)."""
-    import torch
-    dt, rows, d, xs, rs = _norm_args(x, weight, residual)
-    with _on(stream):
-        codes = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device) if codes is None \
-            else _given("codes", codes, x.shape, torch.float8_e4m3fn)
-        scales = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) if scales is None \
-            else _given("scales", scales, x.shape[:-1], torch.float32)
-        if sum_out is not None:
-            _given("sum_out", sum_out, x.shape, x.dtype)
-        elif residual is not None:
-            sum_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _check(lib().moe_add_rmsnorm_fp8(x.data_ptr(), _ptr(residual), weight.data_ptr(), dt, rows, d,
-                                     xs, rs, eps, _ptr(sum_out), codes.data_ptr(),
-                                     scales.data_ptr(), _stream(stream)), "moe_add_rmsnorm_fp8")
-    return codes, scales, sum_out
-
-
-def quantize_fp8(w, codes=None, scales=None, stream=None):
-    """moe_quantize_fp8 of the rows of w (bf16 or float32): (codes
-    float8_e4m3fn, scales float32)."""
-    import torch
-    dt = _moe_dtype("w", w)
-    rows, d, stride = _rows("w", w)
-    with _on(stream):
-        codes = torch.empty(w.shape, dtype=torch.float8_e4m3fn, device=w.device) if codes is None \
-            else _given("codes", codes, w.shape, torch.float8_e4m3fn)
-        scales = torch.empty(w.shape[:-1], dtype=torch.float32, device=w.device) if scales is None \
-            else _given("scales", scales, w.shape[:-1], torch.float32)
-    _check(lib().moe_quantize_fp8(w.data_ptr(), dt, rows, d, stride, codes.data_ptr(),
-                                  scales.data_ptr(), _stream(stream)), "moe_quantize_fp8")
-    return codes, scales
-
-
-def matmul_fp8(x, x_scales, w, w_scales, out=None, stream=None):
-    """moe_matmul_fp8: x float8_e4m3fn [..., K] with scales float32 [...], w
-    float8_e4m3fn [N, K] with scales float32 [N] -> bf16 [..., N].  Rows of x,
-    w and a given 2-D out may be strided."""
-    import torch
-    f8, f32 = torch.float8_e4m3fn, torch.float32
-    T, K, xs = _rows("x", x, f8)
-    N, Kw, ws = _rows("w", w, f8)
-    if w.dim() != 2 or Kw != K:
-        raise ValueError("w must be [N][K] with x's K")
-    lead = x.shape[:-1]
-    if x_scales.dtype != f32 or x_scales.shape != lead or not x_scales.is_contiguous() \
-            or not x_scales.is_cuda:
-        raise ValueError("x_scales must be a contiguous CUDA float32 tensor of x's leading shape")
-    if w_scales.dtype != f32 or w_scales.shape != (N,) or not w_scales.is_contiguous() \
-            or not w_scales.is_cuda:
-        raise ValueError("w_scales must be a contiguous CUDA float32 tensor [N]")
-    os_ = N
-    if out is None:
-        with _on(stream):
-            out = torch.empty((*lead, N), dtype=torch.bfloat16, device=x.device)
-    else:
-        if out.shape != (*lead, N):
-            raise ValueError("out must have x's leading shape and N columns")
-        _, _, os_ = _rows("out", out, torch.bfloat16)
-    _check(lib().moe_matmul_fp8(x.data_ptr(), x_scales.data_ptr(), T, xs, w.data_ptr(),
-                                w_scales.data_ptr(), N, K, ws, out.data_ptr(), os_,
-                                _stream(stream)), "moe_matmul_fp8")
-    return out
-
-
-def _tokens(name, t):
-    """Token stride of bf16 [..., heads, width], tokens evenly spaced."""
-    import torch
-    if t.dtype != torch.bfloat16 or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA bfloat16 tensor")
-    H, w = t.shape[-2:]
-    if t.is_contiguous():
-        return H * w
-    if (w > 1 and t.stride(-1) != 1) or (H > 1 and t.stride(-2) != w):
-        raise ValueError(f"{name}: heads and their width must be contiguous")
-    step = t.stride(-3)
-    if t.dim() == 4 and t.shape[0] > 1:
-        if t.shape[1] == 1:
-            step = t.stride(0)
-        elif t.stride(0) != t.shape[1] * step:
-            raise ValueError(f"{name}: tokens must be evenly spaced")
-    return max(step, H * w) if t.numel() <= H * w else step
-
-
-def gdn_decay_scan(q, k, v, decay, state=None, offsets=None, out=None, state_out=None,
-                   stream=None):
-    """Linear attention with a decay per value head (include/gdn.h).
-
-    q, k: bf16 [n][T][H_k][d_k], v: bf16 [n][T][H_v][d_v] for n sequences of T
-    tokens; or [N][H][d] for one sequence, or, with offsets (int32 [n + 1] on
-    the GPU), for n packed ones.  Tokens may be strided (slices of a fused
-    projection).  decay: float32 [H_v].  state: float32 [n][H_v][d_v][d_k]
-    ([H_v][d_v][d_k] for one sequence of [N][H][d] tokens) or None (zeros).
-    Returns (o bf16 of v's shape, final state); state_out may be `state`.
-    """
-    import torch
-    f32 = torch.float32
-    sq, sv = q.shape, v.shape
-    if len(sq) not in (3, 4) or sq != k.shape or len(sv) != len(sq) or sv[:-2] != sq[:-2]:
-        raise ValueError("shapes of q, k, v do not agree")
-    Hk, dk = sq[-2:]
-    Hv, dv = sv[-2:]
-    if decay.dtype != f32 or decay.shape != (Hv,) or not decay.is_contiguous() \
-            or not decay.is_cuda:
-        raise ValueError("decay must be a contiguous CUDA float32 tensor [H_v]")
-    if len(sq) == 4:
-        if offsets is not None:
-            raise ValueError("offsets go with packed tokens [N][H][d]")
-        n, N = sq[0], sq[0] * sq[1]
-        s_shape = (n, Hv, dv, dk)
-    else:
-        n, N, s_shape = 1, sq[0], (Hv, dv, dk)
-        if offsets is not None:
-            if offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_contiguous() \
-                    or not offsets.is_cuda or offsets.shape[0] < 1:
-                raise ValueError("offsets must be a contiguous CUDA int32 tensor [n + 1]")
-            n = offsets.shape[0] - 1
-            s_shape = (n, Hv, dv, dk)
-    qs, ks, vs = _tokens("q", q), _tokens("k", k), _tokens("v", v)
-    if state is not None:
-        _given("state", state, s_shape, f32)
-    L = lib()
-    need = ctypes.c_size_t(0)
-    _check(L.gdn_decay_workspace(N, n, offsets is not None, Hv, dk, dv, ctypes.byref(need)), "gdn_decay_workspace")
-    with _on(stream):
-        out = torch.empty(sv, dtype=torch.bfloat16, device=v.device) if out is None \
-            else _given("out", out, sv, torch.bfloat16)
-        state_out = torch.empty(s_shape, dtype=f32, device=v.device) if state_out is None \
-            else _given("state_out", state_out, s_shape, f32)
-        ws = torch.empty(need.value, dtype=torch.uint8, device=v.device) if need.value else None
-    _check(L.gdn_decay_scan(q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(),
-                            _ptr(state), state_out.data_ptr(), out.data_ptr(), _ptr(offsets), N,
-                            n, Hk, Hv, dk, dv, qs, ks, vs, _ptr(ws), need.value, _stream(stream)),
-           "gdn_decay_scan")
-    return out, state_out
+def __getattr__(name):
+    """The functions of mixer.py, loaded (with torch) when first used."""
+    if name in _MIXER:
+        from . import mixer
+        for n in _MIXER:
+            globals()[n] = getattr(mixer, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
