@@ -12,13 +12,18 @@
 // bit patterns of |s w| as integers, where a NaN is larger than every number:
 // a row that holds a NaN or an infinity gets NaN codes and a NaN scale.
 //
-// Bound by memory: 7 bytes per element with a bf16 residual and codes.
+// Bound by memory: 7 bytes per element with a bf16 residual and codes.  A block
+// holds one row.  Rows of whole 16-byte vectors move as such; rows of another
+// width one element per lane and load, neighbouring lanes on neighbouring
+// elements (16,384 rows of 1,001: 29 us; cutting such rows into vectors with
+// ragged ends took 32, because the weights lie differently in every row).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include "../../include/moe.h"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace moe {
 
@@ -34,39 +39,72 @@ struct NormArgs {
   long long rows, x_stride, r_stride;  // strides in elements
   int d;
   float eps;
-  bool wide;  // every row of every tensor starts on a 16-byte boundary (codes: 8)
+  bool wide;  // every row of every tensor starts on a 16-byte boundary (codes: 8 or 4)
 };
 
-template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T *p, float (&v)[V], bool wide) {
+// A thread's vectors of a row: columns c0 + p step .. + V - 1, p < kPer.
+template <typename T, int V, int kPer>
+__device__ __forceinline__ void load_row(const T *row, int c0, int step, int d, bool wide,
+                                         float (&v)[kPer][V]) {
   if constexpr (V == 1) {
-    v[0] = static_cast<float>(*p);
-  } else {
-    alignas(16) T t[V];
-    if (wide) {
-      *reinterpret_cast<uint4 *>(t) = *reinterpret_cast<const uint4 *>(p);
-    } else {
 #pragma unroll
-      for (int e = 0; e < V; ++e) t[e] = p[e];
+    for (int p = 0; p < kPer; ++p) {
+      const int c = c0 + p * step;
+      v[p][0] = c < d ? static_cast<float>(row[c]) : 0.0f;
+    }
+  } else if (wide) {
+    uint4 u[kPer];
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) {
+      u[p] = make_uint4(0, 0, 0, 0);
+      if (c0 + p * step < d) u[p] = *reinterpret_cast<const uint4 *>(row + c0 + p * step);
     }
 #pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = static_cast<float>(t[e]);
+    for (int p = 0; p < kPer; ++p) {
+      const uint32_t w[4] = {u[p].x, u[p].y, u[p].z, u[p].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (V == 8) {
+          v[p][2 * i] = __uint_as_float(w[i] << 16);
+          v[p][2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        } else {
+          v[p][i] = __uint_as_float(w[i]);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int p = 0; p < kPer; ++p)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const int c = c0 + p * step;
+        v[p][e] = c < d ? static_cast<float>(row[c + e]) : 0.0f;
+      }
   }
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void store_vec(T *p, const float (&v)[V], bool wide) {
-  if constexpr (V == 1) {
-    *p = static_cast<T>(v[0]);
-  } else {
-    alignas(16) T t[V];
+template <typename T, int V, int kPer>
+__device__ __forceinline__ void store_row(T *row, int c0, int step, int d, bool wide,
+                                          const float (&v)[kPer][V]) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) t[e] = static_cast<T>(v[e]);
-    if (wide) {
-      *reinterpret_cast<uint4 *>(p) = *reinterpret_cast<const uint4 *>(t);
+  for (int p = 0; p < kPer; ++p) {
+    const int c = c0 + p * step;
+    if (c >= d) continue;
+    if (V == 1 || !wide) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) row[c + e] = static_cast<T>(v[p][e]);
     } else {
+      uint32_t w[4];
 #pragma unroll
-      for (int e = 0; e < V; ++e) p[e] = t[e];
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (V == 8) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[p][2 * i], v[p][2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        } else {
+          w[i] = __float_as_uint(v[p][i]);
+        }
+      }
+      *reinterpret_cast<uint4 *>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
@@ -75,88 +113,78 @@ __device__ __forceinline__ uint32_t code2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
-template <int V>
-__device__ __forceinline__ void store_codes(uint8_t *p, const float (&v)[V], bool wide) {
-  if (V == 1 || !wide) {
+template <int V, int kPer>
+__device__ __forceinline__ void store_codes(uint8_t *row, int c0, int step, int d, bool wide,
+                                            const float (&v)[kPer][V]) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) p[e] = __nv_cvt_float_to_fp8(v[e], __NV_SATFINITE, __NV_E4M3);
-  } else if constexpr (V == 4) {
-    *reinterpret_cast<uint32_t *>(p) = code2(v[0], v[1]) | code2(v[2], v[3]) << 16;
-  } else {
-    *reinterpret_cast<uint2 *>(p) = make_uint2(code2(v[0], v[1]) | code2(v[2], v[3]) << 16,
-                                               code2(v[4], v[5]) | code2(v[6], v[7]) << 16);
+  for (int p = 0; p < kPer; ++p) {
+    const int c = c0 + p * step;
+    if (c >= d) continue;
+    if (V == 1 || !wide) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) row[c + e] = __nv_cvt_float_to_fp8(v[p][e], __NV_SATFINITE, __NV_E4M3);
+    } else {
+      uint32_t w[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < V / 4; ++i)
+        w[i] = code2(v[p][4 * i], v[p][4 * i + 1]) | code2(v[p][4 * i + 2], v[p][4 * i + 3]) << 16;
+      if constexpr (V == 8)
+        *reinterpret_cast<uint2 *>(row + c) = make_uint2(w[0], w[1]);
+      else
+        *reinterpret_cast<uint32_t *>(row + c) = w[0];
+    }
   }
 }
 
 }  // namespace
 
-// kTpr threads hold one row: thread i has the vectors i, i + kTpr, .. of V
-// elements, kPer of them.  Blocks of max(kTpr, 128) threads.
-template <typename T, int V, int kTpr, int kPer>
-__global__ void __launch_bounds__(kTpr > 128 ? kTpr : 128) norm_kernel(const NormArgs a) {
-  constexpr int kRows = kTpr >= 128 ? 1 : 128 / kTpr;
-  constexpr int kW = kTpr / 32;  // warps per row
-  const long long row = static_cast<long long>(blockIdx.x) * kRows + threadIdx.x / kTpr;
-  if (row >= a.rows) return;  // (whole warps; whole blocks where kW > 1)
-  const int t = threadIdx.x % kTpr;
+// Thread i has the vectors i, i + kThreads, .. of V elements, kPer of them.
+template <typename T, int V, int kThreads, int kPer>
+__global__ void __launch_bounds__(kThreads) norm_kernel(const NormArgs a) {
+  constexpr int kW = kThreads / 32;
+  __shared__ float s_ss[kW];
+  __shared__ uint32_t s_top[kW];
+  const int t = threadIdx.x, d = a.d;
+  pdl_wait();
+  const long long row = blockIdx.x;
   const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
   const T *w = static_cast<const T *>(a.weight);
+  const int c0 = t * V;
+  constexpr int step = kThreads * V;
   float v[kPer][V];
-#pragma unroll
-  for (int p = 0; p < kPer; ++p) {
-    const int c = (p * kTpr + t) * V;
-    if (c < a.d)
-      load_vec<T, V>(x + c, v[p], a.wide);
-    else
-#pragma unroll
-      for (int e = 0; e < V; ++e) v[p][e] = 0.0f;
-  }
+  load_row<T, V, kPer>(x, c0, step, d, a.wide, v);
   if (a.residual) {
-    const T *r = static_cast<const T *>(a.residual) + row * a.r_stride;
+    float u[kPer][V];
+    load_row<T, V, kPer>(static_cast<const T *>(a.residual) + row * a.r_stride, c0, step, d, a.wide, u);
 #pragma unroll
-    for (int p = 0; p < kPer; ++p) {
-      const int c = (p * kTpr + t) * V;
-      if (c < a.d) {
-        float u[V];
-        load_vec<T, V>(r + c, u, a.wide);
+    for (int p = 0; p < kPer; ++p)
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[p][e] += u[e];
-      }
-    }
+      for (int e = 0; e < V; ++e) v[p][e] += u[p][e];
   }
-  if (a.sum) {
-    T *s = static_cast<T *>(a.sum) + row * a.d;
-#pragma unroll
-    for (int p = 0; p < kPer; ++p) {
-      const int c = (p * kTpr + t) * V;
-      if (c < a.d) store_vec<T, V>(s + c, v[p], a.wide);
-    }
-  }
+  if (a.sum) store_row<T, V, kPer>(static_cast<T *>(a.sum) + row * d, c0, step, d, a.wide, v);
   // mean square, and max|s w| as a bit pattern
   float ss = 0.0f;
   uint32_t top = 0;
 #pragma unroll
-  for (int p = 0; p < kPer; ++p) {
-    const int c = (p * kTpr + t) * V;
+  for (int p = 0; p < kPer; ++p)
 #pragma unroll
     for (int e = 0; e < V; ++e) ss = fmaf(v[p][e], v[p][e], ss);
-    if (w && c < a.d) {
-      float u[V];
-      load_vec<T, V>(w + c, u, a.wide);
+  if (w) {
+    float u[kPer][V];
+    load_row<T, V, kPer>(w, c0, step, d, a.wide, u);
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[p][e] *= u[e];
-    }
+    for (int p = 0; p < kPer; ++p)
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[p][e] *= u[p][e];
+  }
+#pragma unroll
+  for (int p = 0; p < kPer; ++p)
 #pragma unroll
     for (int e = 0; e < V; ++e) top = max(top, __float_as_uint(fabsf(v[p][e])));
-  }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-  }
+  for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  top = __reduce_max_sync(0xffffffffu, top);
   if constexpr (kW > 1) {
-    __shared__ float s_ss[kW];
-    __shared__ uint32_t s_top[kW];
     if ((t & 31) == 0) {
       s_ss[t >> 5] = ss;
       s_top[t >> 5] = top;
@@ -170,18 +198,13 @@ __global__ void __launch_bounds__(kTpr > 128 ? kTpr : 128) norm_kernel(const Nor
       top = max(top, s_top[i]);
     }
   }
-  const float r = w ? rsqrtf(ss / static_cast<float>(a.d) + a.eps) : 1.0f;
+  const float r = w ? rsqrtf(ss / static_cast<float>(d) + a.eps) : 1.0f;
   if (a.out) {
-    T *o = static_cast<T *>(a.out) + row * a.d;
 #pragma unroll
-    for (int p = 0; p < kPer; ++p) {
-      const int c = (p * kTpr + t) * V;
-      if (c < a.d) {
+    for (int p = 0; p < kPer; ++p)
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[p][e] *= r;
-        store_vec<T, V>(o + c, v[p], a.wide);
-      }
-    }
+      for (int e = 0; e < V; ++e) v[p][e] *= r;
+    store_row<T, V, kPer>(static_cast<T *>(a.out) + row * d, c0, step, d, a.wide, v);
   }
   if (a.codes) {
     const float m = __uint_as_float(top);
@@ -191,57 +214,64 @@ __global__ void __launch_bounds__(kTpr > 128 ? kTpr : 128) norm_kernel(const Nor
     // 448 / m stays finite
     const float lift = m < 0x1p-60f ? 0x1p80f : 1.0f;
     const float f = finite ? (scale == 0.0f ? 0.0f : 448.0f / (m * lift)) : scale;
-    uint8_t *q = a.codes + row * a.d;
 #pragma unroll
-    for (int p = 0; p < kPer; ++p) {
-      const int c = (p * kTpr + t) * V;
-      if (c < a.d) {
+    for (int p = 0; p < kPer; ++p)
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[p][e] = v[p][e] * lift * f;
-        store_codes<V>(q + c, v[p], a.wide);
-      }
-    }
+      for (int e = 0; e < V; ++e) v[p][e] = v[p][e] * lift * f;
+    store_codes<V, kPer>(a.codes + row * d, c0, step, d, a.wide, v);
     if (t == 0) a.scales[row] = scale;
   }
 }
 
 namespace {
 
-template <typename T, int V, int kTpr, int kPer>
+template <typename T, int V, int kThreads, int kPer>
 cudaError_t launch_norm(const NormArgs &a, cudaStream_t st) {
-  constexpr int kRows = kTpr >= 128 ? 1 : 128 / kTpr;
-  const long long grid = (a.rows + kRows - 1) / kRows;
-  norm_kernel<T, V, kTpr, kPer>
-      <<<static_cast<unsigned>(grid), kTpr > 128 ? kTpr : 128, 0, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.rows));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_kernel<T, V, kThreads, kPer>, a);
 }
 
+// The width alone decides which thread holds which elements, so a row's result
+// depends neither on where its tensors lie nor on how many rows there are.  Two
+// to four vectors per thread (with a residual and codes, 16,384 rows of 2,048
+// bf16 timed one call at a time: 42.4 us with 64 threads of 4, 42.6 with 128 of
+// 2, 48.9 with 256 of 1; back to back 37.6 us, 6.2 TB/s; one row: 5.5 us each).
+// Blocks that stay and take several rows, loading ahead, were slower (67 us).
 template <typename T>
 cudaError_t pick_norm(const NormArgs &a, cudaStream_t st) {
   constexpr int V = 16 / static_cast<int>(sizeof(T));
-  // The width alone decides which thread holds which elements, so a result
-  // does not depend on where its tensors lie.
-  if (a.d % V == 0) {
-    const int n = a.d / V;
-    if (n <= 128) return launch_norm<T, V, 32, 4>(a, st);
-    if (n <= 256) return launch_norm<T, V, 256, 1>(a, st);
-    if (n <= 512) return launch_norm<T, V, 256, 2>(a, st);
-    if (n <= 1024) return launch_norm<T, V, 256, 4>(a, st);
-    return launch_norm<T, V, 1024, 4>(a, st);
+  if (a.d % V != 0) {
+    if (a.d <= 256) return launch_norm<T, 1, 64, 4>(a, st);
+    if (a.d <= 1024) return launch_norm<T, 1, 128, 8>(a, st);
+    if (a.d <= 2048) return launch_norm<T, 1, 256, 8>(a, st);
+    if (a.d <= 4096) return launch_norm<T, 1, 512, 8>(a, st);
+    return launch_norm<T, 1, 1024, 16>(a, st);
   }
-  if (a.d <= 256) return launch_norm<T, 1, 32, 8>(a, st);
-  if (a.d <= 1024) return launch_norm<T, 1, 256, 4>(a, st);
-  if (a.d <= 2048) return launch_norm<T, 1, 256, 8>(a, st);
-  return launch_norm<T, 1, 1024, 16>(a, st);
+  const int n = a.d / V;
+  if (n <= 64) return launch_norm<T, V, 32, 2>(a, st);
+  if (n <= 128) return launch_norm<T, V, 32, 4>(a, st);
+  if (n <= 256) return launch_norm<T, V, 64, 4>(a, st);
+  if (n <= 512) return launch_norm<T, V, 128, 4>(a, st);
+  if (n <= 1024) return launch_norm<T, V, 256, 4>(a, st);
+  if (n <= 2048) return launch_norm<T, V, 512, 4>(a, st);
+  return launch_norm<T, V, 1024, 4>(a, st);
 }
 
 bool misaligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) != 0; }
 
 int run_norm(NormArgs a, moe_dtype dtype, cudaStream_t st) {
   const uintptr_t esz = dtype == MOE_BF16 ? 2 : 4;
+  const int V = static_cast<int>(16 / esz);
+  a.wide = a.x_stride % V == 0 && (!a.residual || a.r_stride % V == 0) && !misaligned(a.codes, V);
   const void *ptrs[] = {a.x, a.residual, a.weight, a.sum, a.out};
-  a.wide = a.d % static_cast<int>(16 / esz) == 0 && a.x_stride % static_cast<int>(16 / esz) == 0 &&
-             (!a.residual || a.r_stride % static_cast<int>(16 / esz) == 0) && !misaligned(a.codes, 8);
   for (const void *p : ptrs) {
     if (misaligned(p, esz)) return MOE_ERR_ALIGNMENT;
     a.wide = a.wide && !misaligned(p, 16);
