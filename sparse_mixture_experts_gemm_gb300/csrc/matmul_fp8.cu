@@ -223,14 +223,14 @@ __global__ void __launch_bounds__(kMmThreads, 1)
 
 namespace {
 
-// many tokens: a stage holds two column blocks of the CTA's 128 tokens and of
+// many tokens: a stage holds one column block of the CTA's 128 tokens and of
 // its 128 of the tile's 256 channels
-constexpr int kCB = 2;
-constexpr int kHalf = kCB * kBlkBytes;
-constexpr int kStages = 3;
+constexpr int kHalf = kBlkBytes;
+constexpr int kStages = 6;
 constexpr int kPairCols = 512;
 constexpr int kStageOut = 4 * 32 * 17 * 4;  // per epilogue warp: 32 rows of 32 bf16, padded
-constexpr int kPairSmem = kStages * 2 * kHalf + 1024 + kCtrl + kStageOut;
+constexpr int kScales = 4 * 256 * 4;       // per epilogue warp: the tile's channel scales
+constexpr int kPairSmem = kStages * 2 * kHalf + 1024 + kCtrl + kStageOut + kScales;
 constexpr int kBand = 16;  // 256-token tiles per band
 static_assert(kPairSmem <= kMaxSmem, "shared memory");
 
@@ -267,8 +267,8 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(ctrl);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctrl + 512);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(ctrl + 516);
-  float *s_ws = reinterpret_cast<float *>(ctrl + 1024);              // [4 warps][32]
-  uint32_t *s_out = reinterpret_cast<uint32_t *>(ctrl + kCtrl);      // [4 warps][32][17]
+  uint32_t *s_out = reinterpret_cast<uint32_t *>(ctrl + kCtrl);              // [4 warps][32][17]
+  float *s_ws = reinterpret_cast<float *>(ctrl + kCtrl + kStageOut);         // [4 warps][256]
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages;
   const uint32_t tfull0 = empty0 + 8 * kStages, tempty0 = tfull0 + 16, drain_bar = tempty0 + 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   const int rank = static_cast<int>(cluster_ctarank());
   const int cl = static_cast<int>(blockIdx.x >> 1), ncl = static_cast<int>(gridDim.x >> 1);
   constexpr uint16_t kBoth = 3;
-  const int tiles = p.mt * p.nt, nks = (p.nkb + kCB - 1) / kCB;
+  const int tiles = p.mt * p.nt;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -315,20 +315,16 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         int m, n;
         pair_tile(p, ti, m, n);
         const int xrow = (2 * m + rank) * kRowsM, wrow = (2 * n + rank) * kRowsM;
-        for (int ks = 0; ks < nks; ++ks) {
+        for (int kb = 0; kb < p.nkb; ++kb) {
           if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, limit, abort_flag)) {
             fail(p, abort_flag, SITE_PRODUCER_EMPTY);
             ok = false;
             break;
           }
-          const int cb = min(kCB, p.nkb - ks * kCB);
           const uint32_t fb = full0 + 8 * stage, fb0 = cluster_map(fb, 0);
-          if (rank == 0) mbar_arrive_expect_tx(fb, 4 * cb * kBlkBytes);
-          for (int h = 0; h < cb; ++h) {
-            const int kx = (ks * kCB + h) * kBK;
-            tma_load_2d_pair(smem_u32(sA + stage * kHalf + h * kBlkBytes), &tmX, fb0, kx, xrow, pol);
-            tma_load_2d_pair(smem_u32(sB + stage * kHalf + h * kBlkBytes), &tmW, fb0, kx, wrow, pol);
-          }
+          if (rank == 0) mbar_arrive_expect_tx(fb, 4 * kBlkBytes);
+          tma_load_2d_pair(smem_u32(sA + stage * kHalf), &tmX, fb0, kb * kBK, xrow, pol);
+          tma_load_2d_pair(smem_u32(sB + stage * kHalf), &tmW, fb0, kb * kBK, wrow, pol);
           pend_mask |= 1u << stage;
           pend_phase = (pend_phase & ~(1u << stage)) | (phase << stage);
           if (++stage == kStages) {
@@ -356,54 +352,55 @@ __global__ void __launch_bounds__(kMmThreads, 1)
               fail(p, abort_flag, SITE_DRAIN);
     }
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
+    // The whole warp runs the loop, so that descriptors stay in uniform
+    // registers; one lane issues.  All 512 TMEM columns are this CTA's, so
+    // their addresses start at 0.
+    if (rank == 0) {
       constexpr uint32_t idesc = idesc_make(2 * kRowsM, 256, 0);
+      const bool one = elect_one();
+      const uint64_t da = sdesc_sw128(smem_u32(sA)), db = sdesc_sw128(smem_u32(sB));
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
+      auto wait = [&](uint32_t bar, uint32_t parity, int site) {
+        const bool w = mbar_wait(bar, parity, limit, abort_flag);
+        if (__all_sync(0xffffffffu, w)) return true;
+        if (lane == 0) fail(p, abort_flag, site);
+        return false;
+      };
       for (int ti = cl; ok && ti < tiles; ti += ncl) {
-        if (!mbar_wait(tempty0 + 8 * acc, acc_phase ^ 1, limit, abort_flag)) {
-          fail(p, abort_flag, SITE_MMA_TMEM_EMPTY);
-          ok = false;
-          break;
-        }
+        ok = wait(tempty0 + 8 * acc, acc_phase ^ 1, SITE_MMA_TMEM_EMPTY);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
-        for (int ks = 0; ks < nks; ++ks) {
-          if (!mbar_wait(full0 + 8 * stage, phase, limit, abort_flag)) {
-            fail(p, abort_flag, SITE_MMA_FULL);
-            ok = false;
-            break;
-          }
+        for (int kb = 0; kb < p.nkb; ++kb) {
+          ok = wait(full0 + 8 * stage, phase, SITE_MMA_FULL);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t a0 = smem_u32(sA + stage * kHalf), b0 = smem_u32(sB + stage * kHalf);
-          const int cb = min(kCB, p.nkb - ks * kCB);
-          for (int h = 0; h < cb; ++h)
+          if (one) {
+            const uint32_t at = stage * (kHalf >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint32_t off = h * kBlkBytes + 32 * kk;
-              mma2_e4m3(d, sdesc_sw128(a0 + off), sdesc_sw128(b0 + off), idesc,
-                        (ks | h | kk) != 0 ? 1u : 0u);
-            }
-          tc_commit2_mc(empty0 + 8 * stage, kBoth);
+            for (int kk = 0; kk < 4; ++kk)
+              mma2_e4m3(acc * 256, da + at + 2 * kk, db + at + 2 * kk, idesc, (kb | kk) != 0 ? 1u : 0u);
+            tc_commit2_mc(empty0 + 8 * stage, kBoth);
+          }
           if (++stage == kStages) {
             stage = 0;
             phase ^= 1;
           }
         }
         if (!ok) break;
-        tc_commit2_mc(tfull0 + 8 * acc, kBoth);
+        if (one) tc_commit2_mc(tfull0 + 8 * acc, kBoth);
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1;
       }
       if (!ok) {  // the MMAs issued so far end before TMEM or shared memory go away
-        tc_commit2(drain_bar);
-        if (!mbar_wait(drain_bar, 0, limit, nullptr)) fail(p, abort_flag, SITE_DRAIN);
+        if (one) tc_commit2(drain_bar);
+        if (!mbar_wait(drain_bar, 0, limit, nullptr) && lane == 0) fail(p, abort_flag, SITE_DRAIN);
       }
     }
   } else {
     const int wq = warp & 3;
-    float *ws = s_ws + wq * 32;
+    float *ws = s_ws + wq * 256;
     uint32_t *so = s_out + wq * 32 * 17;
     const uint32_t tempty_r = cluster_map(tempty0, 0);
     int acc = 0;
@@ -411,6 +408,19 @@ __global__ void __launch_bounds__(kMmThreads, 1)
     for (int ti = cl; ti < tiles; ti += ncl) {
       int m, n;
       pair_tile(p, ti, m, n);
+      // the tile's scales, under its products
+      const int t0 = (2 * m + rank) * kRowsM + wq * 32, t = t0 + lane;
+      const float xs = t < p.T ? p.xs[t] : 0.0f;
+      float w8[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int nn = n * 256 + 32 * i + lane;
+        w8[i] = nn < p.N ? p.ws[nn] : 0.0f;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ws[32 * i + lane] = w8[i];
+      __syncwarp();
       const bool ok = mbar_wait(tfull0 + 8 * acc, acc_phase, limit, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) {
         if (lane == 0) fail(p, abort_flag, SITE_EPI_TMEM_FULL);
@@ -419,8 +429,6 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       tc_fence_after();
       const uint32_t tb =
           tmem + static_cast<uint32_t>(acc * 256) + (static_cast<uint32_t>(wq * 32) << 16);
-      const int t0 = (2 * m + rank) * kRowsM + wq * 32, t = t0 + lane;
-      const float xs = t < p.T ? p.xs[t] : 0.0f;
       const int rows = min(32, p.T - t0);
 #pragma unroll 1
       for (int c = 0; c < 256; c += 32) {
@@ -428,12 +436,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
         if (nc >= p.N) break;
         float v[32];
         tmem_ld32_sync(tb + c, v);
-        __syncwarp();
-        ws[lane] = nc + lane < p.N ? p.ws[nc + lane] : 0.0f;
-        __syncwarp();
+        __syncwarp();  // (the last columns' readers of the output tile are done)
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
-          const float4 w4 = *reinterpret_cast<const float4 *>(ws + i);
+          const float4 w4 = *reinterpret_cast<const float4 *>(ws + c + i);
           v[i] *= w4.x * xs;
           v[i + 1] *= w4.y * xs;
           v[i + 2] *= w4.z * xs;
