@@ -35,7 +35,7 @@ constexpr int kBK = 128;         // bytes of K per column block (one swizzle row
 constexpr int kRowsM = 128;      // MMA rows of one CTA
 constexpr int kBlkBytes = kRowsM * kBK;
 constexpr int kMmThreads = 192;  // TMA producer, MMA issuer, four epilogue warps
-constexpr int kCtrl = 2048;      // barriers, TMEM address, abort flag, scales
+constexpr int kCtrl = 2048;      // barriers, TMEM address, abort flag, token scales
 constexpr int kMaxSmem = 227 * 1024;
 
 struct MatmulArgs {
@@ -48,12 +48,17 @@ struct MatmulArgs {
   int bt, split, stages, tt;  // tokens per tile, CTAs along K, ring stages, token tiles
   // many tokens
   int mt, nt;  // 256-token and 256-channel tiles
-  bool wide;   // out's rows start on 32-byte boundaries
+  int align;   // every row of out starts on a boundary of so many bytes: 32, 16, 8, 4 or 2
 };
 
 __device__ __forceinline__ void fail(const MatmulArgs &p, volatile int *abort_flag, int site) {
   *abort_flag = 1;
   report_error(p.status, MOE_ERR_DEVICE_TIMEOUT, KID_MATMUL_FP8 * 100 + site);
+}
+
+__device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
@@ -65,19 +70,27 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
 
 // Few tokens.  Cluster of p.split CTAs per (128 channels, p.bt tokens); CTA r
 // multiplies the K blocks [r nkb / split, (r + 1) nkb / split).  TMEM lane =
-// channel, column = token.
+// channel, column = token.  The partial sums are laid out in shared memory
+// [token][128 channels] over the stages, each CTA's share of the tokens goes to
+// it in one bulk copy from every CTA of the cluster (stores into another CTA's
+// shared memory, lane by lane, took 3 us more for 64 tokens), and each adds
+// and stores its share.
 __global__ void __launch_bounds__(kMmThreads, 1)
     matmul_fp8_few_kernel(const __grid_constant__ CUtensorMap tmX,
                           const __grid_constant__ CUtensorMap tmW, const MatmulArgs p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = align1024(smem_raw);
   const int stage_bytes = kBlkBytes + p.bt * kBK;
-  float *exch = reinterpret_cast<float *>(smem + p.stages * stage_bytes);  // [split][bt / split][128]
+  float *part = reinterpret_cast<float *>(smem);  // this CTA's sums, [bt][128], over the stages
+  // the sums handed over: [split][bt / split][128]
+  float *exch = reinterpret_cast<float *>(smem + max(p.stages * stage_bytes, p.bt * kRowsM * 4));
   uint8_t *ctrl = reinterpret_cast<uint8_t *>(exch) + (p.split > 1 ? p.bt * kRowsM * 4 : 0);
   uint64_t *bars = reinterpret_cast<uint64_t *>(ctrl);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctrl + 512);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(ctrl + 516);
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * p.stages, tfull = empty0 + 8 * p.stages;
+  const uint32_t xbar = tfull + 8;  // counts the bytes of the sums handed over
+  float *s_xs = reinterpret_cast<float *>(ctrl + 1024);  // [bt] the tile's token scales
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long limit = MOE_WAIT_LIMIT_CYCLES;
   const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -94,8 +107,10 @@ __global__ void __launch_bounds__(kMmThreads, 1)
       mbar_init(empty0 + 8 * s, 1);
     }
     mbar_init(tfull, 1);
+    mbar_init(xbar, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    if (p.split > 1) mbar_arrive_expect_tx(xbar, p.bt * kRowsM * 4);
     prefetch_tmap(&tmX);
     prefetch_tmap(&tmW);
   }
@@ -107,9 +122,19 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (p.split > 1) cluster_sync_all();  // every CTA of the cluster runs, its barriers exist
   pdl_wait();
+  pdl_launch_dependents();
 
   bool ok = true;
+  // the epilogue's scales, under the products: two channels per thread
+  const int e = static_cast<int>(threadIdx.x) - 64, c = 2 * (e & 63), n = n0 + c;
+  float w0 = 0.0f, w1 = 0.0f;
+  if (warp >= 2) {
+    for (int i = e; i < p.bt; i += 128) s_xs[i] = t0 + i < p.T ? p.xs[t0 + i] : 0.0f;
+    if (n < p.N) w0 = p.ws[n];
+    if (n + 1 < p.N) w1 = p.ws[n + 1];
+  }
   if (warp == 0 && lane == 0) {
     const uint64_t pol = policy_evict_last();
     int stage = 0;
@@ -168,52 +193,69 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   }
   tc_fence_after();
 
-  const int wq = warp & 3;               // TMEM lane quarter of an epilogue warp
-  const int c = wq * 32 + lane;          // its lane's channel in the tile
-  const uint32_t tb = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-  const int n = n0 + c;
-  const bool epi = warp >= 2;
-  const float wsn = (epi && n < p.N) ? p.ws[n] : 0.0f;
-  if (p.split == 1) {
-    if (epi) {
-      for (int j = 0; j < p.bt; j += 16) {
-        float v[16];
-        tmem_ld16_sync(tb + j, v);
+  const int per = p.bt / p.split;
+  if (warp >= 2) {
+    const int wq = warp & 3;       // TMEM lane quarter of an epilogue warp
+    float *to = part + wq * 32 + lane;
+    for (int j = 0; j < p.bt; j += 16) {
+      float v[16];
+      tmem_ld16_sync(tmem + j + (static_cast<uint32_t>(wq * 32) << 16), v);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int t = t0 + j + i;
-          if (t < p.T && n < p.N)
-            p.out[t * p.out_stride + n] = __float2bfloat16_rn(v[i] * wsn * p.xs[t]);
+      for (int i = 0; i < 16; ++i) to[(j + i) * kRowsM] = v[i];
+    }
+    if (p.split > 1) fence_proxy_async_smem();
+    named_bar_sync(1, 128);
+    if (e < p.split && p.split > 1) {
+      const uint32_t bytes = per * kRowsM * 4;
+      asm volatile(
+          "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+              cluster_map(smem_u32(exch) + rank * bytes, e)),
+          "r"(smem_u32(part) + e * bytes), "r"(bytes), "r"(cluster_map(xbar, e))
+          : "memory");
+    }
+    __syncwarp();
+    if (p.split > 1) {
+      ok = mbar_wait(xbar, 0, limit, nullptr);
+      if (!__all_sync(0xffffffffu, ok) && lane == 0) fail(p, abort_flag, SITE_STAGE);
+    }
+    // two channels of every other token per thread
+    const float *sums = p.split > 1 ? exch : part;
+    const int first = rank * per, count = min(per, p.T - t0 - first);
+    __nv_bfloat16 *o = p.out + (t0 + first) * p.out_stride + n;
+    if (n < p.N) {
+      constexpr int kU = 8;  // tokens in flight
+      const bool pair = n + 1 < p.N;
+      for (int i0 = e >> 6; i0 < count; i0 += 2 * kU) {
+        float2 v[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) v[u] = make_float2(0.0f, 0.0f);
+        for (int s = 0; s < p.split; ++s)
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            const int i = min(i0 + 2 * u, per - 1);
+            const float2 x = *reinterpret_cast<const float2 *>(sums + (s * per + i) * kRowsM + c);
+            v[u].x += x.x;
+            v[u].y += x.y;
+          }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int i = i0 + 2 * u;
+          if (i >= count) break;
+          const float xs = s_xs[first + i];
+          const float y0 = v[u].x * (w0 * xs), y1 = v[u].y * (w1 * xs);
+          if (p.align >= 4 && pair) {
+            *reinterpret_cast<uint32_t *>(o + i * p.out_stride) = bf16x2_bits(y0, y1);
+          } else {
+            o[i * p.out_stride] = __float2bfloat16_rn(y0);
+            if (pair) o[i * p.out_stride + 1] = __float2bfloat16_rn(y1);
+          }
         }
       }
     }
-  } else {
-    // tokens [s per, (s + 1) per) of every CTA's partial sums go to CTA s
-    const int per = p.bt / p.split;
-    cluster_sync_all();  // every CTA of the cluster runs
-    if (epi) {
-      const uint32_t mine = smem_u32(exch + (static_cast<long long>(rank) * per) * kRowsM + c);
-      for (int j = 0; j < p.bt; j += 16) {
-        float v[16];
-        tmem_ld16_sync(tb + j, v);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int dst = (j + i) / per, at = (j + i) - dst * per;
-          const uint32_t a = cluster_map(mine + at * kRowsM * 4, dst);
-          asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v[i]) : "memory");
-        }
-      }
-    }
-    cluster_sync_all();
-    if (epi) {
-      for (int i = 0; i < per; ++i) {
-        const int t = t0 + rank * per + i;
-        if (t >= p.T) break;
-        float v = 0.0f;
-        for (int s = 0; s < p.split; ++s) v += exch[(s * per + i) * kRowsM + c];
-        if (n < p.N) p.out[t * p.out_stride + n] = __float2bfloat16_rn(v * wsn * p.xs[t]);
-      }
-    }
+  }
+  if (p.split > 1) {
+    __syncwarp();
+    cluster_sync_all();  // every CTA has its sums: none leaves while one reads from it
   }
   tc_fence_before();
   __syncthreads();
@@ -228,7 +270,8 @@ namespace {
 constexpr int kHalf = kBlkBytes;
 constexpr int kStages = 6;
 constexpr int kPairCols = 512;
-constexpr int kStageOut = 4 * 32 * 17 * 4;  // per epilogue warp: 32 rows of 32 bf16, padded
+constexpr int kOutPitch = 20;                       // words per row of an output tile
+constexpr int kStageOut = 4 * 32 * kOutPitch * 4;  // per epilogue warp: 32 rows of 32 bf16
 constexpr int kScales = 4 * 256 * 4;       // per epilogue warp: the tile's channel scales
 constexpr int kPairSmem = kStages * 2 * kHalf + 1024 + kCtrl + kStageOut + kScales;
 constexpr int kBand = 16;  // 256-token tiles per band
@@ -244,9 +287,27 @@ __device__ __forceinline__ void pair_tile(const MatmulArgs &p, int i, int &m, in
   m = m0 + r - n * h;
 }
 
-__device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t *>(&v);
+}  // namespace
+
+namespace {
+
+// rows x min(left, 32) bf16 of a warp's output tile (rows kOutPitch words
+// apart) to global memory, U's width per lane
+template <typename U>
+__device__ __forceinline__ void store_tile(__nv_bfloat16 *o, long long stride, const uint32_t *tile,
+                                           int lane, int rows, int left) {
+  constexpr int kE = sizeof(U) / 2, kLanes = 32 / kE;  // bf16 per lane, lanes per row
+  const int c = lane % kLanes * kE;
+#pragma unroll 4
+  for (int r = lane / kLanes; r < rows; r += kE) {
+    const uint16_t *src = reinterpret_cast<const uint16_t *>(tile + r * kOutPitch) + c;
+    if (c + kE <= left) {
+      *reinterpret_cast<U *>(o + r * stride + c) = *reinterpret_cast<const U *>(src);
+    } else {
+      for (int x = 0; x < kE && c + x < left; ++x)
+        reinterpret_cast<uint16_t *>(o + r * stride + c)[x] = src[x];
+    }
+  }
 }
 
 }  // namespace
@@ -267,7 +328,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(ctrl);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctrl + 512);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(ctrl + 516);
-  uint32_t *s_out = reinterpret_cast<uint32_t *>(ctrl + kCtrl);              // [4 warps][32][17]
+  uint32_t *s_out = reinterpret_cast<uint32_t *>(ctrl + kCtrl);              // [4 warps][32][kOutPitch]
   float *s_ws = reinterpret_cast<float *>(ctrl + kCtrl + kStageOut);         // [4 warps][256]
   const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kStages;
   const uint32_t tfull0 = empty0 + 8 * kStages, tempty0 = tfull0 + 16, drain_bar = tempty0 + 16;
@@ -303,6 +364,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
+  pdl_launch_dependents();
 
   if (warp == 0) {
     if (lane == 0) {
@@ -401,7 +463,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   } else {
     const int wq = warp & 3;
     float *ws = s_ws + wq * 256;
-    uint32_t *so = s_out + wq * 32 * 17;
+    uint32_t *so = s_out + wq * 32 * kOutPitch;
     const uint32_t tempty_r = cluster_map(tempty0, 0);
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -445,7 +507,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
           v[i + 2] *= w4.z * xs;
           v[i + 3] *= w4.w * xs;
         }
-        if (p.wide && nc + 32 <= p.N) {
+        if (p.align == 32 && nc + 32 <= p.N) {
           // 32 bytes per thread and store: whole sectors
           if (t < p.T) {
             __nv_bfloat16 *o = p.out + t * p.out_stride + nc;
@@ -463,15 +525,23 @@ __global__ void __launch_bounds__(kMmThreads, 1)
           }
         } else {
           // rows off the 32-byte grid, or the last columns: through shared
-          // memory, so that the lanes of a store lie side by side in one row
+          // memory, so that the lanes of a store lie side by side in a row,
+          // with as many bytes each as the rows' alignment allows
 #pragma unroll
-          for (int j = 0; j < 16; ++j) so[lane * 17 + j] = bf16x2_bits(v[2 * j], v[2 * j + 1]);
+          for (int j = 0; j < 16; j += 4)
+            *reinterpret_cast<uint4 *>(so + lane * kOutPitch + j) =
+                make_uint4(bf16x2_bits(v[2 * j], v[2 * j + 1]), bf16x2_bits(v[2 * j + 2], v[2 * j + 3]),
+                           bf16x2_bits(v[2 * j + 4], v[2 * j + 5]), bf16x2_bits(v[2 * j + 6], v[2 * j + 7]));
           __syncwarp();
-          const uint16_t *sh = reinterpret_cast<const uint16_t *>(so);
-          if (nc + lane < p.N)
-            for (int r = 0; r < rows; ++r)
-              reinterpret_cast<uint16_t *>(p.out)[(t0 + r) * p.out_stride + nc + lane] =
-                  sh[r * 34 + lane];
+          __nv_bfloat16 *o = p.out + t0 * p.out_stride + nc;
+          const int left = p.N - nc;
+          if (p.align >= 8) {
+            store_tile<uint2>(o, p.out_stride, so, lane, rows, left);
+          } else if (p.align == 4) {
+            store_tile<uint32_t>(o, p.out_stride, so, lane, rows, left);
+          } else {
+            store_tile<uint16_t>(o, p.out_stride, so, lane, rows, left);
+          }
         }
       }
       tc_fence_before();
@@ -511,6 +581,42 @@ cudaError_t launch_clusters(K kern, int grid, int cluster, int smem, cudaStream_
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, x, w, p);
+}
+
+// Which kernel, and for few tokens how many per tile (bt; 0: the CTA pairs) and
+// how many CTAs along K.
+struct Shape {
+  int bt, split;
+};
+
+// The least of the times that these fits of measured calls give, in us (weights
+// from DRAM, N 512 .. 8192, K 512 .. 4096, T 1 .. 2048; within 20 %).  Few
+// tokens: 0.285 per K block of a CTA, 0.044 per token of its share to store, a
+// cluster's start and exchange.  Pairs: 0.266 per K block, more where out's
+// rows are not on 32-byte boundaries.  E.g. 16 x 2048 x 4096: 6.0 with 8 CTAs
+// along K, 11.9 with one, 13.1 by pairs; 301 x 2500 x 2048: 9.8 in tiles of 64
+// tokens, 16.4 of 32, 12.3 by pairs; 128 x 8192 x 2048: 12.3 in one tile of
+// 128, 10.2 by pairs.
+Shape pick_shape(int T, int N, int nkb, int align, int sms) {
+  auto waves = [](long long ctas, int slots) { return static_cast<double>((ctas + slots - 1) / slots); };
+  const long long tiles = static_cast<long long>((T + 255) / 256) * ((N + 255) / 256);
+  Shape best = {0, 1};
+  double least = 4.2 + waves(tiles, sms / 2) * (0.266 * nkb + 0.7) + (align < 32 ? 2.5 : 0.0);
+  const int most[] = {32, 64, 128};
+  const double start[] = {0.0, 1.1, 1.9, 3.2};
+  for (int m : most) {
+    const int tt = (T + m - 1) / m, bt = ((T + tt - 1) / tt + 15) / 16 * 16;
+    for (int k = 0, split = 1; k < 4 && split <= nkb; ++k, split *= 2) {
+      const long long ctas = static_cast<long long>((N + kRowsM - 1) / kRowsM) * tt * split;
+      const double t = 1.84 + waves(ctas, sms) * (0.285 * ((nkb + split - 1) / split) + 0.0435 * bt / split +
+                                                  start[k] + (split > 1 ? 0.02 * bt : 0.0));
+      if (t < least) {
+        least = t;
+        best = {bt, split};
+      }
+    }
+  }
+  return best;
 }
 
 // Per device: what the launches need to know, looked up once.
@@ -575,33 +681,32 @@ extern "C" int moe_matmul_fp8(const uint8_t *x, const float *x_scales, int T, lo
   p.N = N;
   p.nkb = (K + kBK - 1) / kBK;
   p.status = dev.status;
-  p.wide = !misaligned(out, 32) && out_stride % 16 == 0;
-  CUtensorMap mx, mw;
-  if (!encode_map_2d(&mw, w, 1, N, K, kBK, kRowsM, true, w_stride)) return MOE_ERR_CUDA;
+  p.align = 32;
+  while (misaligned(out, p.align) || 2 * out_stride % p.align != 0) p.align /= 2;
   p.mt = (T + 255) / 256;
   p.nt = (N + 255) / 256;
+  const Shape shape = pick_shape(T, N, p.nkb, p.align, dev.sms);
+  CUtensorMap mx, mw;
+  if (!encode_map_2d(&mw, w, 1, N, K, kBK, kRowsM, true, w_stride) ||
+      !encode_map_2d(&mx, x, 1, T, K, kBK, shape.bt ? shape.bt : kRowsM, true, x_stride))
+    return MOE_ERR_CUDA;
   cudaError_t e;
-  const int pairs = dev.sms / 2;
-  if (p.mt * p.nt > pairs / 2) {
-    if (!encode_map_2d(&mx, x, 1, T, K, kBK, kRowsM, true, x_stride)) return MOE_ERR_CUDA;
-    e = launch_clusters(matmul_fp8_pair_kernel, 2 * (p.mt * p.nt < pairs ? p.mt * p.nt : pairs), 2,
-                        kPairSmem, st, mx, mw, p);
+  if (shape.bt == 0) {
+    const int pairs = dev.sms / 2, tiles = p.mt * p.nt;
+    e = launch_clusters(matmul_fp8_pair_kernel, 2 * (tiles < pairs ? tiles : pairs), 2, kPairSmem, st, mx,
+                        mw, p);
   } else {
-    // tokens in equal tiles of at most 128, and K split over as many CTAs as
-    // keep the grid within the SMs
-    p.tt = (T + 127) / 128;
-    p.bt = ((T + p.tt - 1) / p.tt + 15) / 16 * 16;
-    const int tiles = (N + kRowsM - 1) / kRowsM * p.tt;
-    p.split = 1;
-    while (p.split < 8 && 2 * p.split * tiles <= dev.sms && 2 * p.split <= p.nkb) p.split *= 2;
-    const int stage = kBlkBytes + p.bt * kBK, exch = p.split > 1 ? p.bt * kRowsM * 4 : 0;
+    p.bt = shape.bt;
+    p.split = shape.split;
+    p.tt = (T + p.bt - 1) / p.bt;
+    const int stage = kBlkBytes + p.bt * kBK, part = p.bt * kRowsM * 4, exch = p.split > 1 ? part : 0;
     const int mine = (p.nkb + p.split - 1) / p.split;
     p.stages = (kMaxSmem - 1024 - kCtrl - exch) / stage;
     if (p.stages > mine) p.stages = mine;
     if (p.stages > 16) p.stages = 16;
-    if (!encode_map_2d(&mx, x, 1, T, K, kBK, p.bt, true, x_stride)) return MOE_ERR_CUDA;
-    e = launch_clusters(matmul_fp8_few_kernel, tiles * p.split, p.split,
-                        p.stages * stage + exch + kCtrl + 1024, st, mx, mw, p);
+    const int ring = p.stages * stage;
+    e = launch_clusters(matmul_fp8_few_kernel, (N + kRowsM - 1) / kRowsM * p.tt * p.split, p.split,
+                        (ring > part ? ring : part) + exch + kCtrl + 1024, st, mx, mw, p);
   }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
