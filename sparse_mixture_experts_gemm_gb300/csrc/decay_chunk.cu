@@ -37,10 +37,11 @@
 // all segments at once.  Each lets the next one start its CTAs early (they wait
 // for its results).
 //
-// Roles (512 threads): warp 0 TMA producer; warp 1 issues every MMA, per chunk
-// S Q^T, V^T P^T, the next chunk's scores and its U; warps 4-7 P and V~; warps
-// 8-15 the state (a thread per row and half of d_k) and the outputs.  What a
-// role makes is waited for under other products.  Shared memory is the scarce
+// Roles (512 threads): warp 0 TMA producer; warp 1 issues U's products, warp 2
+// the scores, S Q^T and V^T P^T (one issuer for all left the tensor cores idle
+// for 500 of 2,500 cycles a chunk while it waited for one operand or another);
+// warps 4-7 P and V~; warps 8-15 the state (a thread per row and half of d_k)
+// and the outputs.  Shared memory is the scarce
 // resource (an M = 128, N = 64 product reads 6 KB in its 48 cycles, all of the
 // 128 bytes a cycle): operands that threads make go to TMEM where the MMA can
 // take them from there (V~, S), and the scores use 64 rows.
@@ -596,13 +597,13 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStg; ++s) {
       mbar_init(full0 + 8 * s, 1);
-      mbar_init(empty0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, kOut ? 2 : 1);  // both issuers are done with the stage
     }
     mbar_init(sc_full, 1);
     mbar_init(p_full, 4);
     mbar_init(s_ready, 8);  // the chunk's S is in TMEM, the last chunk's O1, O2 are read
     mbar_init(o_full, 1);
-    mbar_init(drain, 1);
+    mbar_init(drain, kOut ? 2 : 1);
     for (int b = 0; b < 4; ++b) mbar_init(vt_part0 + 8 * b, 1);
     for (int b = 0; b < 2; ++b) {
       // (with outputs, also the last U read: U has one buffer then)
@@ -662,93 +663,87 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
           poll(full0 + 8 * (i % kStg), (i / kStg) & 1, nullptr);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    // The whole warp runs the loop, so that descriptors stay in uniform
+    // ------------------------------------------------------------ issuer of U
+    // A whole warp runs an issuer's loop, so that descriptors stay in uniform
     // registers; one lane issues.  All 512 TMEM columns are this CTA's, so
     // their addresses start at 0.
+    const bool one = elect_one();
+    const uint64_t dk = sdesc_mn(stages + L::kQ, kBlk);
+    uint32_t s = 0;
+    for (int c = 0; c < nc; ++c) {
+      const int ub = c % M::kBufs;
+      const uint32_t u = M::U + ub * kDk, v = M::V + ub * kTerms * 32;
+      const uint64_t k = dk + s * (L::kStage >> 4);
+      // (V~ is made after the chunk's copies have landed; with outputs its
+      // barrier also says that U's one buffer has been read)
+      if ((!kOut && !warp_wait(a, u_empty0 + 8 * ub, ((c >> 1) & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY)) ||
+          !warp_wait(a, vt_full0 + 8 * ub, (c / M::kBufs) & 1, abort_flag, SITE_STAGE))
+        break;
+      tc_fence_after();
+      if (one) {
+        // the small parts of each half of the tokens, then the leading ones:
+        // few sums are truncated at the size of the result, and V~ of the
+        // next chunk can follow part by part
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+          for (int t = kTerms - 1; t > 0; --t) mma_update<kDk>(u, v, k, t, 2 * b, b > 0 || t < kTerms - 1);
+          tc_commit(vt_part0 + 8 * (2 * ub + b));
+        }
+        mma_update<kDk>(u, v, k, 0, 0, true);
+        mma_update<kDk>(u, v, k, 0, 2, true);
+        tc_commit(u_full0 + 8 * ub);
+        tc_commit(empty0 + 8 * s);
+      }
+      s = s + 1 == kStg ? 0 : s + 1;
+    }
+    if (one) tc_commit(drain);
+  } else if (kOut && warp == 2) {
+    // ------------------------------------------------------------ issuer of the scores, O1, O2
     constexpr uint32_t id_sc = idesc_make(64, kC, 1);
     constexpr uint32_t id_o1 = idesc_make(128, kC, 1);
     constexpr uint32_t id_o2 = idesc_make(128, kC, 1) | kTransA;
     const bool one = elect_one();
-    const uint64_t dp = sdesc_sw128(smem_u32(smem) + L::kP);
-    const uint64_t dkm0 = sdesc_mn(stages + L::kQ, kBlk), dvm0 = sdesc_mn(stages + L::kQ + L::kK, kBlk);
-    const uint64_t dk0 = sdesc_sw128(stages + L::kQ), dq0 = sdesc_sw128(stages);
-    // (one lane) U of chunk c, staged at `at` (descriptor units): the small parts
-    // of each half of the tokens, then the leading ones.  Few sums are truncated
-    // at the size of the result, and V~ of the next chunk can follow part by
-    // part.
-    auto update = [&](int c, uint32_t at) {
-      const int ub = c % M::kBufs;
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-#pragma unroll
-        for (int t = kTerms - 1; t > 0; --t)
-          mma_update<kDk>(M::U + ub * kDk, M::V + ub * kTerms * 32, dkm0 + at, t, 2 * b,
-                          b > 0 || t < kTerms - 1);
-        tc_commit(vt_part0 + 8 * (2 * ub + b));
-      }
-      mma_update<kDk>(M::U + ub * kDk, M::V + ub * kTerms * 32, dkm0 + at, 0, 0, true);
-      mma_update<kDk>(M::U + ub * kDk, M::V + ub * kTerms * 32, dkm0 + at, 0, 2, true);
-      tc_commit(u_full0 + 8 * ub);
-    };
-    if (kOut) {
-      uint32_t s = 0;  // stage of chunk c
-      for (int c = -1; c < nc; ++c) {
-        const uint32_t ph = c & 1, next = (c < 0 || s + 1 == kStg) ? 0 : s + 1;
-        if (c >= 0) {
-          const uint32_t at = s * (L::kStage >> 4);
-          if (!warp_wait(a, s_ready, ph, abort_flag, SITE_STAGE)) break;
-          tc_fence_after();
-          if (one) {
-#pragma unroll
-            for (int kk = 0; kk < kDk / 16; ++kk)
-              mma_ts_bf16(M::O1, M::S + 8 * kk, dq0 + at + (((kk >> 2) * kBlk + 32 * (kk & 3)) >> 4), id_o1,
-                          kk > 0 ? 1u : 0u);
-          }
-          if (!warp_wait(a, p_full, ph, abort_flag, SITE_STAGE)) break;
-          tc_fence_after();
-          if (one) {
-#pragma unroll
-            for (int kk = 0; kk < kC / 16; ++kk)
-              MmaKind<__nv_bfloat16>::mma(M::O2, dvm0 + at + kk * (2048 >> 4), dp + ((32 * kk) >> 4), id_o2,
-                                          kk > 0 ? 1u : 0u);
-            tc_commit(o_full);
-            tc_commit(empty0 + 8 * s);
-          }
-        }
-        if (c + 1 < nc) {
-          const uint32_t at = next * (L::kStage >> 4);
-          if (!warp_wait(a, full0 + 8 * next, ((c + 1) / kStg) & 1, abort_flag, SITE_MMA_FULL)) break;
-          tc_fence_after();
-          if (one) {
-            // rows 16 g .. 16 g + 15 of a 64-row accumulator are lanes 32 g ..
-#pragma unroll
-            for (int kk = 0; kk < kDk / 16; ++kk) {
-              const uint32_t off = at + (((kk >> 2) * kBlk + 32 * (kk & 3)) >> 4);
-              MmaKind<__nv_bfloat16>::mma(M::P, dq0 + off, dk0 + off, id_sc, kk > 0 ? 1u : 0u);
-            }
-            tc_commit(sc_full);
-          }
-          if (!warp_wait(a, vt_full0, (c + 1) & 1, abort_flag, SITE_STAGE)) break;
-          tc_fence_after();
-          if (one) update(c + 1, at);
-        }
-        s = next;
-      }
-    } else {
-      uint32_t s = 0;
-      for (int c = 0; c < nc; ++c) {
-        const uint32_t at = s * (L::kStage >> 4);
-        if (!warp_wait(a, u_empty0 + 8 * (c & 1), ((c >> 1) & 1) ^ 1, abort_flag, SITE_MMA_TMEM_EMPTY) ||
-            !warp_wait(a, vt_full0 + 8 * (c & 1), (c >> 1) & 1, abort_flag, SITE_STAGE))
-          break;
+    const uint64_t dp = sdesc_sw128(smem_u32(smem) + L::kP), dv = sdesc_mn(stages + L::kQ + L::kK, kBlk);
+    const uint64_t dk = sdesc_sw128(stages + L::kQ), dq = sdesc_sw128(stages);
+    uint32_t s = 0;
+    for (int c = 0; c <= nc; ++c) {  // scores of chunk c, after the outputs of chunk c - 1
+      const uint32_t ph = c & 1, at = s * (L::kStage >> 4);
+      if (c > 0) {
+        const uint32_t sb = s == 0 ? kStg - 1 : s - 1, before = sb * (L::kStage >> 4);
+        if (!warp_wait(a, s_ready, ph ^ 1, abort_flag, SITE_STAGE)) break;
         tc_fence_after();
         if (one) {
-          update(c, at);
-          tc_commit(empty0 + 8 * s);
+#pragma unroll
+          for (int kk = 0; kk < kDk / 16; ++kk)
+            mma_ts_bf16(M::O1, M::S + 8 * kk, dq + before + (((kk >> 2) * kBlk + 32 * (kk & 3)) >> 4), id_o1,
+                        kk > 0 ? 1u : 0u);
         }
-        s = s + 1 == kStg ? 0 : s + 1;
+        if (!warp_wait(a, p_full, ph ^ 1, abort_flag, SITE_STAGE)) break;
+        tc_fence_after();
+        if (one) {
+#pragma unroll
+          for (int kk = 0; kk < kC / 16; ++kk)
+            MmaKind<__nv_bfloat16>::mma(M::O2, dv + before + kk * (2048 >> 4), dp + ((32 * kk) >> 4), id_o2,
+                                        kk > 0 ? 1u : 0u);
+          tc_commit(o_full);
+          tc_commit(empty0 + 8 * sb);
+        }
       }
+      if (c < nc) {
+        if (!warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL)) break;
+        tc_fence_after();
+        if (one) {
+          // rows 16 g .. 16 g + 15 of a 64-row accumulator are lanes 32 g ..
+#pragma unroll
+          for (int kk = 0; kk < kDk / 16; ++kk) {
+            const uint32_t off = at + (((kk >> 2) * kBlk + 32 * (kk & 3)) >> 4);
+            MmaKind<__nv_bfloat16>::mma(M::P, dq + off, dk + off, id_sc, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(sc_full);
+        }
+      }
+      s = s + 1 == kStg ? 0 : s + 1;
     }
     if (one) tc_commit(drain);
   } else if (warp >= 4 && warp < kState) {
