@@ -37,11 +37,11 @@
 // all segments at once.  Each lets the next one start its CTAs early (they wait
 // for its results).
 //
-// Roles (512 threads): warp 0 TMA producer; warp 1 issues U's products, warp 2
-// the scores, S Q^T and V^T P^T (one issuer for all left the tensor cores idle
-// for 500 of 2,500 cycles a chunk while it waited for one operand or another);
-// warps 4-7 P and V~; warps 8-15 the state (a thread per row and half of d_k)
-// and the outputs.  Shared memory is the scarce
+// Roles (512 threads): warp 0 TMA copies and the products S Q^T, V^T P^T and
+// scores, warp 1 U's products (one issuer for all left the tensor cores idle
+// while it waited for one operand or another); warps 2-5 P (the warps of each
+// TMEM quarter that are free); warps 4-7 V~; warps 8-15 the state (a thread
+// per row and half of d_k) and the outputs.  Shared memory is the scarce
 // resource (an M = 128, N = 64 product reads 6 KB in its 48 cycles, all of the
 // 128 bytes a cycle): operands that threads make go to TMEM where the MMA can
 // take them from there (V~, S), and the scores use 64 rows.
@@ -644,23 +644,122 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
   const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
   const int tail = static_cast<int>(g.len - static_cast<long long>(nc - 1) * kC);  // tokens of the last chunk
 
-  if (warp == 0) {
+  // P of a quarter (16 tokens) by a warp of that TMEM quarter: rows 16 wq +
+  // lane / 4, + 8; columns 8 n + 2 (lane % 4), + 1.  Past column 16 wq + 15
+  // these rows have nothing: zeros, written once.
+  const int pi = 16 * wq + (lane >> 2), pj = 2 * (lane & 3), pm = lane >> 3;
+  // this lane's row address for the matrix stores: rows 0..7, 8..15 of two
+  // neighbouring column groups
+  const uint32_t prow = smem_u32(smem) + L::kP + (16 * wq + 8 * (pm & 1) + (lane & 7)) * 128;
+  int loaded = min(nc, kFirst);  // (warp 0) chunks whose copies were issued
+  auto p_zeros = [&] {
+    for (int n = 2 * wq + 2; n < 8; n += 2) stsm4(prow + (((n + (pm >> 1)) ^ (lane & 7)) << 4), 0u, 0u, 0u, 0u);
+  };
+  auto make_p = [&](int c) {
+    // weights lambda^(row - column): pairs in the copy of the table in which
+    // this lane's pairs start on 8-byte boundaries
+    const float *pw = ctl.rtab[(pi + 1) & 1] + (kC - 1 - pi + ((pi + 1) & 1)) + pj;
+    if (!warp_wait(a, sc_full, c & 1, abort_flag, SITE_EPI_TMEM_FULL)) return false;
+    tc_fence_after();
+    float v[32];
+    tmem_ld_16x64_sync(M::P + lanes, v);
+#pragma unroll
+    for (int n = 0; n < 8; n += 2) {
+      if (n > 2 * wq) break;
+      uint32_t p[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int nn = n + (y >> 1), e = y & 1;
+        float lo = v[4 * nn + 2 * e], hi = v[4 * nn + 2 * e + 1];
+        if (n == 2 * wq) {  // (a score past the diagonal may be anything)
+          const int d = pi + 8 * e - 8 * nn - pj;
+          lo = d >= 0 ? lo : 0.0f;
+          hi = d >= 1 ? hi : 0.0f;
+        }
+        const float2 w = *reinterpret_cast<const float2 *>(pw + 8 * nn - 8 * e);
+        p[y] = bf16x2_bits(lo * w.x, hi * w.y);
+      }
+      stsm4(prow + (((n + (pm >> 1)) ^ (lane & 7)) << 4), p[0], p[1], p[2], p[3]);
+    }
+    fence_proxy_async_smem();
+    warp_arrive(p_full);
+    return true;
+  };
+
+  if (kOut && warp == 0) {
+    // ------------------------------------------------------------ copies; issuer of the scores, O1, O2
+    constexpr uint32_t id_sc = idesc_make(64, kC, 1);
+    constexpr uint32_t id_o1 = idesc_make(128, kC, 1);
+    constexpr uint32_t id_o2 = idesc_make(128, kC, 1) | kTransA;
+    const bool one = elect_one();
+    const uint64_t dp = sdesc_sw128(smem_u32(smem) + L::kP), dv = sdesc_mn(stages + L::kQ + L::kK, kBlk);
+    const uint64_t dk = sdesc_sw128(stages + L::kQ), dq = sdesc_sw128(stages);
+    uint32_t s = 0;
+    for (int c = 0; c <= nc; ++c) {  // scores of chunk c, after the outputs of chunk c - 1
+      const uint32_t ph = c & 1, at = s * (L::kStage >> 4);
+      if (c > 0) {
+        const uint32_t sb = s == 0 ? kStg - 1 : s - 1, before = sb * (L::kStage >> 4);
+        if (!warp_wait(a, s_ready, ph ^ 1, abort_flag, SITE_STAGE)) break;
+        tc_fence_after();
+        if (one) {
+#pragma unroll
+          for (int kk = 0; kk < kDk / 16; ++kk)
+            mma_ts_bf16(M::O1, M::S + 8 * kk, dq + before + (((kk >> 2) * kBlk + 32 * (kk & 3)) >> 4), id_o1,
+                        kk > 0 ? 1u : 0u);
+        }
+        // (the rows past a sequence's end leave V with the last V~)
+        if (!warp_wait(a, p_full, ph ^ 1, abort_flag, SITE_STAGE) ||
+            (c == nc && tail < kC && !warp_wait(a, vt_full0, ph ^ 1, abort_flag, SITE_STAGE)))
+          break;
+        tc_fence_after();
+        if (one) {
+#pragma unroll
+          for (int kk = 0; kk < kC / 16; ++kk)
+            MmaKind<__nv_bfloat16>::mma(M::O2, dv + before + kk * (2048 >> 4), dp + ((32 * kk) >> 4), id_o2,
+                                        kk > 0 ? 1u : 0u);
+          tc_commit(o_full);
+          tc_commit(empty0 + 8 * sb);
+        }
+      }
+      // the copies of chunk c + 2, into the stage of chunk c - 2 (the last two
+      // stages hold the initial state's rows until that is in TMEM)
+      if (c + kFirst < nc) {
+        const int sn = (c + kFirst) % kStg;
+        if (!warp_wait(a, empty0 + 8 * sn, (((c + kFirst) / kStg) & 1) ^ 1, abort_flag, SITE_PRODUCER_EMPTY) ||
+            (c == 0 && !warp_wait(a, s_ready, 0, abort_flag, SITE_STAGE)))
+          break;
+        if (one) load(c + kFirst);
+        loaded = c + kFirst + 1;
+      }
+      if (c < nc) {
+        if (!warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL)) break;
+        tc_fence_after();
+        if (one) {
+          // rows 16 g .. 16 g + 15 of a 64-row accumulator are lanes 32 g ..
+#pragma unroll
+          for (int kk = 0; kk < kDk / 16; ++kk) {
+            const uint32_t off = at + (((kk >> 2) * kBlk + 32 * (kk & 3)) >> 4);
+            MmaKind<__nv_bfloat16>::mma(M::P, dq + off, dk + off, id_sc, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(sc_full);
+        }
+      }
+      s = s + 1 == kStg ? 0 : s + 1;
+    }
+    if (one) tc_commit(drain);
+  } else if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       int c = min(nc, kFirst);
       for (; c < nc; ++c) {
         const int s = c % kStg;
-        if (!poll(empty0 + 8 * s, ((c / kStg) & 1) ^ 1, abort_flag) ||
-            // the last two stages hold the initial state's rows at first
-            (kOut && c == kFirst && !poll(s_ready, 0, abort_flag))) {
+        if (!poll(empty0 + 8 * s, ((c / kStg) & 1) ^ 1, abort_flag)) {
           fail(a, abort_flag, SITE_PRODUCER_EMPTY);
           break;
         }
         load(c);
       }
-      if (*abort_flag)
-        for (int i = max(0, c - kStg); i < c; ++i)
-          poll(full0 + 8 * (i % kStg), (i / kStg) & 1, nullptr);
+      loaded = c;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ issuer of U
@@ -698,69 +797,14 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
       s = s + 1 == kStg ? 0 : s + 1;
     }
     if (one) tc_commit(drain);
-  } else if (kOut && warp == 2) {
-    // ------------------------------------------------------------ issuer of the scores, O1, O2
-    constexpr uint32_t id_sc = idesc_make(64, kC, 1);
-    constexpr uint32_t id_o1 = idesc_make(128, kC, 1);
-    constexpr uint32_t id_o2 = idesc_make(128, kC, 1) | kTransA;
-    const bool one = elect_one();
-    const uint64_t dp = sdesc_sw128(smem_u32(smem) + L::kP), dv = sdesc_mn(stages + L::kQ + L::kK, kBlk);
-    const uint64_t dk = sdesc_sw128(stages + L::kQ), dq = sdesc_sw128(stages);
-    uint32_t s = 0;
-    for (int c = 0; c <= nc; ++c) {  // scores of chunk c, after the outputs of chunk c - 1
-      const uint32_t ph = c & 1, at = s * (L::kStage >> 4);
-      if (c > 0) {
-        const uint32_t sb = s == 0 ? kStg - 1 : s - 1, before = sb * (L::kStage >> 4);
-        if (!warp_wait(a, s_ready, ph ^ 1, abort_flag, SITE_STAGE)) break;
-        tc_fence_after();
-        if (one) {
-#pragma unroll
-          for (int kk = 0; kk < kDk / 16; ++kk)
-            mma_ts_bf16(M::O1, M::S + 8 * kk, dq + before + (((kk >> 2) * kBlk + 32 * (kk & 3)) >> 4), id_o1,
-                        kk > 0 ? 1u : 0u);
-        }
-        if (!warp_wait(a, p_full, ph ^ 1, abort_flag, SITE_STAGE)) break;
-        tc_fence_after();
-        if (one) {
-#pragma unroll
-          for (int kk = 0; kk < kC / 16; ++kk)
-            MmaKind<__nv_bfloat16>::mma(M::O2, dv + before + kk * (2048 >> 4), dp + ((32 * kk) >> 4), id_o2,
-                                        kk > 0 ? 1u : 0u);
-          tc_commit(o_full);
-          tc_commit(empty0 + 8 * sb);
-        }
-      }
-      if (c < nc) {
-        if (!warp_wait(a, full0 + 8 * s, (c / kStg) & 1, abort_flag, SITE_MMA_FULL)) break;
-        tc_fence_after();
-        if (one) {
-          // rows 16 g .. 16 g + 15 of a 64-row accumulator are lanes 32 g ..
-#pragma unroll
-          for (int kk = 0; kk < kDk / 16; ++kk) {
-            const uint32_t off = at + (((kk >> 2) * kBlk + 32 * (kk & 3)) >> 4);
-            MmaKind<__nv_bfloat16>::mma(M::P, dq + off, dk + off, id_sc, kk > 0 ? 1u : 0u);
-          }
-          tc_commit(sc_full);
-        }
-      }
-      s = s + 1 == kStg ? 0 : s + 1;
-    }
-    if (one) tc_commit(drain);
+  } else if (kOut && warp < 4) {
+    // ------------------------------------------------------------ P of quarters 2, 3
+    p_zeros();
+    for (int c = 0; c < nc; ++c)
+      if (!make_p(c)) break;
   } else if (warp >= 4 && warp < kState) {
-    // ------------------------------------------------------------ V~, P
-    // P: rows 16 wq + lane / 4, + 8; columns 8 n + 2 (lane % 4), + 1.  Past
-    // column 16 wq + 15 these rows have nothing: zeros, written once.
-    const int i = 16 * wq + (lane >> 2), j = 2 * (lane & 3);
-    // weights lambda^(row - column): pairs in the copy of the table in which
-    // this lane's pairs start on 8-byte boundaries
-    const float *pw = ctl.rtab[(i + 1) & 1] + (kC - 1 - i + ((i + 1) & 1)) + j;
-    // this lane's row address for P's matrix stores: rows 0..7, 8..15 of two
-    // neighbouring column groups
-    const int m = lane >> 3;
-    const uint32_t dst = smem_u32(smem) + L::kP + (16 * wq + 8 * (m & 1) + (lane & 7)) * 128;
-    if (kOut) {
-      for (int n = 2 * wq + 2; n < 8; n += 2) stsm4(dst + (((n + (m >> 1)) ^ (lane & 7)) << 4), 0u, 0u, 0u, 0u);
-    }
+    // ------------------------------------------------------------ V~ (and P of quarters 0, 1)
+    if (kOut && wq < 2) p_zeros();
     VtWeight w[8];
     vt_weights(ctl.tab, kC, w);
     for (int c = (warp - 4) >> 2; c < nc; c += M::kBufs) {  // (one warpgroup per buffer)
@@ -791,32 +835,7 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
           tmem_st_16x16(ta + 16 * b + (static_cast<uint32_t>(16 * hl) << 16), lead[b][hl]);
       tmem_wait_st();
       warp_arrive(vt_full0 + 8 * vb);
-      if (kOut) {
-        if (!warp_wait(a, sc_full, c & 1, abort_flag, SITE_EPI_TMEM_FULL)) break;
-        tc_fence_after();
-        float v[32];
-        tmem_ld_16x64_sync(M::P + lanes, v);
-#pragma unroll
-        for (int n = 0; n < 8; n += 2) {
-          if (n > 2 * wq) break;
-          uint32_t p[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int nn = n + (y >> 1), e = y & 1;
-            float lo = v[4 * nn + 2 * e], hi = v[4 * nn + 2 * e + 1];
-            if (n == 2 * wq) {  // (a score past the diagonal may be anything)
-              const int g = i + 8 * e - 8 * nn - j;
-              lo = g >= 0 ? lo : 0.0f;
-              hi = g >= 1 ? hi : 0.0f;
-            }
-            const float2 pw2 = *reinterpret_cast<const float2 *>(pw + 8 * nn - 8 * e);
-            p[y] = bf16x2_bits(lo * pw2.x, hi * pw2.y);
-          }
-          stsm4(dst + (((n + (m >> 1)) ^ (lane & 7)) << 4), p[0], p[1], p[2], p[3]);
-        }
-        fence_proxy_async_smem();
-        warp_arrive(p_full);
-      }
+      if (kOut && wq < 2 && !make_p(c)) break;
     }
   } else if (warp >= kState) {
     // ------------------------------------------------------------ state, outputs
@@ -919,6 +938,11 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
     if (dst) store_rows<kHalfDk>(S, srows, dst, kDk, a.dv - d0 - wq * 32);
   }
   __syncwarp();
+  if (warp == 0 && *abort_flag) {  // copies in flight land before the shared memory goes away
+    loaded = __shfl_sync(0xffffffffu, loaded, 0);
+    for (int i = max(0, loaded - kStg); i < loaded; ++i)
+      poll(full0 + 8 * (i % kStg), (i / kStg) & 1, nullptr);
+  }
   const bool fin = poll(drain, 0, nullptr);
   if (!__all_sync(0xffffffffu, fin) && lane == 0) fail(a, abort_flag, SITE_DRAIN);
   tc_fence_before();
