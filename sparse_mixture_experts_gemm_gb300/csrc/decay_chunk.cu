@@ -200,97 +200,6 @@ __device__ __forceinline__ void tmem_st_16x16(uint32_t ta, const uint32_t (&r)[8
                : "memory");
 }
 
-// The segment that work item `item` stands for.
-struct Segment {
-  int seq = -1;          // -1: no such item
-  long long first, len;  // its tokens
-  long long index;       // its place in the sequence
-  bool last;
-  long long slot;        // of the state before it (index > 0); slot + 1: before the next one
-};
-
-// Items in order of the sequences that take this path.  All threads of the
-// block call it; `scratch`: 32 + 4 shared words.
-__device__ __forceinline__ Segment find_segment(const DecayArgs &a, long long item, int *scratch) {
-  Segment g;
-  long long len = 0, first = 0, before = 0;
-  int seq = -1, rank = 0;
-  if (!a.offsets) {
-    len = a.seq_len;  // (fewer than 2^31 tokens, segments and items)
-    const int n = max((static_cast<int>(len) + a.seg_len - 1) / a.seg_len, 1);
-    seq = static_cast<int>(item) / n;
-    if (seq >= a.n_seq) seq = -1;
-    rank = seq;
-    before = n * seq;
-    first = len * seq;
-  } else {
-    // running number of segments, a block's worth of sequences at a time
-    int *warp_sum = scratch, *found = scratch + 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    if (threadIdx.x == 0) found[0] = -1;
-    __syncthreads();
-    long long base = 0;
-    int ranks = 0;  // sequences before this block's worth that take this path
-    for (int i0 = 0; i0 < a.n_seq; i0 += blockDim.x) {
-      const int i = i0 + threadIdx.x;
-      int n = 0;
-      long long l = 0, f = 0;
-      if (i < a.n_seq) {
-        seq_range(a, i, f, l);
-        n = l <= a.recur ? 0 : (static_cast<int>(l) + a.seg_len - 1) / a.seg_len;
-      }
-      int inc = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += u;
-      }
-      const uint32_t mine = __ballot_sync(0xffffffffu, n > 0);
-      if (lane == 31) warp_sum[warp] = inc;
-      __syncthreads();
-      int pre = 0, total = 0;
-      for (int w = 0; w < nw; ++w) {
-        if (w < warp) pre += warp_sum[w];
-        total += warp_sum[w];
-      }
-      const long long lo = base + pre + inc - n;
-      if (n > 0 && item >= lo && item < lo + n) {
-        found[0] = i;
-        found[1] = static_cast<int>(item - lo);
-      }
-      __syncthreads();
-      // ranks of the sequences (one slot fewer than segments each)
-      if (lane == 0) warp_sum[warp] = __popc(mine);
-      __syncthreads();
-      if (n > 0 && found[0] == i) {
-        int r = ranks + __popc(mine & ((1u << lane) - 1u));
-        for (int w = 0; w < warp; ++w) r += warp_sum[w];
-        found[2] = r;
-      }
-      for (int w = 0; w < nw; ++w) ranks += warp_sum[w];
-      base += total;
-      __syncthreads();
-      if (found[0] >= 0) break;
-    }
-    seq = found[0];
-    if (seq >= 0) {
-      rank = found[2];
-      before = item - found[1];
-      seq_range(a, seq, first, len);
-    }
-    __syncthreads();
-  }
-  if (seq < 0) return g;
-  g.seq = seq;
-  g.index = item - before;
-  const long long at = static_cast<long long>(g.index) * a.seg_len;
-  g.first = first + at;
-  g.last = at + a.seg_len >= len;
-  g.len = g.last ? len - at : a.seg_len;
-  g.slot = before - rank + g.index - 1;  // each earlier sequence has one slot fewer than segments
-  return g;
-}
-
 // The weights of two tokens as bf16 parts.
 struct VtWeight {
   __nv_bfloat162 w1, w2, w3;
@@ -483,7 +392,6 @@ struct Ctl {
   uint64_t bars[32];
   uint32_t tmem;
   int abort_flag;
-  int scratch[36];
   // lambda^63 .. lambda^0, then zeros, in copies that start 0 and 1 words late
   alignas(16) float rtab[2][2 * kC + 8];
   float tab[kC + 1];  // lambda^0 .. lambda^64
@@ -493,21 +401,20 @@ static_assert(sizeof(Ctl) <= 2048, "control block");
 }  // namespace
 
 // ws: what each segment leaves -> the state before the next segment, in place,
-// along each sequence.  One thread per 4 elements of a (sequence, head) state;
-// without offsets a block's sequence is known, with them block row y looks at
-// item y and works if that is the first segment of several.
-__global__ void __launch_bounds__(256) decay_chain_kernel(const DecayArgs a, int dk) {
-  __shared__ int scratch[36];
+// along each sequence.  A thread has 4 elements of a (sequence, head) state;
+// without offsets a block's sequence is known, with them a block works if its
+// item is the first segment of several.
+__global__ void __launch_bounds__(512) decay_chain_kernel(const DecayArgs a, int dk) {
   const int per = a.dv * dk / 4;  // vectors of a state
-  const int blocks = (per + 255) / 256;
+  const int blocks = (per + 511) / 512;
   const int hb = static_cast<int>(blockIdx.x) % (a.Hv * blocks), y = static_cast<int>(blockIdx.x) / (a.Hv * blocks);
-  const int h = hb / blocks, e = hb % blocks * 256 + threadIdx.x;
+  const int h = hb / blocks, e = hb % blocks * 512 + static_cast<int>(threadIdx.x);
   pdl_wait();
   pdl_launch_dependents();
   int seq = y, n = (a.seq_len + a.seg_len - 1) / a.seg_len - 1;  // slots of the sequence
   long long slot = static_cast<long long>(n) * y;                // its first one
-  if (a.offsets) {
-    const Segment g = find_segment(a, y, scratch);
+  if (a.table) {
+    const Segment g = find_segment(a, y);
     if (g.seq < 0 || g.index != 0 || g.last) return;
     long long first, len;
     seq_range(a, g.seq, first, len);
@@ -565,7 +472,7 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
   const int h = ht / a.tiles, d0 = ht % a.tiles * 128;
   pdl_wait();
   pdl_launch_dependents();
-  const Segment g = find_segment(a, blockIdx.x / (a.Hv * a.tiles), ctl.scratch);
+  const Segment g = find_segment(a, static_cast<int>(blockIdx.x) / (a.Hv * a.tiles));
   if (g.seq < 0 || (!kOut && (g.last || g.slot + 1 >= a.slots))) return;
   const int nc = static_cast<int>((g.len + kC - 1) / kC);
   const float lam = a.decay[h];
@@ -976,8 +883,8 @@ cudaError_t launch_chunked(const DecayArgs &a, const CUtensorMap &mq, const CUte
     cudaError_t e = launch_pdl(decay_chunk_kernel<kDk, false>, a.items * per, kThreadsC(false),
                                Smem<kDk, false>::kTotal, st, mq, mk, mv, a);
     if (e != cudaSuccess) return e;
-    const long long blocks = (static_cast<long long>(a.dv) * kDk / 4 + 255) / 256;
-    e = launch_pdl(decay_chain_kernel, (a.offsets ? a.items : a.n_seq) * a.Hv * blocks, 256, 0, st, a, kDk);
+    const long long blocks = (static_cast<long long>(a.dv) * kDk / 4 + 511) / 512;
+    e = launch_pdl(decay_chain_kernel, (a.table ? a.items : a.n_seq) * a.Hv * blocks, 512, 0, st, a, kDk);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(decay_chunk_kernel<kDk, true>, a.items * per, kThreadsC(true), Smem<kDk, true>::kTotal,
