@@ -276,12 +276,13 @@ extern "C" int gdn_decay_scan(const void *q, const void *k, const void *v, const
     e = d_k == 128 ? launch_recurrent<128, 8>(a, st) : launch_recurrent<64, 8>(a, st);
   if (e == cudaSuccess && plan.chunked) {
     const uint64_t kw = static_cast<uint64_t>(n_k_heads) * d_k, vw = static_cast<uint64_t>(n_v_heads) * d_v;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mo;
     if (!encode_map_2d(&mq, q, 2, n_tokens, kw, 64, kChunkTok, true, 2 * q_stride) ||
         !encode_map_2d(&mk, k, 2, n_tokens, kw, 64, kChunkTok, true, 2 * k_stride) ||
-        !encode_map_2d(&mv, v, 2, n_tokens, vw, 64, kChunkTok, true, 2 * v_stride))
+        !encode_map_2d(&mv, v, 2, n_tokens, vw, 64, kChunkTok, true, 2 * v_stride) ||
+        !encode_map_2d(&mo, o, 2, n_tokens, vw, 32, 32, false, 0, true))
       return MOE_ERR_CUDA;
-    e = launch_decay_chunked(a, d_k, mq, mk, mv, plan.segmented, st);
+    e = launch_decay_chunked(a, d_k, mq, mk, mv, mo, plan.segmented, st);
   }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

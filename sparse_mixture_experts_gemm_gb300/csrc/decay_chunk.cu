@@ -192,6 +192,21 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
                : "memory");
   return v;
 }
+// a 32 x 32 bf16 tile (64-byte swizzle) to columns x .. of rows y .. of a matrix
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t tile, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(tile), "r"(x), "r"(y)
+      : "memory");
+}
+// this thread's stores have read their tiles; are done
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
 // 16 lanes x 16 columns: lane l of the warp holds rows l / 4 (even registers)
 // and l / 4 + 8 (odd) of column l % 4 of each group of four
 __device__ __forceinline__ void tmem_st_16x16(uint32_t ta, const uint32_t (&r)[8]) {
@@ -453,7 +468,8 @@ template <int kDk, bool kOut>
 __global__ void __launch_bounds__(kThreadsC(kOut), 1)
     decay_chunk_kernel(const __grid_constant__ CUtensorMap tmQ,
                        const __grid_constant__ CUtensorMap tmK,
-                       const __grid_constant__ CUtensorMap tmV, const DecayArgs a) {
+                       const __grid_constant__ CUtensorMap tmV,
+                       const __grid_constant__ CUtensorMap tmO, const DecayArgs a) {
   using L = Smem<kDk, kOut>;
   using M = Cols<kDk, kOut>;
   constexpr int kHalfDk = kDk / 2;
@@ -759,6 +775,7 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
     const uint32_t tile = smem_u32(smem) + L::kO + (warp - kState) * 2048;
     const uint32_t otile = tile + (8 * (mm >> 1) + (lane & 7)) * 64;
     const uint32_t oread = tile + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+    const bool one = elect_one(), whole = d0 + wq * 32 + 32 <= a.dv;
     const bool ovalid = d0 + wq * 32 + 8 * (lane & 3) < a.dv;
     const long long ostride = static_cast<long long>(a.Hv) * a.dv;
     __nv_bfloat16 *obase = a.o + (g.first + 32 * half + (lane >> 2)) * ostride +
@@ -803,6 +820,8 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
         // tokens 32 half .. of the warp's 32 rows of d_v: combined 16 rows at a
         // time, two tokens per word, and stored transposed into the warp's tile
         // of 32 tokens x 64 bytes
+        bulk_wait_read();  // (the last chunk's tile has left)
+        __syncwarp();
 #pragma unroll
         for (int hl = 0; hl < 2; ++hl) {
           float u[16], v[16];
@@ -822,18 +841,25 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
           put_state();  // (S Q^T of this chunk is done: O1 was)
           warp_arrive(s_ready);
         }
-        __syncwarp();
-        // 16 bytes of a token per lane, 8 tokens per store
+        if (32 * half + 32 <= n && whole) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (one)
+            tma_store_2d(&tmO, tile, h * a.dv + d0 + wq * 32, g.first + c * kC + 32 * half);
+        } else {
+          // a sequence's end, or columns past d_v: 16 bytes of a token per lane
+          __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = 8 * i + (lane >> 2);
-          const uint4 r = lds128(oread + 512 * i);
-          if (ovalid && 32 * half + t < n)
-            *reinterpret_cast<uint4 *>(obase + (static_cast<long long>(c) * kC + 8 * i) * ostride) = r;
+          for (int i = 0; i < 4; ++i) {
+            const int t = 8 * i + (lane >> 2);
+            const uint4 r = lds128(oread + 512 * i);
+            if (ovalid && 32 * half + t < n)
+              *reinterpret_cast<uint4 *>(obase + (static_cast<long long>(c) * kC + 8 * i) * ostride) = r;
+          }
         }
-        __syncwarp();
       }
     }
+    if (kOut) bulk_wait_all();
     float *dst = nullptr;
     if (ok) {
       if (!kOut)
@@ -877,18 +903,19 @@ cudaError_t launch_pdl(K kern, long long grid, int threads, int smem, cudaStream
 
 template <int kDk>
 cudaError_t launch_chunked(const DecayArgs &a, const CUtensorMap &mq, const CUtensorMap &mk,
-                           const CUtensorMap &mv, bool segmented, cudaStream_t st) {
+                           const CUtensorMap &mv, const CUtensorMap &mo, bool segmented,
+                           cudaStream_t st) {
   const long long per = static_cast<long long>(a.Hv) * a.tiles;
   if (segmented) {
     cudaError_t e = launch_pdl(decay_chunk_kernel<kDk, false>, a.items * per, kThreadsC(false),
-                               Smem<kDk, false>::kTotal, st, mq, mk, mv, a);
+                               Smem<kDk, false>::kTotal, st, mq, mk, mv, mo, a);
     if (e != cudaSuccess) return e;
     const long long blocks = (static_cast<long long>(a.dv) * kDk / 4 + 511) / 512;
     e = launch_pdl(decay_chain_kernel, (a.table ? a.items : a.n_seq) * a.Hv * blocks, 512, 0, st, a, kDk);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(decay_chunk_kernel<kDk, true>, a.items * per, kThreadsC(true), Smem<kDk, true>::kTotal,
-                    st, mq, mk, mv, a);
+                    st, mq, mk, mv, mo, a);
 }
 
 }  // namespace
@@ -904,10 +931,10 @@ bool decay_chunk_setup() {
 }
 
 cudaError_t launch_decay_chunked(const DecayArgs &a, int dk, const CUtensorMap &mq,
-                                 const CUtensorMap &mk, const CUtensorMap &mv, bool segmented,
-                                 cudaStream_t st) {
-  return dk == 128 ? launch_chunked<128>(a, mq, mk, mv, segmented, st)
-                   : launch_chunked<64>(a, mq, mk, mv, segmented, st);
+                                 const CUtensorMap &mk, const CUtensorMap &mv,
+                                 const CUtensorMap &mo, bool segmented, cudaStream_t st) {
+  return dk == 128 ? launch_chunked<128>(a, mq, mk, mv, mo, segmented, st)
+                   : launch_chunked<64>(a, mq, mk, mv, mo, segmented, st);
 }
 
 }  // namespace moe

@@ -144,7 +144,8 @@ __device__ __forceinline__ float decay_pow(float lam, float n) {
 // decay_chunk.cu
 bool decay_chunk_setup();  // shared-memory attributes; once per device
 cudaError_t launch_decay_chunked(const DecayArgs &a, int dk, const CUtensorMap &mq,
-                                 const CUtensorMap &mk, const CUtensorMap &mv, bool segmented,
+                                 const CUtensorMap &mk, const CUtensorMap &mv,
+                                 const CUtensorMap &mo, bool segmented,
                                  cudaStream_t st);
 
 }  // namespace moe

@@ -191,9 +191,11 @@ cudaError_t gemm_q4_set_smem_attr();
 int *noalloc_status_word();
 
 // moe.cu: tensor-map encoding (host only, no allocation); pitch: bytes from
-// one row to the next, 0 for rows that follow each other
+// one row to the next, 0 for rows that follow each other; swizzle64: the
+// 64-byte swizzle instead
 bool encode_map_2d(CUtensorMap *m, const void *base, size_t esz, uint64_t rows, uint64_t cols,
-                   uint32_t box_cols, uint32_t box_rows, bool swizzle128, uint64_t pitch = 0);
+                   uint32_t box_cols, uint32_t box_rows, bool swizzle128, uint64_t pitch = 0,
+                   bool swizzle64 = false);
 
 // route.cu
 template <typename T>

@@ -56,7 +56,7 @@ EncodeTiledFn get_encode() {
 // box_rows elements; 128-byte swizzle or none; out-of-range elements read as
 // zero.  Host-only (encodes the descriptor, allocates nothing).
 bool moe::encode_map_2d(CUtensorMap *m, const void *base, size_t esz, uint64_t rows, uint64_t cols,
-                        uint32_t box_cols, uint32_t box_rows, bool swizzle128, uint64_t pitch) {
+                        uint32_t box_cols, uint32_t box_rows, bool swizzle128, uint64_t pitch, bool swizzle64) {
   EncodeTiledFn enc = get_encode();
   if (!enc) return false;
   // 2-byte elements travel as bf16 (also the raw bits of 4-bit scales and
@@ -70,7 +70,9 @@ bool moe::encode_map_2d(CUtensorMap *m, const void *base, size_t esz, uint64_t r
   cuuint32_t estr[2] = {1, 1};
   return enc(m, dt, 2, const_cast<void *>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE,
-             swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             swizzle128  ? CU_TENSOR_MAP_SWIZZLE_128B
+             : swizzle64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                         : CU_TENSOR_MAP_SWIZZLE_NONE,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
