@@ -121,7 +121,8 @@ constexpr long long kGpuSms = 152;
 // How a call is cut: the sequences that are not recurrent, their segments.
 struct Plan {
   bool recurrent, chunked, segmented;
-  long long seg_len, items, slots;
+  long long seg_len, items;
+  long long slots;  // states in the workspace
   long long table;  // bytes of the table of segments, at the workspace's start
 };
 
@@ -167,14 +168,13 @@ Plan make_plan(bool ragged, long long n_tokens, long long n_seq, long long heads
   const long long per = ceil_div(len, p.seg_len);
   p.segmented = per > 1;
   if (ragged) {
-    p.slots = p.segmented ? n_tokens / p.seg_len : 0;
     const long long longest = n_tokens / (kRecur + 1);
     p.items = n_tokens / p.seg_len + (n_seq < longest ? n_seq : longest);
     p.table = p.items * static_cast<long long>(sizeof(Segment));
   } else {
     p.items = n_seq * per;
-    p.slots = n_seq * (per - 1);
   }
+  p.slots = p.segmented ? p.items : 0;
   return p;
 }
 
@@ -266,7 +266,6 @@ extern "C" int gdn_decay_scan(const void *q, const void *k, const void *v, const
   a.recur = static_cast<int>(kRecur);
   a.seg_len = static_cast<int>(plan.seg_len);
   a.seq_len = static_cast<int>(n_tokens / n_seq);
-  a.slots = plan.slots;
   a.items = plan.items;
   a.table = plan.table ? static_cast<Segment *>(workspace) : nullptr;
   a.ws = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.table);

@@ -306,9 +306,9 @@ __device__ __forceinline__ void load_rows(float (&v)[kN], uint32_t tile, const f
   }
   __syncwarp();
 }
+// and back: into the tile, then from the tile to global memory
 template <int kN>
-__device__ __forceinline__ void store_rows(const float (&v)[kN], uint32_t tile, float *dst, int pitch,
-                                           int rows) {
+__device__ __forceinline__ void tile_rows(const float (&v)[kN], uint32_t tile) {
   constexpr int kP = kN / 4;
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -316,6 +316,11 @@ __device__ __forceinline__ void store_rows(const float (&v)[kN], uint32_t tile, 
     sts128(tile + (lane * kP + (p ^ (lane & (kP - 1)))) * 16, __float_as_uint(v[4 * p]),
            __float_as_uint(v[4 * p + 1]), __float_as_uint(v[4 * p + 2]), __float_as_uint(v[4 * p + 3]));
   __syncwarp();
+}
+template <int kN>
+__device__ __forceinline__ void store_rows(uint32_t tile, float *dst, int pitch, int rows) {
+  constexpr int kP = kN / 4;
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int i = 0; i < kP; ++i) {
     const int r = (i * 32 + lane) / kP, p = (i * 32 + lane) % kP;
@@ -341,6 +346,47 @@ __device__ __forceinline__ void zero_rows(uint32_t k, uint32_t v, int wq, int n)
   }
   fence_proxy_async_smem();
   __syncwarp();
+}
+
+// A NaN or infinity in v reaches the earlier tokens of its chunk, too: V^T P^T
+// multiplies it by their zeros in P.  It also leaves its row of the state NaN
+// for good, so a row of S that ends as NaN is the sign, and costs the others
+// nothing.  A warp then goes over column j of v: if token t is the first that
+// is not finite, the outputs of the tokens before it in its chunk are made
+// again by the recurrence along the row, from the state before the segment.
+template <int kDk>
+__device__ __noinline__ void redo_row(const DecayArgs &a, int first, int len, int h, int j,
+                                      const float *row) {
+  constexpr int kE = kDk / 32;
+  const int lane = threadIdx.x & 31;
+  const long long hk = static_cast<long long>(h / (a.Hv / a.Hk)) * kDk + kE * lane;
+  const long long hv = static_cast<long long>(h) * a.dv + j;
+  int bad = len;
+  for (int t0 = 0; t0 < len && bad == len; t0 += 32) {
+    const int t = t0 + lane;
+    const bool b = t < len && !isfinite(__bfloat162float(a.v[static_cast<long long>(first + t) * a.v_stride + hv]));
+    const uint32_t m = __ballot_sync(0xffffffffu, b);
+    if (m) bad = t0 + __ffs(m) - 1;
+  }
+  if (bad == len || bad % kC == 0) return;
+  const float lam = a.decay[h];
+  float S[kE];
+#pragma unroll
+  for (int i = 0; i < kE; ++i) S[i] = row ? row[kE * lane + i] : 0.0f;
+  for (int t = 0; t < bad; ++t) {
+    const long long at = first + t;
+    const float v = __bfloat162float(a.v[at * a.v_stride + hv]);
+    float d = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kE; ++i) {
+      S[i] = fmaf(lam, S[i], v * __bfloat162float(a.k[at * a.k_stride + hk + i]));
+      d = fmaf(S[i], __bfloat162float(a.q[at * a.q_stride + hk + i]), d);
+    }
+    if (t < bad - bad % kC) continue;
+#pragma unroll
+    for (int m = 16; m; m >>= 1) d += __shfl_xor_sync(0xffffffffu, d, m);
+    if (lane == 0) a.o[at * a.Hv * a.dv + hv] = __float2bfloat16_rn(d);
+  }
 }
 
 // One part of the update product U[d_v][d_k] = V~^T K over k steps kk0, kk0 + 1
@@ -418,7 +464,8 @@ static_assert(sizeof(Ctl) <= 2048, "control block");
 // ws: what each segment leaves -> the state before the next segment, in place,
 // along each sequence.  A thread has 4 elements of a (sequence, head) state;
 // without offsets a block's sequence is known, with them a block works if its
-// item is the first segment of several.
+// item is the first segment of several.  Where the final state goes over the
+// initial one, that is copied for the first segment.
 __global__ void __launch_bounds__(512) decay_chain_kernel(const DecayArgs a, int dk) {
   const int per = a.dv * dk / 4;  // vectors of a state
   const int blocks = (per + 511) / 512;
@@ -426,8 +473,8 @@ __global__ void __launch_bounds__(512) decay_chain_kernel(const DecayArgs a, int
   const int h = hb / blocks, e = hb % blocks * 512 + static_cast<int>(threadIdx.x);
   pdl_wait();
   pdl_launch_dependents();
-  int seq = y, n = (a.seq_len + a.seg_len - 1) / a.seg_len - 1;  // slots of the sequence
-  long long slot = static_cast<long long>(n) * y;                // its first one
+  int seq = y, n = (a.seq_len + a.seg_len - 1) / a.seg_len - 1;  // states to make
+  long long item = static_cast<long long>(n + 1) * y;            // the first segment's
   if (a.table) {
     const Segment g = find_segment(a, y);
     if (g.seq < 0 || g.index != 0 || g.last) return;
@@ -435,19 +482,20 @@ __global__ void __launch_bounds__(512) decay_chain_kernel(const DecayArgs a, int
     seq_range(a, g.seq, first, len);
     seq = g.seq;
     n = (static_cast<int>(len) + a.seg_len - 1) / a.seg_len - 1;
-    slot = g.slot + 1;
+    item = y;
   }
-  if (e >= per || slot + n > a.slots) return;
+  if (e >= per || item + n >= a.items) return;
   const float f = decay_pow(a.decay[h], static_cast<float>(a.seg_len));
   const long long step = static_cast<long long>(a.Hv) * per;
-  float4 *w = reinterpret_cast<float4 *>(a.ws) + (slot * a.Hv + h) * per + e;
+  float4 *w = reinterpret_cast<float4 *>(a.ws) + (item * a.Hv + h) * per + e;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (a.s_in) s = reinterpret_cast<const float4 *>(a.s_in)[(static_cast<long long>(seq) * a.Hv + h) * per + e];
+  const float4 s0 = s;
   for (int i0 = 0; i0 < n; i0 += 8) {
     float4 u[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i0 + i < n) u[i] = w[(i0 + i) * step];
+      if (i0 + i < n) u[i] = w[(i0 + i + 1) * step];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i0 + i < n) {
@@ -455,15 +503,15 @@ __global__ void __launch_bounds__(512) decay_chain_kernel(const DecayArgs a, int
         s.y = fmaf(f, s.y, u[i].y);
         s.z = fmaf(f, s.z, u[i].z);
         s.w = fmaf(f, s.w, u[i].w);
-        w[(i0 + i) * step] = s;
+        w[(i0 + i + 1) * step] = s;
       }
   }
+  if (a.s_in && a.s_in == a.s_out) *w = s0;
 }
 
-// kOut: the segment's outputs, from the state before it (of its sequence, or
-// slot g.slot), and the final state if it is the sequence's last.  Otherwise:
-// what the segment leaves from a zero state, into slot g.slot + 1, unless it
-// is the last.
+// kOut: the segment's outputs, from the state before it, and the final state if
+// it is the sequence's last.  Otherwise: what the segment leaves from a zero
+// state, into the next item's place, unless it is the last.
 template <int kDk, bool kOut>
 __global__ void __launch_bounds__(kThreadsC(kOut), 1)
     decay_chunk_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -488,8 +536,9 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
   const int h = ht / a.tiles, d0 = ht % a.tiles * 128;
   pdl_wait();
   pdl_launch_dependents();
-  const Segment g = find_segment(a, static_cast<int>(blockIdx.x) / (a.Hv * a.tiles));
-  if (g.seq < 0 || (!kOut && (g.last || g.slot + 1 >= a.slots))) return;
+  const int item = static_cast<int>(blockIdx.x) / (a.Hv * a.tiles);
+  const Segment g = find_segment(a, item);
+  if (g.seq < 0 || (!kOut && (g.last || item + 1 >= a.items))) return;
   const int nc = static_cast<int>((g.len + kC - 1) / kC);
   const float lam = a.decay[h];
   if (threadIdx.x <= kC) {
@@ -543,15 +592,15 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
   const long long srow =
       ((static_cast<long long>(g.seq) * a.Hv + h) * a.dv + d0 + wq * 32) * kDk + half * kHalfDk;
   const uint32_t srows = stages + kFirst * L::kStage + (warp - kState) * 32 * kHalfDk * 4;
+  // this warp's rows of the state before the segment (null: zeros)
+  auto before_rows = [&]() -> const float * {
+    if (g.index == 0 && (!a.s_in || g.last || a.s_in != a.s_out)) return a.s_in ? a.s_in + srow : nullptr;
+    return a.ws + ((static_cast<long long>(item) * a.Hv + h) * a.dv + d0 + wq * 32) * kDk + half * kHalfDk;
+  };
   float S[kHalfDk];
   if (warp >= kState) {
     if (kOut) {
-      const float *src = nullptr;
-      if (g.index == 0)
-        src = a.s_in ? a.s_in + srow : nullptr;
-      else if (g.slot < a.slots)
-        src = a.ws + ((g.slot * a.Hv + h) * a.dv + d0 + wq * 32) * kDk + half * kHalfDk;
-      load_rows<kHalfDk>(S, srows, src, kDk, a.dv - d0 - wq * 32);
+      load_rows<kHalfDk>(S, srows, before_rows(), kDk, a.dv - d0 - wq * 32);
     } else {
 #pragma unroll
       for (int i = 0; i < kHalfDk; ++i) S[i] = 0.0f;
@@ -863,12 +912,26 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
     float *dst = nullptr;
     if (ok) {
       if (!kOut)
-        dst = a.ws + (((g.slot + 1) * a.Hv + h) * a.dv + d0 + wq * 32) * kDk + half * kHalfDk;
+        dst = a.ws + ((static_cast<long long>(item + 1) * a.Hv + h) * a.dv + d0 + wq * 32) * kDk + half * kHalfDk;
       else if (g.last && a.s_out)
         dst = a.s_out + srow;
     }
     // (every product of the CTA that reads the stages is done)
-    if (dst) store_rows<kHalfDk>(S, srows, dst, kDk, a.dv - d0 - wq * 32);
+    if (ok) tile_rows<kHalfDk>(S, srows);
+    if (kOut) {
+      // (outputs are written, and later the state before is read, by all of
+      // these warps before the next one goes on)
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      uint32_t nan = __ballot_sync(0xffffffffu, ok && isnan(S[0]) && d0 + wq * 32 + lane < a.dv);
+      nan &= 0xffffu << (16 * half);  // (the rows' other half has the others)
+      const float *src = before_rows();
+      for (; nan; nan &= nan - 1) {
+        const int r = __ffs(nan) - 1;
+        redo_row<kDk>(a, g.first, g.len, h, d0 + wq * 32 + r, src ? src + r * kDk - half * kHalfDk : nullptr);
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+    }
+    if (dst) store_rows<kHalfDk>(srows, dst, kDk, a.dv - d0 - wq * 32);
   }
   __syncwarp();
   if (warp == 0 && *abort_flag) {  // copies in flight land before the shared memory goes away

@@ -15,10 +15,9 @@ struct alignas(16) Segment {
   int seq;         // -1: none
   int index;       // its place in the sequence
   int first, len;  // its tokens
-  long long slot;  // of the state before it (index > 0); slot + 1: before the next one
-  int last, pad;
+  int last, pad[3];
 };
-static_assert(sizeof(Segment) == 32, "read as two vectors");
+static_assert(sizeof(Segment) == 32, "its first half is read as a vector");
 
 struct DecayArgs {
   const __nv_bfloat16 *q, *k, *v;
@@ -29,11 +28,12 @@ struct DecayArgs {
   long long n_tokens, q_stride, k_stride, v_stride;
   int n_seq, Hk, Hv, dv;
   // Sequences of at most `recur` tokens take the recurrent kernel, the others
-  // the chunked ones, in segments of seg_len tokens (a multiple of 64); ws
-  // holds the state before each segment but a sequence's first, `slots` of
-  // them at most, [slot][Hv][dv][dk].
+  // the chunked ones, in segments of seg_len tokens (a multiple of 64), one per
+  // work item.  ws holds the state before each item's segment, [item][Hv][dv][dk]
+  // (before a sequence's first one only if the state is updated in place, since
+  // the last segment may write it while the first is still to read it).
   int recur, seg_len, seq_len;  // seq_len: of every sequence without offsets
-  long long slots, items;
+  long long items;
   float *ws;
   Segment *table;  // [items], of a call with offsets (made by its recurrent kernel)
   int tiles;  // 128-wide tiles of d_v
@@ -58,10 +58,9 @@ __device__ __forceinline__ void seq_range(const DecayArgs &a, int i, long long &
 // The table of a call with offsets, by one block: segments in order of their
 // sequences.  All threads of the block call it.
 __device__ __forceinline__ void make_table(const DecayArgs &a) {
-  __shared__ int s_seg[32], s_seq[32];
+  __shared__ int s_seg[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = static_cast<int>(blockDim.x) >> 5;
-  long long base = 0;  // segments and sequences before this block's worth
-  int rank0 = 0;
+  long long base = 0;  // segments before this block's worth of sequences
   for (int i0 = 0; i0 < a.n_seq; i0 += static_cast<int>(blockDim.x)) {
     const int i = i0 + static_cast<int>(threadIdx.x);
     long long first = 0, len = 0;
@@ -76,29 +75,20 @@ __device__ __forceinline__ void make_table(const DecayArgs &a) {
       const int u = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += u;
     }
-    const uint32_t mine = __ballot_sync(0xffffffffu, n > 0);
     if (lane == 31) s_seg[warp] = inc;
-    if (lane == 0) s_seq[warp] = __popc(mine);
     __syncthreads();
     long long at = base + inc - n;
-    int rank = rank0 + __popc(mine & ((1u << lane) - 1u));
     for (int w = 0; w < nw; ++w) {
-      if (w < warp) {
-        at += s_seg[w];
-        rank += s_seq[w];
-      }
+      if (w < warp) at += s_seg[w];
       base += s_seg[w];
-      rank0 += s_seq[w];
     }
     for (int k = 0; k < n && at + k < a.items; ++k) {
-      Segment g;
+      Segment g = {};
       g.seq = i;
       g.index = k;
       g.first = static_cast<int>(first) + k * a.seg_len;
       g.last = k == n - 1;
       g.len = g.last ? static_cast<int>(len) - k * a.seg_len : a.seg_len;
-      g.slot = at - rank + k - 1;  // each earlier sequence has one slot fewer than segments
-      g.pad = 0;
       a.table[at + k] = g;
     }
     __syncthreads();
@@ -110,17 +100,14 @@ __device__ __forceinline__ void make_table(const DecayArgs &a) {
 
 // The segment that work item `item` stands for.
 __device__ __forceinline__ Segment find_segment(const DecayArgs &a, int item) {
-  Segment g;
+  Segment g = {};
   if (a.table) {
-    const int4 *t = reinterpret_cast<const int4 *>(a.table + item);
-    const int4 u = t[0], v = t[1];
+    const int4 u = *reinterpret_cast<const int4 *>(a.table + item);
     g.seq = u.x;
     g.index = u.y;
     g.first = u.z;
     g.len = u.w;
-    g.slot = static_cast<long long>(static_cast<unsigned long long>(static_cast<unsigned>(v.y)) << 32 |
-                                    static_cast<unsigned>(v.x));
-    g.last = v.z;
+    g.last = a.table[item].last;
   } else {  // (fewer than 2^31 tokens, segments and items)
     const int n = (a.seq_len + a.seg_len - 1) / a.seg_len, seq = item / n;
     g.seq = seq < a.n_seq ? seq : -1;
@@ -129,9 +116,7 @@ __device__ __forceinline__ Segment find_segment(const DecayArgs &a, int item) {
     g.first = seq * a.seq_len + at;
     g.last = at + a.seg_len >= a.seq_len;
     g.len = g.last ? a.seq_len - at : a.seg_len;
-    g.slot = static_cast<long long>(seq) * (n - 1) + g.index - 1;
   }
-  g.pad = 0;
   return g;
 }
 

@@ -336,6 +336,88 @@ def test_scan_bad_offsets_stay_in_bounds(dev):
 
 
 # ------------------------------------------------------------- streams
+def test_scan_packed_long_sequence_is_cut(dev):
+    """One sequence outlasts its batch and is scanned in segments, between
+    empty and short ones; also with the state updated in place."""
+    lens = [5, 9000, 0, 130]
+    q, k, v, decay, s = scan_inputs(13, sum(lens), 4, 1, 2, 128, 80)
+    decay[1] = 0.999
+    off = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    qd, kd, vd, dd, sd = (x.to(dev) for x in (q, k, v, decay, s))
+    o, S = moe.gdn_decay_scan(qd, kd, vd, dd, sd, off.to(dev))
+    check_scan(o, S, q, k, v, decay, s, off)
+    o2, _ = moe.gdn_decay_scan(qd, kd, vd, dd, sd, off.to(dev), state_out=sd)
+    assert torch.equal(o, o2) and torch.equal(S, sd)
+
+
+@pytest.mark.parametrize("n,T", [(1, 1), (3, 8), (1, 2000), (3, 700)])
+def test_scan_in_place(dev, n, T):
+    """Writing the state over the initial one changes no bit."""
+    q, k, v, decay, s = (x.to(dev) for x in scan_inputs(14, n * T, n, 1, 2, 128, 144))
+    q, k, v = (x.unflatten(0, (n, T)) for x in (q, k, v))
+    o, S = moe.gdn_decay_scan(q, k, v, decay, s)
+    o2, _ = moe.gdn_decay_scan(q, k, v, decay, s, state_out=s)
+    assert torch.equal(o, o2) and torch.equal(S, s)
+
+
+def test_scan_many_packed_sequences(dev):
+    """More sequences than a block has threads, of every kind."""
+    lens = [(7 * i) % 23 if i % 3 else 64 * (i % 5) + i % 2 for i in range(700)]
+    q, k, v, decay, s = scan_inputs(15, sum(lens), 700, 1, 1, 64, 16)
+    off = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    o, S = moe.gdn_decay_scan(*(x.to(dev) for x in (q, k, v, decay, s, off)))
+    check_scan(o, S, q, k, v, decay, s, off)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_scan_nan_stays_in_its_sequence(dev, bad):
+    """Sequences around one of NaN or infinite q, k, v and state: no bit of
+    theirs changes."""
+    lens = [70, 3, 100, 130, 2, 64]
+    q, k, v, decay, s = (x.to(dev) for x in scan_inputs(16, sum(lens), len(lens), 1, 2, 128, 64))
+    off = torch.tensor([0] + lens).cumsum(0).to(torch.int32).to(dev)
+    o, S = moe.gdn_decay_scan(q, k, v, decay, s, off)
+    for i in (1, 2, 4):
+        lo, hi = int(off[i]), int(off[i + 1])
+        x = [t.clone() for t in (q, k, v, s)]
+        for t in x[:3]:
+            t[lo:hi] = bad
+        x[3][i] = bad
+        o2, S2 = moe.gdn_decay_scan(x[0], x[1], x[2], decay, x[3], off)
+        keep = [j for j in range(len(lens)) if j != i]
+        assert torch.equal(S2[keep], S[keep])
+        assert torch.equal(o2[:lo], o[:lo]) and torch.equal(o2[hi:], o[hi:])
+        assert not torch.isfinite(S2[i]).any()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("-inf")])
+@pytest.mark.parametrize("T,at", [(8, 3), (300, 0), (300, 100), (300, 128), (300, 299), (3000, 2000)])
+def test_scan_nan_reaches_no_earlier_token(dev, T, at, bad):
+    """A value that is not finite in one column of one token: the tokens
+    before it and the other columns keep the oracle's results; from it on the
+    column has none."""
+    q, k, v, decay, s = scan_inputs(17, T, 1, 1, 2, 128, 80)
+    decay[0] = 0.0
+    clean = mixer.decay_scan(f64(q), f64(k), f64(v), f64(decay), f64(s))
+    vb = v.clone()
+    vb[at, :, 37] = bad
+    vb[at + (T - at) // 2, 0, 41] = bad
+    o, S = moe.gdn_decay_scan(q.to(dev), k.to(dev), vb.to(dev), decay.to(dev), s[0].to(dev))
+    o, S = f64(o), f64(S)
+    hidden = np.zeros(o.shape, bool)
+    hidden[at:, :, 37] = True
+    hidden[at + (T - at) // 2:, 0, 41] = True
+    assert not np.isfinite(o[hidden]).any() and np.isfinite(o[~hidden]).all()
+    top = np.maximum(np.abs(clean[0]).max(2, keepdims=True), 1e-30)
+    assert (np.where(hidden, 0, np.abs(o - clean[0])) / top).max() <= O_TOL
+    rows = np.ones(S.shape[:2], bool)
+    rows[:, 37] = False
+    rows[0, 41] = False
+    assert not np.isfinite(S[~rows]).any()
+    err = np.abs(S - clean[1].reshape(S.shape))[rows]
+    assert err.max() <= S_TOL * np.abs(clean[1]).max()
+
+
 def test_other_stream(dev):
     """Each operator on a stream that is not the current one, results read
     there; and captured in a CUDA graph on it."""
