@@ -83,14 +83,23 @@ int gdn_scan(const void *q, const void *k, const void *v, const float *alpha, co
  *   workspace device memory of at least the bytes gdn_decay_workspace gives
  *             for the same sizes, 16-byte aligned, used by the call's kernels
  *             alone; NULL where that is 0.
+ * Sequences of up to 8 tokens take the recurrent form (fp32 arithmetic), longer
+ * ones the chunked form on the tensor cores: the state is kept and updated in
+ * fp32 there too (its error stays that of fp32 arithmetic); for the outputs
+ * alone, state and scores are rounded to bf16 before their products.
  * A long sequence may be taken in pieces, passing the state along; pieces
- * agree with one call up to float rounding.  The caller applies the model's
+ * agree with one call up to these roundings.  The same inputs give the same
+ * bits.  NaN and infinities of one sequence reach no other.  The caller applies the model's
  * preprocessing (norms, query scale) before the call.
  * Supported: d_k 64 or 128, d_v a multiple of 16 up to 1024, n_v_heads a
  * multiple of n_k_heads and at most 4096, n_tokens < 2^31.
  * Pointers 16-byte aligned (decay and offsets 4-byte), strides multiples of 8.
  * n_seq == 0 is a no-op.  Asynchronous on cuda_stream; all checks are made on
- * the host before anything is launched.
+ * the host before anything is launched.  A bounded wait in the kernels that
+ * runs out leaves the results unspecified and records MOE_ERR_DEVICE_TIMEOUT
+ * in the status word of the calls without a handle (moe_noalloc_status); the
+ * first call on a device looks that word up, so make it before any stream
+ * capture.
  * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_ALIGNMENT, MOE_ERR_UNSUPPORTED,
  * MOE_ERR_CUDA.
  */

@@ -368,7 +368,8 @@ int moe_decode_noalloc(const moe_config *cfg, const void *x, void *out, void *cu
 
 /*
  * Synchronise cuda_stream, then return and clear the device status word of
- * moe_decode_noalloc on the current device: MOE_OK, MOE_ERR_DEVICE_TIMEOUT or
+ * the calls without a handle that have waits in their kernels
+ * (moe_decode_noalloc, moe_matmul_fp8, gdn_decay_scan) on the current device: MOE_OK, MOE_ERR_DEVICE_TIMEOUT or
  * MOE_ERR_DEVICE_BOUNDS, the first device-side failure of any call since the
  * last read.  If detail != NULL it receives the library-defined code of the
  * kernel and wait that failed (0 when none).  Allocates nothing; like
@@ -429,8 +430,12 @@ int moe_quantize_fp8(const void *w, moe_dtype dtype, long long rows, int cols, l
  * Supported: K a multiple of 16, up to 131072; T up to 4194304; N up to
  * 1048576, any number of either.  x and w start on 16-byte boundaries and
  * their strides are multiples of 16; the others are aligned to their elements.
- * Asynchronous on cuda_stream; the result does not depend on what else runs.
- * T == 0 is a no-op returning MOE_OK.
+ * Asynchronous on cuda_stream; the same inputs give the same bits (sums are
+ * added in a fixed order).  T == 0 is a no-op returning MOE_OK.
+ * A bounded wait in the kernel that runs out leaves out unspecified and
+ * records MOE_ERR_DEVICE_TIMEOUT in the status word of the calls without a
+ * handle (moe_noalloc_status).  The first call on a device looks that word up,
+ * so make it before any stream capture.
  * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, CUDA.
  */
 int moe_matmul_fp8(const uint8_t *x, const float *x_scales, int T, long long x_stride,
