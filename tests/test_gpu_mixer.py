@@ -452,6 +452,17 @@ def test_other_stream(dev):
     assert all(torch.equal(u, v) for u, v in zip(cap, ref))
 
 
+@pytest.mark.parametrize("lens", [(37, 0, 130, 5), (1,), (200, 64, 63)])
+def test_example_layer(dev, lens):
+    """The example's decoding in a graph against one pass.  Codes of nearly
+    equal rows differ by at most the rounding of both: rms 2^-4 / sqrt(3)
+    each, 5e-2 together; the states see bf16 roundings of k and v, 2^-8 each."""
+    from examples import hybrid_layer
+    diff, sdiff, last = hybrid_layer.run(lens, new=4, device=dev)
+    assert diff <= 5e-2 and sdiff <= 2.0 ** -7
+    assert last.shape == (len(lens), 512) and torch.isfinite(last).all()
+
+
 def test_binding_refusals(dev):
     x = torch.zeros(4, 64, dtype=BF16, device=dev)
     w = torch.ones(64, dtype=BF16, device=dev)
