@@ -83,7 +83,7 @@ int gdn_scan(const void *q, const void *k, const void *v, const float *alpha, co
  *   workspace device memory of at least the bytes gdn_decay_workspace gives
  *             for the same sizes, 16-byte aligned, used by the call's kernels
  *             alone; NULL where that is 0.
- * Sequences of up to 8 tokens take the recurrent form (fp32 arithmetic), longer
+ * Sequences of up to 16 tokens take the recurrent form (fp32 arithmetic), longer
  * ones the chunked form on the tensor cores: the state is kept and updated in
  * fp32 there too (its error stays that of fp32 arithmetic); for the outputs
  * alone, state and scores are rounded to bf16 before their products.

@@ -3,11 +3,17 @@
 // its decay:
 //     S <- lambda S + v_t k_t^T,   o_t = S q_t
 //
-// The recurrent form (single tokens): rows of S are independent, so a warp
-// holds a few of them in registers, a row spread over d_k / 4 lanes, for the
-// whole call; each token costs one decay and write (2 operations an element)
-// and one dot product per row.  One token per sequence reads and writes the
-// state once and little else, so it is bound by memory.
+// The recurrent form (up to kRecur tokens): rows of S are independent, so a
+// warp holds eight of them (d_k = 128; sixteen of 64) in registers for the
+// whole call, a row spread over d_k / 4 lanes; each token costs one decay and
+// write (2 operations an element) and one dot product per row.  One token per
+// sequence reads and writes the state once and little else, so it is bound by
+// memory: 64 sequences of 32 heads of 128 x 128 take 41.3 us (6.5 TB/s, 97 % of
+// a plain copy's rate), one sequence 2.2 us.  With more tokens the dot
+// products' sums count: the lanes trade rows while they add (9 shuffles for 8
+// rows, where a tree per row takes 40), and the next token is fetched ahead:
+// 8 tokens of 64 sequences 113 -> 73 us.  Four rows a lane are as fast for
+// single tokens and slower after (84 us), as fewer products share q and k.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -22,22 +28,57 @@ namespace moe {
 
 namespace {
 
-__device__ __forceinline__ float4 ld_bf16x4(const __nv_bfloat16 *p) {
-  const uint2 u = *reinterpret_cast<const uint2 *>(p);
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-}
+constexpr int kRecWarps = 4, kR = 8;  // warps of a CTA, rows of a lane
 
-constexpr int kRecWarps = 4;
+// kN bf16 values (4 or 8) by one load
+template <int kN>
+struct Bf16Vec {
+  uint32_t w[kN / 2];
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+    if constexpr (kN == 8) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(p);
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2 *>(p);
+      w[0] = u.x, w[1] = u.y;
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+  }
+};
+
+// Sums of kR values over kLpr neighbouring lanes: halves of the lanes trade
+// halves of the values until each has one, then add up what is left.  Lane c
+// of the kLpr ends with the sum of value c / (kLpr / kR).
+template <int kLpr>
+__device__ __forceinline__ float sum_rows(float (&d)[kR], int c) {
+  int n = kR;
+#pragma unroll
+  for (int m = kLpr / 2; m; m >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool up = c & m;
+#pragma unroll
+      for (int r = 0; r < kR / 2; ++r) {
+        if (r >= n) break;
+        const float give = up ? d[r] : d[r + n], keep = up ? d[r + n] : d[r];
+        d[r] = keep + __shfl_xor_sync(0xffffffffu, give, m);
+      }
+    } else {
+      d[0] += __shfl_xor_sync(0xffffffffu, d[0], m);
+    }
+  }
+  return d[0];
+}
 
 }  // namespace
 
 // One CTA: kRecWarps * kR * (128 / kDk) rows of one (sequence, value head).
-template <int kDk, int kR>
+template <int kDk>
 __global__ void __launch_bounds__(kRecWarps * 32) decay_recurrent_kernel(const DecayArgs a) {
-  constexpr int kLpr = kDk / 4;          // lanes per row
-  constexpr int kRpl = 32 / kLpr;        // rows per warp-wide load
-  constexpr int kRowsWarp = kR * kRpl;   // rows of a warp
+  constexpr int kLpr = kDk / 4;               // lanes per row
+  constexpr int kRowsWarp = kR * (32 / kLpr);  // rows of a warp
   constexpr int kRows = kRecWarps * kRowsWarp;
   const int tiles = (a.dv + kRows - 1) / kRows;
   if (a.table && blockIdx.x == gridDim.x - 1) {  // one block more: the chunked kernels' segments
@@ -47,62 +88,66 @@ __global__ void __launch_bounds__(kRecWarps * 32) decay_recurrent_kernel(const D
   const int tile = blockIdx.x % tiles;
   const int sh = blockIdx.x / tiles, h = sh % a.Hv, seq = sh / a.Hv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % kLpr;
-  const int j0 = tile * kRows + warp * kRowsWarp + lane / kLpr;  // this lane's rows: j0 + r kRpl
-  if (j0 - lane / kLpr >= a.dv) return;
+  // this lane's rows: j .. j + kR - 1, all of them below d_v or none (d_v is a
+  // multiple of 16, as are a warp's rows or they divide it)
+  const int j = tile * kRows + warp * kRowsWarp + lane / kLpr * kR;
+  if (j - lane / kLpr * kR >= a.dv) return;
   long long first, len;
   seq_range(a, seq, first, len);
   if (len > a.recur) return;  // the chunked kernels take it
-  const long long sbase = (static_cast<long long>(seq) * a.Hv + h) * a.dv * kDk + 4 * c;
+  const long long sbase = ((static_cast<long long>(seq) * a.Hv + h) * a.dv + j) * kDk + 4 * c;
   float4 S[kR];
 #pragma unroll
-  for (int r = 0; r < kR; ++r) {
-    const int j = j0 + r * kRpl;
-    S[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (a.s_in && j < a.dv)
-      S[r] = *reinterpret_cast<const float4 *>(a.s_in + sbase + static_cast<long long>(j) * kDk);
-  }
+  for (int r = 0; r < kR; ++r)
+    S[r] = a.s_in ? *reinterpret_cast<const float4 *>(a.s_in + sbase + r * kDk) : make_float4(0.f, 0.f, 0.f, 0.f);
   const float lam = a.decay[h];
   const int hk = h / (a.Hv / a.Hk);
-  for (long long t = first; t < first + len; ++t) {
-    const float4 q = ld_bf16x4(a.q + t * a.q_stride + hk * kDk + 4 * c);
-    const float4 k = ld_bf16x4(a.k + t * a.k_stride + hk * kDk + 4 * c);
+  const __nv_bfloat16 *qp = a.q + first * a.q_stride + hk * kDk + 4 * c;
+  const __nv_bfloat16 *kp = a.k + first * a.k_stride + hk * kDk + 4 * c;
+  const __nv_bfloat16 *vp = a.v + first * a.v_stride + h * a.dv + j;
+  __nv_bfloat16 *op = a.o + (first * a.Hv + h) * a.dv + j + c / (kLpr / kR);
+  Bf16Vec<4> q, k;
+  Bf16Vec<kR> v;
+  auto fetch = [&] {
+    q.load(qp);
+    k.load(kp);
+    v.load(vp);
+    qp += a.q_stride;
+    kp += a.k_stride;
+    vp += a.v_stride;
+  };
+  if (len > 0) fetch();
+  for (int t = 0; t < static_cast<int>(len); ++t) {
+    const Bf16Vec<4> qt = q, kt = k;
+    const Bf16Vec<kR> vt = v;
+    if (t + 1 < len) fetch();
     float d[kR];
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      const int j = j0 + r * kRpl;
-      const float v = j < a.dv ? __bfloat162float(a.v[t * a.v_stride + h * a.dv + j]) : 0.0f;
-      S[r].x = fmaf(lam, S[r].x, v * k.x);
-      S[r].y = fmaf(lam, S[r].y, v * k.y);
-      S[r].z = fmaf(lam, S[r].z, v * k.z);
-      S[r].w = fmaf(lam, S[r].w, v * k.w);
-      d[r] = S[r].x * q.x + S[r].y * q.y + S[r].z * q.z + S[r].w * q.w;
+      S[r].x = fmaf(lam, S[r].x, vt.at(r) * kt.at(0));
+      S[r].y = fmaf(lam, S[r].y, vt.at(r) * kt.at(1));
+      S[r].z = fmaf(lam, S[r].z, vt.at(r) * kt.at(2));
+      S[r].w = fmaf(lam, S[r].w, vt.at(r) * kt.at(3));
+      d[r] = S[r].x * qt.at(0) + S[r].y * qt.at(1) + S[r].z * qt.at(2) + S[r].w * qt.at(3);
     }
-#pragma unroll
-    for (int r = 0; r < kR; ++r) {
-#pragma unroll
-      for (int m = kLpr / 2; m; m >>= 1) d[r] += __shfl_xor_sync(0xffffffffu, d[r], m);
-      const int j = j0 + r * kRpl;
-      if (c == 0 && j < a.dv)
-        a.o[(t * a.Hv + h) * a.dv + j] = __float2bfloat16_rn(d[r]);
-    }
+    const float o = sum_rows<kLpr>(d, c);
+    if (c % (kLpr / kR) == 0) *op = __float2bfloat16_rn(o);
+    op += static_cast<long long>(a.Hv) * a.dv;
   }
   if (a.s_out) {
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      const int j = j0 + r * kRpl;
-      if (j < a.dv)
-        *reinterpret_cast<float4 *>(a.s_out + sbase + static_cast<long long>(j) * kDk) = S[r];
-    }
+    for (int r = 0; r < kR; ++r) *reinterpret_cast<float4 *>(a.s_out + sbase + r * kDk) = S[r];
   }
 }
 
 namespace {
 
-template <int kDk, int kR>
+template <int kDk>
 cudaError_t launch_recurrent(const DecayArgs &a, cudaStream_t st) {
   constexpr int kRows = kRecWarps * kR * (128 / kDk);
   const int tiles = (a.dv + kRows - 1) / kRows;
-  decay_recurrent_kernel<kDk, kR><<<static_cast<unsigned>(a.n_seq) * a.Hv * tiles + (a.table ? 1 : 0), kRecWarps * 32, 0, st>>>(a);
+  const unsigned blocks = static_cast<unsigned>(a.n_seq) * a.Hv * tiles + (a.table ? 1 : 0);
+  decay_recurrent_kernel<kDk><<<blocks, kRecWarps * 32, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -114,8 +159,13 @@ using namespace moe;
 
 namespace {
 
-// Longest sequence that takes the recurrent form.
-constexpr long long kRecur = 8;
+// Longest sequence that takes the recurrent form.  Its time grows with the
+// tokens, a chunk's does not (32 heads of 128 x 128; recurrent / chunked, us):
+//   tokens   1 sequence   4          16          64
+//   12       5.2 / 8.5    9.2 / 10.5 24.4 / 38.0  93 / 134
+//   16       6.2 / 8.5   10.9 / 10.5 30.3 / 38.0 112 / 133
+//   24       8.2 / 8.5   14.5 / 10.5 42.6 / 38.2 156 / 134
+constexpr long long kRecur = 16;
 constexpr long long kGpuSms = 152;
 
 // How a call is cut: the sequences that are not recurrent, their segments.
@@ -272,7 +322,7 @@ extern "C" int gdn_decay_scan(const void *q, const void *k, const void *v, const
   a.status = dev.status;
   cudaError_t e = cudaSuccess;
   if (plan.recurrent)
-    e = d_k == 128 ? launch_recurrent<128, 8>(a, st) : launch_recurrent<64, 8>(a, st);
+    e = d_k == 128 ? launch_recurrent<128>(a, st) : launch_recurrent<64>(a, st);
   if (e == cudaSuccess && plan.chunked) {
     const uint64_t kw = static_cast<uint64_t>(n_k_heads) * d_k, vw = static_cast<uint64_t>(n_v_heads) * d_v;
     CUtensorMap mq, mk, mv, mo;
