@@ -184,9 +184,12 @@ size_t workspace_bytes_of(const Plan &p, int n_v_heads, int d_k, int d_v) {
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
 // Chunks per segment, by the time of the kernels in units of one chunk of the
-// main kernel (1.4 us): a CTA takes its segment's chunks and 3.2 more to start
-// and end; with more than one segment per sequence the first launch (0.42 per
-// chunk and 2) and the chain (2.5, and its traffic) come before.  With offsets
+// main kernel (1.4 us): a CTA takes its segment's chunks and 3 more to start
+// and end; with more than one segment per sequence the first launch (0.52 per
+// chunk and 4) and the chain (3.5, its steps and its traffic) come before.  The
+// constants were fitted to the times of 1 to 32 segments at 43 sizes (1 to 8
+// sequences of 256 to 32,768 tokens, 2 to 64 heads): the choice is within 12 %
+// of the best in each, within 1 % in 36.  With offsets
 // the lengths are not known here: a segment is as long as for one sequence of
 // all tokens, but at least 64 chunks and an SM's share of all the work, so that
 // only a sequence that would outlast the rest of its batch is cut (nine of 0 to
@@ -200,16 +203,16 @@ Plan make_plan(bool ragged, long long n_tokens, long long n_seq, long long heads
   if (!p.chunked) return p;
   const long long chunks = ceil_div(len, kChunkTok);
   const long long share = ceil_div(chunks * heads, kGpuSms);
-  const long long least = !ragged ? 4 : share > 64 ? share : 64;
+  const long long least = !ragged ? 1 : share > 64 ? share : 64;
   double best = 0;
   for (long long n = 1; n <= 256 && n <= chunks; ++n) {
     const long long lc = ceil_div(chunks, n);
     if (n > 1 && lc < least) break;
     const long long ns = ceil_div(chunks, lc);
-    double t = static_cast<double>(ceil_div(ns * seqs * heads, kGpuSms)) * (lc + 3.2);
+    double t = static_cast<double>(ceil_div(ns * seqs * heads, kGpuSms)) * (lc + 3);
     if (ns > 1)
-      t += static_cast<double>(ceil_div((ns - 1) * seqs * heads, kGpuSms)) * (0.42 * lc + 2) + 2.5 +
-           0.01 * (ns - 1) * seqs * heads;
+      t += static_cast<double>(ceil_div((ns - 1) * seqs * heads, kGpuSms)) * (0.52 * lc + 4) + 3.5 +
+           0.1 * ns + 0.015 * (ns - 1) * seqs * heads;
     if (n == 1 || t < best) {
       best = t;
       p.seg_len = lc * kChunkTok;

@@ -279,21 +279,18 @@ __device__ __forceinline__ void load_rows(float (&v)[kN], uint32_t tile, const f
                                           int rows) {
   constexpr int kP = kN / 4;
   const int lane = threadIdx.x & 31;
-#pragma unroll 1
-  for (int i0 = 0; i0 < kP; i0 += 8) {
-    uint4 u[8];
+  uint4 u[kP];  // (all of them in flight at once)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = ((i0 + i) * 32 + lane) / kP, p = ((i0 + i) * 32 + lane) % kP;
-      u[i] = make_uint4(0, 0, 0, 0);
-      if (src && r < rows)
-        u[i] = *reinterpret_cast<const uint4 *>(src + static_cast<long long>(r) * pitch + 4 * p);
-    }
+  for (int i = 0; i < kP; ++i) {
+    const int r = (i * 32 + lane) / kP, p = (i * 32 + lane) % kP;
+    u[i] = make_uint4(0, 0, 0, 0);
+    if (src && r < rows)
+      u[i] = *reinterpret_cast<const uint4 *>(src + static_cast<long long>(r) * pitch + 4 * p);
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = ((i0 + i) * 32 + lane) / kP, p = ((i0 + i) * 32 + lane) % kP;
-      sts128(tile + (r * kP + (p ^ (r & (kP - 1)))) * 16, u[i].x, u[i].y, u[i].z, u[i].w);
-    }
+  for (int i = 0; i < kP; ++i) {
+    const int r = (i * 32 + lane) / kP, p = (i * 32 + lane) % kP;
+    sts128(tile + (r * kP + (p ^ (r & (kP - 1)))) * 16, u[i].x, u[i].y, u[i].z, u[i].w);
   }
   __syncwarp();
 #pragma unroll
@@ -534,38 +531,6 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3;
   const int ht = static_cast<int>(blockIdx.x % (a.Hv * a.tiles));
   const int h = ht / a.tiles, d0 = ht % a.tiles * 128;
-  pdl_wait();
-  pdl_launch_dependents();
-  const int item = static_cast<int>(blockIdx.x) / (a.Hv * a.tiles);
-  const Segment g = find_segment(a, item);
-  if (g.seq < 0 || (!kOut && (g.last || item + 1 >= a.items))) return;
-  const int nc = static_cast<int>((g.len + kC - 1) / kC);
-  const float lam = a.decay[h];
-  if (threadIdx.x <= kC) {
-    const float p = decay_pow(lam, static_cast<float>(threadIdx.x));
-    ctl.tab[threadIdx.x] = p;
-    if (kOut && threadIdx.x < kC)
-      for (int m = 0; m < 2; ++m) {
-        ctl.rtab[m][m + kC - 1 - threadIdx.x] = p;
-        ctl.rtab[m][m + kC + threadIdx.x] = 0.0f;
-      }
-  }
-  const uint32_t stages = smem_u32(smem);
-  // (one thread) the copies of chunk c
-  auto load = [&](int c) {
-    const uint64_t pol = policy_evict_last();
-    const int s = c % kStg, hk = h / (a.Hv / a.Hk);
-    const uint32_t dst = stages + s * L::kStage, fb = full0 + 8 * s;
-    const int y = static_cast<int>(g.first) + c * kC;
-    mbar_arrive_expect_tx(fb, L::kStage);
-    for (int b = 0; b < kDk / 64; ++b) {
-      tma_load_2d(dst + L::kQ + b * kBlk, &tmK, fb, hk * kDk + 64 * b, y, pol);
-      if (kOut) tma_load_2d(dst + b * kBlk, &tmQ, fb, hk * kDk + 64 * b, y, pol);
-    }
-    for (int b = 0; b < 2; ++b)
-      tma_load_2d(dst + L::kQ + L::kK + b * kBlk, &tmV, fb, h * a.dv + d0 + 64 * b, y, pol);
-  };
-  constexpr int kFirst = kStg - 2;  // chunks whose copies start before the CTA is set up
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStg; ++s) {
       mbar_init(full0 + 8 * s, 1);
@@ -585,7 +550,41 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
     }
     ctl.abort_flag = 0;
     fence_mbar_init();
+  }
+  const int item = static_cast<int>(blockIdx.x) / (a.Hv * a.tiles);
+  Segment g;
+  if (!a.table) g = find_segment(a, item);
+  pdl_wait();  // (all above, while the kernel before this one ends)
+  pdl_launch_dependents();
+  if (a.table) g = find_segment(a, item);
+  if (g.seq < 0 || (!kOut && (g.last || item + 1 >= a.items))) return;
+  const int nc = static_cast<int>((g.len + kC - 1) / kC);
+  const uint32_t stages = smem_u32(smem);
+  // (one thread) the copies of chunk c
+  auto load = [&](int c) {
+    const uint64_t pol = policy_evict_last();
+    const int s = c % kStg, hk = h / (a.Hv / a.Hk);
+    const uint32_t dst = stages + s * L::kStage, fb = full0 + 8 * s;
+    const int y = static_cast<int>(g.first) + c * kC;
+    mbar_arrive_expect_tx(fb, L::kStage);
+    for (int b = 0; b < kDk / 64; ++b) {
+      tma_load_2d(dst + L::kQ + b * kBlk, &tmK, fb, hk * kDk + 64 * b, y, pol);
+      if (kOut) tma_load_2d(dst + b * kBlk, &tmQ, fb, hk * kDk + 64 * b, y, pol);
+    }
+    for (int b = 0; b < 2; ++b)
+      tma_load_2d(dst + L::kQ + L::kK + b * kBlk, &tmV, fb, h * a.dv + d0 + 64 * b, y, pol);
+  };
+  constexpr int kFirst = kStg - 2;  // chunks whose copies start before the CTA is set up
+  if (threadIdx.x == 0)
     for (int c = 0; c < nc && c < kFirst; ++c) load(c);
+  if (const int t = static_cast<int>(threadIdx.x) - 64; t >= 0 && t <= kC) {
+    const float p = decay_pow(a.decay[h], static_cast<float>(t));
+    ctl.tab[t] = p;
+    if (kOut && t < kC)
+      for (int m = 0; m < 2; ++m) {
+        ctl.rtab[m][m + kC - 1 - t] = p;
+        ctl.rtab[m][m + kC + t] = 0.0f;
+      }
   }
   // the state's warps fetch its rows meanwhile
   const int half = (warp - kState) >> 2;
