@@ -237,8 +237,9 @@ def moe_decode_noalloc(cfg: moe_config, x, out, stream=None) -> int:
 
 
 def moe_noalloc_status(stream=None) -> tuple[int, int]:
-    """(code, detail) of moe_decode_noalloc's device status word on the current
-    device; synchronises the stream and clears the word."""
+    """(code, detail) of the device status word of the calls without a handle
+    (moe_decode_noalloc, moe_matmul_fp8, gdn_decay_scan) on the current device;
+    synchronises the stream and clears the word."""
     detail = ctypes.c_int(0)
     rc = lib().moe_noalloc_status(_stream(stream), ctypes.byref(detail))
     return rc, detail.value

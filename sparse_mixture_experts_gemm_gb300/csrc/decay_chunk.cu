@@ -22,12 +22,14 @@
 // multiplied smallest first, each chunk's U starts from zero in TMEM, and the
 // state lives in registers, where lambda^C S + U is one fp32 fused
 // multiply-add per element: tensor-core accumulation truncates, and adding
-// chunk after chunk into one accumulator drifted to several 1e-6 of the state.  The outputs are
-// rounded to bf16 (rms 1.7e-3) in the end; S (state's part of an output) and P
-// (the chunk's own part) enter their products as bf16, as large a rounding
-// each on its part, so that an output's rms error is sqrt(2) times that of the
-// last rounding alone.  A second bf16 part for S or P takes that away and was
-// measured at 15 % of the kernel's time each.
+// chunk after chunk into one accumulator drifted to several 1e-6 of the state
+// (now 3e-7 to 9e-7, as fp32 arithmetic in torch).  The outputs are rounded to
+// bf16 (rms 1.7e-3) in the end; S (the state's part of an output) and P (the
+// chunk's own part) enter their products as bf16, as large a rounding each on
+// its part, so that an output's rms error is sqrt(2) times that of the last
+// rounding alone (2.35e-3).  Two bf16 parts of S and of P take that away; an
+// earlier form of this kernel had them, and without them (and with a transposed
+// output tile) a 4,096-token call went from 67 to 63 us.
 //
 // Work split.  One CTA scans one segment of one (sequence, value head, 128
 // columns of d_v).  A sequence is one segment when the batch has enough heads
@@ -45,6 +47,14 @@
 // resource (an M = 128, N = 64 product reads 6 KB in its 48 cycles, all of the
 // 128 bytes a cycle): operands that threads make go to TMEM where the MMA can
 // take them from there (V~, S), and the scores use 64 rows.
+//
+// Measured, 32 value heads on 16 key heads of 128 x 128: 50.7 us for 4,096
+// tokens (segments 20, chain 5, main 33, their starts overlapped; one CTA per
+// head without segments 95), 272 to 290 us for 32,768 (2.8 TB/s of q, k, v, o).
+// A chunk of the main launch takes 1.4 us, 2,650 cycles, for products of 1,984
+// cycles: its time is the chain V~ -> U -> the TMEM columns of V~ free again,
+// V~'s warps sharing their schedulers with the state's and P's.  A CTA's start
+// and end cost 3 chunks more, and an SM has room for one CTA only.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

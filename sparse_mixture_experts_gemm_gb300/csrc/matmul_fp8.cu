@@ -16,6 +16,11 @@
 //     the two-CTA MMA, each CTA holding its 128 tokens' accumulator twice
 //     (512 TMEM columns), so that one tile is drained while the next is
 //     multiplied.
+// Measured (calls back to back in a graph, weights from DRAM): one token x 8192
+// x 2048 6.9 us (2.5 for its weights at a copy's rate; the rest is the start,
+// the sums' exchange and the end), 16 x 2048 x 4096 6.0 us, 301 x 2500 x 2048
+// 9.8 us, 4096 x 8192 x 2048 40.9 us (3.4 PFLOP/s; tensor pipes busy 82 % of an
+// SM's cycles), 16384 x 8192 x 2048 152 us (3.3 PFLOP/s, at the power limit).
 // Every wait is bounded; one that runs out raises the CTA's abort flag and
 // records a timeout in the status word of the calls without a handle.
 #include <cuda_bf16.h>

@@ -243,7 +243,8 @@ cudaError_t launch_norm(const NormArgs &a, cudaStream_t st) {
 // depends neither on where its tensors lie nor on how many rows there are.  Two
 // to four vectors per thread (with a residual and codes, 16,384 rows of 2,048
 // bf16 timed one call at a time: 42.4 us with 64 threads of 4, 42.6 with 128 of
-// 2, 48.9 with 256 of 1; back to back 37.6 us, 6.2 TB/s; one row: 5.5 us each).
+// 2, 48.9 with 256 of 1; back to back 37.6 us, 6.2 TB/s; one row: 5.5 us each,
+// 2.0 in a graph).
 // Blocks that stay and take several rows, loading ahead, were slower (67 us).
 template <typename T>
 cudaError_t pick_norm(const NormArgs &a, cudaStream_t st) {
