@@ -8,8 +8,8 @@
 // whole call, a row spread over d_k / 4 lanes; each token costs one decay and
 // write (2 operations an element) and one dot product per row.  One token per
 // sequence reads and writes the state once and little else, so it is bound by
-// memory: 64 sequences of 32 heads of 128 x 128 take 41.3 us (6.5 TB/s, 97 % of
-// a plain copy's rate), one sequence 2.2 us.  With more tokens the dot
+// memory: 64 sequences of 32 heads of 128 x 128 take 40.8 us (6.6 TB/s, a
+// plain copy's rate), one sequence 2.0 us.  With more tokens the dot
 // products' sums count: the lanes trade rows while they add (9 shuffles for 8
 // rows, where a tree per row takes 40), and the next token is fetched ahead:
 // 8 tokens of 64 sequences 113 -> 73 us.  Four rows a lane are as fast for
@@ -81,6 +81,8 @@ __global__ void __launch_bounds__(kRecWarps * 32) decay_recurrent_kernel(const D
   constexpr int kRowsWarp = kR * (32 / kLpr);  // rows of a warp
   constexpr int kRows = kRecWarps * kRowsWarp;
   const int tiles = (a.dv + kRows - 1) / kRows;
+  pdl_wait();
+  pdl_launch_dependents();
   if (a.table && blockIdx.x == gridDim.x - 1) {  // one block more: the chunked kernels' segments
     make_table(a);
     return;
@@ -147,8 +149,7 @@ cudaError_t launch_recurrent(const DecayArgs &a, cudaStream_t st) {
   constexpr int kRows = kRecWarps * kR * (128 / kDk);
   const int tiles = (a.dv + kRows - 1) / kRows;
   const unsigned blocks = static_cast<unsigned>(a.n_seq) * a.Hv * tiles + (a.table ? 1 : 0);
-  decay_recurrent_kernel<kDk><<<blocks, kRecWarps * 32, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(decay_recurrent_kernel<kDk>, blocks, kRecWarps * 32, 0, st, a);
 }
 
 }  // namespace
@@ -162,9 +163,9 @@ namespace {
 // Longest sequence that takes the recurrent form.  Its time grows with the
 // tokens, a chunk's does not (32 heads of 128 x 128; recurrent / chunked, us):
 //   tokens   1 sequence   4          16          64
-//   12       5.2 / 8.5    9.2 / 10.5 24.4 / 38.0  93 / 134
-//   16       6.2 / 8.5   10.9 / 10.5 30.3 / 38.0 112 / 133
-//   24       8.2 / 8.5   14.5 / 10.5 42.6 / 38.2 156 / 134
+//   12       4.7 / 7.5    8.6 / 9.6  23.8 / 36    92 / 125
+//   16       5.8 / 7.5   10.4 / 9.6  29.7 / 36   111 / 125
+//   24       8.2 / 7.6   14.5 / 9.7  42.6 / 36   156 / 126
 constexpr long long kRecur = 16;
 constexpr long long kGpuSms = 152;
 

@@ -126,6 +126,23 @@ __device__ __forceinline__ float decay_pow(float lam, float n) {
   return n == 0.0f ? 1.0f : lam == 0.0f ? 0.0f : exp2f(n * log2f(lam));
 }
 
+// Launch of a kernel that may start while the one before it ends (it waits for
+// that one's results itself)
+template <typename K, typename... Args>
+cudaError_t launch_pdl(K kern, long long grid, int threads, int smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // decay_chunk.cu
 bool decay_chunk_setup();  // shared-memory attributes; once per device
 cudaError_t launch_decay_chunked(const DecayArgs &a, int dk, const CUtensorMap &mq,
