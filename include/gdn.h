@@ -86,7 +86,8 @@ int gdn_scan(const void *q, const void *k, const void *v, const float *alpha, co
  * Sequences of up to 16 tokens take the recurrent form (fp32 arithmetic), longer
  * ones the chunked form on the tensor cores: the state is kept and updated in
  * fp32 there too (its error stays that of fp32 arithmetic); for the outputs
- * alone, state and scores are rounded to bf16 before their products.
+ * alone, state and scores are rounded to bf16 before their products (within 2^-8
+ * of each term, so that an output whose terms cancel has lost as much).
  * A long sequence may be taken in pieces, passing the state along; pieces
  * agree with one call up to these roundings.  The same inputs give the same
  * bits.  NaN and infinities of one sequence reach no other.  The caller applies the model's

@@ -149,7 +149,7 @@ cudaError_t launch_recurrent(const DecayArgs &a, cudaStream_t st) {
   constexpr int kRows = kRecWarps * kR * (128 / kDk);
   const int tiles = (a.dv + kRows - 1) / kRows;
   const unsigned blocks = static_cast<unsigned>(a.n_seq) * a.Hv * tiles + (a.table ? 1 : 0);
-  return launch_pdl(decay_recurrent_kernel<kDk>, blocks, kRecWarps * 32, 0, st, a);
+  return launch_pdl(decay_recurrent_kernel<kDk>, grid_of(blocks), kRecWarps * 32, 0, st, a);
 }
 
 }  // namespace
@@ -167,44 +167,56 @@ namespace {
 //   16       5.8 / 7.5   10.4 / 9.6  29.7 / 36   111 / 125
 //   24       8.2 / 7.6   14.5 / 9.7  42.6 / 36   156 / 126
 constexpr long long kRecur = 16;
-constexpr long long kGpuSms = 152;
 
 // How a call is cut: the sequences that are not recurrent, their segments.
 struct Plan {
   bool recurrent, chunked, segmented;
+  // without offsets: rows of chunks on a line cut into shares
+  long long rows, chunks, pitch, width, shares;
+  // with offsets
   long long seg_len, items;
-  long long slots;  // states in the workspace
   long long table;  // bytes of the table of segments, at the workspace's start
+  long long slots;  // states in the workspace
 };
 
 // bytes of a call's workspace
-size_t workspace_bytes_of(const Plan &p, int n_v_heads, int d_k, int d_v) {
-  return static_cast<size_t>(p.table) + static_cast<size_t>(p.slots) * n_v_heads * d_v * d_k * sizeof(float);
+size_t workspace_bytes_of(const Plan &p, int d_k) {
+  return static_cast<size_t>(p.table) + static_cast<size_t>(p.slots) * 128 * d_k * sizeof(float);
 }
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
-// Chunks per segment, by the time of the kernels in units of one chunk of the
-// main kernel (1.4 us): a CTA takes its segment's chunks and 3 more to start
-// and end; with more than one segment per sequence the first launch (0.52 per
-// chunk and 4) and the chain (3.5, its steps and its traffic) come before.  The
-// constants were fitted to the times of 1 to 32 segments at 43 sizes (1 to 8
-// sequences of 256 to 32,768 tokens, 2 to 64 heads): the choice is within 12 %
-// of the best in each, within 1 % in 36.  With offsets
-// the lengths are not known here: a segment is as long as for one sequence of
-// all tokens, but at least 64 chunks and an SM's share of all the work, so that
-// only a sequence that would outlast the rest of its batch is cut (nine of 0 to
-// 2,049 tokens: 93 us with the longest two cut in two, 62 us with none).
-Plan make_plan(bool ragged, long long n_tokens, long long n_seq, long long heads) {
+// How the rows are cut, by the time of the kernels in units of one chunk of the
+// main kernel (1.4 us): a CTA takes its chunks and 3 more to start and end; where
+// a sequence has several segments the first launch (0.52 per chunk and 4) and
+// the chain (3.5, its steps and its traffic) come before.  The constants were
+// fitted to the times of 1 to 32 segments at 43 sizes (1 to 8 sequences of 256
+// to 32,768 tokens, 2 to 64 heads).  Two ways to cut are compared: each row
+// into equal segments; and the whole line into one share per SM, whatever row
+// ends inside it.  A share that holds the end of one row and the start of the
+// next is two CTAs: the larger piece starts at once, and the smaller ones,
+// largest first, follow on the SMs whose piece was the smallest, so that each
+// SM gets a share and two CTAs' start at most (counted as 10 here, for 3: with 6
+// shares won by the model where they lose by 1 to 2 %).  In equal segments /
+// in shares: 16,384 tokens x 32 heads 150 / 142 us, 32,768 x 32 272 / 259,
+// 8,192 x 64 157 / 147; 8,192 x 32 83.8 / 84.5, 16,384 x 16 81.5 / 83.5.
+// With offsets the lengths are not known here: a segment is as long as for one
+// sequence of all tokens, but at least 64 chunks and an SM's share of all the
+// work, so that only a sequence that would outlast the rest of its batch is cut
+// (nine of 0 to 2,049 tokens: 93 us with the longest two cut in two, 62 us with
+// none).
+Plan make_plan(bool ragged, long long n_tokens, long long n_seq, long long n_k_heads, long long heads) {
   Plan p = {};
   const long long len = ragged ? n_tokens : n_seq ? n_tokens / n_seq : 0;
   const long long seqs = ragged ? 1 : n_seq;  // of length len at most
   p.chunked = len > kRecur;
   p.recurrent = ragged || !p.chunked;
   if (!p.chunked) return p;
-  const long long chunks = ceil_div(len, kChunkTok);
+  const long long chunks = ceil_div(len, kChunkTok), bundle = heads / n_k_heads;
   const long long share = ceil_div(chunks * heads, kGpuSms);
   const long long least = !ragged ? 1 : share > 64 ? share : 64;
+  p.rows = seqs * n_k_heads;
+  p.chunks = chunks;
   double best = 0;
   for (long long n = 1; n <= 256 && n <= chunks; ++n) {
     const long long lc = ceil_div(chunks, n);
@@ -216,20 +228,55 @@ Plan make_plan(bool ragged, long long n_tokens, long long n_seq, long long heads
            0.1 * ns + 0.015 * (ns - 1) * seqs * heads;
     if (n == 1 || t < best) {
       best = t;
-      p.seg_len = lc * kChunkTok;
+      p.width = lc;
+      p.pitch = ns * lc;
+      p.shares = p.rows * ns;
     }
   }
-  const long long per = ceil_div(len, p.seg_len);
-  p.segmented = per > 1;
+  p.segmented = p.width < chunks;
   if (ragged) {
+    p.seg_len = p.width * kChunkTok;
     const long long longest = n_tokens / (kRecur + 1);
     p.items = n_tokens / p.seg_len + (n_seq < longest ? n_seq : longest);
     p.table = p.items * static_cast<long long>(sizeof(Segment));
-  } else {
-    p.items = n_seq * per;
+    p.slots = p.segmented ? p.items * heads : 0;
+    return p;
   }
-  p.slots = p.segmented ? p.items : 0;
+  if (bundle <= kGpuSms && p.rows <= kGpuSms / bundle) {
+    const long long w = ceil_div(p.rows * chunks, kGpuSms / bundle);
+    const long long shares = ceil_div(p.rows * chunks, w);
+    const double t = (w + 10) + (0.52 * w + 4) + 3.5 + 0.1 * (ceil_div(chunks, w) + 1) + 0.015 * shares * bundle;
+    if (w < chunks && t < best) {
+      p.segmented = true;
+      p.width = w;
+      p.pitch = chunks;
+      p.shares = shares;
+    }
+  }
+  p.slots = p.segmented ? (p.shares + p.rows) * bundle : 0;
   return p;
+}
+
+// The rows whose end lies inside a share that the next row starts in, by the
+// size of the share's smaller piece; returns their number.
+int small_pieces(const Plan &p, uint8_t *order) {
+  long long size[kGpuSms];
+  int n = 0;
+  if (p.rows > kGpuSms || p.pitch % p.width == 0) return 0;
+  for (long long r = 0; r + 1 < p.rows; ++r) {
+    const long long end = (r + 1) * p.pitch, before = end % p.width;
+    if (before == 0) continue;
+    const long long after = p.width - before < p.chunks ? p.width - before : p.chunks;
+    const long long s = before < after ? before : after;
+    int i = n++;
+    for (; i > 0 && size[i - 1] < s; --i) {
+      size[i] = size[i - 1];
+      order[i] = order[i - 1];
+    }
+    size[i] = s;
+    order[i] = static_cast<uint8_t>(r);
+  }
+  return n;
 }
 
 struct DecayDevice {
@@ -257,9 +304,14 @@ extern "C" int gdn_decay_workspace(long long n_tokens, int n_seq, int ragged, in
                                    int d_v, size_t *bytes) {
   if (!bytes || n_tokens < 0 || n_seq < 0 || n_v_heads <= 0 || d_k <= 0 || d_v <= 0)
     return MOE_ERR_INVALID_ARG;
-  const Plan p = make_plan(ragged != 0, n_tokens, n_seq,
-                           static_cast<long long>(n_v_heads) * ceil_div(d_v, 128));
-  *bytes = workspace_bytes_of(p, n_v_heads, d_k, d_v);
+  // (how heads share keys, which the plan looks at, is not asked for here)
+  *bytes = 0;
+  for (int hk = 1; hk <= n_v_heads; ++hk) {
+    if (n_v_heads % hk != 0) continue;
+    const Plan p = make_plan(ragged != 0, n_tokens, n_seq, hk, n_v_heads * ceil_div(d_v, 128));
+    const size_t need = workspace_bytes_of(p, d_k);
+    if (need > *bytes) *bytes = need;
+  }
   return MOE_OK;
 }
 
@@ -292,11 +344,15 @@ extern "C" int gdn_decay_scan(const void *q, const void *k, const void *v, const
     return MOE_ERR_ALIGNMENT;
   DecayArgs a = {};
   a.tiles = (d_v + 127) / 128;
-  const Plan plan =
-      make_plan(offsets != nullptr, n_tokens, n_seq, static_cast<long long>(n_v_heads) * a.tiles);
-  const size_t need = workspace_bytes_of(plan, n_v_heads, d_k, d_v);
+  a.group = n_v_heads / n_k_heads;
+  a.bundle = a.group * a.tiles;
+  const long long heads = static_cast<long long>(n_v_heads) * a.tiles;
+  const Plan plan = make_plan(offsets != nullptr, n_tokens, n_seq, n_k_heads, heads);
+  const size_t need = workspace_bytes_of(plan, d_k);
   if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_INVALID_ARG;
-  if (plan.items * n_v_heads * ceil_div(static_cast<long long>(d_v) * d_k, 1024) > 0x7fffffffLL)
+  // (CTAs of the largest launch; chunks of all rows)
+  if (plan.rows * plan.pitch > 1 << 30) return MOE_ERR_UNSUPPORTED;
+  if (plan.items * heads * 8 > 0x7fffffffLL || (plan.shares + plan.rows * 8) * (heads / n_k_heads) > 0x7fffffffLL)
     return MOE_ERR_UNSUPPORTED;
   const DecayDevice &dev = decay_device();
   if (dev.rc != MOE_OK) return dev.rc;
@@ -321,6 +377,13 @@ extern "C" int gdn_decay_scan(const void *q, const void *k, const void *v, const
   a.seg_len = static_cast<int>(plan.seg_len);
   a.seq_len = static_cast<int>(n_tokens / n_seq);
   a.items = plan.items;
+  if (!offsets && plan.chunked) {
+    a.chunks = static_cast<int>(plan.chunks);
+    a.width = static_cast<int>(plan.width);
+    a.shares = static_cast<int>(plan.shares);
+    a.pitch = static_cast<int>(plan.pitch);
+    a.smalls = small_pieces(plan, a.order);
+  }
   a.table = plan.table ? static_cast<Segment *>(workspace) : nullptr;
   a.ws = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.table);
   a.status = dev.status;

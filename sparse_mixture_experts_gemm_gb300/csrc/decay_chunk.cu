@@ -23,7 +23,10 @@
 // state lives in registers, where lambda^C S + U is one fp32 fused
 // multiply-add per element: tensor-core accumulation truncates, and adding
 // chunk after chunk into one accumulator drifted to several 1e-6 of the state
-// (now 3e-7 to 9e-7, as fp32 arithmetic in torch).  The outputs are rounded to
+// (now 1.3e-7 to 1.4e-7).  One float for lambda^64 would be off
+// by the same part of an ulp at each chunk; the chunks use the floats below and
+// above it in turn, so that their products stay within an ulp of the power (the
+// state's error was up to 1e-6 at 32,768 tokens, where torch has 3e-7 to 5e-7).  The outputs are rounded to
 // bf16 (rms 1.7e-3) in the end; S (the state's part of an output) and P (the
 // chunk's own part) enter their products as bf16, as large a rounding each on
 // its part, so that an output's rms error is sqrt(2) times that of the last
@@ -33,7 +36,8 @@
 //
 // Work split.  One CTA scans one segment of one (sequence, value head, 128
 // columns of d_v).  A sequence is one segment when the batch has enough heads
-// to fill the GPU; otherwise it is cut: a first launch of the same kernel
+// to fill the GPU; otherwise it is cut (equal segments, or all heads' chunks in
+// equal shares, one per SM; make_plan chooses): a first launch of the same kernel
 // without the outputs computes what each segment leaves, a small kernel
 // chains these into the state before each segment, and the main launch runs
 // all segments at once.  Each lets the next one start its CTAs early (they wait
@@ -48,9 +52,10 @@
 // 128 bytes a cycle): operands that threads make go to TMEM where the MMA can
 // take them from there (V~, S), and the scores use 64 rows.
 //
-// Measured, 32 value heads on 16 key heads of 128 x 128: 50.7 us for 4,096
+// Measured, 32 value heads on 16 key heads of 128 x 128: 51.4 us for 4,096
 // tokens (segments 20, chain 5, main 33, their starts overlapped; one CTA per
-// head without segments 95), 272 to 290 us for 32,768 (2.8 TB/s of q, k, v, o).
+// head without segments 95), 258 us for 32,768 (3.1 TB/s of q, k, v, o)
+// in a graph.
 // A chunk of the main launch takes 1.4 us, 2,650 cycles, for products of 1,984
 // cycles: its time is the chain V~ -> U -> the TMEM columns of V~ free again,
 // V~'s warps sharing their schedulers with the state's and P's.  A CTA's start
@@ -463,62 +468,84 @@ struct Ctl {
   // lambda^63 .. lambda^0, then zeros, in copies that start 0 and 1 words late
   alignas(16) float rtab[2][2 * kC + 8];
   float tab[kC + 1];  // lambda^0 .. lambda^64
+  float step[2], frac;  // the floats around lambda^64, its place between them
 };
 static_assert(sizeof(Ctl) <= 2048, "control block");
 
 }  // namespace
 
 // ws: what each segment leaves -> the state before the next segment, in place,
-// along each sequence.  A thread has 4 elements of a (sequence, head) state;
-// without offsets a block's sequence is known, with them a block works if its
-// item is the first segment of several.  Where the final state goes over the
-// initial one, that is copied for the first segment.
-__global__ void __launch_bounds__(512) decay_chain_kernel(const DecayArgs a, int dk) {
-  const int per = a.dv * dk / 4;  // vectors of a state
-  const int blocks = (per + 511) / 512;
-  const int hb = static_cast<int>(blockIdx.x) % (a.Hv * blocks), y = static_cast<int>(blockIdx.x) / (a.Hv * blocks);
-  const int h = hb / blocks, e = hb % blocks * 512 + static_cast<int>(threadIdx.x);
-  pdl_wait();
-  pdl_launch_dependents();
-  int seq = y, n = (a.seq_len + a.seg_len - 1) / a.seg_len - 1;  // states to make
-  long long item = static_cast<long long>(n + 1) * y;            // the first segment's
+// along each sequence.  A thread has 4 elements of the state of a (sequence,
+// head, tile of d_v); with offsets its block works if its item is the first
+// segment of several.  Where the final state goes over the initial one, that is
+// copied for the first segment.
+__global__ void __launch_bounds__(512, 2) decay_chain_kernel(const DecayArgs a, int dk) {
+  const int per = 32 * dk;  // vectors of a tile
+  const int in = blockIdx.y, e = static_cast<int>(blockIdx.z * 512 + threadIdx.x);
+  if (a.table) pdl_wait();
+  int seq, h, d0, n;                // n: states to make
+  long long at, copy, step;         // places in ws: of the first one, of the initial one, between two
+  float first, len;                 // tokens of the first segment, of the others
   if (a.table) {
-    const Segment g = find_segment(a, y);
+    const int item = blockIdx.x;
+    step = a.Hv * a.tiles;
+    const Segment g = a.table[item];
     if (g.seq < 0 || g.index != 0 || g.last) return;
-    long long first, len;
-    seq_range(a, g.seq, first, len);
+    long long lo, tokens;
+    seq_range(a, g.seq, lo, tokens);
+    n = (static_cast<int>(tokens) + a.seg_len - 1) / a.seg_len - 1;
+    if (item + n >= a.items) return;
     seq = g.seq;
-    n = (static_cast<int>(len) + a.seg_len - 1) / a.seg_len - 1;
-    item = y;
+    h = in / a.tiles;
+    d0 = in % a.tiles * 128;
+    copy = item * step + in;
+    at = copy + step;
+    first = len = static_cast<float>(a.seg_len);
+  } else {
+    const int r = blockIdx.x, bundle = a.bundle, sub = in / a.tiles;
+    const int row = r * a.pitch, cut = row / a.width + 1;
+    n = (row + a.chunks - 1) / a.width - cut + 1;
+    seq = r / a.Hk;
+    h = (r - seq * a.Hk) * a.group + sub;
+    d0 = (in - sub * a.tiles) * 128;
+    step = bundle;
+    at = static_cast<long long>(cut) * bundle + in;
+    copy = static_cast<long long>(a.shares + r) * bundle + in;
+    first = static_cast<float>((cut * a.width - row) * kC);
+    len = static_cast<float>(a.width * kC);
   }
-  if (e >= per || item + n >= a.items) return;
-  const float f = decay_pow(a.decay[h], static_cast<float>(a.seg_len));
-  const long long step = static_cast<long long>(a.Hv) * per;
-  float4 *w = reinterpret_cast<float4 *>(a.ws) + (item * a.Hv + h) * per + e;
+  if (!a.table) pdl_wait();
+  pdl_launch_dependents();
+  if (n <= 0 || e >= min(128, a.dv - d0) * dk / 4) return;
+  const float f0 = decay_pow(a.decay[h], first), f = decay_pow(a.decay[h], len);
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (a.s_in) s = reinterpret_cast<const float4 *>(a.s_in)[(static_cast<long long>(seq) * a.Hv + h) * per + e];
+  if (a.s_in)
+    s = reinterpret_cast<const float4 *>(a.s_in + ((static_cast<long long>(seq) * a.Hv + h) * a.dv + d0) * dk)[e];
   const float4 s0 = s;
+  float4 *w = reinterpret_cast<float4 *>(a.ws) + at * per + e;
+  step *= per;
   for (int i0 = 0; i0 < n; i0 += 8) {
-    float4 u[8];
+    float4 v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i0 + i < n) u[i] = w[(i0 + i + 1) * step];
+      if (i0 + i < n) v[i] = w[(i0 + i) * step];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i0 + i < n) {
-        s.x = fmaf(f, s.x, u[i].x);
-        s.y = fmaf(f, s.y, u[i].y);
-        s.z = fmaf(f, s.z, u[i].z);
-        s.w = fmaf(f, s.w, u[i].w);
-        w[(i0 + i + 1) * step] = s;
+        const float g = i0 + i == 0 ? f0 : f;
+        s.x = fmaf(g, s.x, v[i].x);
+        s.y = fmaf(g, s.y, v[i].y);
+        s.z = fmaf(g, s.z, v[i].z);
+        s.w = fmaf(g, s.w, v[i].w);
+        w[(i0 + i) * step] = s;
       }
   }
-  if (a.s_in && a.s_in == a.s_out) *w = s0;
+  if (a.s_in && a.s_in == a.s_out) reinterpret_cast<float4 *>(a.ws)[copy * per + e] = s0;
 }
 
 // kOut: the segment's outputs, from the state before it, and the final state if
 // it is the sequence's last.  Otherwise: what the segment leaves from a zero
-// state, into the next item's place, unless it is the last.
+// state, unless it is the last.
 template <int kDk, bool kOut>
 __global__ void __launch_bounds__(kThreadsC(kOut), 1)
     decay_chunk_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -539,8 +566,6 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
   const uint32_t o_full = bar + 32, drain = bar + 40;
   const uint32_t vt_full0 = bar + 64, u_full0 = bar + 80, u_empty0 = bar + 96, vt_part0 = bar + 112;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wq = warp & 3;
-  const int ht = static_cast<int>(blockIdx.x % (a.Hv * a.tiles));
-  const int h = ht / a.tiles, d0 = ht % a.tiles * 128;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStg; ++s) {
       mbar_init(full0 + 8 * s, 1);
@@ -561,13 +586,13 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
     ctl.abort_flag = 0;
     fence_mbar_init();
   }
-  const int item = static_cast<int>(blockIdx.x) / (a.Hv * a.tiles);
-  Segment g;
-  if (!a.table) g = find_segment(a, item);
+  Piece g;
+  if (!a.table) g = find_piece<kOut>(a, static_cast<int>(blockIdx.x));
   pdl_wait();  // (all above, while the kernel before this one ends)
   pdl_launch_dependents();
-  if (a.table) g = find_segment(a, item);
-  if (g.seq < 0 || (!kOut && (g.last || item + 1 >= a.items))) return;
+  if (a.table) g = find_piece<kOut>(a, static_cast<int>(blockIdx.x));
+  if (g.seq < 0) return;
+  const int h = g.h, d0 = g.d0;
   const int nc = static_cast<int>((g.len + kC - 1) / kC);
   const uint32_t stages = smem_u32(smem);
   // (one thread) the copies of chunk c
@@ -595,6 +620,19 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
         ctl.rtab[m][m + kC - 1 - t] = p;
         ctl.rtab[m][m + kC + t] = 0.0f;
       }
+    if (t == 0) {  // lambda^64 by squaring, as a sum of two floats
+      float near = a.decay[h], off = 0.0f;
+#pragma unroll
+      for (int i = 1; i < kC; i *= 2) {
+        const float sq = near * near, e = fmaf(2.0f * near, off, fmaf(near, near, -sq));
+        near = sq + e;
+        off = e - (near - sq);
+      }
+      const float other = off == 0.0f ? near : __int_as_float(__float_as_int(near) + (off > 0.0f ? 1 : -1));
+      ctl.step[0] = near;
+      ctl.step[1] = other;
+      ctl.frac = off == 0.0f ? 0.0f : __fdividef(off, other - near);
+    }
   }
   // the state's warps fetch its rows meanwhile
   const int half = (warp - kState) >> 2;
@@ -603,8 +641,8 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
   const uint32_t srows = stages + kFirst * L::kStage + (warp - kState) * 32 * kHalfDk * 4;
   // this warp's rows of the state before the segment (null: zeros)
   auto before_rows = [&]() -> const float * {
-    if (g.index == 0 && (!a.s_in || g.last || a.s_in != a.s_out)) return a.s_in ? a.s_in + srow : nullptr;
-    return a.ws + ((static_cast<long long>(item) * a.Hv + h) * a.dv + d0 + wq * 32) * kDk + half * kHalfDk;
+    if (g.from < 0) return a.s_in ? a.s_in + srow : nullptr;
+    return a.ws + (static_cast<long long>(g.from) * 128 + wq * 32) * kDk + half * kHalfDk;
   };
   float S[kHalfDk];
   if (warp >= kState) {
@@ -858,7 +896,8 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
     for (int c = 0; c < nc; ++c) {
       const int n = c == nc - 1 ? tail : kC;
       const int ub = c % M::kBufs, use = c / M::kBufs;
-      const float f = ctl.tab[n];
+      const float turn = fmaf(ctl.frac, static_cast<float>(c), 0.5f);
+      const float f = n < kC ? ctl.tab[n] : ctl.step[floorf(turn + ctl.frac) > floorf(turn)];
       ok = warp_wait(a, u_full0 + 8 * ub, use & 1, abort_flag, SITE_EPI_TMEM_FULL);
       if (!ok) break;
       tc_fence_after();
@@ -921,8 +960,8 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
     float *dst = nullptr;
     if (ok) {
       if (!kOut)
-        dst = a.ws + ((static_cast<long long>(item + 1) * a.Hv + h) * a.dv + d0 + wq * 32) * kDk + half * kHalfDk;
-      else if (g.last && a.s_out)
+        dst = a.ws + (static_cast<long long>(g.to) * 128 + wq * 32) * kDk + half * kHalfDk;
+      else if (g.to < 0 && a.s_out)
         dst = a.s_out + srow;
     }
     // (every product of the CTA that reads the stages is done)
@@ -962,17 +1001,18 @@ template <int kDk>
 cudaError_t launch_chunked(const DecayArgs &a, const CUtensorMap &mq, const CUtensorMap &mk,
                            const CUtensorMap &mv, const CUtensorMap &mo, bool segmented,
                            cudaStream_t st) {
-  const long long per = static_cast<long long>(a.Hv) * a.tiles;
+  const long long per = static_cast<long long>(a.Hv) * a.tiles, bundle = a.bundle;
   if (segmented) {
-    cudaError_t e = launch_pdl(decay_chunk_kernel<kDk, false>, a.items * per, kThreadsC(false),
-                               Smem<kDk, false>::kTotal, st, mq, mk, mv, mo, a);
+    cudaError_t e = launch_pdl(decay_chunk_kernel<kDk, false>, grid_of(a.table ? a.items * per : (a.shares - 1) * bundle),
+                               kThreadsC(false), Smem<kDk, false>::kTotal, st, mq, mk, mv, mo, a);
     if (e != cudaSuccess) return e;
-    const long long blocks = (static_cast<long long>(a.dv) * kDk / 4 + 511) / 512;
-    e = launch_pdl(decay_chain_kernel, (a.table ? a.items : a.n_seq) * a.Hv * blocks, 512, 0, st, a, kDk);
+    const long long rows = static_cast<long long>(a.n_seq) * a.Hk;
+    const dim3 grid(static_cast<unsigned>(a.table ? a.items : rows), static_cast<unsigned>(a.table ? per : bundle), 32 * kDk / 512);
+    e = launch_pdl(decay_chain_kernel, grid, 512, 0, st, a, kDk);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(decay_chunk_kernel<kDk, true>, a.items * per, kThreadsC(true), Smem<kDk, true>::kTotal,
-                    st, mq, mk, mv, mo, a);
+  return launch_pdl(decay_chunk_kernel<kDk, true>, grid_of(a.table ? a.items * per : (a.shares + a.smalls) * bundle),
+                    kThreadsC(true), Smem<kDk, true>::kTotal, st, mq, mk, mv, mo, a);
 }
 
 }  // namespace

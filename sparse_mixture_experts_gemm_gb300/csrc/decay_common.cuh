@@ -9,8 +9,9 @@
 namespace moe {
 
 constexpr int kChunkTok = 64;  // tokens per chunk of the chunked form
+constexpr int kGpuSms = 152;
 
-// One segment of a sequence that takes the chunked form.
+// One segment of a packed sequence that takes the chunked form.
 struct alignas(16) Segment {
   int seq;         // -1: none
   int index;       // its place in the sequence
@@ -28,16 +29,32 @@ struct DecayArgs {
   long long n_tokens, q_stride, k_stride, v_stride;
   int n_seq, Hk, Hv, dv;
   // Sequences of at most `recur` tokens take the recurrent kernel, the others
-  // the chunked ones, in segments of seg_len tokens (a multiple of 64), one per
-  // work item.  ws holds the state before each item's segment, [item][Hv][dv][dk]
-  // (before a sequence's first one only if the state is updated in place, since
-  // the last segment may write it while the first is still to read it).
-  int recur, seg_len, seq_len;  // seq_len: of every sequence without offsets
-  long long items;
+  // the chunked ones.  ws holds the states between segments, 128 x dk each (a
+  // segment belongs to one tile of d_v), and that before a sequence's first
+  // segment if the state is updated in place, since the last segment may write
+  // it while the first is still to read it.
+  int recur, seq_len;  // seq_len: of every sequence without offsets
+  int tiles;           // 128-wide tiles of d_v
+  int group, bundle;   // value heads of a key head, their tiles
   float *ws;
-  Segment *table;  // [items], of a call with offsets (made by its recurrent kernel)
-  int tiles;  // 128-wide tiles of d_v
   int *status;
+  // Without offsets: rows of `chunks` chunks, one per sequence and key head (the
+  // value heads and tiles of a row, its bundle, are cut alike, so that CTAs that
+  // run together read the same q and k), `pitch` chunks apart on a line that is
+  // cut every `width` chunks into `shares`.
+  int chunks, pitch, width, shares, smalls;
+  uint8_t order[kGpuSms];  // rows whose end lies inside a share, by the share's smaller piece
+  // With offsets: segments of seg_len tokens (a multiple of 64).
+  int seg_len;
+  long long items;
+  Segment *table;  // [items], made by the call's recurrent kernel
+};
+
+// What a CTA of the chunked kernels does.
+struct Piece {
+  int seq, h, d0;       // seq < 0: nothing
+  int first, len;       // its tokens
+  int from, to;         // states in ws before and after it; -1: the call's initial, final one
 };
 
 // first token and number of tokens of sequence i; offsets outside
@@ -98,26 +115,68 @@ __device__ __forceinline__ void make_table(const DecayArgs &a) {
   for (long long k = base + threadIdx.x; k < a.items; k += blockDim.x) a.table[k] = none;
 }
 
-// The segment that work item `item` stands for.
-__device__ __forceinline__ Segment find_segment(const DecayArgs &a, int item) {
-  Segment g = {};
+// The piece of CTA `block`: kOut: all of them, the larger one of each share
+// before the smaller ones; otherwise those whose end state another one needs.
+template <bool kOut>
+__device__ __forceinline__ Piece find_piece(const DecayArgs &a, int block) {
+  const bool in_place = a.s_in && a.s_in == a.s_out;
+  Piece p;
+  p.seq = -1;
   if (a.table) {
+    const int per = a.Hv * a.tiles, item = block / per, ht = block % per;
     const int4 u = *reinterpret_cast<const int4 *>(a.table + item);
-    g.seq = u.x;
-    g.index = u.y;
-    g.first = u.z;
-    g.len = u.w;
-    g.last = a.table[item].last;
-  } else {  // (fewer than 2^31 tokens, segments and items)
-    const int n = (a.seq_len + a.seg_len - 1) / a.seg_len, seq = item / n;
-    g.seq = seq < a.n_seq ? seq : -1;
-    g.index = item - seq * n;
-    const int at = g.index * a.seg_len;
-    g.first = seq * a.seq_len + at;
-    g.last = at + a.seg_len >= a.seq_len;
-    g.len = g.last ? a.seq_len - at : a.seg_len;
+    const bool last = a.table[item].last;
+    if (!kOut && (last || item + 1 >= a.items)) return p;
+    p.seq = u.x;
+    p.h = ht / a.tiles;
+    p.d0 = ht % a.tiles * 128;
+    p.first = u.z;
+    p.len = u.w;
+    p.from = u.y == 0 && (last || !in_place) ? -1 : item * per + ht;
+    p.to = last ? -1 : (item + 1) * per + ht;
+    return p;
   }
-  return g;
+  // (fewer than 2^30 chunks in all rows: their q alone fills the device before;
+  // few and 32-bit unsigned divisions, because a CTA starts with them)
+  const unsigned bundle = a.bundle, b = static_cast<unsigned>(block) / bundle;
+  const unsigned in = block - b * bundle, chunks = a.chunks, width = a.width, pitch = a.pitch;
+  unsigned s = b, r, x, n;  // share, row, first chunk of it, chunks
+  if (!kOut) {       // ends at cut b + 1
+    const unsigned end = (b + 1) * width;
+    r = (end - 1) / pitch;
+    const unsigned y = end - r * pitch;
+    if (y >= chunks) return p;
+    x = y > width ? y - width : 0;
+    n = y - x;
+  } else {
+    const bool small = b >= static_cast<unsigned>(a.shares);
+    if (small) s = (a.order[b - a.shares] + 1) * pitch / width;
+    r = s * width / pitch;
+    x = s * width - r * pitch;
+    n = min(width, chunks - x);
+    // the share's chunks of the next row
+    const unsigned end = (s + 1) * width, row = (r + 1) * pitch;
+    const unsigned next = end > row && r + 1 < a.n_seq * static_cast<unsigned>(a.Hk) ? min(end - row, chunks) : 0;
+    if ((next > n) != small) {
+      ++r;
+      x = 0;
+      n = next;
+    }
+  }
+  const unsigned seq = r / a.Hk, sub = a.tiles == 1 ? in : in / a.tiles;
+  p.seq = seq;
+  p.h = (r - seq * a.Hk) * a.group + sub;
+  p.d0 = (in - sub * a.tiles) * 128;
+  const int at = x * kChunkTok;
+  p.first = p.seq * a.seq_len + at;
+  p.len = min(static_cast<int>(n * kChunkTok), a.seq_len - at);
+  const bool ends = x + n == chunks;
+  // what does not start or end with its row does with the share
+  p.to = ends ? -1 : static_cast<int>((s + 1) * bundle + in);
+  p.from = x > 0                ? static_cast<int>(s * bundle + in)
+           : ends || !in_place ? -1
+                               : static_cast<int>((a.shares + r) * bundle + in);
+  return p;
 }
 
 // lam^n for n >= 0 (0^0 = 1).  The exponent n log2(lam) is rounded once: a
@@ -128,10 +187,11 @@ __device__ __forceinline__ float decay_pow(float lam, float n) {
 
 // Launch of a kernel that may start while the one before it ends (it waits for
 // that one's results itself)
+inline dim3 grid_of(long long n) { return dim3(static_cast<unsigned>(n)); }
 template <typename K, typename... Args>
-cudaError_t launch_pdl(K kern, long long grid, int threads, int smem, cudaStream_t st, Args... args) {
+cudaError_t launch_pdl(K kern, dim3 grid, int threads, int smem, cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

@@ -350,6 +350,41 @@ def test_scan_packed_long_sequence_is_cut(dev):
     assert torch.equal(o, o2) and torch.equal(S, sd)
 
 
+def test_scan_shares(dev):
+    """Heads that are cut into one share per SM, whichever head ends inside it:
+    every output, and the state in place or not.  An output's three roundings to
+    bf16 (state, scores, result) are each within 2^-8 of their terms, whose
+    magnitudes the scan of the magnitudes adds up."""
+    q, k, v, decay, s = scan_inputs(18, 3001, 1, 13, 52, 128, 64)
+    qd, kd, vd, dd, sd = (x.to(dev) for x in (q, k, v, decay, s[0]))
+    o, S = moe.gdn_decay_scan(qd, kd, vd, dd, sd)
+    ro, rs = mixer.decay_scan(f64(q), f64(k), f64(v), f64(decay), f64(s))
+    terms, _ = mixer.decay_scan(*(np.abs(f64(x)) for x in (q, k, v)), f64(decay), np.abs(f64(s)))
+    assert (np.abs(f64(o) - ro) <= 2.0 ** -8 * (np.abs(ro) + terms) * (1 + 2.0 ** -6)).all()
+    assert np.linalg.norm(f64(o) - ro) <= 2.0 ** -8 * np.linalg.norm(ro)
+    assert (np.abs(f64(S) - rs[0]).max((1, 2)) <= S_TOL * np.abs(rs[0]).max((1, 2))).all()
+    o2, _ = moe.gdn_decay_scan(qd, kd, vd, dd, sd, state_out=sd)
+    assert torch.equal(o, o2) and torch.equal(S, sd)
+
+
+@pytest.mark.parametrize("T,Hk,Hv,dv", [(4800, 10, 30, 256), (6401, 6, 60, 80), (10001, 16, 32, 128)])
+def test_scan_shares_in_pieces(dev, T, Hk, Hv, dv):
+    """One call against short ones that pass the state along."""
+    q, k, v, decay, s = (x.to(dev) for x in scan_inputs(19, T, 1, Hk, Hv, 128, dv))
+    o, S = moe.gdn_decay_scan(q, k, v, decay, s[0])
+    st, parts = s[0].clone(), []
+    for a in range(0, T, 600):
+        parts.append(moe.gdn_decay_scan(q[a:a + 600], k[a:a + 600], v[a:a + 600], decay, st, state_out=st)[0])
+    both = torch.cat(parts).float()
+    # both are within the bound of test_scan_shares; without cancellation the
+    # kernel gives the terms' magnitudes to 3 x 2^-8
+    terms, _ = moe.gdn_decay_scan(q.abs(), k.abs(), v.abs(), decay, s[0].abs())
+    bound = 2.0 ** -8 * (both.abs() + terms.float()) * (1 + 2.0 ** -5)
+    assert ((o.float() - both).abs() <= 2 * bound).all()
+    assert (o.float() - both).norm() <= 2 * 2.0 ** -8 * both.norm()
+    assert ((S - st).abs().amax((1, 2)) <= 2 * S_TOL * st.abs().amax((1, 2))).all()
+
+
 @pytest.mark.parametrize("n,T", [(1, 1), (3, 8), (1, 2000), (3, 700)])
 def test_scan_in_place(dev, n, T):
     """Writing the state over the initial one changes no bit."""
