@@ -589,7 +589,6 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
   Piece g;
   if (!a.table) g = find_piece<kOut>(a, static_cast<int>(blockIdx.x));
   pdl_wait();  // (all above, while the kernel before this one ends)
-  pdl_launch_dependents();
   if (a.table) g = find_piece<kOut>(a, static_cast<int>(blockIdx.x));
   if (g.seq < 0) return;
   const int h = g.h, d0 = g.d0;
@@ -660,6 +659,9 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Only now: a CTA of the next kernel may take TMEM columns before it waits
+  // for this grid, and this CTA's allocation has no limit to its wait.
+  pdl_launch_dependents();
   const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
   const int tail = static_cast<int>(g.len - static_cast<long long>(nc - 1) * kC);  // tokens of the last chunk
 
