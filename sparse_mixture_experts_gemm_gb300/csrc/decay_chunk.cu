@@ -647,6 +647,7 @@ __global__ void __launch_bounds__(kThreadsC(kOut), 1)
   if (warp >= kState) {
     if (kOut) {
       load_rows<kHalfDk>(S, srows, before_rows(), kDk, a.dv - d0 - wq * 32);
+      fence_proxy_async_smem();  // (TMA writes over these rows, once s_ready says they are read)
     } else {
 #pragma unroll
       for (int i = 0; i < kHalfDk; ++i) S[i] = 0.0f;

@@ -40,3 +40,14 @@ def test_tmem_is_taken_before_dependents_start(file, name, body):
     assert 0 <= alloc < trigger
     if file in ("decay_chunk.cu", "matmul_fp8.cu"):
         assert "__syncthreads()" in body[alloc:trigger]
+
+
+def test_state_rows_are_fenced_before_copies_reuse_their_stages():
+    """The initial state's rows pass through the last TMA stages by ordinary
+    stores; copies of the asynchronous proxy into the same stages wait for the
+    barrier s_ready, and a proxy fence has to come before its first arrival."""
+    body = next(b for f, n, b in TMEM_KERNELS if f == "decay_chunk.cu" and "load_rows<" in b)
+    stores = body.index("load_rows<")
+    first_arrival = body.index("warp_arrive(s_ready)")
+    assert "fence_proxy_async_smem()" in body[stores:body.index("__syncthreads()", stores)]
+    assert stores < first_arrival
