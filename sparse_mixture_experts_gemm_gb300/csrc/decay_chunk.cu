@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(512, 2) decay_chain_kernel(const DecayArgs a, 
     long long lo, tokens;
     seq_range(a, g.seq, lo, tokens);
     n = (static_cast<int>(tokens) + a.seg_len - 1) / a.seg_len - 1;
-    if (item + n >= a.items) return;
+    if (item + n >= a.cuts) return;
     seq = g.seq;
     h = in / a.tiles;
     d0 = in % a.tiles * 128;
@@ -1006,11 +1006,11 @@ cudaError_t launch_chunked(const DecayArgs &a, const CUtensorMap &mq, const CUte
                            cudaStream_t st) {
   const long long per = static_cast<long long>(a.Hv) * a.tiles, bundle = a.bundle;
   if (segmented) {
-    cudaError_t e = launch_pdl(decay_chunk_kernel<kDk, false>, grid_of(a.table ? a.items * per : (a.shares - 1) * bundle),
+    cudaError_t e = launch_pdl(decay_chunk_kernel<kDk, false>, grid_of(a.table ? a.cuts * per : (a.shares - 1) * bundle),
                                kThreadsC(false), Smem<kDk, false>::kTotal, st, mq, mk, mv, mo, a);
     if (e != cudaSuccess) return e;
     const long long rows = static_cast<long long>(a.n_seq) * a.Hk;
-    const dim3 grid(static_cast<unsigned>(a.table ? a.items : rows), static_cast<unsigned>(a.table ? per : bundle), 32 * kDk / 512);
+    const dim3 grid(static_cast<unsigned>(a.table ? a.cuts : rows), static_cast<unsigned>(a.table ? per : bundle), 32 * kDk / 512);
     e = launch_pdl(decay_chain_kernel, grid, 512, 0, st, a, kDk);
     if (e != cudaSuccess) return e;
   }

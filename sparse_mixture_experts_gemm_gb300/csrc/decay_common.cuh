@@ -46,8 +46,11 @@ struct DecayArgs {
   uint8_t order[kGpuSms];  // rows whose end lies inside a share, by the share's smaller piece
   // With offsets: segments of seg_len tokens (a multiple of 64).
   int seg_len;
-  long long items;
-  Segment *table;  // [items], made by the call's recurrent kernel
+  long long cuts, items;
+  // [items], made by the call's recurrent kernel: first the segments of the
+  // sequences that are cut, `cuts` at most, the only ones with states in ws;
+  // then the sequences of one segment.
+  Segment *table;
 };
 
 // What a CTA of the chunked kernels does.
@@ -75,9 +78,9 @@ __device__ __forceinline__ void seq_range(const DecayArgs &a, int i, long long &
 // The table of a call with offsets, by one block: segments in order of their
 // sequences.  All threads of the block call it.
 __device__ __forceinline__ void make_table(const DecayArgs &a) {
-  __shared__ int s_seg[32];
+  __shared__ int s_cut[32], s_whole[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = static_cast<int>(blockDim.x) >> 5;
-  long long base = 0;  // segments before this block's worth of sequences
+  long long cuts = 0, wholes = a.cuts;  // the next free place of each part
   for (int i0 = 0; i0 < a.n_seq; i0 += static_cast<int>(blockDim.x)) {
     const int i = i0 + static_cast<int>(threadIdx.x);
     long long first = 0, len = 0;
@@ -86,20 +89,32 @@ __device__ __forceinline__ void make_table(const DecayArgs &a) {
       seq_range(a, i, first, len);
       n = len <= a.recur ? 0 : (static_cast<int>(len) + a.seg_len - 1) / a.seg_len;
     }
-    int inc = n;
+    const int whole = n == 1 ? 1 : 0, cut = n > 1 ? n : 0;
+    int inc = cut;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += u;
     }
-    if (lane == 31) s_seg[warp] = inc;
-    __syncthreads();
-    long long at = base + inc - n;
-    for (int w = 0; w < nw; ++w) {
-      if (w < warp) at += s_seg[w];
-      base += s_seg[w];
+    const uint32_t mask = __ballot_sync(0xffffffffu, whole);
+    if (lane == 31) {
+      s_cut[warp] = inc;
+      s_whole[warp] = __popc(mask);
     }
-    for (int k = 0; k < n && at + k < a.items; ++k) {
+    __syncthreads();
+    // (a sequence has places in one part only)
+    long long at = cuts + inc - cut, end = a.cuts;
+    if (whole) {
+      at = wholes + __popc(mask & ((1u << lane) - 1));
+      end = a.items;
+    }
+    for (int w = 0; w < nw; ++w) {
+      if (w < warp) at += whole ? s_whole[w] : s_cut[w];
+      cuts += s_cut[w];
+      wholes += s_whole[w];
+    }
+    // (offsets that overlap may ask for more places than there are)
+    for (int k = 0; k < n && at + k < end; ++k) {
       Segment g = {};
       g.seq = i;
       g.index = k;
@@ -112,7 +127,8 @@ __device__ __forceinline__ void make_table(const DecayArgs &a) {
   }
   Segment none = {};
   none.seq = -1;
-  for (long long k = base + threadIdx.x; k < a.items; k += blockDim.x) a.table[k] = none;
+  for (long long k = cuts + threadIdx.x; k < a.cuts; k += blockDim.x) a.table[k] = none;
+  for (long long k = wholes + threadIdx.x; k < a.items; k += blockDim.x) a.table[k] = none;
 }
 
 // The piece of CTA `block`: kOut: all of them, the larger one of each share
@@ -126,7 +142,7 @@ __device__ __forceinline__ Piece find_piece(const DecayArgs &a, int block) {
     const int per = a.Hv * a.tiles, item = block / per, ht = block % per;
     const int4 u = *reinterpret_cast<const int4 *>(a.table + item);
     const bool last = a.table[item].last;
-    if (!kOut && (last || item + 1 >= a.items)) return p;
+    if (!kOut && (last || item + 1 >= a.cuts)) return p;
     p.seq = u.x;
     p.h = ht / a.tiles;
     p.d0 = ht % a.tiles * 128;

@@ -404,6 +404,20 @@ def test_scan_many_packed_sequences(dev):
     check_scan(o, S, q, k, v, decay, s, off)
 
 
+def test_scan_several_cut_among_many(dev):
+    """Decode tokens, short and long prompts in one call: only the longest are
+    cut, and their segments stand apart from the others in the call's table."""
+    lens = [1] * 50 + [5000] + [3] * 30 + [40] * 200 + [9000, 0, 17, 4097] + [16, 18] * 20
+    q, k, v, decay, s = scan_inputs(20, sum(lens), len(lens), 1, 2, 64, 32)
+    decay[1] = 0.9995
+    off = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    qd, kd, vd, dd, sd, od = (x.to(dev) for x in (q, k, v, decay, s, off))
+    o, S = moe.gdn_decay_scan(qd, kd, vd, dd, sd, od)
+    check_scan(o, S, q, k, v, decay, s, off)
+    o2, _ = moe.gdn_decay_scan(qd, kd, vd, dd, sd, od, state_out=sd)
+    assert torch.equal(o, o2) and torch.equal(S, sd)
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_scan_nan_stays_in_its_sequence(dev, bad):
     """Sequences around one of NaN or infinite q, k, v and state: no bit of

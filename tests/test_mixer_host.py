@@ -208,3 +208,13 @@ def test_decay_workspace_is_asked_for(lib):
         for ws, n in ((None, need.value), (P, need.value - 1)):
             assert lib.gdn_decay_scan(P, P, P, P, None, P, P, None, 65536, 1, 4, 4, 128, 128, 512, 512,
                                       512, ws, n, None) == moe.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("n,N", [(64, 16384), (192, 32768), (256, 65536), (1024, 131072), (257, 16640), (3000, 65536)])
+def test_decay_workspace_of_many_packed_sequences(lib, n, N):
+    """States in the workspace go by the sequences that can be cut, not by all
+    that are packed: at most two per whole segment of the tokens (16 key and 32
+    value heads of 128 x 128, a state of 2 MB)."""
+    need = ctypes.c_size_t(0)
+    assert lib.gdn_decay_workspace(N, n, 1, 32, 128, 128, ctypes.byref(need)) == moe.MOE_OK
+    assert need.value <= 30 << 20
