@@ -175,7 +175,7 @@ struct Plan {
   // without offsets: rows of chunks on a line cut into shares
   long long rows, chunks, pitch, width, shares;
   // with offsets: items of the table, at most `cuts` of them of cut sequences
-  long long seg_len, cuts, items;
+  long long seg_len, cut_from, cuts, items;
   long long table;  // bytes of the table of segments, at the workspace's start
   long long slots;  // states in the workspace
 };
@@ -202,10 +202,16 @@ long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 // in shares: 16,384 tokens x 32 heads 150 / 142 us, 32,768 x 32 272 / 259,
 // 8,192 x 64 157 / 147; 8,192 x 32 83.8 / 84.5, 16,384 x 16 81.5 / 83.5.
 // With offsets the lengths are not known here: a segment is as long as for one
-// sequence of all tokens, but at least 64 chunks and an SM's share of all the
-// work, so that only a sequence that would outlast the rest of its batch is cut
-// (nine of 0 to 2,049 tokens: 93 us with the longest two cut in two, 62 us with
-// none).
+// sequence of all tokens, but no shorter than the SMs that the uncut batch
+// leaves idle can take: the sequences have a CTA per head, or one segment each
+// that is not whole, and the rest of the CTAs that run at once goes to whole
+// segments.  Where no SM is left the cut helps the longest sequence only and
+// costs the others: from 64 chunks, or an SM's share of all the work, on.
+// With that bound / with 64 chunks for every batch: one of 2,900 tokens 25.8 /
+// 71.9 us with 1 head, 29.5 / 73.1 with 4, 53.6 / 73.4 with 32; nine of 0 to
+// 2,049 tokens 30.9 / 55.1 with 4 heads, 39.7 / 56.2 with 8, not cut with 32
+// (62; the longest two cut in two 93); sixteen of 512 with 4 heads, where the
+// launches for cuts find none, 26.3 / 22.6.
 Plan make_plan(bool ragged, long long n_tokens, long long n_seq, long long n_k_heads, long long heads) {
   Plan p = {};
   const long long len = ragged ? n_tokens : n_seq ? n_tokens / n_seq : 0;
@@ -215,7 +221,8 @@ Plan make_plan(bool ragged, long long n_tokens, long long n_seq, long long n_k_h
   if (!p.chunked) return p;
   const long long chunks = ceil_div(len, kChunkTok), bundle = heads / n_k_heads;
   const long long share = ceil_div(chunks * heads, kGpuSms);
-  const long long least = !ragged ? 1 : share > 64 ? share : 64;
+  const long long idle = kGpuSms - n_seq * heads;
+  const long long least = !ragged ? 1 : std::max(share, idle > 0 ? std::min(ceil_div(chunks * heads, idle), 64LL) : 64LL);
   p.rows = seqs * n_k_heads;
   p.chunks = chunks;
   double best = 0;
@@ -236,12 +243,15 @@ Plan make_plan(bool ragged, long long n_tokens, long long n_seq, long long n_k_h
   }
   p.segmented = p.width < chunks;
   if (ragged) {
-    // sequences of more than seg_len tokens are cut; each has one segment more
-    // than whole seg_len in it at most.  Only their segments have states in the
+    // if the longest has more than cut_from tokens, where the launches that come
+    // before cost less (by the costs above) than the chunks that run elsewhere,
+    // all sequences of more than seg_len are cut (those launches delay the short
+    // ones too); each has one segment more than whole seg_len in it at most.  Only their segments have states in the
     // workspace: 192 prompts in 32,768 tokens, 32 heads of 128 x 128, 15 MB
     // and 538 us (411 MB and 627 us with states for all that may be chunked).
     p.seg_len = p.width * kChunkTok;
     const auto sequences = [&](long long longer) { return std::min(n_seq, n_tokens / (longer + 1)); };
+    p.cut_from = (p.width + (52 * p.width + 750) / 100) * kChunkTok;
     p.cuts = p.segmented ? n_tokens / p.seg_len + sequences(p.seg_len) : 0;
     p.items = p.cuts + sequences(kRecur);
     p.table = p.items * static_cast<long long>(sizeof(Segment));
@@ -381,6 +391,7 @@ extern "C" int gdn_decay_scan(const void *q, const void *k, const void *v, const
   a.dv = d_v;
   a.recur = static_cast<int>(kRecur);
   a.seg_len = static_cast<int>(plan.seg_len);
+  a.cut_from = static_cast<int>(std::min(plan.cut_from, n_tokens));
   a.seq_len = static_cast<int>(n_tokens / n_seq);
   a.cuts = plan.cuts;
   a.items = plan.items;

@@ -44,8 +44,9 @@ struct DecayArgs {
   // cut every `width` chunks into `shares`.
   int chunks, pitch, width, shares, smalls;
   uint8_t order[kGpuSms];  // rows whose end lies inside a share, by the share's smaller piece
-  // With offsets: segments of seg_len tokens (a multiple of 64).
-  int seg_len;
+  // With offsets: segments of seg_len tokens (a multiple of 64), if the longest
+  // sequence has more than cut_from; else none is cut.
+  int seg_len, cut_from;
   long long cuts, items;
   // [items], made by the call's recurrent kernel: first the segments of the
   // sequences that are cut, `cuts` at most, the only ones with states in ws;
@@ -80,6 +81,20 @@ __device__ __forceinline__ void seq_range(const DecayArgs &a, int i, long long &
 __device__ __forceinline__ void make_table(const DecayArgs &a) {
   __shared__ int s_cut[32], s_whole[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = static_cast<int>(blockDim.x) >> 5;
+  int longest = 0;
+  if (a.cuts > 0) {
+    for (int i = static_cast<int>(threadIdx.x); i < a.n_seq; i += static_cast<int>(blockDim.x)) {
+      long long first, len;
+      seq_range(a, i, first, len);
+      longest = max(longest, static_cast<int>(len));
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) s_cut[warp] = longest;
+    __syncthreads();
+    for (int w = 0; w < nw; ++w) longest = max(longest, s_cut[w]);
+    __syncthreads();
+  }
+  const int uncut = longest > a.cut_from ? a.seg_len : static_cast<int>(a.n_tokens);
   long long cuts = 0, wholes = a.cuts;  // the next free place of each part
   for (int i0 = 0; i0 < a.n_seq; i0 += static_cast<int>(blockDim.x)) {
     const int i = i0 + static_cast<int>(threadIdx.x);
@@ -87,7 +102,7 @@ __device__ __forceinline__ void make_table(const DecayArgs &a) {
     int n = 0;
     if (i < a.n_seq) {
       seq_range(a, i, first, len);
-      n = len <= a.recur ? 0 : (static_cast<int>(len) + a.seg_len - 1) / a.seg_len;
+      n = len <= a.recur ? 0 : len <= uncut ? 1 : (static_cast<int>(len) + a.seg_len - 1) / a.seg_len;
     }
     const int whole = n == 1 ? 1 : 0, cut = n > 1 ? n : 0;
     int inc = cut;

@@ -218,3 +218,13 @@ def test_decay_workspace_of_many_packed_sequences(lib, n, N):
     need = ctypes.c_size_t(0)
     assert lib.gdn_decay_workspace(N, n, 1, 32, 128, 128, ctypes.byref(need)) == moe.MOE_OK
     assert need.value <= 30 << 20
+
+
+@pytest.mark.parametrize("n,N,heads,cut", [(1, 2900, 1, True), (1, 2900, 32, True), (9, 5461, 4, True), (6, 3400, 8, True),
+                                           (9, 5461, 32, False), (65, 4160, 32, False), (1, 200, 1, False)])
+def test_decay_packed_cut_goes_by_idle_sms(lib, n, N, heads, cut):
+    """Whether the longest sequence of a packed batch may be cut depends on the
+    SMs that its heads leave idle: without a cut the workspace has no state."""
+    need = ctypes.c_size_t(0)
+    assert lib.gdn_decay_workspace(N, n, 1, heads, 128, 128, ctypes.byref(need)) == moe.MOE_OK
+    assert (need.value >= 128 * 128 * 4) == cut
