@@ -198,7 +198,8 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const NormArgs a) {
       top = max(top, s_top[i]);
     }
   }
-  const float r = w ? rsqrtf(ss / static_cast<float>(d) + a.eps) : 1.0f;
+  float r = w ? rsqrtf(ss / static_cast<float>(d) + a.eps) : 1.0f;
+  if (top == 0) r = 0.0f;  // a row of zeros stays one where eps is 0 and r infinite
   if (a.out) {
 #pragma unroll
     for (int p = 0; p < kPer; ++p)

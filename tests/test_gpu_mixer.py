@@ -135,6 +135,25 @@ def test_norm_special_rows(dev):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [7, 256, 2048, 16384])
+def test_norm_zero_rows_without_eps(dev, d, dtype):
+    """eps may be 0: a row of zeros gives zeros, scale 0 and zero codes, by
+    itself and as the sum of two rows that cancel."""
+    g = gen(d)
+    x, w = normal(g, 3, d, dtype=dtype), (1 + normal(g, d, std=0.2)).to(dtype)
+    x[1] = 0
+    r = torch.zeros_like(x)
+    r[2] = -x[2]
+    out, s = moe.add_rmsnorm(x.to(dev), w.to(dev), r.to(dev), eps=0.0)
+    codes, scales, _ = moe.add_rmsnorm_fp8(x.to(dev), w.to(dev), r.to(dev), eps=0.0)
+    assert not out[1:].any() and not s[1:].any() and not scales[1:].any() and not codes[1:].float().any()
+    y, _ = mixer.rmsnorm(f64(x[:1]), f64(w), 0.0)
+    unit = 2.0 ** -18 + (2.0 ** -8 if dtype == BF16 else 0)
+    assert (np.abs(f64(out[:1]) - y) <= np.abs(y) * unit + 1e-30).all()
+    check_codes(codes[:1], scales[:1], y)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("rows,d", [(1, 16), (5, 33), (200, 2048), (3, 16384)])
 def test_quantize(dev, rows, d, dtype):
     w = normal(gen(d), rows, d, dtype=dtype, std=0.02)
