@@ -31,6 +31,13 @@ namespace {
 
 constexpr int kMaxNormD = 16384;
 
+// The sum of squares is taken again from elements times kDown or kUp where it
+// exceeds fp32's range, or where it is below kTinySum and eps below kTinyEps
+// (squares under 2^-126 lose bits, which an eps of normal size hides).  Scaled,
+// 2^128 squares to 2^112 and 2^-149 to 2^-98, 16,384 of either add up in range.
+constexpr float kMaxFloat = 3.402823466e38f, kTinySum = 0x1p-90f, kTinyEps = 0x1p-90f;
+constexpr float kDown = 0x1p-72f, kUp = 0x1p100f;
+
 struct NormArgs {
   const void *x, *residual, *weight;  // residual, weight: null where there is none
   void *sum, *out;                    // null where not asked for
@@ -169,6 +176,16 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const NormArgs a) {
   for (int p = 0; p < kPer; ++p)
 #pragma unroll
     for (int e = 0; e < V; ++e) ss = fmaf(v[p][e], v[p][e], ss);
+  // a thread whose own squares leave that range adds them up scaled, too
+  const float part = ss;
+  float scaled = 0.0f;
+  if (part > kMaxFloat || (a.eps < kTinyEps && part < kTinySum)) {
+    const float f = part > kMaxFloat ? kDown : kUp;
+#pragma unroll
+    for (int p = 0; p < kPer; ++p)
+#pragma unroll
+      for (int e = 0; e < V; ++e) scaled = fmaf(v[p][e] * f, v[p][e] * f, scaled);
+  }
   if (w) {
     float u[kPer][V];
     load_row<T, V, kPer>(w, c0, step, d, a.wide, u);
@@ -198,19 +215,41 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const NormArgs a) {
       top = max(top, s_top[i]);
     }
   }
-  float r = w ? rsqrtf(ss / static_cast<float>(d) + a.eps) : 1.0f;
-  if (top == 0) r = 0.0f;  // a row of zeros stays one where eps is 0 and r infinite
+  // the norm's factor is pre * r
+  float r = 1.0f, pre = 1.0f;
+  if (w) {
+    const bool huge = ss > kMaxFloat, tiny = a.eps < kTinyEps && ss < kTinySum;
+    if (huge || tiny) {  // (one answer in the whole block)
+      // squares past fp32's range, or so small that they lose bits beside an
+      // eps as small: the sum of the scaled elements' instead
+      pre = huge ? kDown : kUp;
+      float x = huge ? (part < kTinySum ? 0.0f : part <= kMaxFloat ? part * kDown * kDown : scaled) : scaled;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      if constexpr (kW > 1) {
+        __syncthreads();
+        if ((t & 31) == 0) s_ss[t >> 5] = x;
+        __syncthreads();
+        x = 0.0f;
+        for (int i = 0; i < kW; ++i) x += s_ss[i];
+      }
+      ss = x;
+    }
+    r = rsqrtf(ss / static_cast<float>(d) + a.eps * pre * pre);
+    // a row of zeros stays one where eps is 0 and r infinite
+    if (top == 0) r = 0.0f;
+  }
   if (a.out) {
 #pragma unroll
     for (int p = 0; p < kPer; ++p)
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[p][e] *= r;
+      for (int e = 0; e < V; ++e) v[p][e] = v[p][e] * pre * r;
     store_row<T, V, kPer>(static_cast<T *>(a.out) + row * d, c0, step, d, a.wide, v);
   }
   if (a.codes) {
     const float m = __uint_as_float(top);
     const bool finite = top < 0x7f800000u;
-    const float scale = finite ? m * r / 448.0f : __uint_as_float(0x7fffffffu);
+    const float scale = finite ? m * pre * r / 448.0f : __uint_as_float(0x7fffffffu);
     // rows of tiny values are lifted by an exact power of two first, so that
     // 448 / m stays finite
     const float lift = m < 0x1p-60f ? 0x1p80f : 1.0f;

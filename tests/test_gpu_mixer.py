@@ -154,6 +154,32 @@ def test_norm_zero_rows_without_eps(dev, d, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [7, 256, 1001, 2048, 16384])
+@pytest.mark.parametrize("eps", [1e-6, 0.0])
+def test_norm_rows_whose_squares_leave_the_range(dev, d, dtype, eps):
+    """Finite rows of 1e18 to 1e38 have their norm, with one large element or
+    with all of them; without eps so have rows of 1e-18 to 1e-36, where a product
+    s w below 2^-126 is off by up to 2^-150.  Weights of 1/2 to 1, so that none
+    exceeds the range."""
+    g = gen(d + 1)
+    sizes = [1e18, 2e19, 1e20, 1e30, 5e37] + ([1e-18, 1e-20, 1e-30, 1e-36] if eps == 0 else [])
+    x = normal(g, 2 * len(sizes), d).clamp(-5, 5)
+    for i, size in enumerate(sizes):
+        x[2 * i] *= size
+        x[2 * i + 1, 1:] *= size * 1e-3
+        x[2 * i + 1, 0] = 3 * size
+    x, w = x.to(dtype), (1 - torch.rand(d, generator=g) / 2).to(dtype)
+    assert torch.isfinite(x).all()
+    y, _ = mixer.rmsnorm(f64(x), f64(w), eps)
+    out, _ = moe.add_rmsnorm(x.to(dev), w.to(dev), eps=eps)
+    codes, scales, _ = moe.add_rmsnorm_fp8(x.to(dev), w.to(dev), eps=eps)
+    unit = 2.0 ** -18 + (2.0 ** -8 if dtype == BF16 else 0)
+    under = 2.0 ** -149 / np.sqrt((f64(x) ** 2).mean(1, keepdims=True) + eps)
+    assert (np.abs(f64(out) - y) <= np.abs(y) * unit + under + 1e-30).all()
+    check_codes(codes, scales, y)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("rows,d", [(1, 16), (5, 33), (200, 2048), (3, 16384)])
 def test_quantize(dev, rows, d, dtype):
     w = normal(gen(d), rows, d, dtype=dtype, std=0.02)
