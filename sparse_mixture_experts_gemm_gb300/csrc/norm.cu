@@ -253,7 +253,10 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const NormArgs a) {
     // rows of tiny values are lifted by an exact power of two first, so that
     // 448 / m stays finite
     const float lift = m < 0x1p-60f ? 0x1p80f : 1.0f;
-    const float f = finite ? (scale == 0.0f ? 0.0f : 448.0f / (m * lift)) : scale;
+    float f = finite ? (scale == 0.0f ? 0.0f : 448.0f / (m * lift)) : scale;
+    // a scale below 2^-126 is off by up to half of itself: the codes make up
+    // for that, as y / scale does (the largest one may then be less than 448)
+    if (finite && scale > 0.0f && scale < 0x1p-126f) f = pre * r / (scale * lift);
 #pragma unroll
     for (int p = 0; p < kPer; ++p)
 #pragma unroll

@@ -180,6 +180,28 @@ def test_norm_rows_whose_squares_leave_the_range(dev, d, dtype, eps):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [7, 264, 2048])
+def test_codes_go_by_the_scale_that_is_returned(dev, d, dtype):
+    """Rows so small that their scale is one of float32's last values, which
+    round max / 448 by up to half: scale * code is still y (the code within 2^-4
+    of y / scale, or 2^-10 below the smallest normal code; past 448, where the
+    scale was rounded down, 448)."""
+    g = gen(d)
+    x = normal(g, 12, d).clamp(-3, 3)
+    for i in range(12):
+        x[i] *= 3e-37 * 4.0 ** -i
+    x = x.to(dtype)
+    codes, scales = moe.quantize_fp8(x.to(dev))
+    c, s, y = codes_of(codes), f64(scales), f64(x)
+    top = np.abs(y).max(1)
+    assert (np.abs(s - top / 448) <= np.maximum(top / 448 * 2.0 ** -23, 2.0 ** -150)).all()
+    live = s > 0
+    assert live.sum() >= 8 and not c[~live].any()
+    r = np.clip(y[live] / s[live, None], -448, 448)
+    assert (np.abs(c[live] - r) <= np.maximum(np.abs(r) * 2.0 ** -4, 2.0 ** -10) * (1 + 2.0 ** -10)).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("rows,d", [(1, 16), (5, 33), (200, 2048), (3, 16384)])
 def test_quantize(dev, rows, d, dtype):
     w = normal(gen(d), rows, d, dtype=dtype, std=0.02)
