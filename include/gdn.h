@@ -93,7 +93,7 @@ int gdn_scan(const void *q, const void *k, const void *v, const float *alpha, co
  * bits.  NaN and infinities of one sequence reach no other.  The caller applies the model's
  * preprocessing (norms, query scale) before the call.
  * Supported: d_k 64 or 128, d_v a multiple of 16 up to 1024, n_v_heads a
- * multiple of n_k_heads and at most 4096, n_tokens < 2^31.
+ * multiple of n_k_heads and at most 4096, n_tokens < 2^31, strides < 2^39.
  * Pointers 16-byte aligned (decay and offsets 4-byte), strides multiples of 8.
  * n_seq == 0 is a no-op.  Asynchronous on cuda_stream; all checks are made on
  * the host before anything is launched.  A bounded wait in the kernels that

@@ -347,7 +347,7 @@ extern "C" int gdn_decay_scan(const void *q, const void *k, const void *v, const
       v_stride < static_cast<long long>(n_v_heads) * d_v)
     return MOE_ERR_INVALID_ARG;
   if ((d_k != 64 && d_k != 128) || d_v % 16 != 0 || d_v > 1024 || n_v_heads > 4096 ||
-      n_tokens > 0x7fffffffLL ||
+      n_tokens > 0x7fffffffLL || std::max({q_stride, k_stride, v_stride}) >= 1LL << 39 ||
       static_cast<long long>(n_seq) * n_v_heads * (d_v / 16) > 0x7fffffffLL)
     return MOE_ERR_UNSUPPORTED;
   auto misaligned = [](const void *p, uintptr_t n) {
@@ -405,18 +405,20 @@ extern "C" int gdn_decay_scan(const void *q, const void *k, const void *v, const
   a.table = plan.table ? static_cast<Segment *>(workspace) : nullptr;
   a.ws = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.table);
   a.status = dev.status;
-  cudaError_t e = cudaSuccess;
-  if (plan.recurrent)
-    e = d_k == 128 ? launch_recurrent<128>(a, st) : launch_recurrent<64>(a, st);
-  if (e == cudaSuccess && plan.chunked) {
+  // the maps before the first launch: a call that fails has launched nothing
+  CUtensorMap mq, mk, mv, mo;
+  if (plan.chunked) {
     const uint64_t kw = static_cast<uint64_t>(n_k_heads) * d_k, vw = static_cast<uint64_t>(n_v_heads) * d_v;
-    CUtensorMap mq, mk, mv, mo;
     if (!encode_map_2d(&mq, q, 2, n_tokens, kw, 64, kChunkTok, true, 2 * q_stride) ||
         !encode_map_2d(&mk, k, 2, n_tokens, kw, 64, kChunkTok, true, 2 * k_stride) ||
         !encode_map_2d(&mv, v, 2, n_tokens, vw, 64, kChunkTok, true, 2 * v_stride) ||
         !encode_map_2d(&mo, o, 2, n_tokens, vw, 32, 32, false, 0, true))
       return MOE_ERR_CUDA;
-    e = launch_decay_chunked(a, d_k, mq, mk, mv, mo, plan.segmented, st);
   }
+  cudaError_t e = cudaSuccess;
+  if (plan.recurrent)
+    e = d_k == 128 ? launch_recurrent<128>(a, st) : launch_recurrent<64>(a, st);
+  if (e == cudaSuccess && plan.chunked)
+    e = launch_decay_chunked(a, d_k, mq, mk, mv, mo, plan.segmented, st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -228,3 +228,15 @@ def test_decay_packed_cut_goes_by_idle_sms(lib, n, N, heads, cut):
     need = ctypes.c_size_t(0)
     assert lib.gdn_decay_workspace(N, n, 1, heads, 128, 128, ctypes.byref(need)) == moe.MOE_OK
     assert (need.value >= 128 * 128 * 4) == cut
+
+
+@pytest.mark.parametrize("which", ["qs", "ks", "vs"])
+@pytest.mark.parametrize("off", [None, P])
+def test_decay_scan_refuses_strides_that_no_tensor_map_takes(lib, which, off):
+    """A tensor map's strides end at 2^40 bytes.  With offsets the recurrent
+    kernel is launched before the chunked ones, so the call has to be refused
+    before either."""
+    a = dict(qs=256, ks=256, vs=256)
+    a[which] = 1 << 39
+    assert lib.gdn_decay_scan(P, P, P, P, None, P, P, off, 64, 2, 2, 4, 128, 64, a["qs"], a["ks"], a["vs"],
+                              P, 1 << 30, None) == moe.MOE_ERR_UNSUPPORTED
