@@ -5,7 +5,8 @@ moe_add_rmsnorm_fp8, moe_quantize_fp8, moe_matmul_fp8; include/gdn.h:
 gdn_decay_scan): they check types, shapes and layouts, allocate what is not
 given, and launch on `stream` (default: torch's current stream).  Results and
 workspaces are allocated on that stream, so that the caching allocator hands
-their memory on in its order.
+their memory on in its order.  The kernels run on the current device: tensors
+or a stream of another one are refused.
 
 One decoded token is a handful of such calls of a few microseconds each, so
 the path of a call with contiguous tensors on the current stream is kept short:
@@ -24,6 +25,7 @@ from . import MOE_BF16, MOE_F32, MoeError, lib
 _BF16, _F32, _F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 _DTYPES = {_BF16: MOE_BF16, _F32: MOE_F32}
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _NONE = contextlib.nullcontext()
 _L = None
 
@@ -35,11 +37,28 @@ def _lib():
     return _L
 
 
-def _on(stream):
-    """(context to allocate in, raw handle) of a caller's stream."""
+def _on(stream, device):
+    """(context to allocate in, raw handle) of a caller's stream on `device`;
+    None: the current one."""
+    if stream is None:
+        return _NONE, _raw_stream(device)
     if isinstance(stream, int):
         return torch.cuda.stream(torch.cuda.ExternalStream(stream)), stream
+    if stream.device_index != device:
+        raise ValueError(f"stream is on device {stream.device_index}, the tensors on {device}")
     return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _device(first, *others):
+    """The device of all these tensors (None: not given), which has to be the
+    current one."""
+    device = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors on device {device} and on device {t.get_device()} in one call")
+    if device != _current_device():
+        raise ValueError(f"tensors on device {device}, current device {_current_device()}")
+    return device
 
 
 def _rows(name, t):
@@ -92,10 +111,7 @@ def _norm(x, weight, residual, eps, out, scales, sum_out, stream, fp8):
             raise ValueError("residual must be a CUDA tensor of x's shape and type")
         _, _, rs = _rows("residual", residual)
         rp = residual.data_ptr()
-    if stream is None:
-        ctx, handle = _NONE, _raw_stream(x.get_device())
-    else:
-        ctx, handle = _on(stream)
+    ctx, handle = _on(stream, _device(x, weight, residual, out, scales, sum_out))
     kind = _F8 if fp8 else dtype
     with ctx:
         plain = x.is_contiguous()
@@ -149,7 +165,7 @@ def quantize_fp8(w, codes=None, scales=None, stream=None):
     if dt is None or not w.is_cuda:
         raise ValueError("w must be a CUDA bfloat16 or float32 tensor")
     rows, d, stride = _rows("w", w)
-    ctx, handle = (_NONE, _raw_stream(w.get_device())) if stream is None else _on(stream)
+    ctx, handle = _on(stream, _device(w, codes, scales))
     with ctx:
         if codes is None:
             codes = torch.empty(w.shape, dtype=_F8, device=w.device)
@@ -179,7 +195,7 @@ def matmul_fp8(x, x_scales, w, w_scales, out=None, stream=None):
     lead = x.shape[:-1]
     _given("x_scales", x_scales, lead, _F32)
     _vector("w_scales", w_scales, N, _F32)
-    ctx, handle = (_NONE, _raw_stream(x.get_device())) if stream is None else _on(stream)
+    ctx, handle = _on(stream, _device(x, x_scales, w, w_scales, out))
     os_ = N
     if out is None:
         with ctx:
@@ -262,7 +278,7 @@ def gdn_decay_scan(q, k, v, decay, state=None, offsets=None, out=None, state_out
         _given("state", state, s_shape, _F32)
         sp = state.data_ptr()
     need = _decay_workspace(N, n, op is not None, Hv, dk, dv)
-    ctx, handle = (_NONE, _raw_stream(v.get_device())) if stream is None else _on(stream)
+    ctx, handle = _on(stream, _device(v, q, k, decay, state, offsets, out, state_out))
     with ctx:
         if out is None:
             out = torch.empty(sv, dtype=_BF16, device=v.device)

@@ -5,8 +5,10 @@ import ctypes
 
 import numpy as np
 import pytest
+import torch
 
 import sparse_mixture_experts_gemm_gb300 as moe
+import sparse_mixture_experts_gemm_gb300.mixer as binding
 from oracle import mixer
 from sparse_mixture_experts_gemm_gb300 import buildlib as moe_build
 
@@ -240,3 +242,88 @@ def test_decay_scan_refuses_strides_that_no_tensor_map_takes(lib, which, off):
     a[which] = 1 << 39
     assert lib.gdn_decay_scan(P, P, P, P, None, P, P, off, 64, 2, 2, 4, 128, 64, a["qs"], a["ks"], a["vs"],
                               P, 1 << 30, None) == moe.MOE_ERR_UNSUPPORTED
+
+
+# ------------------------------------------------------------- the binding
+class OnGpu(torch.Tensor):
+    """A CPU tensor that says it is on GPU `dev`, for checks that come before
+    any launch."""
+    dev = 0
+    is_cuda = True
+
+    def get_device(self):
+        return self.dev
+
+
+def on_gpu(*shape, dtype=torch.bfloat16):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+
+
+CALLS = {
+    "add_rmsnorm": lambda t: binding.add_rmsnorm(t["x"], t["weight"], t["residual"], out=t["out"], sum_out=t["sum"]),
+    "add_rmsnorm_fp8": lambda t: binding.add_rmsnorm_fp8(t["x"], t["weight"], t["residual"], codes=t["codes"],
+                                                         scales=t["scales"], sum_out=t["sum"]),
+    "quantize_fp8": lambda t: binding.quantize_fp8(t["x"], codes=t["codes"], scales=t["scales"]),
+    "matmul_fp8": lambda t: binding.matmul_fp8(t["codes"], t["scales"], t["w"], t["w_scales"], out=t["out"]),
+    "gdn_decay_scan": lambda t: binding.gdn_decay_scan(t["q"], t["k"], t["v"], t["decay"], state=t["state"],
+                                                       offsets=t["offsets"], out=t["o"], state_out=t["state_out"]),
+}
+USES = {
+    "add_rmsnorm": ["x", "weight", "residual", "out", "sum"],
+    "add_rmsnorm_fp8": ["x", "weight", "residual", "codes", "scales", "sum"],
+    "quantize_fp8": ["x", "codes", "scales"],
+    "matmul_fp8": ["codes", "scales", "w", "w_scales", "out"],
+    "gdn_decay_scan": ["q", "k", "v", "decay", "state", "offsets", "o", "state_out"],
+}
+
+
+def operands():
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    t = {"x": on_gpu(4, 64), "weight": on_gpu(64), "residual": on_gpu(4, 64), "out": on_gpu(4, 64), "sum": on_gpu(4, 64),
+         "codes": on_gpu(4, 64, dtype=f8), "scales": on_gpu(4, dtype=f32), "w": on_gpu(64, 64, dtype=f8),
+         "w_scales": on_gpu(64, dtype=f32), "decay": on_gpu(2, dtype=f32), "offsets": on_gpu(3, dtype=torch.int32),
+         "state": on_gpu(2, 2, 64, 64, dtype=f32), "state_out": on_gpu(2, 2, 64, 64, dtype=f32)}
+    for name in ("q", "k", "v", "o"):
+        t[name] = on_gpu(4, 2, 64)
+    return t
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    """The library replaced by a recorder of its calls, on GPU 0 as the current one."""
+    seen = []
+
+    class Recorder:
+        def __getattr__(self, name):
+            return lambda *a: seen.append(name) or 0
+
+    monkeypatch.setattr(binding, "_lib", lambda: Recorder())
+    monkeypatch.setattr(binding, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(binding, "_decay_workspace", lambda *a: 0)
+    monkeypatch.setattr(binding, "_current_device", lambda: 0, raising=False)
+    return seen
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_one_device_per_call(launches, name):
+    """The kernels run on the current device: a tensor of another one, or all of
+    them, is refused before the library is called."""
+    CALLS[name](operands())
+    assert launches == ["moe_" + name if name != "gdn_decay_scan" else name]
+    for elsewhere in [[n] for n in USES[name]] + [USES[name]]:
+        t = operands()
+        for n in elsewhere:
+            t[n].dev = 1
+        with pytest.raises(ValueError, match="device"):
+            CALLS[name](t)
+    assert len(launches) == 1
+
+
+def test_stream_of_another_device_is_refused(launches):
+    class Stream:
+        device_index, cuda_stream = 1, 5
+
+    t = operands()
+    with pytest.raises(ValueError, match="device"):
+        binding.quantize_fp8(t["x"], codes=t["codes"], scales=t["scales"], stream=Stream())
+    assert launches == []
