@@ -17,6 +17,7 @@ import pytest
 import torch
 
 import sparse_mixture_experts_gemm_gb300 as moe
+import sparse_mixture_experts_gemm_gb300.mixer as mixer_binding
 from oracle import mixer
 
 pytestmark = pytest.mark.gpu
@@ -566,6 +567,41 @@ def test_other_stream(dev):
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(u, v) for u, v in zip(cap, ref))
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_segmented_scan_on_another_stream_and_in_a_graph(dev, packed):
+    """A scan with a workspace and three or four launches, on a stream that is
+    not the current one (given as an object and as a handle) and captured; the
+    workspace's memory is handed on to other tensors of that stream meanwhile."""
+    lens = [5, 2900, 0, 130, 1] if packed else [1500, 1500]
+    q, k, v, decay, s = (x.to(dev) for x in scan_inputs(21, sum(lens), len(lens), 2, 4, 128, 128))
+    off = torch.tensor([0] + lens).cumsum(0).to(torch.int32).to(dev) if packed else None
+    if not packed:
+        q, k, v = (x.unflatten(0, (2, 1500)) for x in (q, k, v))
+    need = mixer_binding._decay_workspace(sum(lens), len(lens), packed, 4, 128, 128)
+    assert need >= 4 * 128 * 128 * 4  # (it is cut)
+    ref = moe.gdn_decay_scan(q, k, v, decay, s, off)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    for stream in (side, side.cuda_stream):
+        got.append(moe.gdn_decay_scan(q, k, v, decay, s, off, stream=stream))
+        with torch.cuda.stream(side):
+            torch.empty(need, dtype=torch.uint8, device=dev).fill_(0xff)
+    side.synchronize()
+    with torch.cuda.stream(side):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            cap = moe.gdn_decay_scan(q, k, v, decay, s, off)
+    for _ in range(3):
+        cap[0].zero_()
+        cap[1].zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        got.append(tuple(x.clone() for x in cap))
+    for o, S in got:
+        assert torch.equal(o, ref[0]) and torch.equal(S, ref[1])
 
 
 @pytest.mark.parametrize("lens", [(37, 0, 130, 5), (1,), (200, 64, 63)])
