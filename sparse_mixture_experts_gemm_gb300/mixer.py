@@ -26,6 +26,7 @@ _BF16, _F32, _F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 _DTYPES = {_BF16: MOE_BF16, _F32: MOE_F32}
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+_gpus = 0  # how many there are, once known
 _NONE = contextlib.nullcontext()
 _L = None
 
@@ -50,8 +51,14 @@ def _on(stream, device):
 
 
 def _device(first, *others):
-    """The device of all these tensors (None: not given), which has to be the
-    current one."""
+    """The device of all these CUDA tensors (None: not given), which has to be
+    the current one.  (Where there is one GPU it is that: asking every tensor
+    costs a call 1 to 2 us.)"""
+    global _gpus
+    if _gpus == 1:
+        return 0
+    if not _gpus:
+        _gpus = torch.cuda.device_count()
     device = first.get_device()
     for t in others:
         if t is not None and t.get_device() != device:

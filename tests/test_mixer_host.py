@@ -301,6 +301,7 @@ def launches(monkeypatch):
     monkeypatch.setattr(binding, "_raw_stream", lambda dev: 0)
     monkeypatch.setattr(binding, "_decay_workspace", lambda *a: 0)
     monkeypatch.setattr(binding, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(binding, "_gpus", 2, raising=False)
     return seen
 
 
