@@ -435,6 +435,21 @@ def test_scan_shares(dev):
     assert torch.equal(o, o2) and torch.equal(S, sd)
 
 
+@pytest.mark.parametrize("lens", [[1, 700, 0, 2049, 37, 1311, 64, 300, 999], [2900], [17, 2100, 16, 1800, 1700]])
+def test_scan_packed_and_cut_within_the_bound(dev, lens):
+    """Packed sequences of few heads, cut where SMs are idle: every output within
+    the bound of test_scan_shares."""
+    q, k, v, decay, s = scan_inputs(23, sum(lens), len(lens), 2, 4, 128, 128)
+    off = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    assert mixer_binding._decay_workspace(sum(lens), len(lens), True, 4, 128, 128) >= 4 * 128 * 128 * 4
+    o, S = moe.gdn_decay_scan(*(x.to(dev) for x in (q, k, v, decay, s, off)))
+    ro, rs = mixer.decay_scan(f64(q), f64(k), f64(v), f64(decay), f64(s), off)
+    terms, _ = mixer.decay_scan(*(np.abs(f64(x)) for x in (q, k, v)), f64(decay), np.abs(f64(s)), off)
+    assert (np.abs(f64(o) - ro) <= 2.0 ** -8 * (np.abs(ro) + terms) * (1 + 2.0 ** -6)).all()
+    assert np.linalg.norm(f64(o) - ro) <= 2.0 ** -8 * np.linalg.norm(ro)
+    assert (np.abs(f64(S) - rs).max((2, 3)) <= S_TOL * np.abs(rs).max((2, 3))).all()
+
+
 @pytest.mark.parametrize("T,Hk,Hv,dv", [(4800, 10, 30, 256), (6401, 6, 60, 80), (10001, 16, 32, 128)])
 def test_scan_shares_in_pieces(dev, T, Hk, Hv, dv):
     """One call against short ones that pass the state along."""
@@ -533,6 +548,22 @@ def test_scan_nan_reaches_no_earlier_token(dev, T, at, bad):
     assert not np.isfinite(S[~rows]).any()
     err = np.abs(S - clean[1].reshape(S.shape))[rows]
     assert err.max() <= S_TOL * np.abs(clean[1]).max()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T,at", [(8, 3), (300, 100), (300, 130), (3000, 2000)])
+def test_scan_nan_in_k_or_q_reaches_no_earlier_token(dev, T, at, bad):
+    """No bit of the outputs before the token changes; one in q changes no other
+    token's outputs and no state either."""
+    q, k, v, decay, s = (x.to(dev) for x in scan_inputs(22, T, 1, 1, 2, 128, 80))
+    o, S = moe.gdn_decay_scan(q, k, v, decay, s[0])
+    kb, qb = k.clone(), q.clone()
+    kb[at, 0, 5], qb[at, 0, 5] = bad, bad
+    o2, S2 = moe.gdn_decay_scan(q, kb, v, decay, s[0])
+    assert torch.equal(o2[:at], o[:at]) and not torch.isfinite(S2[..., 5]).any()
+    o3, S3 = moe.gdn_decay_scan(qb, k, v, decay, s[0])
+    rest = [t for t in range(T) if t != at]
+    assert torch.equal(o3[rest], o[rest]) and torch.equal(S3, S) and not torch.isfinite(o3[at]).any()
 
 
 def test_other_stream(dev):
