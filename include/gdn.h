@@ -74,7 +74,8 @@ int gdn_scan(const void *q, const void *k, const void *v, const float *alpha, co
  *   state_in  float32 [n_seq][n_v_heads][d_v][d_k], or NULL for zero states
  *   state_out float32, same layout, or NULL; may be state_in.  A sequence
  *             without tokens gets its state_in.
- *   o         bf16 [n_tokens][n_v_heads][d_v], contiguous, round-to-nearest
+ *   o         bf16 [n_tokens][n_v_heads][d_v], contiguous, round-to-nearest,
+ *             overlapping none of the inputs
  *   offsets   int32 [n_seq + 1] in device memory: sequence i is the tokens
  *             offsets[i] .. offsets[i + 1] - 1 (from 0, never decreasing, to
  *             n_tokens; lengths may be 0).  Values outside that are clamped to
@@ -90,8 +91,10 @@ int gdn_scan(const void *q, const void *k, const void *v, const float *alpha, co
  * of each term, so that an output whose terms cancel has lost as much).
  * A long sequence may be taken in pieces, passing the state along; pieces
  * agree with one call up to these roundings.  The same inputs give the same
- * bits.  NaN and infinities of one sequence reach no other.  The caller applies the model's
- * preprocessing (norms, query scale) before the call.
+ * bits.  NaN and infinities of one sequence reach no other, nor its earlier
+ * tokens; in the chunked form an infinity in k or v may become NaN in the state.
+ * The caller applies the model's preprocessing (norms, query scale) before the
+ * call.
  * Supported: d_k 64 or 128, d_v a multiple of 16 up to 1024, n_v_heads a
  * multiple of n_k_heads and at most 4096, n_tokens < 2^31, strides < 2^39.
  * Pointers 16-byte aligned (decay and offsets 4-byte), strides multiples of 8.
@@ -110,8 +113,10 @@ int gdn_decay_scan(const void *q, const void *k, const void *v, const float *dec
                    long long q_stride, long long k_stride, long long v_stride, void *workspace,
                    size_t workspace_bytes, void *cuda_stream);
 
-/* Bytes of workspace that gdn_decay_scan wants for these sizes; ragged: 1 for
- * a call with offsets, 0 for one without (host only). */
+/* Bytes of workspace that gdn_decay_scan wants for these sizes, whatever the
+ * number of key heads; ragged: 1 for a call with offsets, 0 for one without
+ * (host only).  It holds the states between the segments of cut sequences: with
+ * offsets, at most two for each segment's length of the tokens. */
 int gdn_decay_workspace(long long n_tokens, int n_seq, int ragged, int n_v_heads, int d_k, int d_v,
                         size_t *bytes);
 

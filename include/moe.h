@@ -390,6 +390,10 @@ int moe_noalloc_status(void *cuda_stream, int *detail);
  *     s = x + residual                       (x alone where residual is NULL)
  *     out = s * weight / sqrt(mean(s^2) + eps)
  * and sum = s, each rounded once to dtype.  The norm uses the unrounded s.
+ * Finite rows have their norm whatever their size (also where s^2 leaves
+ * float32's range); s * weight is a float32 product, and a row in which it
+ * exceeds the range counts as one with an infinity.  With eps = 0 a row of zeros
+ * gives zeros.
  *   x, residual  dtype, rows x_stride / residual_stride elements apart
  *                (residual NULL: none, its stride is ignored)
  *   weight       dtype [d]
@@ -422,8 +426,9 @@ int moe_quantize_fp8(const void *w, moe_dtype dtype, long long rows, int cols, l
 /*
  * Matrix product of e4m3 codes with a scale per token and a scale per output
  * channel, out bf16 [T][N]:
- *     out[t][n] = x_scales[t] * w_scales[n] * sum_k x[t][k] * w[n][k]
- * summed in float32 and rounded once.
+ *     out[t][n] = (x_scales[t] * w_scales[n]) * sum_k x[t][k] * w[n][k]
+ * in float32 and rounded once; the scales' product is formed first, so it has to
+ * stay in float32's range.
  *   x  codes [T][K], rows x_stride bytes apart;  x_scales float32 [T]
  *   w  codes [N][K], rows w_stride bytes apart;  w_scales float32 [N]
  *   out  rows out_stride elements apart, overlapping none of the inputs

@@ -9,7 +9,7 @@
 // write (2 operations an element) and one dot product per row.  One token per
 // sequence reads and writes the state once and little else, so it is bound by
 // memory: 64 sequences of 32 heads of 128 x 128 take 40.8 us (6.6 TB/s, a
-// plain copy's rate), one sequence 2.0 us.  With more tokens the dot
+// plain copy's rate), one sequence 2.2 us.  With more tokens the dot
 // products' sums count: the lanes trade rows while they add (9 shuffles for 8
 // rows, where a tree per row takes 40), and the next token is fetched ahead:
 // 8 tokens of 64 sequences 113 -> 73 us.  Four rows a lane are as fast for

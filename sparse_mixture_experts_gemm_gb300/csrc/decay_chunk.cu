@@ -30,9 +30,11 @@
 // bf16 (rms 1.7e-3) in the end; S (the state's part of an output) and P (the
 // chunk's own part) enter their products as bf16, as large a rounding each on
 // its part, so that an output's rms error is sqrt(2) times that of the last
-// rounding alone (2.35e-3).  Two bf16 parts of S and of P take that away; an
-// earlier form of this kernel had them, and without them (and with a transposed
-// output tile) a 4,096-token call went from 67 to 63 us.
+// rounding alone (2.35e-3).  Two bf16 parts of S and of P take that away
+// (1.66e-3) and cost a quarter of the time: 4,096 tokens 63 us, 32,768 334 us,
+// because S's second part finds no free TMEM columns and waits for the first
+// one's product (60 / 308 us; P's alone 53 / 272); with one accumulator for both
+// products of an output, which frees columns, 65 / 345.
 //
 // Work split.  One CTA scans one segment of one (sequence, value head, 128
 // columns of d_v).  A sequence is one segment when the batch has enough heads
@@ -52,9 +54,9 @@
 // 128 bytes a cycle): operands that threads make go to TMEM where the MMA can
 // take them from there (V~, S), and the scores use 64 rows.
 //
-// Measured, 32 value heads on 16 key heads of 128 x 128: 51.4 us for 4,096
+// Measured, 32 value heads on 16 key heads of 128 x 128: 51 us for 4,096
 // tokens (segments 20, chain 5, main 33, their starts overlapped; one CTA per
-// head without segments 95), 258 us for 32,768 (3.1 TB/s of q, k, v, o)
+// head without segments 95), 257 us for 32,768 (3.1 TB/s of q, k, v, o)
 // in a graph.
 // A chunk of the main launch takes 1.4 us, 2,650 cycles, for products of 1,984
 // cycles: its time is the chain V~ -> U -> the TMEM columns of V~ free again,
@@ -164,12 +166,6 @@ __device__ __forceinline__ void tmem_ld_16x32x2_sync(uint32_t ta, uint32_t tb, f
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// a pair rounded to bf16, the first in the low half
-__device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // shared-memory accesses by 32-bit address
@@ -442,11 +438,6 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   tc_fence_before();
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
-}
-
-__device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
-  return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) &
-                                     ~static_cast<uintptr_t>(1023));
 }
 
 // Shared memory: the stages of (Q, K, V), P, a 32 x 32 output tile for each of

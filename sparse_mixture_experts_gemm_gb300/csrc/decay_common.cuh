@@ -9,7 +9,7 @@
 namespace moe {
 
 constexpr int kChunkTok = 64;  // tokens per chunk of the chunked form
-constexpr int kGpuSms = 152;
+constexpr int kGpuSms = 152;   // (the plan is the host's alone and asks no device)
 
 // One segment of a packed sequence that takes the chunked form.
 struct alignas(16) Segment {

@@ -17,10 +17,11 @@
 //     (512 TMEM columns), so that one tile is drained while the next is
 //     multiplied.
 // Measured (calls back to back in a graph, weights from DRAM): one token x 8192
-// x 2048 6.9 us (2.5 for its weights at a copy's rate; the rest is the start,
+// x 2048 6.8 us (2.5 for its weights at a copy's rate; the rest is the start,
 // the sums' exchange and the end), 16 x 2048 x 4096 6.0 us, 301 x 2500 x 2048
-// 9.8 us, 4096 x 8192 x 2048 40.9 us (3.4 PFLOP/s; tensor pipes busy 82 % of an
-// SM's cycles), 16384 x 8192 x 2048 152 us (3.3 PFLOP/s, at the power limit).
+// 9.7 us, 4096 x 8192 x 2048 40.6 us (3.4 PFLOP/s; tensor pipes busy 82 % of an
+// SM's cycles), 16384 x 8192 x 2048 152 us (3.6 PFLOP/s); over seconds 178 us
+// (3.1 PFLOP/s), where the power limit holds the SMs at 1,335 MHz.
 // Every wait is bounded; one that runs out raises the CTA's abort flag and
 // records a timeout in the status word of the calls without a handle.
 #include <cuda_bf16.h>
@@ -59,16 +60,6 @@ struct MatmulArgs {
 __device__ __forceinline__ void fail(const MatmulArgs &p, volatile int *abort_flag, int site) {
   *abort_flag = 1;
   report_error(p.status, MOE_ERR_DEVICE_TIMEOUT, KID_MATMUL_FP8 * 100 + site);
-}
-
-__device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t *>(&v);
-}
-
-__device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
-  return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) &
-                                     ~static_cast<uintptr_t>(1023));
 }
 
 }  // namespace

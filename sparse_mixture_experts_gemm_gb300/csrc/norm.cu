@@ -16,7 +16,8 @@
 // holds one row.  Rows of whole 16-byte vectors move as such; rows of another
 // width one element per lane and load, neighbouring lanes on neighbouring
 // elements (16,384 rows of 1,001: 29 us; cutting such rows into vectors with
-// ragged ends took 32, because the weights lie differently in every row).
+// ragged ends took 32, because the weights lie differently in every row).  Odd
+// widths past 4,096 leave that rate: codes of 16,384 x 4,097 take 292 us.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -286,8 +287,10 @@ cudaError_t launch_norm(const NormArgs &a, cudaStream_t st) {
 // depends neither on where its tensors lie nor on how many rows there are.  Two
 // to four vectors per thread (with a residual and codes, 16,384 rows of 2,048
 // bf16 timed one call at a time: 42.4 us with 64 threads of 4, 42.6 with 128 of
-// 2, 48.9 with 256 of 1; back to back 37.6 us, 6.2 TB/s; one row: 5.5 us each,
-// 2.0 in a graph).
+// 2, 48.9 with 256 of 1; back to back 38.0 us, 6.2 TB/s; one row: 2.2 in a
+// graph).  Rows off the 16-byte boundaries keep their elements' threads and are
+// read element by element: codes of 16,384 x 4,096 from column 3 of a wider
+// tensor 60 to 75 us, from column 0 46.
 // Blocks that stay and take several rows, loading ahead, were slower (67 us).
 template <typename T>
 cudaError_t pick_norm(const NormArgs &a, cudaStream_t st) {
