@@ -447,6 +447,124 @@ int moe_matmul_fp8(const uint8_t *x, const float *x_scales, int T, long long x_s
                    const uint8_t *w, const float *w_scales, int N, int K, long long w_stride,
                    void *out, long long out_stride, void *cuda_stream);
 
+/*
+ * The operators of a full-attention layer: norm and position rotation of
+ * queries and keys, causal attention of prompts, a key/value cache in 4 bits
+ * and attention of new tokens over it.  Several query heads share a key/value
+ * head: query head h goes with key/value head h / (n_q_heads / n_kv_heads).
+ * They need no handle and allocate nothing.  Everything is bfloat16 outside
+ * and float32 inside; each result is rounded once.  Supported: head_dim 128 or
+ * 256, up to 4096 heads of either kind (rotation, cache, decode) and 64 query
+ * heads per key/value head (prefill), fewer than 2^31 tokens, strides < 2^38.
+ * Pointers are device memory, 16-byte aligned (int32 arrays 4, doubles 8);
+ * strides, in elements from one token to the next, are multiples of 8, and the
+ * heads of a token lie side by side.  Asynchronous on cuda_stream; the checks
+ * are made on the host before anything is launched.  No tokens or no sequences
+ * is a no-op returning MOE_OK.  The same inputs give the same bits.  The first
+ * call on a device looks up the status word of the calls without a handle, so
+ * make it before any stream capture.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, CUDA.
+ *
+ * Packed sequences: offsets int32 [n_seq + 1] on the device, sequence i being
+ * the rows offsets[i] .. offsets[i + 1] - 1 (from 0, never decreasing; lengths
+ * may be 0).  Values outside the tensor are clamped to it (what a row that then
+ * lies in several sequences gets is not defined); rows of no sequence are not
+ * written.  NULL: n_seq sequences of equal length.
+ */
+
+/*
+ * Root-mean-square norm of every head's row of queries and keys, and in the same
+ * pass the rotation of its first rot_dim columns by the token's position:
+ *     y = x * weight / sqrt(mean(x^2) + eps),   a_i = position * inv_freq[i]
+ *     out[i]         = y[i] cos a_i - y[i + rot_dim / 2] sin a_i
+ *     out[i + rot_dim / 2] = y[i + rot_dim / 2] cos a_i + y[i] sin a_i
+ * for i < rot_dim / 2; the other columns are y.  The angle is reduced in 64 bits,
+ * so far positions lose nothing.  Finite rows have their norm whatever their
+ * size; with eps = 0 a row of zeros gives zeros.
+ *   q, k               bf16 [n_tokens][heads][head_dim]
+ *   q_weight, k_weight bf16 [head_dim]
+ *   positions          int32 [n_tokens];  inv_freq  double [rot_dim / 2], radians
+ *                      per position (both unused when rot_dim is 0)
+ *   q_out, k_out       as q and k; may be q and k themselves (same stride)
+ * rot_dim: a multiple of 16, 0 .. head_dim.
+ */
+int moe_qk_norm_rope(const void *q, const void *k, const void *q_weight, const void *k_weight,
+                     const int32_t *positions, const double *inv_freq, long long n_tokens,
+                     int n_q_heads, int n_k_heads, int head_dim, int rot_dim, long long q_stride,
+                     long long k_stride, float eps, void *q_out, long long q_out_stride,
+                     void *k_out, long long k_out_stride, void *cuda_stream);
+
+/*
+ * Causal attention of whole prompts.  The queries of a sequence are the last of
+ * its keys: with Lq queries and Lk keys, query i sees the keys
+ * j <= i + Lk - Lq, and
+ *     o_i = sum_j softmax_j(scale * q_i . k_j) v_j .
+ * A query that sees no key (Lk < Lq) gets zeros.
+ *   q    bf16 [n_q][n_q_heads][head_dim];  k, v  bf16 [n_k][n_kv_heads][head_dim]
+ *   out  bf16 [n_q][n_q_heads][head_dim], contiguous, overlapping none of the inputs
+ *   offsets, k_offsets: the sequences' queries and keys; k_offsets NULL: the same
+ *        as offsets (n_k == n_q).  Both NULL: n_seq sequences of n_q / n_seq
+ *        queries and n_k / n_seq keys.
+ * scale > 0 and finite.  A NaN or infinity in k or v reaches no query that does
+ * not see its token.
+ */
+int moe_attention_prefill(const void *q, const void *k, const void *v, const int32_t *offsets,
+                          const int32_t *k_offsets, long long n_q, long long n_k, int n_seq,
+                          int n_q_heads, int n_kv_heads, int head_dim, long long q_stride,
+                          long long k_stride, long long v_stride, float scale, void *out,
+                          void *cuda_stream);
+
+/*
+ * A key/value cache in the 4-bit group-affine format of moe_quantize_q4, in pages
+ * of 64 tokens.  Two device arrays:
+ *   codes   uint8 [n_pages][2][n_heads][64][head_dim / 2]: keys, then values;
+ *           two codes per byte, the even column in the low half
+ *   affine  bf16 [n_pages][2][n_heads][64][head_dim / 64][2]: scale and bias of
+ *           each 64 columns
+ * and a value is scale * code + bias.  pages int32 [n_seq][table_width] says
+ * where a sequence's tokens are: position p is token p % 64 of page
+ * pages[i][p / 64].  A page number outside [0, n_pages) or a position past the
+ * table is skipped (written nowhere, read as zeros, not attended to) and recorded
+ * as MOE_ERR_DEVICE_BOUNDS in the status word (moe_noalloc_status).
+ * n_pages * n_heads <= 2^24 - 1.
+ *
+ * moe_kv_write quantises k and v, bf16 [n_tokens][n_heads][head_dim], and puts
+ * sequence i's tokens at its positions starts[i], starts[i] + 1, .. (starts NULL:
+ * from 0).  Per 64 columns:  bias = bf16(min), scale = bf16((max - min) / 15),
+ * code = round((x - bias) / scale) in 0 .. 15 (0 where scale is 0).  64 columns
+ * that hold a NaN or an infinity read back as NaN.  Two tokens of one call must
+ * not go to the same place of the same page.
+ * moe_kv_read is the way back: k_out, v_out bf16 [n_tokens][n_heads][head_dim],
+ * contiguous, from the same positions, each value rounded once.
+ */
+int moe_kv_write(uint8_t *codes, uint16_t *affine, long long n_pages, const void *k, const void *v,
+                 const int32_t *pages, int table_width, const int32_t *starts,
+                 const int32_t *offsets, long long n_tokens, int n_seq, int n_heads, int head_dim,
+                 long long k_stride, long long v_stride, void *cuda_stream);
+int moe_kv_read(const uint8_t *codes, const uint16_t *affine, long long n_pages,
+                const int32_t *pages, int table_width, const int32_t *starts,
+                const int32_t *offsets, long long n_tokens, int n_seq, int n_heads, int head_dim,
+                void *k_out, void *v_out, void *cuda_stream);
+
+/*
+ * Attention of one query token per sequence over that cache:
+ *     o = sum_t softmax_t(scale * q . k_t) v_t   over positions t < lengths[i],
+ * with k_t and v_t the cache's values (not rounded to bf16).
+ *   q    bf16 [n_seq][n_q_heads][head_dim], sequences q_stride elements apart
+ *   lengths int32 [n_seq], tokens in the cache; 0 gives zeros
+ *   out  bf16 [n_seq][n_q_heads][head_dim], contiguous
+ *   workspace: device memory of at least the bytes that
+ *        moe_attention_decode_workspace gives for the same sizes, 16-byte
+ *        aligned, used by the call's kernels alone; NULL where that is 0
+ */
+int moe_attention_decode(const void *q, long long q_stride, const uint8_t *codes,
+                         const uint16_t *affine, long long n_pages, const int32_t *pages,
+                         int table_width, const int32_t *lengths, int n_seq, int n_q_heads,
+                         int n_kv_heads, int head_dim, float scale, void *out, void *workspace,
+                         size_t workspace_bytes, void *cuda_stream);
+int moe_attention_decode_workspace(int n_seq, int table_width, int n_q_heads, int n_kv_heads,
+                                   int head_dim, size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

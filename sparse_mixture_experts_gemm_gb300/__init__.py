@@ -46,7 +46,9 @@ EXPORTED = ["moe_create", "moe_route", "moe_forward", "moe_forward_routed", "moe
             "moe_strerror", "moe_profile", "moe_profile_read", "moe_debug_wait_timeout",
             "moe_decode_noalloc", "moe_noalloc_status", "moe_create_q4", "moe_quantize_q4",
             "gdn_scan", "moe_add_rmsnorm", "moe_add_rmsnorm_fp8", "moe_quantize_fp8",
-            "moe_matmul_fp8", "gdn_decay_scan", "gdn_decay_workspace"]
+            "moe_matmul_fp8", "gdn_decay_scan", "gdn_decay_workspace", "moe_qk_norm_rope",
+            "moe_attention_prefill", "moe_kv_write", "moe_kv_read", "moe_attention_decode",
+            "moe_attention_decode_workspace"]
 
 Q4_GROUP = 64  # columns per (scale, bias) pair of the 4-bit format
 
@@ -124,6 +126,13 @@ def lib() -> ctypes.CDLL:
     L.gdn_decay_scan.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ll, ip, ip, ip, ip, ip, ll, ll,
                                  ll, vp, ctypes.c_size_t, vp]
     L.gdn_decay_workspace.argtypes = [ll, ip, ip, ip, ip, ip, ctypes.POINTER(ctypes.c_size_t)]
+    sz = ctypes.c_size_t
+    L.moe_qk_norm_rope.argtypes = [vp, vp, vp, vp, vp, vp, ll, ip, ip, ip, ip, ll, ll, fp, vp, ll, vp, ll, vp]
+    L.moe_attention_prefill.argtypes = [vp, vp, vp, vp, vp, ll, ll, ip, ip, ip, ip, ll, ll, ll, fp, vp, vp]
+    L.moe_kv_write.argtypes = [vp, vp, ll, vp, vp, vp, ip, vp, vp, ll, ip, ip, ip, ll, ll, vp]
+    L.moe_kv_read.argtypes = [vp, vp, ll, vp, ip, vp, vp, ll, ip, ip, ip, vp, vp, vp]
+    L.moe_attention_decode.argtypes = [vp, ll, vp, vp, ll, vp, ip, vp, ip, ip, ip, ip, fp, vp, vp, sz, vp]
+    L.moe_attention_decode_workspace.argtypes = [ip, ip, ip, ip, ip, ctypes.POINTER(sz)]
     for name in EXPORTED:
         if name != "moe_strerror":
             getattr(L, name).restype = ip
@@ -238,7 +247,8 @@ def moe_decode_noalloc(cfg: moe_config, x, out, stream=None) -> int:
 
 def moe_noalloc_status(stream=None) -> tuple[int, int]:
     """(code, detail) of the device status word of the calls without a handle
-    (moe_decode_noalloc, moe_matmul_fp8, gdn_decay_scan) on the current device;
+    (moe_decode_noalloc, moe_matmul_fp8, gdn_decay_scan, the attention layer's
+    operators) on the current device;
     synchronises the stream and clears the word."""
     detail = ctypes.c_int(0)
     rc = lib().moe_noalloc_status(_stream(stream), ctypes.byref(detail))
@@ -428,15 +438,23 @@ def gdn_scan(q, k, v, alpha, beta, state=None, out=None, state_out=None, stream=
     return out, state_out
 
 
-# ---------------------------------------------------- the mixer's operators
+# ------------------------------ the mixer's and the attention layer's operators
 _MIXER = ("add_rmsnorm", "add_rmsnorm_fp8", "quantize_fp8", "matmul_fp8", "gdn_decay_scan")
+_ATTENTION = ("qk_norm_rope", "attention_prefill", "kv_cache", "kv_cache_write", "kv_cache_read",
+              "attention_decode")
 
 
 def __getattr__(name):
-    """The functions of mixer.py, loaded (with torch) when first used."""
+    """The functions of mixer.py and attention.py, loaded (with torch) when first
+    used."""
     if name in _MIXER:
         from . import mixer
         for n in _MIXER:
             globals()[n] = getattr(mixer, n)
+        return globals()[name]
+    if name in _ATTENTION:
+        from . import attention
+        for n in _ATTENTION:
+            globals()[n] = getattr(attention, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

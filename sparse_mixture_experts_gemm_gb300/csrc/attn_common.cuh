@@ -1,0 +1,92 @@
+// attn_common.cuh -- what the kernels of a full-attention layer share: the
+// sequences of a packed call and the pages of a 4-bit key/value cache.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/moe.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace moe {
+
+constexpr int kPage = 64;   // tokens per page of the cache
+constexpr int kGroup = 64;  // columns that share a scale and a bias
+
+// rows lo .. hi of sequence i; offsets outside [0, total] or running backwards
+// are clamped.  offsets null: n sequences of total / n rows.
+__device__ __forceinline__ void seq_rows(const int *offsets, int n, long long total, int i, int &lo,
+                                         int &hi) {
+  if (offsets) {
+    lo = static_cast<int>(min(max(static_cast<long long>(offsets[i]), 0LL), total));
+    hi = static_cast<int>(min(max(static_cast<long long>(offsets[i + 1]), static_cast<long long>(lo)), total));
+  } else {
+    const int len = static_cast<int>(total / n);
+    lo = i * len;
+    hi = lo + len;
+  }
+}
+
+// The sequence that row t of a packed call belongs to, -1 for none: the last
+// one that starts at or before t.  All lanes of the warp call it with the same
+// t; each step narrows the range to a 32nd with one load per lane.
+__device__ __forceinline__ int seq_of_row(const int *offsets, int n, long long total, int t) {
+  if (!offsets) return t / static_cast<int>(total / n);
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = n;  // the answer, if there is one, is in lo .. lo + len - 1
+  while (true) {
+    const int step = (len + 31) / 32, at = lo + lane * step;
+    const bool in = lane * step < len && offsets[at] <= t;
+    const int c = __popc(__ballot_sync(0xffffffffu, in));
+    if (c == 0) return -1;
+    lo += (c - 1) * step;
+    len = min(step, n - lo);
+    if (step == 1) break;
+  }
+  return offsets[lo + 1] > t ? lo : -1;
+}
+
+// A key/value cache: codes [pages][2][heads][64][D / 2] (keys, then values; the
+// even column in the low half of a byte), affine [pages][2][heads][64][D / 64][2]
+// (bf16 scale, bias).  table [n_seq][width]: page numbers of each sequence.
+struct CacheArgs {
+  uint8_t *codes;
+  uint32_t *affine;  // one (scale, bias) pair per word, the scale in the low half
+  const int *table;
+  long long n_pages;
+  int width, H, D;
+  int *status;
+};
+
+// the page of position `at` of sequence i, -1 where there is none
+__device__ __forceinline__ int page_of(const CacheArgs &c, int i, long long at) {
+  if (at < 0 || at >= static_cast<long long>(c.width) * kPage) return -1;
+  const int p = c.table[static_cast<long long>(i) * c.width + at / kPage];
+  return p >= 0 && p < c.n_pages ? p : -1;
+}
+// the row of a page's token: index into codes in rows of D / 2 bytes, into
+// affine in rows of D / 64 words
+__device__ __forceinline__ long long cache_row(const CacheArgs &c, int page, int which, int h, int place) {
+  return ((static_cast<long long>(page) * 2 + which) * c.H + h) * kPage + place;
+}
+
+// one launch as a programmatic dependent of the kernel before it
+template <typename K, typename... Args>
+cudaError_t launch_attn(K kern, dim3 grid, int threads, int smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+inline bool off_boundary(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) != 0; }
+
+}  // namespace moe

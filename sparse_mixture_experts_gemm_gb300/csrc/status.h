@@ -15,6 +15,9 @@ enum KernelId {
   KID_MATMUL_FP8 = 7,
   KID_DECAY = 8,
   KID_DEBUG = 9,
+  KID_KV_CACHE = 10,
+  KID_ATTN_PREFILL = 11,
+  KID_ATTN_DECODE = 12,
 };
 
 enum WaitSite {
