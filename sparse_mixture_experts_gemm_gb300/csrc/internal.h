@@ -197,6 +197,10 @@ bool encode_map_2d(CUtensorMap *m, const void *base, size_t esz, uint64_t rows, 
                    uint32_t box_cols, uint32_t box_rows, bool swizzle128, uint64_t pitch = 0,
                    bool swizzle64 = false);
 
+// a 3D map of bf16, 128-byte swizzle (sizes and box innermost first; p1, p2: bytes)
+bool encode_map_3d(CUtensorMap *m, const void *base, uint64_t n0, uint64_t n1, uint64_t n2,
+                   uint64_t p1, uint64_t p2, uint32_t b0, uint32_t b1, uint32_t b2);
+
 // route.cu
 template <typename T>
 cudaError_t launch_router_simt(const T *x, const T *wr, const float *bias, int T_tok, int d, int E,

@@ -76,6 +76,21 @@ bool moe::encode_map_2d(CUtensorMap *m, const void *base, size_t esz, uint64_t r
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 3D map of bf16 [n2][n1][n0], 128-byte swizzle; p1, p2: bytes from one index of
+// n1, n2 to the next.
+bool moe::encode_map_3d(CUtensorMap *m, const void *base, uint64_t n0, uint64_t n1, uint64_t n2,
+                        uint64_t p1, uint64_t p2, uint32_t b0, uint32_t b1, uint32_t b2) {
+  EncodeTiledFn enc = get_encode();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {n0, n1, n2};
+  cuuint64_t strides[2] = {p1, p2};
+  cuuint32_t box[3] = {b0, b1, b2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 // The GEMM operand map: boxes of 128 bytes of columns x box_rows rows, 128-byte swizzle.
