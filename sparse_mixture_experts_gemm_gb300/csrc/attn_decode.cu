@@ -1,10 +1,33 @@
 // attn_decode.cu -- attention of one query token per sequence over a cache held
 // in 4 bits (moe_attention_decode in include/moe.h):
-//     o = sum_t softmax_t(scale q . k_t) v_t,   k_t, v_t = scale * code + bias
-// A warp has one query head of a sequence; the running maximum and sum of the
-// softmax are kept in fp32 and the output accumulated in registers.
+//     o = sum_t softmax_t(scale q . k_t) v_t,   k_t, v_t = scale_t * code + bias_t
+//
+// Bound by the cache's bytes, so every page is read once for the 8 query heads
+// that share it, and the codes go to the tensor cores as they are:
+//     q . k_t = sum_g [ s_tg (q_g . c_tg) + b_tg sum(q_g) ]       g: groups of 64 columns
+//     o_g     = sum_t (p_t s'_tg) (c'_tg - 8) + sum_t p_t (b'_tg + 8 s'_tg)
+// with codes c exact in bf16 (128 + c is one AND-OR away from a nibble), products
+// and sums in fp32, scales and biases applied in fp32.  The only rounding before
+// the result's is that of p_t s'_tg to bf16 (2^-8), which multiplies codes less 8:
+// centred, the sum has no large part that cancels against the bias's.  For the
+// scores 128 is left on the codes and taken off by the bias, -128 s sum(q): four
+// products of 16 columns add up in between, too few to lose anything.
+//
+// Work split.  All (sequence, key/value head, 8 query heads) rows' pages lie on one
+// line that is cut into equal shares, one per SM, whatever the lengths; a CTA
+// finds its share from the lengths on the device.  Rows that are cut leave their
+// parts (maximum, sum, output) in the workspace for a second kernel, which joins
+// them in a fixed order.
+//
+// Roles: warp 8 copies pages by TMA (8 pages deep), warps 0-7 take 16 tokens of a
+// page each, four warps per page, with a running softmax of their own; their parts
+// are joined through shared memory at a row's end.  M of the first product is the
+// query heads, of the second the columns, so that P leaves the one in the layout
+// in which the other takes it.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <mutex>
 
 #include "../../include/moe.h"
 #include "attn_common.cuh"
@@ -13,7 +36,14 @@ namespace moe {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kConsumers = 8;
+constexpr int kThreadsD = 32 * (kConsumers + 1);
+constexpr int kHeads = 8;  // query heads of a row
+constexpr int kPagesDeep = 8;
+constexpr int kJoinThreads = 512;
+constexpr float kLateDecode = 8.0f;  // as in attn_prefill.cu
+constexpr int kShares = 152;         // one per SM
+static_assert(kShares <= kJoinThreads, "a thread per part");
 
 struct DecodeAttnArgs {
   CacheArgs c;
@@ -21,70 +51,592 @@ struct DecodeAttnArgs {
   __nv_bfloat16 *out;
   const int *lengths;
   long long qs;
-  int n_seq, Hq;
-  float scale;  // times log2(e)
+  int n_seq, Hq, group, blocks;  // blocks: rows of a key/value head, 8 query heads each
+  float scale;                   // times log2(e)
+  int4 *head;                    // [kShares]: what is to be joined
+  float *part;                   // [2 kShares][8][D + 2]: output, maximum, sum
 };
+
+template <int D>
+struct Page {
+  static constexpr int kCodes = kPage * D / 2, kAffine = kPage * (D / kGroup) * 4;
+  static constexpr int kBytes = 2 * (kCodes + kAffine);
+  static constexpr int kPitch = D + 8;  // of the warps' outputs
+  static constexpr int kOut = kConsumers * kHeads * kPitch * 4;
+  static constexpr int kCtl = 4096;
+  static constexpr int kTotal = kPagesDeep * kBytes + kOut + kCtl + 1024;
+  static_assert(kTotal <= 227 * 1024 && kBytes % 1024 == 0, "shared memory");
+};
+
+struct DCtl {
+  uint64_t full[kPagesDeep], empty[kPagesDeep];
+  int ok[kPagesDeep];  // whether the stage holds a page
+  int abort_flag, seq;
+  long long at;  // the share's first unit within sequence seq's
+  long long warp_sum[kConsumers + 1];
+  float m[kConsumers][kHeads], l[kConsumers][kHeads], e[kConsumers][kHeads][4];
+};
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&v)[N]) {
+  if constexpr (N == 4) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(a)
+                 : "memory");
+  } else {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(a) : "memory");
+  }
+}
+// nibbles 0 and 4 of w as bf16 128 + c
+__device__ __forceinline__ uint32_t plus128(uint32_t w) { return (w & 0x000f000fu) | 0x43004300u; }
+__device__ __forceinline__ uint32_t centred(uint32_t w) {  // c - 8
+  const uint32_t u = plus128(w);
+  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&u), __float2bfloat162_rn(136.0f));
+  return *reinterpret_cast<const uint32_t *>(&d);
+}
+
+// Token of 8 that column n of a score tile stands for: chosen so that the rows
+// that lanes read at once, columns n = 0 .. 3 and 4 .. 7 (keys) and all even or odd
+// n (values), lie in different quarters of the 128 bytes of shared-memory banks,
+// given the copies' swizzle.
+template <int D>
+__device__ __forceinline__ int token_of(int n) {
+  const int f = n < 4 ? n : (n ^ 1) & 3, b = n >> 2;
+  return D == 256 ? 2 * f + b : (f & 1) | b << 1 | (f >> 1) << 2;
+}
+// byte of a row of codes in a stage, swizzled by TMA (128-byte or 64-byte pattern)
+template <int D>
+__device__ __forceinline__ uint32_t code_at(int row, int byte) {
+  if constexpr (D == 256)
+    return row * 128 + ((((byte >> 4) ^ row) & 7) << 4) + (byte & 15);
+  else
+    return row * 64 + ((((byte >> 4) ^ (row >> 1)) & 3) << 4) + (byte & 15);
+}
+
+// tokens of sequence i in the cache, its pages
+__device__ __forceinline__ int pages_of(const DecodeAttnArgs &a, int i, int &len) {
+  const long long most = static_cast<long long>(a.c.width) * kPage;
+  len = max(a.lengths[i], 0);
+  if (len > most) len = static_cast<int>(most);
+  return len / kPage + (len % kPage != 0);
+}
+
+// where share s of `total` units starts: each of the first min(kShares, total)
+// shares has a unit at least, so the parts of a row are in neighbouring ones
+__device__ __forceinline__ long long share_at(long long total, int s) {
+  return total >= kShares ? total * s / kShares : min(static_cast<long long>(s), total);
+}
+
+__device__ __forceinline__ bool poll_d(uint32_t bar, uint32_t parity, const volatile int *abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (int i = 0; i < (1 << 21); ++i) {
+    if (mbar_try_wait_sleep(bar, parity, 2000u)) return true;
+    if (*abort_flag) return false;
+  }
+  return false;
+}
+// named barrier of the consumers that tells each whether any of them brought `bad`
+__device__ __forceinline__ bool consumers_any(bool bad) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred.aligned q, 2, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(bad ? 1u : 0u), "n"(32 * kConsumers)
+      : "memory");
+  return r != 0;
+}
 
 }  // namespace
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) attn_decode_kernel(const DecodeAttnArgs a) {
-  constexpr int kE = D / 32;  // columns of a lane: kE lane ..
-  const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kThreadsD, 1)
+    attn_decode_kernel(const __grid_constant__ CUtensorMap tm, const DecodeAttnArgs a) {
+  using P = Page<D>;
+  constexpr int kG = D / kGroup;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = align1024(smem_raw);
+  float *obuf = reinterpret_cast<float *>(smem + kPagesDeep * P::kBytes);
+  DCtl &ctl = *reinterpret_cast<DCtl *>(smem + kPagesDeep * P::kBytes + P::kOut);
+  static_assert(sizeof(DCtl) <= P::kCtl, "control block");
+  volatile int *abort_flag = &ctl.abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int R = a.c.H * a.blocks, cta = blockIdx.x;
+  if (tid == 0) {
+    for (int s = 0; s < kPagesDeep; ++s) {
+      mbar_init(smem_u32(&ctl.full[s]), 1);
+      mbar_init(smem_u32(&ctl.empty[s]), 4);
+    }
+    ctl.abort_flag = 0;
+    ctl.seq = 0;
+    ctl.at = 0;
+    fence_mbar_init();
+    prefetch_tmap(&tm);
+  }
   pdl_wait();
   pdl_launch_dependents();
-  const long long unit = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int s = static_cast<int>(unit / a.Hq), h = static_cast<int>(unit % a.Hq), hk = h / (a.Hq / a.c.H);
-  if (s >= a.n_seq) return;
-  int len = a.lengths[s];
-  if (len > static_cast<long long>(a.c.width) * kPage) {
-    len = a.c.width * kPage;
-    if (lane == 0) report_error(a.c.status, MOE_ERR_DEVICE_BOUNDS, KID_ATTN_DECODE * 100 + SITE_INDEX);
+  // pages before each thread's sequences, and the share's start
+  const int per = (a.n_seq + kThreadsD - 1) / kThreadsD, i0 = min(tid * per, a.n_seq), i1 = min(i0 + per, a.n_seq);
+  long long sum = 0;
+  bool over = false;
+  for (int i = i0; i < i1; ++i) {
+    int len;
+    sum += pages_of(a, i, len);
+    over = over || a.lengths[i] > len;
   }
-  float q[kE], o[kE], m = -INFINITY, l = 0.0f;
+  if (over && cta == 0) report_error(a.c.status, MOE_ERR_DEVICE_BOUNDS, KID_ATTN_DECODE * 100 + SITE_INDEX);
+  long long upto = sum;
 #pragma unroll
-  for (int e = 0; e < kE; ++e) {
-    q[e] = __bfloat162float(a.q[s * a.qs + h * D + kE * lane + e]);
-    o[e] = 0.0f;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += u;
   }
-  bool any = false;
-  for (int t = 0; t < len; ++t) {
-    const int page = page_of(a.c, s, t);
-    if (page < 0) {
-      if (lane == 0) report_error(a.c.status, MOE_ERR_DEVICE_BOUNDS, KID_ATTN_DECODE * 100 + SITE_INDEX);
-      continue;
-    }
-    any = true;
-    float kv[2][kE];
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const long long row = cache_row(a.c, page, w, hk, t % kPage);
-      const uint32_t pair = a.c.affine[row * (D / kGroup) + kE * lane / kGroup];
-      const float f = __uint_as_float(pair << 16), b = __uint_as_float(pair & 0xffff0000u);
-#pragma unroll
-      for (int e = 0; e < kE; e += 2) {
-        const uint32_t c = a.c.codes[row * (D / 2) + (kE * lane + e) / 2];
-        kv[w][e] = fmaf(f, static_cast<float>(c & 15u), b);
-        kv[w][e + 1] = fmaf(f, static_cast<float>(c >> 4), b);
+  if (lane == 31) ctl.warp_sum[warp] = upto;
+  __syncthreads();
+  long long before = upto - sum, total = 0;
+  for (int w = 0; w <= kConsumers; ++w) {
+    if (w < warp) before += ctl.warp_sum[w];
+    total += ctl.warp_sum[w];
+  }
+  total *= R;
+  const long long u0 = share_at(total, cta), u1 = share_at(total, cta + 1);
+  if (u0 < u1 && u0 >= before * R && u0 < (before + sum) * R) {
+    long long at = u0 - before * R;
+    for (int i = i0; i < i1; ++i) {
+      int len;
+      const long long mine = static_cast<long long>(pages_of(a, i, len)) * R;
+      if (at < mine) {
+        ctl.seq = i;
+        ctl.at = at;
+        break;
       }
+      at -= mine;
     }
-    float x = 0.0f;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) x = fmaf(q[e], kv[0][e], x);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    x *= a.scale;
-    const float top = fmaxf(m, x), ref = top == -INFINITY ? 0.0f : top;
-    const float f = exp2f(m - ref), p = exp2f(x - ref);
-    m = top;
-    l = l * f + p;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) o[e] = o[e] * f + p * kv[1][e];
   }
+  if (tid == 0) a.head[cta] = make_int4(0, 0, 0, 0);
+  __syncthreads();
+  // sequences without tokens: zeros
+  for (int i = cta; i < a.n_seq; i += kShares)
+    if (a.lengths[i] <= 0 || a.c.width == 0)
+      for (int x = tid; x < a.Hq * D / 8; x += kThreadsD)
+        reinterpret_cast<uint4 *>(a.out + static_cast<long long>(i) * a.Hq * D)[x] = make_uint4(0, 0, 0, 0);
+
+  int seq = ctl.seq, st = 0, len = 0;
+  uint32_t phase = 0;
+  long long u = u0, at = ctl.at;
+  int np = u0 < u1 ? pages_of(a, seq, len) : 0;
+  bool ok = true;
+  if (warp == kConsumers) {
+    // ------------------------------------------------------------ copies
+    const uint64_t pol = policy_evict_first();
+    while (ok && u < u1) {
+      if (at >= static_cast<long long>(np) * R) {
+        ++seq;
+        at = 0;
+        np = pages_of(a, seq, len);
+        continue;
+      }
+      const int h = static_cast<int>(at / np) / a.blocks, p0 = static_cast<int>(at % np);
+      const int n = static_cast<int>(min(static_cast<long long>(min(np - p0, 32)), u1 - u));
+      int page = -1;
+      if (lane < n) {
+        page = page_of(a.c, seq, static_cast<long long>(p0 + lane) * kPage);
+        if (page < 0) report_error(a.c.status, MOE_ERR_DEVICE_BOUNDS, KID_ATTN_DECODE * 100 + SITE_INDEX);
+      }
+      for (int i = 0; i < n; ++i) {
+        const int pg = __shfl_sync(0xffffffffu, page, i);
+        ok = __all_sync(0xffffffffu, poll_d(smem_u32(&ctl.empty[st]), phase ^ 1, abort_flag));
+        if (!ok) {
+          if (lane == 0) {
+            *abort_flag = 1;
+            report_error(a.c.status, MOE_ERR_DEVICE_TIMEOUT, KID_ATTN_DECODE * 100 + SITE_PRODUCER_EMPTY);
+          }
+          break;
+        }
+        if (lane == 0) {
+          ctl.ok[st] = pg >= 0;
+          const uint32_t fb = smem_u32(&ctl.full[st]);
+          uint8_t *dst = smem + st * P::kBytes;
+          if (pg < 0) {
+            mbar_arrive(fb);
+          } else {
+            mbar_arrive_expect_tx(fb, P::kBytes);
+            for (int w = 0; w < 2; ++w) {
+              const long long row = cache_row(a.c, pg, w, h, 0);
+              tma_load_2d(smem_u32(dst) + w * P::kCodes, &tm, fb, 0, static_cast<int>(row), pol);
+              bulk_g2s(dst + 2 * P::kCodes + w * P::kAffine, a.c.affine + row * kG, P::kAffine, &ctl.full[st]);
+            }
+          }
+        }
+        __syncwarp();
+        if (++st == kPagesDeep) {
+          st = 0;
+          phase ^= 1;
+        }
+      }
+      u += n;
+      at += n;
+    }
+    if (!ok && lane == 0)  // copies in flight get time to land
+      for (int i = 0; i < 200; ++i) __nanosleep(1000);
+  } else {
+    // ------------------------------------------------------------ tokens
+    const int g = lane >> 2, c = lane & 3, tile = 16 * (warp & 3);
+    int key[4];  // this lane's tokens: columns 2 c, 2 c + 1 of both score tiles
 #pragma unroll
-  for (int e = 0; e < kE; ++e)
-    a.out[(static_cast<long long>(s) * a.Hq + h) * D + kE * lane + e] = __float2bfloat16_rn(any ? o[e] / l : 0.0f);
+    for (int i = 0; i < 4; ++i) key[i] = tile + 8 * (i >> 1) + token_of<D>(2 * c + (i & 1));
+    const int krow = tile + token_of<D>(g);
+    while (u < u1) {
+      if (at >= static_cast<long long>(np) * R) {
+        ++seq;
+        at = 0;
+        np = pages_of(a, seq, len);
+        continue;
+      }
+      // a row, or the part of it that lies in this share
+      const int rr = static_cast<int>(at / np), h = rr / a.blocks, head0 = rr % a.blocks * kHeads;
+      const int heads = min(kHeads, a.group - head0), p0 = static_cast<int>(at % np);
+      const int n = static_cast<int>(min(static_cast<long long>(np - p0), u1 - u));
+      const long long orow = static_cast<long long>(seq) * a.Hq + h * a.group + head0;
+      // the queries as the first product's A, in the column order in which pairs of
+      // nibbles come out of a word, and their sums over the groups
+      uint32_t q[kG][2][4];
+      float qsum[kG];
+      {
+        const __nv_bfloat16 *src =
+            a.q + seq * a.qs + static_cast<long long>(h * a.group + head0 + (g < heads ? g : 0)) * D + 16 * c;
+#pragma unroll
+        for (int x = 0; x < kG; ++x) {
+          qsum[x] = 0.0f;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (g < heads) v = *reinterpret_cast<const uint4 *>(src + 64 * x + 8 * t);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              qsum[x] += __uint_as_float(w[i] << 16) + __uint_as_float(w[i] & 0xffff0000u);
+            q[x][t][0] = __byte_perm(v.x, v.z, 0x5410);  // columns 0, 4
+            q[x][t][1] = __byte_perm(v.x, v.z, 0x7632);  // 1, 5
+            q[x][t][2] = __byte_perm(v.y, v.w, 0x5410);  // 2, 6
+            q[x][t][3] = __byte_perm(v.y, v.w, 0x7632);  // 3, 7
+          }
+          qsum[x] += __shfl_xor_sync(0xffffffffu, qsum[x], 1);
+          qsum[x] += __shfl_xor_sync(0xffffffffu, qsum[x], 2);
+        }
+      }
+      float o[kG][4][4], e[kG], m = -INFINITY, ref = 0.0f, l = 0.0f;
+#pragma unroll
+      for (int x = 0; x < kG; ++x) {
+        e[x] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) o[x][i][y] = 0.0f;
+      }
+      for (int i = 0; ok && i < n; ++i) {
+        const int now = st;
+        const uint32_t ph = phase;
+        if (++st == kPagesDeep) {
+          st = 0;
+          phase ^= 1;
+        }
+        if (((now ^ (warp >> 2)) & 1) != 0) continue;  // (the other four warps' page)
+        ok = __all_sync(0xffffffffu, poll_d(smem_u32(&ctl.full[now]), ph, abort_flag));
+        if (!ok) {
+          if (lane == 0) {
+            *abort_flag = 1;
+            report_error(a.c.status, MOE_ERR_DEVICE_TIMEOUT, KID_ATTN_DECODE * 100 + SITE_MMA_FULL);
+          }
+          break;
+        }
+        const int left = len - (p0 + i) * kPage;  // tokens of the sequence from this page on
+        if (ctl.ok[now] && tile < left) {
+          const uint32_t sk = smem_u32(smem) + now * P::kBytes, sv = sk + P::kCodes;
+          const uint32_t fk = sv + P::kCodes, fv = fk + P::kAffine;
+          // scores of 16 tokens
+          uint32_t ka[4][kG];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) lds_words<kG>(fk + key[y] * kG * 4, ka[y]);
+          float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int x = 0; x < kG; ++x) {
+            float acc[2][4] = {};
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint2 w = lds64(sk + code_at<D>(krow + 8 * y, 32 * x + 8 * c));
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                const uint32_t v = t ? w.y : w.x;
+                mma_16816(acc[y], q[x][t][0], 0u, q[x][t][1], 0u, plus128(v), plus128(v >> 4));
+                mma_16816(acc[y], q[x][t][2], 0u, q[x][t][3], 0u, plus128(v >> 8), plus128(v >> 12));
+              }
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float f = __uint_as_float(ka[y][x] << 16), b = __uint_as_float(ka[y][x] & 0xffff0000u);
+              s[y] = fmaf(f, acc[y >> 1][y & 1], s[y]);
+              s[y] = fmaf(fmaf(-128.0f, f, b), qsum[x], s[y]);
+            }
+          }
+          uint32_t va[4][kG];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            lds_words<kG>(fv + key[y] * kG * 4, va[y]);
+            s[y] *= a.scale;
+          }
+          if (left < tile + 16) {  // the sequence ends here: nothing of what is behind it
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              if (key[y] >= left) {
+                s[y] = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < kG; ++x) va[y][x] = 0u;
+              }
+          }
+          float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const bool grown = top > m + kLateDecode;
+          if (__any_sync(0xffffffffu, grown)) {
+            const float to = grown ? top : m, f = to == m ? 1.0f : fast_exp2(m - to);
+            m = to;
+            ref = to == -INFINITY ? 0.0f : to;
+            l *= f;
+            const float f0 = __shfl_sync(0xffffffffu, f, 8 * c), f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+#pragma unroll
+            for (int x = 0; x < kG; ++x) {
+              e[x] *= f;
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                o[x][t][0] *= f0;
+                o[x][t][1] *= f1;
+                o[x][t][2] *= f0;
+                o[x][t][3] *= f1;
+              }
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            s[y] = fast_exp2(s[y] - ref);
+            l += s[y];
+          }
+          // the values: the same byte of two tokens' codes side by side in a word
+#pragma unroll
+          for (int x = 0; x < kG; ++x) {
+            float p[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float f = __uint_as_float(va[y][x] << 16), b = __uint_as_float(va[y][x] & 0xffff0000u);
+              p[y] = s[y] * f;
+              e[x] = fmaf(s[y], fmaf(8.0f, f, b), e[x]);
+            }
+            const uint32_t b0 = bf16x2_bits(p[0], p[1]), b1 = bf16x2_bits(p[2], p[3]);
+            uint32_t w[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) w[y] = lds32(sv + code_at<D>(key[y], 32 * x + 4 * g));
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const uint32_t lo = __byte_perm(w[0], w[1], 0x0400 + t * 0x0101);
+              const uint32_t hi = __byte_perm(w[2], w[3], 0x0400 + t * 0x0101);
+              mma_16816(o[x][t], centred(lo), centred(lo >> 4), centred(hi), centred(hi >> 4), b0, b1);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl.empty[now]));
+      }
+      // join the warps' parts (also after an abort: all warps meet here)
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+#pragma unroll
+      for (int x = 0; x < kG; ++x) {
+        e[x] += __shfl_xor_sync(0xffffffffu, e[x], 1);
+        e[x] += __shfl_xor_sync(0xffffffffu, e[x], 2);
+      }
+      if (c == 0) {
+        ctl.m[warp][g] = m;
+        ctl.l[warp][g] = l;
+#pragma unroll
+        for (int x = 0; x < kG; ++x) ctl.e[warp][g][x] = e[x];
+      }
+#pragma unroll
+      for (int x = 0; x < kG; ++x)
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          float *to = obuf + (warp * kHeads + 2 * c + z) * P::kPitch + 64 * x + 8 * g;
+          *reinterpret_cast<float4 *>(to) = make_float4(o[x][0][z], o[x][0][2 + z], o[x][1][z], o[x][1][2 + z]);
+          *reinterpret_cast<float4 *>(to + 4) = make_float4(o[x][2][z], o[x][2][2 + z], o[x][3][z], o[x][3][2 + z]);
+        }
+      named_bar_sync(1, 32 * kConsumers);
+      if (warp < heads) {
+        constexpr int kE = D / 32;  // columns per thread; the head is the warp's
+        const int d0 = kE * lane;
+        float M = -INFINITY, L = 0.0f, v[kE];
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, ctl.m[w][warp]);
+#pragma unroll
+        for (int i = 0; i < kE; ++i) v[i] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) {
+          const float mw = ctl.m[w][warp], f = mw == M ? 1.0f : fast_exp2(mw - M);
+          const float ew = ctl.e[w][warp][d0 / kGroup];
+          L = fmaf(f, ctl.l[w][warp], L);
+          const float *from = obuf + (w * kHeads + warp) * P::kPitch + d0;
+#pragma unroll
+          for (int i = 0; i < kE; ++i) v[i] = fmaf(f, from[i] + ew, v[i]);
+        }
+        if (n == np) {
+          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+          __nv_bfloat16 *to = a.out + (orow + warp) * D + d0;
+#pragma unroll
+          for (int i = 0; i < kE; i += 2)
+            *reinterpret_cast<uint32_t *>(to + i) = bf16x2_bits(v[i] * inv, v[i + 1] * inv);
+        } else {
+          const int slot = 2 * cta + (u == u0 ? 0 : 1);
+          float *to = a.part + (static_cast<long long>(slot) * kHeads + warp) * (D + 2);
+#pragma unroll
+          for (int i = 0; i < kE; i += 2) *reinterpret_cast<float2 *>(to + d0 + i) = make_float2(v[i], v[i + 1]);
+          if (lane == 0) *reinterpret_cast<float2 *>(to + D) = make_float2(M, L);
+          if (p0 == 0 && tid == 0) {  // the row starts here: this share's entry says how it goes on
+            const long long last = u + np - 1;
+            int end = static_cast<int>(min(((last + 1) * kShares - 1) / total, kShares - 1LL));
+            while (share_at(total, end + 1) <= last) ++end;
+            while (share_at(total, end) > last) --end;
+            a.head[cta] = make_int4(end - cta + 1, slot, static_cast<int>(orow), heads);
+          }
+        }
+      }
+      if (consumers_any(!ok)) break;
+      u += n;
+      at += n;
+    }
+  }
 }
+
+// Joins the parts of the row that starts in share blockIdx.x and does not end
+// there, for one of its heads: groups of D / 4 threads add up every so many parts,
+// then their sums are added.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const DecodeAttnArgs a) {
+  constexpr int kT = D / 4, kGroups = kJoinThreads / kT;
+  __shared__ float s_f[kShares], s_red[kJoinThreads / 32], s_l[kJoinThreads / 32];
+  __shared__ float4 s_o[kGroups][kT];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hd = blockIdx.y;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int4 head = a.head[blockIdx.x];
+  const int n = head.x;
+  if (n <= 1 || hd >= head.w) return;
+  auto part = [&](int i) {
+    const int slot = i == 0 ? head.y : 2 * (static_cast<int>(blockIdx.x) + i);
+    return a.part + (static_cast<long long>(slot) * kHeads + hd) * (D + 2);
+  };
+  float2 ml = make_float2(-INFINITY, 0.0f);
+  if (tid < n) ml = *reinterpret_cast<const float2 *>(part(tid) + D);
+  float M = ml.x;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) s_red[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) M = fmaxf(M, s_red[w]);
+  const float f = ml.x == M ? 1.0f : fast_exp2(ml.x - M);
+  if (tid < n) s_f[tid] = f;
+  float L = f * ml.y;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if (lane == 0) s_l[warp] = L;
+  __syncthreads();
+  const int t = tid % kT, grp = tid / kT;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int i = grp; i < n; i += kGroups) {
+    const float2 *p = reinterpret_cast<const float2 *>(part(i) + 4 * t);
+    const float2 x = p[0], y = p[1];
+    const float w = s_f[i];
+    v.x = fmaf(w, x.x, v.x);
+    v.y = fmaf(w, x.y, v.y);
+    v.z = fmaf(w, y.x, v.z);
+    v.w = fmaf(w, y.y, v.w);
+  }
+  s_o[grp][t] = v;
+  __syncthreads();
+  if (grp == 0) {
+    L = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) L += s_l[w];
+#pragma unroll
+    for (int x = 1; x < kGroups; ++x) {
+      const float4 y = s_o[x][t];
+      v.x += y.x;
+      v.y += y.y;
+      v.z += y.z;
+      v.w += y.w;
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    uint32_t *to = reinterpret_cast<uint32_t *>(a.out + (static_cast<long long>(head.z) + hd) * D + 4 * t);
+    to[0] = bf16x2_bits(v.x * inv, v.y * inv);
+    to[1] = bf16x2_bits(v.z * inv, v.w * inv);
+  }
+}
+
+namespace {
+
+struct DecodeDevice {
+  int *status = nullptr;
+  int rc = MOE_ERR_CUDA;
+};
+
+const DecodeDevice &decode_device() {
+  static DecodeDevice devs[64];
+  static std::once_flag once[64];
+  static const DecodeDevice none;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return none;
+  std::call_once(once[dev], [dev] {
+    DecodeDevice &d = devs[dev];
+    d.status = noalloc_status_word();
+    auto set = [](auto kern, int bytes) {
+      return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+    };
+    if (d.status && set(attn_decode_kernel<128>, Page<128>::kTotal) && set(attn_decode_kernel<256>, Page<256>::kTotal))
+      d.rc = MOE_OK;
+  });
+  return devs[dev];
+}
+
+template <int D>
+cudaError_t launch_decode_attn(const CUtensorMap &tm, const DecodeAttnArgs &a, cudaStream_t st) {
+  const cudaError_t e = launch_attn(attn_decode_kernel<D>, dim3(kShares), kThreadsD, Page<D>::kTotal, st, tm, a);
+  if (e != cudaSuccess) return e;
+  return launch_attn(attn_join_kernel<D>, dim3(kShares, a.group < kHeads ? a.group : kHeads), kJoinThreads, 0, st, a);
+}
+
+}  // namespace
 
 }  // namespace moe
 
@@ -94,8 +646,8 @@ extern "C" int moe_attention_decode_workspace(int n_seq, int table_width, int n_
                                               int n_kv_heads, int head_dim, size_t *bytes) {
   if (!bytes || n_seq < 0 || table_width < 0 || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads != 0)
     return MOE_ERR_INVALID_ARG;
-  if ((head_dim != 128 && head_dim != 256) || n_q_heads > 65536 || table_width > (1 << 25)) return MOE_ERR_UNSUPPORTED;
-  *bytes = 0;
+  if ((head_dim != 128 && head_dim != 256) || n_q_heads > 4096 || table_width > (1 << 25)) return MOE_ERR_UNSUPPORTED;
+  *bytes = n_seq == 0 ? 0 : kShares * sizeof(int4) + 2 * kShares * sizeof(float) * kHeads * (head_dim + 2);
   return MOE_OK;
 }
 
@@ -110,31 +662,40 @@ extern "C" int moe_attention_decode(const void *q, long long q_stride, const uin
   if (rc != MOE_OK) return rc;
   if (n_pages < 0 || !(scale > 0.0f) || scale > 3.0e38f || q_stride < static_cast<long long>(n_q_heads) * head_dim)
     return MOE_ERR_INVALID_ARG;
-  if (n_pages > 0x7fffffffLL || n_pages * 2 * n_kv_heads * kPage > 0x7fffffffLL || q_stride >= (1LL << 39)) return MOE_ERR_UNSUPPORTED;
+  if (n_pages > 0x7fffffffLL || n_pages * 2 * n_kv_heads * kPage > 0x7fffffffLL || q_stride >= (1LL << 39) ||
+      static_cast<long long>(n_seq) * n_q_heads > 0x7fffffffLL)
+    return MOE_ERR_UNSUPPORTED;
   if (q_stride % 8 != 0) return MOE_ERR_ALIGNMENT;
   if (n_seq == 0) return MOE_OK;
-  if (!q || !out || !lengths || (n_pages > 0 && (!codes || !affine)) || (table_width > 0 && !pages) ||
-      (need > 0 && (!workspace || workspace_bytes < need)))
+  if (!q || !out || !lengths || (n_pages > 0 && (!codes || !affine)) || (table_width > 0 && !pages) || !workspace ||
+      workspace_bytes < need)
     return MOE_ERR_INVALID_ARG;
   if (off_boundary(q, 16) || off_boundary(out, 16) || off_boundary(codes, 16) || off_boundary(affine, 16) ||
       off_boundary(workspace, 16) || off_boundary(pages, 4) || off_boundary(lengths, 4))
     return MOE_ERR_ALIGNMENT;
+  const DecodeDevice &dev = decode_device();
+  if (dev.rc != MOE_OK) return dev.rc;
   DecodeAttnArgs a = {};
   a.c = {const_cast<uint8_t *>(codes), reinterpret_cast<uint32_t *>(const_cast<uint16_t *>(affine)), pages,
-         n_pages, table_width, n_kv_heads, head_dim, noalloc_status_word()};
-  if (!a.c.status) return MOE_ERR_CUDA;
+         n_pages, table_width, n_kv_heads, head_dim, dev.status};
   a.q = static_cast<const __nv_bfloat16 *>(q);
   a.out = static_cast<__nv_bfloat16 *>(out);
   a.lengths = lengths;
   a.qs = q_stride;
   a.n_seq = n_seq;
   a.Hq = n_q_heads;
+  a.group = n_q_heads / n_kv_heads;
+  a.blocks = (a.group + kHeads - 1) / kHeads;
   a.scale = scale * 1.4426950408889634f;
-  const long long blocks = (static_cast<long long>(n_seq) * n_q_heads + kWarps - 1) / kWarps;
-  if (blocks > 0x7fffffffLL) return MOE_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(blocks));
+  a.head = static_cast<int4 *>(workspace);
+  a.part = reinterpret_cast<float *>(a.head + kShares);
+  // (without pages nothing is read: the map then stands over the queries)
+  CUtensorMap tm;
+  const uint64_t rows = n_pages > 0 ? n_pages * 2 * n_kv_heads * kPage : 1;
+  if (!encode_map_2d(&tm, n_pages > 0 ? static_cast<const void *>(codes) : q, 1, rows, head_dim / 2, head_dim / 2,
+                     kPage, head_dim == 256, 0, head_dim == 128))
+    return MOE_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  const cudaError_t e = head_dim == 128 ? launch_attn(attn_decode_kernel<128>, grid, kWarps * 32, 0, st, a)
-                                        : launch_attn(attn_decode_kernel<256>, grid, kWarps * 32, 0, st, a);
+  const cudaError_t e = head_dim == 128 ? launch_decode_attn<128>(tm, a, st) : launch_decode_attn<256>(tm, a, st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
