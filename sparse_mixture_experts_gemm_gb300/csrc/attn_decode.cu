@@ -6,12 +6,17 @@
 // that share it, and the codes go to the tensor cores as they are:
 //     q . k_t = sum_g [ s_tg (q_g . c_tg) + b_tg sum(q_g) ]       g: groups of 64 columns
 //     o_g     = sum_t (p_t s'_tg) (c'_tg - 8) + sum_t p_t (b'_tg + 8 s'_tg)
-// with codes c exact in bf16 (128 + c is one AND-OR away from a nibble), products
-// and sums in fp32, scales and biases applied in fp32.  The only rounding before
-// the result's is that of p_t s'_tg to bf16 (2^-8), which multiplies codes less 8:
-// centred, the sum has no large part that cancels against the bias's.  For the
-// scores 128 is left on the codes and taken off by the bias, -128 s sum(q): four
-// products of 16 columns add up in between, too few to lose anything.
+// with products and sums in fp32.
+//   * Keys: a code in the low bits of an fp16 is the number c 2^-24, four bits up c
+//     2^-20: one AND makes two.  The queries become fp16 by a power of two per head
+//     (the largest is in [2^12, 2^13): what is lost is below 2^-34 of it).
+//   * Values: weights times scales need bf16's range, and 128 + c is one AND-OR away
+//     from a nibble; a second product takes off 136 p_t s'_tg at once, so that the
+//     sum stays centred and has no large part that cancels against the bias's.
+//   * The biases' sums are products, too: bf16 biases with the sums of q in three bf16
+//     parts, p in two with b' and s'.
+// The only rounding before the result's is that of p_t s'_tg to bf16 (2^-8), which
+// multiplies codes less 8 (and that of p to 2^-16 with the biases).
 //
 // Work split.  All (sequence, key/value head, 8 query heads) rows' pages lie on one
 // line that is cut into equal shares, one per SM, whatever the lengths; a CTA
@@ -19,12 +24,13 @@
 // parts (maximum, sum, output) in the workspace for a second kernel, which joins
 // them in a fixed order.
 //
-// Roles: warp 8 copies pages by TMA (8 pages deep), warps 0-7 take 16 tokens of a
+// Roles: warp 12 copies pages by TMA (6 pages deep), warps 0-11 take 16 tokens of a
 // page each, four warps per page, with a running softmax of their own; their parts
 // are joined through shared memory at a row's end.  M of the first product is the
 // query heads, of the second the columns, so that P leaves the one in the layout
 // in which the other takes it.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <mutex>
@@ -36,10 +42,10 @@ namespace moe {
 
 namespace {
 
-constexpr int kConsumers = 8;
+constexpr int kConsumers = 12;
 constexpr int kThreadsD = 32 * (kConsumers + 1);
 constexpr int kHeads = 8;  // query heads of a row
-constexpr int kPagesDeep = 8;
+constexpr int kPagesDeep = 6;
 constexpr int kJoinThreads = 512;
 constexpr float kLateDecode = 8.0f;  // as in attn_prefill.cu
 constexpr int kShares = 152;         // one per SM
@@ -63,7 +69,7 @@ struct Page {
   static constexpr int kBytes = 2 * (kCodes + kAffine);
   static constexpr int kPitch = D + 8;  // of the warps' outputs
   static constexpr int kOut = kConsumers * kHeads * kPitch * 4;
-  static constexpr int kCtl = 4096;
+  static constexpr int kCtl = 12288;
   static constexpr int kTotal = kPagesDeep * kBytes + kOut + kCtl + 1024;
   static_assert(kTotal <= 227 * 1024 && kBytes % 1024 == 0, "shared memory");
 };
@@ -71,10 +77,13 @@ struct Page {
 struct DCtl {
   uint64_t full[kPagesDeep], empty[kPagesDeep];
   int ok[kPagesDeep];  // whether the stage holds a page
-  int abort_flag, seq;
-  long long at;  // the share's first unit within sequence seq's
-  long long warp_sum[kConsumers + 1];
-  float m[kConsumers][kHeads], l[kConsumers][kHeads], e[kConsumers][kHeads][4];
+  int abort_flag, seq, at;  // at: the share's first unit within sequence seq's
+  int warp_sum[kConsumers + 1];
+  float m[kConsumers][kHeads], l[kConsumers][kHeads];
+  float e[kConsumers][8][kHeads];  // sum of p b' of each group, then of p s'
+  uint4 q[4][2][32];  // a row's queries as the first product's A: [group][8 columns][lane]
+  float qsum[4][kHeads], unit[kHeads][2];
+  uint2 qbias[32];  // the sums of q as the A of the biases' product
 };
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -82,8 +91,15 @@ __device__ __forceinline__ float fast_exp2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -99,6 +115,11 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&v)[N]) {
   if constexpr (N == 4) {
@@ -112,11 +133,7 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&v)[N]) {
 }
 // nibbles 0 and 4 of w as bf16 128 + c
 __device__ __forceinline__ uint32_t plus128(uint32_t w) { return (w & 0x000f000fu) | 0x43004300u; }
-__device__ __forceinline__ uint32_t centred(uint32_t w) {  // c - 8
-  const uint32_t u = plus128(w);
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&u), __float2bfloat162_rn(136.0f));
-  return *reinterpret_cast<const uint32_t *>(&d);
-}
+constexpr uint32_t kMinus136 = 0xc308c308u;  // bf16 -136, twice
 
 // Token of 8 that column n of a score tile stands for: chosen so that the rows
 // that lanes read at once, columns n = 0 .. 3 and 4 .. 7 (keys) and all even or odd
@@ -146,8 +163,8 @@ __device__ __forceinline__ int pages_of(const DecodeAttnArgs &a, int i, int &len
 
 // where share s of `total` units starts: each of the first min(kShares, total)
 // shares has a unit at least, so the parts of a row are in neighbouring ones
-__device__ __forceinline__ long long share_at(long long total, int s) {
-  return total >= kShares ? total * s / kShares : min(static_cast<long long>(s), total);
+__device__ __forceinline__ int share_at(int total, int s) {
+  return total >= kShares ? static_cast<int>(static_cast<long long>(total) * s / kShares) : min(s, total);
 }
 
 __device__ __forceinline__ bool poll_d(uint32_t bar, uint32_t parity, const volatile int *abort_flag) {
@@ -172,6 +189,79 @@ __device__ __forceinline__ bool consumers_any(bool bad) {
 }
 
 }  // namespace
+
+// The queries as the first product's A: fp16 of q 2^-power, in the column order in
+// which nibbles come out of a word (every other pair 4 bits up there, so 2^-4
+// here), and their sums over the groups in the same unit as the products.
+template <int D>
+__device__ __forceinline__ void make_queries(const DecodeAttnArgs &a, DCtl &ctl, int seq, int head, int heads) {
+  constexpr int kG = D / kGroup;
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const __nv_bfloat16 *src = a.q + seq * a.qs + static_cast<long long>(head + (g < heads ? g : 0)) * D + 16 * c;
+  uint4 v[kG][2];
+  uint32_t most = 0;
+#pragma unroll
+  for (int x = 0; x < kG; ++x)
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      v[x][t] = make_uint4(0, 0, 0, 0);
+      if (g < heads) v[x][t] = *reinterpret_cast<const uint4 *>(src + 64 * x + 8 * t);
+      const uint32_t w[4] = {v[x][t].x, v[x][t].y, v[x][t].z, v[x][t].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) most = max(most, max(w[i] << 16 & 0x7fff0000u, w[i] & 0x7fff0000u));
+    }
+  most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+  most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+  const int power = min(max(static_cast<int>(most >> 23) - 127 - 12, -126), 126);
+  const float down = __uint_as_float(static_cast<uint32_t>(127 - power) << 23);
+#pragma unroll
+  for (int x = 0; x < kG; ++x) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint32_t w[4] = {v[x][t].x, v[x][t].y, v[x][t].z, v[x][t].w};
+      float f[8];
+      uint32_t y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16) * down;
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * down;
+        sum += f[2 * i] + f[2 * i + 1];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float up = i & 1 ? 0x1p-4f : 1.0f;
+        const __half2 z = __floats2half2_rn(f[i] * up, f[i + 4] * up);
+        y[i] = *reinterpret_cast<const uint32_t *>(&z);
+      }
+      ctl.q[x][t][lane] = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    if (c == 0) ctl.qsum[x][g] = sum * 0x1p-24f;
+  }
+  __syncwarp();
+  {  // index k of the biases' product: group k % kG of part k / kG of the sums
+    float part[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int k = 2 * c + j + 8 * i, which = k / kG;
+        const float all = ctl.qsum[k % kG][g];
+        const float hi = __bfloat162float(__float2bfloat16_rn(all));
+        const float mid = __bfloat162float(__float2bfloat16_rn(all - hi));
+        part[i][j] = which == 0 ? hi : which == 1 ? mid : which == 2 ? all - hi - mid : 0.0f;
+      }
+    ctl.qbias[lane] = make_uint2(bf16x2_bits(part[0][0], part[0][1]), bf16x2_bits(part[1][0], part[1][1]));
+  }
+  if (c == 0) {
+    // scores come out in units of 2^(power + 24), taken off in two steps within range
+    const int first = (power + 24) / 2;
+    ctl.unit[g][0] = __uint_as_float(static_cast<uint32_t>(127 + first) << 23);
+    ctl.unit[g][1] = a.scale * __uint_as_float(static_cast<uint32_t>(127 + power + 24 - first) << 23);
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreadsD, 1)
@@ -201,7 +291,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
   pdl_launch_dependents();
   // pages before each thread's sequences, and the share's start
   const int per = (a.n_seq + kThreadsD - 1) / kThreadsD, i0 = min(tid * per, a.n_seq), i1 = min(i0 + per, a.n_seq);
-  long long sum = 0;
+  int sum = 0;
   bool over = false;
   for (int i = i0; i < i1; ++i) {
     int len;
@@ -209,26 +299,26 @@ __global__ void __launch_bounds__(kThreadsD, 1)
     over = over || a.lengths[i] > len;
   }
   if (over && cta == 0) report_error(a.c.status, MOE_ERR_DEVICE_BOUNDS, KID_ATTN_DECODE * 100 + SITE_INDEX);
-  long long upto = sum;
+  int upto = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, upto, o);
+    const int u = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += u;
   }
   if (lane == 31) ctl.warp_sum[warp] = upto;
   __syncthreads();
-  long long before = upto - sum, total = 0;
+  int before = upto - sum, total = 0;
   for (int w = 0; w <= kConsumers; ++w) {
     if (w < warp) before += ctl.warp_sum[w];
     total += ctl.warp_sum[w];
   }
   total *= R;
-  const long long u0 = share_at(total, cta), u1 = share_at(total, cta + 1);
+  const int u0 = share_at(total, cta), u1 = share_at(total, cta + 1);
   if (u0 < u1 && u0 >= before * R && u0 < (before + sum) * R) {
-    long long at = u0 - before * R;
+    int at = u0 - before * R;
     for (int i = i0; i < i1; ++i) {
       int len;
-      const long long mine = static_cast<long long>(pages_of(a, i, len)) * R;
+      const int mine = pages_of(a, i, len) * R;
       if (at < mine) {
         ctl.seq = i;
         ctl.at = at;
@@ -247,21 +337,20 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 
   int seq = ctl.seq, st = 0, len = 0;
   uint32_t phase = 0;
-  long long u = u0, at = ctl.at;
+  int u = u0, at = ctl.at;
   int np = u0 < u1 ? pages_of(a, seq, len) : 0;
   bool ok = true;
   if (warp == kConsumers) {
     // ------------------------------------------------------------ copies
     const uint64_t pol = policy_evict_first();
     while (ok && u < u1) {
-      if (at >= static_cast<long long>(np) * R) {
+      if (at >= np * R) {
         ++seq;
         at = 0;
         np = pages_of(a, seq, len);
         continue;
       }
-      const int h = static_cast<int>(at / np) / a.blocks, p0 = static_cast<int>(at % np);
-      const int n = static_cast<int>(min(static_cast<long long>(min(np - p0, 32)), u1 - u));
+      const int h = at / np / a.blocks, p0 = at % np, n = min(min(np - p0, 32), u1 - u);
       int page = -1;
       if (lane < n) {
         page = page_of(a.c, seq, static_cast<long long>(p0 + lane) * kPage);
@@ -310,54 +399,33 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 #pragma unroll
     for (int i = 0; i < 4; ++i) key[i] = tile + 8 * (i >> 1) + token_of<D>(2 * c + (i & 1));
     const int krow = tile + token_of<D>(g);
+    // places in a stage; those of group x are these ^ 32 x
+    const uint32_t kat[2] = {code_at<D>(krow, 8 * c), code_at<D>(krow + 8, 8 * c)};
+    uint32_t vat[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) vat[i] = code_at<D>(key[i], 4 * g);
+    // rows of the product with p: biases of the groups, scales of the groups
+    const uint32_t pick = g < 4 ? 0x7632u : 0x5410u, live = (g & 3) < kG ? 0xffffffffu : 0u;
+    int mine = 0;  // the four warps whose turn the next page is
     while (u < u1) {
-      if (at >= static_cast<long long>(np) * R) {
+      if (at >= np * R) {
         ++seq;
         at = 0;
         np = pages_of(a, seq, len);
         continue;
       }
       // a row, or the part of it that lies in this share
-      const int rr = static_cast<int>(at / np), h = rr / a.blocks, head0 = rr % a.blocks * kHeads;
-      const int heads = min(kHeads, a.group - head0), p0 = static_cast<int>(at % np);
-      const int n = static_cast<int>(min(static_cast<long long>(np - p0), u1 - u));
+      const int rr = at / np, h = rr / a.blocks, head0 = rr % a.blocks * kHeads;
+      const int heads = min(kHeads, a.group - head0), p0 = at % np;
+      const int n = min(np - p0, u1 - u);
       const long long orow = static_cast<long long>(seq) * a.Hq + h * a.group + head0;
-      // the queries as the first product's A, in the column order in which pairs of
-      // nibbles come out of a word, and their sums over the groups
-      uint32_t q[kG][2][4];
-      float qsum[kG];
-      {
-        const __nv_bfloat16 *src =
-            a.q + seq * a.qs + static_cast<long long>(h * a.group + head0 + (g < heads ? g : 0)) * D + 16 * c;
-#pragma unroll
-        for (int x = 0; x < kG; ++x) {
-          qsum[x] = 0.0f;
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (g < heads) v = *reinterpret_cast<const uint4 *>(src + 64 * x + 8 * t);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              qsum[x] += __uint_as_float(w[i] << 16) + __uint_as_float(w[i] & 0xffff0000u);
-            q[x][t][0] = __byte_perm(v.x, v.z, 0x5410);  // columns 0, 4
-            q[x][t][1] = __byte_perm(v.x, v.z, 0x7632);  // 1, 5
-            q[x][t][2] = __byte_perm(v.y, v.w, 0x5410);  // 2, 6
-            q[x][t][3] = __byte_perm(v.y, v.w, 0x7632);  // 3, 7
-          }
-          qsum[x] += __shfl_xor_sync(0xffffffffu, qsum[x], 1);
-          qsum[x] += __shfl_xor_sync(0xffffffffu, qsum[x], 2);
-        }
-      }
-      float o[kG][4][4], e[kG], m = -INFINITY, ref = 0.0f, l = 0.0f;
-#pragma unroll
-      for (int x = 0; x < kG; ++x) {
-        e[x] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) o[x][i][y] = 0.0f;
-      }
+      // (all warps have left the row before)
+      if (warp == 0) make_queries<D>(a, ctl, seq, h * a.group + head0, heads);
+      named_bar_sync(1, 32 * kConsumers);
+      const uint32_t sq = smem_u32(&ctl.q[0][0][lane]);
+      const uint2 qb = ctl.qbias[lane];
+      const float unit0 = ctl.unit[g][0], unit1 = ctl.unit[g][1];
+      float o[kG][4][4] = {}, e[4] = {}, m = -INFINITY, ref = 0.0f, l = 0.0f;
       for (int i = 0; ok && i < n; ++i) {
         const int now = st;
         const uint32_t ph = phase;
@@ -365,7 +433,9 @@ __global__ void __launch_bounds__(kThreadsD, 1)
           st = 0;
           phase ^= 1;
         }
-        if (((now ^ (warp >> 2)) & 1) != 0) continue;  // (the other four warps' page)
+        const bool other = mine != warp >> 2;
+        mine = mine == kConsumers / 4 - 1 ? 0 : mine + 1;
+        if (other) continue;
         ok = __all_sync(0xffffffffu, poll_d(smem_u32(&ctl.full[now]), ph, abort_flag));
         if (!ok) {
           if (lane == 0) {
@@ -378,45 +448,42 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         if (ctl.ok[now] && tile < left) {
           const uint32_t sk = smem_u32(smem) + now * P::kBytes, sv = sk + P::kCodes;
           const uint32_t fk = sv + P::kCodes, fv = fk + P::kAffine;
-          // scores of 16 tokens
+          // scores of 16 tokens: first the biases' part
+          float sb[2][4] = {};
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const uint2 w = lds64(fk + (krow + 8 * y) * kG * 4 + (D == 256 ? 8 * (c & 1) : 0));
+            const uint32_t bb = __byte_perm(w.x, w.y, 0x7632);
+            mma_bf16(sb[y], qb.x, 0u, qb.y, 0u, bb, bb);
+          }
+          float s[4] = {sb[0][0], sb[0][1], sb[1][0], sb[1][1]};
           uint32_t ka[4][kG];
 #pragma unroll
           for (int y = 0; y < 4; ++y) lds_words<kG>(fk + key[y] * kG * 4, ka[y]);
-          float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          const uint32_t k0 = sk + kat[0], k1 = sk + kat[1];
 #pragma unroll
           for (int x = 0; x < kG; ++x) {
+            const uint4 q0 = lds128(sq + x * 1024), q1 = lds128(sq + x * 1024 + 512);
             float acc[2][4] = {};
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const uint2 w = lds64(sk + code_at<D>(krow + 8 * y, 32 * x + 8 * c));
-#pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                const uint32_t v = t ? w.y : w.x;
-                mma_16816(acc[y], q[x][t][0], 0u, q[x][t][1], 0u, plus128(v), plus128(v >> 4));
-                mma_16816(acc[y], q[x][t][2], 0u, q[x][t][3], 0u, plus128(v >> 8), plus128(v >> 12));
-              }
+              const uint2 w = lds64((y ? k1 : k0) ^ (32 * x));
+              const uint32_t u = w.x >> 8, v = w.y >> 8;
+              mma_f16(acc[y], q0.x, 0u, q0.y, 0u, w.x & 0x000f000fu, w.x & 0x00f000f0u);
+              mma_f16(acc[y], q0.z, 0u, q0.w, 0u, u & 0x000f000fu, u & 0x00f000f0u);
+              mma_f16(acc[y], q1.x, 0u, q1.y, 0u, w.y & 0x000f000fu, w.y & 0x00f000f0u);
+              mma_f16(acc[y], q1.z, 0u, q1.w, 0u, v & 0x000f000fu, v & 0x00f000f0u);
             }
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const float f = __uint_as_float(ka[y][x] << 16), b = __uint_as_float(ka[y][x] & 0xffff0000u);
-              s[y] = fmaf(f, acc[y >> 1][y & 1], s[y]);
-              s[y] = fmaf(fmaf(-128.0f, f, b), qsum[x], s[y]);
-            }
+            for (int y = 0; y < 4; ++y) s[y] = fmaf(__uint_as_float(ka[y][x] << 16), acc[y >> 1][y & 1], s[y]);
           }
-          uint32_t va[4][kG];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            lds_words<kG>(fv + key[y] * kG * 4, va[y]);
-            s[y] *= a.scale;
-          }
-          if (left < tile + 16) {  // the sequence ends here: nothing of what is behind it
+          for (int y = 0; y < 4; ++y) s[y] = s[y] * unit0 * unit1;
+          const bool end = left < tile + 16;  // the sequence ends in these tokens
+          if (end) {
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-              if (key[y] >= left) {
-                s[y] = -INFINITY;
-#pragma unroll
-                for (int x = 0; x < kG; ++x) va[y][x] = 0u;
-              }
+              if (key[y] >= left) s[y] = -INFINITY;
           }
           float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -428,9 +495,10 @@ __global__ void __launch_bounds__(kThreadsD, 1)
             ref = to == -INFINITY ? 0.0f : to;
             l *= f;
             const float f0 = __shfl_sync(0xffffffffu, f, 8 * c), f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+            e[0] *= f0;
+            e[1] *= f1;
 #pragma unroll
             for (int x = 0; x < kG; ++x) {
-              e[x] *= f;
 #pragma unroll
               for (int t = 0; t < 4; ++t) {
                 o[x][t][0] *= f0;
@@ -445,25 +513,47 @@ __global__ void __launch_bounds__(kThreadsD, 1)
             s[y] = fast_exp2(s[y] - ref);
             l += s[y];
           }
+          // scales of the values; of what is behind the end nothing may be seen (0 x NaN
+          // is NaN)
+          uint32_t va[4][kG], ve[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            ve[y] = lds32(fv + (key[y] * kG + (g & (kG - 1))) * 4) & live;
+            lds_words<kG>(fv + key[y] * kG * 4, va[y]);
+          }
+          if (end) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              if (key[y] >= left) {
+                ve[y] = 0u;
+#pragma unroll
+                for (int x = 0; x < kG; ++x) va[y][x] = 0u;
+              }
+          }
+          {  // sums of p b' and p s'
+            const uint32_t h0 = bf16x2_bits(s[0], s[1]), h1 = bf16x2_bits(s[2], s[3]);
+            const uint32_t l0 = bf16x2_bits(s[0] - __uint_as_float(h0 << 16), s[1] - __uint_as_float(h0 & 0xffff0000u));
+            const uint32_t l1 = bf16x2_bits(s[2] - __uint_as_float(h1 << 16), s[3] - __uint_as_float(h1 & 0xffff0000u));
+            const uint32_t a0 = __byte_perm(ve[0], ve[1], pick), a2 = __byte_perm(ve[2], ve[3], pick);
+            mma_bf16(e, a0, 0u, a2, 0u, h0, h1);
+            mma_bf16(e, a0, 0u, a2, 0u, l0, l1);
+          }
           // the values: the same byte of two tokens' codes side by side in a word
+          const uint32_t v0 = sv + vat[0], v1 = sv + vat[1], v2 = sv + vat[2], v3 = sv + vat[3];
 #pragma unroll
           for (int x = 0; x < kG; ++x) {
             float p[4];
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const float f = __uint_as_float(va[y][x] << 16), b = __uint_as_float(va[y][x] & 0xffff0000u);
-              p[y] = s[y] * f;
-              e[x] = fmaf(s[y], fmaf(8.0f, f, b), e[x]);
-            }
+            for (int y = 0; y < 4; ++y) p[y] = s[y] * __uint_as_float(va[y][x] << 16);
             const uint32_t b0 = bf16x2_bits(p[0], p[1]), b1 = bf16x2_bits(p[2], p[3]);
-            uint32_t w[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) w[y] = lds32(sv + code_at<D>(key[y], 32 * x + 4 * g));
+            const uint32_t w0 = lds32(v0 ^ (32 * x)), w1 = lds32(v1 ^ (32 * x));
+            const uint32_t w2 = lds32(v2 ^ (32 * x)), w3 = lds32(v3 ^ (32 * x));
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-              const uint32_t lo = __byte_perm(w[0], w[1], 0x0400 + t * 0x0101);
-              const uint32_t hi = __byte_perm(w[2], w[3], 0x0400 + t * 0x0101);
-              mma_16816(o[x][t], centred(lo), centred(lo >> 4), centred(hi), centred(hi >> 4), b0, b1);
+              const uint32_t lo = __byte_perm(w0, w1, 0x0400 + t * 0x0101);
+              const uint32_t hi = __byte_perm(w2, w3, 0x0400 + t * 0x0101);
+              mma_bf16(o[x][t], plus128(lo), plus128(lo >> 4), plus128(hi), plus128(hi >> 4), b0, b1);
+              mma_bf16(o[x][t], kMinus136, kMinus136, kMinus136, kMinus136, b0, b1);
             }
           }
         }
@@ -473,17 +563,11 @@ __global__ void __launch_bounds__(kThreadsD, 1)
       // join the warps' parts (also after an abort: all warps meet here)
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
-#pragma unroll
-      for (int x = 0; x < kG; ++x) {
-        e[x] += __shfl_xor_sync(0xffffffffu, e[x], 1);
-        e[x] += __shfl_xor_sync(0xffffffffu, e[x], 2);
-      }
       if (c == 0) {
         ctl.m[warp][g] = m;
         ctl.l[warp][g] = l;
-#pragma unroll
-        for (int x = 0; x < kG; ++x) ctl.e[warp][g][x] = e[x];
       }
+      *reinterpret_cast<float2 *>(&ctl.e[warp][g][2 * c]) = make_float2(e[0], e[1]);
 #pragma unroll
       for (int x = 0; x < kG; ++x)
 #pragma unroll
@@ -504,7 +588,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 #pragma unroll
         for (int w = 0; w < kConsumers; ++w) {
           const float mw = ctl.m[w][warp], f = mw == M ? 1.0f : fast_exp2(mw - M);
-          const float ew = ctl.e[w][warp][d0 / kGroup];
+          const float ew = fmaf(8.0f, ctl.e[w][4 + d0 / kGroup][warp], ctl.e[w][d0 / kGroup][warp]);
           L = fmaf(f, ctl.l[w][warp], L);
           const float *from = obuf + (w * kHeads + warp) * P::kPitch + d0;
 #pragma unroll
@@ -523,8 +607,8 @@ __global__ void __launch_bounds__(kThreadsD, 1)
           for (int i = 0; i < kE; i += 2) *reinterpret_cast<float2 *>(to + d0 + i) = make_float2(v[i], v[i + 1]);
           if (lane == 0) *reinterpret_cast<float2 *>(to + D) = make_float2(M, L);
           if (p0 == 0 && tid == 0) {  // the row starts here: this share's entry says how it goes on
-            const long long last = u + np - 1;
-            int end = static_cast<int>(min(((last + 1) * kShares - 1) / total, kShares - 1LL));
+            const int last = u + np - 1;
+            int end = static_cast<int>(min(((last + 1LL) * kShares - 1) / total, kShares - 1LL));
             while (share_at(total, end + 1) <= last) ++end;
             while (share_at(total, end) > last) --end;
             a.head[cta] = make_int4(end - cta + 1, slot, static_cast<int>(orow), heads);
@@ -663,7 +747,9 @@ extern "C" int moe_attention_decode(const void *q, long long q_stride, const uin
   if (n_pages < 0 || !(scale > 0.0f) || scale > 3.0e38f || q_stride < static_cast<long long>(n_q_heads) * head_dim)
     return MOE_ERR_INVALID_ARG;
   if (n_pages > 0x7fffffffLL || n_pages * 2 * n_kv_heads * kPage > 0x7fffffffLL || q_stride >= (1LL << 39) ||
-      static_cast<long long>(n_seq) * n_q_heads > 0x7fffffffLL)
+      static_cast<long long>(n_seq) * n_q_heads > 0x7fffffffLL ||
+      static_cast<long long>(n_seq) * table_width >
+          0x7fffffffLL / (n_kv_heads * ((n_q_heads / n_kv_heads + kHeads - 1) / kHeads)))
     return MOE_ERR_UNSUPPORTED;
   if (q_stride % 8 != 0) return MOE_ERR_ALIGNMENT;
   if (n_seq == 0) return MOE_OK;
