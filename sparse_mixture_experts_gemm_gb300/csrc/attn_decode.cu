@@ -26,9 +26,9 @@
 //
 // Roles: warp 12 copies pages by TMA (6 pages deep), warps 0-11 take 16 tokens of a
 // page each, four warps per page, with a running softmax of their own; their parts
-// are joined through shared memory at a row's end.  M of the first product is the
-// query heads, of the second the columns, so that P leaves the one in the layout
-// in which the other takes it.
+// are joined through shared memory at a row's end.  The codes are the A operand of
+// both products (tokens x columns, columns x tokens), whose four registers the
+// dequantisation fills as they are; P is turned in between, four 8 x 8 matrices.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -43,10 +43,12 @@ namespace moe {
 namespace {
 
 constexpr int kConsumers = 12;
+constexpr int kTeams = kConsumers / 4;  // of four warps, that take a page each
 constexpr int kThreadsD = 32 * (kConsumers + 1);
 constexpr int kHeads = 8;  // query heads of a row
 constexpr int kPagesDeep = 6;
 constexpr int kJoinThreads = 512;
+static_assert(kPagesDeep % kTeams == 0, "a team's pages are in the same stages");
 constexpr float kLateDecode = 8.0f;  // as in attn_prefill.cu
 constexpr int kShares = 152;         // one per SM
 static_assert(kShares <= kJoinThreads, "a thread per part");
@@ -105,6 +107,21 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// the first of a sum
+__device__ __forceinline__ void mma0_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma0_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -135,22 +152,32 @@ __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&v)[N]) {
 __device__ __forceinline__ uint32_t plus128(uint32_t w) { return (w & 0x000f000fu) | 0x43004300u; }
 constexpr uint32_t kMinus136 = 0xc308c308u;  // bf16 -136, twice
 
-// Token of 8 that column n of a score tile stands for: chosen so that the rows
-// that lanes read at once, columns n = 0 .. 3 and 4 .. 7 (keys) and all even or odd
-// n (values), lie in different quarters of the 128 bytes of shared-memory banks,
-// given the copies' swizzle.
-template <int D>
-__device__ __forceinline__ int token_of(int n) {
-  const int f = n < 4 ? n : (n ^ 1) & 3, b = n >> 2;
-  return D == 256 ? 2 * f + b : (f & 1) | b << 1 | (f >> 1) << 2;
+// four 8 x 8 matrices of 16-bit values: lane l gets row l / 4, values 2 (l % 4), + 1
+// of each; lanes 8 m .. 8 m + 7 the addresses of matrix m's rows
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
 }
-// byte of a row of codes in a stage, swizzled by TMA (128-byte or 64-byte pattern)
+// the same, transposed: rows 2 (l % 4), + 1 of value l / 4
+__device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+// an 8 x 8 matrix of 16-bit values (row l / 4, values 2 (l % 4), + 1 in lane l) transposed
+__device__ __forceinline__ uint32_t turned(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+// 16-byte piece of a row of codes in a stage, swizzled by TMA (128-byte or 64-byte
+// pattern: the same piece of 8 rows lies in all banks); piece ^ p is that ^ 16 p
 template <int D>
-__device__ __forceinline__ uint32_t code_at(int row, int byte) {
-  if constexpr (D == 256)
-    return row * 128 + ((((byte >> 4) ^ row) & 7) << 4) + (byte & 15);
-  else
-    return row * 64 + ((((byte >> 4) ^ (row >> 1)) & 3) << 4) + (byte & 15);
+__device__ __forceinline__ uint32_t piece_at(int row, int piece) {
+  return D == 256 ? row * 128 + (((piece ^ row) & 7) << 4) : row * 64 + (((piece ^ (row >> 1)) & 3) << 4);
 }
 
 // tokens of sequence i in the cache, its pages
@@ -197,7 +224,7 @@ template <int D>
 __device__ __forceinline__ void make_queries(const DecodeAttnArgs &a, DCtl &ctl, int seq, int head, int heads) {
   constexpr int kG = D / kGroup;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const __nv_bfloat16 *src = a.q + seq * a.qs + static_cast<long long>(head + (g < heads ? g : 0)) * D + 16 * c;
+  const __nv_bfloat16 *src = a.q + seq * a.qs + static_cast<long long>(head + (g < heads ? g : 0)) * D + 8 * c;
   uint4 v[kG][2];
   uint32_t most = 0;
 #pragma unroll
@@ -205,7 +232,7 @@ __device__ __forceinline__ void make_queries(const DecodeAttnArgs &a, DCtl &ctl,
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       v[x][t] = make_uint4(0, 0, 0, 0);
-      if (g < heads) v[x][t] = *reinterpret_cast<const uint4 *>(src + 64 * x + 8 * t);
+      if (g < heads) v[x][t] = *reinterpret_cast<const uint4 *>(src + 64 * x + 32 * t);
       const uint32_t w[4] = {v[x][t].x, v[x][t].y, v[x][t].z, v[x][t].w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) most = max(most, max(w[i] << 16 & 0x7fff0000u, w[i] & 0x7fff0000u));
@@ -395,18 +422,14 @@ __global__ void __launch_bounds__(kThreadsD, 1)
   } else {
     // ------------------------------------------------------------ tokens
     const int g = lane >> 2, c = lane & 3, tile = 16 * (warp & 3);
-    int key[4];  // this lane's tokens: columns 2 c, 2 c + 1 of both score tiles
-#pragma unroll
-    for (int i = 0; i < 4; ++i) key[i] = tile + 8 * (i >> 1) + token_of<D>(2 * c + (i & 1));
-    const int krow = tile + token_of<D>(g);
-    // places in a stage; those of group x are these ^ 32 x
-    const uint32_t kat[2] = {code_at<D>(krow, 8 * c), code_at<D>(krow + 8, 8 * c)};
-    uint32_t vat[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) vat[i] = code_at<D>(key[i], 4 * g);
-    // rows of the product with p: biases of the groups, scales of the groups
-    const uint32_t pick = g < 4 ? 0x7632u : 0x5410u, live = (g & 3) < kG ? 0xffffffffu : 0u;
-    int mine = 0;  // the four warps whose turn the next page is
+    // this lane's tokens: columns 2 c, 2 c + 1 of the two score tiles of 8
+    const int key = tile + 2 * c;
+    // rows of codes for the matrix loads: keys 8 (m & 1) + .. , pieces m >> 1 of matrix
+    // m; values the same
+    const int mrow = tile + 8 * ((lane >> 3) & 1) + (lane & 7);
+    const uint32_t mat = piece_at<D>(mrow, lane >> 4);
+    int mine = warp >> 2;
+    st = mine;
     while (u < u1) {
       if (at >= np * R) {
         ++seq;
@@ -424,18 +447,19 @@ __global__ void __launch_bounds__(kThreadsD, 1)
       named_bar_sync(1, 32 * kConsumers);
       const uint32_t sq = smem_u32(&ctl.q[0][0][lane]);
       const uint2 qb = ctl.qbias[lane];
-      const float unit0 = ctl.unit[g][0], unit1 = ctl.unit[g][1];
-      float o[kG][4][4] = {}, e[4] = {}, m = -INFINITY, ref = 0.0f, l = 0.0f;
-      for (int i = 0; ok && i < n; ++i) {
+      const float2 unit[2] = {*reinterpret_cast<const float2 *>(ctl.unit[2 * c]),
+                              *reinterpret_cast<const float2 *>(ctl.unit[2 * c + 1])};
+      // heads 2 c, 2 c + 1
+      float o[kG][4][4] = {}, e[4] = {}, m[2] = {-INFINITY, -INFINITY}, ref[2] = {0.0f, 0.0f}, l[2] = {0.0f, 0.0f};
+      // the pages of these four warps: mine pages on, and every kTeams-th
+      int i = mine;
+      for (; ok && i < n; i += kTeams) {
         const int now = st;
         const uint32_t ph = phase;
-        if (++st == kPagesDeep) {
-          st = 0;
+        if ((st += kTeams) >= kPagesDeep) {
+          st -= kPagesDeep;
           phase ^= 1;
         }
-        const bool other = mine != warp >> 2;
-        mine = mine == kConsumers / 4 - 1 ? 0 : mine + 1;
-        if (other) continue;
         ok = __all_sync(0xffffffffu, poll_d(smem_u32(&ctl.full[now]), ph, abort_flag));
         if (!ok) {
           if (lane == 0) {
@@ -448,110 +472,118 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         if (ctl.ok[now] && tile < left) {
           const uint32_t sk = smem_u32(smem) + now * P::kBytes, sv = sk + P::kCodes;
           const uint32_t fk = sv + P::kCodes, fv = fk + P::kAffine;
-          // scores of 16 tokens: first the biases' part
-          float sb[2][4] = {};
+          // scores of 16 tokens (rows g, g + 8; heads 2 c, 2 c + 1): first the biases' part
+          float s[4];
+          {
+            uint32_t bb[2];
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint2 w = lds64(fk + (krow + 8 * y) * kG * 4 + (D == 256 ? 8 * (c & 1) : 0));
-            const uint32_t bb = __byte_perm(w.x, w.y, 0x7632);
-            mma_bf16(sb[y], qb.x, 0u, qb.y, 0u, bb, bb);
+            for (int y = 0; y < 2; ++y) {
+              const uint2 w = lds64(fk + (tile + g + 8 * y) * kG * 4 + (D == 256 ? 8 * (c & 1) : 0));
+              bb[y] = __byte_perm(w.x, w.y, 0x7632);
+            }
+            mma0_bf16(s, bb[0], bb[1], bb[0], bb[1], qb.x, qb.y);
           }
-          float s[4] = {sb[0][0], sb[0][1], sb[1][0], sb[1][1]};
-          uint32_t ka[4][kG];
+          uint32_t ka[2][kG];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) lds_words<kG>(fk + key[y] * kG * 4, ka[y]);
-          const uint32_t k0 = sk + kat[0], k1 = sk + kat[1];
+          for (int y = 0; y < 2; ++y) lds_words<kG>(fk + (tile + g + 8 * y) * kG * 4, ka[y]);
 #pragma unroll
           for (int x = 0; x < kG; ++x) {
             const uint4 q0 = lds128(sq + x * 1024), q1 = lds128(sq + x * 1024 + 512);
-            float acc[2][4] = {};
+            float acc[4];
+            uint32_t w[4], u[4];  // 8 columns of the keys 0 .. 7, 8 .. 15, then 32 columns on
+            ldsm4((sk + mat) ^ (32 * x), w);
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint2 w = lds64((y ? k1 : k0) ^ (32 * x));
-              const uint32_t u = w.x >> 8, v = w.y >> 8;
-              mma_f16(acc[y], q0.x, 0u, q0.y, 0u, w.x & 0x000f000fu, w.x & 0x00f000f0u);
-              mma_f16(acc[y], q0.z, 0u, q0.w, 0u, u & 0x000f000fu, u & 0x00f000f0u);
-              mma_f16(acc[y], q1.x, 0u, q1.y, 0u, w.y & 0x000f000fu, w.y & 0x00f000f0u);
-              mma_f16(acc[y], q1.z, 0u, q1.w, 0u, v & 0x000f000fu, v & 0x00f000f0u);
-            }
+            for (int y = 0; y < 4; ++y) u[y] = w[y] >> 8;
+            mma0_f16(acc, w[0] & 0x000f000fu, w[1] & 0x000f000fu, w[0] & 0x00f000f0u, w[1] & 0x00f000f0u, q0.x, q0.y);
+            mma_f16(acc, u[0] & 0x000f000fu, u[1] & 0x000f000fu, u[0] & 0x00f000f0u, u[1] & 0x00f000f0u, q0.z, q0.w);
+            mma_f16(acc, w[2] & 0x000f000fu, w[3] & 0x000f000fu, w[2] & 0x00f000f0u, w[3] & 0x00f000f0u, q1.x, q1.y);
+            mma_f16(acc, u[2] & 0x000f000fu, u[3] & 0x000f000fu, u[2] & 0x00f000f0u, u[3] & 0x00f000f0u, q1.z, q1.w);
 #pragma unroll
-            for (int y = 0; y < 4; ++y) s[y] = fmaf(__uint_as_float(ka[y][x] << 16), acc[y >> 1][y & 1], s[y]);
+            for (int y = 0; y < 4; ++y) s[y] = fmaf(__uint_as_float(ka[y >> 1][x] << 16), acc[y], s[y]);
           }
 #pragma unroll
-          for (int y = 0; y < 4; ++y) s[y] = s[y] * unit0 * unit1;
+          for (int y = 0; y < 4; ++y) s[y] = s[y] * unit[y & 1].x * unit[y & 1].y;
           const bool end = left < tile + 16;  // the sequence ends in these tokens
           if (end) {
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-              if (key[y] >= left) s[y] = -INFINITY;
+              if (tile + g + 8 * (y >> 1) >= left) s[y] = -INFINITY;
           }
-          float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const bool grown = top > m + kLateDecode;
-          if (__any_sync(0xffffffffu, grown)) {
-            const float to = grown ? top : m, f = to == m ? 1.0f : fast_exp2(m - to);
-            m = to;
-            ref = to == -INFINITY ? 0.0f : to;
-            l *= f;
-            const float f0 = __shfl_sync(0xffffffffu, f, 8 * c), f1 = __shfl_sync(0xffffffffu, f, 8 * c + 4);
-            e[0] *= f0;
-            e[1] *= f1;
+          float top[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
+          if (__any_sync(0xffffffffu, top[0] > m[0] + kLateDecode || top[1] > m[1] + kLateDecode)) {
+            float f[2];
 #pragma unroll
-            for (int x = 0; x < kG; ++x) {
+            for (int z = 0; z < 2; ++z) {
 #pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                o[x][t][0] *= f0;
-                o[x][t][1] *= f1;
-                o[x][t][2] *= f0;
-                o[x][t][3] *= f1;
-              }
+              for (int x = 4; x < 32; x *= 2) top[z] = fmaxf(top[z], __shfl_xor_sync(0xffffffffu, top[z], x));
+              const float to = top[z] > m[z] + kLateDecode ? top[z] : m[z];
+              f[z] = to == m[z] ? 1.0f : fast_exp2(m[z] - to);
+              m[z] = to;
+              ref[z] = to == -INFINITY ? 0.0f : to;
+              l[z] *= f[z];
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              e[y] *= f[y & 1];
+#pragma unroll
+              for (int x = 0; x < kG; ++x)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) o[x][t][y] *= f[y & 1];
             }
           }
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            s[y] = fast_exp2(s[y] - ref);
-            l += s[y];
+            s[y] = fast_exp2(s[y] - ref[y & 1]);
+            l[y & 1] += s[y];
           }
+          // P turned (head g, tokens 2 c, 2 c + 1 of both halves), in two bf16 parts
+          uint32_t h0 = bf16x2_bits(s[0], s[1]), h1 = bf16x2_bits(s[2], s[3]);
+          uint32_t l0 = bf16x2_bits(s[0] - __uint_as_float(h0 << 16), s[1] - __uint_as_float(h0 & 0xffff0000u));
+          uint32_t l1 = bf16x2_bits(s[2] - __uint_as_float(h1 << 16), s[3] - __uint_as_float(h1 & 0xffff0000u));
+          h0 = turned(h0);
+          h1 = turned(h1);
+          l0 = turned(l0);
+          l1 = turned(l1);
+          const float pt[4] = {__uint_as_float(h0 << 16) + __uint_as_float(l0 << 16),
+                               __uint_as_float(h0 & 0xffff0000u) + __uint_as_float(l0 & 0xffff0000u),
+                               __uint_as_float(h1 << 16) + __uint_as_float(l1 << 16),
+                               __uint_as_float(h1 & 0xffff0000u) + __uint_as_float(l1 & 0xffff0000u)};
           // scales of the values; of what is behind the end nothing may be seen (0 x NaN
           // is NaN)
           uint32_t va[4][kG], ve[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            ve[y] = lds32(fv + (key[y] * kG + (g & (kG - 1))) * 4) & live;
-            lds_words<kG>(fv + key[y] * kG * 4, va[y]);
+            const uint32_t at4 = fv + (key + 8 * (y >> 1) + (y & 1)) * kG * 4;
+            ve[y] = lds32(at4 + (g & (kG - 1)) * 4);
+            lds_words<kG>(at4, va[y]);
           }
           if (end) {
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-              if (key[y] >= left) {
+              if (key + 8 * (y >> 1) + (y & 1) >= left) {
                 ve[y] = 0u;
 #pragma unroll
                 for (int x = 0; x < kG; ++x) va[y][x] = 0u;
               }
           }
-          {  // sums of p b' and p s'
-            const uint32_t h0 = bf16x2_bits(s[0], s[1]), h1 = bf16x2_bits(s[2], s[3]);
-            const uint32_t l0 = bf16x2_bits(s[0] - __uint_as_float(h0 << 16), s[1] - __uint_as_float(h0 & 0xffff0000u));
-            const uint32_t l1 = bf16x2_bits(s[2] - __uint_as_float(h1 << 16), s[3] - __uint_as_float(h1 & 0xffff0000u));
-            const uint32_t a0 = __byte_perm(ve[0], ve[1], pick), a2 = __byte_perm(ve[2], ve[3], pick);
-            mma_bf16(e, a0, 0u, a2, 0u, h0, h1);
-            mma_bf16(e, a0, 0u, a2, 0u, l0, l1);
+          {  // sums of p b' (rows g, group g % kG) and p s' (rows g + 8)
+            const uint32_t a0 = __byte_perm(ve[0], ve[1], 0x7632), a1 = __byte_perm(ve[0], ve[1], 0x5410);
+            const uint32_t a2 = __byte_perm(ve[2], ve[3], 0x7632), a3 = __byte_perm(ve[2], ve[3], 0x5410);
+            mma_bf16(e, a0, a1, a2, a3, h0, h1);
+            mma_bf16(e, a0, a1, a2, a3, l0, l1);
           }
-          // the values: the same byte of two tokens' codes side by side in a word
-          const uint32_t v0 = sv + vat[0], v1 = sv + vat[1], v2 = sv + vat[2], v3 = sv + vat[3];
+          // the values: transposed, so that a word has four columns of two tokens
 #pragma unroll
           for (int x = 0; x < kG; ++x) {
             float p[4];
 #pragma unroll
-            for (int y = 0; y < 4; ++y) p[y] = s[y] * __uint_as_float(va[y][x] << 16);
+            for (int y = 0; y < 4; ++y) p[y] = pt[y] * __uint_as_float(va[y][x] << 16);
             const uint32_t b0 = bf16x2_bits(p[0], p[1]), b1 = bf16x2_bits(p[2], p[3]);
-            const uint32_t w0 = lds32(v0 ^ (32 * x)), w1 = lds32(v1 ^ (32 * x));
-            const uint32_t w2 = lds32(v2 ^ (32 * x)), w3 = lds32(v3 ^ (32 * x));
+            uint32_t w[4];  // tokens 0 .. 7, 8 .. 15 of 32 columns, then 32 columns on
+            ldsm4_t((sv + mat) ^ (32 * x), w);
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-              const uint32_t lo = __byte_perm(w0, w1, 0x0400 + t * 0x0101);
-              const uint32_t hi = __byte_perm(w2, w3, 0x0400 + t * 0x0101);
+              const uint32_t lo = w[t & 2] >> (8 * (t & 1)), hi = w[(t & 2) + 1] >> (8 * (t & 1));
               mma_bf16(o[x][t], plus128(lo), plus128(lo >> 4), plus128(hi), plus128(hi >> 4), b0, b1);
               mma_bf16(o[x][t], kMinus136, kMinus136, kMinus136, kMinus136, b0, b1);
             }
@@ -560,21 +592,28 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&ctl.empty[now]));
       }
+      mine = i - n;
       // join the warps' parts (also after an abort: all warps meet here)
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if (c == 0) {
-        ctl.m[warp][g] = m;
-        ctl.l[warp][g] = l;
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) l[z] += __shfl_xor_sync(0xffffffffu, l[z], x);
+        if (g == 0) {
+          ctl.m[warp][2 * c + z] = m[z];
+          ctl.l[warp][2 * c + z] = l[z];
+        }
       }
-      *reinterpret_cast<float2 *>(&ctl.e[warp][g][2 * c]) = make_float2(e[0], e[1]);
+      if (g < kG) {
+        *reinterpret_cast<float2 *>(&ctl.e[warp][g][2 * c]) = make_float2(e[0], e[1]);
+        *reinterpret_cast<float2 *>(&ctl.e[warp][4 + g][2 * c]) = make_float2(e[2], e[3]);
+      }
 #pragma unroll
       for (int x = 0; x < kG; ++x)
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          float *to = obuf + (warp * kHeads + 2 * c + z) * P::kPitch + 64 * x + 8 * g;
+          float *to = obuf + (warp * kHeads + 2 * c + z) * P::kPitch + 64 * x + 4 * g;
           *reinterpret_cast<float4 *>(to) = make_float4(o[x][0][z], o[x][0][2 + z], o[x][1][z], o[x][1][2 + z]);
-          *reinterpret_cast<float4 *>(to + 4) = make_float4(o[x][2][z], o[x][2][2 + z], o[x][3][z], o[x][3][2 + z]);
+          *reinterpret_cast<float4 *>(to + 32) = make_float4(o[x][2][z], o[x][2][2 + z], o[x][3][z], o[x][3][2 + z]);
         }
       named_bar_sync(1, 32 * kConsumers);
       if (warp < heads) {
