@@ -33,6 +33,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cstddef>
 #include <mutex>
 
 #include "../../include/moe.h"
@@ -44,7 +45,9 @@ namespace {
 
 constexpr int kConsumers = 12;
 constexpr int kTeams = kConsumers / 4;  // of four warps, that take a page each
-constexpr int kThreadsD = 32 * (kConsumers + 1);
+constexpr int kThreadsD = 32 * (kConsumers + 4);  // (whole warpgroups, for their shares of the registers)
+// 128 registers a thread at launch: 16 warps x 32 x 128 = 12 x 32 x 152 + 4 x 32 x 40 + 2048
+constexpr int kRegsConsumer = 152, kRegsProducer = 40;
 constexpr int kHeads = 8;  // query heads of a row
 constexpr int kPagesDeep = 6;
 constexpr int kJoinThreads = 512;
@@ -80,11 +83,12 @@ struct DCtl {
   uint64_t full[kPagesDeep], empty[kPagesDeep];
   int ok[kPagesDeep];  // whether the stage holds a page
   int abort_flag, seq, at;  // at: the share's first unit within sequence seq's
-  int warp_sum[kConsumers + 1];
+  int warp_sum[kConsumers + 4];
   float m[kConsumers][kHeads], l[kConsumers][kHeads];
-  float e[kConsumers][8][kHeads];  // sum of p b' of each group, then of p s'
+  alignas(16) float e[kConsumers][8][kHeads];  // sum of p b' of each group, then of p s'
   uint4 q[4][2][32];  // a row's queries as the first product's A: [group][8 columns][lane]
-  float qsum[4][kHeads], unit[kHeads][2];
+  float qsum[4][kHeads];
+  alignas(16) float unit[kHeads][2];
   uint2 qbias[32];  // the sums of q as the A of the biases' product
 };
 
@@ -95,14 +99,14 @@ __device__ __forceinline__ float fast_exp2(float x) {
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -110,14 +114,14 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
 // the first of a sum
 __device__ __forceinline__ void mma0_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ void mma0_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
@@ -170,7 +174,7 @@ __device__ __forceinline__ void ldsm4_t(uint32_t a, uint32_t (&r)[4]) {
 // an 8 x 8 matrix of 16-bit values (row l / 4, values 2 (l % 4), + 1 in lane l) transposed
 __device__ __forceinline__ uint32_t turned(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 // 16-byte piece of a row of codes in a stage, swizzled by TMA (128-byte or 64-byte
@@ -216,6 +220,10 @@ __device__ __forceinline__ bool consumers_any(bool bad) {
 }
 
 }  // namespace
+
+static_assert(offsetof(DCtl, e) % 16 == 0 && offsetof(DCtl, unit) % 16 == 0 && offsetof(DCtl, q) % 16 == 0 &&
+                  offsetof(DCtl, qbias) % 8 == 0,
+              "read and written as vectors");
 
 // The queries as the first product's A: fp16 of q 2^-power, in the column order in
 // which nibbles come out of a word (every other pair 4 bits up there, so 2^-4
@@ -335,7 +343,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
   if (lane == 31) ctl.warp_sum[warp] = upto;
   __syncthreads();
   int before = upto - sum, total = 0;
-  for (int w = 0; w <= kConsumers; ++w) {
+  for (int w = 0; w < kThreadsD / 32; ++w) {
     if (w < warp) before += ctl.warp_sum[w];
     total += ctl.warp_sum[w];
   }
@@ -367,8 +375,10 @@ __global__ void __launch_bounds__(kThreadsD, 1)
   int u = u0, at = ctl.at;
   int np = u0 < u1 ? pages_of(a, seq, len) : 0;
   bool ok = true;
-  if (warp == kConsumers) {
+  if (warp >= kConsumers) {
     // ------------------------------------------------------------ copies
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProducer));
+    if (warp > kConsumers) return;
     const uint64_t pol = policy_evict_first();
     while (ok && u < u1) {
       if (at >= np * R) {
@@ -421,6 +431,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
       for (int i = 0; i < 200; ++i) __nanosleep(1000);
   } else {
     // ------------------------------------------------------------ tokens
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsConsumer));
     const int g = lane >> 2, c = lane & 3, tile = 16 * (warp & 3);
     // this lane's tokens: columns 2 c, 2 c + 1 of the two score tiles of 8
     const int key = tile + 2 * c;
