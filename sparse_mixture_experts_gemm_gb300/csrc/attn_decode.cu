@@ -19,16 +19,18 @@
 // multiplies codes less 8 (and that of p to 2^-16 with the biases).
 //
 // Work split.  All (sequence, key/value head, 8 query heads) rows' pages lie on one
-// line that is cut into equal shares, one per SM, whatever the lengths; a CTA
-// finds its share from the lengths on the device.  Rows that are cut leave their
-// parts (maximum, sum, output) in the workspace for a second kernel, which joins
+// line that is cut into equal shares, three per SM, whatever the lengths; a CTA
+// finds its shares from the lengths on the device.  Rows that are cut leave their
+// parts (output, maximum, sum) in the workspace for a second kernel, which joins
 // them in a fixed order.
 //
-// Roles: warp 12 copies pages by TMA (6 pages deep), warps 0-11 take 16 tokens of a
-// page each, four warps per page, with a running softmax of their own; their parts
-// are joined through shared memory at a row's end.  The codes are the A operand of
-// both products (tokens x columns, columns x tokens), whose four registers the
-// dequantisation fills as they are; P is turned in between, four 8 x 8 matrices.
+// Roles: three teams of four warps have a share each; a page's tokens go to the four
+// warps by 16, with a running softmax of their own, and their parts are joined
+// through shared memory at a row's end, while the other teams go on (with one share
+// per SM and all warps on it, every row's end cost 5 us).  Warps 12-14 walk along the
+// teams' rows and copy their pages by TMA, three ahead.  The codes are the A operand of both products (tokens x columns, columns x
+// tokens), whose four registers the dequantisation fills as they are; P is turned in
+// between, four 8 x 8 matrices.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -43,18 +45,17 @@ namespace moe {
 
 namespace {
 
-constexpr int kConsumers = 12;
-constexpr int kTeams = kConsumers / 4;  // of four warps, that take a page each
+constexpr int kTeams = 3, kTeamWarps = 4;
+constexpr int kConsumers = kTeams * kTeamWarps;
 constexpr int kThreadsD = 32 * (kConsumers + 4);  // (whole warpgroups, for their shares of the registers)
-// 128 registers a thread at launch: 16 warps x 32 x 128 = 12 x 32 x 152 + 4 x 32 x 40 + 2048
-constexpr int kRegsConsumer = 152, kRegsProducer = 40;
-constexpr int kHeads = 8;  // query heads of a row
-constexpr int kPagesDeep = 6;
-constexpr int kJoinThreads = 512;
-static_assert(kPagesDeep % kTeams == 0, "a team's pages are in the same stages");
+// 128 registers a thread at launch: 16 x 32 x 128 = 12 x 32 x 152 + 4 x 32 x 48 + 1024
+constexpr int kRegsConsumer = 152, kRegsProducer = 48;
+constexpr int kHeads = 8;      // query heads of a row
+constexpr int kPagesDeep = 3;  // of a team
+constexpr int kRowsDeep = 4;   // more than kPagesDeep: that many rows can the copies be ahead
+constexpr int kJoinThreads = 256;
 constexpr float kLateDecode = 8.0f;  // as in attn_prefill.cu
-constexpr int kShares = 152;         // one per SM
-static_assert(kShares <= kJoinThreads, "a thread per part");
+constexpr int kCtas = 152, kShares = kCtas * kTeams;  // one CTA per SM
 
 struct DecodeAttnArgs {
   CacheArgs c;
@@ -65,32 +66,48 @@ struct DecodeAttnArgs {
   int n_seq, Hq, group, blocks;  // blocks: rows of a key/value head, 8 query heads each
   float scale;                   // times log2(e)
   int4 *head;                    // [kShares]: what is to be joined
-  float *part;                   // [2 kShares][8][D + 2]: output, maximum, sum
+  float *part;                   // [2 kShares][8][D + 4]: output, maximum, sum
+};
+
+// A row, or the part of it that lies in a share: what the roles walk along.
+struct Row {
+  int u, at, seq, np, len;  // unit, unit within the sequence's, the sequence, its pages and tokens
+  int h, head0, heads;      // key/value head, first query head of the 8 in its group, how many
+  int p0, n;                // first page, pages
+};
+
+struct Team {
+  uint64_t full[kPagesDeep], empty[kPagesDeep], row[kRowsDeep];
+  int ok[kPagesDeep];  // whether the stage holds a page
+  int u0, u1, seq, at;  // the share; its first unit's sequence, unit within the sequence's
+  // rows: pages (0: no more), tokens from the first on, heads, row of out, place of
+  // the part or -1, sequence, query head.  Read until the row's end, when the copies
+  // are at most kPagesDeep rows on.
+  struct {
+    int n, left, heads, out, slot, seq, head;
+  } todo[2 * kRowsDeep];
+  float m[kTeamWarps][kHeads], l[kTeamWarps][kHeads];
+  uint32_t most[kTeamWarps][kHeads];
+  float qsum[4][kHeads];
+  alignas(16) uint4 q[4][2][32];  // a row's queries as the first product's B: [group][32 columns][lane]
+};
+
+struct DCtl {
+  Team team[kTeams];
+  int abort_flag, total;  // total: all units
+  int warp_sum[4];
 };
 
 template <int D>
 struct Page {
   static constexpr int kCodes = kPage * D / 2, kAffine = kPage * (D / kGroup) * 4;
   static constexpr int kBytes = 2 * (kCodes + kAffine);
-  static constexpr int kPitch = D + 8;  // of the warps' outputs
-  static constexpr int kOut = kConsumers * kHeads * kPitch * 4;
-  static constexpr int kCtl = 12288;
-  static constexpr int kTotal = kPagesDeep * kBytes + kOut + kCtl + 1024;
+  static constexpr int kOut = kHeads * D * 4;  // a warp's output
+  static constexpr int kSlots = kTeams * 2;
+  static constexpr int kTotal = kTeams * kPagesDeep * kBytes + kSlots * kOut + static_cast<int>(sizeof(DCtl)) + 1024;
   static_assert(kTotal <= 227 * 1024 && kBytes % 1024 == 0, "shared memory");
 };
-
-struct DCtl {
-  uint64_t full[kPagesDeep], empty[kPagesDeep];
-  int ok[kPagesDeep];  // whether the stage holds a page
-  int abort_flag, seq, at;  // at: the share's first unit within sequence seq's
-  int warp_sum[kConsumers + 4];
-  float m[kConsumers][kHeads], l[kConsumers][kHeads];
-  alignas(16) float e[kConsumers][8][kHeads];  // sum of p b' of each group, then of p s'
-  uint4 q[4][2][32];  // a row's queries as the first product's A: [group][8 columns][lane]
-  float qsum[4][kHeads];
-  alignas(16) float unit[kHeads][2];
-  uint2 qbias[32];  // the sums of q as the A of the biases' product
-};
+static_assert(offsetof(Team, q) % 16 == 0 && sizeof(Team) % 16 == 0, "read and written as vectors");
 
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
@@ -207,95 +224,133 @@ __device__ __forceinline__ bool poll_d(uint32_t bar, uint32_t parity, const vola
   }
   return false;
 }
-// named barrier of the consumers that tells each whether any of them brought `bad`
-__device__ __forceinline__ bool consumers_any(bool bad) {
+// named barrier of a team that tells each whether any of them brought `bad`
+__device__ __forceinline__ bool team_any(int id, bool bad) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred.aligned q, 2, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.or.pred.aligned q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(bad ? 1u : 0u), "n"(32 * kConsumers)
+      : "r"(bad ? 1u : 0u), "r"(id), "n"(32 * kTeamWarps)
       : "memory");
   return r != 0;
 }
 
 }  // namespace
 
-static_assert(offsetof(DCtl, e) % 16 == 0 && offsetof(DCtl, unit) % 16 == 0 && offsetof(DCtl, q) % 16 == 0 &&
-                  offsetof(DCtl, qbias) % 8 == 0,
-              "read and written as vectors");
+// the share's start; then to the next row, false: the share is done
+__device__ __forceinline__ void start_row(Row &r, const DecodeAttnArgs &a, const Team &t) {
+  r.u = t.u0;
+  r.at = t.at;
+  r.seq = t.seq;
+  r.np = r.len = r.n = 0;
+  if (t.u0 < t.u1) r.np = pages_of(a, r.seq, r.len);
+}
+__device__ __forceinline__ bool next_row(Row &r, const DecodeAttnArgs &a, const Team &t) {
+  r.u += r.n;
+  r.at += r.n;
+  if (r.u >= t.u1) return false;
+  while (r.at >= r.np * a.c.H * a.blocks) {
+    ++r.seq;
+    r.at = 0;
+    r.np = pages_of(a, r.seq, r.len);
+  }
+  const int x = r.at / r.np;
+  r.h = x / a.blocks;
+  r.head0 = x % a.blocks * kHeads;
+  r.heads = min(kHeads, a.group - r.head0);
+  r.p0 = r.at % r.np;
+  r.n = min(r.np - r.p0, t.u1 - r.u);
+  return true;
+}
 
-// The queries as the first product's A: fp16 of q 2^-power, in the column order in
-// which nibbles come out of a word (every other pair 4 bits up there, so 2^-4
-// here), and their sums over the groups in the same unit as the products.
+// A row's queries as the first product's B, by a team's warps, which have a group of
+// 64 columns each (lane (g, c): head g, columns 8 c .. of each 32): fp16 of q
+// 2^-power, in the column order in which nibbles come out of a word (every other
+// pair 4 bits up there, so 2^-4 here), and their sums in the same unit as the
+// products, all of which each warp then takes as the B of the biases' product.
+// unit: what scores of heads 2 c, 2 c + 1 are to be multiplied with, in two steps
+// within range.
 template <int D>
-__device__ __forceinline__ void make_queries(const DecodeAttnArgs &a, DCtl &ctl, int seq, int head, int heads) {
+__device__ __forceinline__ void make_queries(const DecodeAttnArgs &a, Team &t, int tw, int sync, int seq, int head,
+                                             int heads, uint2 &qbias, float2 (&unit)[2]) {
   constexpr int kG = D / kGroup;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const __nv_bfloat16 *src = a.q + seq * a.qs + static_cast<long long>(head + (g < heads ? g : 0)) * D + 8 * c;
-  uint4 v[kG][2];
+  uint32_t w[2][4] = {};
+  if (tw < kG && g < heads) {
+    const __nv_bfloat16 *src = a.q + seq * a.qs + static_cast<long long>(head + g) * D + 64 * tw + 8 * c;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(src + 32 * i);
+      w[i][0] = v.x;
+      w[i][1] = v.y;
+      w[i][2] = v.z;
+      w[i][3] = v.w;
+    }
+  }
   uint32_t most = 0;
 #pragma unroll
-  for (int x = 0; x < kG; ++x)
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      v[x][t] = make_uint4(0, 0, 0, 0);
-      if (g < heads) v[x][t] = *reinterpret_cast<const uint4 *>(src + 64 * x + 32 * t);
-      const uint32_t w[4] = {v[x][t].x, v[x][t].y, v[x][t].z, v[x][t].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) most = max(most, max(w[i] << 16 & 0x7fff0000u, w[i] & 0x7fff0000u));
-    }
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t x = w[i >> 2][i & 3];
+    most = max(most, max(x << 16 & 0x7fff0000u, x & 0x7fff0000u));
+  }
   most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
   most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
-  const int power = min(max(static_cast<int>(most >> 23) - 127 - 12, -126), 126);
-  const float down = __uint_as_float(static_cast<uint32_t>(127 - power) << 23);
+  if (c == 0) t.most[tw][g] = most;
+  named_bar_sync(sync, 32 * kTeamWarps);
+  auto power_of = [&](int hd) {
+    uint32_t x = 0;
 #pragma unroll
-  for (int x = 0; x < kG; ++x) {
+    for (int i = 0; i < kG; ++i) x = max(x, t.most[i][hd]);
+    return min(max(static_cast<int>(x >> 23) - 127 - 12, -126), 126);
+  };
+  const int power = power_of(g);
+  const float down = __uint_as_float(static_cast<uint32_t>(127 - power) << 23);
+  if (tw < kG) {
     float sum = 0.0f;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const uint32_t w[4] = {v[x][t].x, v[x][t].y, v[x][t].z, v[x][t].w};
+    for (int i = 0; i < 2; ++i) {
       float f[8];
       uint32_t y[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16) * down;
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * down;
-        sum += f[2 * i] + f[2 * i + 1];
+      for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(w[i][j] << 16) * down;
+        f[2 * j + 1] = __uint_as_float(w[i][j] & 0xffff0000u) * down;
+        sum += f[2 * j] + f[2 * j + 1];
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float up = i & 1 ? 0x1p-4f : 1.0f;
-        const __half2 z = __floats2half2_rn(f[i] * up, f[i + 4] * up);
-        y[i] = *reinterpret_cast<const uint32_t *>(&z);
+      for (int j = 0; j < 4; ++j) {
+        const float up = j & 1 ? 0x1p-4f : 1.0f;
+        const __half2 z = __floats2half2_rn(f[j] * up, f[j + 4] * up);
+        y[j] = *reinterpret_cast<const uint32_t *>(&z);
       }
-      ctl.q[x][t][lane] = make_uint4(y[0], y[1], y[2], y[3]);
+      t.q[tw][i][lane] = make_uint4(y[0], y[1], y[2], y[3]);
     }
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    if (c == 0) ctl.qsum[x][g] = sum * 0x1p-24f;
+    if (c == 0) t.qsum[tw][g] = sum * 0x1p-24f;
   }
-  __syncwarp();
-  {  // index k of the biases' product: group k % kG of part k / kG of the sums
-    float part[2][2];
+  // scores come out in units of 2^(power + 24)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+  for (int z = 0; z < 2; ++z) {
+    const int all = power_of(2 * c + z) + 24, first = all / 2;
+    unit[z] = make_float2(__uint_as_float(static_cast<uint32_t>(127 + first) << 23),
+                          a.scale * __uint_as_float(static_cast<uint32_t>(127 + all - first) << 23));
+  }
+  named_bar_sync(sync, 32 * kTeamWarps);
+  // index k of the biases' product: group k % kG of part k / kG of the sums
+  float part[2][2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int k = 2 * c + j + 8 * i, which = k / kG;
-        const float all = ctl.qsum[k % kG][g];
-        const float hi = __bfloat162float(__float2bfloat16_rn(all));
-        const float mid = __bfloat162float(__float2bfloat16_rn(all - hi));
-        part[i][j] = which == 0 ? hi : which == 1 ? mid : which == 2 ? all - hi - mid : 0.0f;
-      }
-    ctl.qbias[lane] = make_uint2(bf16x2_bits(part[0][0], part[0][1]), bf16x2_bits(part[1][0], part[1][1]));
-  }
-  if (c == 0) {
-    // scores come out in units of 2^(power + 24), taken off in two steps within range
-    const int first = (power + 24) / 2;
-    ctl.unit[g][0] = __uint_as_float(static_cast<uint32_t>(127 + first) << 23);
-    ctl.unit[g][1] = a.scale * __uint_as_float(static_cast<uint32_t>(127 + power + 24 - first) << 23);
-  }
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int k = 2 * c + j + 8 * i, which = k / kG;
+      const float all = t.qsum[k % kG][g];
+      const float hi = __bfloat162float(__float2bfloat16_rn(all));
+      const float mid = __bfloat162float(__float2bfloat16_rn(all - hi));
+      part[i][j] = which == 0 ? hi : which == 1 ? mid : which == 2 ? all - hi - mid : 0.0f;
+    }
+  qbias = make_uint2(bf16x2_bits(part[0][0], part[0][1]), bf16x2_bits(part[1][0], part[1][1]));
 }
 
 template <int D>
@@ -305,203 +360,221 @@ __global__ void __launch_bounds__(kThreadsD, 1)
   constexpr int kG = D / kGroup;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = align1024(smem_raw);
-  float *obuf = reinterpret_cast<float *>(smem + kPagesDeep * P::kBytes);
-  DCtl &ctl = *reinterpret_cast<DCtl *>(smem + kPagesDeep * P::kBytes + P::kOut);
-  static_assert(sizeof(DCtl) <= P::kCtl, "control block");
+  uint8_t *slots = smem + kTeams * kPagesDeep * P::kBytes;
+  DCtl &ctl = *reinterpret_cast<DCtl *>(slots + P::kSlots * P::kOut);
   volatile int *abort_flag = &ctl.abort_flag;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int R = a.c.H * a.blocks, cta = blockIdx.x;
-  if (tid == 0) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, cta = blockIdx.x;
+  if (tid < kTeams) {
+    Team &t = ctl.team[tid];
     for (int s = 0; s < kPagesDeep; ++s) {
-      mbar_init(smem_u32(&ctl.full[s]), 1);
-      mbar_init(smem_u32(&ctl.empty[s]), 4);
+      mbar_init(smem_u32(&t.full[s]), 1);
+      mbar_init(smem_u32(&t.empty[s]), kTeamWarps);
     }
+    for (int r = 0; r < kRowsDeep; ++r) mbar_init(smem_u32(&t.row[r]), 1);
+    t.seq = t.at = 0;
     ctl.abort_flag = 0;
-    ctl.seq = 0;
-    ctl.at = 0;
     fence_mbar_init();
     prefetch_tmap(&tm);
   }
-  pdl_wait();
-  pdl_launch_dependents();
-  // pages before each thread's sequences, and the share's start
-  const int per = (a.n_seq + kThreadsD - 1) / kThreadsD, i0 = min(tid * per, a.n_seq), i1 = min(i0 + per, a.n_seq);
-  int sum = 0;
-  bool over = false;
-  for (int i = i0; i < i1; ++i) {
-    int len;
-    sum += pages_of(a, i, len);
-    over = over || a.lengths[i] > len;
-  }
-  if (over && cta == 0) report_error(a.c.status, MOE_ERR_DEVICE_BOUNDS, KID_ATTN_DECODE * 100 + SITE_INDEX);
-  int upto = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += u;
-  }
-  if (lane == 31) ctl.warp_sum[warp] = upto;
   __syncthreads();
-  int before = upto - sum, total = 0;
-  for (int w = 0; w < kThreadsD / 32; ++w) {
-    if (w < warp) before += ctl.warp_sum[w];
-    total += ctl.warp_sum[w];
-  }
-  total *= R;
-  const int u0 = share_at(total, cta), u1 = share_at(total, cta + 1);
-  if (u0 < u1 && u0 >= before * R && u0 < (before + sum) * R) {
-    int at = u0 - before * R;
+  auto timeout = [&](int site) {
+    if (lane == 0) {
+      *abort_flag = 1;
+      report_error(a.c.status, MOE_ERR_DEVICE_TIMEOUT, KID_ATTN_DECODE * 100 + site);
+    }
+  };
+  constexpr int kSetup = 4, kSync = 5, kEnd = 8;  // named barriers; the last two one per team
+
+  if (warp >= kConsumers) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProducer));
+    const int x = tid - 32 * kConsumers, role = warp - kConsumers;
+    const int R = a.c.H * a.blocks;
+    pdl_wait();
+    pdl_launch_dependents();
+    // pages before each thread's sequences, and the shares' starts
+    const int per = (a.n_seq + 127) / 128, i0 = min(x * per, a.n_seq), i1 = min(i0 + per, a.n_seq);
+    int sum = 0;
+    bool over = false;
     for (int i = i0; i < i1; ++i) {
       int len;
-      const int mine = pages_of(a, i, len) * R;
-      if (at < mine) {
-        ctl.seq = i;
-        ctl.at = at;
-        break;
-      }
-      at -= mine;
+      sum += pages_of(a, i, len);
+      over = over || a.lengths[i] > len;
     }
-  }
-  if (tid == 0) a.head[cta] = make_int4(0, 0, 0, 0);
-  __syncthreads();
-  // sequences without tokens: zeros
-  for (int i = cta; i < a.n_seq; i += kShares)
-    if (a.lengths[i] <= 0 || a.c.width == 0)
-      for (int x = tid; x < a.Hq * D / 8; x += kThreadsD)
-        reinterpret_cast<uint4 *>(a.out + static_cast<long long>(i) * a.Hq * D)[x] = make_uint4(0, 0, 0, 0);
-
-  int seq = ctl.seq, st = 0, len = 0;
-  uint32_t phase = 0;
-  int u = u0, at = ctl.at;
-  int np = u0 < u1 ? pages_of(a, seq, len) : 0;
-  bool ok = true;
-  if (warp >= kConsumers) {
-    // ------------------------------------------------------------ copies
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProducer));
-    if (warp > kConsumers) return;
-    const uint64_t pol = policy_evict_first();
-    while (ok && u < u1) {
-      if (at >= np * R) {
-        ++seq;
-        at = 0;
-        np = pages_of(a, seq, len);
-        continue;
-      }
-      const int h = at / np / a.blocks, p0 = at % np, n = min(min(np - p0, 32), u1 - u);
-      int page = -1;
-      if (lane < n) {
-        page = page_of(a.c, seq, static_cast<long long>(p0 + lane) * kPage);
-        if (page < 0) report_error(a.c.status, MOE_ERR_DEVICE_BOUNDS, KID_ATTN_DECODE * 100 + SITE_INDEX);
-      }
-      for (int i = 0; i < n; ++i) {
-        const int pg = __shfl_sync(0xffffffffu, page, i);
-        ok = __all_sync(0xffffffffu, poll_d(smem_u32(&ctl.empty[st]), phase ^ 1, abort_flag));
-        if (!ok) {
-          if (lane == 0) {
-            *abort_flag = 1;
-            report_error(a.c.status, MOE_ERR_DEVICE_TIMEOUT, KID_ATTN_DECODE * 100 + SITE_PRODUCER_EMPTY);
+    if (over && cta == 0) report_error(a.c.status, MOE_ERR_DEVICE_BOUNDS, KID_ATTN_DECODE * 100 + SITE_INDEX);
+    int upto = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += u;
+    }
+    if (lane == 31) ctl.warp_sum[role] = upto;
+    named_bar_sync(kSetup, 128);
+    int before = upto - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      if (w < role) before += ctl.warp_sum[w];
+      total += ctl.warp_sum[w];
+    }
+    total *= R;
+    for (int k = 0; k < kTeams; ++k) {
+      // (the first shares, which have units when there are few, are on different SMs)
+      const int share = k * kCtas + cta, u0 = share_at(total, share), u1 = share_at(total, share + 1);
+      Team &t = ctl.team[k];
+      if (u0 < u1 && u0 >= before * R && u0 < (before + sum) * R) {
+        int at = u0 - before * R;
+        for (int i = i0; i < i1; ++i) {
+          int len;
+          const int units = pages_of(a, i, len) * R;
+          if (at < units) {
+            t.seq = i;
+            t.at = at;
+            break;
           }
-          break;
+          at -= units;
         }
+      }
+      if (x == k) {
+        t.u0 = u0;
+        t.u1 = u1;
+        a.head[share] = make_int4(0, 0, 0, 0);
+      }
+    }
+    named_bar_sync(kSetup, 128);
+    bool ok = true;
+    if (role < kTeams) {
+      // ---------------------------------------------------------- copies of a team's pages
+      Team &t = ctl.team[role];
+      uint8_t *stages = smem + role * kPagesDeep * P::kBytes;
+      const uint64_t pol = policy_evict_first();
+      Row r;
+      start_row(r, a, t);
+      int st = 0;
+      uint32_t phase = 0;
+      for (int nr = 0; ok; ++nr) {
+        const bool more = next_row(r, a, t);
         if (lane == 0) {
-          ctl.ok[st] = pg >= 0;
-          const uint32_t fb = smem_u32(&ctl.full[st]);
-          uint8_t *dst = smem + st * P::kBytes;
-          if (pg < 0) {
-            mbar_arrive(fb);
-          } else {
-            mbar_arrive_expect_tx(fb, P::kBytes);
-            for (int w = 0; w < 2; ++w) {
-              const long long row = cache_row(a.c, pg, w, h, 0);
-              tma_load_2d(smem_u32(dst) + w * P::kCodes, &tm, fb, 0, static_cast<int>(row), pol);
-              bulk_g2s(dst + 2 * P::kCodes + w * P::kAffine, a.c.affine + row * kG, P::kAffine, &ctl.full[st]);
+          auto &todo = t.todo[nr % (2 * kRowsDeep)];
+          const int share = role * kCtas + cta;
+          const bool whole = r.n == r.np;
+          todo.n = more ? r.n : 0;
+          todo.left = r.len - r.p0 * kPage;
+          todo.heads = r.heads;
+          todo.seq = r.seq;
+          todo.head = r.h * a.group + r.head0;
+          todo.out = r.seq * a.Hq + todo.head;
+          todo.slot = whole ? -1 : 2 * share + (r.u == t.u0 ? 0 : 1);
+          mbar_arrive(smem_u32(&t.row[nr % kRowsDeep]));
+        }
+        if (!more) break;
+        int pages = -1;  // numbers of 32 pages at a time
+        for (int i = 0; i < r.n; ++i) {
+          if ((i & 31) == 0) {
+            pages = -1;
+            if (i + lane < r.n) {
+              pages = page_of(a.c, r.seq, static_cast<long long>(r.p0 + i + lane) * kPage);
+              if (pages < 0) report_error(a.c.status, MOE_ERR_DEVICE_BOUNDS, KID_ATTN_DECODE * 100 + SITE_INDEX);
             }
           }
+          const int page = __shfl_sync(0xffffffffu, pages, i & 31);
+          ok = __all_sync(0xffffffffu, poll_d(smem_u32(&t.empty[st]), phase ^ 1, abort_flag));
+          if (!ok) {
+            timeout(SITE_PRODUCER_EMPTY);
+            break;
+          }
+          if (lane == 0) {
+            t.ok[st] = page >= 0;
+            const uint32_t fb = smem_u32(&t.full[st]);
+            uint8_t *dst = stages + st * P::kBytes;
+            if (page < 0) {
+              mbar_arrive(fb);
+            } else {
+              mbar_arrive_expect_tx(fb, P::kBytes);
+              for (int w = 0; w < 2; ++w) {
+                const long long row = cache_row(a.c, page, w, r.h, 0);
+                tma_load_2d(smem_u32(dst) + w * P::kCodes, &tm, fb, 0, static_cast<int>(row), pol);
+                bulk_g2s(dst + 2 * P::kCodes + w * P::kAffine, a.c.affine + row * kG, P::kAffine, &t.full[st]);
+              }
+            }
+          }
+          __syncwarp();
+          if (++st == kPagesDeep) {
+            st = 0;
+            phase ^= 1;
+          }
+        }
+        if (lane == 0 && r.p0 == 0 && r.n < r.np) {  // the row starts here: this share's entry says how it goes on
+          const int share = role * kCtas + cta, last = r.u + r.np - 1;
+          int end = static_cast<int>(min(((last + 1LL) * kShares - 1) / total, kShares - 1LL));
+          while (share_at(total, end + 1) <= last) ++end;
+          while (share_at(total, end) > last) --end;
+          a.head[share] = make_int4(end - share + 1, 2 * share + (r.u == t.u0 ? 0 : 1),
+                                    r.seq * a.Hq + r.h * a.group + r.head0, r.heads);
         }
         __syncwarp();
-        if (++st == kPagesDeep) {
-          st = 0;
-          phase ^= 1;
-        }
       }
-      u += n;
-      at += n;
+      if (!ok && lane == 0)  // copies in flight get time to land
+        for (int i = 0; i < 200; ++i) __nanosleep(1000);
+    } else {
+      // sequences without tokens: zeros
+      for (int i = cta; i < a.n_seq; i += kCtas)
+        if (a.lengths[i] <= 0 || a.c.width == 0)
+          for (int y = lane; y < a.Hq * D / 8; y += 32)
+            reinterpret_cast<uint4 *>(a.out + static_cast<long long>(i) * a.Hq * D)[y] = make_uint4(0, 0, 0, 0);
     }
-    if (!ok && lane == 0)  // copies in flight get time to land
-      for (int i = 0; i < 200; ++i) __nanosleep(1000);
   } else {
     // ------------------------------------------------------------ tokens
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsConsumer));
-    const int g = lane >> 2, c = lane & 3, tile = 16 * (warp & 3);
-    // this lane's tokens: columns 2 c, 2 c + 1 of the two score tiles of 8
-    const int key = tile + 2 * c;
-    // rows of codes for the matrix loads: keys 8 (m & 1) + .. , pieces m >> 1 of matrix
-    // m; values the same
-    const int mrow = tile + 8 * ((lane >> 3) & 1) + (lane & 7);
-    const uint32_t mat = piece_at<D>(mrow, lane >> 4);
-    int mine = warp >> 2;
-    st = mine;
-    while (u < u1) {
-      if (at >= np * R) {
-        ++seq;
-        at = 0;
-        np = pages_of(a, seq, len);
-        continue;
-      }
-      // a row, or the part of it that lies in this share
-      const int rr = at / np, h = rr / a.blocks, head0 = rr % a.blocks * kHeads;
-      const int heads = min(kHeads, a.group - head0), p0 = at % np;
-      const int n = min(np - p0, u1 - u);
-      const long long orow = static_cast<long long>(seq) * a.Hq + h * a.group + head0;
-      // (all warps have left the row before)
-      if (warp == 0) make_queries<D>(a, ctl, seq, h * a.group + head0, heads);
-      named_bar_sync(1, 32 * kConsumers);
-      const uint32_t sq = smem_u32(&ctl.q[0][0][lane]);
-      const uint2 qb = ctl.qbias[lane];
-      const float2 unit[2] = {*reinterpret_cast<const float2 *>(ctl.unit[2 * c]),
-                              *reinterpret_cast<const float2 *>(ctl.unit[2 * c + 1])};
+    const int team = warp / kTeamWarps, tw = warp % kTeamWarps;
+    const int g = lane >> 2, c = lane & 3, tile = 16 * tw;
+    Team &t = ctl.team[team];
+    // places in a stage: rows of codes for the matrix loads (matrix m: rows 8 (m & 1)
+    // .. of 16, piece m >> 1), scales and biases of this lane's tokens as rows of the
+    // scores (g, g + 8 of 16) and as columns (2 c, 2 c + 1, + 8)
+    const uint32_t stages = smem_u32(smem) + team * kPagesDeep * P::kBytes;
+    const uint32_t mat = piece_at<D>(tile + (lane & 15), lane >> 4);
+    const uint32_t rowat = (tile + g) * kG * 4, colat = (tile + 2 * c) * kG * 4;
+    const uint32_t sq = smem_u32(&t.q[0][0][lane]);
+    int st = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    pdl_wait();
+    for (int nr = 0;; ++nr) {
+      ok = __all_sync(0xffffffffu, poll_d(smem_u32(&t.row[nr % kRowsDeep]), nr / kRowsDeep & 1, abort_flag));
+      if (!ok) timeout(SITE_STAGE);
+      const auto &todo = t.todo[nr % (2 * kRowsDeep)];
+      const int n = ok ? todo.n : 1;
+      if (n == 0) break;
+      int left = todo.left;  // tokens of the sequence from the page on
+      uint2 qb;
+      float2 unit[2];
+      make_queries<D>(a, t, tw, kSync + team, todo.seq, todo.head, ok ? todo.heads : 0, qb, unit);
       // heads 2 c, 2 c + 1
       float o[kG][4][4] = {}, e[4] = {}, m[2] = {-INFINITY, -INFINITY}, ref[2] = {0.0f, 0.0f}, l[2] = {0.0f, 0.0f};
-      // the pages of these four warps: mine pages on, and every kTeams-th
-      int i = mine;
-      for (; ok && i < n; i += kTeams) {
-        const int now = st;
-        const uint32_t ph = phase;
-        if ((st += kTeams) >= kPagesDeep) {
-          st -= kPagesDeep;
-          phase ^= 1;
-        }
-        ok = __all_sync(0xffffffffu, poll_d(smem_u32(&ctl.full[now]), ph, abort_flag));
+      for (int i = 0; ok && i < n; ++i, left -= kPage) {
+        ok = __all_sync(0xffffffffu, poll_d(smem_u32(&t.full[st]), phase, abort_flag));
         if (!ok) {
-          if (lane == 0) {
-            *abort_flag = 1;
-            report_error(a.c.status, MOE_ERR_DEVICE_TIMEOUT, KID_ATTN_DECODE * 100 + SITE_MMA_FULL);
-          }
+          timeout(SITE_MMA_FULL);
           break;
         }
-        const int left = len - (p0 + i) * kPage;  // tokens of the sequence from this page on
-        if (ctl.ok[now] && tile < left) {
-          const uint32_t sk = smem_u32(smem) + now * P::kBytes, sv = sk + P::kCodes;
+        if (t.ok[st] && tile < left) {
+          const uint32_t sk = stages + st * P::kBytes, sv = sk + P::kCodes;
           const uint32_t fk = sv + P::kCodes, fv = fk + P::kAffine;
           // scores of 16 tokens (rows g, g + 8; heads 2 c, 2 c + 1): first the biases' part
           float s[4];
-          {
-            uint32_t bb[2];
+          uint32_t ka[2][kG], bb[2];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const uint2 w = lds64(fk + (tile + g + 8 * y) * kG * 4 + (D == 256 ? 8 * (c & 1) : 0));
-              bb[y] = __byte_perm(w.x, w.y, 0x7632);
-            }
-            mma0_bf16(s, bb[0], bb[1], bb[0], bb[1], qb.x, qb.y);
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t at4 = fk + rowat + 8 * y * kG * 4;
+            const uint2 w = lds64(at4 + (D == 256 ? 8 * (c & 1) : 0));
+            bb[y] = __byte_perm(w.x, w.y, 0x7632);
+            lds_words<kG>(at4, ka[y]);
           }
-          uint32_t ka[2][kG];
-#pragma unroll
-          for (int y = 0; y < 2; ++y) lds_words<kG>(fk + (tile + g + 8 * y) * kG * 4, ka[y]);
+          mma0_bf16(s, bb[0], bb[1], bb[0], bb[1], qb.x, qb.y);
 #pragma unroll
           for (int x = 0; x < kG; ++x) {
             const uint4 q0 = lds128(sq + x * 1024), q1 = lds128(sq + x * 1024 + 512);
-            float acc[4];
             uint32_t w[4], u[4];  // 8 columns of the keys 0 .. 7, 8 .. 15, then 32 columns on
+            float acc[4];
             ldsm4((sk + mat) ^ (32 * x), w);
 #pragma unroll
             for (int y = 0; y < 4; ++y) u[y] = w[y] >> 8;
@@ -539,202 +612,258 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 #pragma unroll
               for (int x = 0; x < kG; ++x)
 #pragma unroll
-                for (int t = 0; t < 4; ++t) o[x][t][y] *= f[y & 1];
+                for (int z = 0; z < 4; ++z) o[x][z][y] *= f[y & 1];
             }
           }
+          // P turned (head g, tokens 2 c, 2 c + 1 of both halves), in two bf16 parts
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             s[y] = fast_exp2(s[y] - ref[y & 1]);
             l[y & 1] += s[y];
           }
-          // P turned (head g, tokens 2 c, 2 c + 1 of both halves), in two bf16 parts
-          uint32_t h0 = bf16x2_bits(s[0], s[1]), h1 = bf16x2_bits(s[2], s[3]);
-          uint32_t l0 = bf16x2_bits(s[0] - __uint_as_float(h0 << 16), s[1] - __uint_as_float(h0 & 0xffff0000u));
-          uint32_t l1 = bf16x2_bits(s[2] - __uint_as_float(h1 << 16), s[3] - __uint_as_float(h1 & 0xffff0000u));
-          h0 = turned(h0);
-          h1 = turned(h1);
-          l0 = turned(l0);
-          l1 = turned(l1);
-          const float pt[4] = {__uint_as_float(h0 << 16) + __uint_as_float(l0 << 16),
-                               __uint_as_float(h0 & 0xffff0000u) + __uint_as_float(l0 & 0xffff0000u),
-                               __uint_as_float(h1 << 16) + __uint_as_float(l1 << 16),
-                               __uint_as_float(h1 & 0xffff0000u) + __uint_as_float(l1 & 0xffff0000u)};
+          float pt[4];
+          uint32_t hi[2], lo[2], ve[4], va[4][kG];
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const float a0 = s[2 * z], a1 = s[2 * z + 1];
+            hi[z] = bf16x2_bits(a0, a1);
+            lo[z] = bf16x2_bits(a0 - __uint_as_float(hi[z] << 16), a1 - __uint_as_float(hi[z] & 0xffff0000u));
+            hi[z] = turned(hi[z]);
+            lo[z] = turned(lo[z]);
+            pt[2 * z] = __uint_as_float(hi[z] << 16) + __uint_as_float(lo[z] << 16);
+            pt[2 * z + 1] = __uint_as_float(hi[z] & 0xffff0000u) + __uint_as_float(lo[z] & 0xffff0000u);
+          }
           // scales of the values; of what is behind the end nothing may be seen (0 x NaN
           // is NaN)
-          uint32_t va[4][kG], ve[4];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const uint32_t at4 = fv + (key + 8 * (y >> 1) + (y & 1)) * kG * 4;
-            ve[y] = lds32(at4 + (g & (kG - 1)) * 4);
-            lds_words<kG>(at4, va[y]);
+          for (int z = 0; z < 4; ++z) {
+            const uint32_t at4 = fv + colat + (8 * (z >> 1) + (z & 1)) * kG * 4;
+            ve[z] = lds32(at4 + (g & (kG - 1)) * 4);
+            lds_words<kG>(at4, va[z]);
           }
           if (end) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-              if (key + 8 * (y >> 1) + (y & 1) >= left) {
-                ve[y] = 0u;
+            for (int z = 0; z < 4; ++z)
+              if (tile + 2 * c + 8 * (z >> 1) + (z & 1) >= left) {
+                ve[z] = 0u;
 #pragma unroll
-                for (int x = 0; x < kG; ++x) va[y][x] = 0u;
+                for (int x = 0; x < kG; ++x) va[z][x] = 0u;
               }
           }
           {  // sums of p b' (rows g, group g % kG) and p s' (rows g + 8)
             const uint32_t a0 = __byte_perm(ve[0], ve[1], 0x7632), a1 = __byte_perm(ve[0], ve[1], 0x5410);
             const uint32_t a2 = __byte_perm(ve[2], ve[3], 0x7632), a3 = __byte_perm(ve[2], ve[3], 0x5410);
-            mma_bf16(e, a0, a1, a2, a3, h0, h1);
-            mma_bf16(e, a0, a1, a2, a3, l0, l1);
+            mma_bf16(e, a0, a1, a2, a3, hi[0], hi[1]);
+            mma_bf16(e, a0, a1, a2, a3, lo[0], lo[1]);
           }
           // the values: transposed, so that a word has four columns of two tokens
 #pragma unroll
           for (int x = 0; x < kG; ++x) {
             float p[4];
 #pragma unroll
-            for (int y = 0; y < 4; ++y) p[y] = pt[y] * __uint_as_float(va[y][x] << 16);
+            for (int z = 0; z < 4; ++z) p[z] = pt[z] * __uint_as_float(va[z][x] << 16);
             const uint32_t b0 = bf16x2_bits(p[0], p[1]), b1 = bf16x2_bits(p[2], p[3]);
             uint32_t w[4];  // tokens 0 .. 7, 8 .. 15 of 32 columns, then 32 columns on
             ldsm4_t((sv + mat) ^ (32 * x), w);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              const uint32_t lo = w[t & 2] >> (8 * (t & 1)), hi = w[(t & 2) + 1] >> (8 * (t & 1));
-              mma_bf16(o[x][t], plus128(lo), plus128(lo >> 4), plus128(hi), plus128(hi >> 4), b0, b1);
-              mma_bf16(o[x][t], kMinus136, kMinus136, kMinus136, kMinus136, b0, b1);
+            for (int z = 0; z < 4; ++z) {
+              const uint32_t v0 = w[z & 2] >> (8 * (z & 1)), v1 = w[(z & 2) + 1] >> (8 * (z & 1));
+              mma_bf16(o[x][z], plus128(v0), plus128(v0 >> 4), plus128(v1), plus128(v1 >> 4), b0, b1);
             }
+#pragma unroll
+            for (int z = 0; z < 4; ++z) mma_bf16(o[x][z], kMinus136, kMinus136, kMinus136, kMinus136, b0, b1);
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl.empty[now]));
+        if (lane == 0) mbar_arrive(smem_u32(&t.empty[st]));
+        if (++st == kPagesDeep) {
+          st = 0;
+          phase ^= 1;
+        }
       }
-      mine = i - n;
-      // join the warps' parts (also after an abort: all warps meet here)
+      // join the warps' parts (also after an abort: all warps meet here): the biases'
+      // sums of group x are with the lanes g = x
+      e[0] = fmaf(8.0f, e[2], e[0]);
+      e[1] = fmaf(8.0f, e[3], e[1]);
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
+      for (int x = 0; x < kG; ++x) {
+        const float e0 = __shfl_sync(0xffffffffu, e[0], 4 * x + c), e1 = __shfl_sync(0xffffffffu, e[1], 4 * x + c);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          o[x][z][0] += e0;
+          o[x][z][1] += e1;
+          o[x][z][2] += e0;
+          o[x][z][3] += e1;
+        }
+      }
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
 #pragma unroll
         for (int x = 4; x < 32; x *= 2) l[z] += __shfl_xor_sync(0xffffffffu, l[z], x);
-        if (g == 0) {
-          ctl.m[warp][2 * c + z] = m[z];
-          ctl.l[warp][2 * c + z] = l[z];
-        }
-      }
-      if (g < kG) {
-        *reinterpret_cast<float2 *>(&ctl.e[warp][g][2 * c]) = make_float2(e[0], e[1]);
-        *reinterpret_cast<float2 *>(&ctl.e[warp][4 + g][2 * c]) = make_float2(e[2], e[3]);
-      }
+      // warps 2, 3 to 0, 1, then 1 to 0: four registers of a lane side by side
+      float4 *slot = reinterpret_cast<float4 *>(slots + (team * 2 + (tw & 1)) * P::kOut) + lane;
+      auto put = [&] {
 #pragma unroll
-      for (int x = 0; x < kG; ++x)
+        for (int x = 0; x < kG; ++x)
+#pragma unroll
+          for (int z = 0; z < 4; ++z) slot[(x * 4 + z) * 32] = make_float4(o[x][z][0], o[x][z][1], o[x][z][2], o[x][z][3]);
+        if (g == 0) {
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            t.m[tw][2 * c + z] = m[z];
+            t.l[tw][2 * c + z] = l[z];
+          }
+        }
+      };
+      auto take = [&](int from, const float4 *src) {
+        float f[2], to[2];
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          float *to = obuf + (warp * kHeads + 2 * c + z) * P::kPitch + 64 * x + 4 * g;
-          *reinterpret_cast<float4 *>(to) = make_float4(o[x][0][z], o[x][0][2 + z], o[x][1][z], o[x][1][2 + z]);
-          *reinterpret_cast<float4 *>(to + 32) = make_float4(o[x][2][z], o[x][2][2 + z], o[x][3][z], o[x][3][2 + z]);
+          const float other = t.m[from][2 * c + z], M = fmaxf(m[z], other);
+          f[z] = m[z] == M ? 1.0f : fast_exp2(m[z] - M);
+          to[z] = other == M ? 1.0f : fast_exp2(other - M);
+          m[z] = M;
+          l[z] = l[z] * f[z] + to[z] * t.l[from][2 * c + z];
         }
-      named_bar_sync(1, 32 * kConsumers);
-      if (warp < heads) {
-        constexpr int kE = D / 32;  // columns per thread; the head is the warp's
-        const int d0 = kE * lane;
-        float M = -INFINITY, L = 0.0f, v[kE];
 #pragma unroll
-        for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, ctl.m[w][warp]);
+        for (int x = 0; x < kG; ++x)
 #pragma unroll
-        for (int i = 0; i < kE; ++i) v[i] = 0.0f;
+          for (int z = 0; z < 4; ++z) {
+            const float4 v = src[(x * 4 + z) * 32];
+            o[x][z][0] = fmaf(to[0], v.x, f[0] * o[x][z][0]);
+            o[x][z][1] = fmaf(to[1], v.y, f[1] * o[x][z][1]);
+            o[x][z][2] = fmaf(to[0], v.z, f[0] * o[x][z][2]);
+            o[x][z][3] = fmaf(to[1], v.w, f[1] * o[x][z][3]);
+          }
+      };
+      if (tw >= 2) put();
+      named_bar_sync(kSync + team, 32 * kTeamWarps);
+      if (tw < 2) take(tw + 2, slot);
+      if (tw == 1) put();  // (over what it has read itself)
+      named_bar_sync(kSync + team, 32 * kTeamWarps);
+      if (tw == 0 && ok) {
+        take(1, slot + P::kOut / 16);
+        // o[x][z]: columns 64 x + 32 (z / 2) + 4 g + 2 (z % 2) + 0 (registers 0, 1), + 1 (2, 3)
 #pragma unroll
-        for (int w = 0; w < kConsumers; ++w) {
-          const float mw = ctl.m[w][warp], f = mw == M ? 1.0f : fast_exp2(mw - M);
-          const float ew = fmaf(8.0f, ctl.e[w][4 + d0 / kGroup][warp], ctl.e[w][d0 / kGroup][warp]);
-          L = fmaf(f, ctl.l[w][warp], L);
-          const float *from = obuf + (w * kHeads + warp) * P::kPitch + d0;
+        for (int y = 0; y < 2; ++y) {
+          if (2 * c + y >= todo.heads) continue;
+          if (todo.slot < 0) {
+            const float inv = l[y] == 0.0f ? 0.0f : 1.0f / l[y];
+            __nv_bfloat16 *to = a.out + static_cast<long long>(todo.out + 2 * c + y) * D + 4 * g;
 #pragma unroll
-          for (int i = 0; i < kE; ++i) v[i] = fmaf(f, from[i] + ew, v[i]);
-        }
-        if (n == np) {
-          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-          __nv_bfloat16 *to = a.out + (orow + warp) * D + d0;
+            for (int x = 0; x < kG; ++x)
 #pragma unroll
-          for (int i = 0; i < kE; i += 2)
-            *reinterpret_cast<uint32_t *>(to + i) = bf16x2_bits(v[i] * inv, v[i + 1] * inv);
-        } else {
-          const int slot = 2 * cta + (u == u0 ? 0 : 1);
-          float *to = a.part + (static_cast<long long>(slot) * kHeads + warp) * (D + 2);
+              for (int z = 0; z < 4; z += 2)
+                *reinterpret_cast<uint2 *>(to + 64 * x + 16 * z) =
+                    make_uint2(bf16x2_bits(o[x][z][y] * inv, o[x][z][2 + y] * inv),
+                               bf16x2_bits(o[x][z + 1][y] * inv, o[x][z + 1][2 + y] * inv));
+          } else {
+            float *to = a.part + (static_cast<long long>(todo.slot) * kHeads + 2 * c + y) * (D + 4) + 4 * g;
 #pragma unroll
-          for (int i = 0; i < kE; i += 2) *reinterpret_cast<float2 *>(to + d0 + i) = make_float2(v[i], v[i + 1]);
-          if (lane == 0) *reinterpret_cast<float2 *>(to + D) = make_float2(M, L);
-          if (p0 == 0 && tid == 0) {  // the row starts here: this share's entry says how it goes on
-            const int last = u + np - 1;
-            int end = static_cast<int>(min(((last + 1LL) * kShares - 1) / total, kShares - 1LL));
-            while (share_at(total, end + 1) <= last) ++end;
-            while (share_at(total, end) > last) --end;
-            a.head[cta] = make_int4(end - cta + 1, slot, static_cast<int>(orow), heads);
+            for (int x = 0; x < kG; ++x)
+#pragma unroll
+              for (int z = 0; z < 4; z += 2)
+                *reinterpret_cast<float4 *>(to + 64 * x + 16 * z) =
+                    make_float4(o[x][z][y], o[x][z][2 + y], o[x][z + 1][y], o[x][z + 1][2 + y]);
+            if (g == 0) *reinterpret_cast<float2 *>(to + D) = make_float2(m[y], l[y]);
           }
         }
       }
-      if (consumers_any(!ok)) break;
-      u += n;
-      at += n;
+      if (team_any(kEnd + team, !ok)) break;
     }
   }
 }
 
-// Joins the parts of the row that starts in share blockIdx.x and does not end
-// there, for one of its heads: groups of D / 4 threads add up every so many parts,
-// then their sums are added.
+// Joins the parts of the rows that are cut.  Each block lists them (the shares whose
+// entry says that the row that starts there goes on) and takes every so many'th
+// piece of 64 to 1,024 columns of their 8 heads, more of them the fewer rows there are;
+// its threads take 4 columns of every so many'th part, with a running maximum and
+// sum, and add up through shared memory.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const DecodeAttnArgs a) {
-  constexpr int kT = D / 4, kGroups = kJoinThreads / kT;
-  __shared__ float s_f[kShares], s_red[kJoinThreads / 32], s_l[kJoinThreads / 32];
-  __shared__ float4 s_o[kGroups][kT];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hd = blockIdx.y;
+  __shared__ int s_row[kShares], s_warp[kJoinThreads / 32];
+  __shared__ float4 s_o[kJoinThreads];
+  __shared__ float2 s_ml[kJoinThreads];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_launch_dependents();
-  const int4 head = a.head[blockIdx.x];
-  const int n = head.x;
-  if (n <= 1 || hd >= head.w) return;
-  auto part = [&](int i) {
-    const int slot = i == 0 ? head.y : 2 * (static_cast<int>(blockIdx.x) + i);
-    return a.part + (static_cast<long long>(slot) * kHeads + hd) * (D + 2);
-  };
-  float2 ml = make_float2(-INFINITY, 0.0f);
-  if (tid < n) ml = *reinterpret_cast<const float2 *>(part(tid) + D);
-  float M = ml.x;
+  int rows = 0;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) s_red[warp] = M;
-  __syncthreads();
+  for (int i0 = 0; i0 < kShares; i0 += kJoinThreads) {
+    const int i = i0 + tid;
+    const bool cut = i < kShares && a.head[i].x > 1;
+    const uint32_t mask = __ballot_sync(0xffffffffu, cut);
+    if (lane == 0) s_warp[warp] = __popc(mask);
+    __syncthreads();
+    int at = rows + __popc(mask & ((1u << lane) - 1));
 #pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) M = fmaxf(M, s_red[w]);
-  const float f = ml.x == M ? 1.0f : fast_exp2(ml.x - M);
-  if (tid < n) s_f[tid] = f;
-  float L = f * ml.y;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  if (lane == 0) s_l[warp] = L;
-  __syncthreads();
-  const int t = tid % kT, grp = tid / kT;
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int i = grp; i < n; i += kGroups) {
-    const float2 *p = reinterpret_cast<const float2 *>(part(i) + 4 * t);
-    const float2 x = p[0], y = p[1];
-    const float w = s_f[i];
-    v.x = fmaf(w, x.x, v.x);
-    v.y = fmaf(w, x.y, v.y);
-    v.z = fmaf(w, y.x, v.z);
-    v.w = fmaf(w, y.y, v.w);
-  }
-  s_o[grp][t] = v;
-  __syncthreads();
-  if (grp == 0) {
-    L = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) L += s_l[w];
-#pragma unroll
-    for (int x = 1; x < kGroups; ++x) {
-      const float4 y = s_o[x][t];
-      v.x += y.x;
-      v.y += y.y;
-      v.z += y.z;
-      v.w += y.w;
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+      if (w < warp) at += s_warp[w];
+      rows += s_warp[w];
     }
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-    uint32_t *to = reinterpret_cast<uint32_t *>(a.out + (static_cast<long long>(head.z) + hd) * D + 4 * t);
-    to[0] = bf16x2_bits(v.x * inv, v.y * inv);
-    to[1] = bf16x2_bits(v.z * inv, v.w * inv);
+    if (cut) s_row[at] = i;
+    __syncthreads();
+  }
+  // columns of a piece: a power of two that gives every block a piece if it can
+  constexpr int kLeast = 64, kMost = 4 * kJoinThreads;
+  int wide = kLeast;
+  while (wide < kMost && rows * (kHeads * D / wide) > static_cast<int>(gridDim.x)) wide *= 2;
+  const int pieces = kHeads * D / wide, lanes = wide / 4, groups = kJoinThreads / lanes;
+  const int grp = tid / lanes;
+  for (int piece = blockIdx.x; piece < rows * pieces; piece += static_cast<int>(gridDim.x)) {
+    const int share = s_row[piece / pieces], col = piece % pieces * wide + 4 * (tid % lanes);
+    const int hd = col / D, d = col % D;
+    const int4 head = a.head[share];
+    float M = -INFINITY, L = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (hd < head.w)
+      for (int i0 = grp; i0 < head.x; i0 += 4 * groups) {
+        float4 x[4];
+        float2 ml[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = i0 + j * groups;
+          ml[j] = make_float2(-INFINITY, 0.0f);
+          x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (i < head.x) {
+            const float *p = a.part + (static_cast<long long>(i == 0 ? head.y : 2 * (share + i)) * kHeads + hd) * (D + 4);
+            ml[j] = *reinterpret_cast<const float2 *>(p + D);
+            x[j] = *reinterpret_cast<const float4 *>(p + d);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float to = fmaxf(M, ml[j].x);
+          const float f = M == to ? 1.0f : fast_exp2(M - to), w = ml[j].x == to ? 1.0f : fast_exp2(ml[j].x - to);
+          M = to;
+          L = L * f + w * ml[j].y;
+          v.x = v.x * f + w * x[j].x;
+          v.y = v.y * f + w * x[j].y;
+          v.z = v.z * f + w * x[j].z;
+          v.w = v.w * f + w * x[j].w;
+        }
+      }
+    s_o[tid] = v;
+    s_ml[tid] = make_float2(M, L);
+    __syncthreads();
+    if (grp == 0 && hd < head.w) {
+      for (int w = 1; w < groups; ++w) {
+        const float2 ml = s_ml[w * lanes + tid];
+        const float4 y = s_o[w * lanes + tid];
+        const float to = fmaxf(M, ml.x);
+        const float f = M == to ? 1.0f : fast_exp2(M - to), u = ml.x == to ? 1.0f : fast_exp2(ml.x - to);
+        M = to;
+        L = L * f + u * ml.y;
+        v.x = v.x * f + u * y.x;
+        v.y = v.y * f + u * y.y;
+        v.z = v.z * f + u * y.z;
+        v.w = v.w * f + u * y.w;
+      }
+      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+      *reinterpret_cast<uint2 *>(a.out + (static_cast<long long>(head.z) + hd) * D + d) =
+          make_uint2(bf16x2_bits(v.x * inv, v.y * inv), bf16x2_bits(v.z * inv, v.w * inv));
+    }
+    __syncthreads();
   }
 }
 
@@ -765,9 +894,9 @@ const DecodeDevice &decode_device() {
 
 template <int D>
 cudaError_t launch_decode_attn(const CUtensorMap &tm, const DecodeAttnArgs &a, cudaStream_t st) {
-  const cudaError_t e = launch_attn(attn_decode_kernel<D>, dim3(kShares), kThreadsD, Page<D>::kTotal, st, tm, a);
+  const cudaError_t e = launch_attn(attn_decode_kernel<D>, dim3(kCtas), kThreadsD, Page<D>::kTotal, st, tm, a);
   if (e != cudaSuccess) return e;
-  return launch_attn(attn_join_kernel<D>, dim3(kShares, a.group < kHeads ? a.group : kHeads), kJoinThreads, 0, st, a);
+  return launch_attn(attn_join_kernel<D>, dim3(3 * kCtas), kJoinThreads, 0, st, a);
 }
 
 }  // namespace
@@ -781,7 +910,7 @@ extern "C" int moe_attention_decode_workspace(int n_seq, int table_width, int n_
   if (!bytes || n_seq < 0 || table_width < 0 || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads != 0)
     return MOE_ERR_INVALID_ARG;
   if ((head_dim != 128 && head_dim != 256) || n_q_heads > 4096 || table_width > (1 << 25)) return MOE_ERR_UNSUPPORTED;
-  *bytes = n_seq == 0 ? 0 : kShares * sizeof(int4) + 2 * kShares * sizeof(float) * kHeads * (head_dim + 2);
+  *bytes = n_seq == 0 ? 0 : kShares * sizeof(int4) + 2 * kShares * sizeof(float) * kHeads * (head_dim + 4);
   return MOE_OK;
 }
 
