@@ -53,7 +53,7 @@ constexpr int kRegsConsumer = 152, kRegsProducer = 48;
 constexpr int kHeads = 8;      // query heads of a row
 constexpr int kPagesDeep = 3;  // of a team
 constexpr int kRowsDeep = 4;   // more than kPagesDeep: that many rows can the copies be ahead
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 512;
 constexpr float kLateDecode = 8.0f;  // as in attn_prefill.cu
 constexpr int kCtas = 152, kShares = kCtas * kTeams;  // one CTA per SM
 
@@ -504,7 +504,8 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         }
         if (lane == 0 && r.p0 == 0 && r.n < r.np) {  // the row starts here: this share's entry says how it goes on
           const int share = role * kCtas + cta, last = r.u + r.np - 1;
-          int end = static_cast<int>(min(((last + 1LL) * kShares - 1) / total, kShares - 1LL));
+          // (an estimate, within one or two; a division of 64 bits took 2 us here)
+          int end = total < kShares ? last : min(static_cast<int>(__fdividef(static_cast<float>(last), static_cast<float>(total)) * kShares), kShares - 1);
           while (share_at(total, end + 1) <= last) ++end;
           while (share_at(total, end) > last) --end;
           a.head[share] = make_int4(end - share + 1, 2 * share + (r.u == t.u0 ? 0 : 1),
@@ -776,36 +777,44 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 
 // Joins the parts of the rows that are cut.  Each block lists them (the shares whose
 // entry says that the row that starts there goes on) and takes every so many'th
-// piece of 64 to 1,024 columns of their 8 heads, more of them the fewer rows there are;
+// piece of 64 or more columns of their 8 heads, more of them the fewer rows there are;
 // its threads take 4 columns of every so many'th part, with a running maximum and
 // sum, and add up through shared memory.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const DecodeAttnArgs a) {
+  __shared__ int4 s_head[kShares];
   __shared__ int s_row[kShares], s_warp[kJoinThreads / 32];
   __shared__ float4 s_o[kJoinThreads];
   __shared__ float2 s_ml[kJoinThreads];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_launch_dependents();
+  static_assert(kShares <= kJoinThreads, "a thread per entry");
   int rows = 0;
-#pragma unroll
-  for (int i0 = 0; i0 < kShares; i0 += kJoinThreads) {
-    const int i = i0 + tid;
-    const bool cut = i < kShares && a.head[i].x > 1;
+  {
+    const int4 head = tid < kShares ? a.head[tid] : make_int4(0, 0, 0, 0);
+    const bool cut = head.x > 1;
     const uint32_t mask = __ballot_sync(0xffffffffu, cut);
     if (lane == 0) s_warp[warp] = __popc(mask);
     __syncthreads();
-    int at = rows + __popc(mask & ((1u << lane) - 1));
+    // lane w: the entries of warp w, those up to it, all
+    int upto = lane < kJoinThreads / 32 ? s_warp[lane] : 0;
 #pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) {
-      if (w < warp) at += s_warp[w];
-      rows += s_warp[w];
+    for (int o = 1; o < kJoinThreads / 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += u;
     }
-    if (cut) s_row[at] = i;
+    rows = __shfl_sync(0xffffffffu, upto, kJoinThreads / 32 - 1);
+    const int before = __shfl_sync(0xffffffffu, upto, max(warp - 1, 0));
+    if (cut) {
+      const int at = (warp ? before : 0) + __popc(mask & ((1u << lane) - 1));
+      s_row[at] = tid;
+      s_head[at] = head;
+    }
     __syncthreads();
   }
   // columns of a piece: a power of two that gives every block a piece if it can
-  constexpr int kLeast = 64, kMost = 4 * kJoinThreads;
+  constexpr int kLeast = 64, kMost = kHeads * D, kU = 8;
   int wide = kLeast;
   while (wide < kMost && rows * (kHeads * D / wide) > static_cast<int>(gridDim.x)) wide *= 2;
   const int pieces = kHeads * D / wide, lanes = wide / 4, groups = kJoinThreads / lanes;
@@ -813,15 +822,15 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const DecodeAtt
   for (int piece = blockIdx.x; piece < rows * pieces; piece += static_cast<int>(gridDim.x)) {
     const int share = s_row[piece / pieces], col = piece % pieces * wide + 4 * (tid % lanes);
     const int hd = col / D, d = col % D;
-    const int4 head = a.head[share];
+    const int4 head = s_head[piece / pieces];
     float M = -INFINITY, L = 0.0f;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (hd < head.w)
-      for (int i0 = grp; i0 < head.x; i0 += 4 * groups) {
-        float4 x[4];
-        float2 ml[4];
+      for (int i0 = grp; i0 < head.x; i0 += kU * groups) {
+        float4 x[kU];
+        float2 ml[kU];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kU; ++j) {
           const int i = i0 + j * groups;
           ml[j] = make_float2(-INFINITY, 0.0f);
           x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -832,7 +841,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const DecodeAtt
           }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kU; ++j) {
+          if (i0 + j * groups >= head.x) break;
           const float to = fmaxf(M, ml[j].x);
           const float f = M == to ? 1.0f : fast_exp2(M - to), w = ml[j].x == to ? 1.0f : fast_exp2(ml[j].x - to);
           M = to;
@@ -846,19 +856,31 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const DecodeAtt
     s_o[tid] = v;
     s_ml[tid] = make_float2(M, L);
     __syncthreads();
-    if (grp == 0 && hd < head.w) {
-      for (int w = 1; w < groups; ++w) {
-        const float2 ml = s_ml[w * lanes + tid];
-        const float4 y = s_o[w * lanes + tid];
-        const float to = fmaxf(M, ml.x);
-        const float f = M == to ? 1.0f : fast_exp2(M - to), u = ml.x == to ? 1.0f : fast_exp2(ml.x - to);
-        M = to;
-        L = L * f + u * ml.y;
-        v.x = v.x * f + u * y.x;
-        v.y = v.y * f + u * y.y;
-        v.z = v.z * f + u * y.z;
-        v.w = v.w * f + u * y.w;
+    // four groups' sums into one until one is left
+    for (int left = groups; left > 1; left = (left + 3) / 4) {
+      const int next = (left + 3) / 4;
+      if (grp < next) {
+        for (int w = grp + next; w < left; w += next) {
+          const int at = w * lanes + tid % lanes;
+          const float2 ml = s_ml[at];
+          const float4 y = s_o[at];
+          const float to = fmaxf(M, ml.x);
+          const float f = M == to ? 1.0f : fast_exp2(M - to), u = ml.x == to ? 1.0f : fast_exp2(ml.x - to);
+          M = to;
+          L = L * f + u * ml.y;
+          v.x = v.x * f + u * y.x;
+          v.y = v.y * f + u * y.y;
+          v.z = v.z * f + u * y.z;
+          v.w = v.w * f + u * y.w;
+        }
+        if (next > 1) {
+          s_o[tid] = v;
+          s_ml[tid] = make_float2(M, L);
+        }
       }
+      __syncthreads();
+    }
+    if (grp == 0 && hd < head.w) {
       const float inv = L == 0.0f ? 0.0f : 1.0f / L;
       *reinterpret_cast<uint2 *>(a.out + (static_cast<long long>(head.z) + hd) * D + d) =
           make_uint2(bf16x2_bits(v.x * inv, v.y * inv), bf16x2_bits(v.z * inv, v.w * inv));
