@@ -19,15 +19,27 @@
 // sums lose nothing, and O is rarely scaled again.  P is rounded to bf16 (2^-8 of
 // each weight, as large as the result's own rounding; an output's rms error grows
 // by sqrt 2); the sum of the softmax is taken before that, in fp32.
+//   * D = 256: O takes half of TMEM.  All eight softmax warps make each tile's P,
+//     16 rows each (a row lies in a quad, its maximum takes two shuffles); the
+//     products of a tile, 2,048 cycles, hide that.
+//   * D = 128: a tile's products take 1,024 cycles, less than the softmax of one
+//     tile from end to end.  Even and odd tiles are therefore two streams, each with
+//     an O, a maximum and a sum of its own, four warps with a row per thread for
+//     either; they are joined at a row's end.
+//
+// Schedule.  As many clusters as fit stay; one warp per CTA looks up the next tile of
+// rows while the others work.  Tiles are numbered by falling number of key tiles over
+// all sequences, and cluster c of P takes the numbers c, 2P - 1 - c, 2P + c, ..: the
+// largest go first and the sums stay even.  The next tile's copies and scores run
+// during the outputs of the one before.
 //
 // A key or value row that some of the tile's queries must not see is masked in
 // the scores; but 0 x NaN is NaN, so in the tiles at the causal edge (and at a
 // sequence's end) values that are not finite are taken out of V in shared memory,
 // and the queries that do see them are set to NaN in the end.
 //
-// Roles (320 threads): warp 0 TMA copies; warp 1 the MMAs (CTA 0), or telling CTA 0
-// that P is there (CTA 1); warps 2-9 the softmax, a warp per 16 rows, so that a row
-// lies in one quad and its maximum takes two shuffles.
+// Roles (352 threads): warp 0 TMA copies; warp 1 the MMAs (CTA 0), or telling CTA 0
+// that P is there (CTA 1); warps 2-9 the softmax and the outputs; warp 10 the schedule.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -40,21 +52,12 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreadsA = 320;
+constexpr int kThreadsA = 352;
 constexpr int kKeys = 128;  // keys per tile
-constexpr int kCtlBytes = 3072;
+constexpr int kItems = 2;   // tiles of rows looked up ahead
+constexpr int kReaders = 10;  // warps that read an item
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLate = 8.0f;  // log2 of how far a row's maximum may grow before m follows
-
-template <int D>
-struct Plan {
-  static constexpr int kSlot = 64 * D * 2;  // a CTA's half of a tile of keys or of values
-  static constexpr int kSlots = D == 256 ? 5 : 10;
-  static constexpr int kQ = 128 * D * 2;
-  static constexpr int kTotal = kCtlBytes + kQ + kSlots * kSlot;
-  static constexpr uint32_t O = 0, S = D;  // TMEM columns: O, then two of S
-  static_assert(kTotal <= 227 * 1024, "shared memory");
-};
 
 struct PrefillArgs {
   __nv_bfloat16 *out;
@@ -72,16 +75,33 @@ struct Item {
   int valid;
 };
 
+template <int D>
 struct Ctl {
   uint64_t full[10], empty[10], vloc[10];
-  uint64_t q_full, s_full[2], p_full[2], p_loc[2], pv_done, drain;
+  uint64_t q_full, q_empty, s_full[2], p_full[2], p_loc[2], pv_done, o_full, drain;
+  uint64_t it_full[kItems], it_empty[kItems];
   uint32_t tmem, sink;
   int abort_flag;
-  Item item;
-  float sum[128];
-  uint32_t bad[128];  // two columns per word: first key (from the first masked tile on) that is not finite
+  Item item[kItems];
+  // of three tiles of rows in turn, two columns per word: first key (from the first
+  // masked tile on) whose value is not finite
+  uint32_t bad[3][128];
+  float sum[128];                            // D = 256: sums of the rows
+  float2 stream[2][D == 128 ? 128 : 1];      // D = 128: maximum and sum of each stream's rows
 };
-static_assert(sizeof(Ctl) <= kCtlBytes, "control block");
+
+template <int D>
+struct Plan {
+  static constexpr int kCtlBytes = D == 256 ? 3072 : 5120;
+  static constexpr int kSlot = 64 * D * 2;  // a CTA's half of a tile of keys or of values
+  static constexpr int kSlots = D == 256 ? 5 : 10;
+  static constexpr int kQ = 128 * D * 2;
+  static constexpr int kTotal = kCtlBytes + kQ + kSlots * kSlot;
+  static constexpr int kStreams = D == 128 ? 2 : 1;
+  static constexpr uint32_t O = 0, S = kStreams * D;  // TMEM columns: O of each stream, then two of S
+  static constexpr int kMakers = kStreams == 2 ? 4 : 8;  // warps of a tile's P
+  static_assert(kTotal <= 227 * 1024 && sizeof(Ctl<D>) <= kCtlBytes && S + 2 * kKeys <= kTmemCols, "room");
+};
 
 // operand whose N index is contiguous (see the same layout in decay_chunk.cu)
 __device__ __forceinline__ uint64_t sdesc_cols(uint32_t saddr, uint32_t lbo) {
@@ -151,6 +171,16 @@ __device__ __forceinline__ void st_pairs_16x32(uint32_t ta, const uint32_t (&r)[
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(ta)
       : "memory");
 }
+// 32 lanes x 32 columns, a lane per thread
+__device__ __forceinline__ void st_32x32(uint32_t ta, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::
+          "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+      "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(ta)
+      : "memory");
+}
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -182,71 +212,123 @@ __device__ __forceinline__ bool warp_wait(const PrefillArgs &a, uint32_t bar, ui
   return false;
 }
 
-// The n-th tile of the call (one warp): sequences in order, in a sequence the
-// last tile, which sees the most keys, first.
-__device__ __forceinline__ Item find_item(const PrefillArgs &a, long long n) {
-  const int lane = threadIdx.x & 31, per = 2 * a.tokens;
-  Item it = {};
-  it.head = static_cast<int>(n % a.Hk);
-  long long left = n / a.Hk;
-  for (int i0 = 0; i0 < a.n_seq; i0 += 32) {
-    const int i = i0 + lane;
-    int lo = 0, hi = 0;
-    if (i < a.n_seq) seq_rows(a.offsets, a.n_seq, a.n_q, i, lo, hi);
-    const int tiles = (hi - lo + per - 1) / per;
-    long long upto = tiles;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += u;
-    }
-    const uint32_t hit = __ballot_sync(0xffffffffu, upto > left);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      const long long back = upto - 1 - left;  // tiles behind it in the sequence
-      it.valid = 1;
-      it.q0 = __shfl_sync(0xffffffffu, lo, src);
-      it.lq = __shfl_sync(0xffffffffu, hi, src) - it.q0;
-      it.t0 = __shfl_sync(0xffffffffu, static_cast<int>(back), src) * per;
-      seq_rows(a.k_offsets, a.n_seq, a.n_k, i0 + src, it.k0, it.lk);
-      it.lk -= it.k0;
-      return it;
-    }
-    left -= __shfl_sync(0xffffffffu, upto, 31);
+// The schedule (one warp): tiles of rows by falling number of key tiles.
+struct Schedule {
+  const PrefillArgs &a;
+  int per;           // queries of a tile
+  int lq, shift;     // (n_seq <= 32) this lane's sequence: queries, keys less queries
+
+  __device__ __forceinline__ Schedule(const PrefillArgs &args) : a(args), per(2 * args.tokens) {
+    lq = shift = 0;
+    if (a.n_seq <= 32 && (threadIdx.x & 31) < a.n_seq) lengths(threadIdx.x & 31, lq, shift);
   }
-  return it;
-}
+  __device__ __forceinline__ void lengths(int i, int &queries, int &ahead) const {
+    int q0, q1, k0, k1;
+    seq_rows(a.offsets, a.n_seq, a.n_q, i, q0, q1);
+    seq_rows(a.k_offsets, a.n_seq, a.n_k, i, k0, k1);
+    queries = q1 - q0;
+    ahead = (k1 - k0) - queries;
+  }
+  // tiles of a sequence with at least c key tiles: the last query of tile b, at
+  // min((b + 1) per, queries) - 1, sees more than 128 (c - 1) keys
+  __device__ __forceinline__ int least(int queries, int ahead, int c) const {
+    const int tiles = (queries + per - 1) / per;
+    const long long from = 128LL * (c - 1) - ahead;
+    if (c <= 0 || from < 0) return tiles;
+    return from >= queries ? 0 : tiles - static_cast<int>(from) / per;
+  }
+  // that of the sequence i0 + lane
+  __device__ __forceinline__ int mine(int i0, int c) const {
+    const int i = i0 + static_cast<int>(threadIdx.x & 31);
+    if (a.n_seq <= 32) return least(lq, shift, c);
+    if (i >= a.n_seq) return 0;
+    int queries, ahead;
+    lengths(i, queries, ahead);
+    return least(queries, ahead, c);
+  }
+  __device__ __forceinline__ long long all(int c) const {
+    long long sum = 0;
+    for (int i0 = 0; i0 < a.n_seq; i0 += 32) sum += __reduce_add_sync(0xffffffffu, mine(i0, c));
+    return sum;
+  }
+  // the n-th tile; n < all(0) heads
+  __device__ __forceinline__ Item find(long long n) const {
+    const int lane = threadIdx.x & 31;
+    Item it = {};
+    it.valid = 1;
+    it.head = static_cast<int>(n % a.Hk);
+    long long left = n / a.Hk;
+    int lo = 0, hi = static_cast<int>((a.n_k + kKeys - 1) / kKeys) + 1;  // all(lo) > left >= all(hi)
+    long long behind = 0;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      const long long m = all(mid);
+      if (m > left) {
+        lo = mid;
+      } else {
+        hi = mid;
+        behind = m;
+      }
+    }
+    left -= behind;
+    for (int i0 = 0; i0 < a.n_seq; i0 += 32) {
+      const int from = mine(i0, lo), count = from - mine(i0, hi);
+      int upto = count;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += u;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, upto > left);
+      if (hit) {
+        const int src = __ffs(hit) - 1, i = i0 + src;
+        const int nth = static_cast<int>(left) - __shfl_sync(0xffffffffu, upto - count, src);
+        const int first = __shfl_sync(0xffffffffu, from, src);  // tiles from its level on
+        int k1;
+        seq_rows(a.offsets, a.n_seq, a.n_q, i, it.q0, it.lq);
+        seq_rows(a.k_offsets, a.n_seq, a.n_k, i, it.k0, k1);
+        it.lq -= it.q0;
+        it.lk = k1 - it.k0;
+        it.t0 = ((it.lq + per - 1) / per - first + nth) * per;
+        return it;
+      }
+      left -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+    it.valid = 0;  // (not reached)
+    return it;
+  }
+};
 
 // Values of a masked tile that are not finite become zeros in this CTA's half of
-// V (blocks of [128 keys][64 columns], 128-byte swizzle), thread e of 256; the
-// first such key of each column is noted in both CTAs.
-template <int D>
-__device__ __noinline__ void take_out(Ctl &ctl, uint32_t v, int e, int rank, int key0, int lk, int base) {
-  constexpr int kPer = D / 128 * 128 * 8 / 256;  // 16-byte pieces per thread
-  const int r = e & 127, part = e >> 7;
-  const uint32_t row = v + (D == 256 ? part * 16384 : 0) + r * 128;
+// V (blocks of [128 keys][64 columns], 128-byte swizzle), thread e of kN; the first
+// such key of each column is noted in both CTAs.
+template <int D, int kN>
+__device__ __noinline__ void take_out(uint32_t bad, uint32_t v, int e, int rank, int key0, int lk, int base) {
+  constexpr int kPer = D * 8 / kN;  // 16-byte pieces per thread
+  const int r = e & 127;
   for (int i = 0; i < kPer; ++i) {
-    const int piece = ((D == 256 ? i : part * 4 + i) ^ (r & 7));
+    const int at = (e >> 7) * kPer + i;  // piece of the row: block at / 8
+    const int piece = (at & 7) ^ (r & 7);
+    const uint32_t where = v + (at >> 3) * 16384 + r * 128 + piece * 16;
     uint32_t w[4];
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(row + piece * 16)
+                 : "r"(where)
                  : "memory");
     bool hit = false;
 #pragma unroll
     for (int x = 0; x < 4; ++x)
       hit = hit || (w[x] & 0x7f80u) == 0x7f80u || (w[x] & 0x7f800000u) == 0x7f800000u;
     if (!hit) continue;
-    const int c0 = rank * (D / 2) + (D == 256 ? part * 64 : 0) + (piece ^ (r & 7)) * 8;
+    const int c0 = rank * (D / 2) + at * 8;
     for (int x = 0; x < 8; ++x) {
       const uint32_t half = 0xffffu << (16 * (x & 1));
       if ((w[x >> 1] & half & 0x7f807f80u) != (half & 0x7f807f80u)) continue;
       w[x >> 1] &= ~half;
       if (key0 + r >= lk) continue;  // (another sequence's: nobody sees it)
       const uint32_t mark = static_cast<uint32_t>(key0 + r - base);
-      const uint32_t at = smem_u32(&ctl.bad[(c0 + x) >> 1]);
       for (uint32_t to = 0; to < 2; ++to) {
-        const uint32_t p = cluster_map(at, to);
+        const uint32_t p = cluster_map(bad + (c0 + x) / 2 * 4, to);
         uint32_t old;
         asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(old) : "r"(p) : "memory");
         for (int tries = 0; tries < 1 << 16; ++tries) {
@@ -263,13 +345,25 @@ __device__ __noinline__ void take_out(Ctl &ctl, uint32_t v, int e, int rank, int
         }
       }
     }
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row + piece * 16), "r"(w[0]), "r"(w[1]),
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(where), "r"(w[0]), "r"(w[1]),
                  "r"(w[2]), "r"(w[3])
                  : "memory");
   }
   asm volatile("fence.acq_rel.cluster;" ::: "memory");
   fence_proxy_async_smem();
 }
+
+// What the roles derive from an item
+struct Tile {
+  int shift, nk, jm, mine;  // keys less queries, key tiles, first one that hides keys from a query, this CTA's first query
+  __device__ __forceinline__ Tile(const PrefillArgs &a, const Item &it, int rank) {
+    shift = it.lk - it.lq;
+    const int end = min(it.t0 + 2 * a.tokens, it.lq);
+    nk = (max(0, end + shift) + kKeys - 1) / kKeys;
+    jm = max(0, it.t0 + shift + 1) / kKeys;
+    mine = it.t0 + rank * a.tokens;
+  }
+};
 
 }  // namespace
 
@@ -279,46 +373,45 @@ __global__ void __launch_bounds__(kThreadsA, 1)
                         const __grid_constant__ CUtensorMap tmV, const PrefillArgs a) {
   using P = Plan<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  Ctl &ctl = *reinterpret_cast<Ctl *>(smem);
+  Ctl<D> &ctl = *reinterpret_cast<Ctl<D> *>(smem);
   volatile int *abort_flag = &ctl.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
-  const uint32_t sQ = smem_u32(smem) + kCtlBytes, ring = sQ + P::kQ;
+  const uint32_t sQ = smem_u32(smem) + P::kCtlBytes, ring = sQ + P::kQ;
   constexpr uint16_t kBoth = 3;
 
-  pdl_wait();
-  if (warp == 0) {
-    const Item it = find_item(a, blockIdx.x >> 1);
-    if (lane == 0) ctl.item = it;
-  }
-  if (threadIdx.x == 32) {
+  if (threadIdx.x == 0) {
     for (int s = 0; s < P::kSlots; ++s) {
       mbar_init(smem_u32(&ctl.full[s]), 1);
       mbar_init(smem_u32(&ctl.empty[s]), 1);
       mbar_init(smem_u32(&ctl.vloc[s]), 1);
     }
     mbar_init(smem_u32(&ctl.q_full), 1);
+    mbar_init(smem_u32(&ctl.q_empty), 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&ctl.s_full[b]), 1);
-      mbar_init(smem_u32(&ctl.p_full[b]), 8);
-      mbar_init(smem_u32(&ctl.p_loc[b]), 8);
+      mbar_init(smem_u32(&ctl.p_full[b]), P::kMakers);
+      mbar_init(smem_u32(&ctl.p_loc[b]), P::kMakers);
     }
     mbar_init(smem_u32(&ctl.pv_done), 1);
+    mbar_init(smem_u32(&ctl.o_full), 1);
     mbar_init(smem_u32(&ctl.drain), 1);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(smem_u32(&ctl.it_full[i]), 1);
+      mbar_init(smem_u32(&ctl.it_empty[i]), kReaders);
+    }
     ctl.abort_flag = 0;
     fence_mbar_init();
     prefetch_tmap(&tmQ);
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
-  for (int i = static_cast<int>(threadIdx.x); i < 128; i += kThreadsA) ctl.bad[i] = 0xffffffffu;
-  __syncthreads();
-  const Item it = ctl.item;
-  // (the whole cluster leaves; a misplaced shared memory, which the attribute
-  // above excludes, would break the swizzle)
-  if (!it.valid || (smem_u32(smem) & 1023u) != 0) {
-    if (it.valid && threadIdx.x == 0) report_error(a.status, MOE_ERR_DEVICE_BOUNDS, KID_ATTN_PREFILL * 100 + SITE_INDEX);
-    pdl_launch_dependents();
+  for (int i = static_cast<int>(threadIdx.x); i < 384; i += kThreadsA) ctl.bad[i >> 7][i & 127] = 0xffffffffu;
+  // (a misplaced shared memory, which the attribute above excludes, would break the
+  // swizzle)
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (threadIdx.x == 0) report_error(a.status, MOE_ERR_DEVICE_BOUNDS, KID_ATTN_PREFILL * 100 + SITE_INDEX);
+    pdl_wait();
     return;
   }
   if (warp == 1) {
@@ -329,59 +422,97 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   __syncthreads();
   cluster_sync_all();  // both CTAs' barriers exist
   tc_fence_after();
+  // Only now: a CTA of the next kernel may take TMEM columns before it waits for this
+  // grid.  (All 512 columns are this CTA's: their addresses start at 0.)
   pdl_launch_dependents();
-  // (all 512 columns are this CTA's: their addresses start at 0)
+  pdl_wait();
 
-  const int shift = it.lk - it.lq, per = 2 * a.tokens;
-  const int t_end = min(it.t0 + per, it.lq);           // the cluster's queries end here
-  const int seen = max(0, t_end + shift);              // keys that its last query sees
-  const int nk = (seen + kKeys - 1) / kKeys;
-  const int jm = max(0, it.t0 + shift + 1) / kKeys;    // first tile that hides keys from a query
-  const int mine = it.t0 + rank * a.tokens;            // this CTA's first query
+  // the k-th item of this cluster, read by a warp; false: an abort or the end
+  auto next_item = [&](int k, Item &it) {
+    const int i = k % kItems;
+    if (!warp_wait(a, smem_u32(&ctl.it_full[i]), (k / kItems) & 1, abort_flag, SITE_STAGE)) return false;
+    it = ctl.item[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&ctl.it_empty[i]));
+    return it.valid != 0;
+  };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ copies
-    if (lane == 0 && nk > 0) {
-      const uint64_t pol = policy_evict_last();
-      const uint32_t q0 = cluster_map(smem_u32(&ctl.q_full), 0);
-      if (rank == 0) mbar_arrive_expect_tx(smem_u32(&ctl.q_full), 2 * a.tokens * a.group * D * 2);
-      for (int b = 0; b < D / 64; ++b)
-        tma_load_3d_pair(sQ + b * 16384, &tmQ, q0, 64 * b, it.head * a.group, it.q0 + mine);
-      int r = 0;
-      auto load = [&](bool values, int j) {
-        const int s = r % P::kSlots;
-        const uint32_t fb = smem_u32(&ctl.full[s]), dst = ring + s * P::kSlot;
-        if (!poll(smem_u32(&ctl.empty[s]), ((r / P::kSlots) & 1) ^ 1, abort_flag)) {
-          fail(a, abort_flag, SITE_PRODUCER_EMPTY);
-          return false;
-        }
-        if (!values) {
-          if (rank == 0) mbar_arrive_expect_tx(fb, 2 * P::kSlot);
-          const uint32_t to = cluster_map(fb, 0);
-          for (int b = 0; b < D / 64; ++b)
-            tma_load_2d_pair(dst + b * 8192, &tmK, to, it.head * D + 64 * b, it.k0 + j * kKeys + rank * 64, pol);
-        } else {
-          uint32_t to = cluster_map(fb, 0);
-          if (j >= jm) {  // the softmax's warps see to these first: their copy is this CTA's matter
-            if (rank == 0) mbar_arrive(fb);
-            mbar_arrive_expect_tx(smem_u32(&ctl.vloc[s]), P::kSlot);
-            to = cluster_map(smem_u32(&ctl.vloc[s]), rank);
-          } else if (rank == 0) {
-            mbar_arrive_expect_tx(fb, 2 * P::kSlot);
-          }
-          for (int b = 0; b < D / 128; ++b)
-            tma_load_2d_pair(dst + b * 16384, &tmV, to, it.head * D + rank * (D / 2) + 64 * b, it.k0 + j * kKeys, pol);
-        }
-        ++r;
-        return true;
-      };
-      bool ok = load(false, 0);
-      for (int j = 0; ok && j < nk; ++j) {
-        if (j + 1 < nk) ok = load(false, j + 1);
-        if (ok) ok = load(true, j);
+  if (warp == 10) {
+    // ------------------------------------------------------------ schedule
+    const Schedule plan(a);
+    const long long clusters = gridDim.x >> 1, c = blockIdx.x >> 1, total = plan.all(0) * a.Hk;
+    for (int k = 0;; ++k) {
+      const long long n = k & 1 ? (k + 1) * clusters - 1 - c : k * clusters + c;
+      Item it = {};
+      if (n < total) it = plan.find(n);
+      if (!warp_wait(a, smem_u32(&ctl.it_empty[k % kItems]), ((k / kItems) & 1) ^ 1, abort_flag, SITE_STAGE)) break;
+      if (lane == 0) {
+        ctl.item[k % kItems] = it;
+        mbar_arrive(smem_u32(&ctl.it_full[k % kItems]));
       }
-      // the commits of the last slots arrive here too: none may land after the
-      // CTA has ended
+      __syncwarp();
+      if (!it.valid) break;
+    }
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ copies
+    const uint64_t pol = policy_evict_last();
+    int r = 0;  // uses of the ring
+    bool ok = true;
+    Item it;
+    for (int k = 0, used = 0; ok && next_item(k, it); ++k) {
+      const Tile t(a, it, rank);
+      if (t.nk == 0) continue;
+      if (lane == 0) {
+        // Q, once the scores of the tile before are made
+        if (!poll(smem_u32(&ctl.q_empty), (used & 1) ^ 1, abort_flag)) {
+          fail(a, abort_flag, SITE_PRODUCER_EMPTY);
+          ok = false;
+        }
+        const uint32_t q0 = cluster_map(smem_u32(&ctl.q_full), 0);
+        if (ok) {
+          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&ctl.q_full), 2 * a.tokens * a.group * D * 2);
+          for (int b = 0; b < D / 64; ++b)
+            tma_load_3d_pair(sQ + b * 16384, &tmQ, q0, 64 * b, it.head * a.group, it.q0 + t.mine);
+        }
+        auto load = [&](bool values, int j) {
+          const int s = r % P::kSlots;
+          const uint32_t fb = smem_u32(&ctl.full[s]), dst = ring + s * P::kSlot;
+          if (!poll(smem_u32(&ctl.empty[s]), ((r / P::kSlots) & 1) ^ 1, abort_flag)) {
+            fail(a, abort_flag, SITE_PRODUCER_EMPTY);
+            return false;
+          }
+          if (!values) {
+            if (rank == 0) mbar_arrive_expect_tx(fb, 2 * P::kSlot);
+            const uint32_t to = cluster_map(fb, 0);
+            for (int b = 0; b < D / 64; ++b)
+              tma_load_2d_pair(dst + b * 8192, &tmK, to, it.head * D + 64 * b, it.k0 + j * kKeys + rank * 64, pol);
+          } else {
+            uint32_t to = cluster_map(fb, 0);
+            if (j >= t.jm) {  // the softmax's warps see to these first: their copy is this CTA's matter
+              if (rank == 0) mbar_arrive(fb);
+              mbar_arrive_expect_tx(smem_u32(&ctl.vloc[s]), P::kSlot);
+              to = cluster_map(smem_u32(&ctl.vloc[s]), rank);
+            } else if (rank == 0) {
+              mbar_arrive_expect_tx(fb, 2 * P::kSlot);
+            }
+            for (int b = 0; b < D / 128; ++b)
+              tma_load_2d_pair(dst + b * 16384, &tmV, to, it.head * D + rank * (D / 2) + 64 * b, it.k0 + j * kKeys, pol);
+          }
+          ++r;
+          return true;
+        };
+        if (ok) ok = load(false, 0);
+        for (int j = 0; ok && j < t.nk; ++j) {
+          if (j + 1 < t.nk) ok = load(false, j + 1);
+          if (ok) ok = load(true, j);
+        }
+      }
+      ++used;
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    // the commits of the last slots and of Q arrive here too: none may land after the
+    // CTA has ended
+    if (lane == 0 && ok && !*abort_flag) {
       for (int i = 0; ok && i < P::kSlots; ++i, ++r)
         if (r >= P::kSlots && !poll(smem_u32(&ctl.empty[r % P::kSlots]), ((r / P::kSlots) & 1) ^ 1, abort_flag)) {
           fail(a, abort_flag, SITE_DRAIN);
@@ -389,204 +520,359 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         }
     }
   } else if (warp == 1) {
-    if (rank == 0 && nk > 0) {
+    Item it;
+    if (rank == 0) {
       // ------------------------------------------------------------ MMAs
       // (the whole warp runs the loop, so that descriptors stay in uniform
       // registers; one lane issues)
       constexpr uint32_t id_s = idesc_make(256, kKeys, 1), id_o = idesc_make(256, D, 1) | kTransposeB;
       const bool one = elect_one();
       const uint64_t dq = sdesc_sw128(sQ), dk = sdesc_sw128(ring), dv = sdesc_cols(ring, 16384);
-      int r = 0;
-      bool ok = warp_wait(a, smem_u32(&ctl.q_full), 0, abort_flag, SITE_MMA_FULL);
-      auto scores = [&](int j) {
-        const int s = r % P::kSlots;
-        if (!warp_wait(a, smem_u32(&ctl.full[s]), (r / P::kSlots) & 1, abort_flag, SITE_MMA_FULL)) return false;
-        tc_fence_after();
-        if (one) {
-          const uint64_t k = dk + s * (P::kSlot >> 4);
+      int r = 0, done = 0;  // uses of the ring; key tiles of the items before
+      bool ok = true;
+      for (int k = 0, used = 0; ok && next_item(k, it); ++k) {
+        const Tile t(a, it, rank);
+        if (t.nk == 0) continue;
+        ok = warp_wait(a, smem_u32(&ctl.q_full), used & 1, abort_flag, SITE_MMA_FULL);
+        ++used;
+        auto scores = [&](int j) {
+          const int s = r % P::kSlots, b = (done + j) & 1;
+          if (!warp_wait(a, smem_u32(&ctl.full[s]), (r / P::kSlots) & 1, abort_flag, SITE_MMA_FULL)) return false;
+          tc_fence_after();
+          if (one) {
+            const uint64_t keys = dk + s * (P::kSlot >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma2_bf16(P::S + (j & 1) * kKeys, dq + (((kk >> 2) * 16384 + 32 * (kk & 3)) >> 4),
-                      k + (((kk >> 2) * 8192 + 32 * (kk & 3)) >> 4), id_s, kk > 0 ? 1u : 0u);
-          tc_commit2_mc(smem_u32(&ctl.s_full[j & 1]), kBoth);
-          tc_commit2_mc(smem_u32(&ctl.empty[s]), kBoth);
-        }
-        ++r;
-        return true;
-      };
-      auto output = [&](int j) {
-        const int s = r % P::kSlots;
-        if (!warp_wait(a, smem_u32(&ctl.full[s]), (r / P::kSlots) & 1, abort_flag, SITE_MMA_FULL) ||
-            !warp_wait(a, smem_u32(&ctl.p_full[j & 1]), (j >> 1) & 1, abort_flag, SITE_STAGE))
-          return false;
-        tc_fence_after();
-        if (one) {
-          const uint64_t v = dv + s * (P::kSlot >> 4);
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma2_bf16(P::S + b * kKeys, dq + (((kk >> 2) * 16384 + 32 * (kk & 3)) >> 4),
+                        keys + (((kk >> 2) * 8192 + 32 * (kk & 3)) >> 4), id_s, kk > 0 ? 1u : 0u);
+            tc_commit2_mc(smem_u32(&ctl.s_full[b]), kBoth);
+            tc_commit2_mc(smem_u32(&ctl.empty[s]), kBoth);
+            if (j == t.nk - 1) tc_commit2_mc(smem_u32(&ctl.q_empty), kBoth);
+          }
+          ++r;
+          return true;
+        };
+        auto output = [&](int j) {
+          const int s = r % P::kSlots, n = done + j, b = n & 1;
+          if (!warp_wait(a, smem_u32(&ctl.full[s]), (r / P::kSlots) & 1, abort_flag, SITE_MMA_FULL) ||
+              !warp_wait(a, smem_u32(&ctl.p_full[b]), (n >> 1) & 1, abort_flag, SITE_STAGE))
+            return false;
+          tc_fence_after();
+          if (one) {
+            const uint64_t v = dv + s * (P::kSlot >> 4);
+            const uint32_t o = P::O + (P::kStreams == 2 ? b * D : 0);
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma2_ts_bf16(P::O, P::S + (j & 1) * kKeys + 8 * kk, v + kk * (2048 >> 4), id_o, (j | kk) != 0 ? 1u : 0u);
-          tc_commit2_mc(smem_u32(&ctl.pv_done), kBoth);
-          tc_commit2_mc(smem_u32(&ctl.empty[s]), kBoth);
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              mma2_ts_bf16(o, P::S + b * kKeys + 8 * kk, v + kk * (2048 >> 4), id_o,
+                           j >= P::kStreams || kk != 0 ? 1u : 0u);
+            if (P::kStreams == 1) tc_commit2_mc(smem_u32(&ctl.pv_done), kBoth);
+            tc_commit2_mc(smem_u32(&ctl.empty[s]), kBoth);
+            if (j == t.nk - 1) tc_commit2_mc(smem_u32(&ctl.o_full), kBoth);
+          }
+          ++r;
+          return true;
+        };
+        if (ok) ok = scores(0);
+        for (int j = 0; ok && j < t.nk; ++j) {
+          if (j + 1 < t.nk) ok = scores(j + 1);
+          if (ok) ok = output(j);
         }
-        ++r;
-        return true;
-      };
-      if (ok) ok = scores(0);
-      for (int j = 0; ok && j < nk; ++j) {
-        if (j + 1 < nk) ok = scores(j + 1);
-        if (ok) ok = output(j);
+        done += t.nk;
       }
-      if (!ok) {  // the MMAs issued so far end before TMEM or shared memory go away
+      if (!ok || *abort_flag) {  // the MMAs issued so far end before TMEM or shared memory go away
         if (one) tc_commit2(smem_u32(&ctl.drain));
         if (!poll(smem_u32(&ctl.drain), 0, nullptr) && lane == 0) fail(a, abort_flag, SITE_DRAIN);
       }
-    } else if (rank == 1) {
+    } else {
       // ------------------------------------------------------------ P is there
-      for (int j = 0; j < nk; ++j) {
-        if (!warp_wait(a, smem_u32(&ctl.p_loc[j & 1]), (j >> 1) & 1, abort_flag, SITE_STAGE)) break;
-        const uint32_t to = cluster_map(smem_u32(&ctl.p_full[j & 1]), 0);
-        if (lane == 0) st_async_tx4(cluster_map(smem_u32(&ctl.sink), 0), 0u, to);  // (nothing reads the word)
+      int done = 0;
+      bool ok = true;
+      for (int k = 0; ok && next_item(k, it); ++k) {
+        const Tile t(a, it, rank);
+        for (int j = 0; ok && j < t.nk; ++j) {
+          const int n = done + j;
+          ok = warp_wait(a, smem_u32(&ctl.p_loc[n & 1]), (n >> 1) & 1, abort_flag, SITE_STAGE);
+          const uint32_t to = cluster_map(smem_u32(&ctl.p_full[n & 1]), 0);
+          if (ok && lane == 0) st_async_tx4(cluster_map(smem_u32(&ctl.sink), 0), 0u, to);  // (nothing reads the word)
+        }
+        done += t.nk;
       }
     }
   } else {
-    // ------------------------------------------------------------ softmax
-    const int wq = warp & 3, half = (warp - 2) >> 2, e = static_cast<int>(threadIdx.x) - 64;
-    const uint32_t lanes = static_cast<uint32_t>(wq * 32 + half * 16) << 16;
-    // this thread's two rows: the last key each sees, -1 where it is no query
-    int limit[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int row = wq * 32 + half * 16 + 8 * x + (lane >> 2), t = mine + row / a.group;
-      limit[x] = row < a.tokens * a.group && t < it.lq ? min(t + shift, it.lk - 1) : -1;
-    }
-    const int own = max(0, mine + shift + 1) / kKeys;  // first tile masked for this CTA
-    float m[2] = {-INFINITY, -INFINITY}, ref[2] = {0.0f, 0.0f}, l[2] = {0.0f, 0.0f};
+    // ------------------------------------------------------------ softmax, outputs
+    const int wq = warp & 3, half = (warp - 2) >> 2;
     const float c = a.scale, late = kLate / c;
-    uint32_t vphase = 0;
+    int done = 0, base = 0, used = 0;  // key tiles, uses of the ring of the items before; items with keys, of three
+    uint32_t vphase = 0, o_phase = 0;
     bool ok = true;
-    for (int j = 0; j < nk; ++j) {
-      const uint32_t ts = P::S + (j & 1) * kKeys + lanes;
-      ok = warp_wait(a, smem_u32(&ctl.s_full[j & 1]), (j >> 1) & 1, abort_flag, SITE_EPI_TMEM_FULL);
-      if (!ok) break;
-      tc_fence_after();
-      float x[2][32];
-      ld_16x64(ts, x[0]);
-      ld_16x64(ts + 64, x[1]);
-      if (j >= own) {
-        const int key = j * kKeys + 2 * (lane & 3);
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (key + 64 * y + 8 * (i >> 2) + (i & 1) > limit[(i >> 1) & 1]) x[y][i] = -INFINITY;
-      }
-      float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int y = 0; y < 2; ++y)
-#pragma unroll
-        for (int i = 0; i < 32; ++i) top[(i >> 1) & 1] = fmaxf(top[(i >> 1) & 1], x[y][i]);
-      bool grown = false;
-#pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        top[z] = fmaxf(top[z], __shfl_xor_sync(0xffffffffu, top[z], 1));
-        top[z] = fmaxf(top[z], __shfl_xor_sync(0xffffffffu, top[z], 2));
-        grown = grown || top[z] > m[z] + late;
-      }
-      if (__any_sync(0xffffffffu, grown)) {
-        float f[2];
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          const float to = top[z] > m[z] + late ? top[z] : m[z];
-          f[z] = to == m[z] ? 1.0f : fast_exp2((m[z] - to) * c);
-          m[z] = to;
-          ref[z] = to == -INFINITY ? 0.0f : to * c;
-          l[z] *= f[z];
-        }
-        if (j > 0) {  // O of the tiles before
-          ok = warp_wait(a, smem_u32(&ctl.pv_done), (j - 1) & 1, abort_flag, SITE_STAGE);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int d = 0; d < D; d += 64) {
-            float o[32];
-            ld_16x64(P::O + lanes + d, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= f[(i >> 1) & 1];
-            st_16x64(P::O + lanes + d, o);
-          }
-        }
-      }
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        uint32_t p[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int z = i & 1;
-          const float u = fast_exp2(fmaf(x[y][2 * i], c, -ref[z])), w = fast_exp2(fmaf(x[y][2 * i + 1], c, -ref[z]));
-          l[z] += u + w;
-          p[i] = bf16x2_bits(u, w);
-        }
-        st_pairs_16x32(ts + 32 * y, p);
-      }
-      wait_st();
-      if (j >= jm) {
-        const int rv = j + 1 < nk ? 2 * j + 2 : 2 * j + 1, s = rv % P::kSlots;  // V's place in the ring
-        ok = warp_wait(a, smem_u32(&ctl.vloc[s]), (vphase >> s) & 1, abort_flag, SITE_MMA_FULL);
-        if (!ok) break;
-        vphase ^= 1u << s;
-        take_out<D>(ctl, ring + s * P::kSlot, e, rank, j * kKeys, it.lk, jm * kKeys);
-      }
+    Item it;
+    // P of tile n is in TMEM: CTA 0 hears of it
+    auto made = [&](int n) {
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         if (rank == 1) {
-          mbar_arrive(smem_u32(&ctl.p_loc[j & 1]));
-        } else if (warp == 2) {
-          mbar_arrive_expect_tx(smem_u32(&ctl.p_full[j & 1]), 4);  // the other CTA's word
+          mbar_arrive(smem_u32(&ctl.p_loc[n & 1]));
+        } else if (wq == 2 && (P::kStreams == 2 || half == 0)) {
+          mbar_arrive_expect_tx(smem_u32(&ctl.p_full[n & 1]), 4);  // the other CTA's word
         } else {
-          mbar_arrive(smem_u32(&ctl.p_full[j & 1]));
+          mbar_arrive(smem_u32(&ctl.p_full[n & 1]));
         }
       }
-    }
-    // ------------------------------------------------------------ outputs
-    if (ok && nk > 0) {
-      ok = (nk < 2 || warp_wait(a, smem_u32(&ctl.pv_done), (nk - 2) & 1, abort_flag, SITE_EPI_TMEM_FULL)) &&
-           warp_wait(a, smem_u32(&ctl.pv_done), (nk - 1) & 1, abort_flag, SITE_EPI_TMEM_FULL);
-      tc_fence_after();
+    };
+    for (int k = 0; ok && next_item(k, it); ++k) {
+      const Tile t(a, it, rank);
+      const uint32_t bad = smem_u32(&ctl.bad[used][0]);
+      const int own = max(0, t.mine + t.shift + 1) / kKeys;  // first tile masked for this CTA
+      // the values of a masked tile
+      auto clean = [&](int j) {
+        const int s = (base + (j + 1 < t.nk ? 2 * j + 2 : 2 * j + 1)) % P::kSlots;  // V's place in the ring
+        if (!warp_wait(a, smem_u32(&ctl.vloc[s]), (vphase >> s) & 1, abort_flag, SITE_MMA_FULL)) return false;
+        const int e = static_cast<int>(threadIdx.x) - 64 - (P::kStreams == 2 ? half * 128 : 0);
+        take_out<D, P::kMakers * 32>(bad, ring + s * P::kSlot, e, rank, j * kKeys, it.lk, t.jm * kKeys);
+        return true;
+      };
+      auto passed = [&](int j) {  // (every softmax warp follows the phases of the masked tiles' copies)
+        if (j >= t.jm) vphase ^= 1u << (base + (j + 1 < t.nk ? 2 * j + 2 : 2 * j + 1)) % P::kSlots;
+      };
+      if constexpr (D == 256) {
+        const uint32_t lanes = static_cast<uint32_t>(wq * 32 + half * 16) << 16;
+        // this thread's two rows: the last key each sees, -1 where it is no query
+        int limit[2];
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        l[z] += __shfl_xor_sync(0xffffffffu, l[z], 1);
-        l[z] += __shfl_xor_sync(0xffffffffu, l[z], 2);
-        if ((lane & 3) == 0) ctl.sum[wq * 32 + half * 16 + 8 * z + (lane >> 2)] = l[z];
-      }
-    }
-    // the two warps of a TMEM quarter take half of the columns each, a row per thread
-    named_bar_sync(1 + wq, 64);
-    const int row = wq * 32 + lane, t = mine + row / a.group;
-    const bool valid = ok && row < a.tokens * a.group && t < it.lq;
-    const int lim = t + shift;
-    const float inv = nk > 0 && lim >= 0 ? 1.0f / ctl.sum[row] : 0.0f;
-    __nv_bfloat16 *o = a.out + (static_cast<long long>(it.q0 + t) * a.Hq + it.head * a.group + row % a.group) * D;
-    const int mark = lim - jm * kKeys;
+        for (int x = 0; x < 2; ++x) {
+          const int row = wq * 32 + half * 16 + 8 * x + (lane >> 2), at = t.mine + row / a.group;
+          limit[x] = row < a.tokens * a.group && at < it.lq ? min(at + t.shift, it.lk - 1) : -1;
+        }
+        float m[2] = {-INFINITY, -INFINITY}, ref[2] = {0.0f, 0.0f}, l[2] = {0.0f, 0.0f};
+        for (int j = 0; ok && j < t.nk; ++j) {
+          const int n = done + j;
+          const uint32_t ts = P::S + (n & 1) * kKeys + lanes;
+          ok = warp_wait(a, smem_u32(&ctl.s_full[n & 1]), (n >> 1) & 1, abort_flag, SITE_EPI_TMEM_FULL);
+          if (!ok) break;
+          tc_fence_after();
+          float x[2][32];
+          ld_16x64(ts, x[0]);
+          ld_16x64(ts + 64, x[1]);
+          if (j >= own) {
+            const int key = j * kKeys + 2 * (lane & 3);
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (key + 64 * y + 8 * (i >> 2) + (i & 1) > limit[(i >> 1) & 1]) x[y][i] = -INFINITY;
+          }
+          float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int y = 0; y < 2; ++y)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) top[(i >> 1) & 1] = fmaxf(top[(i >> 1) & 1], x[y][i]);
+          bool grown = false;
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            top[z] = fmaxf(top[z], __shfl_xor_sync(0xffffffffu, top[z], 1));
+            top[z] = fmaxf(top[z], __shfl_xor_sync(0xffffffffu, top[z], 2));
+            grown = grown || top[z] > m[z] + late;
+          }
+          if (__any_sync(0xffffffffu, grown)) {
+            float f[2];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const float to = top[z] > m[z] + late ? top[z] : m[z];
+              f[z] = to == m[z] ? 1.0f : fast_exp2((m[z] - to) * c);
+              m[z] = to;
+              ref[z] = to == -INFINITY ? 0.0f : to * c;
+              l[z] *= f[z];
+            }
+            if (j > 0) {  // O of the tiles before
+              ok = warp_wait(a, smem_u32(&ctl.pv_done), (n - 1) & 1, abort_flag, SITE_STAGE);
+              if (!ok) break;
+              tc_fence_after();
 #pragma unroll 1
-    for (int d = half * (D / 2); ok && d < (half + 1) * (D / 2); d += 32) {
-      float v[32];
-      if (nk > 0) {
-        tmem_ld32_sync(P::O + (static_cast<uint32_t>(wq * 32) << 16) + d, v);
-      }
-      uint32_t w[16];
+              for (int d = 0; d < D; d += 64) {
+                float o[32];
+                ld_16x64(P::O + lanes + d, o);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint32_t bad = ctl.bad[d / 2 + i];
-        float x0 = nk > 0 && lim >= 0 ? v[2 * i] * inv : 0.0f, x1 = nk > 0 && lim >= 0 ? v[2 * i + 1] * inv : 0.0f;
-        if (mark >= static_cast<int>(bad & 0xffffu)) x0 = __uint_as_float(0x7fffffffu);
-        if (mark >= static_cast<int>(bad >> 16)) x1 = __uint_as_float(0x7fffffffu);
-        w[i] = bf16x2_bits(x0, x1);
-      }
-      if (valid)
+                for (int i = 0; i < 32; ++i) o[i] *= f[(i >> 1) & 1];
+                st_16x64(P::O + lanes + d, o);
+              }
+            }
+          }
 #pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<uint4 *>(o + d + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+          for (int y = 0; y < 2; ++y) {
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int z = i & 1;
+              const float u = fast_exp2(fmaf(x[y][2 * i], c, -ref[z])), w = fast_exp2(fmaf(x[y][2 * i + 1], c, -ref[z]));
+              l[z] += u + w;
+              p[i] = bf16x2_bits(u, w);
+            }
+            st_pairs_16x32(ts + 32 * y, p);
+          }
+          wait_st();
+          if (j >= t.jm) ok = clean(j);
+          passed(j);
+          if (!ok) break;
+          made(n);
+        }
+        if (ok && t.nk > 0) {
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            l[z] += __shfl_xor_sync(0xffffffffu, l[z], 1);
+            l[z] += __shfl_xor_sync(0xffffffffu, l[z], 2);
+            if ((lane & 3) == 0) ctl.sum[wq * 32 + half * 16 + 8 * z + (lane >> 2)] = l[z];
+          }
+        }
+      } else {
+        const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
+        const int row = wq * 32 + lane, at = t.mine + row / a.group;
+        const int limit = row < a.tokens * a.group && at < it.lq ? min(at + t.shift, it.lk - 1) : -1;
+        float m = -INFINITY, ref = 0.0f, l = 0.0f;
+        for (int j = 0; ok && j < t.nk; ++j) {
+          const int n = done + j;
+          if ((n & 1) != half) {  // the other stream's
+            passed(j);
+            continue;
+          }
+          const uint32_t ts = P::S + half * kKeys + lanes, to = P::O + half * D + lanes;
+          ok = warp_wait(a, smem_u32(&ctl.s_full[half]), (n >> 1) & 1, abort_flag, SITE_EPI_TMEM_FULL);
+          if (!ok) break;
+          tc_fence_after();
+          float x[4][32];
+          tmem_ld32x2_sync(ts, ts + 32, x[0], x[1]);
+          tmem_ld32x2_sync(ts + 64, ts + 96, x[2], x[3]);
+          if (j >= own) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (j * kKeys + 32 * y + i > limit) x[y][i] = -INFINITY;
+          }
+          float top4[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            top4[y] = x[y][0];
+#pragma unroll
+            for (int i = 1; i < 32; ++i) top4[y] = fmaxf(top4[y], x[y][i]);
+          }
+          const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+          if (__any_sync(0xffffffffu, top > m + late)) {
+            const float next = top > m + late ? top : m;
+            const float f = next == m ? 1.0f : fast_exp2((m - next) * c);
+            m = next;
+            ref = next == -INFINITY ? 0.0f : next * c;
+            l *= f;
+            // O of the stream's tiles before: their products are done, the scores of this
+            // tile were issued behind them
+            if (j >= 2) {
+#pragma unroll 1
+              for (int d = 0; d < D; d += 32) {
+                float o[32];
+                uint32_t w[32];
+                tmem_ld32_sync(to + d, o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(o[i] * f);
+                st_32x32(to + d, w);
+              }
+            }
+          }
+          float l4[4] = {};
+#pragma unroll
+          for (int y = 0; y < 4; y += 2) {
+            uint32_t p[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float u = fast_exp2(fmaf(x[y + (i >> 4)][2 * (i & 15)], c, -ref));
+              const float w = fast_exp2(fmaf(x[y + (i >> 4)][2 * (i & 15) + 1], c, -ref));
+              l4[i & 3] += u + w;
+              p[i] = bf16x2_bits(u, w);
+            }
+            st_32x32(ts + 16 * y, p);
+          }
+          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          wait_st();
+          if (j >= t.jm) ok = clean(j);
+          passed(j);
+          if (!ok) break;
+          made(n);
+        }
+        ctl.stream[half][row] = make_float2(m, l);
+      }
+      // ------------------------------------------------------------ outputs
+      if (ok && t.nk > 0) {
+        ok = warp_wait(a, smem_u32(&ctl.o_full), o_phase, abort_flag, SITE_EPI_TMEM_FULL);
+        o_phase ^= 1;
+        tc_fence_after();
+        // All warps of both CTAs have made P of this item, so they are past the outputs of
+        // the one before: its marks make room for the item after the next, whose scores
+        // wait for this warp's P of the next.
+        const int e = static_cast<int>(threadIdx.x) - 64;
+        if (e < 128) ctl.bad[used == 0 ? 2 : used - 1][e] = 0xffffffffu;
+      }
+      // the two warps of a TMEM quarter take half of the columns each, a row per thread
+      named_bar_sync(1 + wq, 64);
+      const int row = wq * 32 + lane, at = t.mine + row / a.group, lim = at + t.shift;
+      const bool valid = ok && row < a.tokens * a.group && at < it.lq, any = t.nk > 0 && lim >= 0;
+      // factors of the streams' outputs
+      float f0, f1 = 0.0f;
+      if constexpr (D == 256) {
+        f0 = any ? 1.0f / ctl.sum[row] : 0.0f;
+      } else {
+        const float2 s0 = ctl.stream[0][row], s1 = ctl.stream[1][row];
+        const float M = fmaxf(s0.x, s1.x);
+        f0 = s0.x == M ? 1.0f : fast_exp2((s0.x - M) * c);
+        f1 = s1.x == M ? 1.0f : fast_exp2((s1.x - M) * c);
+        const float inv = any ? 1.0f / (f0 * s0.y + f1 * s1.y) : 0.0f;
+        f0 *= inv;
+        f1 *= inv;
+      }
+      __nv_bfloat16 *o = a.out + (static_cast<long long>(it.q0 + at) * a.Hq + it.head * a.group + row % a.group) * D;
+      const int mark = lim - t.jm * kKeys;
+#pragma unroll 1
+      for (int d = half * (D / 2); ok && d < (half + 1) * (D / 2); d += 32) {
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+        if (t.nk > 0) {
+          const uint32_t ta = P::O + (static_cast<uint32_t>(wq * 32) << 16) + d;
+          if constexpr (D == 256) {
+            tmem_ld32_sync(ta, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = any ? v[i] * f0 : 0.0f;
+          } else {
+            float w[32];
+            if (t.nk > 1) {
+              tmem_ld32x2_sync(ta, ta + D, v, w);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = any ? fmaf(w[i], f1, v[i] * f0) : 0.0f;
+            } else {  // (the other stream's O is another row's)
+              tmem_ld32_sync(ta + (done & 1) * D, v);
+              const float f = done & 1 ? f1 : f0;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = any ? v[i] * f : 0.0f;
+            }
+          }
+        }
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t first = ctl.bad[used][d / 2 + i];
+          if (mark >= static_cast<int>(first & 0xffffu)) v[2 * i] = __uint_as_float(0x7fffffffu);
+          if (mark >= static_cast<int>(first >> 16)) v[2 * i + 1] = __uint_as_float(0x7fffffffu);
+          w[i] = bf16x2_bits(v[2 * i], v[2 * i + 1]);
+        }
+        if (valid)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<uint4 *>(o + d + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+      }
+      tc_fence_before();
+      // both have read O and the sums before either goes on
+      named_bar_sync(1 + wq, 64);
+      if (t.nk > 0) used = used == 2 ? 0 : used + 1;
+      done += t.nk;
+      base += 2 * t.nk;
     }
   }
   __syncwarp();
@@ -602,9 +888,23 @@ __global__ void __launch_bounds__(kThreadsA, 1)
 namespace {
 
 struct PrefillDevice {
+  int clusters[2] = {0, 0};  // that can be resident at once (D = 128, 256)
   int *status = nullptr;
   int rc = MOE_ERR_CUDA;
 };
+
+// clusters of two CTAs, as a programmatic dependent of the kernel before (attr[1])
+void prefill_config(cudaLaunchConfig_t &cfg, cudaLaunchAttribute *attr, int ctas, int smem, cudaStream_t st) {
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kThreadsA);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+}
 
 const PrefillDevice &prefill_device() {
   static PrefillDevice devs[64];
@@ -615,10 +915,16 @@ const PrefillDevice &prefill_device() {
   std::call_once(once[dev], [dev] {
     PrefillDevice &d = devs[dev];
     d.status = noalloc_status_word();
-    auto set = [](auto kern, int bytes) {
-      return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+    auto set = [](auto kern, int bytes, int &clusters) {
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr;
+      prefill_config(cfg, &attr, 2, bytes, nullptr);
+      cfg.numAttrs = 1;
+      return cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) == cudaSuccess && clusters > 0;
     };
-    if (d.status && set(attn_prefill_kernel<128>, Plan<128>::kTotal) && set(attn_prefill_kernel<256>, Plan<256>::kTotal))
+    if (d.status && set(attn_prefill_kernel<128>, Plan<128>::kTotal, d.clusters[0]) &&
+        set(attn_prefill_kernel<256>, Plan<256>::kTotal, d.clusters[1]))
       d.rc = MOE_OK;
   });
   return devs[dev];
@@ -626,20 +932,12 @@ const PrefillDevice &prefill_device() {
 
 template <int D>
 cudaError_t launch_prefill(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
-                           const PrefillArgs &a, long long clusters, cudaStream_t st) {
+                           const PrefillArgs &a, int clusters, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters));
-  cfg.blockDim = dim3(kThreadsA);
-  cfg.dynamicSmemBytes = Plan<D>::kTotal;
-  cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  prefill_config(cfg, attr, 2 * clusters, Plan<D>::kTotal, st);
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D>, mq, mk, mv, a);
 }
@@ -695,8 +993,8 @@ extern "C" int moe_attention_prefill(const void *q, const void *k, const void *v
   // tiles of the call, or as many as there can be
   const long long per = 2 * a.tokens;
   const long long tiles = offsets ? n_q / per + n_seq : n_seq * ((n_q / n_seq + per - 1) / per);
-  const long long clusters = tiles * n_kv_heads;
-  if (clusters > 0x3fffffffLL) return MOE_ERR_UNSUPPORTED;
+  const int most = dev.clusters[head_dim == 256];
+  const int clusters = tiles * n_kv_heads < most ? static_cast<int>(tiles * n_kv_heads) : most;
   const uint64_t d = head_dim, hk = n_kv_heads;
   const uint64_t keys = n_k > 0 ? n_k : 1;  // (no key is read where there is none)
   const void *kb = n_k > 0 ? k : q, *vb = n_k > 0 ? v : q;
