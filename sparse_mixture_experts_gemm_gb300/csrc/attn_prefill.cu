@@ -64,6 +64,7 @@ struct PrefillArgs {
   const int *offsets, *k_offsets;
   long long n_q, n_k;
   int n_seq, Hq, Hk, group, tokens;  // tokens: of a CTA's tile
+  uint32_t per_mul, per_shift;       // x / (2 tokens) = (x per_mul >> 32) >> per_shift, x < 2^31
   float scale;                       // times log2(e)
   int *status;
 };
@@ -85,8 +86,7 @@ struct Ctl {
   Item item[kItems];
   // of three tiles of rows in turn, two columns per word: first key (from the first
   // masked tile on) whose value is not finite
-  uint32_t bad[3][128];
-  float sum[128];                            // D = 256: sums of the rows
+  uint32_t bad[3][128], hit[3];  // hit: whether there is one
   float2 stream[2][D == 128 ? 128 : 1];      // D = 128: maximum and sum of each stream's rows
 };
 
@@ -171,7 +171,14 @@ __device__ __forceinline__ void st_pairs_16x32(uint32_t ta, const uint32_t (&r)[
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(ta)
       : "memory");
 }
-// 32 lanes x 32 columns, a lane per thread
+// 32 lanes x 16 or 32 columns, a lane per thread
+__device__ __forceinline__ void st_32x16(uint32_t ta, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::
+          "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(ta)
+      : "memory");
+}
 __device__ __forceinline__ void st_32x32(uint32_t ta, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::
@@ -182,6 +189,40 @@ __device__ __forceinline__ void st_32x32(uint32_t ta, const uint32_t (&r)[32]) {
       : "memory");
 }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// two fp32 values side by side
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t p, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// 4 x 4 words of a quad's lanes turned: r[i] of lane q becomes r[q] of lane i
+__device__ __forceinline__ void turn_quad(uint32_t (&r)[4]) {
+  const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const uint32_t t = __shfl_xor_sync(0xffffffffu, odd ? r[i] : r[i + 1], 1);
+    if (odd) r[i] = t; else r[i + 1] = t;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t t = __shfl_xor_sync(0xffffffffu, high ? r[i] : r[i + 2], 2);
+    if (high) r[i] = t; else r[i + 2] = t;
+  }
+}
 
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
@@ -217,10 +258,15 @@ struct Schedule {
   const PrefillArgs &a;
   int per;           // queries of a tile
   int lq, shift;     // (n_seq <= 32) this lane's sequence: queries, keys less queries
+  bool alike;        // all sequences are of one length
 
   __device__ __forceinline__ Schedule(const PrefillArgs &args) : a(args), per(2 * args.tokens) {
     lq = shift = 0;
+    alike = !a.offsets || a.n_seq == 1;
     if (a.n_seq <= 32 && (threadIdx.x & 31) < a.n_seq) lengths(threadIdx.x & 31, lq, shift);
+  }
+  __device__ __forceinline__ int tiles_of(int x) const {  // x / per
+    return static_cast<int>(__umulhi(static_cast<uint32_t>(x), a.per_mul) >> a.per_shift);
   }
   __device__ __forceinline__ void lengths(int i, int &queries, int &ahead) const {
     int q0, q1, k0, k1;
@@ -232,10 +278,10 @@ struct Schedule {
   // tiles of a sequence with at least c key tiles: the last query of tile b, at
   // min((b + 1) per, queries) - 1, sees more than 128 (c - 1) keys
   __device__ __forceinline__ int least(int queries, int ahead, int c) const {
-    const int tiles = (queries + per - 1) / per;
+    const int tiles = tiles_of(queries + per - 1);
     const long long from = 128LL * (c - 1) - ahead;
     if (c <= 0 || from < 0) return tiles;
-    return from >= queries ? 0 : tiles - static_cast<int>(from) / per;
+    return from >= queries ? 0 : tiles - tiles_of(static_cast<int>(from));
   }
   // that of the sequence i0 + lane
   __device__ __forceinline__ int mine(int i0, int c) const {
@@ -247,6 +293,11 @@ struct Schedule {
     return least(queries, ahead, c);
   }
   __device__ __forceinline__ long long all(int c) const {
+    if (alike && c == 0) {
+      int queries, ahead;
+      lengths(0, queries, ahead);
+      return static_cast<long long>(tiles_of(queries + per - 1)) * a.n_seq;
+    }
     long long sum = 0;
     for (int i0 = 0; i0 < a.n_seq; i0 += 32) sum += __reduce_add_sync(0xffffffffu, mine(i0, c));
     return sum;
@@ -258,6 +309,16 @@ struct Schedule {
     it.valid = 1;
     it.head = static_cast<int>(n % a.Hk);
     long long left = n / a.Hk;
+    if (alike) {  // the last tiles of all sequences, then those before
+      const int back = static_cast<int>(left / a.n_seq), i = static_cast<int>(left % a.n_seq);
+      int k1;
+      seq_rows(a.offsets, a.n_seq, a.n_q, i, it.q0, it.lq);
+      seq_rows(a.k_offsets, a.n_seq, a.n_k, i, it.k0, k1);
+      it.lq -= it.q0;
+      it.lk = k1 - it.k0;
+      it.t0 = (tiles_of(it.lq + per - 1) - 1 - back) * per;
+      return it;
+    }
     int lo = 0, hi = static_cast<int>((a.n_k + kKeys - 1) / kKeys) + 1;  // all(lo) > left >= all(hi)
     long long behind = 0;
     while (hi - lo > 1) {
@@ -289,7 +350,7 @@ struct Schedule {
         seq_rows(a.k_offsets, a.n_seq, a.n_k, i, it.k0, k1);
         it.lq -= it.q0;
         it.lk = k1 - it.k0;
-        it.t0 = ((it.lq + per - 1) / per - first + nth) * per;
+        it.t0 = (tiles_of(it.lq + per - 1) - first + nth) * per;
         return it;
       }
       left -= __shfl_sync(0xffffffffu, upto, 31);
@@ -303,9 +364,11 @@ struct Schedule {
 // V (blocks of [128 keys][64 columns], 128-byte swizzle), thread e of kN; the first
 // such key of each column is noted in both CTAs.
 template <int D, int kN>
-__device__ __noinline__ void take_out(uint32_t bad, uint32_t v, int e, int rank, int key0, int lk, int base) {
+__device__ __noinline__ void take_out(uint32_t bad, uint32_t flag, uint32_t v, int e, int rank, int key0, int lk, int base) {
   constexpr int kPer = D * 8 / kN;  // 16-byte pieces per thread
   const int r = e & 127;
+  bool wrote = false;
+#pragma unroll 4
   for (int i = 0; i < kPer; ++i) {
     const int at = (e >> 7) * kPer + i;  // piece of the row: block at / 8
     const int piece = (at & 7) ^ (r & 7);
@@ -320,6 +383,7 @@ __device__ __noinline__ void take_out(uint32_t bad, uint32_t v, int e, int rank,
     for (int x = 0; x < 4; ++x)
       hit = hit || (w[x] & 0x7f80u) == 0x7f80u || (w[x] & 0x7f800000u) == 0x7f800000u;
     if (!hit) continue;
+    wrote = true;
     const int c0 = rank * (D / 2) + at * 8;
     for (int x = 0; x < 8; ++x) {
       const uint32_t half = 0xffffu << (16 * (x & 1));
@@ -328,6 +392,7 @@ __device__ __noinline__ void take_out(uint32_t bad, uint32_t v, int e, int rank,
       if (key0 + r >= lk) continue;  // (another sequence's: nobody sees it)
       const uint32_t mark = static_cast<uint32_t>(key0 + r - base);
       for (uint32_t to = 0; to < 2; ++to) {
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_map(flag, to)), "r"(1u) : "memory");
         const uint32_t p = cluster_map(bad + (c0 + x) / 2 * 4, to);
         uint32_t old;
         asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(old) : "r"(p) : "memory");
@@ -349,8 +414,10 @@ __device__ __noinline__ void take_out(uint32_t bad, uint32_t v, int e, int rank,
                  "r"(w[2]), "r"(w[3])
                  : "memory");
   }
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
-  fence_proxy_async_smem();
+  if (wrote) {
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    fence_proxy_async_smem();
+  }
 }
 
 // What the roles derive from an item
@@ -406,6 +473,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
+  if (threadIdx.x < 3) ctl.hit[threadIdx.x] = 0;
   for (int i = static_cast<int>(threadIdx.x); i < 384; i += kThreadsA) ctl.bad[i >> 7][i & 127] = 0xffffffffu;
   // (a misplaced shared memory, which the attribute above excludes, would break the
   // swizzle)
@@ -417,6 +485,15 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   if (warp == 1) {
     tmem_alloc2(smem_u32(&ctl.tmem), kTmemCols);
     tmem_relinquish2();
+  }
+  long long total = 0;
+  if (warp == 10) {  // the first item, meanwhile
+    pdl_wait();
+    const Schedule plan(a);
+    total = plan.all(0) * a.Hk;
+    Item it = {};
+    if ((blockIdx.x >> 1) < total) it = plan.find(blockIdx.x >> 1);
+    if (lane == 0) ctl.item[0] = it;
   }
   tc_fence_before();
   __syncthreads();
@@ -440,19 +517,22 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   if (warp == 10) {
     // ------------------------------------------------------------ schedule
     const Schedule plan(a);
-    const long long clusters = gridDim.x >> 1, c = blockIdx.x >> 1, total = plan.all(0) * a.Hk;
-    for (int k = 0;; ++k) {
-      const long long n = k & 1 ? (k + 1) * clusters - 1 - c : k * clusters + c;
-      Item it = {};
-      if (n < total) it = plan.find(n);
-      if (!warp_wait(a, smem_u32(&ctl.it_empty[k % kItems]), ((k / kItems) & 1) ^ 1, abort_flag, SITE_STAGE)) break;
-      if (lane == 0) {
-        ctl.item[k % kItems] = it;
-        mbar_arrive(smem_u32(&ctl.it_full[k % kItems]));
+    const long long clusters = gridDim.x >> 1, c = blockIdx.x >> 1;
+    if (lane == 0) mbar_arrive(smem_u32(&ctl.it_full[0]));
+    __syncwarp();
+    if (c < total)
+      for (int k = 1;; ++k) {
+        const long long n = k & 1 ? (k + 1) * clusters - 1 - c : k * clusters + c;
+        Item it = {};
+        if (n < total) it = plan.find(n);
+        if (!warp_wait(a, smem_u32(&ctl.it_empty[k % kItems]), ((k / kItems) & 1) ^ 1, abort_flag, SITE_STAGE)) break;
+        if (lane == 0) {
+          ctl.item[k % kItems] = it;
+          mbar_arrive(smem_u32(&ctl.it_full[k % kItems]));
+        }
+        __syncwarp();
+        if (!it.valid) break;
       }
-      __syncwarp();
-      if (!it.valid) break;
-    }
   } else if (warp == 0) {
     // ------------------------------------------------------------ copies
     const uint64_t pol = policy_evict_last();
@@ -622,14 +702,15 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     };
     for (int k = 0; ok && next_item(k, it); ++k) {
       const Tile t(a, it, rank);
-      const uint32_t bad = smem_u32(&ctl.bad[used][0]);
+      const uint32_t bad = smem_u32(&ctl.bad[used][0]), flag = smem_u32(&ctl.hit[used]);
       const int own = max(0, t.mine + t.shift + 1) / kKeys;  // first tile masked for this CTA
+      float f0[2], f1[2];  // factors of the outputs of this thread's two rows there
       // the values of a masked tile
       auto clean = [&](int j) {
         const int s = (base + (j + 1 < t.nk ? 2 * j + 2 : 2 * j + 1)) % P::kSlots;  // V's place in the ring
         if (!warp_wait(a, smem_u32(&ctl.vloc[s]), (vphase >> s) & 1, abort_flag, SITE_MMA_FULL)) return false;
         const int e = static_cast<int>(threadIdx.x) - 64 - (P::kStreams == 2 ? half * 128 : 0);
-        take_out<D, P::kMakers * 32>(bad, ring + s * P::kSlot, e, rank, j * kKeys, it.lk, t.jm * kKeys);
+        take_out<D, P::kMakers * 32>(bad, flag, ring + s * P::kSlot, e, rank, j * kKeys, it.lk, t.jm * kKeys);
         return true;
       };
       auto passed = [&](int j) {  // (every softmax warp follows the phases of the masked tiles' copies)
@@ -698,17 +779,27 @@ __global__ void __launch_bounds__(kThreadsA, 1)
               }
             }
           }
+          const uint64_t c2 = pair_of(c, c), back[2] = {pair_of(-ref[0], -ref[0]), pair_of(-ref[1], -ref[1])};
+          uint64_t sums[2] = {0, 0};
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             uint32_t p[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const int z = i & 1;
-              const float u = fast_exp2(fmaf(x[y][2 * i], c, -ref[z])), w = fast_exp2(fmaf(x[y][2 * i + 1], c, -ref[z]));
-              l[z] += u + w;
+              float u, w;
+              split(fma2(pair_of(x[y][2 * i], x[y][2 * i + 1]), c2, back[i & 1]), u, w);
+              u = fast_exp2(u);
+              w = fast_exp2(w);
+              sums[i & 1] = add2(sums[i & 1], pair_of(u, w));
               p[i] = bf16x2_bits(u, w);
             }
             st_pairs_16x32(ts + 32 * y, p);
+          }
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            float u, w;
+            split(sums[z], u, w);
+            l[z] += u + w;
           }
           wait_st();
           if (j >= t.jm) ok = clean(j);
@@ -716,13 +807,11 @@ __global__ void __launch_bounds__(kThreadsA, 1)
           if (!ok) break;
           made(n);
         }
-        if (ok && t.nk > 0) {
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            l[z] += __shfl_xor_sync(0xffffffffu, l[z], 1);
-            l[z] += __shfl_xor_sync(0xffffffffu, l[z], 2);
-            if ((lane & 3) == 0) ctl.sum[wq * 32 + half * 16 + 8 * z + (lane >> 2)] = l[z];
-          }
+        for (int z = 0; z < 2; ++z) {
+          l[z] += __shfl_xor_sync(0xffffffffu, l[z], 1);
+          l[z] += __shfl_xor_sync(0xffffffffu, l[z], 2);
+          f0[z] = 1.0f / l[z];
         }
       } else {
         const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
@@ -739,24 +828,30 @@ __global__ void __launch_bounds__(kThreadsA, 1)
           ok = warp_wait(a, smem_u32(&ctl.s_full[half]), (n >> 1) & 1, abort_flag, SITE_EPI_TMEM_FULL);
           if (!ok) break;
           tc_fence_after();
-          float x[4][32];
-          tmem_ld32x2_sync(ts, ts + 32, x[0], x[1]);
-          tmem_ld32x2_sync(ts + 64, ts + 96, x[2], x[3]);
-          if (j >= own) {
+          // once for the maximum, once more for P (128 values a thread would not stay in
+          // registers)
+          const bool masked = j >= own;
+          const int hidden = limit - j * kKeys;  // columns past this are masked
+          float top = -INFINITY;
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
+          for (int y = 0; y < kKeys; y += 64) {
+            float x0[32], x1[32];
+            tmem_ld32x2_sync(ts + y, ts + y + 32, x0, x1);
+            if (masked) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (j * kKeys + 32 * y + i > limit) x[y][i] = -INFINITY;
+              for (int i = 0; i < 32; ++i) {
+                if (y + i > hidden) x0[i] = -INFINITY;
+                if (y + 32 + i > hidden) x1[i] = -INFINITY;
+              }
+            }
+            float t4[4] = {x0[0], x0[1], x1[0], x1[1]};
+#pragma unroll
+            for (int i = 2; i < 32; ++i) {
+              t4[i & 1] = fmaxf(t4[i & 1], x0[i]);
+              t4[2 + (i & 1)] = fmaxf(t4[2 + (i & 1)], x1[i]);
+            }
+            top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
           }
-          float top4[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            top4[y] = x[y][0];
-#pragma unroll
-            for (int i = 1; i < 32; ++i) top4[y] = fmaxf(top4[y], x[y][i]);
-          }
-          const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
           if (__any_sync(0xffffffffu, top > m + late)) {
             const float next = top > m + late ? top : m;
             const float f = next == m ? 1.0f : fast_exp2((m - next) * c);
@@ -777,20 +872,34 @@ __global__ void __launch_bounds__(kThreadsA, 1)
               }
             }
           }
-          float l4[4] = {};
+          const uint64_t c2 = pair_of(c, c), back = pair_of(-ref, -ref);
+          uint64_t sums[4] = {0, 0, 0, 0};
 #pragma unroll
-          for (int y = 0; y < 4; y += 2) {
-            uint32_t p[32];
+          for (int y = 0; y < kKeys; y += 32) {  // (P of 32 columns goes over scores that are read)
+            float x[32];
+            uint32_t p[16];
+            tmem_ld32_sync(ts + y, x);
+            if (masked) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float u = fast_exp2(fmaf(x[y + (i >> 4)][2 * (i & 15)], c, -ref));
-              const float w = fast_exp2(fmaf(x[y + (i >> 4)][2 * (i & 15) + 1], c, -ref));
-              l4[i & 3] += u + w;
+              for (int i = 0; i < 32; ++i)
+                if (y + i > hidden) x[i] = -INFINITY;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float u, w;
+              split(fma2(pair_of(x[2 * i], x[2 * i + 1]), c2, back), u, w);
+              u = fast_exp2(u);
+              w = fast_exp2(w);
+              sums[i & 3] = add2(sums[i & 3], pair_of(u, w));
               p[i] = bf16x2_bits(u, w);
             }
-            st_32x32(ts + 16 * y, p);
+            st_32x16(ts + y / 2, p);
           }
-          l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+          {
+            float u, w;
+            split(add2(add2(sums[0], sums[1]), add2(sums[2], sums[3])), u, w);
+            l += u + w;
+          }
           wait_st();
           if (j >= t.jm) ok = clean(j);
           passed(j);
@@ -808,68 +917,92 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         // the one before: its marks make room for the item after the next, whose scores
         // wait for this warp's P of the next.
         const int e = static_cast<int>(threadIdx.x) - 64;
-        if (e < 128) ctl.bad[used == 0 ? 2 : used - 1][e] = 0xffffffffu;
+        const int before = used == 0 ? 2 : used - 1;
+        if (e < 128) ctl.bad[before][e] = 0xffffffffu;
+        if (e == 0) ctl.hit[before] = 0;
       }
-      // the two warps of a TMEM quarter take half of the columns each, a row per thread
-      named_bar_sync(1 + wq, 64);
-      const int row = wq * 32 + lane, at = t.mine + row / a.group, lim = at + t.shift;
-      const bool valid = ok && row < a.tokens * a.group && at < it.lq, any = t.nk > 0 && lim >= 0;
-      // factors of the streams' outputs
-      float f0, f1 = 0.0f;
-      if constexpr (D == 256) {
-        f0 = any ? 1.0f / ctl.sum[row] : 0.0f;
-      } else {
-        const float2 s0 = ctl.stream[0][row], s1 = ctl.stream[1][row];
-        const float M = fmaxf(s0.x, s1.x);
-        f0 = s0.x == M ? 1.0f : fast_exp2((s0.x - M) * c);
-        f1 = s1.x == M ? 1.0f : fast_exp2((s1.x - M) * c);
-        const float inv = any ? 1.0f / (f0 * s0.y + f1 * s1.y) : 0.0f;
-        f0 *= inv;
-        f1 *= inv;
+      // 16 rows per warp, 64 columns at a time (lane l: rows l / 4, + 8); the words of a
+      // quad are turned, so that a lane stores 16 bytes and a row gets 64 at once
+      int row[2], lim[2];
+      bool valid[2], any[2];
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        row[z] = wq * 32 + half * 16 + 8 * z + (lane >> 2);
+        const int at = t.mine + row[z] / a.group;
+        lim[z] = at + t.shift;
+        valid[z] = ok && row[z] < a.tokens * a.group && at < it.lq;
+        any[z] = t.nk > 0 && lim[z] >= 0;
       }
-      __nv_bfloat16 *o = a.out + (static_cast<long long>(it.q0 + at) * a.Hq + it.head * a.group + row % a.group) * D;
-      const int mark = lim - t.jm * kKeys;
+      if constexpr (D == 128) {
+        named_bar_sync(1 + wq, 64);
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const float2 s0 = ctl.stream[0][row[z]], s1 = ctl.stream[1][row[z]];
+          const float M = fmaxf(s0.x, s1.x);
+          f0[z] = s0.x == M ? 1.0f : fast_exp2((s0.x - M) * c);
+          f1[z] = s1.x == M ? 1.0f : fast_exp2((s1.x - M) * c);
+          const float inv = 1.0f / (f0[z] * s0.y + f1[z] * s1.y);
+          f0[z] *= inv;
+          f1[z] *= inv;
+        }
+      }
+      __nv_bfloat16 *o[2];
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+        o[z] = a.out + (static_cast<long long>(it.q0 + t.mine + row[z] / a.group) * a.Hq + it.head * a.group +
+                        row[z] % a.group) * D + 8 * (lane & 3);
+      const bool marked = t.nk > 0 && *static_cast<volatile uint32_t *>(&ctl.hit[used]) != 0;
+      const uint32_t from = P::O + (static_cast<uint32_t>(wq * 32 + half * 16) << 16);
 #pragma unroll 1
-      for (int d = half * (D / 2); ok && d < (half + 1) * (D / 2); d += 32) {
+      for (int d = 0; ok && d < D; d += 64) {
         float v[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = 0.0f;
         if (t.nk > 0) {
-          const uint32_t ta = P::O + (static_cast<uint32_t>(wq * 32) << 16) + d;
           if constexpr (D == 256) {
-            tmem_ld32_sync(ta, v);
+            ld_16x64(from + d, v);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = any ? v[i] * f0 : 0.0f;
+            for (int i = 0; i < 32; ++i) v[i] *= f0[(i >> 1) & 1];
           } else {
-            float w[32];
+            // (with one tile, the other stream's O is another row's)
+            const int first = done & 1;
+            ld_16x64(from + first * D + d, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= first ? f1[(i >> 1) & 1] : f0[(i >> 1) & 1];
             if (t.nk > 1) {
-              tmem_ld32x2_sync(ta, ta + D, v, w);
+              float w[32];
+              ld_16x64(from + (first ^ 1) * D + d, w);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = any ? fmaf(w[i], f1, v[i] * f0) : 0.0f;
-            } else {  // (the other stream's O is another row's)
-              tmem_ld32_sync(ta + (done & 1) * D, v);
-              const float f = done & 1 ? f1 : f0;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = any ? v[i] * f : 0.0f;
+              for (int i = 0; i < 32; ++i) v[i] = fmaf(w[i], first ? f0[(i >> 1) & 1] : f1[(i >> 1) & 1], v[i]);
             }
           }
         }
-        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t first = ctl.bad[used][d / 2 + i];
-          if (mark >= static_cast<int>(first & 0xffffu)) v[2 * i] = __uint_as_float(0x7fffffffu);
-          if (mark >= static_cast<int>(first >> 16)) v[2 * i + 1] = __uint_as_float(0x7fffffffu);
-          w[i] = bf16x2_bits(v[2 * i], v[2 * i + 1]);
+        for (int i = 0; i < 32; ++i) v[i] = any[(i >> 1) & 1] ? v[i] : 0.0f;
+        if (marked) {
+#pragma unroll 1
+          for (int n = 0; n < 8; ++n) {
+            const uint32_t first = ctl.bad[used][d / 2 + 4 * n + (lane & 3)];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const uint32_t key = i & 1 ? first >> 16 : first & 0xffffu;
+              if (i >> 2 == n && lim[(i >> 1) & 1] - t.jm * kKeys >= static_cast<int>(key))
+                v[i] = __uint_as_float(0x7fffffffu);
+            }
+          }
         }
-        if (valid)
 #pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<uint4 *>(o + d + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = bf16x2_bits(v[16 * h + 4 * i + 2 * z], v[16 * h + 4 * i + 2 * z + 1]);
+            turn_quad(w);
+            if (valid[z]) *reinterpret_cast<uint4 *>(o[z] + d + 32 * h) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
       }
       tc_fence_before();
-      // both have read O and the sums before either goes on
-      named_bar_sync(1 + wq, 64);
+      // (D = 128: the streams' sums have been read before either goes on)
+      if (D == 128) named_bar_sync(1 + wq, 64);
       if (t.nk > 0) used = used == 2 ? 0 : used + 1;
       done += t.nk;
       base += 2 * t.nk;
@@ -961,7 +1094,7 @@ extern "C" int moe_attention_prefill(const void *q, const void *k, const void *v
   if (offsets ? (!k_offsets && n_q != n_k) : (n_seq > 0 && (n_q % n_seq != 0 || n_k % n_seq != 0)))
     return MOE_ERR_INVALID_ARG;
   if ((head_dim != 128 && head_dim != 256) || n_q_heads / n_kv_heads > 64 || n_kv_heads > 4096 ||
-      n_q > 0x7fffffffLL || n_k > 0x7fffffffLL)
+      n_q > (1LL << 30) || n_k > (1LL << 30))
     return MOE_ERR_UNSUPPORTED;
   const long long qw = static_cast<long long>(n_q_heads) * head_dim, kw = static_cast<long long>(n_kv_heads) * head_dim;
   if (q_stride < qw || k_stride < kw || v_stride < kw) return MOE_ERR_INVALID_ARG;
@@ -990,6 +1123,12 @@ extern "C" int moe_attention_prefill(const void *q, const void *k, const void *v
   a.tokens = 128 / a.group;
   a.scale = scale * 1.4426950408889634f;
   a.status = dev.status;
+  // x / d = (x m) >> (31 + s), x < 2^31, with 2^(s - 1) < d <= 2^s and m = 2^(31 + s) / d + 1
+  const uint32_t divisor = 2 * a.tokens;
+  uint32_t s = 1;
+  while ((1u << s) < divisor) ++s;
+  a.per_mul = static_cast<uint32_t>((1ULL << (31 + s)) / divisor + 1);
+  a.per_shift = s - 1;
   // tiles of the call, or as many as there can be
   const long long per = 2 * a.tokens;
   const long long tiles = offsets ? n_q / per + n_seq : n_seq * ((n_q / n_seq + per - 1) / per);
