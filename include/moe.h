@@ -455,7 +455,7 @@ int moe_matmul_fp8(const uint8_t *x, const float *x_scales, int T, long long x_s
  * They need no handle and allocate nothing.  Everything is bfloat16 outside
  * and float32 inside; each result is rounded once.  Supported: head_dim 128 or
  * 256, up to 4096 heads of either kind (rotation, cache, decode) and 64 query
- * heads per key/value head (prefill), fewer than 2^31 tokens (prefill: 2^30
+ * heads per key/value head (prefill), fewer than 2^31 tokens (prefill: up to 2^29
  * queries and keys), strides < 2^38.
  * Pointers are device memory, 16-byte aligned (int32 arrays 4, doubles 8);
  * strides, in elements from one token to the next, are multiples of 8, and the

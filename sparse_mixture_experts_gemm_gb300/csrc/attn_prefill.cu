@@ -364,61 +364,62 @@ struct Schedule {
 // V (blocks of [128 keys][64 columns], 128-byte swizzle), thread e of kN; the first
 // such key of each column is noted in both CTAs.
 template <int D, int kN>
-__device__ __noinline__ void take_out(uint32_t bad, uint32_t flag, uint32_t v, int e, int rank, int key0, int lk, int base) {
-  constexpr int kPer = D * 8 / kN;  // 16-byte pieces per thread
-  const int r = e & 127;
-  bool wrote = false;
-#pragma unroll 4
-  for (int i = 0; i < kPer; ++i) {
-    const int at = (e >> 7) * kPer + i;  // piece of the row: block at / 8
-    const int piece = (at & 7) ^ (r & 7);
-    const uint32_t where = v + (at >> 3) * 16384 + r * 128 + piece * 16;
-    uint32_t w[4];
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(where)
-                 : "memory");
-    bool hit = false;
+struct Cleaner {
+  static constexpr int kPer = D * 8 / kN;  // 16-byte pieces per thread, of one row
+  static __device__ __forceinline__ uint32_t where(uint32_t v, int e, int i) {
+    const int r = e & 127, at = (e >> 7) * kPer + i;  // piece of the row: block at / 8
+    return v + (at >> 3) * 16384 + r * 128 + (((at & 7) ^ (r & 7)) << 4);
+  }
+  static __device__ __forceinline__ void clean(uint32_t bad, uint32_t flag, uint32_t v, int e, int rank, int key0,
+                                               int lk, int base) {
+    uint32_t top = 0;  // bit 15 or 31 of a sum: an exponent of ones
+    uint32_t w[kPer][4];
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
-      hit = hit || (w[x] & 0x7f80u) == 0x7f80u || (w[x] & 0x7f800000u) == 0x7f800000u;
-    if (!hit) continue;
-    wrote = true;
-    const int c0 = rank * (D / 2) + at * 8;
-    for (int x = 0; x < 8; ++x) {
-      const uint32_t half = 0xffffu << (16 * (x & 1));
-      if ((w[x >> 1] & half & 0x7f807f80u) != (half & 0x7f807f80u)) continue;
-      w[x >> 1] &= ~half;
-      if (key0 + r >= lk) continue;  // (another sequence's: nobody sees it)
-      const uint32_t mark = static_cast<uint32_t>(key0 + r - base);
-      for (uint32_t to = 0; to < 2; ++to) {
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_map(flag, to)), "r"(1u) : "memory");
-        const uint32_t p = cluster_map(bad + (c0 + x) / 2 * 4, to);
-        uint32_t old;
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(old) : "r"(p) : "memory");
-        for (int tries = 0; tries < 1 << 16; ++tries) {
-          const uint32_t now = (old >> (16 * (x & 1))) & 0xffffu;
-          if (now <= mark) break;
-          const uint32_t want = (old & ~half) | mark << (16 * (x & 1));
-          uint32_t got;
-          asm volatile("atom.shared::cluster.cas.b32 %0, [%1], %2, %3;"
-                       : "=r"(got)
-                       : "r"(p), "r"(old), "r"(want)
-                       : "memory");
-          if (got == old) break;
-          old = got;
+    for (int i = 0; i < kPer; ++i)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                   : "r"(where(v, e, i))
+                   : "memory");
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) top |= (w[i][x] & 0x7f807f80u) + 0x00800080u;
+    if (top & 0x80008000u) take_out(bad, flag, v, e, rank, key0, lk, base);
+  }
+  static __device__ __noinline__ void take_out(uint32_t bad, uint32_t flag, uint32_t v, int e, int rank, int key0,
+                                               int lk, int base) {
+    const int key = key0 + (e & 127);
+    for (int i = 0; i < kPer; ++i)
+      for (int x = 0; x < 8; ++x) {
+        const uint32_t at = where(v, e, i) + 2 * x;
+        uint16_t bits;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(bits) : "r"(at) : "memory");
+        if ((bits & 0x7f80u) != 0x7f80u) continue;
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(0)) : "memory");
+        if (key >= lk) continue;  // (another sequence's: nobody sees it)
+        const int c = rank * (D / 2) + ((e >> 7) * kPer + i) * 8 + x;
+        const uint32_t mark = static_cast<uint32_t>(key - base), shift = 16 * (c & 1);
+        for (uint32_t to = 0; to < 2; ++to) {
+          asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_map(flag, to)), "r"(1u) : "memory");
+          const uint32_t p = cluster_map(bad + c / 2 * 4, to);
+          uint32_t old;
+          asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(old) : "r"(p) : "memory");
+          for (int tries = 0; tries < 1 << 16 && (old >> shift & 0xffffu) > mark; ++tries) {
+            const uint32_t want = (old & ~(0xffffu << shift)) | mark << shift;
+            uint32_t got;
+            asm volatile("atom.shared::cluster.cas.b32 %0, [%1], %2, %3;"
+                         : "=r"(got)
+                         : "r"(p), "r"(old), "r"(want)
+                         : "memory");
+            if (got == old) break;
+            old = got;
+          }
         }
       }
-    }
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(where), "r"(w[0]), "r"(w[1]),
-                 "r"(w[2]), "r"(w[3])
-                 : "memory");
-  }
-  if (wrote) {
     asm volatile("fence.acq_rel.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
-}
+};
 
 // What the roles derive from an item
 struct Tile {
@@ -686,6 +687,16 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     uint32_t vphase = 0, o_phase = 0;
     bool ok = true;
     Item it;
+    // this thread's rows of the outputs (and, with 256 columns, of the scores) as token
+    // and head of the tile
+    int token[2], head[2];
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const int row = wq * 32 + half * 16 + 8 * z + (lane >> 2);
+      token[z] = row < a.tokens * a.group ? row / a.group : 1 << 30;
+      head[z] = row % a.group;
+    }
+    const int mine = wq * 32 + lane < a.tokens * a.group ? (wq * 32 + lane) / a.group : 1 << 30;
     // P of tile n is in TMEM: CTA 0 hears of it
     auto made = [&](int n) {
       tc_fence_before();
@@ -710,7 +721,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         const int s = (base + (j + 1 < t.nk ? 2 * j + 2 : 2 * j + 1)) % P::kSlots;  // V's place in the ring
         if (!warp_wait(a, smem_u32(&ctl.vloc[s]), (vphase >> s) & 1, abort_flag, SITE_MMA_FULL)) return false;
         const int e = static_cast<int>(threadIdx.x) - 64 - (P::kStreams == 2 ? half * 128 : 0);
-        take_out<D, P::kMakers * 32>(bad, flag, ring + s * P::kSlot, e, rank, j * kKeys, it.lk, t.jm * kKeys);
+        Cleaner<D, P::kMakers * 32>::clean(bad, flag, ring + s * P::kSlot, e, rank, j * kKeys, it.lk, t.jm * kKeys);
         return true;
       };
       auto passed = [&](int j) {  // (every softmax warp follows the phases of the masked tiles' copies)
@@ -722,8 +733,8 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         int limit[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int row = wq * 32 + half * 16 + 8 * x + (lane >> 2), at = t.mine + row / a.group;
-          limit[x] = row < a.tokens * a.group && at < it.lq ? min(at + t.shift, it.lk - 1) : -1;
+          const int at = t.mine + token[x];
+          limit[x] = at < it.lq ? min(at + t.shift, it.lk - 1) : -1;
         }
         float m[2] = {-INFINITY, -INFINITY}, ref[2] = {0.0f, 0.0f}, l[2] = {0.0f, 0.0f};
         for (int j = 0; ok && j < t.nk; ++j) {
@@ -815,8 +826,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         }
       } else {
         const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
-        const int row = wq * 32 + lane, at = t.mine + row / a.group;
-        const int limit = row < a.tokens * a.group && at < it.lq ? min(at + t.shift, it.lk - 1) : -1;
+        const int at = t.mine + mine, limit = at < it.lq ? min(at + t.shift, it.lk - 1) : -1;
         float m = -INFINITY, ref = 0.0f, l = 0.0f;
         for (int j = 0; ok && j < t.nk; ++j) {
           const int n = done + j;
@@ -906,7 +916,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
           if (!ok) break;
           made(n);
         }
-        ctl.stream[half][row] = make_float2(m, l);
+        ctl.stream[half][wq * 32 + lane] = make_float2(m, l);
       }
       // ------------------------------------------------------------ outputs
       if (ok && t.nk > 0) {
@@ -923,21 +933,21 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       }
       // 16 rows per warp, 64 columns at a time (lane l: rows l / 4, + 8); the words of a
       // quad are turned, so that a lane stores 16 bytes and a row gets 64 at once
-      int row[2], lim[2];
+      int lim[2];
       bool valid[2], any[2];
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
-        row[z] = wq * 32 + half * 16 + 8 * z + (lane >> 2);
-        const int at = t.mine + row[z] / a.group;
+        const int at = t.mine + token[z];
         lim[z] = at + t.shift;
-        valid[z] = ok && row[z] < a.tokens * a.group && at < it.lq;
+        valid[z] = ok && at < it.lq;
         any[z] = t.nk > 0 && lim[z] >= 0;
       }
       if constexpr (D == 128) {
         named_bar_sync(1 + wq, 64);
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-          const float2 s0 = ctl.stream[0][row[z]], s1 = ctl.stream[1][row[z]];
+          const int row = wq * 32 + half * 16 + 8 * z + (lane >> 2);
+          const float2 s0 = ctl.stream[0][row], s1 = ctl.stream[1][row];
           const float M = fmaxf(s0.x, s1.x);
           f0[z] = s0.x == M ? 1.0f : fast_exp2((s0.x - M) * c);
           f1[z] = s1.x == M ? 1.0f : fast_exp2((s1.x - M) * c);
@@ -949,8 +959,8 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       __nv_bfloat16 *o[2];
 #pragma unroll
       for (int z = 0; z < 2; ++z)
-        o[z] = a.out + (static_cast<long long>(it.q0 + t.mine + row[z] / a.group) * a.Hq + it.head * a.group +
-                        row[z] % a.group) * D + 8 * (lane & 3);
+        o[z] = a.out + (static_cast<long long>(it.q0 + t.mine + (valid[z] ? token[z] : 0)) * a.Hq + it.head * a.group +
+                        head[z]) * D + 8 * (lane & 3);
       const bool marked = t.nk > 0 && *static_cast<volatile uint32_t *>(&ctl.hit[used]) != 0;
       const uint32_t from = P::O + (static_cast<uint32_t>(wq * 32 + half * 16) << 16);
 #pragma unroll 1
@@ -1094,7 +1104,7 @@ extern "C" int moe_attention_prefill(const void *q, const void *k, const void *v
   if (offsets ? (!k_offsets && n_q != n_k) : (n_seq > 0 && (n_q % n_seq != 0 || n_k % n_seq != 0)))
     return MOE_ERR_INVALID_ARG;
   if ((head_dim != 128 && head_dim != 256) || n_q_heads / n_kv_heads > 64 || n_kv_heads > 4096 ||
-      n_q > (1LL << 30) || n_k > (1LL << 30))
+      n_q > (1LL << 29) || n_k > (1LL << 29))
     return MOE_ERR_UNSUPPORTED;
   const long long qw = static_cast<long long>(n_q_heads) * head_dim, kw = static_cast<long long>(n_kv_heads) * head_dim;
   if (q_stride < qw || k_stride < kw || v_stride < kw) return MOE_ERR_INVALID_ARG;
