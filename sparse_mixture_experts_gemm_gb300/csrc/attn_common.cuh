@@ -71,6 +71,26 @@ __device__ __forceinline__ long long cache_row(const CacheArgs &c, int page, int
   return ((static_cast<long long>(page) * 2 + which) * c.H + h) * kPage + place;
 }
 
+// two fp32 values side by side
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t p, float &a, float &b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // one launch as a programmatic dependent of the kernel before it
 template <typename K, typename... Args>
 cudaError_t launch_attn(K kern, dim3 grid, int threads, int smem, cudaStream_t st, Args... args) {

@@ -9,8 +9,7 @@
 // from halves.  A group that holds a NaN or an infinity has scale and bias NaN
 // and reads back as NaN.
 //
-// Bound by memory, 2.56 bytes moved per column.  8 columns per lane: one 16-byte
-// vector of keys or values, one word of codes.
+// Bound by memory, 2.56 bytes moved per column, and by instructions: see the kernels.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -24,6 +23,9 @@ namespace moe {
 namespace {
 
 constexpr int kKvWarps = 4;
+constexpr int kBatch = 2;  // rows of a lane in flight (1: 1 us more for 16,384 tokens of 2 heads of 256 written, 4: 1.5)
+// the sum of 0x4b400000 << 4 e, the bits of 2^23 + 2^22, modulo 2^32
+constexpr uint32_t kMagicBits = 0x3f400000u;
 
 struct KvArgs {
   CacheArgs c;
@@ -31,90 +33,189 @@ struct KvArgs {
   __nv_bfloat16 *ko, *vo;
   const int *starts, *offsets;
   long long n_tokens, ks, vs;
-  int n_seq;
+  int n_seq, tokens;  // tokens: of a block, up to 32
+  float per_rows;     // 1 / (2 H)
 };
+
+// row r of a block (below 2^21) is row x of token t
+__device__ __forceinline__ void split_row(const KvArgs &a, int r, int &t, int &x) {
+  t = static_cast<int>((static_cast<float>(r) + 0.5f) * a.per_rows);
+  x = r - t * 2 * a.c.H;
+}
 
 __device__ __forceinline__ void bad_page(const CacheArgs &c) {
   report_error(c.status, MOE_ERR_DEVICE_BOUNDS, KID_KV_CACHE * 100 + SITE_INDEX);
 }
 
-// page and place of token t (the whole warp); false: none
-__device__ __forceinline__ bool slot_of(const KvArgs &a, int t, int &page, int &place) {
-  const int i = seq_of_row(a.offsets, a.n_seq, a.n_tokens, t);
-  if (i < 0) return false;
-  int lo, hi;
-  seq_rows(a.offsets, a.n_seq, a.n_tokens, i, lo, hi);
-  const long long at = static_cast<long long>(a.starts ? a.starts[i] : 0) + t - lo;
-  page = page_of(a.c, i, at);
-  place = static_cast<int>(at & (kPage - 1));
-  return true;
+// Where the tokens of a block are, by its first warp, one token per lane: page (-1:
+// outside the cache, -2: a token of no sequence) and place.
+__device__ __forceinline__ void find_slots(const KvArgs &a, long long t0, int (&page)[32], int (&place)[32]) {
+  const int lane = threadIdx.x;
+  if (lane >= 32) return;
+  const long long t = t0 + lane;
+  int pg = -2, pl = 0;
+  if (lane < a.tokens && t < a.n_tokens) {
+    int i = -1;
+    if (a.offsets) {  // the last sequence that starts at or before t, unless it has ended
+      int lo = 0, hi = a.n_seq;  // offsets[lo - 1] <= t < offsets[hi]
+      while (lo < hi) {
+        const int mid = lo + (hi - lo) / 2;
+        if (a.offsets[mid] <= t) {
+          lo = mid + 1;
+        } else {
+          hi = mid;
+        }
+      }
+      if (lo > 0 && a.offsets[lo] > t) i = lo - 1;
+    } else {
+      i = static_cast<int>(t) / static_cast<int>(a.n_tokens / a.n_seq);
+    }
+    if (i >= 0) {
+      int q0, q1;
+      seq_rows(a.offsets, a.n_seq, a.n_tokens, i, q0, q1);
+      const long long at = static_cast<long long>(a.starts ? a.starts[i] : 0) + t - q0;
+      pg = page_of(a.c, i, at);
+      pl = static_cast<int>(at & (kPage - 1));
+      if (pg < 0) bad_page(a.c);
+    }
+  }
+  page[lane] = pg;
+  place[lane] = pl;
 }
 
 }  // namespace
 
-// A warp per token: its 2 H rows of keys and values, 32 lanes over 256 columns.
+namespace {
+
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+}  // namespace
+
+// A block has a.tokens tokens: 2 H rows of keys and values each, kBatch rows of a
+// lane in flight, 16 columns per lane.
 template <int D>
 __global__ void __launch_bounds__(kKvWarps * 32) kv_write_kernel(const KvArgs a) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+  __shared__ int s_page[32], s_place[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
-  const long long t = static_cast<long long>(blockIdx.x) * kKvWarps + warp;
-  if (t >= a.n_tokens) return;
-  int page, place;
-  if (!slot_of(a, static_cast<int>(t), page, place)) return;
-  if (page < 0) {
-    if (lane == 0) bad_page(a.c);
-    return;
-  }
-  const int sub = lane / kLanes, c = lane % kLanes * 8, H = a.c.H;
-  for (int r0 = 0; r0 < 2 * H; r0 += kRows) {
-    const int r = min(r0 + sub, 2 * H - 1), which = r >= H, h = r - which * H;
-    const __nv_bfloat16 *src = (which ? a.v + t * a.vs : a.k + t * a.ks) + h * D + c;
-    const uint4 u = *reinterpret_cast<const uint4 *>(src);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    float x[8];
+  const long long t0 = static_cast<long long>(blockIdx.x) * a.tokens;
+  const int H = a.c.H, c = lane % kLanes * 16;
+  const int rows = 2 * H * static_cast<int>(min(static_cast<long long>(a.tokens), a.n_tokens - t0));
+  auto source = [&](int r) {
+    int t, x;
+    split_row(a, r, t, x);
+    return c + (x >= H ? a.v + (t0 + t) * a.vs + (x - H) * D : a.k + (t0 + t) * a.ks + x * D);
+  };
+  uint4 u[kBatch][2];
+  auto fetch = [&](int r0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int b = 0; b < kBatch; ++b) {
+      const int r = r0 + b * kRows;
+      u[b][0] = u[b][1] = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(source(r));
+        u[b][0] = src[0];
+        u[b][1] = src[1];
+      }
     }
-    float lo = x[0], hi = x[0];
-    bool fin = true;
+  };
+  const int mine = warp * kBatch * kRows + lane / kLanes;  // this lane's first row
+  fetch(mine);
+  find_slots(a, t0, s_page, s_place);
+  __syncthreads();
+  // (all lanes stay in the loop: the rows of a warp are of one count)
+  for (int r0 = mine; r0 - lane / kLanes < rows; r0 += kKvWarps * kBatch * kRows) {
+    if (r0 != mine) fetch(r0);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      lo = fminf(lo, x[e]);
-      hi = fmaxf(hi, x[e]);
-      fin = fin && fabsf(x[e]) <= 3.402823466e38f;
-    }
+    for (int b = 0; b < kBatch; ++b) {
+      const int r = r0 + b * kRows;
+      if (r - lane / kLanes >= rows) break;  // (the whole warp)
+      const uint32_t w[8] = {u[b][0].x, u[b][0].y, u[b][0].z, u[b][0].w,
+                             u[b][1].x, u[b][1].y, u[b][1].z, u[b][1].w};
+      // smallest and largest of the group's 64 columns; a NaN among them stays
+      uint32_t least = w[0], most = w[0];
 #pragma unroll
-    for (int o = 4; o; o >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
-    const uint32_t all = __ballot_sync(0xffffffffu, fin);
-    fin = ((all >> (lane & 24)) & 255u) == 255u;  // the group's eight lanes
-    // halves where the range leaves fp32
-    const float f = hi - lo > 3.402823466e38f ? 0.5f : 1.0f;
-    __nv_bfloat16 bias = __float2bfloat16_rn(lo);
-    __nv_bfloat16 scale = __float2bfloat16_rn(__fdiv_rn(hi * f - lo * f, 15.0f * f));
-    const float s = __bfloat162float(scale), b = __bfloat162float(bias);
-    uint32_t code = 0;
+      for (int i = 1; i < 8; ++i) {
+        least = min2(least, w[i]);
+        most = max2(most, w[i]);
+      }
+      // the two halves: (least, - most), whose least over the group's lanes is sought
+      const uint32_t flip = most ^ 0x80008000u;
+      uint32_t both = min2(__byte_perm(least, flip, 0x5410), __byte_perm(least, flip, 0x7632));
+      both = min2(both, __shfl_xor_sync(0xffffffffu, both, 2));
+      both = min2(both, __shfl_xor_sync(0xffffffffu, both, 1));
+      const float lo = __uint_as_float(both << 16), hi = -__uint_as_float(both & 0xffff0000u);
+      const bool finite = fabsf(lo) <= 3.402823466e38f && fabsf(hi) <= 3.402823466e38f;
+      // halves where the range leaves fp32
+      const float f = hi - lo > 3.402823466e38f ? 0.5f : 1.0f;
+      const __nv_bfloat16 scale = __float2bfloat16_rn(__fdiv_rn(hi * f - lo * f, 15.0f * f));
+      const float s = __bfloat162float(scale);
+      // A code is the quotient (x - bias) / scale, rounded to even.  Two estimates of it,
+      // a little more and a little less than the quotient, are rounded: by the sum with
+      // 2^23 + 2^22, which leaves the code in the low bits.  Where they agree, that is
+      // the code.  (1 / scale is within 2^-22 of itself, so that 2^-20 more and less
+      // enclose the quotient as divided; where scale has no such reciprocal or the range
+      // was halved, none is taken to agree.)  Else the quotient itself is formed:
+      // one code in some hundreds, as values of 8 bits often fall between two codes.
+      const float inv = __fdividef(1.0f, s), top = 15.0f * s;
+      const uint64_t less = pair_of(-lo, -lo), magic = pair_of(12582912.0f, 12582912.0f);
+      const float up = inv * (1.0f + 0x1p-20f), down = inv * (1.0f - 0x1p-20f);
+      const uint64_t up2 = pair_of(up, up), down2 = pair_of(down, down);
+      const bool plain = s > 0x1p-100f && s < 0x1p100f && f == 1.0f;
+      uint32_t code[2] = {0, 0};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float y = s == 0.0f ? 0.0f : rintf(__fdiv_rn(x[e] * f - b * f, s * f));
-      code |= static_cast<uint32_t>(fminf(fmaxf(y, 0.0f), 15.0f)) << (4 * e);
-    }
-    uint32_t pair = static_cast<uint32_t>(__bfloat16_as_ushort(scale)) |
-                    static_cast<uint32_t>(__bfloat16_as_ushort(bias)) << 16;
-    if (!fin) {
-      code = 0;
-      pair = 0x7fff7fffu;
-    }
-    if (r0 + sub < 2 * H) {
-      const long long row = cache_row(a.c, page, which, h, place);
-      *reinterpret_cast<uint32_t *>(a.c.codes + row * (D / 2) + c / 2) = code;
-      if ((lane & 7) == 0) a.c.affine[row * (D / kGroup) + c / kGroup] = pair;
+      for (int z = 0; z < 2; ++z) {
+        uint32_t low = 0;
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+          const uint32_t v = w[z * 4 + i];
+          float y0, y1, m0, m1;
+          split(add2(pair_of(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)), less), y0, y1);
+          const uint64_t y = pair_of(fminf(y0, top), fminf(y1, top));
+          split(fma2(y, up2, magic), m0, m1);
+          code[z] = (code[z] * 16 + __float_as_uint(m1)) * 16 + __float_as_uint(m0);
+          split(fma2(y, down2, magic), m0, m1);
+          low = (low * 16 + __float_as_uint(m1)) * 16 + __float_as_uint(m0);
+        }
+        code[z] -= kMagicBits;
+        uint32_t open = plain ? code[z] ^ (low - kMagicBits) : 0xffffffffu;
+        while (open) {
+          const int e = (__ffs(open) - 1) / 4;
+          const uint32_t v0 = e & 2 ? w[z * 4 + 1] : w[z * 4], v1 = e & 2 ? w[z * 4 + 3] : w[z * 4 + 2];
+          const uint32_t v = e & 4 ? v1 : v0;
+          const float y = __uint_as_float(e & 1 ? v & 0xffff0000u : v << 16) * f - lo * f;
+          const float quot = s == 0.0f ? 0.0f : __fdiv_rn(y, s * f);
+          const uint32_t n = static_cast<uint32_t>(fminf(rintf(quot), 15.0f)), nibble = 15u << (4 * e);
+          code[z] = (code[z] & ~nibble) | n << (4 * e);
+          open &= ~nibble;
+        }
+      }
+      uint32_t pair = static_cast<uint32_t>(__bfloat16_as_ushort(scale)) | both << 16;
+      if (!finite) {
+        code[0] = code[1] = 0;
+        pair = 0x7fff7fffu;
+      }
+      if (r < rows) {
+        int t, y;
+        split_row(a, r, t, y);
+        const int which = y >= H, page = s_page[t];
+        if (page >= 0) {
+          const long long row = cache_row(a.c, page, which, y - which * H, s_place[t]);
+          *reinterpret_cast<uint2 *>(a.c.codes + row * (D / 2) + c / 2) = make_uint2(code[0], code[1]);
+          if ((lane & 3) == 0) a.c.affine[row * (D / kGroup) + c / kGroup] = pair;
+        }
+      }
     }
   }
 }
@@ -122,34 +223,63 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_write_kernel(const KvArgs a)
 template <int D>
 __global__ void __launch_bounds__(kKvWarps * 32) kv_read_kernel(const KvArgs a) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  __shared__ int s_page[32], s_place[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
-  const long long t = static_cast<long long>(blockIdx.x) * kKvWarps + warp;
-  if (t >= a.n_tokens) return;
-  int page, place;
-  if (!slot_of(a, static_cast<int>(t), page, place)) return;
-  if (page < 0 && lane == 0) bad_page(a.c);
-  const int sub = lane / kLanes, c = lane % kLanes * 8, H = a.c.H;
-  for (int r = sub; r < 2 * H; r += kRows) {
-    const int which = r >= H, h = r - which * H;
-    uint32_t code = 0, pair = 0;
-    if (page >= 0) {
-      const long long row = cache_row(a.c, page, which, h, place);
-      code = *reinterpret_cast<const uint32_t *>(a.c.codes + row * (D / 2) + c / 2);
-      pair = a.c.affine[row * (D / kGroup) + c / kGroup];
-    }
-    const float s = __uint_as_float(pair << 16), b = __uint_as_float(pair & 0xffff0000u);
-    float x[8];
+  const long long t0 = static_cast<long long>(blockIdx.x) * a.tokens;
+  const int H = a.c.H, c = lane % kLanes * 8;
+  const int rows = 2 * H * static_cast<int>(min(static_cast<long long>(a.tokens), a.n_tokens - t0));
+  find_slots(a, t0, s_page, s_place);
+  __syncthreads();
+  for (int r0 = warp * kBatch * kRows + lane / kLanes; r0 < rows; r0 += kKvWarps * kBatch * kRows) {
+    uint32_t code[kBatch], pair[kBatch];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = fmaf(s, static_cast<float>(code >> (4 * e) & 15u), b);
-    __nv_bfloat16 *o = (which ? a.vo : a.ko) + (t * H + h) * D + c;
-    *reinterpret_cast<uint4 *>(o) = make_uint4(bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3]),
-                                               bf16x2_bits(x[4], x[5]), bf16x2_bits(x[6], x[7]));
+    for (int b = 0; b < kBatch; ++b) {
+      const int r = r0 + b * kRows;
+      code[b] = pair[b] = 0;
+      if (r < rows) {
+        int t, y;
+        split_row(a, r, t, y);
+        const int which = y >= H, page = s_page[t];
+        if (page >= 0) {
+          const long long row = cache_row(a.c, page, which, y - which * H, s_place[t]);
+          code[b] = *reinterpret_cast<const uint32_t *>(a.c.codes + row * (D / 2) + c / 2);
+          pair[b] = a.c.affine[row * (D / kGroup) + c / kGroup];
+        }
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int r = r0 + b * kRows;
+      if (r >= rows) break;
+      int t, y;
+      split_row(a, r, t, y);
+      const int which = y >= H;
+      if (s_page[t] == -2) continue;
+      const float s = __uint_as_float(pair[b] << 16), z = __uint_as_float(pair[b] & 0xffff0000u);
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)  // 2^23 + code, less 2^23: a conversion at the rate of sums
+        x[e] = fmaf(s, __uint_as_float((code[b] >> (4 * e) & 15u) | 0x4b000000u) - 8388608.0f, z);
+      __nv_bfloat16 *o = (which ? a.vo : a.ko) + ((t0 + t) * H + y - which * H) * D + c;
+      *reinterpret_cast<uint4 *>(o) = make_uint4(bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3]),
+                                                 bf16x2_bits(x[4], x[5]), bf16x2_bits(x[6], x[7]));
+    }
   }
 }
 
 namespace {
+
+// Tokens of a block: as many as its warps have rows in flight for in two rounds, if
+// that leaves two blocks per SM.
+int block_tokens(long long n_tokens, int H, int D) {
+  const int rows = 2 * kKvWarps * kBatch * (256 / D), fit = rows / (2 * H);
+  const long long spread = n_tokens / (2 * 152);
+  long long t = fit < spread ? fit : spread;
+  t = t < 1 ? 1 : t;
+  return static_cast<int>(t > 32 ? 32 : t);
+}
 
 // the checks that write and read share; MOE_OK with n_tokens or n_seq 0 is "nothing to do"
 int check_kv(const void *codes, const void *affine, long long n_pages, const int32_t *pages,
@@ -200,7 +330,9 @@ extern "C" int moe_kv_write(uint8_t *codes, uint16_t *affine, long long n_pages,
   a.ks = k_stride;
   a.vs = v_stride;
   a.n_seq = n_seq;
-  const dim3 grid(static_cast<unsigned>((n_tokens + kKvWarps - 1) / kKvWarps));
+  a.tokens = block_tokens(n_tokens, n_heads, head_dim);
+  a.per_rows = 1.0f / (2.0f * static_cast<float>(n_heads));
+  const dim3 grid(static_cast<unsigned>((n_tokens + a.tokens - 1) / a.tokens));
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const cudaError_t e = head_dim == 128 ? launch_attn(kv_write_kernel<128>, grid, kKvWarps * 32, 0, st, a)
                                         : launch_attn(kv_write_kernel<256>, grid, kKvWarps * 32, 0, st, a);
@@ -225,7 +357,9 @@ extern "C" int moe_kv_read(const uint8_t *codes, const uint16_t *affine, long lo
   a.offsets = offsets;
   a.n_tokens = n_tokens;
   a.n_seq = n_seq;
-  const dim3 grid(static_cast<unsigned>((n_tokens + kKvWarps - 1) / kKvWarps));
+  a.tokens = block_tokens(n_tokens, n_heads, head_dim);
+  a.per_rows = 1.0f / (2.0f * static_cast<float>(n_heads));
+  const dim3 grid(static_cast<unsigned>((n_tokens + a.tokens - 1) / a.tokens));
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
   const cudaError_t e = head_dim == 128 ? launch_attn(kv_read_kernel<128>, grid, kKvWarps * 32, 0, st, a)
                                         : launch_attn(kv_read_kernel<256>, grid, kKvWarps * 32, 0, st, a);
