@@ -51,6 +51,11 @@ def _offsets(name, t):
     return t.shape[0] - 1, t.data_ptr()
 
 
+def _empty(t):
+    """An output of t's shape, contiguous."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=_BF16, device=t.device)
+
+
 def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, q_out=None, k_out=None,
                  stream=None):
     """moe_qk_norm_rope: norm of every head's row of q [..., H_q, D] and
@@ -59,8 +64,9 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, q_out=
     float64 [R / 2], radians per position (None: no rotation, positions unused).
     Returns (q, k); q_out may be q and k_out may be k."""
     N, Hq, D = _heads("q", q)
-    Nk, Hk, Dk = _heads("k", k)
-    if Dk != D or k.shape[:-2] != q.shape[:-2]:
+    Hk = k.shape[-2] if k.dim() > 1 else 0
+    lead = q.shape[:-2]
+    if Hk == 0 or k.shape[-1] != D or k.shape[:-2] != lead:
         raise ValueError("shapes of q and k do not agree")
     qs, ks = _stride("q", q, Hq, D), _stride("k", k, Hk, D)
     _vector("q_weight", q_weight, D, _BF16)
@@ -70,17 +76,23 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, q_out=
         _vector("inv_freq", inv_freq, inv_freq.numel(), torch.float64)
         rot = 2 * inv_freq.shape[0]
         if rot:
-            _given("positions", positions, q.shape[:-2], _I32)
+            _given("positions", positions, lead, _I32)
             pp, fp = positions.data_ptr(), inv_freq.data_ptr()
     ctx, handle = _on(stream, _device(q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out))
+    qos, kos = Hq * D, Hk * D
     with ctx:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=_BF16, device=q.device)
+            q_out = _empty(q)
+        elif q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+        else:
+            qos = _stride("q_out", q_out, Hq, D)
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=_BF16, device=k.device)
-    if q_out.shape != q.shape or k_out.shape != k.shape:
-        raise ValueError("q_out and k_out must have the shapes of q and k")
-    qos, kos = _stride("q_out", q_out, Hq, D), _stride("k_out", k_out, Hk, D)
+            k_out = _empty(k)
+        elif k_out.shape != k.shape:
+            raise ValueError("k_out must have the shape of k")
+        else:
+            kos = _stride("k_out", k_out, Hk, D)
     _check(_lib().moe_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_weight.data_ptr(), k_weight.data_ptr(), pp, fp,
                                    N, Hq, Hk, D, rot, qs, ks, eps, q_out.data_ptr(), qos, k_out.data_ptr(), kos,
                                    handle), "moe_qk_norm_rope")
@@ -120,7 +132,7 @@ def attention_prefill(q, k, v, offsets=None, k_offsets=None, scale=None, out=Non
     ctx, handle = _on(stream, _device(q, k, v, offsets, k_offsets, out))
     if out is None:
         with ctx:
-            out = torch.empty(q.shape, dtype=_BF16, device=q.device)
+            out = _empty(q)
     else:
         _given("out", out, q.shape, _BF16)
     _check(_lib().moe_attention_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), op, kp, N, M, n, Hq, Hk, D, qs,
@@ -199,10 +211,12 @@ def kv_cache_read(cache, pages, offsets, tokens, starts=None, k_out=None, v_out=
     with ctx:
         if k_out is None:
             k_out = torch.empty(shape, dtype=_BF16, device=codes.device)
+        else:
+            _given("k_out", k_out, shape, _BF16)
         if v_out is None:
             v_out = torch.empty(shape, dtype=_BF16, device=codes.device)
-    _given("k_out", k_out, shape, _BF16)
-    _given("v_out", v_out, shape, _BF16)
+        else:
+            _given("v_out", v_out, shape, _BF16)
     _check(_lib().moe_kv_read(codes.data_ptr(), affine.data_ptr(), P, pages.data_ptr(), width,
                               None if starts is None else starts.data_ptr(), op, tokens, n, H, D,
                               k_out.data_ptr(), v_out.data_ptr(), handle), "moe_kv_read")
@@ -233,7 +247,7 @@ def attention_decode(q, cache, pages, lengths, scale=None, out=None, stream=None
     ctx, handle = _on(stream, _device(q, codes, affine, pages, lengths, out))
     with ctx:
         if out is None:
-            out = torch.empty(q.shape, dtype=_BF16, device=q.device)
+            out = _empty(q)
         else:
             _given("out", out, q.shape, _BF16)
         ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
