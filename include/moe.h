@@ -369,7 +369,9 @@ int moe_decode_noalloc(const moe_config *cfg, const void *x, void *out, void *cu
 /*
  * Synchronise cuda_stream, then return and clear the device status word of
  * the calls without a handle that have waits in their kernels
- * (moe_decode_noalloc, moe_matmul_fp8, gdn_decay_scan) on the current device: MOE_OK, MOE_ERR_DEVICE_TIMEOUT or
+ * (moe_decode_noalloc, moe_matmul_fp8, gdn_decay_scan, moe_attention_prefill,
+ * moe_attention_decode) or that find a bad page (moe_kv_write, moe_kv_read,
+ * moe_attention_decode) on the current device: MOE_OK, MOE_ERR_DEVICE_TIMEOUT or
  * MOE_ERR_DEVICE_BOUNDS, the first device-side failure of any call since the
  * last read.  If detail != NULL it receives the library-defined code of the
  * kernel and wait that failed (0 when none).  Allocates nothing; like
@@ -455,8 +457,9 @@ int moe_matmul_fp8(const uint8_t *x, const float *x_scales, int T, long long x_s
  * They need no handle and allocate nothing.  Everything is bfloat16 outside
  * and float32 inside; each result is rounded once.  Supported: head_dim 128 or
  * 256, up to 4096 heads of either kind (rotation, cache, decode) and 64 query
- * heads per key/value head (prefill), fewer than 2^31 tokens (prefill: up to 2^29
- * queries and keys), strides < 2^38.
+ * heads per key/value head (prefill), fewer than 2^31 tokens (prefill: 2^29 queries
+ * and keys at most; decode: n_seq * table_width * n_kv_heads times the eights of query
+ * heads that share one, rounded up, below 2^31), strides < 2^38.
  * Pointers are device memory, 16-byte aligned (int32 arrays 4, doubles 8);
  * strides, in elements from one token to the next, are multiples of 8, and the
  * heads of a token lie side by side.  Asynchronous on cuda_stream; the checks

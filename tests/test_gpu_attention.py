@@ -648,3 +648,145 @@ def test_refuses_tensors_of_other_types(dev):
             call()
     with pytest.raises(moe.MoeError):
         moe.attention_prefill(q[..., :64].contiguous(), k[..., :64].contiguous(), k[..., :64].contiguous())
+
+
+# ------------------------------------------------------------ further cases
+@pytest.mark.parametrize("H,D,starts,lens", [(1, 128, [5, 0, 40], [9000, 1, 4000]), (3, 256, [0], [7000]),
+                                             (5, 128, [0, 64], [2500, 700]), (40, 256, [3], [130])])
+def test_cache_long(dev, H, D, starts, lens):
+    """Blocks of several tokens, of one sequence and across the end of one."""
+    test_cache_write_and_read(dev, H, D, starts, lens)
+
+
+@pytest.mark.parametrize("e", [-120, -60, -9, 0, 60, 119])
+def test_cache_codes_on_borders(dev, e):
+    """Multiples of 2^e, many of which lie exactly between two codes (those round to
+    the even one): differences, scales and those borders are exact in fp32."""
+    g = gen(e + 200)
+    span = torch.randint(1, 8, (300, 2, 2, 1), generator=g) * 30  # scale 2, 4, .. times 2^e
+    x = (torch.rand(300, 2, 2, 64, generator=g) * (span + 1)).floor().clamp(max=span)
+    x[..., :1], x[..., 1:2] = torch.zeros_like(span, dtype=x.dtype), span.to(x.dtype)
+    x = ((x - (span // 2)).double() * 2.0 ** e).to(BF16).flatten(2)
+    cache = moe.kv_cache(5, 2, 128, dev)
+    table = torch.tensor([[4, 1, 0, 2, 3]], dtype=I32)
+    moe.kv_cache_write(cache, x.to(dev), -x.to(dev), table.to(dev))
+    codes, affine = rows_of(cache, table, 0, 0, 300)
+    for w, y in enumerate((x, -x)):
+        c, s, b = oracle.quantise(f64(y))
+        assert np.array_equal(oracle.unpack(codes[:, w].numpy()), c)
+        assert np.array_equal(f64(affine[:, w, ..., 0]), s) and np.array_equal(f64(affine[:, w, ..., 1]), b)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_powers_of_two_pass_through(dev, D):
+    """Values times 2^j give results times 2^j; queries times 2^j with keys by 2^-j
+    change nothing: no sum or part of it has a range of its own."""
+    g = gen(D + 1)
+    q, k, v = (x.to(dev) for x in prefill_inputs(D + 2, 200, 200, 4, 2, D))
+    ref = moe.attention_prefill(q, k, v)
+    lens = [150, 700]
+    table, P = make_table(g, lens)
+    codes, affine = random_cache(g, P, 2, D, dev)
+    qd, td, L = normal(g, 2, 8, D).to(dev), table.to(dev), torch.tensor(lens, dtype=I32, device=dev)
+    want = moe.attention_decode(qd, (codes, affine), td, L)
+    for j in (-80, -30, 30, 80):
+        f = 2.0 ** j
+        assert torch.equal(moe.attention_prefill(q, k, v * f), ref * f)
+        assert torch.equal(moe.attention_prefill(q * f, k / f, v), ref)
+        a = affine.clone()
+        a[:, 1] *= f
+        assert torch.equal(moe.attention_decode(qd, (codes, a), td, L), want * f)
+        a = affine.clone()
+        a[:, 0] /= f
+        assert torch.equal(moe.attention_decode(qd * f, (codes, a), td, L), want)
+
+
+def test_prefill_dense_behind_a_prefix(dev):
+    """[n][T] queries over [n][M] keys: what packed ones give; also T > M."""
+    for T, M in ((33, 170), (1, 90), (90, 40)):
+        q, _, _ = prefill_inputs(T, 3 * T, 1, 8, 2, 128)
+        _, k, v = prefill_inputs(M, 1, 3 * M, 8, 2, 128)
+        a, b, c = q.to(dev), k.to(dev), v.to(dev)
+        got = moe.attention_prefill(*(x.unflatten(0, (3, -1)) for x in (a, b, c)))
+        assert torch.equal(got.flatten(0, 1), moe.attention_prefill(a, b, c, ends([T] * 3, dev), ends([M] * 3, dev)))
+
+
+@pytest.mark.parametrize("D,Hq", [(128, 8), (256, 16)])
+def test_prefill_leaves_rows_of_no_sequence(dev, D, Hq):
+    """Rows before the first and behind the last sequence, next to tiles that are not full."""
+    q, k, v = (x.to(dev) for x in prefill_inputs(D, 300, 400, Hq, 2, D))
+    oq = torch.tensor([7, 50, 50, 203], dtype=I32, device=dev)
+    ok = torch.tensor([3, 100, 101, 390], dtype=I32, device=dev)
+    out = torch.full_like(q, 7.0)
+    moe.attention_prefill(q, k, v, oq, ok, out=out)
+    assert (out[:7] == 7).all() and (out[203:] == 7).all()
+    assert torch.equal(out[7:50], moe.attention_prefill(q[7:50], k[3:100], v[3:100]))
+    assert torch.equal(out[50:203], moe.attention_prefill(q[50:203], k[101:390], v[101:390]))
+
+
+def test_decode_shared_pages(dev):
+    """Sequences whose first pages are the same ones, and one in the table twice."""
+    g = gen(21)
+    cache = random_cache(g, 9, 2, 256, dev)
+    table = torch.tensor([[3, 1, 7, 0], [3, 1, 8, 2], [3, 1, 7, 0], [4, 4, 4, 4]], dtype=I32)
+    lens = [250, 190, 130, 200]
+    q = normal(g, 4, 16, 256)
+    got = moe.attention_decode(q.to(dev), cache, table.to(dev), torch.tensor(lens, dtype=I32, device=dev))
+    check_decode(got, q, cache, table, lens, 256 ** -0.5)
+
+
+def test_decode_more_rows_than_shares(dev):
+    g = gen(22)
+    lens = torch.randint(1, 140, (700,), generator=g).tolist()
+    table, P = make_table(g, lens)
+    cache = random_cache(g, P, 2, 128, dev)
+    q = normal(g, len(lens), 20, 128)  # 10 query heads a key/value head: rows of 8 and of 2
+    got = moe.attention_decode(q.to(dev), cache, table.to(dev), torch.tensor(lens, dtype=I32, device=dev))
+    check_decode(got, q, cache, table, lens, 128 ** -0.5)
+
+
+def test_nothing_to_do(dev):
+    e = lambda *shape: torch.zeros(*shape, dtype=BF16, device=dev)  # noqa: E731
+    i = lambda *shape: torch.zeros(*shape, dtype=I32, device=dev)  # noqa: E731
+    cache = moe.kv_cache(2, 2, 128, dev)
+    assert moe.attention_prefill(e(0, 4, 128), e(0, 2, 128), e(0, 2, 128), i(3)).shape == (0, 4, 128)
+    assert not moe.attention_prefill(e(5, 4, 128) + 1, e(0, 2, 128), e(0, 2, 128)).any()
+    assert moe.attention_decode(e(0, 4, 128), cache, i(0, 3), i(0)).shape == (0, 4, 128)
+    assert not moe.attention_decode(e(3, 4, 128) + 1, cache, i(3, 0), i(3)).any()
+    assert moe.kv_cache_read(cache, i(0, 1), i(1), 0)[0].shape == (0, 2, 128)
+    moe.kv_cache_write(cache, e(0, 2, 128), e(0, 2, 128), i(1, 2))
+    assert moe.qk_norm_rope(e(0, 4, 128), e(0, 2, 128), e(128), e(128), None, None)[1].shape == (0, 2, 128)
+
+
+def test_calls_at_once_on_two_streams(dev):
+    """Both operators on two streams at a time: each call has its own workspace."""
+    g = gen(23)
+    work = []
+    for i in range(2):
+        lens = [3000 + 500 * i, 70, 1, 900]
+        table, P = make_table(g, lens)
+        cache = random_cache(g, P, 2, 256, dev)
+        q, k, v = (x.to(dev) for x in prefill_inputs(30 + i, 900, 900, 16, 2, 256))
+        qd = normal(g, 4, 16, 256).to(dev)
+        args = (qd, cache, table.to(dev), torch.tensor(lens, dtype=I32, device=dev))
+        work.append((args, (q, k, v), moe.attention_decode(*args), moe.attention_prefill(q, k, v), torch.cuda.Stream(dev)))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for (args, qkv, _, _, s), to in zip(work, got):
+            to.append((moe.attention_decode(*args, stream=s), moe.attention_prefill(*qkv, stream=s)))
+    torch.cuda.synchronize()
+    for (_, _, a, b, _), to in zip(work, got):
+        assert all(torch.equal(x, a) and torch.equal(y, b) for x, y in to)
+
+
+@pytest.mark.parametrize("lens", [(37, 0, 130, 5), (1,), (200, 64, 63)])
+def test_example_layer(dev, lens):
+    """The example's decoding in a graph against attention over the cache's values
+    read back: those are rounded to bf16, as are the weights of both ways and both
+    results, each by 2^-8 at most (a key's roundings move a score of its size by as
+    much): eight of them at most, 2^-5."""
+    from examples import attention_layer
+    diff, last = attention_layer.run(lens, new=4, device=dev)
+    assert diff <= 2.0 ** -5
+    assert last.shape == (len(lens), 512) and torch.isfinite(last).all()
