@@ -9,7 +9,12 @@
 // from halves.  A group that holds a NaN or an infinity has scale and bias NaN
 // and reads back as NaN.
 //
-// Bound by memory, 2.56 bytes moved per column, and by instructions: see the kernels.
+// Bound by memory, 2.56 bytes moved per column, and on the way there by instructions,
+// those of the addresses as much as those of the columns: 16 columns per lane, a
+// block of several tokens whose places its first warp looks up, one token per lane.
+// 16,384 tokens of 2 heads of 256 are written in 14 us (3.1 TB/s) and read in 8.5
+// (5.1 TB/s); with a warp per token, a division per code and 8 columns per lane both
+// took 43 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -23,7 +28,7 @@ namespace moe {
 namespace {
 
 constexpr int kKvWarps = 4;
-constexpr int kBatch = 2;  // rows of a lane in flight (1: 1 us more for 16,384 tokens of 2 heads of 256 written, 4: 1.5)
+constexpr int kBatch = 2;  // rows of a lane in flight (4: 1.5 us more of those 14)
 // the sum of 0x4b400000 << 4 e, the bits of 2^23 + 2^22, modulo 2^32
 constexpr uint32_t kMagicBits = 0x3f400000u;
 
@@ -220,9 +225,10 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_write_kernel(const KvArgs a)
   }
 }
 
+// 16 columns per lane, half of the row apart, so that the addresses are shared.
 template <int D>
 __global__ void __launch_bounds__(kKvWarps * 32) kv_read_kernel(const KvArgs a) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
   __shared__ int s_page[32], s_place[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
@@ -233,48 +239,58 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_read_kernel(const KvArgs a) 
   find_slots(a, t0, s_page, s_place);
   __syncthreads();
   for (int r0 = warp * kBatch * kRows + lane / kLanes; r0 < rows; r0 += kKvWarps * kBatch * kRows) {
-    uint32_t code[kBatch], pair[kBatch];
+    uint32_t code[kBatch][2], pair[kBatch][2];
+    __nv_bfloat16 *to[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       const int r = r0 + b * kRows;
-      code[b] = pair[b] = 0;
+      code[b][0] = code[b][1] = pair[b][0] = pair[b][1] = 0;
+      to[b] = nullptr;
       if (r < rows) {
         int t, y;
         split_row(a, r, t, y);
         const int which = y >= H, page = s_page[t];
+        if (page != -2) to[b] = (which ? a.vo : a.ko) + ((t0 + t) * H + y - which * H) * D + c;
         if (page >= 0) {
           const long long row = cache_row(a.c, page, which, y - which * H, s_place[t]);
-          code[b] = *reinterpret_cast<const uint32_t *>(a.c.codes + row * (D / 2) + c / 2);
-          pair[b] = a.c.affine[row * (D / kGroup) + c / kGroup];
+          const uint8_t *codes = a.c.codes + row * (D / 2) + c / 2;
+          const uint32_t *affine = a.c.affine + row * (D / kGroup) + c / kGroup;
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            code[b][z] = *reinterpret_cast<const uint32_t *>(codes + z * (D / 4));
+            pair[b][z] = affine[z * (D / kGroup / 2)];
+          }
         }
       }
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int r = r0 + b * kRows;
-      if (r >= rows) break;
-      int t, y;
-      split_row(a, r, t, y);
-      const int which = y >= H;
-      if (s_page[t] == -2) continue;
-      const float s = __uint_as_float(pair[b] << 16), z = __uint_as_float(pair[b] & 0xffff0000u);
-      float x[8];
+      if (!to[b]) continue;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)  // 2^23 + code, less 2^23: a conversion at the rate of sums
-        x[e] = fmaf(s, __uint_as_float((code[b] >> (4 * e) & 15u) | 0x4b000000u) - 8388608.0f, z);
-      __nv_bfloat16 *o = (which ? a.vo : a.ko) + ((t0 + t) * H + y - which * H) * D + c;
-      *reinterpret_cast<uint4 *>(o) = make_uint4(bf16x2_bits(x[0], x[1]), bf16x2_bits(x[2], x[3]),
-                                                 bf16x2_bits(x[4], x[5]), bf16x2_bits(x[6], x[7]));
+      for (int z = 0; z < 2; ++z) {
+        const float s = __uint_as_float(pair[b][z] << 16), bias = __uint_as_float(pair[b][z] & 0xffff0000u);
+        uint32_t out[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // 2^23 + code, less 2^23: a conversion at the rate of sums
+          const uint64_t two = pair_of(__uint_as_float((code[b][z] >> (8 * i) & 15u) | 0x4b000000u),
+                                       __uint_as_float((code[b][z] >> (8 * i + 4) & 15u) | 0x4b000000u));
+          float x, y;
+          split(fma2(pair_of(s, s), add2(two, pair_of(-8388608.0f, -8388608.0f)), pair_of(bias, bias)), x, y);
+          out[i] = bf16x2_bits(x, y);
+        }
+        *reinterpret_cast<uint4 *>(to[b] + z * (D / 2)) = make_uint4(out[0], out[1], out[2], out[3]);
+      }
     }
   }
 }
 
 namespace {
 
-// Tokens of a block: as many as its warps have rows in flight for in two rounds, if
-// that leaves two blocks per SM.
+// Tokens of a block: 16 rows of 256 columns, or twice that of 128, if that leaves two
+// blocks per SM.  (Half as many tokens: 16.4 and 10.2 us in place of 14 and 8.5; twice
+// as many: 14.4 and 9.)
 int block_tokens(long long n_tokens, int H, int D) {
-  const int rows = 2 * kKvWarps * kBatch * (256 / D), fit = rows / (2 * H);
+  const int rows = 16 * (256 / D), fit = rows / (2 * H);
   const long long spread = n_tokens / (2 * 152);
   long long t = fit < spread ? fit : spread;
   t = t < 1 ? 1 : t;

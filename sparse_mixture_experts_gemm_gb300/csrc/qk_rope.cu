@@ -9,12 +9,13 @@
 // turns position * inv_freq / (2 pi) are formed in 64 bits, whole turns are
 // dropped there, and sine and cosine see at most half a turn in fp32.
 //
-// Bound by memory.  A warp has one token and some of its rows, 8 columns of a row
-// per lane: in the part that turns 4 and their 4 partners, so that no value is
-// exchanged.  (8 columns in one load there and 8 shuffles of a row: half as many
-// instructions again, and 67 us for 16,384 tokens of 18 heads of 256 in place of 59,
-// 5.1 TB/s.)  The token's angles are made once, one frequency per lane, and handed
-// round through shared memory.
+// Bound by memory, and by instructions on the way there.  A warp has one token and
+// some of its rows, 16 columns of a row per lane: in the part that turns 8 and their 8
+// partners, so that no value is exchanged (with 8 columns in one load and 8 shuffles
+// a row 16,384 tokens of 18 heads of 256 took 67 us in place of 56, 5.4 TB/s).  The
+// next row is on its way meanwhile; two rows ahead, or more warps by fewer registers
+// (60 us at 72, 67 at 64), gained nothing.  The token's angles are made once, one
+// frequency per lane, and handed round through shared memory.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -42,21 +43,29 @@ struct RopeArgs {
 // small, are taken again from elements scaled by a power of two
 constexpr float kMaxFloat = 3.402823466e38f, kTiny = 0x1p-90f, kDown = 0x1p-72f, kUp = 0x1p100f;
 
-// 4 bf16 as two pairs of fp32
-__device__ __forceinline__ void unpack4(const uint2 &u, float (&v)[4]) {
-  v[0] = __uint_as_float(u.x << 16);
-  v[1] = __uint_as_float(u.x & 0xffff0000u);
-  v[2] = __uint_as_float(u.y << 16);
-  v[3] = __uint_as_float(u.y & 0xffff0000u);
+// 8 bf16 as pairs of fp32
+__device__ __forceinline__ void unpack8(const uint4 &u, uint64_t (&v)[4]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = pair_of(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ uint4 pack8(const uint64_t (&v)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    split(v[i], a, b);
+    w[i] = bf16x2_bits(a, b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 }  // namespace
 
 template <int D>
 __global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_kernel(const RopeArgs a) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows side by side
-  constexpr int kBatch = 2;                           // rows of a lane in flight ahead (4: 64 us in place of 59)
-  __shared__ __align__(16) float2 s_turn[kRopeWarps][D / 2];
+  constexpr int kLanes = D / 16, kRows = 32 / kLanes;  // lanes of a row, rows side by side
+  __shared__ __align__(16) float s_cos[kRopeWarps][D / 2], s_sin[kRopeWarps][D / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_launch_dependents();
@@ -65,116 +74,94 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_rope_kernel(const RopeArgs
   if (token >= a.tokens) return;
   const int first = static_cast<int>(unit % a.split) * a.per, H = a.Hq + a.Hk, last = min(first + a.per, H);
   const int half = a.rot / 2, sub = lane / kLanes, l = lane % kLanes;
-  const bool turned = 8 * l < a.rot;
-  // this lane's columns: c0 .. c0 + 3, c1 .. c1 + 3
-  const int c0 = turned ? 4 * l : 8 * l, c1 = turned ? half + 4 * l : 8 * l + 4;
+  const bool turned = 16 * l < a.rot;
+  // this lane's columns: c0 .. c0 + 7, c1 .. c1 + 7
+  const int c0 = turned ? 8 * l : a.rot + 8 * l - half, c1 = c0 + (turned ? half : (D - a.rot) / 2);
 
-  uint2 next[kBatch][2];
-  auto fetch = [&](int r0) {
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int r = r0 + b * kRows + sub;
-      next[b][0] = next[b][1] = make_uint2(0, 0);
-      if (r < last) {
-        const __nv_bfloat16 *x = r < a.Hq ? a.q + token * a.qs + r * D : a.k + token * a.ks + (r - a.Hq) * D;
-        if (turned) {
-          next[b][0] = *reinterpret_cast<const uint2 *>(x + c0);
-          next[b][1] = *reinterpret_cast<const uint2 *>(x + c1);
-        } else {
-          const uint4 u = *reinterpret_cast<const uint4 *>(x + c0);
-          next[b][0] = make_uint2(u.x, u.y);
-          next[b][1] = make_uint2(u.z, u.w);
-        }
-      }
+  uint4 next[2];
+  auto fetch = [&](int r) {
+    next[0] = next[1] = make_uint4(0, 0, 0, 0);
+    if (r < last) {
+      const __nv_bfloat16 *x = r < a.Hq ? a.q + token * a.qs + r * D : a.k + token * a.ks + (r - a.Hq) * D;
+      next[0] = *reinterpret_cast<const uint4 *>(x + c0);
+      next[1] = *reinterpret_cast<const uint4 *>(x + c1);
     }
   };
-  fetch(first);
+  fetch(first + sub);
   if (half) {
     const double p = static_cast<double>(a.positions[token]) * 0.15915494309189533577;  // 1 / (2 pi)
     for (int i = lane; i < half; i += 32) {
       const double t = p * a.freq[i];
       float sn, cs;
       sincospif(2.0f * static_cast<float>(t - rint(t)), &sn, &cs);
-      s_turn[warp][i] = make_float2(cs, sn);
+      s_cos[warp][i] = cs;
+      s_sin[warp][i] = sn;
     }
     __syncwarp();
   }
-  float cs[4], sn[4];
+  uint64_t cs[4] = {}, sn[4] = {};
+  if (turned)
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 t = turned ? s_turn[warp][4 * l + e] : make_float2(1.0f, 0.0f);
-    cs[e] = t.x;
-    sn[e] = t.y;
-  }
-  float w[2][4];   // the weights of the kind of rows at hand
+    for (int i = 0; i < 4; ++i) {
+      cs[i] = *reinterpret_cast<const uint64_t *>(&s_cos[warp][8 * l + 2 * i]);
+      sn[i] = *reinterpret_cast<const uint64_t *>(&s_sin[warp][8 * l + 2 * i]);
+    }
+  uint64_t w[2][4];  // the weights of the kind of rows at hand
   int kind = -1;
 
-  for (int r0 = first; r0 < last; r0 += kBatch * kRows) {
-    uint2 now[kBatch][2];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      now[b][0] = next[b][0];
-      now[b][1] = next[b][1];
+  for (int r0 = first; r0 < last; r0 += kRows) {
+    const int r = r0 + sub;
+    uint64_t v[2][4];
+    unpack8(next[0], v[0]);
+    unpack8(next[1], v[1]);
+    fetch(r + kRows);
+    if (kind != (r >= a.Hq)) {
+      kind = r >= a.Hq;
+      const __nv_bfloat16 *from = kind ? a.kw : a.qw;
+      unpack8(*reinterpret_cast<const uint4 *>(from + c0), w[0]);
+      unpack8(*reinterpret_cast<const uint4 *>(from + c1), w[1]);
     }
-    fetch(r0 + kBatch * kRows);
+    auto squares = [&] {
+      uint64_t two[2] = {0, 0};
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int r = r0 + b * kRows + sub;
-      if (r0 + b * kRows >= last) break;  // (the whole warp)
-      if (kind != (r >= a.Hq)) {
-        kind = r >= a.Hq;
-        const __nv_bfloat16 *from = kind ? a.kw : a.qw;
-        unpack4(*reinterpret_cast<const uint2 *>(from + c0), w[0]);
-        unpack4(*reinterpret_cast<const uint2 *>(from + c1), w[1]);
+      for (int i = 0; i < 4; ++i) {
+        two[0] = fma2(v[0][i], v[0][i], two[0]);
+        two[1] = fma2(v[1][i], v[1][i], two[1]);
       }
-      float v[2][4], ss = 0.0f;
+      float x, y;
+      split(add2(two[0], two[1]), x, y);
+      x += y;
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        unpack4(now[b][z], v[z]);
+      for (int o = kLanes / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      return x;
+    };
+    auto times = [&](float f) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ss = fmaf(v[z][e], v[z][e], ss);
+      for (int i = 0; i < 8; ++i) v[i >> 2][i & 3] = mul2(v[i >> 2][i & 3], pair_of(f, f));
+    };
+    float ss = squares();
+    const bool huge = ss > kMaxFloat, tiny = a.eps < kTiny && ss < kTiny;
+    float pre = 1.0f;
+    if (__any_sync(0xffffffffu, huge || tiny)) {
+      if (huge || tiny) pre = huge ? kDown : kUp;
+      times(pre);
+      ss = squares();
+    }
+    // (a row of zeros stays one where eps is 0)
+    times(ss == 0.0f ? 0.0f : rsqrtf(ss * (1.0f / D) + a.eps * pre * pre));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i >> 2][i & 3] = mul2(v[i >> 2][i & 3], w[i >> 2][i & 3]);
+    if (turned)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint64_t x = v[0][i], y = v[1][i];
+        v[0][i] = fma2(x, cs[i], mul2(y, sn[i]) ^ 0x8000000080000000ull);
+        v[1][i] = fma2(y, cs[i], mul2(x, sn[i]));
       }
-#pragma unroll
-      for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const bool huge = ss > kMaxFloat, tiny = a.eps < kTiny && ss < kTiny;
-      float pre = 1.0f;
-      if (__any_sync(0xffffffffu, huge || tiny)) {
-        if (huge || tiny) pre = huge ? kDown : kUp;
-        ss = 0.0f;
-#pragma unroll
-        for (int z = 0; z < 2; ++z)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[z][e] *= pre;
-            ss = fmaf(v[z][e], v[z][e], ss);
-          }
-#pragma unroll
-        for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      }
-      // (a row of zeros stays one where eps is 0)
-      const float g = ss == 0.0f ? 0.0f : rsqrtf(ss * (1.0f / D) + a.eps * pre * pre);
-#pragma unroll
-      for (int z = 0; z < 2; ++z)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[z][e] = v[z][e] * g * w[z][e];
-      if (turned)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = v[0][e], y = v[1][e];
-          v[0][e] = fmaf(x, cs[e], -y * sn[e]);
-          v[1][e] = fmaf(y, cs[e], x * sn[e]);
-        }
-      if (r < last) {
-        __nv_bfloat16 *o = kind ? a.ko + token * a.kos + (r - a.Hq) * D : a.qo + token * a.qos + r * D;
-        const uint2 y0 = make_uint2(bf16x2_bits(v[0][0], v[0][1]), bf16x2_bits(v[0][2], v[0][3]));
-        const uint2 y1 = make_uint2(bf16x2_bits(v[1][0], v[1][1]), bf16x2_bits(v[1][2], v[1][3]));
-        if (turned) {
-          *reinterpret_cast<uint2 *>(o + c0) = y0;
-          *reinterpret_cast<uint2 *>(o + c1) = y1;
-        } else {
-          *reinterpret_cast<uint4 *>(o + c0) = make_uint4(y0.x, y0.y, y1.x, y1.y);
-        }
-      }
+    if (r < last) {
+      __nv_bfloat16 *o = kind ? a.ko + token * a.kos + (r - a.Hq) * D : a.qo + token * a.qos + r * D;
+      *reinterpret_cast<uint4 *>(o + c0) = pack8(v[0]);
+      *reinterpret_cast<uint4 *>(o + c1) = pack8(v[1]);
     }
   }
 }
