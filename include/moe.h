@@ -511,12 +511,18 @@ int moe_qk_norm_rope(const void *q, const void *k, const void *q_weight, const v
  *        queries and n_k / n_seq keys.
  * scale > 0 and finite.  A NaN or infinity in k or v reaches no query that does
  * not see its token.
+ *   workspace: device memory of at least the bytes that
+ *        moe_attention_prefill_workspace gives for the same sizes, 16-byte
+ *        aligned, used by the call's kernels alone; NULL where that is 0.  (Few
+ *        queries over many keys: the keys are cut into parts, which are joined.)
  */
 int moe_attention_prefill(const void *q, const void *k, const void *v, const int32_t *offsets,
                           const int32_t *k_offsets, long long n_q, long long n_k, int n_seq,
                           int n_q_heads, int n_kv_heads, int head_dim, long long q_stride,
                           long long k_stride, long long v_stride, float scale, void *out,
-                          void *cuda_stream);
+                          void *workspace, size_t workspace_bytes, void *cuda_stream);
+int moe_attention_prefill_workspace(long long n_q, long long n_k, int n_seq, int n_q_heads,
+                                    int n_kv_heads, int head_dim, size_t *bytes);
 
 /*
  * A key/value cache in the 4-bit group-affine format of moe_quantize_q4, in pages

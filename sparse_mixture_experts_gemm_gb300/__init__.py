@@ -47,7 +47,7 @@ EXPORTED = ["moe_create", "moe_route", "moe_forward", "moe_forward_routed", "moe
             "moe_decode_noalloc", "moe_noalloc_status", "moe_create_q4", "moe_quantize_q4",
             "gdn_scan", "moe_add_rmsnorm", "moe_add_rmsnorm_fp8", "moe_quantize_fp8",
             "moe_matmul_fp8", "gdn_decay_scan", "gdn_decay_workspace", "moe_qk_norm_rope",
-            "moe_attention_prefill", "moe_kv_write", "moe_kv_read", "moe_attention_decode",
+            "moe_attention_prefill", "moe_attention_prefill_workspace", "moe_kv_write", "moe_kv_read", "moe_attention_decode",
             "moe_attention_decode_workspace"]
 
 Q4_GROUP = 64  # columns per (scale, bias) pair of the 4-bit format
@@ -128,7 +128,8 @@ def lib() -> ctypes.CDLL:
     L.gdn_decay_workspace.argtypes = [ll, ip, ip, ip, ip, ip, ctypes.POINTER(ctypes.c_size_t)]
     sz = ctypes.c_size_t
     L.moe_qk_norm_rope.argtypes = [vp, vp, vp, vp, vp, vp, ll, ip, ip, ip, ip, ll, ll, fp, vp, ll, vp, ll, vp]
-    L.moe_attention_prefill.argtypes = [vp, vp, vp, vp, vp, ll, ll, ip, ip, ip, ip, ll, ll, ll, fp, vp, vp]
+    L.moe_attention_prefill.argtypes = [vp, vp, vp, vp, vp, ll, ll, ip, ip, ip, ip, ll, ll, ll, fp, vp, vp, sz, vp]
+    L.moe_attention_prefill_workspace.argtypes = [ll, ll, ip, ip, ip, ip, ctypes.POINTER(sz)]
     L.moe_kv_write.argtypes = [vp, vp, ll, vp, vp, vp, ip, vp, vp, ll, ip, ip, ip, ll, ll, vp]
     L.moe_kv_read.argtypes = [vp, vp, ll, vp, ip, vp, vp, ll, ip, ip, ip, vp, vp, vp]
     L.moe_attention_decode.argtypes = [vp, ll, vp, vp, ll, vp, ip, vp, ip, ip, ip, ip, fp, vp, vp, sz, vp]

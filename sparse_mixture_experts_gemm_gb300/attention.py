@@ -99,6 +99,15 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps=1e-6, q_out=
     return q_out, k_out
 
 
+@functools.lru_cache(maxsize=1024)
+def _prefill_workspace(N, M, n, Hq, Hk, D):
+    """Bytes that moe_attention_prefill wants for these sizes."""
+    need = ctypes.c_size_t(0)
+    _check(_lib().moe_attention_prefill_workspace(N, M, n, Hq, Hk, D, ctypes.byref(need)),
+           "moe_attention_prefill_workspace")
+    return need.value
+
+
 def attention_prefill(q, k, v, offsets=None, k_offsets=None, scale=None, out=None, stream=None):
     """moe_attention_prefill: causal attention of q bf16 [n][T][H_q][D] over
     k, v bf16 [n][M][H_kv][D] (n sequences, the queries being the last of the keys),
@@ -130,14 +139,18 @@ def attention_prefill(q, k, v, offsets=None, k_offsets=None, scale=None, out=Non
             raise ValueError("k and v must have q's tokens where there are no k_offsets")
     qs, ks, vs = _tokens("q", q, Hq, D), _tokens("k", k, Hk, D), _tokens("v", v, Hk, D)
     ctx, handle = _on(stream, _device(q, k, v, offsets, k_offsets, out))
-    if out is None:
-        with ctx:
+    need, wp = _prefill_workspace(N, M, n, Hq, Hk, D), None
+    with ctx:
+        if out is None:
             out = _empty(q)
-    else:
-        _given("out", out, q.shape, _BF16)
+        else:
+            _given("out", out, q.shape, _BF16)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+            wp = ws.data_ptr()
     _check(_lib().moe_attention_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), op, kp, N, M, n, Hq, Hk, D, qs,
-                                        ks, vs, D ** -0.5 if scale is None else scale, out.data_ptr(), handle),
-           "moe_attention_prefill")
+                                        ks, vs, D ** -0.5 if scale is None else scale, out.data_ptr(), wp, need,
+                                        handle), "moe_attention_prefill")
     return out
 
 

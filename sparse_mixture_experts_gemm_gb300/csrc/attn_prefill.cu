@@ -67,13 +67,16 @@ struct PrefillArgs {
   uint32_t per_mul, per_shift;       // x / (2 tokens) = (x per_mul >> 32) >> per_shift, x < 2^31
   float scale;                       // times log2(e)
   int *status;
+  int splits;   // parts of each tile's keys
+  float *part;  // (splits > 1) [splits][n_q][Hq][D]: outputs before the division
+  float2 *stat; // [splits][n_q][Hq]: maximum, sum
 };
 
 struct Item {
   int q0, lq;    // first query and queries of the sequence
   int k0, lk;    // first key and keys
   int t0, head;  // first query of the cluster's tile (in the sequence), key/value head
-  int valid;
+  int valid, part;
 };
 
 template <int D>
@@ -283,11 +286,16 @@ struct Schedule {
     for (int i0 = 0; i0 < a.n_seq; i0 += 32) sum += __reduce_add_sync(0xffffffffu, mine(i0, c));
     return sum;
   }
-  // the n-th tile; n < all(0) heads
+  // tiles and parts of all heads; the n-th of them
+  __device__ __forceinline__ long long total() const { return all(0) * a.Hk * a.splits; }
   __device__ __forceinline__ Item find(long long n) const {
     const int lane = threadIdx.x & 31;
     Item it = {};
     it.valid = 1;
+    if (a.splits > 1) {
+      it.part = static_cast<int>(n % a.splits);
+      n /= a.splits;
+    }
     it.head = static_cast<int>(n % a.Hk);
     long long left = n / a.Hk;
     if (alike) {  // the last tiles of all sequences, then those before
@@ -404,12 +412,18 @@ struct Cleaner {
 
 // What the roles derive from an item
 struct Tile {
-  int shift, nk, jm, mine;  // keys less queries, key tiles, first one that hides keys from a query, this CTA's first query
+  int shift, mine;  // keys less queries, this CTA's first query
+  int j0, nk, jm;   // first key tile of this part, how many, from which of them on some query must not see a key
   __device__ __forceinline__ Tile(const PrefillArgs &a, const Item &it, int rank) {
     shift = it.lk - it.lq;
     const int end = min(it.t0 + 2 * a.tokens, it.lq);
     nk = (max(0, end + shift) + kKeys - 1) / kKeys;
-    jm = max(0, it.t0 + shift + 1) / kKeys;
+    j0 = 0;
+    if (a.splits > 1) {
+      j0 = nk * it.part / a.splits;
+      nk = nk * (it.part + 1) / a.splits - j0;
+    }
+    jm = max(0, max(0, it.t0 + shift + 1) / kKeys - j0);
     mine = it.t0 + rank * a.tokens;
   }
 };
@@ -472,7 +486,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   if (warp == 10) {  // the first item, meanwhile
     pdl_wait();
     const Schedule plan(a);
-    total = plan.all(0) * a.Hk;
+    total = plan.total();
     Item it = {};
     if ((blockIdx.x >> 1) < total) it = plan.find(blockIdx.x >> 1);
     if (lane == 0) ctl.item[0] = it;
@@ -547,7 +561,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
             if (rank == 0) mbar_arrive_expect_tx(fb, 2 * P::kSlot);
             const uint32_t to = cluster_map(fb, 0);
             for (int b = 0; b < D / 64; ++b)
-              tma_load_2d_pair(dst + b * 8192, &tmK, to, it.head * D + 64 * b, it.k0 + j * kKeys + rank * 64, pol);
+              tma_load_2d_pair(dst + b * 8192, &tmK, to, it.head * D + 64 * b, it.k0 + (t.j0 + j) * kKeys + rank * 64, pol);
           } else {
             uint32_t to = cluster_map(fb, 0);
             if (j >= t.jm) {  // the softmax's warps see to these first: their copy is this CTA's matter
@@ -558,7 +572,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
               mbar_arrive_expect_tx(fb, 2 * P::kSlot);
             }
             for (int b = 0; b < D / 128; ++b)
-              tma_load_2d_pair(dst + b * 16384, &tmV, to, it.head * D + rank * (D / 2) + 64 * b, it.k0 + j * kKeys, pol);
+              tma_load_2d_pair(dst + b * 16384, &tmV, to, it.head * D + rank * (D / 2) + 64 * b, it.k0 + (t.j0 + j) * kKeys, pol);
           }
           ++r;
           return true;
@@ -695,14 +709,16 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     for (int k = 0; ok && next_item(k, it); ++k) {
       const Tile t(a, it, rank);
       const uint32_t bad = smem_u32(&ctl.bad[used][0]), flag = smem_u32(&ctl.hit[used]);
-      const int own = max(0, t.mine + t.shift + 1) / kKeys;  // first tile masked for this CTA
+      const int own = max(0, t.mine + t.shift + 1) / kKeys - t.j0;  // first tile masked for this CTA
       float f0[2], f1[2];  // factors of the outputs of this thread's two rows there
+      float2 stat[2];      // their maximum and sum
       // the values of a masked tile
       auto clean = [&](int j) {
         const int s = (base + (j + 1 < t.nk ? 2 * j + 2 : 2 * j + 1)) % P::kSlots;  // V's place in the ring
         if (!warp_wait(a, smem_u32(&ctl.vloc[s]), (vphase >> s) & 1, abort_flag, SITE_MMA_FULL)) return false;
         const int e = static_cast<int>(threadIdx.x) - 64 - (P::kStreams == 2 ? half * 128 : 0);
-        Cleaner<D, P::kMakers * 32>::clean(bad, flag, ring + s * P::kSlot, e, rank, j * kKeys, it.lk, t.jm * kKeys);
+        Cleaner<D, P::kMakers * 32>::clean(bad, flag, ring + s * P::kSlot, e, rank, (t.j0 + j) * kKeys, it.lk,
+                                            (t.j0 + t.jm) * kKeys);
         return true;
       };
       auto passed = [&](int j) {  // (every softmax warp follows the phases of the masked tiles' copies)
@@ -728,7 +744,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
           ld_16x64(ts, x[0]);
           ld_16x64(ts + 64, x[1]);
           if (j >= own) {
-            const int key = j * kKeys + 2 * (lane & 3);
+            const int key = (t.j0 + j) * kKeys + 2 * (lane & 3);
 #pragma unroll
             for (int y = 0; y < 2; ++y)
 #pragma unroll
@@ -803,7 +819,8 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         for (int z = 0; z < 2; ++z) {
           l[z] += __shfl_xor_sync(0xffffffffu, l[z], 1);
           l[z] += __shfl_xor_sync(0xffffffffu, l[z], 2);
-          f0[z] = 1.0f / l[z];
+          f0[z] = a.splits > 1 ? 1.0f : 1.0f / l[z];
+          stat[z] = make_float2(m[z], l[z]);
         }
       } else {
         const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
@@ -822,7 +839,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
           // once for the maximum, once more for P (128 values a thread would not stay in
           // registers)
           const bool masked = j >= own;
-          const int hidden = limit - j * kKeys;  // columns past this are masked
+          const int hidden = limit - (t.j0 + j) * kKeys;  // columns past this are masked
           float top = -INFINITY;
 #pragma unroll
           for (int y = 0; y < kKeys; y += 64) {
@@ -932,16 +949,23 @@ __global__ void __launch_bounds__(kThreadsA, 1)
           const float M = fmaxf(s0.x, s1.x);
           f0[z] = s0.x == M ? 1.0f : fast_exp2((s0.x - M) * c);
           f1[z] = s1.x == M ? 1.0f : fast_exp2((s1.x - M) * c);
-          const float inv = 1.0f / (f0[z] * s0.y + f1[z] * s1.y);
+          stat[z] = make_float2(M, f0[z] * s0.y + f1[z] * s1.y);
+          const float inv = a.splits > 1 ? 1.0f : 1.0f / stat[z].y;
           f0[z] *= inv;
           f1[z] *= inv;
         }
       }
-      __nv_bfloat16 *o[2];
+      long long row[2];  // of out
 #pragma unroll
       for (int z = 0; z < 2; ++z)
-        o[z] = a.out + (static_cast<long long>(it.q0 + t.mine + (valid[z] ? token[z] : 0)) * a.Hq + it.head * a.group +
-                        head[z]) * D + 8 * (lane & 3);
+        row[z] = static_cast<long long>(it.q0 + t.mine + (valid[z] ? token[z] : 0)) * a.Hq + it.head * a.group + head[z];
+      if (a.splits > 1) {
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          row[z] += it.part * a.n_q * a.Hq;
+          if (valid[z] && (lane & 3) == 0) a.stat[row[z]] = stat[z];
+        }
+      }
       const bool marked = t.nk > 0 && *static_cast<volatile uint32_t *>(&ctl.hit[used]) != 0;
       const uint32_t from = P::O + (static_cast<uint32_t>(wq * 32 + half * 16) << 16);
 #pragma unroll 1
@@ -975,10 +999,21 @@ __global__ void __launch_bounds__(kThreadsA, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const uint32_t key = i & 1 ? first >> 16 : first & 0xffffu;
-              if (i >> 2 == n && lim[(i >> 1) & 1] - t.jm * kKeys >= static_cast<int>(key))
+              if (i >> 2 == n && lim[(i >> 1) & 1] - (t.j0 + t.jm) * kKeys >= static_cast<int>(key))
                 v[i] = __uint_as_float(0x7fffffffu);
             }
           }
+        }
+        if (a.splits > 1) {
+#pragma unroll
+          for (int z = 0; z < 2; ++z)
+            if (valid[z]) {
+              float *to = a.part + row[z] * D + d + 2 * (lane & 3);
+#pragma unroll
+              for (int n = 0; n < 8; ++n)
+                *reinterpret_cast<float2 *>(to + 8 * n) = make_float2(v[4 * n + 2 * z], v[4 * n + 2 * z + 1]);
+            }
+          continue;
         }
 #pragma unroll
         for (int z = 0; z < 2; ++z)
@@ -988,7 +1023,8 @@ __global__ void __launch_bounds__(kThreadsA, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = bf16x2_bits(v[16 * h + 4 * i + 2 * z], v[16 * h + 4 * i + 2 * z + 1]);
             turn_quad(w);
-            if (valid[z]) *reinterpret_cast<uint4 *>(o[z] + d + 32 * h) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (valid[z])
+              *reinterpret_cast<uint4 *>(a.out + row[z] * D + d + 32 * h + 8 * (lane & 3)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
       }
       tc_fence_before();
@@ -1007,6 +1043,66 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   if (warp == 1) tmem_dealloc2(0, kTmemCols);
   if (*abort_flag)  // after an abort the copies in flight get time to land
     for (int i = 0; i < 200; ++i) __nanosleep(1000);
+}
+
+// Joins the parts of tiles whose keys were split: a block has some of a tile's 256
+// rows, found as the main kernel finds them; D / 4 threads per row.
+constexpr int kJoinThreads = 1024;
+template <int D>
+constexpr int kJoinRows = kJoinThreads / (D / 4);
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attn_prefill_join_kernel(const PrefillArgs a) {
+  constexpr int kBlocks = 256 / kJoinRows<D>;  // of a tile
+  __shared__ Item s_item;
+  pdl_wait();
+  pdl_launch_dependents();
+  const long long n = blockIdx.x / kBlocks;
+  if (threadIdx.x < 32) {
+    const Schedule plan(a);
+    Item it = {};
+    if (n * a.splits < plan.total()) it = plan.find(n * a.splits);
+    if (threadIdx.x == 0) s_item = it;
+  }
+  __syncthreads();
+  const Item it = s_item;
+  if (!it.valid) return;
+  const int d = static_cast<int>(threadIdx.x) % (D / 4) * 4;
+  const int at = static_cast<int>(blockIdx.x % kBlocks) * kJoinRows<D> + static_cast<int>(threadIdx.x) / (D / 4);
+  const int rank = at >> 7, r = at & 127, t = it.t0 + rank * a.tokens + r / a.group;
+  if (r >= a.tokens * a.group || t >= it.lq) return;  // (whole warps)
+  const long long row = static_cast<long long>(it.q0 + t) * a.Hq + it.head * a.group + r % a.group, step = a.n_q * a.Hq;
+  // lane s of a warp, all of one row, has part s's maximum and sum
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  const float2 ml = lane < a.splits ? a.stat[row + lane * step] : make_float2(-INFINITY, 0.0f);
+  float M = ml.x;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float mine = ml.y == 0.0f ? 0.0f : ml.x == M ? 1.0f : fast_exp2((ml.x - M) * a.scale);
+  const uint32_t seen = __ballot_sync(0xffffffffu, ml.y != 0.0f);  // parts with keys for this row
+  float L = mine * ml.y;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+  for (int s0 = 0; s0 < a.splits; s0 += 8) {
+    float4 y[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (seen >> (s0 + s) & 1) y[s] = *reinterpret_cast<const float4 *>(a.part + (row + (s0 + s) * step) * D + d);
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const float f = __shfl_sync(0xffffffffu, mine, s0 + s);
+      if (!(seen >> (s0 + s) & 1)) continue;
+      o.x = fmaf(f, y[s].x, o.x);
+      o.y = fmaf(f, y[s].y, o.y);
+      o.z = fmaf(f, y[s].z, o.z);
+      o.w = fmaf(f, y[s].w, o.w);
+    }
+  }
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+  *reinterpret_cast<uint2 *>(a.out + row * D + d) =
+      make_uint2(bf16x2_bits(o.x * inv, o.y * inv), bf16x2_bits(o.z * inv, o.w * inv));
 }
 
 namespace {
@@ -1054,16 +1150,48 @@ const PrefillDevice &prefill_device() {
   return devs[dev];
 }
 
+// Parts into which each tile's keys are cut where there are few tiles.  Times are in
+// tiles of 128 keys (about 1 us): rounds of clusters of a part's tiles and 3 for its
+// start and end, 5 for the second kernel, and the parts' outputs, which move to and fro
+// at 3 MB a tile's time.  Measured, 16 query heads on 2 of 256: 1 query over 4,096 keys
+// in 16.6 us (16 parts) against 41, over 16,384 in 24 against 142, 64 over 4,096 in 21
+// against 42, 300 over 8,192 in 45 (3 parts) against 76 (4 parts, more than there are
+// clusters: 60); not cut: 5 over 1,024 16.7 (15.4 with 4 parts), 700 over 2,000 26 (48
+// with 2), 1,300 over 4,000 63 (97).  The lengths are on the device: the longest
+// sequence counts as of twice the mean length.
+int splits_of(long long n_q, long long n_k, int n_seq, int n_q_heads, int n_kv_heads, int head_dim) {
+  constexpr int kPairs = 76, kMost = 32;
+  const long long per = 2 * (128 / (n_q_heads / n_kv_heads));
+  const long long tiles = ((n_q + per - 1) / per + n_seq - 1) * n_kv_heads;
+  const long long keys = ((n_seq > 2 ? 2 * (n_k / n_seq) : n_k) + kKeys - 1) / kKeys;
+  const double moved = static_cast<double>(n_q) * n_q_heads * head_dim * 4 / 3e6;
+  auto time = [&](int s) {
+    const long long rounds = (tiles * s + kPairs - 1) / kPairs;
+    return rounds * ((keys + s - 1) / s + 3) + (s > 1 ? 5 + s * moved : 0.0);
+  };
+  int best = 1;
+  double least = 0.9 * time(1);  // (what is cut should gain)
+  for (int s = 2; s <= kMost && s <= keys && tiles * s <= 4 * kPairs; ++s)
+    if (time(s) < least) {
+      least = time(s);
+      best = s;
+    }
+  return best;
+}
+
 template <int D>
 cudaError_t launch_prefill(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
-                           const PrefillArgs &a, int clusters, cudaStream_t st) {
+                           const PrefillArgs &a, int clusters, long long tiles, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   prefill_config(cfg, attr, 2 * clusters, Plan<D>::kTotal, st);
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D>, mq, mk, mv, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D>, mq, mk, mv, a);
+  if (e != cudaSuccess || a.splits == 1) return e;
+  return launch_attn(attn_prefill_join_kernel<D>, dim3(static_cast<unsigned>(tiles * (256 / kJoinRows<D>))), kJoinThreads, 0, st,
+                     a);
 }
 
 }  // namespace
@@ -1072,21 +1200,33 @@ cudaError_t launch_prefill(const CUtensorMap &mq, const CUtensorMap &mk, const C
 
 using namespace moe;
 
+extern "C" int moe_attention_prefill_workspace(long long n_q, long long n_k, int n_seq, int n_q_heads,
+                                               int n_kv_heads, int head_dim, size_t *bytes) {
+  if (!bytes || n_q < 0 || n_k < 0 || n_seq < 0 || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads != 0)
+    return MOE_ERR_INVALID_ARG;
+  if ((head_dim != 128 && head_dim != 256) || n_q_heads / n_kv_heads > 64 || n_kv_heads > 4096 ||
+      n_q > (1LL << 29) || n_k > (1LL << 29))
+    return MOE_ERR_UNSUPPORTED;
+  *bytes = 0;
+  if (n_q == 0 || n_seq == 0) return MOE_OK;
+  const int splits = splits_of(n_q, n_k, n_seq, n_q_heads, n_kv_heads, head_dim);
+  if (splits > 1) *bytes = splits * static_cast<size_t>(n_q) * n_q_heads * (head_dim * sizeof(float) + sizeof(float2));
+  return MOE_OK;
+}
+
 extern "C" int moe_attention_prefill(const void *q, const void *k, const void *v,
                                      const int32_t *offsets, const int32_t *k_offsets,
                                      long long n_q, long long n_k, int n_seq, int n_q_heads,
                                      int n_kv_heads, int head_dim, long long q_stride,
                                      long long k_stride, long long v_stride, float scale, void *out,
-                                     void *cuda_stream) {
-  if (n_q < 0 || n_k < 0 || n_seq < 0 || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads != 0 ||
-      !(scale > 0.0f) || scale > 3.0e38f)
-    return MOE_ERR_INVALID_ARG;
+                                     void *workspace, size_t workspace_bytes, void *cuda_stream) {
+  size_t need = 0;
+  const int rc = moe_attention_prefill_workspace(n_q, n_k, n_seq, n_q_heads, n_kv_heads, head_dim, &need);
+  if (rc != MOE_OK) return rc;
+  if (!(scale > 0.0f) || scale > 3.0e38f) return MOE_ERR_INVALID_ARG;
   if (k_offsets && !offsets) return MOE_ERR_INVALID_ARG;
   if (offsets ? (!k_offsets && n_q != n_k) : (n_seq > 0 && (n_q % n_seq != 0 || n_k % n_seq != 0)))
     return MOE_ERR_INVALID_ARG;
-  if ((head_dim != 128 && head_dim != 256) || n_q_heads / n_kv_heads > 64 || n_kv_heads > 4096 ||
-      n_q > (1LL << 29) || n_k > (1LL << 29))
-    return MOE_ERR_UNSUPPORTED;
   const long long qw = static_cast<long long>(n_q_heads) * head_dim, kw = static_cast<long long>(n_kv_heads) * head_dim;
   if (q_stride < qw || k_stride < kw || v_stride < kw) return MOE_ERR_INVALID_ARG;
   const long long strides[] = {q_stride, k_stride, v_stride};
@@ -1095,8 +1235,10 @@ extern "C" int moe_attention_prefill(const void *q, const void *k, const void *v
     if (s % 8 != 0) return MOE_ERR_ALIGNMENT;
   }
   if (n_q == 0 || n_seq == 0) return MOE_OK;
-  if (!q || !out || (n_k > 0 && (!k || !v))) return MOE_ERR_INVALID_ARG;
+  if (!q || !out || (n_k > 0 && (!k || !v)) || (need > 0 && !workspace) || workspace_bytes < need)
+    return MOE_ERR_INVALID_ARG;
   if (off_boundary(q, 16) || off_boundary(k, 16) || off_boundary(v, 16) || off_boundary(out, 16) ||
+      off_boundary(workspace, 16) ||
       off_boundary(offsets, 4) || off_boundary(k_offsets, 4))
     return MOE_ERR_ALIGNMENT;
   const PrefillDevice &dev = prefill_device();
@@ -1114,6 +1256,9 @@ extern "C" int moe_attention_prefill(const void *q, const void *k, const void *v
   a.tokens = 128 / a.group;
   a.scale = scale * 1.4426950408889634f;
   a.status = dev.status;
+  a.splits = splits_of(n_q, n_k, n_seq, n_q_heads, n_kv_heads, head_dim);
+  a.part = static_cast<float *>(workspace);
+  if (a.splits > 1) a.stat = reinterpret_cast<float2 *>(a.part + a.splits * n_q * n_q_heads * head_dim);
   // x / d = (x m) >> (31 + s), x < 2^31, with 2^(s - 1) < d <= 2^s and m = 2^(31 + s) / d + 1
   const uint32_t divisor = 2 * a.tokens;
   uint32_t s = 1;
@@ -1122,9 +1267,9 @@ extern "C" int moe_attention_prefill(const void *q, const void *k, const void *v
   a.per_shift = s - 1;
   // tiles of the call, or as many as there can be
   const long long per = 2 * a.tokens;
-  const long long tiles = offsets ? n_q / per + n_seq : n_seq * ((n_q / n_seq + per - 1) / per);
+  const long long tiles = (offsets ? n_q / per + n_seq : n_seq * ((n_q / n_seq + per - 1) / per)) * n_kv_heads;
   const int most = dev.clusters[head_dim == 256];
-  const int clusters = tiles * n_kv_heads < most ? static_cast<int>(tiles * n_kv_heads) : most;
+  const int clusters = tiles * a.splits < most ? static_cast<int>(tiles * a.splits) : most;
   const uint64_t d = head_dim, hk = n_kv_heads;
   const uint64_t keys = n_k > 0 ? n_k : 1;  // (no key is read where there is none)
   const void *kb = n_k > 0 ? k : q, *vb = n_k > 0 ? v : q;
@@ -1134,7 +1279,7 @@ extern "C" int moe_attention_prefill(const void *q, const void *k, const void *v
       !encode_map_2d(&mv, vb, 2, keys, hk * d, 64, 128, true, 2 * v_stride))
     return MOE_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
-  const cudaError_t e = head_dim == 128 ? launch_prefill<128>(mq, mk, mv, a, clusters, st)
-                                        : launch_prefill<256>(mq, mk, mv, a, clusters, st);
+  const cudaError_t e = head_dim == 128 ? launch_prefill<128>(mq, mk, mv, a, clusters, tiles, st)
+                                        : launch_prefill<256>(mq, mk, mv, a, clusters, tiles, st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

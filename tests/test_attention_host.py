@@ -107,7 +107,8 @@ def test_rope_refusals(lib, kw, code):
 
 
 def _prefill(lib, **kw):
-    a = dict(q=P, k=P, v=P, off=P, koff=P, nq=4, nk=8, n=2, Hq=4, Hk=2, D=128, qs=512, ks=256, vs=256, scale=0.1, out=P)
+    a = dict(q=P, k=P, v=P, off=P, koff=P, nq=4, nk=8, n=2, Hq=4, Hk=2, D=128, qs=512, ks=256, vs=256, scale=0.1, out=P,
+             ws=None, bytes=0)
     a.update(kw)
     return lib.moe_attention_prefill(*a.values(), None)
 
@@ -121,10 +122,33 @@ def _prefill(lib, **kw):
     (dict(D=64), UNSUP), (dict(Hq=130, qs=130 * 128), UNSUP), (dict(nq=1 << 31), UNSUP), (dict(ks=1 << 38), UNSUP),
     (dict(q=P + 8), ALIGN), (dict(out=P + 8), ALIGN), (dict(off=P + 2), ALIGN), (dict(koff=P + 1), ALIGN),
     (dict(vs=260), ALIGN),
+    (dict(nk=1 << 20), BAD), (dict(nk=1 << 20, ws=P, bytes=1 << 10), BAD), (dict(nk=1 << 20, bytes=1 << 30), BAD),
+    (dict(nk=1 << 20, ws=P + 8, bytes=1 << 30), ALIGN),
     (dict(nq=0, q=None, out=None), OK), (dict(n=0), OK),
 ])
 def test_prefill_refusals(lib, kw, code):
     assert _prefill(lib, **kw) == code
+
+
+def test_prefill_workspace(lib):
+    """None where the tiles fill the GPU or keys are few, else room for the parts:
+    a row of outputs, a maximum and a sum per query, head and part."""
+    need = ctypes.c_size_t(0)
+
+    def size(*a):
+        assert lib.moe_attention_prefill_workspace(*a, ctypes.byref(need)) == OK
+        return need.value
+
+    assert size(4096, 4096, 1, 16, 2, 256) == 0 and size(17, 17, 1, 16, 2, 256) == 0 and size(64, 256, 2, 8, 2, 128) == 0
+    for a in ((1, 4096, 1, 16, 2, 256), (40, 20000, 1, 32, 8, 128), (8, 65536, 4, 4, 4, 256), (1, 1 << 29, 1, 64, 1, 128)):
+        row = a[0] * a[3] * (a[5] * 4 + 8)
+        parts = size(*a) // row
+        assert 2 <= parts <= 32 and need.value == parts * row
+    assert size(0, 100, 1, 16, 2, 256) == 0 and size(5, 0, 1, 16, 2, 256) == 0 and size(5, 5000, 0, 16, 2, 256) == 0
+    for a, code in (((-1, 4, 1, 4, 2, 128), BAD), ((1, -4, 1, 4, 2, 128), BAD), ((1, 4, -1, 4, 2, 128), BAD),
+                    ((1, 4, 1, 3, 2, 128), BAD), ((1, 4, 1, 4, 2, 64), UNSUP), ((1 << 30, 4, 1, 4, 2, 128), UNSUP)):
+        assert lib.moe_attention_prefill_workspace(*a, ctypes.byref(need)) == code
+    assert lib.moe_attention_prefill_workspace(4, 4, 1, 4, 2, 128, None) == BAD
 
 
 def _write(lib, **kw):

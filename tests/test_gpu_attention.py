@@ -269,6 +269,54 @@ def test_prefill_bad_offsets_stay_in_bounds(dev):
     assert torch.equal(out[10:90], moe.attention_prefill(q[10:90], k[10:90], v[10:90]))
 
 
+SPLIT = [([5], [5000], 16, 2, 256), ([1], [9001], 16, 2, 256), ([1], [700], 1, 1, 128), ([3, 40], [3000, 6000], 8, 2, 128),
+         ([200], [4000], 8, 4, 128), ([0, 17, 0, 300], [9, 20, 0, 6000], 8, 1, 256), ([60, 2], [2500, 1], 5, 5, 128),
+         ([2, 2, 2, 2], [4000, 100, 0, 3000], 12, 2, 256), ([500], [1900], 8, 2, 256), ([33], [2048], 64, 1, 128)]
+
+
+@pytest.mark.parametrize("ql,kl,Hq,Hk,D", SPLIT)
+def test_prefill_few_queries_over_many_keys(dev, ql, kl, Hq, Hk, D):
+    """The keys are cut into parts: sequences with fewer tiles than parts, with
+    queries that see nothing, and rows of no sequence, which stay."""
+    from sparse_mixture_experts_gemm_gb300 import attention
+    N, M, front = sum(ql), sum(kl), 3
+    if M >= 2000:  # (700 keys, and 500 queries over 1,900, are not worth a second kernel)
+        assert attention._prefill_workspace(N + 2 * front, M, len(ql), Hq, Hk, D) > 0
+    q, k, v = prefill_inputs(N + M, N + 2 * front, M, Hq, Hk, D)
+    oq, ok = ends(ql) + front, ends(kl)
+    out = torch.full((N + 2 * front, Hq, D), 7.0, dtype=BF16, device=dev)
+    moe.attention_prefill(q.to(dev), k.to(dev), v.to(dev), oq.to(dev), ok.to(dev), out=out)
+    check_attend(out[front:-front], q[front:-front], k, v, D ** -0.5, oq - front, ok)
+    assert (out[:front] == 7).all() and (out[-front:] == 7).all()
+    again = torch.full_like(out, 7.0)
+    moe.attention_prefill(q.to(dev), k.to(dev), v.to(dev), oq.to(dev), ok.to(dev), out=again)
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("what", ["nan", "inf"])
+def test_prefill_hidden_tokens_of_parts(dev, D, what):
+    """As above, where the keys are cut: a token among the last, which some queries
+    see, and one that all of them see."""
+    T, M = 40, 3000
+    q, k, v = prefill_inputs(D, T, M + 70, 8, 2, D)
+    oq, ok = torch.tensor([0, T], dtype=I32, device=dev), torch.tensor([0, M], dtype=I32, device=dev)
+    ref = moe.attention_prefill(q.to(dev), k.to(dev), v.to(dev), oq, ok).cpu()
+    x = float(what)
+    for at in (M - 1, M - 20, M - T, 1500, M, M + 69):  # the last two: behind the sequence
+        for side in ("k", "v"):
+            k2, v2 = k.clone(), v.clone()
+            (k2 if side == "k" else v2)[at, 1, 5] = x
+            got = moe.attention_prefill(q.to(dev), k2.to(dev), v2.to(dev), oq, ok).cpu()
+            keep = torch.ones(T, 8, dtype=torch.bool)
+            if at < M:
+                keep[max(0, at - (M - T)):, 4:] = False
+            assert torch.equal(got[keep], ref[keep])
+            if at < M and (side == "v" or what == "nan"):
+                hit = got[max(0, at - (M - T)):, 4:].float()
+                assert (~torch.isfinite(hit[..., 5]) if side == "v" else ~torch.isfinite(hit).all(-1)).all()
+
+
 def test_prefill_is_repeatable(dev):
     q, k, v = (x.to(dev) for x in prefill_inputs(5, 1500, 1500, 16, 2, 256))
     first = moe.attention_prefill(q, k, v)
