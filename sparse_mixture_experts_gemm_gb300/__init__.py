@@ -47,8 +47,8 @@ EXPORTED = ["moe_create", "moe_route", "moe_forward", "moe_forward_routed", "moe
             "moe_decode_noalloc", "moe_noalloc_status", "moe_create_q4", "moe_quantize_q4",
             "gdn_scan", "moe_add_rmsnorm", "moe_add_rmsnorm_fp8", "moe_quantize_fp8",
             "moe_matmul_fp8", "gdn_decay_scan", "gdn_decay_workspace", "moe_qk_norm_rope",
-            "moe_attention_prefill", "moe_attention_prefill_workspace", "moe_kv_write", "moe_kv_read", "moe_attention_decode",
-            "moe_attention_decode_workspace"]
+            "moe_attention_prefill", "moe_attention_prefill_workspace", "moe_kv_write",
+            "moe_kv_read", "moe_attention_decode", "moe_attention_decode_workspace"]
 
 Q4_GROUP = 64  # columns per (scale, bias) pair of the 4-bit format
 

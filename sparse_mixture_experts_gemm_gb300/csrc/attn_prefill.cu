@@ -31,7 +31,9 @@
 // rows while the others work.  Tiles are numbered by falling number of key tiles over
 // all sequences, and cluster c of P takes the numbers c, 2P - 1 - c, 2P + c, ..: the
 // largest go first and the sums stay even.  The next tile's copies and scores run
-// during the outputs of the one before.
+// during the outputs of the one before.  Where tiles are few, or some see many more
+// keys than others, their keys are cut into parts: outputs without the division,
+// maxima and sums go to the workspace, and a second kernel joins them in order.
 //
 // A key or value row that some of the tile's queries must not see is masked in
 // the scores; but 0 x NaN is NaN, so in the tiles at the causal edge (and at a
@@ -67,9 +69,9 @@ struct PrefillArgs {
   uint32_t per_mul, per_shift;       // x / (2 tokens) = (x per_mul >> 32) >> per_shift, x < 2^31
   float scale;                       // times log2(e)
   int *status;
-  int splits;   // parts of each tile's keys
-  float *part;  // (splits > 1) [splits][n_q][Hq][D]: outputs before the division
-  float2 *stat; // [splits][n_q][Hq]: maximum, sum
+  int parts, length;  // most parts of a tile's keys (1: none are cut), key tiles of a part
+  float *part;        // (parts > 1) [parts][n_q][Hq][D]: outputs before the division
+  float2 *stat;       // [parts][n_q][Hq]: maximum, sum
 };
 
 struct Item {
@@ -237,7 +239,9 @@ __device__ __forceinline__ bool warp_wait(const PrefillArgs &a, uint32_t bar, ui
   return false;
 }
 
-// The schedule (one warp): tiles of rows by falling number of key tiles.
+// The schedule (one warp): tiles of rows by falling number of key tiles; kCut: keys of
+// some are cut into parts.
+template <bool kCut>
 struct Schedule {
   const PrefillArgs &a;
   int per;           // queries of a tile
@@ -286,18 +290,59 @@ struct Schedule {
     for (int i0 = 0; i0 < a.n_seq; i0 += 32) sum += __reduce_add_sync(0xffffffffu, mine(i0, c));
     return sum;
   }
-  // tiles and parts of all heads; the n-th of them
-  __device__ __forceinline__ long long total() const { return all(0) * a.Hk * a.splits; }
+  // tiles that have a p-th part: the first so many, as they are in falling order
+  __device__ __forceinline__ int from(int p) const { return p == 0 ? 0 : p * a.length + 1; }
+  // Parts in their order: all second ones, all third ones, .., then the first, which
+  // alone may be short in great number; lane i has those up to the i-th kind.
+  __device__ __forceinline__ int kind(int i) const { return i + 1 < a.parts ? i + 1 : 0; }
+  __device__ __forceinline__ long long parts_upto(long long &mine_of) const {
+    const int lane = threadIdx.x & 31;
+    mine_of = 0;
+    if (a.n_seq <= 32) {
+      for (int i = 0; i < a.n_seq; ++i) {
+        const int queries = __shfl_sync(0xffffffffu, lq, i), ahead = __shfl_sync(0xffffffffu, shift, i);
+        if (lane < a.parts) mine_of += least(queries, ahead, from(kind(lane)));
+      }
+    } else {
+      for (int i = 0; i < a.parts; ++i) {
+        const long long tiles = all(from(kind(i)));
+        if (lane == i) mine_of = tiles;
+      }
+    }
+    long long upto = mine_of;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += u;
+    }
+    return upto;
+  }
+  __device__ __forceinline__ long long total() const {
+    if (!kCut) return all(0) * a.Hk;
+    long long own;
+    return __shfl_sync(0xffffffffu, parts_upto(own), 31) * a.Hk;
+  }
+  // the n-th part of a tile; n < total()
   __device__ __forceinline__ Item find(long long n) const {
+    const int head = static_cast<int>(n % a.Hk);
+    long long left = n / a.Hk;
+    int part = 0;
+    if (kCut) {
+      long long own;
+      const long long upto = parts_upto(own);
+      const int i = __ffs(__ballot_sync(0xffffffffu, upto > left)) - 1;
+      left -= __shfl_sync(0xffffffffu, upto - own, i);
+      part = kind(i);
+    }
+    return tile(left, head, part);
+  }
+  // the left-th tile
+  __device__ __forceinline__ Item tile(long long left, int head, int part) const {
     const int lane = threadIdx.x & 31;
     Item it = {};
     it.valid = 1;
-    if (a.splits > 1) {
-      it.part = static_cast<int>(n % a.splits);
-      n /= a.splits;
-    }
-    it.head = static_cast<int>(n % a.Hk);
-    long long left = n / a.Hk;
+    it.head = head;
+    it.part = part;
     if (alike) {  // the last tiles of all sequences, then those before
       const int back = static_cast<int>(left / a.n_seq), i = static_cast<int>(left % a.n_seq);
       int k1;
@@ -411,17 +456,21 @@ struct Cleaner {
 };
 
 // What the roles derive from an item
+template <bool kCut>
 struct Tile {
   int shift, mine;  // keys less queries, this CTA's first query
   int j0, nk, jm;   // first key tile of this part, how many, from which of them on some query must not see a key
+  int parts;        // of the tile
   __device__ __forceinline__ Tile(const PrefillArgs &a, const Item &it, int rank) {
     shift = it.lk - it.lq;
     const int end = min(it.t0 + 2 * a.tokens, it.lq);
     nk = (max(0, end + shift) + kKeys - 1) / kKeys;
     j0 = 0;
-    if (a.splits > 1) {
-      j0 = nk * it.part / a.splits;
-      nk = nk * (it.part + 1) / a.splits - j0;
+    parts = 1;
+    if (kCut && nk > a.length) {
+      parts = (nk + a.length - 1) / a.length;
+      j0 = it.part * a.length;
+      nk = min(nk - j0, a.length);
     }
     jm = max(0, max(0, it.t0 + shift + 1) / kKeys - j0);
     mine = it.t0 + rank * a.tokens;
@@ -430,7 +479,7 @@ struct Tile {
 
 }  // namespace
 
-template <int D>
+template <int D, bool kCut>
 __global__ void __launch_bounds__(kThreadsA, 1)
     attn_prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const PrefillArgs a) {
@@ -485,7 +534,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   long long total = 0;
   if (warp == 10) {  // the first item, meanwhile
     pdl_wait();
-    const Schedule plan(a);
+    const Schedule<kCut> plan(a);
     total = plan.total();
     Item it = {};
     if ((blockIdx.x >> 1) < total) it = plan.find(blockIdx.x >> 1);
@@ -512,7 +561,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
 
   if (warp == 10) {
     // ------------------------------------------------------------ schedule
-    const Schedule plan(a);
+    const Schedule<kCut> plan(a);
     const long long clusters = gridDim.x >> 1, c = blockIdx.x >> 1;
     if (lane == 0) mbar_arrive(smem_u32(&ctl.it_full[0]));
     __syncwarp();
@@ -536,7 +585,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     bool ok = true;
     Item it;
     for (int k = 0, used = 0; ok && next_item(k, it); ++k) {
-      const Tile t(a, it, rank);
+      const Tile<kCut> t(a, it, rank);
       if (t.nk == 0) continue;
       if (lane == 0) {
         // Q, once the scores of the tile before are made
@@ -607,7 +656,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       int r = 0, done = 0;  // uses of the ring; key tiles of the items before
       bool ok = true;
       for (int k = 0, used = 0; ok && next_item(k, it); ++k) {
-        const Tile t(a, it, rank);
+        const Tile<kCut> t(a, it, rank);
         if (t.nk == 0) continue;
         ok = warp_wait(a, smem_u32(&ctl.q_full), used & 1, abort_flag, SITE_MMA_FULL);
         ++used;
@@ -664,7 +713,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       int done = 0;
       bool ok = true;
       for (int k = 0; ok && next_item(k, it); ++k) {
-        const Tile t(a, it, rank);
+        const Tile<kCut> t(a, it, rank);
         for (int j = 0; ok && j < t.nk; ++j) {
           const int n = done + j;
           ok = warp_wait(a, smem_u32(&ctl.p_loc[n & 1]), (n >> 1) & 1, abort_flag, SITE_STAGE);
@@ -707,7 +756,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       }
     };
     for (int k = 0; ok && next_item(k, it); ++k) {
-      const Tile t(a, it, rank);
+      const Tile<kCut> t(a, it, rank);
       const uint32_t bad = smem_u32(&ctl.bad[used][0]), flag = smem_u32(&ctl.hit[used]);
       const int own = max(0, t.mine + t.shift + 1) / kKeys - t.j0;  // first tile masked for this CTA
       float f0[2], f1[2];  // factors of the outputs of this thread's two rows there
@@ -819,7 +868,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         for (int z = 0; z < 2; ++z) {
           l[z] += __shfl_xor_sync(0xffffffffu, l[z], 1);
           l[z] += __shfl_xor_sync(0xffffffffu, l[z], 2);
-          f0[z] = a.splits > 1 ? 1.0f : 1.0f / l[z];
+          f0[z] = kCut && t.parts > 1 ? 1.0f : 1.0f / l[z];
           stat[z] = make_float2(m[z], l[z]);
         }
       } else {
@@ -950,7 +999,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
           f0[z] = s0.x == M ? 1.0f : fast_exp2((s0.x - M) * c);
           f1[z] = s1.x == M ? 1.0f : fast_exp2((s1.x - M) * c);
           stat[z] = make_float2(M, f0[z] * s0.y + f1[z] * s1.y);
-          const float inv = a.splits > 1 ? 1.0f : 1.0f / stat[z].y;
+          const float inv = kCut && t.parts > 1 ? 1.0f : 1.0f / stat[z].y;
           f0[z] *= inv;
           f1[z] *= inv;
         }
@@ -959,7 +1008,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
 #pragma unroll
       for (int z = 0; z < 2; ++z)
         row[z] = static_cast<long long>(it.q0 + t.mine + (valid[z] ? token[z] : 0)) * a.Hq + it.head * a.group + head[z];
-      if (a.splits > 1) {
+      if (kCut && t.parts > 1) {
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           row[z] += it.part * a.n_q * a.Hq;
@@ -1004,7 +1053,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
             }
           }
         }
-        if (a.splits > 1) {
+        if (kCut && t.parts > 1) {
 #pragma unroll
           for (int z = 0; z < 2; ++z)
             if (valid[z]) {
@@ -1045,8 +1094,8 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     for (int i = 0; i < 200; ++i) __nanosleep(1000);
 }
 
-// Joins the parts of tiles whose keys were split: a block has some of a tile's 256
-// rows, found as the main kernel finds them; D / 4 threads per row.
+// Joins the parts of tiles whose keys were cut: a block has some of a tile's 256 rows,
+// found as the main kernel finds them; D / 4 threads per row.
 constexpr int kJoinThreads = 1024;
 template <int D>
 constexpr int kJoinRows = kJoinThreads / (D / 4);
@@ -1059,9 +1108,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_prefill_join_kernel(const P
   pdl_launch_dependents();
   const long long n = blockIdx.x / kBlocks;
   if (threadIdx.x < 32) {
-    const Schedule plan(a);
+    const Schedule<true> plan(a);
     Item it = {};
-    if (n * a.splits < plan.total()) it = plan.find(n * a.splits);
+    if (n / a.Hk < plan.all(plan.from(1))) it = plan.tile(n / a.Hk, static_cast<int>(n % a.Hk), 0);
     if (threadIdx.x == 0) s_item = it;
   }
   __syncthreads();
@@ -1073,8 +1122,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_prefill_join_kernel(const P
   if (r >= a.tokens * a.group || t >= it.lq) return;  // (whole warps)
   const long long row = static_cast<long long>(it.q0 + t) * a.Hq + it.head * a.group + r % a.group, step = a.n_q * a.Hq;
   // lane s of a warp, all of one row, has part s's maximum and sum
-  const int lane = static_cast<int>(threadIdx.x) & 31;
-  const float2 ml = lane < a.splits ? a.stat[row + lane * step] : make_float2(-INFINITY, 0.0f);
+  const int lane = static_cast<int>(threadIdx.x) & 31, parts = Tile<true>(a, it, 0).parts;
+  const float2 ml = lane < parts ? a.stat[row + lane * step] : make_float2(-INFINITY, 0.0f);
   float M = ml.x;
 #pragma unroll
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -1085,7 +1134,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_prefill_join_kernel(const P
   for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-  for (int s0 = 0; s0 < a.splits; s0 += 8) {
+  for (int s0 = 0; s0 < parts; s0 += 8) {
     float4 y[8];
 #pragma unroll
     for (int s = 0; s < 8; ++s)
@@ -1143,27 +1192,36 @@ const PrefillDevice &prefill_device() {
       cfg.numAttrs = 1;
       return cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) == cudaSuccess && clusters > 0;
     };
-    if (d.status && set(attn_prefill_kernel<128>, Plan<128>::kTotal, d.clusters[0]) &&
-        set(attn_prefill_kernel<256>, Plan<256>::kTotal, d.clusters[1]))
+    int cut[2];  // (as many)
+    if (d.status && set(attn_prefill_kernel<128, false>, Plan<128>::kTotal, d.clusters[0]) &&
+        set(attn_prefill_kernel<256, false>, Plan<256>::kTotal, d.clusters[1]) &&
+        set(attn_prefill_kernel<128, true>, Plan<128>::kTotal, cut[0]) &&
+        set(attn_prefill_kernel<256, true>, Plan<256>::kTotal, cut[1]))
       d.rc = MOE_OK;
   });
   return devs[dev];
 }
 
-// Parts into which each tile's keys are cut where there are few tiles.  Times are in
-// tiles of 128 keys (about 1 us): rounds of clusters of a part's tiles and 3 for its
-// start and end, 5 for the second kernel, and the parts' outputs, which move to and fro
-// at 3 MB a tile's time.  Measured, 16 query heads on 2 of 256: 1 query over 4,096 keys
-// in 16.6 us (16 parts) against 41, over 16,384 in 24 against 142, 64 over 4,096 in 21
-// against 42, 300 over 8,192 in 45 (3 parts) against 76 (4 parts, more than there are
-// clusters: 60); not cut: 5 over 1,024 16.7 (15.4 with 4 parts), 700 over 2,000 26 (48
-// with 2), 1,300 over 4,000 63 (97).  The lengths are on the device: the longest
-// sequence counts as of twice the mean length.
-int splits_of(long long n_q, long long n_k, int n_seq, int n_q_heads, int n_kv_heads, int head_dim) {
-  constexpr int kPairs = 76, kMost = 32;
+// Where there are few tiles of rows, or some see many more keys than others, keys
+// are cut into parts.  Times are in tiles of 128 keys (about 1 us): rounds of clusters
+// of a part's tiles and 3 for its start and end, 5 for the second kernel, and the
+// parts' outputs, which move to and fro at 3 MB a tile's time.  Measured, 16 query heads
+// on 2 of 256: 1 query over 4,096 keys in 17.7 us (16 parts) against 41, over 16,384 in
+// 25 against 142, 64 over 4,096 in 22 against 42, 300 over 8,192 in 45 (3 parts) against
+// 76 (4 parts, more than there are clusters: 60); not cut: 700 over 2,000 26 (48 with 2),
+// 1,300 over 4,000 63 (97).  1,016 queries over 16,484 keys packed with a prompt of 3,765,
+// 4 heads on 1: 97 in place of 149.
+struct Cut {
+  int parts, length;
+};
+Cut cut_of(long long n_q, long long n_k, int n_seq, int n_q_heads, int n_kv_heads, int head_dim) {
+  constexpr int kPairs = 76, kMost = 16, kUneven = 8;
   const long long per = 2 * (128 / (n_q_heads / n_kv_heads));
   const long long tiles = ((n_q + per - 1) / per + n_seq - 1) * n_kv_heads;
-  const long long keys = ((n_seq > 2 ? 2 * (n_k / n_seq) : n_k) + kKeys - 1) / kKeys;
+  // The lengths are on the device: for the first rule the longest sequence counts as of
+  // twice the mean length.
+  const long long all = (n_k + kKeys - 1) / kKeys, mean = (n_k / n_seq + kKeys - 1) / kKeys;
+  const long long keys = n_seq > 2 ? 2 * mean : all;
   const double moved = static_cast<double>(n_q) * n_q_heads * head_dim * 4 / 3e6;
   auto time = [&](int s) {
     const long long rounds = (tiles * s + kPairs - 1) / kPairs;
@@ -1176,7 +1234,20 @@ int splits_of(long long n_q, long long n_k, int n_seq, int n_q_heads, int n_kv_h
       least = time(s);
       best = s;
     }
-  return best;
+  long long length = (keys + best - 1) / best, most = kMost;
+  if (best == 1) {
+    // Several sequences with keys before their queries may differ by any factor (where
+    // all keys have their queries a long sequence has many tiles, and all clusters
+    // work).  The longest are cut to about a cluster's share of the work, if one
+    // sequence of all the keys would be far longer than that.
+    if (n_seq == 1 || n_k == n_q || tiles > 2 * kPairs) return {1, 0};
+    length = tiles * mean / (2 * kPairs);
+    if (length < 16) length = 16;
+    if (all < 2 * length) return {1, 0};
+    most = kUneven;
+  }
+  if (length < (all + most - 1) / most) length = (all + most - 1) / most;
+  return {static_cast<int>((all + length - 1) / length), static_cast<int>(length)};
 }
 
 template <int D>
@@ -1188,8 +1259,9 @@ cudaError_t launch_prefill(const CUtensorMap &mq, const CUtensorMap &mk, const C
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D>, mq, mk, mv, a);
-  if (e != cudaSuccess || a.splits == 1) return e;
+  if (a.parts == 1) return cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D, false>, mq, mk, mv, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, attn_prefill_kernel<D, true>, mq, mk, mv, a);
+  if (e != cudaSuccess) return e;
   return launch_attn(attn_prefill_join_kernel<D>, dim3(static_cast<unsigned>(tiles * (256 / kJoinRows<D>))), kJoinThreads, 0, st,
                      a);
 }
@@ -1209,8 +1281,8 @@ extern "C" int moe_attention_prefill_workspace(long long n_q, long long n_k, int
     return MOE_ERR_UNSUPPORTED;
   *bytes = 0;
   if (n_q == 0 || n_seq == 0) return MOE_OK;
-  const int splits = splits_of(n_q, n_k, n_seq, n_q_heads, n_kv_heads, head_dim);
-  if (splits > 1) *bytes = splits * static_cast<size_t>(n_q) * n_q_heads * (head_dim * sizeof(float) + sizeof(float2));
+  const int parts = cut_of(n_q, n_k, n_seq, n_q_heads, n_kv_heads, head_dim).parts;
+  if (parts > 1) *bytes = parts * static_cast<size_t>(n_q) * n_q_heads * (head_dim * sizeof(float) + sizeof(float2));
   return MOE_OK;
 }
 
@@ -1256,9 +1328,11 @@ extern "C" int moe_attention_prefill(const void *q, const void *k, const void *v
   a.tokens = 128 / a.group;
   a.scale = scale * 1.4426950408889634f;
   a.status = dev.status;
-  a.splits = splits_of(n_q, n_k, n_seq, n_q_heads, n_kv_heads, head_dim);
+  const Cut cut = cut_of(n_q, n_k, n_seq, n_q_heads, n_kv_heads, head_dim);
+  a.parts = cut.parts;
+  a.length = cut.length;
   a.part = static_cast<float *>(workspace);
-  if (a.splits > 1) a.stat = reinterpret_cast<float2 *>(a.part + a.splits * n_q * n_q_heads * head_dim);
+  if (a.parts > 1) a.stat = reinterpret_cast<float2 *>(a.part + a.parts * n_q * n_q_heads * head_dim);
   // x / d = (x m) >> (31 + s), x < 2^31, with 2^(s - 1) < d <= 2^s and m = 2^(31 + s) / d + 1
   const uint32_t divisor = 2 * a.tokens;
   uint32_t s = 1;
@@ -1269,7 +1343,7 @@ extern "C" int moe_attention_prefill(const void *q, const void *k, const void *v
   const long long per = 2 * a.tokens;
   const long long tiles = (offsets ? n_q / per + n_seq : n_seq * ((n_q / n_seq + per - 1) / per)) * n_kv_heads;
   const int most = dev.clusters[head_dim == 256];
-  const int clusters = tiles * a.splits < most ? static_cast<int>(tiles * a.splits) : most;
+  const int clusters = tiles * a.parts < most ? static_cast<int>(tiles * a.parts) : most;
   const uint64_t d = head_dim, hk = n_kv_heads;
   const uint64_t keys = n_k > 0 ? n_k : 1;  // (no key is read where there is none)
   const void *kb = n_k > 0 ? k : q, *vb = n_k > 0 ? v : q;

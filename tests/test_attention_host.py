@@ -140,7 +140,8 @@ def test_prefill_workspace(lib):
         return need.value
 
     assert size(4096, 4096, 1, 16, 2, 256) == 0 and size(17, 17, 1, 16, 2, 256) == 0 and size(64, 256, 2, 8, 2, 128) == 0
-    for a in ((1, 4096, 1, 16, 2, 256), (40, 20000, 1, 32, 8, 128), (8, 65536, 4, 4, 4, 256), (1, 1 << 29, 1, 64, 1, 128)):
+    for a in ((1, 4096, 1, 16, 2, 256), (40, 20000, 1, 32, 8, 128), (8, 65536, 4, 4, 4, 256), (1, 1 << 29, 1, 64, 1, 128),
+              (4781, 20254, 2, 4, 1, 256), (2000, 50000, 8, 8, 2, 256)):
         row = a[0] * a[3] * (a[5] * 4 + 8)
         parts = size(*a) // row
         assert 2 <= parts <= 32 and need.value == parts * row

@@ -271,7 +271,8 @@ def test_prefill_bad_offsets_stay_in_bounds(dev):
 
 SPLIT = [([5], [5000], 16, 2, 256), ([1], [9001], 16, 2, 256), ([1], [700], 1, 1, 128), ([3, 40], [3000, 6000], 8, 2, 128),
          ([200], [4000], 8, 4, 128), ([0, 17, 0, 300], [9, 20, 0, 6000], 8, 1, 256), ([60, 2], [2500, 1], 5, 5, 128),
-         ([2, 2, 2, 2], [4000, 100, 0, 3000], 12, 2, 256), ([500], [1900], 8, 2, 256), ([33], [2048], 64, 1, 128)]
+         ([2, 2, 2, 2], [4000, 100, 0, 3000], 12, 2, 256), ([500], [1900], 8, 2, 256), ([33], [2048], 64, 1, 128),
+         ([1500, 130], [1510, 7000], 4, 1, 256), ([900, 0, 70, 40, 300], [900, 5, 4000, 6000, 310], 8, 2, 128)]
 
 
 @pytest.mark.parametrize("ql,kl,Hq,Hk,D", SPLIT)
