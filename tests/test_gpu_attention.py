@@ -9,8 +9,9 @@ Tolerances, from the arithmetic (half a step of bf16 is 2^-8 of a value):
     its weight by scale times that, in the numerator and in the sum; sums over L
     keys on hardware that truncates: (L / 16 + 64) 2^-23 of A;
   * decode: the same, but what is rounded is weight times scale, which multiplies
-    codes less 8: at most 8 p_t scale_t each; the rest is fp32 of magnitudes at
-    most 15 scale + |bias|;
+    codes less 8: at most 8 p_t scale_t each; the weights that multiply biases
+    are two bf16 parts (the second rounds what the first, off by 2^-8, leaves: 2^-16
+    of the weight); the rest is fp32 of magnitudes at most 15 scale + |bias|;
   * the cache: codes, scales and biases exactly those of the definition, values
     within half a step.
 """
@@ -272,6 +273,7 @@ def test_prefill_bad_offsets_stay_in_bounds(dev):
 SPLIT = [([5], [5000], 16, 2, 256), ([1], [9001], 16, 2, 256), ([1], [700], 1, 1, 128), ([3, 40], [3000, 6000], 8, 2, 128),
          ([200], [4000], 8, 4, 128), ([0, 17, 0, 300], [9, 20, 0, 6000], 8, 1, 256), ([60, 2], [2500, 1], 5, 5, 128),
          ([2, 2, 2, 2], [4000, 100, 0, 3000], 12, 2, 256), ([500], [1900], 8, 2, 256), ([33], [2048], 64, 1, 128),
+         ([1] * 40, [(37 * i) % 300 for i in range(39)] + [9000], 8, 1, 128),
          ([1500, 130], [1510, 7000], 4, 1, 256), ([900, 0, 70, 40, 300], [900, 5, 4000, 6000, 310], 8, 2, 128)]
 
 
@@ -292,6 +294,36 @@ def test_prefill_few_queries_over_many_keys(dev, ql, kl, Hq, Hk, D):
     again = torch.full_like(out, 7.0)
     moe.attention_prefill(q.to(dev), k.to(dev), v.to(dev), oq.to(dev), ok.to(dev), out=again)
     assert torch.equal(again, out)
+
+
+def test_prefill_few_queries_dense(dev):
+    """[n][T] queries over [n][M] keys in parts."""
+    q, k, v = prefill_inputs(77, 4 * 3, 4 * 3000, 8, 2, 256)
+    got = moe.attention_prefill(*(x.to(dev).unflatten(0, (4, -1)) for x in (q, k, v)))
+    check_attend(got.flatten(0, 1), q, k, v, 256 ** -0.5, ends([3] * 4), ends([3000] * 4))
+
+
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+@pytest.mark.parametrize("D", [128, 256])
+def test_queries_that_are_not_finite_keep_to_themselves(dev, D, bad):
+    for T, M in ((150, 150), (3, 3000)):
+        q, k, v = (x.to(dev) for x in prefill_inputs(T + D, T, M, 8, 2, D))
+        ref = moe.attention_prefill(q, k, v)
+        q[1, 5, 7] = float(bad)
+        got = moe.attention_prefill(q, k, v)
+        keep = torch.ones(T, 8, dtype=torch.bool, device=dev)
+        keep[1, 5] = False
+        assert torch.equal(got[keep], ref[keep]) and not torch.isfinite(got[1, 5]).all()
+    g = gen(D)
+    table, P = make_table(g, [70, 900])
+    cache, L = random_cache(g, P, 2, D, dev), torch.tensor([70, 900], dtype=I32, device=dev)
+    q = normal(g, 2, 8, D).to(dev)
+    ref = moe.attention_decode(q, cache, table.to(dev), L)
+    q[1, 5, 7] = float(bad)
+    got = moe.attention_decode(q, cache, table.to(dev), L)
+    keep = torch.ones(2, 8, dtype=torch.bool, device=dev)
+    keep[1, 5] = False
+    assert torch.equal(got[keep], ref[keep]) and not torch.isfinite(got[1, 5]).all()
 
 
 @pytest.mark.parametrize("D", [128, 256])
@@ -481,7 +513,7 @@ def check_decode(got, q, cache, table, lens, scale):
                                     [0, 1], [0, L])
         score = 2 * scale * reach * (D / 8 + 8) * 2.0 ** -23
         tol = 2.0 ** -8 * (np.abs(ref) + rounded) * (1 + 2.0 ** -6) + \
-            mag * ((L / 16 + 64) * 2.0 ** -23 + score[..., None])
+            mag * (2.0 ** -16 + (L / 16 + 64) * 2.0 ** -23 + score[..., None])
         err = np.abs(f64(got[i:i + 1]) - ref)
         assert (err <= tol).all(), (i, L, (err / tol).max())
 
