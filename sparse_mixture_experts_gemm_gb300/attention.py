@@ -17,7 +17,7 @@ import functools
 import torch
 
 from . import MoeError
-from .mixer import _BF16, _F32, _device, _given, _lib, _on, _tokens, _vector
+from .mixer import _BF16, _device, _given, _lib, _on, _tokens, _vector
 
 PAGE = 64   # tokens per page of a cache
 GROUP = 64  # columns that share a scale and a bias
