@@ -40,14 +40,16 @@
 // sequence's end) values that are not finite are taken out of V in shared memory,
 // and the queries that do see them are set to NaN in the end.
 //
-// Measured: 4,096 tokens of 16 heads of 256 on 2 in 83 us (1.65 PFLOP/s, tensor pipes
+// Measured: 4,096 tokens of 16 heads of 256 on 2 in 81.5 us (1.69 PFLOP/s, tensor pipes
 // busy 73 % of the cycles; the rest goes at the changes of tile, about 4,500 cycles
 // each), 8,192 behind 24,576 in 1.85 ms (2.1 PFLOP/s); 2 x 2,048 tokens of 32 heads of
-// 128 on 8 in 88 us (0.78 PFLOP/s, the handover between softmax and products, 1,800
-// cycles a tile).
+// 128 on 8 in 84 us (0.82 PFLOP/s, the handover between softmax and products, about
+// 1,700 cycles a tile).
 //
-// Roles (352 threads): warp 0 TMA copies; warp 1 the MMAs (CTA 0), or telling CTA 0
-// that P is there (CTA 1); warps 2-9 the softmax and the outputs; warp 10 the schedule.
+// Roles (352 threads): warp 0 TMA copies; warp 1 the MMAs (CTA 0); warps 2-9 the
+// softmax and the outputs, each telling CTA 0 that its P is there (through a warp of
+// CTA 1 that gathered these, 2 x 2,048 tokens of 128 took 87.4 us in place of 84.2);
+// warp 10 the schedule.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -90,7 +92,7 @@ struct Item {
 template <int D>
 struct Ctl {
   uint64_t full[10], empty[10], vloc[10];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], p_loc[2], pv_done, o_full, drain;
+  uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done, o_full, drain;
   uint64_t it_full[kItems], it_empty[kItems];
   uint32_t tmem, sink;
   int abort_flag;
@@ -509,14 +511,13 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&ctl.s_full[b]), 1);
       mbar_init(smem_u32(&ctl.p_full[b]), P::kMakers);
-      mbar_init(smem_u32(&ctl.p_loc[b]), P::kMakers);
     }
     mbar_init(smem_u32(&ctl.pv_done), 1);
     mbar_init(smem_u32(&ctl.o_full), 1);
     mbar_init(smem_u32(&ctl.drain), 1);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(smem_u32(&ctl.it_full[i]), 1);
-      mbar_init(smem_u32(&ctl.it_empty[i]), kReaders);
+      mbar_init(smem_u32(&ctl.it_empty[i]), rank == 0 ? kReaders : kReaders - 1);  // (no MMAs in CTA 1)
     }
     ctl.abort_flag = 0;
     fence_mbar_init();
@@ -714,20 +715,6 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         if (one) tc_commit2(smem_u32(&ctl.drain));
         if (!poll(smem_u32(&ctl.drain), 0, nullptr) && lane == 0) fail(a, abort_flag, SITE_DRAIN);
       }
-    } else {
-      // ------------------------------------------------------------ P is there
-      int done = 0;
-      bool ok = true;
-      for (int k = 0; ok && next_item(k, it); ++k) {
-        const Tile<kCut> t(a, it, rank);
-        for (int j = 0; ok && j < t.nk; ++j) {
-          const int n = done + j;
-          ok = warp_wait(a, smem_u32(&ctl.p_loc[n & 1]), (n >> 1) & 1, abort_flag, SITE_STAGE);
-          const uint32_t to = cluster_map(smem_u32(&ctl.p_full[n & 1]), 0);
-          if (ok && lane == 0) st_async_tx4(cluster_map(smem_u32(&ctl.sink), 0), 0u, to);  // (nothing reads the word)
-        }
-        done += t.nk;
-      }
     }
   } else {
     // ------------------------------------------------------------ softmax, outputs
@@ -753,9 +740,10 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       __syncwarp();
       if (lane == 0) {
         if (rank == 1) {
-          mbar_arrive(smem_u32(&ctl.p_loc[n & 1]));
+          // (a remote arrival would hold the warp for a round trip; nothing reads the word)
+          st_async_tx4(cluster_map(smem_u32(&ctl.sink), 0), 0u, cluster_map(smem_u32(&ctl.p_full[n & 1]), 0));
         } else if (wq == 2 && (P::kStreams == 2 || half == 0)) {
-          mbar_arrive_expect_tx(smem_u32(&ctl.p_full[n & 1]), 4);  // the other CTA's word
+          mbar_arrive_expect_tx(smem_u32(&ctl.p_full[n & 1]), 4 * P::kMakers);  // the other CTA's words
         } else {
           mbar_arrive(smem_u32(&ctl.p_full[n & 1]));
         }
