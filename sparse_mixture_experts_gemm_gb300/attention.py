@@ -34,7 +34,8 @@ def _heads(name, t):
     """(tokens, heads, width) of [..., heads, width]"""
     if t.dim() not in (2, 3, 4):
         raise ValueError(f"{name} must be [..., heads, head_dim]")
-    H, w = t.shape[-2:]
+    shape = t.shape
+    H, w = shape[-2], shape[-1]
     if H * w == 0:
         raise ValueError(f"{name} must have heads and columns")
     return t.numel() // (H * w), H, w
@@ -165,10 +166,11 @@ def kv_cache(pages, heads, head_dim, device="cuda"):
 def _cache(cache):
     """(codes, affine, pages, heads, head_dim)"""
     codes, affine = cache
-    if codes.dim() != 5 or codes.shape[1] != 2 or codes.shape[3] != PAGE:
-        raise ValueError("codes must be uint8 [pages][2][heads][64][head_dim / 2]")
-    P, _, H, _, half = codes.shape
-    _given("codes", codes, (P, 2, H, PAGE, half), torch.uint8)
+    shape = codes.shape
+    if len(shape) != 5 or shape[1] != 2 or shape[3] != PAGE or codes.dtype != torch.uint8 \
+            or not codes.is_contiguous() or not codes.is_cuda:
+        raise ValueError("codes must be a contiguous CUDA uint8 tensor [pages][2][heads][64][head_dim / 2]")
+    P, _, H, _, half = shape
     _given("affine", affine, (P, 2, H, PAGE, 2 * half // GROUP, 2), _BF16)
     return codes, affine, P, H, 2 * half
 
@@ -186,13 +188,14 @@ def kv_cache_write(cache, k, v, pages, starts=None, offsets=None, stream=None):
     codes, affine, P, H, D = _cache(cache)
     n, width = _table(pages)
     dims = k.dim()
-    if dims not in (3, 4) or k.shape != v.shape or tuple(k.shape[-2:]) != (H, D):
+    shape = k.shape
+    if dims not in (3, 4) or shape != v.shape or shape[-2] != H or shape[-1] != D:
         raise ValueError("k and v must be [n][T][H][D] or [N][H][D] with the cache's heads")
-    N, op = k.numel() // (H * D), None
+    N, op = shape[0] if dims == 3 else shape[0] * shape[1], None
     if dims == 4:
         if offsets is not None:
             raise ValueError("offsets go with packed tokens [N][H][D]")
-        m = k.shape[0]
+        m = shape[0]
     elif offsets is None:
         m = 1
     else:
@@ -227,7 +230,7 @@ def kv_cache_read(cache, pages, offsets, tokens, starts=None, k_out=None, v_out=
         else:
             _given("k_out", k_out, shape, _BF16)
         if v_out is None:
-            v_out = torch.empty(shape, dtype=_BF16, device=codes.device)
+            v_out = torch.empty_like(k_out)
         else:
             _given("v_out", v_out, shape, _BF16)
     _check(_lib().moe_kv_read(codes.data_ptr(), affine.data_ptr(), P, pages.data_ptr(), width,
@@ -251,9 +254,10 @@ def attention_decode(q, cache, pages, lengths, scale=None, out=None, stream=None
     the cache.  scale: D ** -0.5 unless given.  Returns bf16 of q's shape."""
     codes, affine, P, H, D = _cache(cache)
     n, width = _table(pages)
-    if q.dim() != 3 or q.shape[0] != n or q.shape[2] != D or q.shape[1] == 0:
+    shape = q.shape
+    if len(shape) != 3 or shape[0] != n or shape[2] != D or shape[1] == 0:
         raise ValueError("q must be [n][H_q][D] with a row of pages per sequence and the cache's columns")
-    Hq = q.shape[1]
+    Hq = shape[1]
     qs = _tokens("q", q, Hq, D)
     _vector("lengths", lengths, n, _I32)
     need = _decode_workspace(n, width, Hq, H, D)
