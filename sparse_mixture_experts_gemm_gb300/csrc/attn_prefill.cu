@@ -1100,52 +1100,57 @@ __global__ void __launch_bounds__(kJoinThreads) attn_prefill_join_kernel(const P
   __shared__ Item s_item;
   pdl_wait();
   pdl_launch_dependents();
-  const long long n = blockIdx.x / kBlocks;
-  if (threadIdx.x < 32) {
-    const Schedule<true> plan(a);
-    Item it = {};
-    if (n / a.Hk < plan.all(plan.from(1))) it = plan.tile(n / a.Hk, static_cast<int>(n % a.Hk), 0);
-    if (threadIdx.x == 0) s_item = it;
-  }
-  __syncthreads();
-  const Item it = s_item;
-  if (!it.valid) return;
-  const int d = static_cast<int>(threadIdx.x) % (D / 4) * 4;
+  const int d = static_cast<int>(threadIdx.x) % (D / 4) * 4, lane = static_cast<int>(threadIdx.x) & 31;
   const int at = static_cast<int>(blockIdx.x % kBlocks) * kJoinRows<D> + static_cast<int>(threadIdx.x) / (D / 4);
-  const int rank = at >> 7, r = at & 127, t = it.t0 + rank * a.tokens + r / a.group;
-  if (r >= a.tokens * a.group || t >= it.lq) return;  // (whole warps)
-  const long long row = static_cast<long long>(it.q0 + t) * a.Hq + it.head * a.group + r % a.group, step = a.n_q * a.Hq;
-  // lane s of a warp, all of one row, has part s's maximum and sum
-  const int lane = static_cast<int>(threadIdx.x) & 31, parts = Tile<true>(a, it, 0).parts;
-  const float2 ml = lane < parts ? a.stat[row + lane * step] : make_float2(-INFINITY, 0.0f);
-  float M = ml.x;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  const float mine = ml.y == 0.0f ? 0.0f : ml.x == M ? 1.0f : fast_exp2((ml.x - M) * a.scale);
-  const uint32_t seen = __ballot_sync(0xffffffffu, ml.y != 0.0f);  // parts with keys for this row
-  float L = mine * ml.y;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 1
-  for (int s0 = 0; s0 < parts; s0 += 8) {
-    float4 y[8];
-#pragma unroll
-    for (int s = 0; s < 8; ++s)
-      if (seen >> (s0 + s) & 1) y[s] = *reinterpret_cast<const float4 *>(a.part + (row + (s0 + s) * step) * D + d);
-#pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      const float f = __shfl_sync(0xffffffffu, mine, s0 + s);
-      if (!(seen >> (s0 + s) & 1)) continue;
-      o.x = fmaf(f, y[s].x, o.x);
-      o.y = fmaf(f, y[s].y, o.y);
-      o.z = fmaf(f, y[s].z, o.z);
-      o.w = fmaf(f, y[s].w, o.w);
+  const int rank = at >> 7, r = at & 127;
+  const long long step = a.n_q * a.Hq;
+  // (more tiles than the grid has room for only where offsets run backwards)
+  for (long long n = blockIdx.x / kBlocks;; n += gridDim.x / kBlocks) {
+    if (threadIdx.x < 32) {
+      const Schedule<true> plan(a);
+      Item it = {};
+      if (n / a.Hk < plan.all(plan.from(1))) it = plan.tile(n / a.Hk, static_cast<int>(n % a.Hk), 0);
+      if (threadIdx.x == 0) s_item = it;
     }
+    __syncthreads();
+    const Item it = s_item;
+    __syncthreads();
+    if (!it.valid) return;
+    const int t = it.t0 + rank * a.tokens + r / a.group;
+    if (r >= a.tokens * a.group || t >= it.lq) continue;  // (whole warps)
+    const long long row = static_cast<long long>(it.q0 + t) * a.Hq + it.head * a.group + r % a.group;
+    // lane s of a warp, all of one row, has part s's maximum and sum
+    const int parts = Tile<true>(a, it, 0).parts;
+    const float2 ml = lane < parts ? a.stat[row + lane * step] : make_float2(-INFINITY, 0.0f);
+    float M = ml.x;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float mine = ml.y == 0.0f ? 0.0f : ml.x == M ? 1.0f : fast_exp2((ml.x - M) * a.scale);
+    const uint32_t seen = __ballot_sync(0xffffffffu, ml.y != 0.0f);  // parts with keys for this row
+    float L = mine * ml.y;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+    for (int s0 = 0; s0 < parts; s0 += 8) {
+      float4 y[8];
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        if (seen >> (s0 + s) & 1) y[s] = *reinterpret_cast<const float4 *>(a.part + (row + (s0 + s) * step) * D + d);
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const float f = __shfl_sync(0xffffffffu, mine, s0 + s);
+        if (!(seen >> (s0 + s) & 1)) continue;
+        o.x = fmaf(f, y[s].x, o.x);
+        o.y = fmaf(f, y[s].y, o.y);
+        o.z = fmaf(f, y[s].z, o.z);
+        o.w = fmaf(f, y[s].w, o.w);
+      }
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    *reinterpret_cast<uint2 *>(a.out + row * D + d) =
+        make_uint2(bf16x2_bits(o.x * inv, o.y * inv), bf16x2_bits(o.z * inv, o.w * inv));
   }
-  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-  *reinterpret_cast<uint2 *>(a.out + row * D + d) =
-      make_uint2(bf16x2_bits(o.x * inv, o.y * inv), bf16x2_bits(o.z * inv, o.w * inv));
 }
 
 namespace {
@@ -1201,7 +1206,7 @@ const PrefillDevice &prefill_device() {
 // of a part's tiles and 3 for its start and end, 5 for the second kernel, and the
 // parts' outputs, which move to and fro at 3 MB a tile's time.  Measured, 16 query heads
 // on 2 of 256: 1 query over 4,096 keys in 17.7 us (16 parts) against 41, over 16,384 in
-// 25 against 142, 64 over 4,096 in 22 against 42, 300 over 8,192 in 45 (3 parts) against
+// 25 against 142, 64 over 4,096 in 23 against 42, 300 over 8,192 in 47 (3 parts) against
 // 76 (4 parts, more than there are clusters: 60); not cut: 700 over 2,000 26 (48 with 2),
 // 1,300 over 4,000 63 (97).  1,016 queries over 16,484 keys packed with a prompt of 3,765,
 // 4 heads on 1: 97 in place of 149.

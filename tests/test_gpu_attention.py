@@ -296,6 +296,20 @@ def test_prefill_few_queries_over_many_keys(dev, ql, kl, Hq, Hk, D):
     assert torch.equal(again, out)
 
 
+def test_prefill_bad_offsets_in_parts(dev):
+    """Offsets that run to and fro, so that there are more tiles than the sizes alone
+    allow: a row of one sequence has its results, the others lie in several."""
+    q, k, v = prefill_inputs(78, 42, 9000, 16, 1, 128)
+    oq = torch.tensor([0, 40] + [1, 40] * 6, dtype=I32, device=dev)
+    ok = torch.tensor([0, 9000] * 7, dtype=I32, device=dev)
+    from sparse_mixture_experts_gemm_gb300 import attention
+    assert attention._prefill_workspace(42, 9000, 13, 16, 1, 128) > 0
+    out = torch.full((42, 16, 128), 7.0, dtype=BF16, device=dev)
+    moe.attention_prefill(q.to(dev), k.to(dev), v.to(dev), oq, ok, out=out)
+    check_attend(out[:1], q[:1], k[:8961], v[:8961], 128 ** -0.5, [0, 1], [0, 8961])
+    assert (out[40:] == 7).all()
+
+
 def test_prefill_few_queries_dense(dev):
     """[n][T] queries over [n][M] keys in parts."""
     q, k, v = prefill_inputs(77, 4 * 3, 4 * 3000, 8, 2, 256)
