@@ -48,7 +48,8 @@ EXPORTED = ["moe_create", "moe_route", "moe_forward", "moe_forward_routed", "moe
             "gdn_scan", "moe_add_rmsnorm", "moe_add_rmsnorm_fp8", "moe_quantize_fp8",
             "moe_matmul_fp8", "gdn_decay_scan", "gdn_decay_workspace", "moe_qk_norm_rope",
             "moe_attention_prefill", "moe_attention_prefill_workspace", "moe_kv_write",
-            "moe_kv_read", "moe_attention_decode", "moe_attention_decode_workspace"]
+            "moe_kv_read", "moe_attention_decode", "moe_attention_decode_workspace",
+            "moe_debug_attention_stall"]
 
 Q4_GROUP = 64  # columns per (scale, bias) pair of the 4-bit format
 
@@ -134,6 +135,7 @@ def lib() -> ctypes.CDLL:
     L.moe_kv_read.argtypes = [vp, vp, ll, vp, ip, vp, vp, ll, ip, ip, ip, vp, vp, vp]
     L.moe_attention_decode.argtypes = [vp, ll, vp, vp, ll, vp, ip, vp, ip, ip, ip, ip, fp, vp, vp, sz, vp]
     L.moe_attention_decode_workspace.argtypes = [ip, ip, ip, ip, ip, ctypes.POINTER(sz)]
+    L.moe_debug_attention_stall.argtypes = [ip, ip]
     for name in EXPORTED:
         if name != "moe_strerror":
             getattr(L, name).restype = ip
@@ -237,6 +239,10 @@ def moe_profile_read(h: int) -> dict:
 def moe_debug_wait_timeout(h: int, wait_us: int, stream=None) -> int:
     return _check(lib().moe_debug_wait_timeout(h, wait_us, _stream(stream)),
                   "moe_debug_wait_timeout")
+
+
+def moe_debug_attention_stall(loads: int, wait_us: int = 1) -> int:
+    return _check(lib().moe_debug_attention_stall(loads, wait_us), "moe_debug_attention_stall")
 
 
 def moe_decode_noalloc(cfg: moe_config, x, out, stream=None) -> int:

@@ -71,6 +71,7 @@ struct DecodeAttnArgs {
   long long qs;
   int n_seq, Hq, group, blocks;  // blocks: rows of a key/value head, 8 query heads each
   float scale;                   // times log2(e)
+  AttnWaits waits;
   int4 *head;                    // [kShares]: what is to be joined
   float *part;                   // [2 kShares][8][D + 4]: output, maximum, sum
 };
@@ -221,27 +222,15 @@ __device__ __forceinline__ int share_at(int total, int s) {
   return total >= kShares ? static_cast<int>(static_cast<long long>(total) * s / kShares) : min(s, total);
 }
 
-__device__ __forceinline__ bool poll_d(uint32_t bar, uint32_t parity, const volatile int *abort_flag) {
+__device__ __forceinline__ bool poll_d(uint32_t bar, uint32_t parity, const volatile int *abort_flag, int polls) {
   if (mbar_try_wait(bar, parity)) return true;
 #pragma unroll 1
-  for (int i = 0; i < (1 << 21); ++i) {
+  for (int i = 0; i < polls; ++i) {
     if (mbar_try_wait_sleep(bar, parity, 2000u)) return true;
     if (*abort_flag) return false;
   }
   return false;
 }
-// named barrier of a team that tells each whether any of them brought `bad`
-__device__ __forceinline__ bool team_any(int id, bool bad) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred.aligned q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(bad ? 1u : 0u), "r"(id), "n"(32 * kTeamWarps)
-      : "memory");
-  return r != 0;
-}
-
 }  // namespace
 
 // the share's start; then to the next row, false: the share is done
@@ -389,7 +378,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
       report_error(a.c.status, MOE_ERR_DEVICE_TIMEOUT, KID_ATTN_DECODE * 100 + site);
     }
   };
-  constexpr int kSetup = 4, kSync = 5, kEnd = 8;  // named barriers; the last two one per team
+  constexpr int kSetup = 4, kSync = 5, kVote = 8;  // named barriers; the last two one per team
 
   if (warp >= kConsumers) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProducer));
@@ -454,7 +443,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
       const uint64_t pol = policy_evict_first();
       Row r;
       start_row(r, a, t);
-      int st = 0;
+      int st = 0, loads = 0;
       uint32_t phase = 0;
       for (int nr = 0; ok; ++nr) {
         const bool more = next_row(r, a, t);
@@ -482,9 +471,13 @@ __global__ void __launch_bounds__(kThreadsD, 1)
             }
           }
           const int page = __shfl_sync(0xffffffffu, pages, i & 31);
-          ok = __all_sync(0xffffffffu, poll_d(smem_u32(&t.empty[st]), phase ^ 1, abort_flag));
+          ok = __all_sync(0xffffffffu, poll_d(smem_u32(&t.empty[st]), phase ^ 1, abort_flag, a.waits.polls));
           if (!ok) {
             timeout(SITE_PRODUCER_EMPTY);
+            break;
+          }
+          if (loads++ >= a.waits.loads) {
+            ok = false;
             break;
           }
           if (lane == 0) {
@@ -519,8 +512,6 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         }
         __syncwarp();
       }
-      if (!ok && lane == 0)  // copies in flight get time to land
-        for (int i = 0; i < 200; ++i) __nanosleep(1000);
     } else {
       // sequences without tokens: zeros
       for (int i = cta; i < a.n_seq; i += kCtas)
@@ -546,19 +537,23 @@ __global__ void __launch_bounds__(kThreadsD, 1)
     bool ok = true;
     pdl_wait();
     for (int nr = 0;; ++nr) {
-      ok = __all_sync(0xffffffffu, poll_d(smem_u32(&t.row[nr % kRowsDeep]), nr / kRowsDeep & 1, abort_flag));
-      if (!ok) timeout(SITE_STAGE);
+      if (ok) {
+        ok = __all_sync(0xffffffffu, poll_d(smem_u32(&t.row[nr % kRowsDeep]), nr / kRowsDeep & 1, abort_flag, a.waits.polls));
+        if (!ok) timeout(SITE_STAGE);
+      }
+      // the team goes on, or leaves, as one (and all are done with the row before)
+      if (named_bar_any(kVote + team, 32 * kTeamWarps, !ok)) break;
       const auto &todo = t.todo[nr % (2 * kRowsDeep)];
-      const int n = ok ? todo.n : 1;
+      const int n = todo.n;
       if (n == 0) break;
       int left = todo.left;  // tokens of the sequence from the page on
       uint2 qb;
       float2 unit[2];
-      make_queries<D>(a, t, tw, kSync + team, todo.seq, todo.head, ok ? todo.heads : 0, qb, unit);
+      make_queries<D>(a, t, tw, kSync + team, todo.seq, todo.head, todo.heads, qb, unit);
       // heads 2 c, 2 c + 1
       float o[kG][4][4] = {}, e[4] = {}, m[2] = {-INFINITY, -INFINITY}, ref[2] = {0.0f, 0.0f}, l[2] = {0.0f, 0.0f};
       for (int i = 0; ok && i < n; ++i, left -= kPage) {
-        ok = __all_sync(0xffffffffu, poll_d(smem_u32(&t.full[st]), phase, abort_flag));
+        ok = __all_sync(0xffffffffu, poll_d(smem_u32(&t.full[st]), phase, abort_flag, a.waits.polls));
         if (!ok) {
           timeout(SITE_MMA_FULL);
           break;
@@ -776,9 +771,11 @@ __global__ void __launch_bounds__(kThreadsD, 1)
           }
         }
       }
-      if (team_any(kEnd + team, !ok)) break;
     }
   }
+  __syncthreads();
+  if (*abort_flag)  // after an abort the copies in flight get time to land
+    for (int i = 0; i < 200; ++i) __nanosleep(1000);
 }
 
 // Joins the parts of the rows that are cut.  Each block lists them (the shares whose
@@ -980,6 +977,7 @@ extern "C" int moe_attention_decode(const void *q, long long q_stride, const uin
   a.group = n_q_heads / n_kv_heads;
   a.blocks = (a.group + kHeads - 1) / kHeads;
   a.scale = scale * 1.4426950408889634f;
+  a.waits = attn_waits();
   a.head = static_cast<int4 *>(workspace);
   a.part = reinterpret_cast<float *>(a.head + kShares);
   // (without pages nothing is read: the map then stands over the queries)

@@ -17,6 +17,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
@@ -75,6 +76,12 @@ bool moe::encode_map_2d(CUtensorMap *m, const void *base, size_t esz, uint64_t r
                          : CU_TENSOR_MAP_SWIZZLE_NONE,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
+constexpr AttnWaits kAttnWaits{1 << 21, 0x7fffffff};
+std::atomic<AttnWaits> g_attn_waits{kAttnWaits};
+}  // namespace
+AttnWaits moe::attn_waits() { return g_attn_waits; }
 
 // 3D map of bf16 [n2][n1][n0], 128-byte swizzle; p1, p2: bytes from one index of
 // n1, n2 to the next.
@@ -1050,6 +1057,13 @@ int moe_profile_read(moe_handle *h, float *ms, int64_t *launches, int n) {
     if (ms) ms[r.kind] += t;
     if (launches) launches[r.kind] += 1;
   }
+  return MOE_OK;
+}
+
+int moe_debug_attention_stall(int loads, int wait_us) {
+  if (loads >= 0 && (wait_us < 1 || wait_us > 2000000)) return MOE_ERR_INVALID_ARG;
+  // (a poll sleeps for up to 2 us)
+  g_attn_waits = loads < 0 ? kAttnWaits : AttnWaits{wait_us / 2 + 1, loads};
   return MOE_OK;
 }
 

@@ -433,6 +433,19 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
+// The same, which tells each thread whether any of them brought `bad`.  Warps that
+// meet at a named barrier leave their loop by such a vote alone: one that left on what
+// it saw itself, of an abort say, would leave the others waiting for ever.
+__device__ __forceinline__ bool named_bar_any(int id, int nthreads, bool bad) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred.aligned q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(bad ? 1u : 0u), "r"(id), "r"(nthreads)
+      : "memory");
+  return r != 0;
+}
 
 // ---------------------------------------------------------------- cp.async
 // 16-byte global -> shared copy through L2 only (the generic proxy: a reader

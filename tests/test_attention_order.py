@@ -1,0 +1,87 @@
+"""Orders inside the attention kernels that no run can show to be right, checked in
+their source (as in test_kernel_order.py), and the test hook's arguments."""
+import os
+import re
+
+import pytest
+
+import sparse_mixture_experts_gemm_gb300 as moe
+from sparse_mixture_experts_gemm_gb300 import buildlib as moe_build
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "sparse_mixture_experts_gemm_gb300", "csrc")
+
+
+def source(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def block(text, start):
+    """The braces' body that opens first behind `start`."""
+    at = depth = text.index("{", text.index(start))
+    depth = 0
+    for i in range(at, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return text[at + 1:i]
+    raise AssertionError(start)
+
+
+def outer_exits(body):
+    """Positions of the breaks that leave the loop whose body this is: those in no
+    loop further in."""
+    inner = re.sub(r"for \([^{;]*;[^{;]*;[^{]*\) \{", lambda m: "\x01" * len(m.group(0)), body)
+    exits, depth, loops = [], 0, []
+    for i, c in enumerate(inner):
+        if c == "\x01" and (i + 1 == len(inner) or inner[i + 1] != "\x01"):
+            depth += 1
+            loops.append(depth)
+        elif c == "{":
+            depth += 1
+        elif c == "}":
+            if loops and loops[-1] == depth:
+                loops.pop()
+            depth -= 1
+        elif inner.startswith("break;", i) and not loops:
+            exits.append(i)
+    return exits
+
+
+def test_exits_are_found():
+    assert outer_exits("if (a) break; for (int i = 0; i < 3; ++i) { if (b) { break; } } { break; }") == [7, 66]
+
+
+def test_a_team_of_decode_leaves_its_rows_by_a_vote():
+    """The four warps of a team meet at named barriers in every row.  A warp that
+    left, or stayed, on what it saw of an abort itself could leave the others
+    waiting: after the wait for a row they vote, and what comes before the vote
+    leaves no loop."""
+    rows = block(source("attn_decode.cu"), "for (int nr = 0;; ++nr)")
+    vote = rows.index("named_bar_any(kVote + team, 32 * kTeamWarps, !ok)")
+    exits = outer_exits(rows)
+    assert len(exits) == 2 and vote < exits[0] < exits[1]
+    assert rows.index("poll_d(") < vote < rows.index("todo.n") < rows.index("make_queries<D>")
+    assert "named_bar" not in rows[:vote] and "return" not in rows
+
+
+def test_a_cta_of_decode_waits_for_copies_after_an_abort():
+    """Whichever role aborted: the consumers may do so when the copies' warps have ended."""
+    body = source("attn_decode.cu").split("__global__")[1]
+    end = body.rindex("__syncthreads()")
+    assert end < body.index("__nanosleep", end) and "if (*abort_flag)" in body[end:]
+    assert "poll_d(" not in body[end:]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    moe_build.build()
+    return moe.lib()
+
+
+@pytest.mark.parametrize("args,code", [((0, 0), moe.MOE_ERR_INVALID_ARG), ((5, 2000001), moe.MOE_ERR_INVALID_ARG),
+                                       ((0, -1), moe.MOE_ERR_INVALID_ARG), ((5, 2000000), moe.MOE_OK),
+                                       ((-1, 0), moe.MOE_OK)])
+def test_stall_hook_arguments(lib, args, code):
+    assert lib.moe_debug_attention_stall(*args) == code
+    assert lib.moe_debug_attention_stall(-1, 0) == moe.MOE_OK
