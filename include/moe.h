@@ -337,10 +337,11 @@ int moe_profile_read(moe_handle *h, float *ms, int64_t *launches, int n);
 int moe_debug_wait_timeout(moe_handle *h, int wait_us, void *cuda_stream);
 
 /*
- * Test hook for the device failure path of moe_attention_decode: in the calls
- * that follow, from any thread, the copies of each of a CTA's three teams stop
- * after `loads` pages (loads >= 0), and waits give up after about wait_us
- * microseconds (1 <= wait_us <= 2000000).  A call that has more to copy records
+ * Test hook for the device failure path of moe_attention_prefill and
+ * moe_attention_decode: in the calls that follow, from any thread, the copies of
+ * a CTA stop after `loads` tiles of keys or of values (decode: those of each of
+ * its three teams after `loads` pages; loads >= 0), and waits give up after about
+ * wait_us microseconds (1 <= wait_us <= 2000000).  A call that has more to copy records
  * MOE_ERR_DEVICE_TIMEOUT in the status word that moe_noalloc_status reads and
  * ends, its outputs unspecified; the context stays usable.  loads < 0: calls run
  * as ever (wait_us is not looked at).

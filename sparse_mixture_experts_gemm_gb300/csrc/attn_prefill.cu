@@ -77,6 +77,7 @@ struct PrefillArgs {
   uint32_t per_mul, per_shift;       // x / (2 tokens) = (x per_mul >> 32) >> per_shift, x < 2^31
   float scale;                       // times log2(e)
   int *status;
+  AttnWaits waits;
   int parts, length;  // most parts of a tile's keys (1: none are cut), key tiles of a part
   float *part;        // (parts > 1) [parts][n_q][Hq][D]: outputs before the division
   float2 *stat;       // [parts][n_q][Hq]: maximum, sum
@@ -230,11 +231,10 @@ __device__ __forceinline__ void fail(const PrefillArgs &a, volatile int *abort_f
 }
 // A warp's wait for phase `parity`: false in every lane when the CTA aborted or
 // the polls, each of which sleeps in the barrier for a while, ran out.
-constexpr int kPolls = 1 << 21;
-__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, const volatile int *abort_flag) {
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, const volatile int *abort_flag, int polls) {
   if (mbar_try_wait(bar, parity)) return true;
 #pragma unroll 1
-  for (int i = 0; i < kPolls; ++i) {
+  for (int i = 0; i < polls; ++i) {
     if (mbar_try_wait_sleep(bar, parity, 2000u)) return true;
     if (abort_flag && *abort_flag) return false;
   }
@@ -242,7 +242,7 @@ __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, const volati
 }
 __device__ __forceinline__ bool warp_wait(const PrefillArgs &a, uint32_t bar, uint32_t parity,
                                           volatile int *abort_flag, int site) {
-  if (__all_sync(0xffffffffu, poll(bar, parity, abort_flag))) return true;
+  if (__all_sync(0xffffffffu, poll(bar, parity, abort_flag, a.waits.polls))) return true;
   if ((threadIdx.x & 31) == 0) fail(a, abort_flag, site);
   return false;
 }
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       if (t.nk == 0) continue;
       if (lane == 0) {
         // Q, once the scores of the tile before are made
-        if (!poll(smem_u32(&ctl.q_empty), (used & 1) ^ 1, abort_flag)) {
+        if (!poll(smem_u32(&ctl.q_empty), (used & 1) ^ 1, abort_flag, a.waits.polls)) {
           fail(a, abort_flag, SITE_PRODUCER_EMPTY);
           ok = false;
         }
@@ -607,9 +607,10 @@ __global__ void __launch_bounds__(kThreadsA, 1)
             tma_load_3d_pair(sQ + b * 16384, &tmQ, q0, 64 * b, it.head * a.group, it.q0 + t.mine);
         }
         auto load = [&](bool values, int j) {
+          if (r >= a.waits.loads) return false;
           const int s = r % P::kSlots;
           const uint32_t fb = smem_u32(&ctl.full[s]), dst = ring + s * P::kSlot;
-          if (!poll(smem_u32(&ctl.empty[s]), ((r / P::kSlots) & 1) ^ 1, abort_flag)) {
+          if (!poll(smem_u32(&ctl.empty[s]), ((r / P::kSlots) & 1) ^ 1, abort_flag, a.waits.polls)) {
             fail(a, abort_flag, SITE_PRODUCER_EMPTY);
             return false;
           }
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     // CTA has ended
     if (lane == 0 && ok && !*abort_flag) {
       for (int i = 0; ok && i < P::kSlots; ++i, ++r)
-        if (r >= P::kSlots && !poll(smem_u32(&ctl.empty[r % P::kSlots]), ((r / P::kSlots) & 1) ^ 1, abort_flag)) {
+        if (r >= P::kSlots && !poll(smem_u32(&ctl.empty[r % P::kSlots]), ((r / P::kSlots) & 1) ^ 1, abort_flag, a.waits.polls)) {
           fail(a, abort_flag, SITE_DRAIN);
           ok = false;
         }
@@ -711,10 +712,12 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         }
         done += t.nk;
       }
-      if (!ok || *abort_flag) {  // the MMAs issued so far end before TMEM or shared memory go away
-        if (one) tc_commit2(smem_u32(&ctl.drain));
-        if (!poll(smem_u32(&ctl.drain), 0, nullptr) && lane == 0) fail(a, abort_flag, SITE_DRAIN);
-      }
+      // The MMAs issued so far end before TMEM or shared memory go away: always, as the
+      // warps that wait for them otherwise may abort after this one has ended.
+      if (one) tc_commit2(smem_u32(&ctl.drain));
+      __syncwarp();
+      if (!__all_sync(0xffffffffu, poll(smem_u32(&ctl.drain), 0, nullptr, 1 << 21)) && lane == 0)
+        fail(a, abort_flag, SITE_DRAIN);
     }
   } else {
     // ------------------------------------------------------------ softmax, outputs
@@ -749,7 +752,11 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         }
       }
     };
-    for (int k = 0; ok && next_item(k, it); ++k) {
+    for (int k = 0;; ++k) {
+      const bool more = ok && next_item(k, it);
+      // D = 128: the two warps of a quarter meet in every item, so they go on, or leave, as
+      // one; and both have read the streams' sums of the item before.
+      if (D == 128 ? named_bar_any(1 + wq, 64, !more) : !more) break;
       const Tile<kCut> t(a, it, rank);
       const uint32_t bad = smem_u32(&ctl.bad[used][0]), flag = smem_u32(&ctl.hit[used]);
       const int own = max(0, t.mine + t.shift + 1) / kKeys - t.j0;  // first tile masked for this CTA
@@ -1071,8 +1078,6 @@ __global__ void __launch_bounds__(kThreadsA, 1)
           }
       }
       tc_fence_before();
-      // (D = 128: the streams' sums have been read before either goes on)
-      if (D == 128) named_bar_sync(1 + wq, 64);
       if (t.nk > 0) used = used == 2 ? 0 : used + 1;
       done += t.nk;
       base += 2 * t.nk;
@@ -1081,10 +1086,12 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag)  // the other CTA hears of an abort
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_map(smem_u32(&ctl.abort_flag), rank ^ 1)), "r"(1) : "memory");
   cluster_sync_all();  // no MMA of the pair is in flight, no arrival is pending
   tc_fence_after();
   if (warp == 1) tmem_dealloc2(0, kTmemCols);
-  if (*abort_flag)  // after an abort the copies in flight get time to land
+  if (*abort_flag)  // after an abort the copies and arrivals in flight, in either, get time to land
     for (int i = 0; i < 200; ++i) __nanosleep(1000);
 }
 
@@ -1327,6 +1334,7 @@ extern "C" int moe_attention_prefill(const void *q, const void *k, const void *v
   a.tokens = 128 / a.group;
   a.scale = scale * 1.4426950408889634f;
   a.status = dev.status;
+  a.waits = attn_waits();
   const Cut cut = cut_of(n_q, n_k, n_seq, n_q_heads, n_kv_heads, head_dim);
   a.parts = cut.parts;
   a.length = cut.length;

@@ -201,8 +201,9 @@ bool encode_map_2d(CUtensorMap *m, const void *base, size_t esz, uint64_t rows, 
 bool encode_map_3d(CUtensorMap *m, const void *base, uint64_t n0, uint64_t n1, uint64_t n2,
                    uint64_t p1, uint64_t p2, uint32_t b0, uint32_t b1, uint32_t b2);
 
-// Waits of the attention kernels: polls of each, and pages that a team copies before
-// it stops: as many as there are, but for the test hook (moe_debug_attention_stall).
+// Waits of the attention kernels: polls of each, and tiles or pages that are copied
+// before copies stop: as many as there are, but for the test hook
+// (moe_debug_attention_stall).
 struct AttnWaits {
   int polls, loads;
 };

@@ -73,6 +73,33 @@ def test_a_cta_of_decode_waits_for_copies_after_an_abort():
     assert "poll_d(" not in body[end:]
 
 
+def test_softmax_warps_of_prefill_leave_their_items_by_a_vote():
+    """With heads of 128 two warps meet at a named barrier in every item, so whether
+    they take the next is decided by both; with an item both meet once more,
+    whatever they see of an abort meanwhile."""
+    body = source("attn_prefill.cu").split("__global__")[1]
+    items = block(body, "for (int k = 0;; ++k) {\n      const bool more")
+    vote = items.index("if (D == 128 ? named_bar_any(1 + wq, 64, !more) : !more) break;")
+    assert items.index("next_item(k, it)") < vote < items.index("Tile<kCut>")
+    assert [items.startswith("break;", e) for e in outer_exits(items)] == [True] and outer_exits(items)[0] < items.index("Tile<kCut>")
+    meets = [m.start() for m in re.finditer(r"named_bar_sync\(1 \+ wq, 64\)", items)]
+    assert len(meets) == 1 and "return" not in re.sub(r"auto \w+ = \[&\]\([^)]*\) \{.*?\n      \};", "", items, flags=re.S)
+    # not within a loop or a branch on what a warp saw: the last brace before it opens the case of 128 columns
+    assert items.rindex("if constexpr (D == 128) {", 0, meets[0]) > items.rindex("}", 0, meets[0])
+
+
+def test_products_of_prefill_end_before_their_memory_goes():
+    """The warp of the MMAs waits for them whether or not it saw an abort, by a limit
+    that no hook shortens; both CTAs of a pair wait for what is in flight."""
+    body = source("attn_prefill.cu").split("__global__")[1]
+    drain = body.index("tc_commit2(smem_u32(&ctl.drain))")
+    before = body[:drain].rstrip()
+    assert before.endswith("if (one)") and before[:-len("if (one)")].rstrip().endswith("}")
+    assert "poll(smem_u32(&ctl.drain), 0, nullptr, 1 << 21)" in body[drain:]
+    told, met = body.index("cluster_map(smem_u32(&ctl.abort_flag), rank ^ 1)"), body.rindex("cluster_sync_all()")
+    assert drain < told < met < body.index("tmem_dealloc2") < body.index("__nanosleep")
+
+
 @pytest.fixture(scope="module")
 def lib():
     moe_build.build()

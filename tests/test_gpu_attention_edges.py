@@ -47,3 +47,36 @@ def test_decode_ends_when_a_wait_runs_out(dev, stall, D, loads):
     moe.moe_debug_attention_stall(-1)
     assert torch.equal(moe.attention_decode(*args), ref)
     assert moe.moe_noalloc_status()[0] == moe.MOE_OK
+
+
+@pytest.mark.parametrize("loads", [0, 1, 2, 3, 4, 7, 12, 23, 1000])
+@pytest.mark.parametrize("D,Hq,Hk,ql,kl", [(128, 8, 2, [700, 90], [700, 90]), (256, 16, 2, [700, 90], [700, 90]),
+                                           (128, 8, 2, [60], [9000]), (256, 16, 2, [60], [9000])])
+def test_prefill_ends_when_a_wait_runs_out(dev, stall, D, Hq, Hk, ql, kl, loads):
+    """Copies that stop anywhere in a tile of rows, of one or of several a cluster, with
+    keys whole and in parts."""
+    q, k, v = (x.to(dev) for x in prefill_inputs(D + loads, sum(ql), sum(kl), Hq, Hk, D))
+    args = (q, k, v, ends(ql, dev), ends(kl, dev))
+    ref = moe.attention_prefill(*args)
+    assert moe.moe_noalloc_status()[0] == moe.MOE_OK
+    stall(loads)
+    moe.attention_prefill(*args)
+    code, detail = moe.moe_noalloc_status()
+    # (a tile of rows at the least has its first keys and values to copy)
+    assert code == moe.MOE_ERR_DEVICE_TIMEOUT if loads < 2 else code in (moe.MOE_ERR_DEVICE_TIMEOUT, moe.MOE_OK)
+    assert detail // 100 == (11 if code else 0) and (code == moe.MOE_OK or loads < 1000)
+    moe.moe_debug_attention_stall(-1)
+    assert torch.equal(moe.attention_prefill(*args), ref)
+    assert moe.moe_noalloc_status()[0] == moe.MOE_OK
+
+
+def test_prefill_of_many_tiles_ends_when_a_wait_runs_out(dev, stall):
+    """Clusters with several tiles of rows each: aborts in a later one."""
+    q, k, v = (x.to(dev) for x in prefill_inputs(3, 3000, 3000, 32, 8, 128))
+    ref = moe.attention_prefill(q, k, v)
+    for loads in (30, 61, 90):
+        stall(loads)
+        moe.attention_prefill(q, k, v)
+        assert moe.moe_noalloc_status()[0] == moe.MOE_ERR_DEVICE_TIMEOUT
+        moe.moe_debug_attention_stall(-1)
+        assert torch.equal(moe.attention_prefill(q, k, v), ref)
