@@ -1126,14 +1126,16 @@ __global__ void __launch_bounds__(kJoinThreads) attn_prefill_join_kernel(const P
     const int t = it.t0 + rank * a.tokens + r / a.group;
     if (r >= a.tokens * a.group || t >= it.lq) continue;  // (whole warps)
     const long long row = static_cast<long long>(it.q0 + t) * a.Hq + it.head * a.group + r % a.group;
-    // lane s of a warp, all of one row, has part s's maximum and sum
-    const int parts = Tile<true>(a, it, 0).parts;
+    // Lane s of a warp, all of one row, has part s's maximum and sum, of the parts that
+    // have keys for this row.  (By their place, not by the sums: one may be 0 as all its
+    // scores are minus infinity, and where all are, the row is 0 / 0 as it is uncut.)
+    const int last = t + it.lk - it.lq;
+    const int parts = last < 0 ? 0 : min(Tile<true>(a, it, 0).parts, last / (a.length * kKeys) + 1);
     const float2 ml = lane < parts ? a.stat[row + lane * step] : make_float2(-INFINITY, 0.0f);
     float M = ml.x;
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float mine = ml.y == 0.0f ? 0.0f : ml.x == M ? 1.0f : fast_exp2((ml.x - M) * a.scale);
-    const uint32_t seen = __ballot_sync(0xffffffffu, ml.y != 0.0f);  // parts with keys for this row
+    const float mine = lane >= parts ? 0.0f : ml.x == M ? 1.0f : fast_exp2((ml.x - M) * a.scale);
     float L = mine * ml.y;
 #pragma unroll
     for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
@@ -1143,18 +1145,18 @@ __global__ void __launch_bounds__(kJoinThreads) attn_prefill_join_kernel(const P
       float4 y[8];
 #pragma unroll
       for (int s = 0; s < 8; ++s)
-        if (seen >> (s0 + s) & 1) y[s] = *reinterpret_cast<const float4 *>(a.part + (row + (s0 + s) * step) * D + d);
+        if (s0 + s < parts) y[s] = *reinterpret_cast<const float4 *>(a.part + (row + (s0 + s) * step) * D + d);
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
         const float f = __shfl_sync(0xffffffffu, mine, s0 + s);
-        if (!(seen >> (s0 + s) & 1)) continue;
+        if (s0 + s >= parts) break;
         o.x = fmaf(f, y[s].x, o.x);
         o.y = fmaf(f, y[s].y, o.y);
         o.z = fmaf(f, y[s].z, o.z);
         o.w = fmaf(f, y[s].w, o.w);
       }
     }
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    const float inv = parts == 0 ? 0.0f : 1.0f / L;
     *reinterpret_cast<uint2 *>(a.out + row * D + d) =
         make_uint2(bf16x2_bits(o.x * inv, o.y * inv), bf16x2_bits(o.z * inv, o.w * inv));
   }

@@ -80,3 +80,23 @@ def test_prefill_of_many_tiles_ends_when_a_wait_runs_out(dev, stall):
         assert moe.moe_noalloc_status()[0] == moe.MOE_ERR_DEVICE_TIMEOUT
         moe.moe_debug_attention_stall(-1)
         assert torch.equal(moe.attention_prefill(q, k, v), ref)
+
+
+# ------------------------------------- scores and weights at the ends of float32
+@pytest.mark.parametrize("Hq,Hk,D", [(16, 2, 256), (8, 4, 128)])
+def test_prefill_scores_of_minus_infinity(dev, Hq, Hk, D):
+    """Keys whose score is minus infinity weigh nothing; a row of no others is 0 / 0,
+    whether its keys are cut into parts or not; rows that see no key are zeros."""
+    for T, M in ((4, 4000), (100, 300)):  # in parts, and not
+        q, k, v = prefill_inputs(T, T, M, Hq, Hk, D)
+        q[..., 5] = q[..., 5].abs() + 1
+        hidden = k.clone()
+        hidden[:M // 2, :, 5] = float("-inf")
+        got = moe.attention_prefill(q.to(dev), hidden.to(dev), v.to(dev))
+        check_attend(got, q, k[M // 2:], v[M // 2:], D ** -0.5, [0, T], [0, M - M // 2])
+        hidden[:, :, 5] = float("-inf")
+        assert torch.isnan(moe.attention_prefill(q.to(dev), hidden.to(dev), v.to(dev))).all()
+    q, k, v = prefill_inputs(9, 40, 9000, Hq, Hk, D)
+    off, koff = ends([3, 37], dev), ends([8999, 1], dev)
+    got = moe.attention_prefill(q.to(dev), k.to(dev), v.to(dev), off, koff)
+    assert not got[3:39].any() and got[:3].any() and got[39].any()
