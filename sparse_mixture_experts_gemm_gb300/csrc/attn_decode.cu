@@ -61,6 +61,7 @@ constexpr int kPagesDeep = 3;  // of a team
 constexpr int kRowsDeep = 4;   // more than kPagesDeep: that many rows can the copies be ahead
 constexpr int kJoinThreads = 512;
 constexpr float kLateDecode = 8.0f;  // as in attn_prefill.cu
+constexpr float kLowest = -3.402823466e38f;
 constexpr int kCtas = 152, kShares = kCtas * kTeams;  // one CTA per SM
 
 struct DecodeAttnArgs {
@@ -595,7 +596,9 @@ __global__ void __launch_bounds__(kThreadsD, 1)
             for (int y = 0; y < 4; ++y)
               if (tile + g + 8 * (y >> 1) >= left) s[y] = -INFINITY;
           }
-          float top[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
+          // (not below the lowest number: m is minus infinity where no token was attended to,
+          // and there alone the result is zero)
+          float top[2] = {fmaxf(fmaxf(s[0], s[2]), kLowest), fmaxf(fmaxf(s[1], s[3]), kLowest)};
           if (__any_sync(0xffffffffu, top[0] > m[0] + kLateDecode || top[1] > m[1] + kLateDecode)) {
             float f[2];
 #pragma unroll
@@ -605,7 +608,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
               const float to = top[z] > m[z] + kLateDecode ? top[z] : m[z];
               f[z] = to == m[z] ? 1.0f : fast_exp2(m[z] - to);
               m[z] = to;
-              ref[z] = to == -INFINITY ? 0.0f : to;
+              ref[z] = to;
               l[z] *= f[z];
             }
 #pragma unroll
@@ -750,7 +753,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
         for (int y = 0; y < 2; ++y) {
           if (2 * c + y >= todo.heads) continue;
           if (todo.slot < 0) {
-            const float inv = l[y] == 0.0f ? 0.0f : 1.0f / l[y];
+            const float inv = m[y] == -INFINITY ? 0.0f : 1.0f / l[y];
             __nv_bfloat16 *to = a.out + static_cast<long long>(todo.out + 2 * c + y) * D + 4 * g;
 #pragma unroll
             for (int x = 0; x < kG; ++x)
@@ -884,7 +887,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const DecodeAtt
       __syncthreads();
     }
     if (grp == 0 && hd < head.w) {
-      const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+      const float inv = M == -INFINITY ? 0.0f : 1.0f / L;
       *reinterpret_cast<uint2 *>(a.out + (static_cast<long long>(head.z) + hd) * D + d) =
           make_uint2(bf16x2_bits(v.x * inv, v.y * inv), bf16x2_bits(v.z * inv, v.w * inv));
     }

@@ -7,7 +7,7 @@ import torch
 import sparse_mixture_experts_gemm_gb300 as moe
 from oracle import attention as oracle
 from test_gpu_attention import BF16, I32, check_attend, check_decode, ends, f64, gen, make_table, normal, \
-    prefill_inputs, random_cache
+    prefill_inputs, random_cache, rows_of
 
 pytestmark = pytest.mark.gpu
 
@@ -100,3 +100,30 @@ def test_prefill_scores_of_minus_infinity(dev, Hq, Hk, D):
     off, koff = ends([3, 37], dev), ends([8999, 1], dev)
     got = moe.attention_prefill(q.to(dev), k.to(dev), v.to(dev), off, koff)
     assert not got[3:39].any() and got[:3].any() and got[39].any()
+
+
+@pytest.mark.parametrize("L", [40, 64, 900, 30000])
+@pytest.mark.parametrize("D", [128, 256])
+def test_decode_scores_of_minus_infinity(dev, D, L):
+    """Tokens whose score is below what float32 holds weigh nothing next to others; a
+    row of no others is not a number, as 0 / 0 is, and not that of an empty sequence."""
+    g = gen(L + D)
+    table, P = make_table(g, [L])
+    codes, affine = random_cache(g, P, 1, D, dev)
+    q = (normal(g, 1, 4, D).abs() + 1) * 2.0 ** 20
+    hidden = affine.clone()
+    at = torch.arange(L // 2)
+    hidden[table[0].long()[at // 64].to(dev), 0, :, (at % 64).to(dev), 0] = torch.tensor([0.0, -2.0 ** 127], dtype=BF16, device=dev)
+    n = torch.tensor([L], dtype=I32, device=dev)
+    got = moe.attention_decode(q.to(dev), (codes, hidden), table.to(dev), n, scale=2.0 ** -24)
+    # the same as over the other tokens, in a cache of their own
+    m = L - L // 2
+    rest = [torch.zeros(-(-m // 64), *t.shape[1:], dtype=t.dtype) for t in (codes, affine)]
+    to = torch.arange(m)
+    for t, x in zip(rest, rows_of((codes, affine), table, 0, L // 2, L)):
+        t[to // 64, :, :, to % 64] = x
+    check_decode(got, q, rest, torch.arange(len(rest[0]))[None], [m], 2.0 ** -24)
+    hidden[:, 0, :, :, 0] = torch.tensor([0.0, -2.0 ** 127], dtype=BF16, device=dev)
+    got = moe.attention_decode(q.to(dev), (codes, hidden), table.to(dev), n, scale=2.0 ** -24)
+    assert torch.isnan(got).all()
+    assert not moe.attention_decode(q.to(dev), (codes, hidden), table.to(dev), n * 0, scale=2.0 ** -24).any()
