@@ -68,6 +68,11 @@ constexpr int kItems = 2;   // tiles of rows looked up ahead
 constexpr int kReaders = 10;  // warps that read an item
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLate = 8.0f;  // log2 of how far a row's maximum may grow before m follows
+// A weight is exp2(c x - c m) by one fused sum, in which c m is rounded: off by up to
+// 2^-24 of itself, the same for all of a row's weights, but past 2^30 a weight of 1 then
+// leaves fp32, and two streams or parts are weighed against each other by it.  Past this
+// size m is therefore taken off x first, which costs a sum per weight in rows that large.
+constexpr float kFar = 1024.0f;
 
 struct PrefillArgs {
   __nv_bfloat16 *out;
@@ -837,7 +842,17 @@ __global__ void __launch_bounds__(kThreadsA, 1)
               }
             }
           }
-          const uint64_t c2 = pair_of(c, c), back[2] = {pair_of(-ref[0], -ref[0]), pair_of(-ref[1], -ref[1])};
+          float b0 = -ref[0], b1 = -ref[1];
+          if (__any_sync(0xffffffffu, fmaxf(fabsf(b0), fabsf(b1)) > kFar)) {
+            const float off[2] = {fabsf(b0) > kFar ? m[0] : 0.0f, fabsf(b1) > kFar ? m[1] : 0.0f};
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[y][i] -= off[(i >> 1) & 1];
+            if (fabsf(b0) > kFar) b0 = 0.0f;
+            if (fabsf(b1) > kFar) b1 = 0.0f;
+          }
+          const uint64_t c2 = pair_of(c, c), back[2] = {pair_of(b0, b0), pair_of(b1, b1)};
           uint64_t sums[2] = {0, 0};
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
@@ -876,6 +891,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         const uint32_t lanes = static_cast<uint32_t>(wq * 32) << 16;
         const int at = t.mine + mine, limit = at < it.lq ? min(at + t.shift, it.lk - 1) : -1;
         float m = -INFINITY, ref = 0.0f, l = 0.0f;
+        bool far = false;  // (kept with m: with a vote per tile 2 x 2,048 tokens took 86.4 us in place of 84.9)
         for (int j = 0; ok && j < t.nk; ++j) {
           const int n = done + j;
           if ((n & 1) != half) {  // the other stream's
@@ -915,6 +931,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
             const float f = next == m ? 1.0f : fast_exp2((m - next) * c);
             m = next;
             ref = next == -INFINITY ? 0.0f : next * c;
+            far = __any_sync(0xffffffffu, fabsf(ref) > kFar);
             l *= f;
             // O of the stream's tiles before: their products are done, the scores of this
             // tile were issued behind them
@@ -930,10 +947,9 @@ __global__ void __launch_bounds__(kThreadsA, 1)
               }
             }
           }
-          const uint64_t c2 = pair_of(c, c), back = pair_of(-ref, -ref);
+          const uint64_t c2 = pair_of(c, c);
           uint64_t sums[4] = {0, 0, 0, 0};
-#pragma unroll
-          for (int y = 0; y < kKeys; y += 32) {  // (P of 32 columns goes over scores that are read)
+          auto weights = [&](int y, uint64_t back, bool less, float off) {
             float x[32];
             uint32_t p[16];
             tmem_ld32_sync(ts + y, x);
@@ -941,6 +957,10 @@ __global__ void __launch_bounds__(kThreadsA, 1)
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (y + i > hidden) x[i] = -INFINITY;
+            }
+            if (less) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] -= off;
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -952,6 +972,16 @@ __global__ void __launch_bounds__(kThreadsA, 1)
               p[i] = bf16x2_bits(u, w);
             }
             st_32x16(ts + y / 2, p);
+          };
+          // (P of 32 columns goes over scores that are read)
+          if (far) {
+            const bool mine = fabsf(ref) > kFar;
+            const float b = mine ? 0.0f : -ref;
+#pragma unroll 1
+            for (int y = 0; y < kKeys; y += 32) weights(y, pair_of(b, b), true, mine ? m : 0.0f);
+          } else {
+#pragma unroll
+            for (int y = 0; y < kKeys; y += 32) weights(y, pair_of(-ref, -ref), false, 0.0f);
           }
           {
             float u, w;

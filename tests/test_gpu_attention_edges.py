@@ -127,3 +127,50 @@ def test_decode_scores_of_minus_infinity(dev, D, L):
     got = moe.attention_decode(q.to(dev), (codes, hidden), table.to(dev), n, scale=2.0 ** -24)
     assert torch.isnan(got).all()
     assert not moe.attention_decode(q.to(dev), (codes, hidden), table.to(dev), n * 0, scale=2.0 ** -24).any()
+
+
+FAR = [([300], [300], 16, 2, 256), ([300], [300], 8, 2, 128), ([5], [6000], 16, 2, 256), ([5], [6000], 8, 2, 128)]
+
+
+@pytest.mark.parametrize("ql,kl,Hq,Hk,D", FAR)
+@pytest.mark.parametrize("e", [12, 20, 30, 40, 60, 100])
+def test_prefill_large_scores(dev, ql, kl, Hq, Hk, D, e):
+    """Scores of small whole numbers times 2^e, exact in fp32: each query has the mean
+    of the values of its largest.  (Half a step of bf16 for each weight, and one for
+    the result.)"""
+    g = gen(e + D + sum(kl))
+    T, M = sum(ql), sum(kl)
+    q = torch.zeros(T, Hq, D)
+    q.scatter_(2, torch.randint(0, D, (T, Hq, 1), generator=g), 2.0 ** (e // 2))
+    k = torch.randint(-3, 4, (M, Hk, D), generator=g) * 2.0 ** (e - e // 2)
+    v = normal(g, M, Hk, D)
+    q, k = q.to(BF16), k.to(BF16)
+    got = f64(moe.attention_prefill(q.to(dev), k.to(dev), v.to(dev), ends(ql, dev), ends(kl, dev)))
+    for h in range(Hq):
+        s = f64(q[:, h]) @ f64(k[:, h // (Hq // Hk)]).T
+        s[np.arange(M)[None] > np.arange(T)[:, None] + M - T] = -np.inf
+        p = (s == s.max(1, keepdims=True)) / 1.0
+        p /= p.sum(1, keepdims=True)
+        x = f64(v[:, h // (Hq // Hk)])
+        ref, mag = p @ x, p @ np.abs(x)
+        assert (np.abs(got[:, h] - ref) <= 2.0 ** -8 * (np.abs(ref) + mag) * (1 + 2.0 ** -6) + mag * (M / 16 + 64) * 2.0 ** -23).all()
+
+
+@pytest.mark.parametrize("ql,kl,Hq,Hk,D", FAR)
+@pytest.mark.parametrize("e", [8, 14, 18])
+def test_prefill_scores_far_from_zero(dev, ql, kl, Hq, Hk, D, e):
+    """Scores that differ by a few units next to a common part of up to 2^18, exact in
+    fp32: the weights are those of the differences (scale and log2(e) rounded to
+    fp32 and the exponential's last bits leave 2^-19 of a weight)."""
+    g = gen(e + D + sum(kl))
+    T, M = sum(ql), sum(kl)
+    q, k, v = torch.zeros(T, Hq, D), torch.zeros(M, Hk, D), normal(g, M, Hk, D)
+    q[..., 0], k[..., 0] = 2.0 ** (e // 2), 2.0 ** (e - e // 2)
+    q[..., 1] = 1
+    k[..., 1] = torch.arange(M)[:, None] % 89 * 2.0 ** -4  # the largest in each tile or part another
+    q, k = q.to(BF16), k.to(BF16)
+    got = moe.attention_prefill(q.to(dev), k.to(dev), v.to(dev), ends(ql, dev), ends(kl, dev), scale=1.0)
+    k[..., 0] = 0
+    ref, mag, _ = oracle.attend(f64(q), f64(k), f64(v), 1.0, ends(ql), ends(kl))
+    tol = 2.0 ** -8 * (np.abs(ref) + mag) * (1 + 2.0 ** -6) + mag * ((M / 16 + 64) * 2.0 ** -23 + 2.0 ** -18)
+    assert (np.abs(f64(got) - ref) <= tol).all()
