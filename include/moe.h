@@ -521,7 +521,7 @@ int moe_qk_norm_rope(const void *q, const void *k, const void *q_weight, const v
  *   offsets, k_offsets: the sequences' queries and keys; k_offsets NULL: the same
  *        as offsets (n_k == n_q).  Both NULL: n_seq sequences of n_q / n_seq
  *        queries and n_k / n_seq keys.
- * scale > 0 and finite.  A NaN or infinity in k or v reaches no query that does
+ * 0 < scale <= 2.35e38 (times log2(e) it is finite).  A NaN or infinity in k or v reaches no query that does
  * not see its token.
  *   workspace: device memory of at least the bytes that
  *        moe_attention_prefill_workspace gives for the same sizes, 16-byte
@@ -573,6 +573,7 @@ int moe_kv_read(const uint8_t *codes, const uint16_t *affine, long long n_pages,
  *     o = sum_t softmax_t(scale * q . k_t) v_t   over positions t < lengths[i],
  * with k_t and v_t the cache's values (not rounded to bf16).
  *   q    bf16 [n_seq][n_q_heads][head_dim], sequences q_stride elements apart
+ *   scale as for moe_attention_prefill
  *   lengths int32 [n_seq], tokens in the cache; 0 gives zeros
  *   out  bf16 [n_seq][n_q_heads][head_dim], contiguous
  *   workspace: device memory of at least the bytes that

@@ -14,6 +14,9 @@ namespace moe {
 constexpr int kPage = 64;   // tokens per page of the cache
 constexpr int kGroup = 64;  // columns that share a scale and a bias
 
+// scores are exponents of 2: scale times this, which has to be finite
+constexpr float kLog2e = 1.4426950408889634f, kMostScale = 2.35e38f;
+
 // rows lo .. hi of sequence i; offsets outside [0, total] or running backwards
 // are clamped.  offsets null: n sequences of total / n rows.
 __device__ __forceinline__ void seq_rows(const int *offsets, int n, long long total, int i, int &lo,

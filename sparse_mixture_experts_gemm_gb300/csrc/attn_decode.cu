@@ -951,7 +951,7 @@ extern "C" int moe_attention_decode(const void *q, long long q_stride, const uin
   size_t need = 0;
   const int rc = moe_attention_decode_workspace(n_seq, table_width, n_q_heads, n_kv_heads, head_dim, &need);
   if (rc != MOE_OK) return rc;
-  if (n_pages < 0 || !(scale > 0.0f) || scale > 3.0e38f || q_stride < static_cast<long long>(n_q_heads) * head_dim)
+  if (n_pages < 0 || !(scale > 0.0f) || scale > kMostScale || q_stride < static_cast<long long>(n_q_heads) * head_dim)
     return MOE_ERR_INVALID_ARG;
   if (n_pages > 0x7fffffffLL || n_pages * 2 * n_kv_heads * kPage > 0x7fffffffLL || q_stride >= (1LL << 39) ||
       static_cast<long long>(n_seq) * n_q_heads > 0x7fffffffLL ||
@@ -979,7 +979,7 @@ extern "C" int moe_attention_decode(const void *q, long long q_stride, const uin
   a.Hq = n_q_heads;
   a.group = n_q_heads / n_kv_heads;
   a.blocks = (a.group + kHeads - 1) / kHeads;
-  a.scale = scale * 1.4426950408889634f;
+  a.scale = scale * kLog2e;
   a.waits = attn_waits();
   a.head = static_cast<int4 *>(workspace);
   a.part = reinterpret_cast<float *>(a.head + kShares);

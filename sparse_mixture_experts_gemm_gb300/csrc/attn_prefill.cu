@@ -1333,7 +1333,7 @@ extern "C" int moe_attention_prefill(const void *q, const void *k, const void *v
   size_t need = 0;
   const int rc = moe_attention_prefill_workspace(n_q, n_k, n_seq, n_q_heads, n_kv_heads, head_dim, &need);
   if (rc != MOE_OK) return rc;
-  if (!(scale > 0.0f) || scale > 3.0e38f) return MOE_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || scale > kMostScale) return MOE_ERR_INVALID_ARG;
   if (k_offsets && !offsets) return MOE_ERR_INVALID_ARG;
   if (offsets ? (!k_offsets && n_q != n_k) : (n_seq > 0 && (n_q % n_seq != 0 || n_k % n_seq != 0)))
     return MOE_ERR_INVALID_ARG;
@@ -1364,7 +1364,7 @@ extern "C" int moe_attention_prefill(const void *q, const void *k, const void *v
   a.Hk = n_kv_heads;
   a.group = n_q_heads / n_kv_heads;
   a.tokens = 128 / a.group;
-  a.scale = scale * 1.4426950408889634f;
+  a.scale = scale * kLog2e;
   a.status = dev.status;
   a.waits = attn_waits();
   const Cut cut = cut_of(n_q, n_k, n_seq, n_q_heads, n_kv_heads, head_dim);

@@ -3,6 +3,7 @@ their source (as in test_kernel_order.py), and the test hook's arguments."""
 import os
 import re
 
+import numpy as np
 import pytest
 
 import sparse_mixture_experts_gemm_gb300 as moe
@@ -112,3 +113,14 @@ def lib():
 def test_stall_hook_arguments(lib, args, code):
     assert lib.moe_debug_attention_stall(*args) == code
     assert lib.moe_debug_attention_stall(-1, 0) == moe.MOE_OK
+
+
+def test_scales_whose_exponents_of_two_are_infinite_are_refused(lib):
+    """Scores are multiplied by scale times log2(e): that is finite up to 2.35e38."""
+    P = 0x10000  # never dereferenced
+    prefill = lambda s: lib.moe_attention_prefill(P, P, P, None, None, 0, 8, 2, 4, 2, 128, 512, 256, 256, s, P, None, 0, None)  # noqa: E731
+    decode = lambda s: lib.moe_attention_decode(P, 512, P, P, 8, P, 4, P, 0, 4, 2, 128, s, P, P, 0, None)  # noqa: E731
+    for call in (prefill, decode):
+        assert call(2.35e38) == moe.MOE_OK and call(1e-45) == moe.MOE_OK
+        assert call(2.4e38) == moe.MOE_ERR_INVALID_ARG and call(3e38) == moe.MOE_ERR_INVALID_ARG
+    assert np.isfinite(np.float32(2.35e38) * np.float32(np.log2(np.e)))

@@ -174,3 +174,19 @@ def test_prefill_scores_far_from_zero(dev, ql, kl, Hq, Hk, D, e):
     ref, mag, _ = oracle.attend(f64(q), f64(k), f64(v), 1.0, ends(ql), ends(kl))
     tol = 2.0 ** -8 * (np.abs(ref) + mag) * (1 + 2.0 ** -6) + mag * ((M / 16 + 64) * 2.0 ** -23 + 2.0 ** -18)
     assert (np.abs(f64(got) - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("T,M", [(150, 150), (3, 5000)])
+@pytest.mark.parametrize("D", [128, 256])
+def test_scales_near_the_ends_of_float32(dev, D, T, M):
+    """Scores that a scale brings into range, and scales of which nothing but means are left."""
+    q, k, v = prefill_inputs(D + T, T, M, 4, 2, D)
+    table, P = make_table(gen(T), [M])
+    codes, affine = random_cache(gen(D), P, 2, D, dev)
+    n = torch.tensor([M], dtype=I32, device=dev)
+    for scale, e in ((2.0 ** 100 * D ** -0.5, -50), (1e-44, 0), (1e-38, 0)):
+        qs, ks, a = q * 2.0 ** e, k * 2.0 ** e, affine.clone()
+        a[:, 0] *= 2.0 ** e
+        check_attend(moe.attention_prefill(qs.to(dev), ks.to(dev), v.to(dev), scale=scale), qs, ks, v, scale)
+        got = moe.attention_decode(qs[:1].to(dev), (codes, a), table.to(dev), n, scale=scale)
+        check_decode(got, qs[:1], (codes, a), table, [M], scale)
