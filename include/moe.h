@@ -522,7 +522,8 @@ int moe_qk_norm_rope(const void *q, const void *k, const void *q_weight, const v
  *        as offsets (n_k == n_q).  Both NULL: n_seq sequences of n_q / n_seq
  *        queries and n_k / n_seq keys.
  * 0 < scale <= 2.35e38 (times log2(e) it is finite).  A NaN or infinity in k or v reaches no query that does
- * not see its token.
+ * not see its token; one that sees an infinity in v has it in that column (NaN next
+ * to a NaN or one of the other sign, or where its weight is below what float32 holds).
  *   workspace: device memory of at least the bytes that
  *        moe_attention_prefill_workspace gives for the same sizes, 16-byte
  *        aligned, used by the call's kernels alone; NULL where that is 0.  (Few

@@ -38,7 +38,8 @@
 // A key or value row that some of the tile's queries must not see is masked in
 // the scores; but 0 x NaN is NaN, so in the tiles at the causal edge (and at a
 // sequence's end) values that are not finite are taken out of V in shared memory,
-// and the queries that do see them are set to NaN in the end.
+// and infinity, its negative, or both for a NaN, are added to the outputs of the
+// queries that do see them.
 //
 // Measured: 4,096 tokens of 16 heads of 256 on 2 in 81.5 us (1.69 PFLOP/s, tensor pipes
 // busy 73 % of the cycles; the rest goes at the changes of tile, about 4,500 cycles
@@ -103,9 +104,9 @@ struct Ctl {
   uint32_t tmem, sink;
   int abort_flag;
   Item item[kItems];
-  // of three tiles of rows in turn, two columns per word: first key (from the first
-  // masked tile on) whose value is not finite
-  uint32_t bad[3][128], hit[3];  // hit: whether there is one
+  // of three tiles of rows in turn, three columns per word: first key (from the first
+  // masked tile on) whose value is infinity, and minus infinity, or in both a NaN
+  uint32_t bad[3][2][(D + 2) / 3], hit[3];  // hit: whether there is one
   float2 stream[2][D == 128 ? 128 : 1];      // D = 128: maximum and sum of each stream's rows
 };
 
@@ -120,6 +121,7 @@ struct Plan {
   static constexpr uint32_t O = 0, S = kStreams * D;  // TMEM columns: O of each stream, then two of S
   static constexpr int kMakers = kStreams == 2 ? 4 : 8;  // warps of a tile's P
   static_assert(kTotal <= 227 * 1024 && sizeof(Ctl<D>) <= kCtlBytes && S + 2 * kKeys <= kTmemCols, "room");
+  static_assert(sizeof(Ctl<D>::bad) / 12 <= 256, "a thread of the softmax per word");
 };
 
 // operand whose N index is contiguous (see the same layout in decay_chunk.cu)
@@ -412,6 +414,8 @@ struct Schedule {
 // such key of each column is noted in both CTAs.
 template <int D, int kN>
 struct Cleaner {
+  static constexpr int kWords = (D + 2) / 3;
+  static constexpr uint32_t kMark = 0x3ffu;
   static constexpr int kPer = D * 8 / kN;  // 16-byte pieces per thread, of one row
   static __device__ __forceinline__ uint32_t where(uint32_t v, int e, int i) {
     const int r = e & 127, at = (e >> 7) * kPer + i;  // piece of the row: block at / 8
@@ -445,14 +449,17 @@ struct Cleaner {
         asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(0)) : "memory");
         if (key >= lk) continue;  // (another sequence's: nobody sees it)
         const int c = rank * (D / 2) + ((e >> 7) * kPer + i) * 8 + x;
-        const uint32_t mark = static_cast<uint32_t>(key - base), shift = 16 * (c & 1);
-        for (uint32_t to = 0; to < 2; ++to) {
+        // (masked tiles are four at most)
+        const uint32_t mark = static_cast<uint32_t>(key - base), shift = 10 * (c % 3);
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t to = y & 1, minus = y >> 1;
+          if ((bits & 0x7fu) == 0 && (bits >> 15) != minus) continue;
           asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_map(flag, to)), "r"(1u) : "memory");
-          const uint32_t p = cluster_map(bad + c / 2 * 4, to);
+          const uint32_t p = cluster_map(bad + (minus * kWords + c / 3) * 4, to);
           uint32_t old;
           asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(old) : "r"(p) : "memory");
-          for (int tries = 0; tries < 1 << 16 && (old >> shift & 0xffffu) > mark; ++tries) {
-            const uint32_t want = (old & ~(0xffffu << shift)) | mark << shift;
+          for (int tries = 0; tries < 1 << 16 && (old >> shift & kMark) > mark; ++tries) {
+            const uint32_t want = (old & ~(kMark << shift)) | mark << shift;
             uint32_t got;
             asm volatile("atom.shared::cluster.cas.b32 %0, [%1], %2, %3;"
                          : "=r"(got)
@@ -465,6 +472,19 @@ struct Cleaner {
       }
     asm volatile("fence.acq_rel.cluster;" ::: "memory");
     fence_proxy_async_smem();
+  }
+  // The marks' infinities into what a thread has stored of a row: its columns
+  // 4 wide n + wide sub + 0 .. wide - 1; seen: of the keys from base on, the last that the row sees.
+  template <typename T>
+  static __device__ __forceinline__ void put_back(const uint32_t (&bad)[2][kWords], T *row, int seen, int sub) {
+    constexpr int kWide = sizeof(T) == 2 ? 8 : 2;
+#pragma unroll 1
+    for (int i = 0; i < D / 4; ++i) {
+      const int c = i / kWide * (4 * kWide) + kWide * sub + i % kWide;
+      for (int y = 0; y < 2; ++y)
+        if (seen >= static_cast<int>(bad[y][c / 3] >> 10 * (c % 3) & kMark))
+          row[c] = static_cast<T>(static_cast<float>(row[c]) + (y ? -INFINITY : INFINITY));
+    }
   }
 };
 
@@ -531,7 +551,8 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     prefetch_tmap(&tmV);
   }
   if (threadIdx.x < 3) ctl.hit[threadIdx.x] = 0;
-  for (int i = static_cast<int>(threadIdx.x); i < 384; i += kThreadsA) ctl.bad[i >> 7][i & 127] = 0xffffffffu;
+  for (int i = static_cast<int>(threadIdx.x); i < static_cast<int>(sizeof ctl.bad / 4); i += kThreadsA)
+    (&ctl.bad[0][0][0])[i] = 0xffffffffu;
   // (a misplaced shared memory, which the attribute above excludes, would break the
   // swizzle)
   if ((smem_u32(smem) & 1023u) != 0) {
@@ -763,7 +784,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       // one; and both have read the streams' sums of the item before.
       if (D == 128 ? named_bar_any(1 + wq, 64, !more) : !more) break;
       const Tile<kCut> t(a, it, rank);
-      const uint32_t bad = smem_u32(&ctl.bad[used][0]), flag = smem_u32(&ctl.hit[used]);
+      const uint32_t bad = smem_u32(&ctl.bad[used][0][0]), flag = smem_u32(&ctl.hit[used]);
       const int own = max(0, t.mine + t.shift + 1) / kKeys - t.j0;  // first tile masked for this CTA
       float f0[2], f1[2];  // factors of the outputs of this thread's two rows there
       float2 stat[2];      // their maximum and sum
@@ -1006,7 +1027,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         // wait for this warp's P of the next.
         const int e = static_cast<int>(threadIdx.x) - 64;
         const int before = used == 0 ? 2 : used - 1;
-        if (e < 128) ctl.bad[before][e] = 0xffffffffu;
+        if (e < static_cast<int>(sizeof ctl.bad / 12)) (&ctl.bad[before][0][0])[e] = 0xffffffffu;
         if (e == 0) ctl.hit[before] = 0;
       }
       // 16 rows per warp, 64 columns at a time (lane l: rows l / 4, + 8); the words of a
@@ -1072,18 +1093,6 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         }
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = any[(i >> 1) & 1] ? v[i] : 0.0f;
-        if (marked) {
-#pragma unroll 1
-          for (int n = 0; n < 8; ++n) {
-            const uint32_t first = ctl.bad[used][d / 2 + 4 * n + (lane & 3)];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const uint32_t key = i & 1 ? first >> 16 : first & 0xffffu;
-              if (i >> 2 == n && lim[(i >> 1) & 1] - (t.j0 + t.jm) * kKeys >= static_cast<int>(key))
-                v[i] = __uint_as_float(0x7fffffffu);
-            }
-          }
-        }
         if (kCut && t.parts > 1) {
 #pragma unroll
           for (int z = 0; z < 2; ++z)
@@ -1106,6 +1115,18 @@ __global__ void __launch_bounds__(kThreadsA, 1)
             if (valid[z])
               *reinterpret_cast<uint4 *>(a.out + row[z] * D + d + 32 * h + 8 * (lane & 3)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
+      }
+      if (marked && ok) {
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          if (!valid[z]) continue;
+          const int seen = lim[z] - (t.j0 + t.jm) * kKeys;
+          if (kCut && t.parts > 1) {
+            Cleaner<D, 256>::put_back(ctl.bad[used], a.part + row[z] * D, seen, lane & 3);
+          } else {
+            Cleaner<D, 256>::put_back(ctl.bad[used], a.out + row[z] * D, seen, lane & 3);
+          }
+        }
       }
       tc_fence_before();
       if (t.nk > 0) used = used == 2 ? 0 : used + 1;

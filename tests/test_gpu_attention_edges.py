@@ -190,3 +190,31 @@ def test_scales_near_the_ends_of_float32(dev, D, T, M):
         check_attend(moe.attention_prefill(qs.to(dev), ks.to(dev), v.to(dev), scale=scale), qs, ks, v, scale)
         got = moe.attention_decode(qs[:1].to(dev), (codes, a), table.to(dev), n, scale=scale)
         check_decode(got, qs[:1], (codes, a), table, [M], scale)
+
+
+@pytest.mark.parametrize("T,M,Hq,Hk,D", [(600, 600, 8, 2, 128), (600, 600, 16, 2, 256), (300, 300, 1, 1, 256), (40, 3000, 8, 2, 128),
+                                         (40, 3000, 16, 2, 256)])
+def test_prefill_infinite_values(dev, T, M, Hq, Hk, D):
+    """A query that sees an infinity in v has it, one that sees both or a NaN has NaN,
+    wherever their tokens fall among the tiles and parts; other columns, heads and
+    earlier queries are as they were."""
+    q, k, v = prefill_inputs(T + M + D, T, M, Hq, Hk, D)
+    ref = moe.attention_prefill(q.to(dev), k.to(dev), v.to(dev)).cpu()
+    inf, nan, h = float("inf"), float("nan"), Hk - 1
+    rng = np.random.default_rng(T + D)
+    what = {}  # column -> [(token, value)]
+    for c in range(0, D, 3):
+        places = [0, M // 3, M - 1, M - 2, M - T, M - T // 2, *rng.integers(M - T, M, 8), *rng.integers(0, M, 4)]
+        what[c] = [(int(x), rng.choice([inf, -inf, inf, -inf, nan])) for x in rng.permutation(places)[:rng.integers(1, 3)]]
+    for c, marks in what.items():
+        for at, x in marks:
+            v[at, h, c] = x
+    got = moe.attention_prefill(q.to(dev), k.to(dev), v.to(dev)).cpu()
+    want = ref.clone().float()
+    group = slice(h * (Hq // Hk), (h + 1) * (Hq // Hk))
+    for c, marks in what.items():
+        for at in {at for at, _ in marks}:
+            x = v[at, h, c].float()  # (of two at one place the last)
+            want[max(0, at - (M - T)):, group, c] += x
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(got.float(), nan=0.0), torch.nan_to_num(want, nan=0.0))
