@@ -769,7 +769,14 @@ __global__ void __launch_bounds__(kThreadsA, 1)
       __syncwarp();
       if (lane == 0) {
         if (rank == 1) {
-          // (a remote arrival would hold the warp for a round trip; nothing reads the word)
+          // (A remote arrival would hold the warp for a round trip; nothing reads the word.)
+          // Its release is an asynchronous store's, which need not cover the warp's earlier
+          // stores; there are none left to cover.  What it tells of is done when it is
+          // issued, not only ordered before it: P is in TMEM when wait::st has returned,
+          // the values that a lane has cleaned are visible to the pair and to the MMAs when
+          // its own fences have (take_out), and __syncwarp comes after both in every lane.
+          // (A fence of the cluster here as well waits for a round trip, too: 4,096 tokens
+          // took 107 us in place of 82.)
           st_async_tx4(cluster_map(smem_u32(&ctl.sink), 0), 0u, cluster_map(smem_u32(&ctl.p_full[n & 1]), 0));
         } else if (wq == 2 && (P::kStreams == 2 || half == 0)) {
           mbar_arrive_expect_tx(smem_u32(&ctl.p_full[n & 1]), 4 * P::kMakers);  // the other CTA's words

@@ -89,6 +89,23 @@ def test_softmax_warps_of_prefill_leave_their_items_by_a_vote():
     assert items.rindex("if constexpr (D == 128) {", 0, meets[0]) > items.rindex("}", 0, meets[0])
 
 
+def test_what_a_signal_of_prefill_tells_of_is_done_before_it():
+    """The signal to the other CTA that P is there is an asynchronous store, whose
+    release need not cover the warp's earlier stores: those have to be done, in every
+    lane, when it is issued."""
+    text = source("attn_prefill.cu")
+    cleaned = block(text, "static __device__ __noinline__ void take_out")
+    last = max(cleaned.rindex("st.shared"), cleaned.rindex("atom.shared"))
+    assert last < cleaned.index('"fence.acq_rel.cluster;"') < cleaned.index("fence_proxy_async_smem()")
+    made = block(text, "auto made = [&](int n)")
+    assert made.index("tc_fence_before()") < made.index("__syncwarp()") < made.index("st_async_tx4")
+    body = text.split("__global__")[1]
+    for at in (m.start() for m in re.finditer(r"\bmade\(n\);", body)):
+        before = body[:at]
+        stored = max(before.rindex("st_pairs_16x32("), before.rfind("st_32x16("))
+        assert stored < before.rindex("wait_st()") < before.rindex("clean(j)")
+
+
 def test_products_of_prefill_end_before_their_memory_goes():
     """The warp of the MMAs waits for them whether or not it saw an abort, by a limit
     that no hook shortens; both CTAs of a pair wait for what is in flight."""
