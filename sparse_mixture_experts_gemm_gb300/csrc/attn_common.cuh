@@ -31,25 +31,6 @@ __device__ __forceinline__ void seq_rows(const int *offsets, int n, long long to
   }
 }
 
-// The sequence that row t of a packed call belongs to, -1 for none: the last
-// one that starts at or before t.  All lanes of the warp call it with the same
-// t; each step narrows the range to a 32nd with one load per lane.
-__device__ __forceinline__ int seq_of_row(const int *offsets, int n, long long total, int t) {
-  if (!offsets) return t / static_cast<int>(total / n);
-  const int lane = threadIdx.x & 31;
-  int lo = 0, len = n;  // the answer, if there is one, is in lo .. lo + len - 1
-  while (true) {
-    const int step = (len + 31) / 32, at = lo + lane * step;
-    const bool in = lane * step < len && offsets[at] <= t;
-    const int c = __popc(__ballot_sync(0xffffffffu, in));
-    if (c == 0) return -1;
-    lo += (c - 1) * step;
-    len = min(step, n - lo);
-    if (step == 1) break;
-  }
-  return offsets[lo + 1] > t ? lo : -1;
-}
-
 // A key/value cache: codes [pages][2][heads][64][D / 2] (keys, then values; the
 // even column in the low half of a byte), affine [pages][2][heads][64][D / 64][2]
 // (bf16 scale, bias).  table [n_seq][width]: page numbers of each sequence.
@@ -97,6 +78,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // one launch as a programmatic dependent of the kernel before it

@@ -9,7 +9,7 @@
 // with products and sums in fp32.
 //   * Keys: a code in the low bits of an fp16 is the number c 2^-24, four bits up c
 //     2^-20: one AND makes two.  The queries become fp16 by a power of two per head
-//     (the largest is in [2^12, 2^13): what is lost is below 2^-34 of it).
+//     (the largest is in [2^12, 2^13): what is lost is at most 2^-33 of it).
 //   * Values: weights times scales need bf16's range, and 128 + c is one AND-OR away
 //     from a nibble; a second product takes off 136 p_t s'_tg at once, so that the
 //     sum stays centred and has no large part that cancels against the bias's.
@@ -117,11 +117,6 @@ struct Page {
 };
 static_assert(offsetof(Team, q) % 16 == 0 && sizeof(Team) % 16 == 0, "read and written as vectors");
 
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
   asm(

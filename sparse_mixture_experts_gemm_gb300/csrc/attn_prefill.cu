@@ -226,12 +226,6 @@ __device__ __forceinline__ void turn_quad(uint32_t (&r)[4]) {
   }
 }
 
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ void fail(const PrefillArgs &a, volatile int *abort_flag, int site) {
   *abort_flag = 1;
   report_error(a.status, MOE_ERR_DEVICE_TIMEOUT, KID_ATTN_PREFILL * 100 + site);

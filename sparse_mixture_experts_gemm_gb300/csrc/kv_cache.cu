@@ -18,8 +18,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <mutex>
-
 #include "../../include/moe.h"
 #include "attn_common.cuh"
 
