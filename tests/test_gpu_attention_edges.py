@@ -6,8 +6,8 @@ import torch
 
 import sparse_mixture_experts_gemm_gb300 as moe
 from oracle import attention as oracle
-from test_gpu_attention import BF16, I32, check_attend, check_decode, ends, f64, gen, make_table, normal, \
-    prefill_inputs, random_cache, rows_of
+from test_gpu_attention import BF16, I32, check_attend, check_decode, check_rope, ends, f64, gen, \
+    make_table, normal, prefill_inputs, random_cache, rope_freq, rows_of
 
 pytestmark = pytest.mark.gpu
 
@@ -218,3 +218,66 @@ def test_prefill_infinite_values(dev, T, M, Hq, Hk, D):
             want[max(0, at - (M - T)):, group, c] += x
     assert torch.equal(torch.isnan(got), torch.isnan(want))
     assert torch.equal(torch.nan_to_num(got.float(), nan=0.0), torch.nan_to_num(want, nan=0.0))
+
+
+# --------------------------------------------------- the largest and the widest
+def test_cache_past_32_bits(dev):
+    """Pages whose codes lie more than 2^32 bytes into the cache, written, read back and
+    attended to."""
+    g = gen(31)
+    H, D, P, L = 2, 256, 140000, 300
+    cache = (torch.zeros(P, 2, H, 64, D // 2, dtype=torch.uint8, device=dev),
+             torch.zeros(P, 2, H, 64, D // 64, 2, dtype=BF16, device=dev))
+    assert cache[0].numel() > 1 << 32
+    table = torch.tensor([[P - 1, 0, P - 2, 131072, 70000]], dtype=I32)
+    k, v, q = normal(g, L, H, D), normal(g, L, H, D), normal(g, 1, 16, D)
+    moe.kv_cache_write(cache, k.to(dev), v.to(dev), table.to(dev))
+    ko, vo = moe.kv_cache_read(cache, table.to(dev), ends([L], dev), L)
+    for got, x in ((ko, k), (vo, v)):
+        ref = oracle.values(*oracle.quantise(f64(x)))
+        assert (np.abs(f64(got) - ref) <= np.abs(ref) * 2.0 ** -8 * (1 + 2.0 ** -14)).all()
+    pages = table[0].long()
+    small = tuple(t[pages.to(dev)] for t in cache)
+    got = moe.attention_decode(q.to(dev), cache, table.to(dev), torch.tensor([L], dtype=I32, device=dev))
+    check_decode(got, q, small, torch.arange(5)[None], [L], D ** -0.5)
+
+
+def test_prefill_past_32_bits(dev):
+    """Keys, values and outputs more than 2^31 elements into their tensors."""
+    g = gen(32)
+    Hk, D, M = 8, 256, (1 << 20) + 1000
+    k = torch.zeros(M, Hk, D, dtype=BF16, device=dev)
+    v = torch.zeros(M, Hk, D, dtype=BF16, device=dev)
+    assert k.numel() > 1 << 31
+    a, b, c = normal(g, 3, 16, D), normal(g, 900, Hk, D), normal(g, 900, Hk, D)
+    k[-900:], v[-900:] = b.to(dev), c.to(dev)
+    got = moe.attention_prefill(a.to(dev), k, v, ends([1, 2], dev), ends([M - 900, 900], dev))
+    assert not got[0].any()  # (zero values)
+    check_attend(got[1:], a[1:], b, c, D ** -0.5)
+    del v
+    # as queries: those of the last sequence, far into q and out
+    out = torch.full_like(k, 7.0)
+    off = torch.tensor([M - 900, M], dtype=I32, device=dev)
+    moe.attention_prefill(k, b.to(dev), c.to(dev), off, ends([900], dev), out=out)
+    check_attend(out[-900:], b, b, c, D ** -0.5)
+    assert (out[:100] == 7).all() and (out[M - 1000:M - 900] == 7).all()
+
+
+@pytest.mark.parametrize("Hq,Hk,D", [(4096, 4096, 128), (4096, 1, 128), (4096, 64, 256), (2047, 89, 256)])
+def test_many_heads(dev, Hq, Hk, D):
+    g = gen(Hk)
+    q, k, v = (normal(g, 3, h, D) for h in (Hq, Hk, Hk))
+    w, f, pos = torch.ones(D, dtype=BF16), rope_freq(64), torch.tensor([0, 5, 77], dtype=I32)
+    qo, ko = moe.qk_norm_rope(*(x.to(dev) for x in (q, k, w, w, pos, f)))
+    check_rope(qo, q, w, pos, f, 1e-6)
+    check_rope(ko, k, w, pos, f, 1e-6)
+    if Hq // Hk <= 64:
+        check_attend(moe.attention_prefill(q.to(dev), k.to(dev), v.to(dev)), q, k, v, D ** -0.5)
+    cache = moe.kv_cache(2, Hk, D, dev)
+    table, n = torch.tensor([[1, 0]], dtype=I32), torch.tensor([3], dtype=I32, device=dev)
+    moe.kv_cache_write(cache, k.to(dev), v.to(dev), table.to(dev))
+    kr, vr = moe.kv_cache_read(cache, table.to(dev), ends([3], dev), 3)
+    for got, x in ((kr, k), (vr, v)):
+        ref = oracle.values(*oracle.quantise(f64(x)))
+        assert (np.abs(f64(got) - ref) <= np.abs(ref) * 2.0 ** -8 * (1 + 2.0 ** -14)).all()
+    check_decode(moe.attention_decode(q[:1].to(dev), cache, table.to(dev), n), q[:1], cache, table, [3], D ** -0.5)
