@@ -197,8 +197,16 @@ __global__ void __launch_bounds__(kKvWarps * 32) kv_write_kernel(const KvArgs a)
           const int e = (__ffs(open) - 1) / 4;
           const uint32_t v0 = e & 2 ? w[z * 4 + 1] : w[z * 4], v1 = e & 2 ? w[z * 4 + 3] : w[z * 4 + 2];
           const uint32_t v = e & 4 ? v1 : v0;
-          const float y = __uint_as_float(e & 1 ? v & 0xffff0000u : v << 16) * f - lo * f;
-          const float quot = s == 0.0f ? 0.0f : __fdiv_rn(y, s * f);
+          const float x = __uint_as_float(e & 1 ? v & 0xffff0000u : v << 16) * f, from = lo * f, y = x - from;
+          float quot = s == 0.0f ? 0.0f : __fdiv_rn(y, s * f);
+          // Half way between two codes the exact quotient decides: what is left of y, which
+          // a fused sum has exactly, else what x - bias lost when it was rounded to y.
+          const float low = floorf(quot);
+          if (quot - low == 0.5f) {
+            const float left = fmaf(-(low + 0.5f), s * f, y), took = y - x;
+            const float more = left != 0.0f ? left : (x - (y - took)) + (-from - took);
+            if (more != 0.0f) quot = more > 0.0f ? low + 1.0f : low;
+          }
           const uint32_t n = static_cast<uint32_t>(fminf(rintf(quot), 15.0f)), nibble = 15u << (4 * e);
           code[z] = (code[z] & ~nibble) | n << (4 * e);
           open &= ~nibble;

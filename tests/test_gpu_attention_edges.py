@@ -281,3 +281,27 @@ def test_many_heads(dev, Hq, Hk, D):
         ref = oracle.values(*oracle.quantise(f64(x)))
         assert (np.abs(f64(got) - ref) <= np.abs(ref) * 2.0 ** -8 * (1 + 2.0 ** -14)).all()
     check_decode(moe.attention_decode(q[:1].to(dev), cache, table.to(dev), n), q[:1], cache, table, [3], D ** -0.5)
+
+
+@pytest.mark.parametrize("e", [0, -60, 100])
+def test_cache_codes_next_to_borders(dev, e):
+    """Values that are next to the middle between two codes by less than float32 holds
+    beside the bias: the code is that of the definition, on either side of it."""
+    odd = torch.arange(1, 16, 2)  # bias -1, -3, ..: next to zero (x - bias) / 2 is 0.5, 1.5, ..
+    rows = []
+    for b in odd.tolist():
+        for lo, hi in ((-b, 30 - b), (-b * 5, 150 - b * 5)):  # scale 2, 10
+            near = torch.tensor([s * m for m in (2.0 ** -24, 2.0 ** -30, 2.0 ** -45) for s in (1, -1)] + [0.0])
+            row = torch.zeros(64, dtype=torch.float64)
+            row[0], row[1], row[2:9] = lo, hi, near
+            row[9:16] = torch.tensor([lo + (hi - lo) / 30 * i for i in (1, 3, 5, 7, 9, 11, 13)], dtype=torch.float64)
+            rows.append(row)
+    x = (torch.stack(rows) * 2.0 ** e).to(BF16).view(8, 1, 128)
+    cache = moe.kv_cache(1, 1, 128, dev)
+    table = torch.zeros(1, 1, dtype=I32)
+    moe.kv_cache_write(cache, x.to(dev), -x.to(dev), table.to(dev))
+    codes, affine = rows_of(cache, table, 0, 0, 8)
+    for w, y in enumerate((x, -x)):
+        c, s, b = oracle.quantise(f64(y))
+        assert np.array_equal(f64(affine[:, w, ..., 0]), s) and np.array_equal(f64(affine[:, w, ..., 1]), b)
+        assert np.array_equal(oracle.unpack(codes[:, w].numpy()), c)
