@@ -242,8 +242,8 @@ __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, const volati
   return false;
 }
 __device__ __forceinline__ bool warp_wait(const PrefillArgs &a, uint32_t bar, uint32_t parity,
-                                          volatile int *abort_flag, int site) {
-  if (__all_sync(0xffffffffu, poll(bar, parity, abort_flag, a.waits.polls))) return true;
+                                          volatile int *abort_flag, int site, int times = 1) {
+  if (__all_sync(0xffffffffu, poll(bar, parity, abort_flag, times * a.waits.polls))) return true;
   if ((threadIdx.x & 31) == 0) fail(a, abort_flag, site);
   return false;
 }
@@ -597,7 +597,8 @@ __global__ void __launch_bounds__(kThreadsA, 1)
         const long long n = k & 1 ? (k + 1) * clusters - 1 - c : k * clusters + c;
         Item it = {};
         if (n < total) it = plan.find(n);
-        if (!warp_wait(a, smem_u32(&ctl.it_empty[k % kItems]), ((k / kItems) & 1) ^ 1, abort_flag, SITE_STAGE)) break;
+        // (the one wait that may be as long as a tile of rows, which over 2^28 keys is seconds)
+        if (!warp_wait(a, smem_u32(&ctl.it_empty[k % kItems]), ((k / kItems) & 1) ^ 1, abort_flag, SITE_STAGE, 64)) break;
         if (lane == 0) {
           ctl.item[k % kItems] = it;
           mbar_arrive(smem_u32(&ctl.it_full[k % kItems]));

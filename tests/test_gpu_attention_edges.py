@@ -82,6 +82,18 @@ def test_prefill_of_many_tiles_ends_when_a_wait_runs_out(dev, stall):
         assert torch.equal(moe.attention_prefill(q, k, v), ref)
 
 
+def test_prefill_tiles_of_rows_may_outlast_a_wait(dev, stall):
+    """The schedule is two tiles of rows ahead and waits for one to be done, which
+    over the longest keys takes longer than any other wait: here some 300 us, with
+    100 us for the others."""
+    q, k, v = (x.to(dev) for x in prefill_inputs(4, 32768, 32768, 4, 4, 128))
+    ref = moe.attention_prefill(q, k, v)
+    moe.moe_debug_attention_stall(2 ** 31 - 1, 100)
+    got = moe.attention_prefill(q, k, v)
+    assert moe.moe_noalloc_status()[0] == moe.MOE_OK
+    assert torch.equal(got, ref)
+
+
 # ------------------------------------- scores and weights at the ends of float32
 @pytest.mark.parametrize("Hq,Hk,D", [(16, 2, 256), (8, 4, 128)])
 def test_prefill_scores_of_minus_infinity(dev, Hq, Hk, D):
