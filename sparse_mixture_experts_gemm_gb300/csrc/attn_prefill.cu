@@ -554,6 +554,14 @@ __global__ void __launch_bounds__(kThreadsA, 1)
     pdl_wait();
     return;
   }
+  // Rows of Q past the tile's last token, which no copy writes: zeros, so that their
+  // scores, which the MMAs form all the same, never count as far or as grown.
+  const int rows = a.tokens * a.group;
+  for (int i = static_cast<int>(threadIdx.x); i < (128 - rows) * (D / 8); i += kThreadsA) {
+    const uint32_t at = sQ + i / ((128 - rows) * 8) * 16384 + rows * 128 + i % ((128 - rows) * 8) * 16;
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+  }
+  fence_proxy_async_smem();
   if (warp == 1) {
     tmem_alloc2(smem_u32(&ctl.tmem), kTmemCols);
     tmem_relinquish2();

@@ -106,6 +106,22 @@ def test_what_a_signal_of_prefill_tells_of_is_done_before_it():
         assert stored < before.rindex("wait_st()") < before.rindex("clean(j)")
 
 
+def test_rows_of_queries_that_no_copy_writes_are_zeros():
+    """Where a group of heads does not divide 128 the last rows of a tile of queries
+    belong to no token; they are written once, before the first copy and product."""
+    body = source("attn_prefill.cu").split("__global__")[1]
+    at = body.index("const int rows = a.tokens * a.group;")
+    fence = body.index("fence_proxy_async_smem();", at)
+    assert at < body.index("st.shared.v4.u32", at) < fence < body.index("__syncthreads()") < body.index("tma_load_3d_pair")
+    for D in (128, 256):  # the same arithmetic: each 16-byte piece of those rows once, and no other
+        for group in range(1, 65):
+            rows = 128 // group * group
+            n = 128 - rows
+            pieces = [i // (n * 8) * 16384 + rows * 128 + i % (n * 8) * 16 for i in range(n * (D // 8))]
+            want = [b * 16384 + r * 128 + 16 * p for b in range(D // 64) for r in range(rows, 128) for p in range(8)]
+            assert pieces == want
+
+
 def test_products_of_prefill_end_before_their_memory_goes():
     """The warp of the MMAs waits for them whether or not it saw an abort, by a limit
     that no hook shortens; both CTAs of a pair wait for what is in flight."""
