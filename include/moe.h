@@ -466,12 +466,19 @@ int moe_matmul_fp8(const uint8_t *x, const float *x_scales, int T, long long x_s
  * queries and keys, causal attention of prompts, a key/value cache in 4 bits
  * and attention of new tokens over it.  Several query heads share a key/value
  * head: query head h goes with key/value head h / (n_q_heads / n_kv_heads).
- * They need no handle and allocate nothing.  Everything is bfloat16 outside
- * and float32 inside; each result is rounded once.  Supported: head_dim 128 or
- * 256, up to 4096 heads of either kind (rotation, cache, decode) and 64 query
- * heads per key/value head (prefill), fewer than 2^31 tokens (prefill: 2^29 queries
- * and keys at most; decode: n_seq * table_width * n_kv_heads times the eights of query
- * heads that share one, rounded up, below 2^31), strides < 2^38.
+ * They need no handle and allocate nothing.  Everything is bfloat16 outside;
+ * scores, the softmax's statistics, sums and norms are float32, and each result is
+ * rounded once.  Besides that, weights are rounded before they multiply values, by
+ * 2^-8 of each at most, as much as the result's own rounding: in prefill to bfloat16
+ * (their sum is taken before), in decode as weight times the values' scale to
+ * bfloat16, which multiplies codes less 8 (and to 2^-16 with the biases).  Weights
+ * in sums are up to 2^8, so values past 2^119 over the number of keys may overflow, as
+ * scores past float32's range do.
+ * Supported: head_dim 128 or 256, up to 4096 heads of either kind (rotation, cache,
+ * decode), 4096 key/value heads and 64 query heads for each (prefill), fewer than 2^31
+ * tokens (prefill: 2^29 queries and keys at most; decode: n_seq * table_width *
+ * n_kv_heads times the eights of query heads that share one, rounded up, below
+ * 2^31), strides < 2^38.
  * Pointers are device memory, 16-byte aligned (int32 arrays 4, doubles 8);
  * strides, in elements from one token to the next, are multiples of 8, and the
  * heads of a token lie side by side.  Asynchronous on cuda_stream; the checks
@@ -521,9 +528,10 @@ int moe_qk_norm_rope(const void *q, const void *k, const void *q_weight, const v
  *   offsets, k_offsets: the sequences' queries and keys; k_offsets NULL: the same
  *        as offsets (n_k == n_q).  Both NULL: n_seq sequences of n_q / n_seq
  *        queries and n_k / n_seq keys.
- * 0 < scale <= 2.35e38 (times log2(e) it is finite).  A NaN or infinity in k or v reaches no query that does
- * not see its token; one that sees an infinity in v has it in that column (NaN next
- * to a NaN or one of the other sign, or where its weight is below what float32 holds).
+ * 0 < scale <= 2.35e38 (times log2(e) it is finite).  A NaN or infinity in k or v
+ * reaches no query that does not see its token; one that sees an infinity in v has
+ * it in that column (NaN next to a NaN or one of the other sign, or where its weight
+ * is below what float32 holds).  A row whose scores are all minus infinity is NaN.
  *   workspace: device memory of at least the bytes that
  *        moe_attention_prefill_workspace gives for the same sizes, 16-byte
  *        aligned, used by the call's kernels alone; NULL where that is 0.  (Few
