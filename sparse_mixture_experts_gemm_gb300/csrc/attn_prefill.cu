@@ -443,7 +443,7 @@ struct Cleaner {
         asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(0)) : "memory");
         if (key >= lk) continue;  // (another sequence's: nobody sees it)
         const int c = rank * (D / 2) + ((e >> 7) * kPer + i) * 8 + x;
-        // (masked tiles are four at most)
+        // (masked tiles are three at most)
         const uint32_t mark = static_cast<uint32_t>(key - base), shift = 10 * (c % 3);
         for (int y = 0; y < 4; ++y) {
           const uint32_t to = y & 1, minus = y >> 1;
@@ -1127,6 +1127,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
           }
       }
       if (marked && ok) {
+        asm volatile("" ::: "memory");  // (what was stored as words is read as numbers)
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
           if (!valid[z]) continue;

@@ -84,11 +84,11 @@ def test_prefill_of_many_tiles_ends_when_a_wait_runs_out(dev, stall):
 
 def test_prefill_tiles_of_rows_may_outlast_a_wait(dev, stall):
     """The schedule is two tiles of rows ahead and waits for one to be done, which
-    over the longest keys takes longer than any other wait: here some 300 us, with
-    100 us for the others."""
-    q, k, v = (x.to(dev) for x in prefill_inputs(4, 32768, 32768, 4, 4, 128))
+    over the longest keys takes longer than any other wait: here up to 650 us, with
+    200 us for the others."""
+    q, k, v = (x.to(dev) for x in prefill_inputs(4, 65536, 65536, 4, 4, 128))
     ref = moe.attention_prefill(q, k, v)
-    moe.moe_debug_attention_stall(2 ** 31 - 1, 100)
+    moe.moe_debug_attention_stall(2 ** 31 - 1, 200)
     got = moe.attention_prefill(q, k, v)
     assert moe.moe_noalloc_status()[0] == moe.MOE_OK
     assert torch.equal(got, ref)
