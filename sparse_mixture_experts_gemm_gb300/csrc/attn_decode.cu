@@ -33,10 +33,13 @@
 // dequantisation fills as they are; P is turned in between, four 8 x 8 matrices.
 //
 // Measured, 16 query heads on 2 of 256: 64 sequences of 17 to 8,192 tokens 44 us (148 MB,
-// 3.4 TB/s), one of 131,072 26.5 us, one of 4,097 9.3 us.  What bounds it are the
-// dequantisation's instructions, 5 per 8 codes of the keys and 7 of the values: ALU 57 %
-// busy, matrix instructions 31 %.  Scores of the next page between the products of this
-// one (47 us) and shifts by high products on the other pipe (48) gained nothing.
+// 3.3 TB/s), one of 131,072 26.6 us, one of 4,097 9.2 us.  32 on 8 of 128: the same 64
+// sequences 89 us (294 MB, 3.3 TB/s), one of 131,072 42 us; 16 on 2 of 128: 30, 17.4 us.
+// No unit is at its limit (ALU 57 % busy, matrix instructions 32 %, issue 50 %, DRAM 45 %):
+// three warps a scheduler have a long chain from codes to scores to weights to values
+// to cover, with 5 ALU instructions per 8 codes of the keys and 7 of the values.  Scores of
+// the next page between the products of this one (47 us) and shifts by high products on the
+// other pipe (48) gained nothing.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -41,11 +41,12 @@
 // and infinity, its negative, or both for a NaN, are added to the outputs of the
 // queries that do see them.
 //
-// Measured: 4,096 tokens of 16 heads of 256 on 2 in 81.5 us (1.69 PFLOP/s, tensor pipes
-// busy 73 % of the cycles; the rest goes at the changes of tile, about 4,500 cycles
-// each), 8,192 behind 24,576 in 1.85 ms (2.1 PFLOP/s); 2 x 2,048 tokens of 32 heads of
-// 128 on 8 in 84 us (0.82 PFLOP/s, the handover between softmax and products, about
-// 1,700 cycles a tile).
+// Measured, back to back in a graph (in brackets: calls one after another, under the
+// power limit): 4,096 tokens of 16 heads of 256 on 2 in 83 us, 1.66 PFLOP/s (90, 1.53),
+// tensor pipes busy 73 % of the cycles; the rest goes at the changes of tile, about 4,500
+// cycles each.  8,192 tokens behind 24,576 in 1.83 to 1.87 ms, 2.1 PFLOP/s (2.12, 1.82).
+// 2 x 2,048 tokens of 32 heads of 128 on 8 in 85 us, 0.81 PFLOP/s, tensor pipes 35 %: the
+// handover between softmax and products, about 1,700 cycles a tile.
 //
 // Roles (352 threads): warp 0 TMA copies; warp 1 the MMAs (CTA 0); warps 2-9 the
 // softmax and the outputs, each telling CTA 0 that its P is there (through a warp of
@@ -249,7 +250,9 @@ __device__ __forceinline__ bool warp_wait(const PrefillArgs &a, uint32_t bar, ui
 }
 
 // The schedule (one warp): tiles of rows by falling number of key tiles; kCut: keys of
-// some are cut into parts.
+// some are cut into parts.  Past 32 sequences a tile is found by a search whose every
+// step reads all offsets, so that many short ones cost the square of their number: 64
+// prompts of 64 tokens 31 us, 256 244 us, 1,024 3.8 ms (16 heads of 256 on 2).
 template <bool kCut>
 struct Schedule {
   const PrefillArgs &a;
@@ -1276,11 +1279,12 @@ const PrefillDevice &prefill_device() {
 // are cut into parts.  Times are in tiles of 128 keys (about 1 us): rounds of clusters
 // of a part's tiles and 3 for its start and end, 5 for the second kernel, and the
 // parts' outputs, which move to and fro at 3 MB a tile's time.  Measured, 16 query heads
-// on 2 of 256: 1 query over 4,096 keys in 17.7 us (16 parts) against 41, over 16,384 in
+// on 2 of 256: 1 query over 4,096 keys in 18 us (16 parts) against 41, over 16,384 in
 // 25 against 142, 64 over 4,096 in 23 against 42, 300 over 8,192 in 47 (3 parts) against
 // 76 (4 parts, more than there are clusters: 60); not cut: 700 over 2,000 26 (48 with 2),
-// 1,300 over 4,000 63 (97).  1,016 queries over 16,484 keys packed with a prompt of 3,765,
-// 4 heads on 1: 97 in place of 149.
+// 1,300 over 4,000 61 (97).  1,016 queries over 16,484 keys packed with a prompt of 3,765,
+// 4 heads on 1: 100 in place of 149.  Not cut, though it should be: one query over 131,072
+// keys next to 63 over 600, 16 heads of 128 on 4, 0.91 ms.
 struct Cut {
   int parts, length;
 };

@@ -12,9 +12,9 @@
 // Bound by memory, 2.56 bytes moved per column, and on the way there by instructions,
 // those of the addresses as much as those of the columns: 16 columns per lane, a
 // block of several tokens whose places its first warp looks up, one token per lane.
-// 16,384 tokens of 2 heads of 256 are written in 14 us (3.1 TB/s) and read in 8.5
-// (5.1 TB/s); with a warp per token, a division per code and 8 columns per lane both
-// took 43 us.
+// 16,384 tokens of 2 heads of 256 are written in 14.4 us (3.0 TB/s) and read in 10
+// (4.3 TB/s), four caches in turn; with a warp per token, a division per code and 8
+// columns per lane both took 43 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
