@@ -774,6 +774,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
       }
     }
   }
+  __syncwarp();
   __syncthreads();
   if (*abort_flag)  // after an abort the copies in flight get time to land
     for (int i = 0; i < 200; ++i) __nanosleep(1000);

@@ -1153,6 +1153,7 @@ __global__ void __launch_bounds__(kThreadsA, 1)
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag)  // the other CTA hears of an abort
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_map(smem_u32(&ctl.abort_flag), rank ^ 1)), "r"(1) : "memory");
+  __syncwarp();
   cluster_sync_all();  // no MMA of the pair is in flight, no arrival is pending
   tc_fence_after();
   if (warp == 1) tmem_dealloc2(0, kTmemCols);

@@ -131,6 +131,7 @@ def test_products_of_prefill_end_before_their_memory_goes():
     assert before.endswith("if (one)") and before[:-len("if (one)")].rstrip().endswith("}")
     assert "poll(smem_u32(&ctl.drain), 0, nullptr, 1 << 21)" in body[drain:]
     told, met = body.index("cluster_map(smem_u32(&ctl.abort_flag), rank ^ 1)"), body.rindex("cluster_sync_all()")
+    assert "__syncwarp();" in body[told:met]  # (the pair's barrier wants whole warps)
     assert drain < told < met < body.index("tmem_dealloc2") < body.index("__nanosleep")
 
 
