@@ -317,3 +317,37 @@ def test_cache_codes_next_to_borders(dev, e):
         c, s, b = oracle.quantise(f64(y))
         assert np.array_equal(f64(affine[:, w, ..., 0]), s) and np.array_equal(f64(affine[:, w, ..., 1]), b)
         assert np.array_equal(oracle.unpack(codes[:, w].numpy()), c)
+
+
+@pytest.mark.parametrize("T,M,Hq,Hk,D", [(300, 300, 8, 2, 128), (300, 300, 16, 2, 256), (40, 3000, 8, 2, 128), (40, 3000, 16, 2, 256)])
+@pytest.mark.parametrize("x", [float("inf"), -float("inf")])
+def test_prefill_infinite_keys(dev, T, M, Hq, Hk, D, x):
+    """An infinity in a key: for queries whose score it makes minus infinity the key
+    weighs nothing, for the others that see it the row is NaN."""
+    q, k, v = prefill_inputs(T + M + D + 1, T, M, Hq, Hk, D)
+    h, group = Hk - 1, slice((Hk - 1) * (Hq // Hk), Hq)
+    clean = moe.attention_prefill(q.to(dev), k.to(dev), v.to(dev)).cpu()
+    for at in (0, M // 3, M - T, M - T // 2, M - 1):
+        k2 = k.clone()
+        k2[at, h, 9] = x
+        got = moe.attention_prefill(q.to(dev), k2.to(dev), v.to(dev)).cpu()
+        sees = (torch.arange(T) + M - T >= at)[:, None].expand(T, Hq).clone()
+        sees[:, :group.start] = False
+        gone = sees & (q[..., 9].float() * x < 0)
+        if at == 0 and T == M:
+            gone[0] = False  # (no other key)
+        assert torch.equal(torch.isnan(got).all(-1), sees & ~gone) and torch.equal(torch.isnan(got).any(-1), sees & ~gone)
+        assert torch.equal(got[~sees], clean[~sees])
+        keep = np.arange(M) != at
+        for i in np.flatnonzero(gone.any(1).numpy())[::7]:
+            n = M - T + i + 1
+            rows = np.flatnonzero(gone[i].numpy())
+            a, b = f64(k[:n, h])[keep[:n]], f64(v[:n, h])[keep[:n]]
+            s = f64(q[i, rows]) @ a.T * D ** -0.5
+            p = np.exp(s - s.max(1, keepdims=True))
+            p /= p.sum(1, keepdims=True)
+            ref, mag = p @ b, p @ np.abs(b)
+            reach = (np.abs(f64(q[i, rows])) @ np.abs(a).T).max(1, keepdims=True)
+            tol = 2.0 ** -8 * (np.abs(ref) + mag) * (1 + 2.0 ** -6) + \
+                mag * ((n / 16 + 64) * 2.0 ** -23 + 2 * D ** -0.5 * reach * (D / 8 + 8) * 2.0 ** -23)
+            assert (np.abs(f64(got[i, rows]) - ref) <= tol).all()
